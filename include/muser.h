@@ -531,6 +531,118 @@ int muser_kv_restore(muser_kv_plane* plane, const uint16_t* k_rows, const uint16
                      int64_t origin_logical, int64_t len, void* stream);
 
 /*
+ * The speculative step.  M rows go through the layers together: row 0 is the
+ * last accepted token, rows 1..M-1 are drafted tokens.  `parent` is a host
+ * array of M rows: parent[0] = -1, 0 <= parent[i] < i; NULL is a chain
+ * (parent[i] = i - 1).  A row's depth is its number of ancestors; its
+ * position is origin_logical + len of the plane plus its depth.  The rows'
+ * K and V stay out of the planes until they are accepted: a sliding-window
+ * ring is as long as its window, so a drafted row stored early would evict a
+ * row that other drafted rows still see.  One decode step is then, per layer,
+ * muser_qmatvec_group and muser_kv_tree_attention; muser_lm_head;
+ * muser_tree_verify; and muser_kv_tree_commit over all layers.  M = 1 is plain
+ * decoding.  The attention call is the attention of Ch 10 Figure 10.1 with
+ * the window of Ch 15 §15.2 and the output's sigmoid gate (Ch 2 §2.7).
+ */
+
+/* Scratch bytes muser_kv_tree_attention needs; it does not depend on the
+ * plane's length.  0 for a shape the call does not take. */
+size_t muser_kv_tree_attention_scratch_bytes(int64_t kv_dim, int64_t head_dim, int M, int n_heads);
+
+/*
+ * muser_kv_tree_attention -- out[i, h] = sum_j a_j v_j over the rows j that
+ *   row i sees, a = softmax(scale * q[i, h] . k_j); with `gate`, times
+ *   1/(1+exp(-gate[i, h])) elementwise.  Query head h reads K/V head
+ *   h / (n_heads / kv_heads), kv_heads = kv_dim / head_dim.
+ *   Row i, at position t, sees
+ *    - the plane's live row of logical position p if t - p < window (window 0:
+ *      always) or p < n_sink;
+ *    - the sink plane's live row p if p < n_sink and the plane holds no p that
+ *      small (p < plane->origin_logical): first tokens that a ring has since
+ *      evicted, kept apart by the caller;
+ *    - itself, and an ancestor j if depth_i - depth_j < window or j's
+ *      position is below n_sink.
+ *   No other row has any influence, whatever its slot holds (infinities and
+ *   NaN included).  A score or a value that is not finite in a row that is
+ *   seen makes the outputs that read it not finite.
+ *   plane: host struct, read only, head_dim set in both layouts; sink: the
+ *   same kv_dim and head_dim, either layout, or NULL.  q, out, gate: device
+ *   f32 [M * n_heads*head_dim]; k, v: device f32 [M * kv_dim], used as
+ *   muser_kv_ring_write would store them (rounded to binary16).  Scores, the
+ *   softmax and the sums are binary32.  n_heads is a multiple of kv_heads;
+ *   head_dim <= 256, n_heads <= 1024 (MUSER_ERR_UNSUPPORTED).
+ *   scratch: device memory of muser_kv_tree_attention_scratch_bytes(),
+ *   16-byte aligned, zero-filled before its first use.  It holds partial
+ *   results and is not left zero-filled: lend it to no call that wants that.
+ *   Calls that can run at the same time must not share it.  out and scratch
+ *   overlap nothing else.
+ */
+int muser_kv_tree_attention(const muser_kv_plane* plane, const muser_kv_plane* sink, const float* q, const float* k,
+                            const float* v, const float* gate, int M, int n_heads, const int32_t* parent,
+                            int64_t window, int64_t n_sink, float scale, float* out, void* scratch,
+                            size_t scratch_bytes, void* stream);
+
+/* Scratch bytes muser_tree_verify needs (0 for sizes it does not take). */
+size_t muser_tree_verify_scratch_bytes(int64_t vocab, int M);
+
+/*
+ * muser_tree_verify -- which drafted tokens are kept, and the token after them.
+ *   p_i = softmax(target_i / temperature), q_i = softmax(draft_i /
+ *   temperature).  From row 0, the children i of the present row r are tried
+ *   in order on what the rejected ones before them left of p_r: with c = 0,
+ *   z = 1 at first, child i of token x is accepted, and becomes the present
+ *   row, if uniform[i] * z * q_r(x) < p_r(x) - c * q_r(x); otherwise c grows
+ *   by z and z becomes sum_v max(p_r(v) - c * q_r(v), 0).  (Accepting with
+ *   probability min(1, p/q) and going on with the normalised residual
+ *   max(p - q, 0), in closed form for repeated rejections.)  At a row whose
+ *   children are all rejected, or that has none, the next token is the first
+ *   v with sum_{w<=v} max(p_r(w) - c * q_r(w), 0) > uniform[0] * z; where
+ *   nothing is left, p_r itself is sampled.
+ *   draft NULL: the drafted tokens are taken as certain; child i is accepted
+ *   if uniform[i] times what is left of p_r without the rejected siblings'
+ *   tokens is below p_r(x).  temperature 0: greedy; child i is accepted if
+ *   its token is the first maximum of target_r, which is also the next token;
+ *   draft and uniform are not read.
+ *   target, draft: device f32 [M * vocab]; draft row r is what r's children
+ *   were drawn from (rows without children are not read); tokens: device
+ *   int32 [M] (tokens[0] is not read; a token outside 0..vocab-1 has
+ *   probability 0); uniform: device f32 [M] in [0, 1); result: device int32
+ *   [M + 2]: the number n of kept rows (row 0 included), the next token, the
+ *   kept rows ascending, then -1.  The token is -1 when the walk meets a row
+ *   with a NaN, a +infinity, only -infinities, or a largest logit /
+ *   temperature beyond about +-22,000.  vocab <= 2^20, temperature 0 or >= 0.001.
+ *   Probabilities below 2^-42 of the row's largest may count as 0; decisions
+ *   are otherwise those of exact arithmetic to about 2^-37 (2^-33 where logit /
+ *   temperature is in the thousands), and a remainder of
+ *   a smaller share than that may count as nothing left.
+ *   One cooperative launch whose blocks wait for one another (bounded in
+ *   time, muser_device_status() bit 1, result then unwritten).
+ *   scratch: device memory of muser_tree_verify_scratch_bytes(), 16-byte
+ *   aligned, zero-filled before its first use; its first 256 bytes are left
+ *   zero, the rest is not.  Calls that can run at the same time must not
+ *   share it.
+ */
+int muser_tree_verify(const float* target, const float* draft, const int32_t* tokens, const int32_t* parent, int M,
+                      int64_t vocab, double temperature, const float* uniform, int32_t* result, void* scratch,
+                      size_t scratch_bytes, void* stream);
+
+/*
+ * muser_kv_tree_commit -- append the accepted rows of a tree to the planes of
+ *   up to 128 layers in one launch: to each plane i, rows path[0..n) of k[i]
+ *   and v[i], exactly as n muser_kv_ring_write calls of one row from
+ *   `position` on.  Every plane must end at `position` (else
+ *   MUSER_ERR_CACHE_DISCONTINUITY); planes may differ in layout, capacity and
+ *   length, and must not share memory.
+ *   planes: host array, updated on success; k, v: host arrays of device f32
+ *   [M * kv_dim] pointers, 4-byte aligned (16-byte aligned ones with kv_dim,
+ *   and head_dim for head-major planes, multiples of 8 take 16-byte
+ *   accesses); path: host array of n rows, ascending, in 0..M-1.  n == 0
+ *   launches nothing.  Any error changes no plane.
+ */
+int muser_kv_tree_commit(muser_kv_plane* planes, int n_planes, const float* const* k, const float* const* v, int M,
+                         const int32_t* path, int n, int64_t position, void* stream);
+
+/*
  * muser_sync -- wait until all work enqueued on `stream` has finished, for at
  *   most timeout_ms milliseconds (the book's bounded wait_for_completion,
  *   Ch 2 §2.10).  Returns MUSER_OK, MUSER_ERR_TIMEOUT (the work keeps

@@ -90,6 +90,9 @@ def lib():
                                        ctypes.POINTER(I64)]
             L.orc_kv_snapshot.argtypes = [ctypes.POINTER(Ring), P, P, I64, I64, I, I64, I64, P, P]
             L.orc_kv_restore.argtypes = [ctypes.POINTER(Ring), P, P, I64, I64, I, P, P, I64, I64]
+            L.orc_tree_attention.argtypes = [ctypes.POINTER(Ring), P, P, I, ctypes.POINTER(Ring), P, P, I, I64, I64, P, P,
+                                             P, P, I64, I64, P, I64, I64, D, P]
+            L.orc_tree_verify.argtypes = [P, P, P, P, I64, I64, D, P, P]
             L.orc_num_threads.restype = I
             L.orc_set_num_threads.argtypes = [I]
             _lib = L
@@ -367,3 +370,39 @@ def kv_restore(ring: Ring, key: np.ndarray, value: np.ndarray, kv_dim: int, head
     assert kr.shape == vr.shape
     return lib().orc_kv_restore(ctypes.byref(ring), _p(key), _p(value), kv_dim, head_dim,
                                 int(bool(head_major)), _p(kr), _p(vr), origin, kr.shape[0])
+
+
+# --------------------------------------------------------- speculative step
+def tree_attention(ring: Ring, key: np.ndarray, value: np.ndarray, kv_dim: int, head_dim: int, head_major: bool,
+                   q: np.ndarray, k: np.ndarray, v: np.ndarray, n_heads: int, scale: float, parent=None,
+                   window: int = 0, n_sink: int = 0, sink=None, gate=None) -> np.ndarray:
+    """Attention of the tree rows q, k, v [M][..] over a plane; sink: (Ring, key,
+    value, head_major) or None.  Returns f32 [M][n_heads * head_dim]."""
+    q, k, v = (np.ascontiguousarray(t, dtype=np.float32) for t in (q, k, v))
+    M = q.shape[0]
+    parent = np.ascontiguousarray(range(-1, M - 1) if parent is None else parent, dtype=np.int32)
+    gate = None if gate is None else np.ascontiguousarray(gate, dtype=np.float32)
+    out = np.empty((M, n_heads * head_dim), np.float32)
+    srefs = (None, None, None, 0) if sink is None else (ctypes.byref(sink[0]), _p(sink[1]), _p(sink[2]), int(sink[3]))
+    rc = lib().orc_tree_attention(ctypes.byref(ring), _p(key), _p(value), int(bool(head_major)), *srefs, kv_dim,
+                                  head_dim, _p(q), _p(k), _p(v), None if gate is None else _p(gate), M, n_heads,
+                                  _p(parent), window, n_sink, scale, _p(out))
+    if rc != 0:
+        raise ValueError(f"orc_tree_attention: {rc}")
+    return out
+
+
+def tree_verify(target: np.ndarray, tokens, temperature: float, uniform=None, draft=None, parent=None) -> np.ndarray:
+    """Verification of drafted tokens; returns int32 [M + 2] as muser_tree_verify writes it."""
+    target = np.ascontiguousarray(np.atleast_2d(target), dtype=np.float32)
+    M, vocab = target.shape
+    parent = np.ascontiguousarray(range(-1, M - 1) if parent is None else parent, dtype=np.int32)
+    tokens = np.ascontiguousarray(tokens, dtype=np.int32)
+    uniform = np.zeros(M, np.float32) if uniform is None else np.ascontiguousarray(uniform, dtype=np.float32)
+    draft = None if draft is None else np.ascontiguousarray(draft, dtype=np.float32)
+    result = np.empty(M + 2, np.int32)
+    rc = lib().orc_tree_verify(_p(target), None if draft is None else _p(draft), _p(tokens), _p(parent), M, vocab,
+                               float(temperature), _p(uniform), _p(result))
+    if rc != 0:
+        raise ValueError(f"orc_tree_verify: {rc}")
+    return result

@@ -462,3 +462,170 @@ int orc_kv_restore(orc_ring* r, uint16_t* key, uint16_t* value, int64_t kv_dim, 
     r->origin_physical = rotation;
     return ORC_OK;
 }
+
+/* ------------------------------------------------- the speculative step
+ * Attention of M tree rows over a cached plane (the attention of Ch 10 Figure
+ * 10.1; window: Ch 15 §15.2; output gate: Ch 2 §2.7).  Row i sees cached row p
+ * when t_i - p < window (window 0: always) or p < n_sink, the rows p < n_sink
+ * of the sink plane that lie before the plane's first row, itself, and its
+ * ancestors under the same rule.  Tree rows are used rounded to binary16.  One
+ * softmax in fp64 per (row, head), one rounding at the end. */
+typedef struct {
+    const orc_ring* ring;
+    const uint16_t* key;
+    const uint16_t* value;
+    int64_t head_major;
+} orc_plane;
+
+int orc_tree_attention(const orc_ring* ring, const uint16_t* key, const uint16_t* value, int head_major,
+                       const orc_ring* sink, const uint16_t* sink_key, const uint16_t* sink_value,
+                       int sink_head_major, int64_t kv_dim, int64_t head_dim, const float* q, const float* k,
+                       const float* v, const float* gate, int64_t M, int64_t n_heads, const int32_t* parent,
+                       int64_t window, int64_t n_sink, double scale, float* out) {
+    const int64_t kv_heads = kv_dim / head_dim, end = ring->origin_logical + ring->len;
+    const orc_plane planes[2] = {{sink, sink_key, sink_value, sink_head_major}, {ring, key, value, head_major}};
+    if (M < 1 || M > 64 || n_heads % kv_heads) return ORC_ERR_ARG;
+    int64_t depth[64];
+    for (int64_t i = 0; i < M; ++i) depth[i] = parent[i] < 0 ? 0 : depth[parent[i]] + 1;
+    int rc = ORC_OK;
+#pragma omp parallel for collapse(2) schedule(dynamic)
+    for (int64_t i = 0; i < M; ++i)
+        for (int64_t h = 0; h < n_heads; ++h) {
+            const int64_t g = h / (n_heads / kv_heads), t = end + depth[i];
+            const float* qv = q + (i * n_heads + h) * head_dim;
+            int64_t cap = M;
+            for (int pl = 0; pl < 2; ++pl) cap += planes[pl].ring ? planes[pl].ring->len : 0;
+            double* score = (double*)malloc(sizeof(double) * (size_t)cap);
+            double* val = (double*)malloc(sizeof(double) * (size_t)(cap * head_dim));
+            if (!score || !val) {
+#pragma omp critical
+                rc = ORC_ERR_ARG;
+                free(score);
+                free(val);
+                continue;
+            }
+            int64_t n = 0;
+            for (int pl = 0; pl < 2; ++pl) {
+                const orc_ring* r = planes[pl].ring;
+                if (!r) continue;
+                for (int64_t j = 0; j < r->len; ++j) {
+                    const int64_t p = r->origin_logical + j;
+                    if (pl == 0 ? (p >= n_sink || p >= ring->origin_logical)
+                                : (window > 0 && t - p >= window && p >= n_sink))
+                        continue;
+                    const int64_t slot = (r->origin_physical + j) % r->capacity;
+                    double s = 0.0;
+                    for (int64_t d = 0; d < head_dim; ++d) {
+                        const int64_t at = orc_kv_index(slot, g * head_dim + d, kv_dim, head_dim,
+                                                        (int)planes[pl].head_major, r->capacity);
+                        s += (double)qv[d] * orc_f16_to_f64(planes[pl].key[at]);
+                        val[n * head_dim + d] = orc_f16_to_f64(planes[pl].value[at]);
+                    }
+                    score[n++] = s * scale;
+                }
+            }
+            for (int64_t j = i; j >= 0; j = parent[j]) {
+                if (window > 0 && depth[i] - depth[j] >= window && end + depth[j] >= n_sink) continue;
+                double s = 0.0;
+                for (int64_t d = 0; d < head_dim; ++d) {
+                    const int64_t at = j * kv_dim + g * head_dim + d;
+                    s += (double)qv[d] * orc_f16_to_f64(orc_f32_to_f16(k[at]));
+                    val[n * head_dim + d] = orc_f16_to_f64(orc_f32_to_f16(v[at]));
+                }
+                score[n++] = s * scale;
+            }
+            double m = score[0], l = 0.0;
+            for (int64_t j = 1; j < n; ++j) m = score[j] > m ? score[j] : m;
+            for (int64_t j = 0; j < n; ++j) {
+                score[j] = exp(score[j] - m);
+                l += score[j];
+            }
+            for (int64_t d = 0; d < head_dim; ++d) {
+                double o = 0.0;
+                for (int64_t j = 0; j < n; ++j) o += score[j] * val[j * head_dim + d];
+                o /= l;
+                const int64_t at = (i * n_heads + h) * head_dim + d;
+                if (gate) o /= 1.0 + exp(-(double)gate[at]);
+                out[at] = (float)o;
+            }
+            free(score);
+            free(val);
+        }
+    return rc;
+}
+
+/* Verification of drafted tokens as the acceptance rule is usually stated: the
+ * children of the present row are tried in order; child i of token x is
+ * accepted with probability min(1, r(x)/q(x)), decided by uniform[i]; a
+ * rejection replaces r by the normalised max(r - q, 0) (drafts that are
+ * certain: r without x).  The next token is drawn from the last r by
+ * uniform[0].  temperature 0: greedy.  result: n, token, the kept rows, -1. */
+static void orc_softmax(const float* x, int64_t n, double temperature, double* p) {
+    double m = x[0], s = 0.0;
+    for (int64_t i = 1; i < n; ++i) m = x[i] > m ? x[i] : m;
+    for (int64_t i = 0; i < n; ++i) s += p[i] = exp(((double)x[i] - m) / temperature);
+    for (int64_t i = 0; i < n; ++i) p[i] /= s;
+}
+
+int orc_tree_verify(const float* target, const float* draft, const int32_t* tokens, const int32_t* parent, int64_t M,
+                    int64_t vocab, double temperature, const float* uniform, int32_t* result) {
+    double* p = (double*)malloc(sizeof(double) * (size_t)vocab * 3);
+    if (!p) return ORC_ERR_ARG;
+    double *q = p + vocab, *r = p + 2 * vocab;
+    int64_t cur = 0, n = 0, next = -1;
+    for (;;) {
+        const float* row = target + cur * vocab;
+        int64_t taken = -1;
+        result[2 + n++] = (int32_t)cur;
+        if (temperature == 0.0) {
+            next = 0;
+            for (int64_t v = 1; v < vocab; ++v)
+                if (row[v] > row[next]) next = v;
+            for (int64_t i = 1; i < M && taken < 0; ++i)
+                if (parent[i] == cur && tokens[i] == next) taken = i;
+        } else {
+            orc_softmax(row, vocab, temperature, p);
+            for (int64_t v = 0; v < vocab; ++v) r[v] = p[v];
+            if (draft) orc_softmax(draft + cur * vocab, vocab, temperature, q);
+            for (int64_t i = 1; i < M && taken < 0; ++i) {
+                if (parent[i] != cur) continue;
+                const int64_t x = tokens[i];
+                const int in = x >= 0 && x < vocab;
+                double left = 0.0;
+                if (draft) {
+                    if (in && (double)uniform[i] * q[x] < r[x]) {
+                        taken = i;
+                        break;
+                    }
+                    for (int64_t v = 0; v < vocab; ++v) left += r[v] = r[v] > q[v] ? r[v] - q[v] : 0.0;
+                    if (left > 0.0)
+                        for (int64_t v = 0; v < vocab; ++v) r[v] /= left;
+                } else {
+                    for (int64_t v = 0; v < vocab; ++v) left += r[v];
+                    if (in && (double)uniform[i] * left < r[x]) taken = i;
+                    else if (in) r[x] = 0.0;
+                }
+            }
+        }
+        if (taken < 0) break;
+        cur = taken;
+    }
+    if (temperature != 0.0) {
+        double total = 0.0, sum = 0.0;
+        for (int64_t v = 0; v < vocab; ++v) total += r[v];
+        if (total <= 0.0) {
+            total = 0.0;
+            for (int64_t v = 0; v < vocab; ++v) total += r[v] = p[v];
+        }
+        for (int64_t v = 0; v < vocab; ++v) {
+            sum += r[v];
+            if (r[v] > 0.0) next = v; /* the last token with any weight, should rounding run past the end */
+            if (sum > (double)uniform[0] * total) break;
+        }
+    }
+    result[0] = (int32_t)n;
+    result[1] = (int32_t)next;
+    for (; n < M; ++n) result[2 + n] = -1;
+    free(p);
+    return ORC_OK;
+}

@@ -26,7 +26,9 @@ __all__ = [
     "muser_fused_residual_dual_rmsnorm", "muser_scratch_bytes",
     "muser_qmatvec_residual_dual_rmsnorm", "muser_qmatvec_residual_dual_rmsnorm_static",
     "MUSER_STATIC_SCRATCH_BYTES", "MUSER_BOUNDARY_SCRATCH_BYTES", "FfnLayer", "muser_ffn_workspace_bytes", "muser_ffn_stack_launches",
-    "muser_ffn_stack", "KvPlane", "muser_kv_ring_write", "muser_kv_snapshot", "muser_kv_restore", "muser_sync", "muser_debug_spin", "muser_debug_occupy",
+    "muser_ffn_stack", "KvPlane", "muser_kv_ring_write", "muser_kv_snapshot", "muser_kv_restore",
+    "muser_kv_tree_attention_scratch_bytes", "muser_kv_tree_attention", "muser_tree_verify_scratch_bytes",
+    "muser_tree_verify", "muser_kv_tree_commit", "muser_sync", "muser_debug_spin", "muser_debug_occupy",
     "muser_device_sm_count", "muser_device_status",
 ]
 
@@ -122,6 +124,12 @@ def lib():
                                         ctypes.POINTER(I64), P]),
             "muser_kv_snapshot": (I, [ctypes.POINTER(KvPlane), I64, I64, P, P, P]),
             "muser_kv_restore": (I, [ctypes.POINTER(KvPlane), P, P, I64, I64, P]),
+            "muser_kv_tree_attention_scratch_bytes": (SZ, [I64, I64, I, I]),
+            "muser_kv_tree_attention": (I, [ctypes.POINTER(KvPlane), ctypes.POINTER(KvPlane), P, P, P, P, I, I, P,
+                                            I64, I64, F, P, P, SZ, P]),
+            "muser_tree_verify_scratch_bytes": (SZ, [I64, I]),
+            "muser_tree_verify": (I, [P, P, P, P, I, I64, ctypes.c_double, P, P, P, SZ, P]),
+            "muser_kv_tree_commit": (I, [ctypes.POINTER(KvPlane), I, P, P, I, P, I, I64, P]),
             "muser_sync": (I, [P, I]),
             "muser_debug_spin": (I, [I64, P]),
             "muser_debug_occupy": (I, [I, I64, P]),
@@ -369,6 +377,70 @@ def muser_kv_restore(plane: KvPlane, k_rows, v_rows, origin_logical: int, length
     _check("muser_kv_restore",
            lib().muser_kv_restore(ctypes.byref(plane), _ptr(k_rows), _ptr(v_rows), origin_logical,
                                   length, _stream(stream)))
+
+
+def _ints(values):
+    """A host int32 array from a sequence; None and ctypes arrays pass through."""
+    if values is None or isinstance(values, ctypes.Array):
+        return values
+    return (ctypes.c_int32 * len(values))(*values)
+
+
+def _ptrs(values):
+    """A host array of device pointers from a sequence; ctypes arrays pass through."""
+    if isinstance(values, ctypes.Array):
+        return values
+    return (ctypes.c_void_p * len(values))(*[_ptr(t) for t in values])
+
+
+def muser_kv_tree_attention_scratch_bytes(kv_dim: int, head_dim: int, M: int, n_heads: int) -> int:
+    return lib().muser_kv_tree_attention_scratch_bytes(kv_dim, head_dim, M, n_heads)
+
+
+def muser_kv_tree_attention(plane: KvPlane, q, k, v, M: int, n_heads: int, out, scale: float, scratch,
+                            scratch_bytes: int, parent=None, window: int = 0, n_sink: int = 0, sink=None, gate=None,
+                            stream=None) -> None:
+    """Attention of M tree rows (K and V in k, v) over the plane and the tree.
+    parent: a sequence or ctypes array of M parent rows (None: a chain); sink: a
+    KvPlane of first tokens, or None."""
+    parent = _ints(parent)
+    if parent is not None and len(parent) != M:
+        raise ValueError("parent: one entry per row")
+    _check("muser_kv_tree_attention",
+           lib().muser_kv_tree_attention(ctypes.byref(plane), None if sink is None else ctypes.byref(sink), _ptr(q),
+                                         _ptr(k), _ptr(v), _ptr(gate), M, n_heads, parent, window, n_sink, scale,
+                                         _ptr(out), _ptr(scratch), scratch_bytes, _stream(stream)))
+
+
+def muser_tree_verify_scratch_bytes(vocab: int, M: int) -> int:
+    return lib().muser_tree_verify_scratch_bytes(vocab, M)
+
+
+def muser_tree_verify(target, draft, tokens, parent, M: int, vocab: int, temperature: float, uniform, result, scratch,
+                      scratch_bytes: int, stream=None) -> None:
+    """draft None: drafted tokens are certain; parent None: a chain.  result
+    (int32 [M + 2]): kept rows, next token, the kept rows, -1 behind them."""
+    parent = _ints(parent)
+    if parent is not None and len(parent) != M:
+        raise ValueError("parent: one entry per row")
+    _check("muser_tree_verify",
+           lib().muser_tree_verify(_ptr(target), _ptr(draft), _ptr(tokens), parent, M, vocab, temperature,
+                                   _ptr(uniform), _ptr(result), _ptr(scratch), scratch_bytes, _stream(stream)))
+
+
+def muser_kv_tree_commit(planes, ks, vs, M: int, path, position: int, stream=None) -> None:
+    """planes: a ctypes array of KvPlane (updated), or a list of KvPlane (whose
+    elements are updated); ks, vs: one tensor or pointer per plane; path: the
+    accepted rows, ascending."""
+    arr = planes if isinstance(planes, ctypes.Array) else (KvPlane * len(planes))(*planes)
+    ks, vs, path = _ptrs(ks), _ptrs(vs), _ints(path)
+    if not (len(ks) == len(arr) == len(vs)):
+        raise ValueError("one k and one v per plane")
+    _check("muser_kv_tree_commit",
+           lib().muser_kv_tree_commit(arr, len(arr), ks, vs, M, path, len(path), position, _stream(stream)))
+    if arr is not planes:
+        for mine, new in zip(planes, arr):
+            mine.len, mine.origin_logical, mine.origin_physical = new.len, new.origin_logical, new.origin_physical
 
 
 def muser_sync(stream=None, timeout_ms: int = -1) -> int:

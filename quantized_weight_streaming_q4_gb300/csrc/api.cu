@@ -8,7 +8,9 @@
 #include <cstdio>
 #include <cmath>
 #include <mutex>
+#include <utility>
 
+#include "attn.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -1135,6 +1137,242 @@ int muser_kv_restore(muser_kv_plane* plane, const uint16_t* k_rows, const uint16
     P.len = len;
     P.origin_logical = origin_logical;
     P.origin_physical = rotation;
+    return MUSER_OK;
+}
+
+// A drafted tree's parent rows: row 0 is the root, every other row's parent
+// is an earlier row (NULL: a chain).  Fills depth when it is not null.
+static int check_tree(const char* fn, const int32_t* parent, int M, int* depth) {
+    for (int i = 0; i < M; ++i) {
+        const int p = parent ? parent[i] : i - 1;
+        if (i == 0 ? p != -1 : (p < 0 || p >= i))
+            return set_error(MUSER_ERR_INVALID_ARG, "%s: parent[%d] = %d (row 0: -1, row i: 0..i-1)", fn, i, p);
+        if (depth) depth[i] = i == 0 ? 0 : depth[p] + 1;
+    }
+    return MUSER_OK;
+}
+
+// Appends the live rows of logical positions [first, last) of a plane to the
+// list of row runs (two when they wrap); returns the number of runs added.
+static int plane_runs(const muser_kv_plane& P, int64_t head_dim, int64_t first, int64_t last, AttnSeg* seg,
+                      int64_t* rows) {
+    int n = 0;
+    const int64_t row_stride = P.head_major ? head_dim : P.kv_dim;
+    const int64_t head_stride = P.head_major ? P.capacity * head_dim : head_dim;
+    while (first < last) {
+        const int64_t slot = (P.origin_physical + (first - P.origin_logical)) % P.capacity;
+        const int64_t count = std::min(last - first, P.capacity - slot);
+        seg[n] = AttnSeg{P.key + slot * row_stride, P.value + slot * row_stride, row_stride, head_stride};
+        rows[n++] = count;
+        first += count;
+    }
+    return n;
+}
+
+// The checks of an attention call's head layout.
+static int check_heads(const char* fn, int64_t kv_dim, int64_t head_dim, int M, int n_heads) {
+    MUSER_TRY(check_M(fn, M));
+    if (head_dim < 1 || kv_dim < 1 || kv_dim % head_dim != 0)
+        return set_error(MUSER_ERR_INVALID_ARG, "%s: bad kv_dim/head_dim", fn);
+    if (n_heads < 1 || n_heads % (kv_dim / head_dim) != 0)
+        return set_error(MUSER_ERR_INVALID_ARG, "%s: n_heads = %d is not a multiple of the %lld K/V heads", fn, n_heads,
+                         (long long)(kv_dim / head_dim));
+    if (head_dim > kAttnMaxHeadDim || n_heads > 1024)
+        return set_error(MUSER_ERR_UNSUPPORTED, "%s: head_dim <= %d and n_heads <= 1024 only", fn, kAttnMaxHeadDim);
+    return MUSER_OK;
+}
+
+size_t muser_kv_tree_attention_scratch_bytes(int64_t kv_dim, int64_t head_dim, int M, int n_heads) {
+    clear_error();
+    if (check_heads("muser_kv_tree_attention_scratch_bytes", kv_dim, head_dim, M, n_heads) != MUSER_OK) return 0;
+    return attn_scratch_bytes(kv_dim, head_dim, M, n_heads);
+}
+
+int muser_kv_tree_attention(const muser_kv_plane* plane, const muser_kv_plane* sink, const float* q, const float* k,
+                            const float* v, const float* gate, int M, int n_heads, const int32_t* parent,
+                            int64_t window, int64_t n_sink, float scale, float* out, void* scratch,
+                            size_t scratch_bytes, void* stream) {
+    clear_error();
+    const char* fn = "muser_kv_tree_attention";
+    MUSER_TRY(check_plane(plane, fn));
+    const muser_kv_plane& P = *plane;
+    MUSER_TRY(check_heads(fn, P.kv_dim, P.head_dim, M, n_heads));
+    int depth[MUSER_MAX_M];
+    MUSER_TRY(check_tree(fn, parent, M, depth));
+    if (sink) {
+        MUSER_TRY(check_plane(sink, fn));
+        if (sink->kv_dim != P.kv_dim || (sink->head_major && sink->head_dim != P.head_dim))
+            return set_error(MUSER_ERR_INVALID_ARG, "%s: the sink plane's kv_dim/head_dim differ from the plane's", fn);
+    }
+    if (window < 0 || n_sink < 0) return set_error(MUSER_ERR_INVALID_ARG, "%s: window and n_sink must be >= 0", fn);
+    if (!std::isfinite(scale)) return set_error(MUSER_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    if (P.len > (int64_t{1} << 29) || (sink && sink->len > (int64_t{1} << 29)))
+        return set_error(MUSER_ERR_UNSUPPORTED, "%s: more than 2^29 cached rows", fn);
+    MUSER_TRY(check_f32(fn, "q", q));
+    MUSER_TRY(check_f32(fn, "k", k));
+    MUSER_TRY(check_f32(fn, "v", v));
+    if (gate) MUSER_TRY(check_f32(fn, "gate", gate));
+    MUSER_TRY(check_f32(fn, "out", out));
+    MUSER_TRY(check_f32(fn, "scratch", scratch));
+    const size_t need = attn_scratch_bytes(P.kv_dim, P.head_dim, M, n_heads);
+    if (scratch_bytes < need)
+        return set_error(MUSER_ERR_INVALID_ARG, "%s: scratch_bytes %zu < %zu", fn, scratch_bytes, need);
+    const size_t nq = static_cast<size_t>(M) * n_heads * P.head_dim * 4u, nk = static_cast<size_t>(M) * P.kv_dim * 4u;
+    const struct { const void* p; size_t n; } in[] = {{q, nq}, {k, nk}, {v, nk}, {gate, gate ? nq : 0}};
+    for (const auto& r : in)
+        if (ranges_overlap(out, nq, r.p, r.n) || ranges_overlap(scratch, scratch_bytes, r.p, r.n))
+            return set_error(MUSER_ERR_INVALID_ARG, "%s: out and scratch must not overlap q, k, v or gate", fn);
+    if (ranges_overlap(out, nq, scratch, scratch_bytes))
+        return set_error(MUSER_ERR_INVALID_ARG, "%s: out and scratch must not overlap", fn);
+
+    AttnArgs a{};
+    a.q = q;
+    a.kt = k;
+    a.vt = v;
+    a.gate = gate;
+    a.out = out;
+    a.M = M;
+    a.H = n_heads;
+    a.D = P.head_dim;
+    a.G = P.kv_dim / P.head_dim;
+    a.group = n_heads / a.G;
+    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    const int64_t first = P.origin_logical, end = first + P.len;  // end: the root's position
+    int deepest = 0;
+    for (int i = 0; i < M; ++i) deepest = std::max(deepest, depth[i]);
+    // every row sees first rows [.., kept) and the window of the deepest one
+    // from `low` on; the cached rows in [edge, low) are in some windows only
+    const int64_t kept = std::min(std::max(n_sink, first), end);
+    int64_t edge = kept, low = kept;
+    if (window > 0) {
+        edge = std::min(end, std::max(kept, end - window + 1));
+        low = std::min(end, std::max(kept, end + deepest - window + 1));
+    }
+    int64_t rows[kAttnMaxSeg], erows[2] = {0, 0};
+    int n = 0;
+    if (sink) n += plane_runs(*sink, P.head_dim, sink->origin_logical,
+                              std::min(std::min(sink->origin_logical + sink->len, n_sink), first), a.seg + n, rows + n);
+    if (low == kept) {
+        n += plane_runs(P, P.head_dim, first, end, a.seg + n, rows + n);
+    } else {
+        n += plane_runs(P, P.head_dim, first, kept, a.seg + n, rows + n);
+        n += plane_runs(P, P.head_dim, low, end, a.seg + n, rows + n);
+    }
+    a.nseg = n;
+    int32_t common = 0;
+    for (int i = 0; i < kAttnMaxSeg; ++i) {
+        if (i < n) common += static_cast<int32_t>(rows[i]);
+        a.seg_end[i] = common;
+    }
+    a.n_common = common;
+    plane_runs(P, P.head_dim, edge, low, a.edge, erows);
+    a.edge0 = static_cast<int32_t>(erows[0]);
+    a.n_edge = static_cast<int32_t>(low - edge);
+    for (int i = 0; i < M; ++i) {
+        const int64_t t = end + depth[i];
+        for (int64_t p = edge; p < low; ++p)
+            if (t - p < window) a.mask[i] |= 1u << (p - edge);
+        for (int j = i; j >= 0; j = j == 0 ? -1 : (parent ? parent[j] : j - 1))
+            if (window == 0 || depth[i] - depth[j] < window || end + depth[j] < n_sink) a.mask[i] |= 1u << (a.n_edge + j);
+    }
+    return launch_attention(a, scratch, as_stream(stream));
+}
+
+size_t muser_tree_verify_scratch_bytes(int64_t vocab, int M) {
+    if (vocab < 1 || vocab > kVerifyMaxVocab || M < 1 || M > MUSER_MAX_M) return 0;
+    return verify_scratch_bytes();
+}
+
+int muser_tree_verify(const float* target, const float* draft, const int32_t* tokens, const int32_t* parent, int M,
+                      int64_t vocab, double temperature, const float* uniform, int32_t* result, void* scratch,
+                      size_t scratch_bytes, void* stream) {
+    clear_error();
+    const char* fn = "muser_tree_verify";
+    MUSER_TRY(check_M(fn, M));
+    MUSER_TRY(check_tree(fn, parent, M, nullptr));
+    if (vocab < 1) return set_error(MUSER_ERR_INVALID_ARG, "%s: vocab = %lld", fn, (long long)vocab);
+    if (vocab > kVerifyMaxVocab)
+        return set_error(MUSER_ERR_UNSUPPORTED, "%s: vocab = %lld above %lld", fn, (long long)vocab,
+                         (long long)kVerifyMaxVocab);
+    if (!(temperature >= 0.0) || !std::isfinite(temperature) || (temperature > 0.0 && temperature < 1e-3))
+        return set_error(MUSER_ERR_INVALID_ARG, "%s: temperature must be 0 (greedy) or at least 0.001", fn);
+    MUSER_TRY(check_f32(fn, "target", target));
+    if (temperature > 0.0) {
+        if (draft) MUSER_TRY(check_f32(fn, "draft", draft));
+        if (!uniform) return set_error(MUSER_ERR_INVALID_ARG, "%s: uniform is NULL", fn);
+        if (!is_aligned(uniform, 4)) return set_error(MUSER_ERR_MISALIGNED, "%s: uniform must be 4-byte aligned", fn);
+    }
+    if (!result || (!tokens && M > 1)) return set_error(MUSER_ERR_INVALID_ARG, "%s: tokens/result NULL", fn);
+    if (!is_aligned(tokens, 4) || !is_aligned(result, 4))
+        return set_error(MUSER_ERR_MISALIGNED, "%s: tokens/result must be 4-byte aligned", fn);
+    MUSER_TRY(check_f32(fn, "scratch", scratch));
+    if (scratch_bytes < verify_scratch_bytes())
+        return set_error(MUSER_ERR_INVALID_ARG, "%s: scratch_bytes %zu < %zu", fn, scratch_bytes, verify_scratch_bytes());
+    const size_t nl = static_cast<size_t>(M) * static_cast<size_t>(vocab) * 4u, nr = (static_cast<size_t>(M) + 2u) * 4u;
+    const struct { const void* p; size_t n; } in[] = {
+        {target, nl}, {temperature > 0.0 ? draft : nullptr, draft && temperature > 0.0 ? nl : 0},
+        {tokens, tokens ? static_cast<size_t>(M) * 4u : 0}, {uniform, uniform ? static_cast<size_t>(M) * 4u : 0}};
+    for (const auto& r : in)
+        if (ranges_overlap(result, nr, r.p, r.n) || ranges_overlap(scratch, scratch_bytes, r.p, r.n))
+            return set_error(MUSER_ERR_INVALID_ARG, "%s: result and scratch must not overlap the inputs", fn);
+    if (ranges_overlap(result, nr, scratch, scratch_bytes))
+        return set_error(MUSER_ERR_INVALID_ARG, "%s: result and scratch must not overlap", fn);
+    return launch_verify(target, draft, tokens, parent, M, vocab, temperature, uniform, result, scratch,
+                         as_stream(stream));
+}
+
+int muser_kv_tree_commit(muser_kv_plane* planes, int n_planes, const float* const* k, const float* const* v, int M,
+                         const int32_t* path, int n, int64_t position, void* stream) {
+    clear_error();
+    const char* fn = "muser_kv_tree_commit";
+    MUSER_TRY(check_M(fn, M));
+    if (n_planes < 1 || n_planes > kCommitMaxPlanes)
+        return set_error(MUSER_ERR_INVALID_ARG, "%s: n_planes = %d outside 1..%d", fn, n_planes, kCommitMaxPlanes);
+    if (!planes) return set_error(MUSER_ERR_INVALID_ARG, "%s: planes is NULL", fn);
+    if (n < 0 || n > M) return set_error(MUSER_ERR_INVALID_ARG, "%s: n = %d outside 0..M", fn, n);
+    if (n > 0 && (!path || !k || !v)) return set_error(MUSER_ERR_INVALID_ARG, "%s: path/k/v NULL", fn);
+    CommitArgs a;
+    a.n_planes = n_planes;
+    a.n = n;
+    for (int j = 0; j < n; ++j) {
+        if (path[j] < 0 || path[j] >= M || (j > 0 && path[j] <= path[j - 1]))
+            return set_error(MUSER_ERR_INVALID_ARG, "%s: path[%d] = %d (rows 0..M-1, ascending)", fn, j, path[j]);
+        a.path[j] = path[j];
+    }
+    std::pair<uintptr_t, uintptr_t> span[2 * kCommitMaxPlanes];
+    for (int i = 0; i < n_planes; ++i) {
+        MUSER_TRY(check_plane(planes + i, fn));
+        const muser_kv_plane& P = planes[i];
+        if (P.origin_logical + P.len != position)
+            return set_error(MUSER_ERR_CACHE_DISCONTINUITY, "%s: plane %d: cache discontinuity: expected position %lld, got %lld",
+                             fn, i, (long long)(P.origin_logical + P.len), (long long)position);
+        if (n == 0) continue;
+        if (!k[i] || !v[i]) return set_error(MUSER_ERR_INVALID_ARG, "%s: k/v of plane %d NULL", fn, i);
+        if (!is_aligned(k[i], 4) || !is_aligned(v[i], 4))
+            return set_error(MUSER_ERR_MISALIGNED, "%s: k/v must be 4-byte aligned", fn);
+        CommitPlane& C = a.plane[i];
+        C = CommitPlane{P.key, P.value, k[i], v[i], P.capacity, (P.origin_physical + P.len) % P.capacity,
+                        P.kv_dim, P.head_major ? P.head_dim : P.kv_dim, P.head_major, 0,
+                        static_cast<int32_t>(std::max<int64_t>(0, n - P.capacity))};
+        C.vec = C.head_dim % 8 == 0 && is_aligned(P.key, 16) && is_aligned(P.value, 16) && is_aligned(k[i], 16) &&
+                is_aligned(v[i], 16);
+        const uintptr_t bytes = static_cast<uintptr_t>(P.capacity) * static_cast<uintptr_t>(P.kv_dim) * 2u;
+        span[2 * i] = {reinterpret_cast<uintptr_t>(P.key), reinterpret_cast<uintptr_t>(P.key) + bytes};
+        span[2 * i + 1] = {reinterpret_cast<uintptr_t>(P.value), reinterpret_cast<uintptr_t>(P.value) + bytes};
+    }
+    if (n == 0) return MUSER_OK;
+    std::sort(span, span + 2 * n_planes);
+    for (int i = 1; i < 2 * n_planes; ++i)
+        if (span[i].first < span[i - 1].second)
+            return set_error(MUSER_ERR_INVALID_ARG, "%s: two planes share memory", fn);
+    MUSER_TRY(launch_kv_commit(a, as_stream(stream)));
+    for (int i = 0; i < n_planes; ++i) {
+        muser_kv_plane& P = planes[i];
+        const int64_t over = std::max<int64_t>(0, P.len + n - P.capacity);
+        P.len = P.len + n - over;
+        P.origin_logical += over;
+        P.origin_physical = (P.origin_physical + over) % P.capacity;
+    }
     return MUSER_OK;
 }
 

@@ -1,0 +1,164 @@
+// attn.cu -- attention of M drafted (tree) rows over a K/V plane, with a
+// sliding window and first tokens that stay visible.
+#include <algorithm>
+
+#include "attn.cuh"
+#include "kernels.cuh"
+
+namespace muser {
+namespace {
+
+constexpr float kNegInf = -INFINITY;
+
+// ------------------------------------------------ any head size, CUDA cores
+// softmax over base 2: s = scale * log2(e) * (q . k), m = running max of s,
+// l = sum 2^(s - m), o = sum 2^(s - m) v; one pass over the rows.  A block
+// takes one K/V head, one chunk of rows and 16 of the group's M * group query
+// vectors; 32 rows at a time sit in shared memory as binary32, a lane scores
+// one row, then owns the output elements d = lane, lane + 32, ...
+constexpr int kGenWarps = 4, kGenQ = 4, kGenTile = 32, kGenMaxD = 256;
+
+template <int ND>  // output elements per lane: D <= 32 * ND
+__global__ void __launch_bounds__(kGenWarps * 32) attn_generic_kernel(const __grid_constant__ AttnArgs a) {
+    extern __shared__ float sm[];
+    const int D = a.D, DP = D + 1;
+    float* ks = sm;                    // [32][D + 1]
+    float* vs = ks + kGenTile * DP;    // [32][D + 1]
+    float* qs = vs + kGenTile * DP;    // [16][D]
+    const int g = blockIdx.y, c = blockIdx.x, rb = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = a.M * a.group;    // row r: tree row r / group, head g * group + r % group
+    const int r0 = rb * kGenWarps * kGenQ;
+    for (int x = threadIdx.x; x < kGenWarps * kGenQ * D; x += blockDim.x) {
+        const int r = r0 + x / D, d = x % D;
+        qs[x] = r < rows ? a.q[static_cast<int64_t>(r / a.group) * a.H * D + (g * a.group + r % a.group) * D + d] : 0.f;
+    }
+    float m[kGenQ], l[kGenQ], o[kGenQ][ND];
+#pragma unroll
+    for (int u = 0; u < kGenQ; ++u) {
+        m[u] = kNegInf;
+        l[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < ND; ++e) o[u][e] = 0.f;
+    }
+    const int first = c * a.chunk, last = min(first + a.chunk, a.n_common);
+    const bool ragged = c == a.nchunks - 1;
+    const int ncommon_tiles = (last - first + kGenTile - 1) / kGenTile;
+    const int ntiles = ncommon_tiles + (ragged ? 1 : 0);
+    for (int t = 0; t < ntiles; ++t) {
+        const bool rag = t == ncommon_tiles;
+        const int n = rag ? a.n_edge + a.M : min(kGenTile, last - first - t * kGenTile);
+        __syncthreads();
+        for (int x = threadIdx.x; x < n * D; x += blockDim.x) {
+            const int r = x / D, d = x % D;
+            if (rag) {
+                ks[r * DP + d] = attn_ragged(a, g, r, d, false);
+                vs[r * DP + d] = attn_ragged(a, g, r, d, true);
+            } else {
+                ks[r * DP + d] = h2f(ldg_u16(attn_row(a, g, first + t * kGenTile + r, false) + d));
+                vs[r * DP + d] = h2f(ldg_u16(attn_row(a, g, first + t * kGenTile + r, true) + d));
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kGenQ; ++u) {
+            const int r = r0 + warp * kGenQ + u;
+            if (r >= rows) break;
+            const uint32_t seen = rag ? a.mask[r / a.group] : (n == 32 ? 0xffffffffu : (1u << n) - 1u);
+            const bool mine = (seen >> lane) & 1u;
+            float s = kNegInf;
+            if (mine) {
+                const float* qr = qs + (warp * kGenQ + u) * D;
+                float acc = 0.f;
+                for (int d = 0; d < D; ++d) acc = fmaf(qr[d], ks[lane * DP + d], acc);
+                s = acc * a.scale_log2;
+            }
+            float tm = s;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, x));
+            const float mn = fmaxf(m[u], tm);
+            if (seen == 0) continue;
+            const float al = m[u] == kNegInf ? 0.f : exp2f(m[u] - mn);
+            const float p = mine ? exp2f(s - mn) : 0.f;
+            l[u] = l[u] * al + warp_sum(p);
+            m[u] = mn;
+#pragma unroll
+            for (int e = 0; e < ND; ++e) o[u][e] *= al;
+            // a row that this query does not see is skipped, whatever it holds
+            for (uint32_t left = seen; left; left &= left - 1) {
+                const int k = __ffs(left) - 1;
+                const float pk = __shfl_sync(0xffffffffu, p, k);
+#pragma unroll
+                for (int e = 0; e < ND; ++e)
+                    if (lane + 32 * e < D) o[u][e] = fmaf(pk, vs[k * DP + lane + 32 * e], o[u][e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kGenQ; ++u) {
+        const int r = r0 + warp * kGenQ + u;
+        if (r >= rows) break;
+        const int64_t row = static_cast<int64_t>(r / a.group) * a.H + g * a.group + r % a.group;
+        const int64_t slot = static_cast<int64_t>(c) * a.M * a.H + row;
+        if (lane == 0) a.part_ml[slot] = make_float2(m[u], l[u]);
+#pragma unroll
+        for (int e = 0; e < ND; ++e)
+            if (lane + 32 * e < D) a.part_o[slot * D + lane + 32 * e] = o[u][e];
+    }
+}
+
+// Joins the chunks: out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c, times
+// sigmoid(gate).  One block per query vector; the chunks in a fixed order.
+__global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnArgs a) {
+    const int64_t row = blockIdx.x, rows = static_cast<int64_t>(a.M) * a.H;
+    float m = kNegInf;
+    for (int c = 0; c < a.nchunks; ++c) m = fmaxf(m, a.part_ml[c * rows + row].x);
+    for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
+        float l = 0.f, o = 0.f;
+        for (int c = 0; c < a.nchunks; ++c) {
+            const float2 ml = a.part_ml[c * rows + row];
+            if (ml.x == kNegInf && ml.y == 0.f) continue;  // a chunk without rows
+            const float w = exp2f(ml.x - m);
+            l = fmaf(w, ml.y, l);
+            o = fmaf(w, a.part_o[(c * rows + row) * a.D + d], o);
+        }
+        o /= l;
+        if (a.gate) o /= 1.f + expf(-a.gate[row * a.D + d]);
+        a.out[row * a.D + d] = o;
+    }
+}
+
+// Chunks of the common rows: about two blocks per SM, at least 64 rows each.
+int generic_chunks(int G, int blocks_per_head, int n_common) {
+    const int want = std::max(1, kAttnBlocks / std::max(1, G * blocks_per_head));
+    return std::max(1, std::min(want, (n_common + 63) / 64));
+}
+
+}  // namespace
+
+size_t attn_scratch_bytes(int64_t kv_dim, int64_t head_dim, int M, int n_heads) {
+    const int64_t G = kv_dim / head_dim, rows = static_cast<int64_t>(M) * (n_heads / G);
+    const int64_t blocks = (rows + kGenWarps * kGenQ - 1) / (kGenWarps * kGenQ);
+    const int64_t chunks = std::max<int64_t>(1, kAttnBlocks / std::max<int64_t>(1, G * blocks));
+    return static_cast<size_t>(chunks * M * n_heads * (head_dim + 2)) * 4u;
+}
+
+int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
+    const int rows = a.M * a.group, blocks = (rows + kGenWarps * kGenQ - 1) / (kGenWarps * kGenQ);
+    a.nchunks = generic_chunks(a.G, blocks, a.n_common);
+    a.chunk = std::max(32, ((a.n_common + a.nchunks - 1) / a.nchunks + 31) / 32 * 32);
+    a.nchunks = std::max(1, (a.n_common + a.chunk - 1) / a.chunk);
+    a.part_ml = static_cast<float2*>(scratch);
+    a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<int64_t>(a.nchunks) * a.M * a.H);
+    const size_t smem = (2 * kGenTile * (a.D + 1) + kGenWarps * kGenQ * a.D) * sizeof(float);
+    const dim3 grid(static_cast<unsigned>(a.nchunks), static_cast<unsigned>(a.G), static_cast<unsigned>(blocks));
+    auto kern = a.D <= 64 ? attn_generic_kernel<2> : a.D <= 128 ? attn_generic_kernel<4> : attn_generic_kernel<8>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
+    kern<<<grid, kGenWarps * 32, smem, s>>>(a);
+    MUSER_TRY(check_launch("attention"));
+    attn_combine_kernel<<<a.M * a.H, 128, 0, s>>>(a);
+    return check_launch("attention combine");
+}
+
+}  // namespace muser

@@ -1,0 +1,75 @@
+// attn.cuh -- what the tree-attention kernels share: the call's arguments as
+// the host lays them out, and the exact treatment of the rows whose
+// visibility differs between query rows.
+#pragma once
+
+#include "common.cuh"
+
+namespace muser {
+
+// A run of consecutive cache slots, read as rows of head_dim binary16 values:
+// row r of K/V head g starts at k + g * head_stride + r * row_stride (the same
+// for v).  Token-major planes have row_stride = kv_dim and head_stride =
+// head_dim; head-major ones row_stride = head_dim and head_stride = capacity *
+// head_dim.
+struct AttnSeg {
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t row_stride, head_stride;
+};
+constexpr int kAttnMaxSeg = 6;   // sink plane, first rows, window: each may wrap once
+constexpr int kAttnMaxRagged = MUSER_MAX_M - 1 + MUSER_MAX_M;  // fits a 32-bit mask
+constexpr int kAttnBlocks = 304;  // blocks that a split aims at: two per SM
+constexpr int kAttnMaxHeadDim = 256;
+
+// One call.  The cached rows that every query row sees are the "common" rows
+// 0..n_common-1, the segments one after another.  The rows only some query
+// rows see are the "ragged" ones: up to 15 cached rows at the window's lower
+// edge (deeper tree rows see less far back), then the M tree rows; bit r of
+// mask[i] says that query row i sees ragged row r.
+struct AttnArgs {
+    const float* q;     // [M][H*D]
+    const float* kt;    // [M][G*D] tree rows
+    const float* vt;
+    const float* gate;  // [M][H*D] or null
+    float* out;
+    int M, H, G, D, group;  // group = H / G query heads per K/V head
+    float scale_log2;       // scale * log2(e)
+    int nseg;
+    AttnSeg seg[kAttnMaxSeg];
+    int32_t seg_end[kAttnMaxSeg];  // common row index behind segment s
+    int32_t n_common;
+    AttnSeg edge[2];  // the ragged cached rows: at most one wrap
+    int32_t edge0;    // rows of edge[0]
+    int32_t n_edge;
+    uint32_t mask[MUSER_MAX_M];
+    // split: chunk c of the common rows is [c * chunk, min((c + 1) * chunk,
+    // n_common)); the ragged rows belong to the last chunk
+    int32_t chunk, nchunks;
+    float* part_o;   // [nchunks][M*H][D]  unnormalised sums
+    float2* part_ml; // [nchunks][M*H]     running maximum (base 2) and sum
+};
+
+__device__ __forceinline__ const uint16_t* attn_row(const AttnArgs& a, int g, int r, bool value) {
+    int s = 0;
+#pragma unroll
+    for (int i = 0; i < kAttnMaxSeg - 1; ++i) s += (i < a.nseg - 1 && r >= a.seg_end[i]) ? 1 : 0;
+    const int r0 = s == 0 ? 0 : a.seg_end[s - 1];
+    const AttnSeg& S = a.seg[s];
+    return (value ? S.v : S.k) + g * S.head_stride + (r - r0) * S.row_stride;
+}
+
+// Element d of ragged row r of K/V head g, binary32.  A tree row's value is
+// rounded to binary16 first: that is what the cache will hold of it.
+__device__ __forceinline__ float attn_ragged(const AttnArgs& a, int g, int r, int d, bool value) {
+    if (r < a.n_edge) {
+        const int e = r < a.edge0 ? 0 : 1;
+        const AttnSeg& S = a.edge[e];
+        const uint16_t* p = (value ? S.v : S.k) + g * S.head_stride + (r - (e ? a.edge0 : 0)) * S.row_stride + d;
+        return h2f(ldg_u16(p));
+    }
+    const float f = (value ? a.vt : a.kt)[(r - a.n_edge) * a.G * a.D + g * a.D + d];
+    return __half2float(__float2half_rn(f));
+}
+
+}  // namespace muser

@@ -167,6 +167,18 @@ bool mvs_supported(int gu_qtype, int down_qtype, int64_t hidden, int64_t ffn, in
 size_t mvs_scratch_bytes(int64_t hidden, int64_t ffn);
 int launch_mvs(MvsArgs a, void* scratch, cudaStream_t s);
 
+// Attention of M tree rows over a K/V plane (attn.cu; attn.cuh has the arguments).
+struct AttnArgs;
+size_t attn_scratch_bytes(int64_t kv_dim, int64_t head_dim, int M, int n_heads);
+int launch_attention(AttnArgs a, void* scratch, cudaStream_t s);
+
+// Verification of drafted tokens (verify.cu).
+constexpr int64_t kVerifyMaxVocab = int64_t{1} << 20;
+size_t verify_scratch_bytes();
+int launch_verify(const float* target, const float* draft, const int32_t* tokens, const int32_t* parent, int M,
+                  int64_t vocab, double temperature, const float* uniform, int32_t* result, void* scratch,
+                  cudaStream_t s);
+
 // misc.cu
 int launch_dequantize(int qtype, const uint8_t* W, int64_t rows, int64_t cols, float* out,
                       cudaStream_t s);
@@ -184,6 +196,24 @@ int launch_kv_store(uint16_t* key, uint16_t* value, const float* k, const float*
 int launch_kv_window(uint16_t* key, uint16_t* value, uint16_t* k_rows, uint16_t* v_rows,
                      int64_t kv_dim, int64_t head_dim, int head_major, int64_t capacity,
                      int64_t phys0, int64_t count, bool to_plane, cudaStream_t s);
+// The accepted rows of a drafted tree appended to many planes (one launch):
+// rows path[j0..n) of k[p] and v[p] go to slots (slot + j) % capacity.  Rows
+// before j0 do not survive the append (a plane of fewer than n slots).
+constexpr int kCommitMaxPlanes = 128;
+struct CommitPlane {
+    uint16_t* key;
+    uint16_t* value;
+    const float* k;
+    const float* v;
+    int64_t capacity, slot;  // slot of row path[0]
+    int32_t kv_dim, head_dim, head_major, vec, j0;
+};
+struct CommitArgs {
+    int n_planes, n;
+    int32_t path[MUSER_MAX_M];
+    CommitPlane plane[kCommitMaxPlanes];
+};
+int launch_kv_commit(const CommitArgs& a, cudaStream_t s);
 int launch_spin(int64_t microseconds, cudaStream_t s);
 // `ctas` blocks that each hold kOccupySmemBytes of shared memory (one block
 // per SM) and busy-wait `microseconds` on the global timer.

@@ -197,6 +197,36 @@ __global__ void kv_store_kernel(uint16_t* key, uint16_t* value, const float* k, 
     }
 }
 
+// The accepted rows of a drafted tree, binary32 to binary16, into the planes
+// of many layers: blockIdx.y is the plane, a thread takes 8 (vec) or 1
+// consecutive elements of one row of K and of V.
+__global__ void kv_commit_kernel(const __grid_constant__ CommitArgs a) {
+    const CommitPlane& P = a.plane[blockIdx.y];
+    const int step = P.vec ? 8 : 1;
+    const int per_row = P.kv_dim / step, total = (a.n - P.j0) * per_row;
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < total; i += gridDim.x * blockDim.x) {
+        const int j = P.j0 + i / per_row, e = (i % per_row) * step;
+        int64_t slot = P.slot + j;  // slot < capacity, j < 16
+        slot %= P.capacity;
+        const int64_t dst = P.head_major ? (static_cast<int64_t>(e / P.head_dim) * P.capacity + slot) * P.head_dim + e % P.head_dim
+                                         : slot * P.kv_dim + e;
+        const int64_t src = static_cast<int64_t>(a.path[j]) * P.kv_dim + e;
+        if (P.vec) {
+            const float4 k0 = __ldg(reinterpret_cast<const float4*>(P.k + src)), k1 = __ldg(reinterpret_cast<const float4*>(P.k + src + 4));
+            const float4 v0 = __ldg(reinterpret_cast<const float4*>(P.v + src)), v1 = __ldg(reinterpret_cast<const float4*>(P.v + src + 4));
+            const auto pack = [](float lo, float hi) {
+                return static_cast<uint32_t>(__half_as_ushort(__float2half_rn(lo))) |
+                       (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(hi))) << 16);
+            };
+            *reinterpret_cast<uint4*>(P.key + dst) = make_uint4(pack(k0.x, k0.y), pack(k0.z, k0.w), pack(k1.x, k1.y), pack(k1.z, k1.w));
+            *reinterpret_cast<uint4*>(P.value + dst) = make_uint4(pack(v0.x, v0.y), pack(v0.z, v0.w), pack(v1.x, v1.y), pack(v1.z, v1.w));
+        } else {
+            P.key[dst] = __half_as_ushort(__float2half_rn(__ldg(P.k + src)));
+            P.value[dst] = __half_as_ushort(__float2half_rn(__ldg(P.v + src)));
+        }
+    }
+}
+
 // Muser book Ch 15 §15.6: moves `count` token rows between a K/V plane pair
 // and detached token-major rows.  Row j of the window <-> physical slot
 // (phys0 + j) % capacity, in either plane layout (§15.3 Figure 15.1).  This
@@ -410,6 +440,18 @@ int launch_kv_window(uint16_t* key, uint16_t* value, uint16_t* k_rows, uint16_t*
         kv_window_kernel<false><<<g, bs, 0, s>>>(key, value, k_rows, v_rows, kv_dim, head_dim,
                                                    head_major, capacity, phys0, count);
     return check_launch("kv_window");
+}
+
+int launch_kv_commit(const CommitArgs& a, cudaStream_t s) {
+    int64_t most = 1;
+    for (int p = 0; p < a.n_planes; ++p) {
+        const int64_t items = static_cast<int64_t>(a.n) * a.plane[p].kv_dim / (a.plane[p].vec ? 8 : 1);
+        most = std::max(most, items);
+    }
+    const int bs = 128;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((most + bs - 1) / bs, 1024)), static_cast<unsigned>(a.n_planes));
+    kv_commit_kernel<<<grid, bs, 0, s>>>(a);
+    return check_launch("kv_commit");
 }
 
 int launch_occupy(int ctas, int64_t microseconds, cudaStream_t s) {
