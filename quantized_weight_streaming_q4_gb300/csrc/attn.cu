@@ -108,14 +108,14 @@ __global__ void __launch_bounds__(kGenWarps * 32) attn_generic_kernel(const __gr
 }
 
 // Joins the chunks: out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c, times
-// sigmoid(gate).  One block per query vector; the chunks in a fixed order.
-__global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnArgs a) {
+// sigmoid(gate).  One block per query vector; the parts in a fixed order.
+__global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnArgs a, int parts) {
     const int64_t row = blockIdx.x, rows = static_cast<int64_t>(a.M) * a.H;
     float m = kNegInf;
-    for (int c = 0; c < a.nchunks; ++c) m = fmaxf(m, a.part_ml[c * rows + row].x);
+    for (int c = 0; c < parts; ++c) m = fmaxf(m, a.part_ml[c * rows + row].x);
     for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
         float l = 0.f, o = 0.f;
-        for (int c = 0; c < a.nchunks; ++c) {
+        for (int c = 0; c < parts; ++c) {
             const float2 ml = a.part_ml[c * rows + row];
             if (ml.x == kNegInf && ml.y == 0.f) continue;  // a chunk without rows
             const float w = exp2f(ml.x - m);
@@ -136,20 +136,36 @@ int generic_chunks(int G, int blocks_per_head, int n_common) {
 
 }  // namespace
 
-size_t attn_scratch_bytes(int64_t kv_dim, int64_t head_dim, int M, int n_heads) {
-    const int64_t G = kv_dim / head_dim, rows = static_cast<int64_t>(M) * (n_heads / G);
+// The most parts a call leaves for the second kernel.
+static int64_t max_parts(int64_t G, int64_t rows) {
     const int64_t blocks = (rows + kGenWarps * kGenQ - 1) / (kGenWarps * kGenQ);
-    const int64_t chunks = std::max<int64_t>(1, kAttnBlocks / std::max<int64_t>(1, G * blocks));
-    return static_cast<size_t>(chunks * M * n_heads * (head_dim + 2)) * 4u;
+    return std::max<int64_t>(1, kAttnBlocks / std::max<int64_t>(1, G * blocks));
 }
 
-int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
+size_t attn_scratch_bytes(int64_t kv_dim, int64_t head_dim, int M, int n_heads) {
+    const int64_t G = kv_dim / head_dim;
+    const int64_t parts = max_parts(G, static_cast<int64_t>(M) * (n_heads / G));
+    return (static_cast<size_t>(parts * M * n_heads * (head_dim + 2)) * 4u + 15u) / 16u * 16u;
+}
+
+namespace {
+
+void place_parts(AttnArgs& a, int parts, void* scratch) {
+    a.part_o = static_cast<float*>(scratch);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(parts) * a.M * a.H * a.D);
+}
+
+int launch_combine(const AttnArgs& a, int parts, cudaStream_t s) {
+    attn_combine_kernel<<<a.M * a.H, 128, 0, s>>>(a, parts);
+    return check_launch("attention combine");
+}
+
+int launch_generic(AttnArgs a, void* scratch, cudaStream_t s) {
     const int rows = a.M * a.group, blocks = (rows + kGenWarps * kGenQ - 1) / (kGenWarps * kGenQ);
     a.nchunks = generic_chunks(a.G, blocks, a.n_common);
     a.chunk = std::max(32, ((a.n_common + a.nchunks - 1) / a.nchunks + 31) / 32 * 32);
     a.nchunks = std::max(1, (a.n_common + a.chunk - 1) / a.chunk);
-    a.part_ml = static_cast<float2*>(scratch);
-    a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<int64_t>(a.nchunks) * a.M * a.H);
+    place_parts(a, a.nchunks, scratch);
     const size_t smem = (2 * kGenTile * (a.D + 1) + kGenWarps * kGenQ * a.D) * sizeof(float);
     const dim3 grid(static_cast<unsigned>(a.nchunks), static_cast<unsigned>(a.G), static_cast<unsigned>(blocks));
     auto kern = a.D <= 64 ? attn_generic_kernel<2> : a.D <= 128 ? attn_generic_kernel<4> : attn_generic_kernel<8>;
@@ -157,8 +173,33 @@ int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
     if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
     kern<<<grid, kGenWarps * 32, smem, s>>>(a);
     MUSER_TRY(check_launch("attention"));
-    attn_combine_kernel<<<a.M * a.H, 128, 0, s>>>(a);
-    return check_launch("attention combine");
+    return launch_combine(a, a.nchunks, s);
+}
+
+}  // namespace
+
+int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
+    if (!attn_mma_supported(a)) return launch_generic(a, scratch, s);
+    const int rows = a.M * a.group, rt = attn_mma_row_tiles(a.D, rows);
+    const int blocks = (rows + 16 * rt - 1) / (16 * rt), heads = a.G * blocks;
+    const int tiles = std::max(1, (a.n_common + 63) / 64);
+    // up to 16 chunks of at least 128 keys: one cluster and no second kernel;
+    // longer ones: about two blocks per SM in clusters of 8
+    const int one = std::min(16, std::max(1, (tiles + 1) / 2));
+    int chunks = one;
+    a.cluster = 1;
+    while (a.cluster < one) a.cluster *= 2;
+    if (tiles > 64 && kAttnBlocks / heads > 16) {
+        a.cluster = 8;
+        chunks = std::min({kAttnBlocks / heads, tiles / 2, static_cast<int>(8 * max_parts(a.G, rows))});
+    }
+    const int per = (tiles + chunks - 1) / chunks;
+    a.chunk = per * 64;
+    a.nchunks = std::max(1, (tiles + per - 1) / per);
+    const int clusters = (a.nchunks + a.cluster - 1) / a.cluster;
+    place_parts(a, clusters, scratch);
+    MUSER_TRY(launch_attn_mma(a, dim3(static_cast<unsigned>(clusters * a.cluster), static_cast<unsigned>(a.G), static_cast<unsigned>(blocks)), rt, s));
+    return clusters > 1 ? launch_combine(a, clusters, s) : MUSER_OK;
 }
 
 }  // namespace muser

@@ -46,8 +46,9 @@ struct AttnArgs {
     // split: chunk c of the common rows is [c * chunk, min((c + 1) * chunk,
     // n_common)); the ragged rows belong to the last chunk
     int32_t chunk, nchunks;
-    float* part_o;   // [nchunks][M*H][D]  unnormalised sums
-    float2* part_ml; // [nchunks][M*H]     running maximum (base 2) and sum
+    int32_t cluster;  // blocks of a cluster (attn_mma.cu); chunks behind nchunks are empty
+    float* part_o;   // [parts][M*H][D]  unnormalised sums, one part per chunk or cluster
+    float2* part_ml; // [parts][M*H]     maximum (base 2) and sum
 };
 
 __device__ __forceinline__ const uint16_t* attn_row(const AttnArgs& a, int g, int r, bool value) {
@@ -71,5 +72,10 @@ __device__ __forceinline__ float attn_ragged(const AttnArgs& a, int g, int r, in
     const float f = (value ? a.vt : a.kt)[(r - a.n_edge) * a.G * a.D + g * a.D + d];
     return __half2float(__float2half_rn(f));
 }
+
+// attn_mma.cu
+bool attn_mma_supported(const AttnArgs& a);
+int attn_mma_row_tiles(int D, int rows);  // 16-row tiles of a block
+int launch_attn_mma(const AttnArgs& a, dim3 grid, int row_tiles, cudaStream_t s);
 
 }  // namespace muser

@@ -1,0 +1,503 @@
+// attn_mma.cu -- tree attention on warp-level matrix products (mma.sync), for
+// head sizes that are multiples of 8 up to 256 and 16-byte aligned planes.
+//
+// A block takes one K/V head, 16 * RT of the group's M * group query vectors
+// and one chunk of the cached rows; its four warps are RT row tiles times
+// 4 / RT shares of every stage's keys.  K and V tiles come by 16-byte
+// asynchronous copies, kStages deep; a row's 16-byte pieces are stored
+// exclusive-or its low three bits, so the fragment loads of eight rows hit
+// eight different bank groups.
+//
+// Precision: the planes are binary16, q is binary32 and so is the result.  A
+// query vector is scaled by a power of two and split into two binary16 parts
+// (22 bits); p = 2^(s - m + 14) is split likewise (the offset keeps the low
+// part of all but vanishing weights out of the subnormals), so both products
+// run twice, and sums are binary32.  One part alone would be off by 2^-12.
+//
+// The blocks of a cluster hold neighbouring chunks of the same rows and join
+// their (maximum, sum, output) triples through distributed shared memory; with
+// one cluster per row block the result is final and there is no second kernel.
+#include <algorithm>
+
+#include "attn.cuh"
+#include "kernels.cuh"
+
+namespace muser {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kTileKeys = 64;
+constexpr float kOffset = 14.f;  // p <= 2^14
+constexpr float kNegInf = -INFINITY;
+
+template <int DP>
+constexpr int kStages = DP == 64 ? 4 : DP == 128 ? 3 : 2;
+template <int DP>
+constexpr int kTileBytes = kTileKeys * DP * 2;  // of K or of V
+template <int DP, int RT>
+struct Layout {
+    static constexpr int R = 16 * RT, KW = kWarps / RT;
+    static constexpr int kOutStride = DP + 8;  // floats; rows 32 bytes apart in the banks
+    static constexpr int kStageOff = 0;
+    static constexpr int kOutOff = kStages<DP> * 2 * kTileBytes<DP>;            // q parts, then the block's output
+    static constexpr int kMlOff = kOutOff + R * kOutStride * 4;                 // float2[R]: the block's maximum and sum
+    static constexpr int kMlwOff = kMlOff + R * 8;                              // float2[KW][R]
+    static constexpr int kScaleOff = kMlwOff + KW * R * 8;                      // float[R]
+    static constexpr int kFlagOff = kScaleOff + R * 4;                          // uint32: ragged rows that are not finite
+    static constexpr int kBytes = kFlagOff + 16;
+    static_assert(R * kOutStride * 4 >= 2 * R * DP * 2, "the q parts fit under the output");
+    static_assert(KW == 1 || KW * R * kOutStride * 4 <= kOutOff, "the warps' outputs fit under the stages");
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// Copies 16 bytes, or zeroes them where `real` is false (src is then not read).
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The parts of two neighbouring elements: x = hi + lo to 22 bits.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(x0, x1);
+    const float2 f = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = pack_h2(x0 - f.x, x1 - f.y);
+}
+// Byte offset of 16-byte piece c of row r in a tile of rows of DP halves.
+template <int DP>
+__device__ __forceinline__ uint32_t piece(int r, int c) {
+    return static_cast<uint32_t>(r * DP * 2 + ((c ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+// 2^(m - M) of a partial result with maximum m, 0 where it has no rows.
+__device__ __forceinline__ float share(float m, float M) { return m == kNegInf ? 0.f : exp2f(m - M); }
+
+// Stage `buf` <- common rows [r0, r0 + 64) of K/V head g; rows at or behind
+// `end`, and pieces behind the head's size, are zero.
+template <int DP>
+__device__ __forceinline__ void load_tile(const AttnArgs& a, int g, int r0, int end, uint32_t buf) {
+    constexpr int kPieces = DP / 8, kRowsAtOnce = kThreads / kPieces;
+    const int c = threadIdx.x % kPieces, first = threadIdx.x / kPieces;
+    const bool in = c * 8 < a.D;
+#pragma unroll
+    for (int j = 0; j < kTileKeys / kRowsAtOnce; ++j) {
+        const int r = first + j * kRowsAtOnce, row = min(r0 + r, end - 1);
+        const bool real = in && r0 + r < end;
+        int s = 0;
+#pragma unroll
+        for (int i = 0; i < kAttnMaxSeg - 1; ++i) s += (i < a.nseg - 1 && row >= a.seg_end[i]) ? 1 : 0;
+        const AttnSeg& S = a.seg[s];
+        const int64_t off = g * S.head_stride + (row - (s == 0 ? 0 : a.seg_end[s - 1])) * S.row_stride + (in ? c * 8 : 0);
+        cp_async16_zfill(buf + piece<DP>(r, c), S.k + off, real);
+        cp_async16_zfill(buf + kTileBytes<DP> + piece<DP>(r, c), S.v + off, real);
+    }
+}
+
+template <int DP, int RT>
+__global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constant__ AttnArgs a) {
+    using L = Layout<DP, RT>;
+    constexpr int R = L::R, KW = L::KW, NS = kStages<DP>;
+    constexpr bool kQReg = DP <= 128;  // the q parts stay in registers
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rt = warp % RT, kw = warp / RT;
+    const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * R;
+    const int rows = a.M * a.group;
+    const int first = min(c * a.chunk, a.n_common), end = min(first + a.chunk, a.n_common);
+    const int ntiles = (end - first + kTileKeys - 1) / kTileKeys;
+    const bool ragged = c == a.nchunks - 1;
+    float* cs = reinterpret_cast<float*>(smem + L::kScaleOff);
+    uint32_t* flags = reinterpret_cast<uint32_t*>(smem + L::kFlagOff);
+    if (tid == 0) *flags = 0;
+
+    // the first stages' copies go out; the last stage is left to the ragged rows
+#pragma unroll
+    for (int t = 0; t < NS - 1; ++t) {
+        if (t < ntiles) load_tile<DP>(a, g, first + t * kTileKeys, end, base + t * 2 * kTileBytes<DP>);
+        cp_async_commit();
+    }
+
+    // q: scaled to base 2 and to [2^7, 2^8), split, into shared memory
+    for (int rr = warp; rr < R; rr += kWarps) {
+        const int r = r0 + rr;
+        float x[DP / 32];
+        float mx = 0.f;
+#pragma unroll
+        for (int u = 0; u < DP / 32; u += 2) {
+            const int d = u * 32 + 2 * lane;
+            float2 f = make_float2(0.f, 0.f);
+            if (r < rows && d < a.D)
+                f = *reinterpret_cast<const float2*>(a.q + (static_cast<int64_t>(r / a.group) * a.H + g * a.group + r % a.group) * a.D + d);
+            x[u] = f.x * a.scale_log2;
+            x[u + 1] = f.y * a.scale_log2;
+            mx = fmaxf(mx, fmaxf(fabsf(x[u]), fabsf(x[u + 1])));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int e = min(100, max(-100, ((__float_as_int(mx) >> 23) & 0xff) - 127)) - 7;
+        const float f = __int_as_float((127 - e) << 23);
+        if (lane == 0) cs[rr] = __int_as_float((127 + e) << 23);
+#pragma unroll
+        for (int u = 0; u < DP / 32; u += 2) {
+            uint32_t hi, lo;
+            split2(x[u] * f, x[u + 1] * f, hi, lo);
+            const uint32_t at = piece<DP>(rr, (u * 32 + 2 * lane) >> 3) + ((2 * lane) & 7) * 2;
+            *reinterpret_cast<uint32_t*>(smem + L::kOutOff + at) = hi;
+            *reinterpret_cast<uint32_t*>(smem + L::kOutOff + R * DP * 2 + at) = lo;
+        }
+    }
+    __syncthreads();
+
+    const int gr = lane >> 2, qt = lane & 3;  // fragment row and column pair
+    uint32_t qh[kQReg ? DP / 16 : 1][4], ql[kQReg ? DP / 16 : 1][4];
+    auto q_addr = [&](int ks) { return base + L::kOutOff + piece<DP>(rt * 16 + (lane & 15), ks * 2 + (lane >> 4)); };
+    if constexpr (kQReg) {
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+            ldsm4(qh[ks], q_addr(ks));
+            ldsm4(ql[ks], q_addr(ks) + R * DP * 2);
+        }
+    }
+    const float c0 = cs[rt * 16 + gr], c1 = cs[rt * 16 + gr + 8];
+    float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;
+    float o[DP / 8][4];
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+
+    // 16 keys of the tile at `kbuf`: keys k0..k0+15; bit j of see0/see1: the
+    // two fragment rows see key k0 + j
+    auto step = [&](uint32_t kbuf, int k0, uint32_t see0, uint32_t see1, bool all) {
+        float sh[2][4], sl[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sh[n][e] = sl[n][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+            uint32_t kf[4];  // keys 0-7: d 0-7, 8-15; keys 8-15: the same
+            ldsm4(kf, kbuf + piece<DP>(k0 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)));
+            if constexpr (kQReg) {
+                mma16816(sl[0], ql[ks], kf[0], kf[1]);
+                mma16816(sl[1], ql[ks], kf[2], kf[3]);
+                mma16816(sh[0], qh[ks], kf[0], kf[1]);
+                mma16816(sh[1], qh[ks], kf[2], kf[3]);
+            } else {
+                uint32_t f[4];
+                ldsm4(f, q_addr(ks) + R * DP * 2);
+                mma16816(sl[0], f, kf[0], kf[1]);
+                mma16816(sl[1], f, kf[2], kf[3]);
+                ldsm4(f, q_addr(ks));
+                mma16816(sh[0], f, kf[0], kf[1]);
+                mma16816(sh[1], f, kf[2], kf[3]);
+            }
+        }
+        float t0 = kNegInf, t1 = kNegInf;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = n * 8 + 2 * qt + e;
+                sh[n][e] = all || ((see0 >> j) & 1u) ? (sh[n][e] + sl[n][e]) * c0 : kNegInf;
+                sh[n][e + 2] = all || ((see1 >> j) & 1u) ? (sh[n][e + 2] + sl[n][e + 2]) * c1 : kNegInf;
+                t0 = fmaxf(t0, sh[n][e]);
+                t1 = fmaxf(t1, sh[n][e + 2]);
+            }
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1) {
+            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
+            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
+        }
+        if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
+            const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+            const float a0 = m0 == kNegInf ? 0.f : ex2(m0 - n0), a1 = m1 == kNegInf ? 0.f : ex2(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n) {
+                o[n][0] *= a0;
+                o[n][1] *= a0;
+                o[n][2] *= a1;
+                o[n][3] *= a1;
+            }
+        }
+        const float b0 = m0 == kNegInf ? 0.f : m0 - kOffset, b1 = m1 == kNegInf ? 0.f : m1 - kOffset;
+        uint32_t ph[4], pl[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const float p0 = ex2(sh[n][0] - b0), p1 = ex2(sh[n][1] - b0);
+            const float p2 = ex2(sh[n][2] - b1), p3 = ex2(sh[n][3] - b1);
+            l0 += p0 + p1;
+            l1 += p2 + p3;
+            split2(p0, p1, ph[2 * n], pl[2 * n]);
+            split2(p2, p3, ph[2 * n + 1], pl[2 * n + 1]);
+        }
+        const uint32_t vbuf = kbuf + kTileBytes<DP>;
+#pragma unroll
+        for (int n = 0; n < DP / 16; ++n) {
+            uint32_t vf[4];  // d 0-7: keys 0-7, 8-15; d 8-15: the same
+            ldsm4t(vf, vbuf + piece<DP>(k0 + (lane & 15), n * 2 + (lane >> 4)));
+            mma16816(o[2 * n], pl, vf[0], vf[1]);
+            mma16816(o[2 * n + 1], pl, vf[2], vf[3]);
+            mma16816(o[2 * n], ph, vf[0], vf[1]);
+            mma16816(o[2 * n + 1], ph, vf[2], vf[3]);
+        }
+    };
+
+    // the ragged rows: up to 31 keys with a mask for each query row.  A value
+    // that is not finite is replaced by 0 and noted, so that it reaches no row
+    // that does not see it; those that do become NaN at the end.
+    bool spoiled0 = false, spoiled1 = false;
+    if (ragged) {
+        const uint32_t buf = (NS - 1) * 2 * kTileBytes<DP>;
+        const int n = a.n_edge + a.M;
+        uint32_t bad = 0;
+        for (int x = tid; x < 32 * DP; x += kThreads) {
+            const int r = x / DP, d = x % DP;
+            float k = 0.f, v = 0.f;
+            if (r < n && d < a.D) {
+                k = attn_ragged(a, g, r, d, false);
+                v = attn_ragged(a, g, r, d, true);
+                if (!(fabsf(k) < INFINITY) || !(fabsf(v) < INFINITY)) {
+                    bad |= 1u << r;
+                    k = v = 0.f;
+                }
+            }
+            const uint32_t at = buf + piece<DP>(r, d >> 3) + (d & 7) * 2;
+            *reinterpret_cast<__half*>(smem + at) = __float2half_rn(k);
+            *reinterpret_cast<__half*>(smem + at + kTileBytes<DP>) = __float2half_rn(v);
+        }
+        if (bad) atomicOr(flags, bad);
+        __syncthreads();
+        const int q0 = r0 + rt * 16 + gr, q1 = q0 + 8;
+        const uint32_t see0 = q0 < rows ? a.mask[q0 / a.group] : 0u, see1 = q1 < rows ? a.mask[q1 / a.group] : 0u;
+        for (int k0 = kw * 16; k0 < n; k0 += KW * 16) step(base + buf, k0, see0 >> k0, see1 >> k0, false);
+        spoiled0 = (see0 & *flags) != 0;
+        spoiled1 = (see1 & *flags) != 0;
+        __syncthreads();
+    }
+
+    for (int t = 0; t < ntiles; ++t) {
+        cp_async_wait<NS - 2>();
+        __syncthreads();
+        {
+            const int nx = t + NS - 1;  // into the stage that every warp has left
+            if (nx < ntiles) load_tile<DP>(a, g, first + nx * kTileKeys, end, base + (nx % NS) * 2 * kTileBytes<DP>);
+            cp_async_commit();
+        }
+        const uint32_t kbuf = base + (t % NS) * 2 * kTileBytes<DP>;
+        const int n = end - first - t * kTileKeys;  // keys of this tile: at least 1
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+            const int k0 = (kw + j * KW) * 16;
+            const uint32_t see = n - k0 >= 16 ? 0xffffu : (1u << max(0, n - k0)) - 1u;
+            if (n > k0) step(kbuf, k0, see, see, n - k0 >= 16);
+        }
+    }
+    cp_async_wait<0>();
+
+    // the block's result: rows' maxima and sums over the warps that share them
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    }
+    if (spoiled0) l0 = NAN;
+    if (spoiled1) l1 = NAN;
+    float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
+    float2* mlw = reinterpret_cast<float2*>(smem + L::kMlwOff);
+    float* out = reinterpret_cast<float*>(smem + L::kOutOff);
+    if (qt == 0) {
+        mlw[kw * R + rt * 16 + gr] = make_float2(m0, l0);
+        mlw[kw * R + rt * 16 + gr + 8] = make_float2(m1, l1);
+    }
+    __syncthreads();  // also: nobody reads the stages or q any more
+    float* mine = KW == 1 ? out : reinterpret_cast<float*>(smem) + kw * R * L::kOutStride;
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) {
+        *reinterpret_cast<float2*>(mine + (rt * 16 + gr) * L::kOutStride + n * 8 + 2 * qt) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2*>(mine + (rt * 16 + gr + 8) * L::kOutStride + n * 8 + 2 * qt) = make_float2(o[n][2], o[n][3]);
+    }
+    if constexpr (KW == 1) {
+        if (tid < R) ml[tid] = mlw[tid];
+    } else {
+        __syncthreads();
+        for (int x = tid; x < R * DP / 4; x += kThreads) {
+            const int r = x / (DP / 4), d = x % (DP / 4) * 4;
+            float M = kNegInf;
+#pragma unroll
+            for (int w = 0; w < KW; ++w) M = fmaxf(M, mlw[w * R + r].x);
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+                const float f = share(mlw[w * R + r].x, M);
+                const float4 v = lds_float4(reinterpret_cast<const float*>(smem) + (w * R + r) * L::kOutStride + d);
+                s.x = fmaf(f, v.x, s.x);
+                s.y = fmaf(f, v.y, s.y);
+                s.z = fmaf(f, v.z, s.z);
+                s.w = fmaf(f, v.w, s.w);
+                l = fmaf(f, mlw[w * R + r].y, l);
+            }
+            *reinterpret_cast<float4*>(out + r * L::kOutStride + d) = s;
+            if (d == 0) ml[r] = make_float2(M, l);
+        }
+    }
+
+    // the cluster's result, each block a share of the elements
+    const uint32_t cs_n = a.cluster, rank = cs_n > 1 ? cluster_rank() : 0;
+    if (cs_n > 1) cluster_sync();
+    else __syncthreads();
+    const int units = R * DP / 4, u0 = static_cast<int>(units * rank / cs_n), u1 = static_cast<int>(units * (rank + 1) / cs_n);
+    const int nclusters = gridDim.x / cs_n;
+    for (int x = u0 + tid; x < u1; x += kThreads) {
+        const int r = x / (DP / 4), d = x % (DP / 4) * 4;
+        if (r0 + r >= rows || d >= a.D) continue;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f, M = kNegInf;
+        const uint32_t mla = base + L::kMlOff + r * 8, oa = base + L::kOutOff + (r * L::kOutStride + d) * 4;
+        if (cs_n == 1) {
+            s = lds_float4(out + r * L::kOutStride + d);
+            M = ml[r].x;
+            l = ml[r].y;
+        } else {
+            for (uint32_t b = 0; b < cs_n; ++b) M = fmaxf(M, ld_cluster2(map_rank(mla, b)).x);
+#pragma unroll 4
+            for (uint32_t b = 0; b < cs_n; ++b) {
+                const float2 w = ld_cluster2(map_rank(mla, b));
+                const float4 v = ld_cluster4(map_rank(oa, b));
+                const float f = share(w.x, M);
+                l = fmaf(f, w.y, l);
+                s.x = fmaf(f, v.x, s.x);
+                s.y = fmaf(f, v.y, s.y);
+                s.z = fmaf(f, v.z, s.z);
+                s.w = fmaf(f, v.w, s.w);
+            }
+        }
+        const int64_t row = static_cast<int64_t>((r0 + r) / a.group) * a.H + g * a.group + (r0 + r) % a.group;
+        if (nclusters > 1) {
+            const int64_t slot = static_cast<int64_t>(c / static_cast<int>(cs_n)) * a.M * a.H + row;
+            *reinterpret_cast<float4*>(a.part_o + slot * a.D + d) = s;
+            if (d == 0) a.part_ml[slot] = make_float2(M, l);
+        } else {
+            const float inv = 1.f / l;
+            float4 y = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+            if (a.gate) {
+                const float4 z = *reinterpret_cast<const float4*>(a.gate + row * a.D + d);
+                y.x /= 1.f + expf(-z.x);
+                y.y /= 1.f + expf(-z.y);
+                y.z /= 1.f + expf(-z.z);
+                y.w /= 1.f + expf(-z.w);
+            }
+            *reinterpret_cast<float4*>(a.out + row * a.D + d) = y;
+        }
+    }
+    if (cs_n > 1) cluster_sync();  // nobody leaves while its shared memory is read
+}
+
+template <int DP, int RT>
+int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
+    using L = Layout<DP, RT>;
+    auto kern = attn_mma_kernel<DP, RT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    if (e == cudaSuccess && a.cluster > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaLaunchKernelEx");
+    return check_launch("attention");
+}
+
+}  // namespace
+
+// Whether the planes' rows can be copied 16 bytes at a time.
+bool attn_mma_supported(const AttnArgs& a) {
+    if (a.D % 8 != 0) return false;
+    auto ok = [](const AttnSeg& s) {
+        return is_aligned(s.k, 16) && is_aligned(s.v, 16) && s.row_stride % 8 == 0 && s.head_stride % 8 == 0;
+    };
+    for (int i = 0; i < a.nseg; ++i)
+        if (!ok(a.seg[i])) return false;
+    return true;
+}
+
+int attn_mma_row_tiles(int D, int rows) {
+    const int rt = rows <= 16 ? 1 : rows <= 32 || D > 128 ? 2 : 4;
+    return rt;
+}
+
+int launch_attn_mma(const AttnArgs& a, dim3 grid, int rt, cudaStream_t s) {
+    if (a.D <= 64) return rt == 1 ? launch<64, 1>(a, grid, s) : rt == 2 ? launch<64, 2>(a, grid, s) : launch<64, 4>(a, grid, s);
+    if (a.D <= 128) return rt == 1 ? launch<128, 1>(a, grid, s) : rt == 2 ? launch<128, 2>(a, grid, s) : launch<128, 4>(a, grid, s);
+    return rt == 1 ? launch<256, 1>(a, grid, s) : launch<256, 2>(a, grid, s);
+}
+
+}  // namespace muser
