@@ -184,18 +184,20 @@ int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
     const int blocks = (rows + 16 * rt - 1) / (16 * rt), heads = a.G * blocks;
     const int tiles = std::max(1, (a.n_common + 63) / 64);
     // up to 16 chunks of at least 128 keys: one cluster and no second kernel;
-    // longer ones: about two blocks per SM in clusters of 8
+    // longer ones: as many clusters of 8 as run at once
     const int one = std::min(16, std::max(1, (tiles + 1) / 2));
     int chunks = one;
     a.cluster = 1;
     while (a.cluster < one) a.cluster *= 2;
-    if (tiles > 64 && kAttnBlocks / heads > 16) {
-        a.cluster = 8;
-        chunks = std::min({kAttnBlocks / heads, tiles / 2, static_cast<int>(8 * max_parts(a.G, rows))});
+    if (tiles > 64) {
+        const int most = attn_mma_resident(a.D, rt) / heads;
+        if (most > 2) {
+            a.cluster = 8;
+            chunks = std::min({8 * most, tiles / 2, static_cast<int>(8 * max_parts(a.G, rows))});
+        }
     }
-    const int per = (tiles + chunks - 1) / chunks;
-    a.chunk = per * 64;
-    a.nchunks = std::max(1, (tiles + per - 1) / per);
+    a.chunk = std::max(64, ((a.n_common + chunks - 1) / chunks + 15) / 16 * 16);
+    a.nchunks = std::max(1, (a.n_common + a.chunk - 1) / a.chunk);
     const int clusters = (a.nchunks + a.cluster - 1) / a.cluster;
     place_parts(a, clusters, scratch);
     MUSER_TRY(launch_attn_mma(a, dim3(static_cast<unsigned>(clusters * a.cluster), static_cast<unsigned>(a.G), static_cast<unsigned>(blocks)), rt, s));

@@ -75,7 +75,8 @@ __device__ __forceinline__ float attn_ragged(const AttnArgs& a, int g, int r, in
 
 // attn_mma.cu
 bool attn_mma_supported(const AttnArgs& a);
-int attn_mma_row_tiles(int D, int rows);  // 16-row tiles of a block
+int attn_mma_row_tiles(int D, int rows);   // 16-row tiles of a block
+int attn_mma_resident(int D, int row_tiles);  // clusters of 8 blocks that run at once (0: unknown)
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int row_tiles, cudaStream_t s);
 
 }  // namespace muser

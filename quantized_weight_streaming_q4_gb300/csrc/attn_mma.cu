@@ -18,6 +18,8 @@
 // their (maximum, sum, output) triples through distributed shared memory; with
 // one cluster per row block the result is final and there is no second kernel.
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "attn.cuh"
 #include "kernels.cuh"
@@ -125,22 +127,60 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
 // 2^(m - M) of a partial result with maximum m, 0 where it has no rows.
 __device__ __forceinline__ float share(float m, float M) { return m == kNegInf ? 0.f : exp2f(m - M); }
 
+// Eight elements from d on of ragged row r, as binary16 (see attn_ragged).
+__device__ __forceinline__ uint4 attn_ragged8(const AttnArgs& a, int g, int r, int d, bool value) {
+    if (r < a.n_edge) {
+        const int e = r < a.edge0 ? 0 : 1;
+        const AttnSeg& S = a.edge[e];
+        return __ldcg(reinterpret_cast<const uint4*>((value ? S.v : S.k) + g * S.head_stride + (r - (e ? a.edge0 : 0)) * S.row_stride + d));
+    }
+    const float4* p = reinterpret_cast<const float4*>((value ? a.vt : a.kt) + (r - a.n_edge) * a.G * a.D + g * a.D + d);
+    const float4 x = __ldcg(p), y = __ldcg(p + 1);
+    return make_uint4(pack_h2(x.x, x.y), pack_h2(x.z, x.w), pack_h2(y.x, y.y), pack_h2(y.z, y.w));
+}
+// Whether one of eight binary16 values is infinite or NaN.
+__device__ __forceinline__ bool not_finite8(uint4 v) {
+    auto two = [](uint32_t w) { return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u; };
+    return two(v.x) || two(v.y) || two(v.z) || two(v.w);
+}
+
 // Stage `buf` <- common rows [r0, r0 + 64) of K/V head g; rows at or behind
-// `end`, and pieces behind the head's size, are zero.
+// `end`, and pieces behind the head's size, are zero.  `s`: the segment of
+// row r0, moved on from tile to tile.
 template <int DP>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, int g, int r0, int end, uint32_t buf) {
-    constexpr int kPieces = DP / 8, kRowsAtOnce = kThreads / kPieces;
+__device__ __forceinline__ void load_tile(const AttnArgs& a, int g, int r0, int end, uint32_t buf, int& s) {
+    constexpr int kPieces = DP / 8, kRowsAtOnce = kThreads / kPieces, kEach = kTileKeys / kRowsAtOnce;
     const int c = threadIdx.x % kPieces, first = threadIdx.x / kPieces;
     const bool in = c * 8 < a.D;
-#pragma unroll
-    for (int j = 0; j < kTileKeys / kRowsAtOnce; ++j) {
-        const int r = first + j * kRowsAtOnce, row = min(r0 + r, end - 1);
-        const bool real = in && r0 + r < end;
-        int s = 0;
-#pragma unroll
-        for (int i = 0; i < kAttnMaxSeg - 1; ++i) s += (i < a.nseg - 1 && row >= a.seg_end[i]) ? 1 : 0;
+    // a row's pieces keep their place modulo 8 rows: kRowsAtOnce is 4, 8 or 16
+    const uint32_t dst = buf + piece<DP>(first, c), dst4 = buf + piece<DP>(first + 4, c);
+    auto at = [&](int j) {
+        return kRowsAtOnce == 4 ? ((j & 1) ? dst4 : dst) + (j >> 1) * 8 * DP * 2 : dst + j * kRowsAtOnce * DP * 2;
+    };
+    while (r0 >= a.seg_end[s]) ++s;
+    if (r0 + kTileKeys <= min(a.seg_end[s], end)) {  // the whole tile in one run of slots
         const AttnSeg& S = a.seg[s];
-        const int64_t off = g * S.head_stride + (row - (s == 0 ? 0 : a.seg_end[s - 1])) * S.row_stride + (in ? c * 8 : 0);
+        const int64_t off = g * S.head_stride + (r0 - (s == 0 ? 0 : a.seg_end[s - 1]) + first) * S.row_stride + (in ? c * 8 : 0);
+        const uint16_t* k = S.k + off;
+        const uint16_t* v = S.v + off;
+        const int64_t step = kRowsAtOnce * S.row_stride;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            cp_async16_zfill(at(j), k, in);
+            cp_async16_zfill(at(j) + kTileBytes<DP>, v, in);
+            k += step;
+            v += step;
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int j = 0; j < kEach; ++j) {
+        const int r = first + j * kRowsAtOnce, row = min(r0 + r, end - 1);
+        int t = s;
+        while (row >= a.seg_end[t]) ++t;
+        const AttnSeg& S = a.seg[t];
+        const int64_t off = g * S.head_stride + (row - (t == 0 ? 0 : a.seg_end[t - 1])) * S.row_stride + (in ? c * 8 : 0);
+        const bool real = in && r0 + r < end;
         cp_async16_zfill(buf + piece<DP>(r, c), S.k + off, real);
         cp_async16_zfill(buf + kTileBytes<DP> + piece<DP>(r, c), S.v + off, real);
     }
@@ -164,40 +204,75 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
     uint32_t* flags = reinterpret_cast<uint32_t*>(smem + L::kFlagOff);
     if (tid == 0) *flags = 0;
 
+    int seg = 0;
     // the first stages' copies go out; the last stage is left to the ragged rows
 #pragma unroll
     for (int t = 0; t < NS - 1; ++t) {
-        if (t < ntiles) load_tile<DP>(a, g, first + t * kTileKeys, end, base + t * 2 * kTileBytes<DP>);
+        if (t < ntiles) load_tile<DP>(a, g, first + t * kTileKeys, end, base + t * 2 * kTileBytes<DP>, seg);
         cp_async_commit();
     }
 
-    // q: scaled to base 2 and to [2^7, 2^8), split, into shared memory
-    for (int rr = warp; rr < R; rr += kWarps) {
-        const int r = r0 + rr;
-        float x[DP / 32];
-        float mx = 0.f;
+    // the ragged rows' loads (below) go out before q's
+    constexpr int kPieces = DP / 8, kEach = 32 * kPieces / kThreads;  // 8-element pieces, of K and of V
+    const int nragged = a.n_edge + a.M;
+    uint4 kp[kEach], vp[kEach];
+    if (ragged) {
 #pragma unroll
-        for (int u = 0; u < DP / 32; u += 2) {
-            const int d = u * 32 + 2 * lane;
-            float2 f = make_float2(0.f, 0.f);
-            if (r < rows && d < a.D)
-                f = *reinterpret_cast<const float2*>(a.q + (static_cast<int64_t>(r / a.group) * a.H + g * a.group + r % a.group) * a.D + d);
-            x[u] = f.x * a.scale_log2;
-            x[u + 1] = f.y * a.scale_log2;
-            mx = fmaxf(mx, fmaxf(fabsf(x[u]), fabsf(x[u + 1])));
+        for (int j = 0; j < kEach; ++j) {
+            const int x = tid + j * kThreads, r = x / kPieces, d = x % kPieces * 8;
+            kp[j] = vp[j] = make_uint4(0, 0, 0, 0);
+            if (r < nragged && d < a.D) {
+                kp[j] = attn_ragged8(a, g, r, d, false);
+                vp[j] = attn_ragged8(a, g, r, d, true);
+            }
+        }
+    }
+
+    // q: scaled to base 2 and to [2^7, 2^8), split, into shared memory; a
+    // warp's rows in batches whose loads are in flight together
+    constexpr int kQRows = R / kWarps, kQBatch = kQRows < 8 ? kQRows : (DP > 128 ? 4 : 8), kQV = (DP + 127) / 128;
+#pragma unroll
+    for (int b = 0; b < kQRows; b += kQBatch) {
+        float4 x[kQBatch][kQV];
+#pragma unroll
+        for (int j = 0; j < kQBatch; ++j) {
+            const int r = r0 + (b + j) * kWarps + warp;
+            const float* row = a.q + (static_cast<int64_t>(r / a.group) * a.H + g * a.group + r % a.group) * a.D;
+#pragma unroll
+            for (int u = 0; u < kQV; ++u) {
+                const int d = u * 128 + 4 * lane;
+                x[j][u] = r < rows && d < a.D ? __ldcg(reinterpret_cast<const float4*>(row + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const int e = min(100, max(-100, ((__float_as_int(mx) >> 23) & 0xff) - 127)) - 7;
-        const float f = __int_as_float((127 - e) << 23);
-        if (lane == 0) cs[rr] = __int_as_float((127 + e) << 23);
+        for (int j = 0; j < kQBatch; ++j) {
+            const int rr = (b + j) * kWarps + warp;
+            float mx = 0.f;
 #pragma unroll
-        for (int u = 0; u < DP / 32; u += 2) {
-            uint32_t hi, lo;
-            split2(x[u] * f, x[u + 1] * f, hi, lo);
-            const uint32_t at = piece<DP>(rr, (u * 32 + 2 * lane) >> 3) + ((2 * lane) & 7) * 2;
-            *reinterpret_cast<uint32_t*>(smem + L::kOutOff + at) = hi;
-            *reinterpret_cast<uint32_t*>(smem + L::kOutOff + R * DP * 2 + at) = lo;
+            for (int u = 0; u < kQV; ++u) {
+                x[j][u].x *= a.scale_log2;
+                x[j][u].y *= a.scale_log2;
+                x[j][u].z *= a.scale_log2;
+                x[j][u].w *= a.scale_log2;
+                mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x[j][u].x), fabsf(x[j][u].y))), fmaxf(fabsf(x[j][u].z), fabsf(x[j][u].w)));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int e = min(100, max(-100, ((__float_as_int(mx) >> 23) & 0xff) - 127)) - 7;
+            const float f = __int_as_float((127 - e) << 23);
+            if (lane == 0) cs[rr] = __int_as_float((127 + e) << 23);
+#pragma unroll
+            for (int u = 0; u < kQV; ++u) {
+                const int d = u * 128 + 4 * lane;
+                uint2 hi, lo;
+                split2(x[j][u].x * f, x[j][u].y * f, hi.x, lo.x);
+                split2(x[j][u].z * f, x[j][u].w * f, hi.y, lo.y);
+                if (d < DP) {
+                    const uint32_t at = piece<DP>(rr, d >> 3) + (d & 7) * 2;
+                    *reinterpret_cast<uint2*>(smem + L::kOutOff + at) = hi;
+                    *reinterpret_cast<uint2*>(smem + L::kOutOff + R * DP * 2 + at) = lo;
+                }
+            }
         }
     }
     __syncthreads();
@@ -307,28 +382,23 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
     bool spoiled0 = false, spoiled1 = false;
     if (ragged) {
         const uint32_t buf = (NS - 1) * 2 * kTileBytes<DP>;
-        const int n = a.n_edge + a.M;
         uint32_t bad = 0;
-        for (int x = tid; x < 32 * DP; x += kThreads) {
-            const int r = x / DP, d = x % DP;
-            float k = 0.f, v = 0.f;
-            if (r < n && d < a.D) {
-                k = attn_ragged(a, g, r, d, false);
-                v = attn_ragged(a, g, r, d, true);
-                if (!(fabsf(k) < INFINITY) || !(fabsf(v) < INFINITY)) {
-                    bad |= 1u << r;
-                    k = v = 0.f;
-                }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int x = tid + j * kThreads, r = x / kPieces;
+            if (not_finite8(kp[j]) || not_finite8(vp[j])) {
+                bad |= 1u << r;
+                kp[j] = vp[j] = make_uint4(0, 0, 0, 0);
             }
-            const uint32_t at = buf + piece<DP>(r, d >> 3) + (d & 7) * 2;
-            *reinterpret_cast<__half*>(smem + at) = __float2half_rn(k);
-            *reinterpret_cast<__half*>(smem + at + kTileBytes<DP>) = __float2half_rn(v);
+            const uint32_t at = buf + piece<DP>(r, x % kPieces);
+            sts_uint4(smem + at, kp[j]);
+            sts_uint4(smem + at + kTileBytes<DP>, vp[j]);
         }
         if (bad) atomicOr(flags, bad);
         __syncthreads();
         const int q0 = r0 + rt * 16 + gr, q1 = q0 + 8;
         const uint32_t see0 = q0 < rows ? a.mask[q0 / a.group] : 0u, see1 = q1 < rows ? a.mask[q1 / a.group] : 0u;
-        for (int k0 = kw * 16; k0 < n; k0 += KW * 16) step(base + buf, k0, see0 >> k0, see1 >> k0, false);
+        for (int k0 = kw * 16; k0 < nragged; k0 += KW * 16) step(base + buf, k0, see0 >> k0, see1 >> k0, false);
         spoiled0 = (see0 & *flags) != 0;
         spoiled1 = (see1 & *flags) != 0;
         __syncthreads();
@@ -339,7 +409,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
         __syncthreads();
         {
             const int nx = t + NS - 1;  // into the stage that every warp has left
-            if (nx < ntiles) load_tile<DP>(a, g, first + nx * kTileKeys, end, base + (nx % NS) * 2 * kTileBytes<DP>);
+            if (nx < ntiles) load_tile<DP>(a, g, first + nx * kTileKeys, end, base + (nx % NS) * 2 * kTileBytes<DP>, seg);
             cp_async_commit();
         }
         const uint32_t kbuf = base + (t % NS) * 2 * kTileBytes<DP>;
@@ -453,27 +523,79 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
 }
 
 template <int DP, int RT>
-int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
-    using L = Layout<DP, RT>;
-    auto kern = attn_mma_kernel<DP, RT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-    if (e == cudaSuccess && a.cluster > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
+cudaLaunchConfig_t config(const AttnArgs& a, dim3 grid, cudaStream_t s, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = L::kBytes;
+    cfg.dynamicSmemBytes = Layout<DP, RT>::kBytes;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, a);
+    return cfg;
+}
+
+// The kernel's attributes, set once per device.
+template <int DP, int RT>
+int prepare() {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaGetDevice");
+    if (dev < 64 && ((done.load(std::memory_order_acquire) >> dev) & 1u)) return MUSER_OK;
+    e = cudaFuncSetAttribute(attn_mma_kernel<DP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP, RT>::kBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_mma_kernel<DP, RT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
+    if (dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+    return MUSER_OK;
+}
+
+template <int DP, int RT>
+int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
+    MUSER_TRY((prepare<DP, RT>()));
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config<DP, RT>(a, grid, s, attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<DP, RT>, a);
     if (e != cudaSuccess) return cuda_fail(e, "attention: cudaLaunchKernelEx");
     return check_launch("attention");
+}
+
+// Clusters of 8 blocks that the device holds at once.
+template <int DP, int RT>
+int resident() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (prepare<DP, RT>() != MUSER_OK || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    AttnArgs a{};
+    a.cluster = 8;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config<DP, RT>(a, dim3(8), nullptr, attr);
+    if (cudaOccupancyMaxActiveClusters(&n, attn_mma_kernel<DP, RT>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// The row tiles' and head sizes' instantiation.
+template <typename F>
+auto dispatch(int D, int rt, F&& f) {
+    using std::integral_constant;
+    auto rows = [&](auto dp) {
+        constexpr int DP = decltype(dp)::value;
+        if (rt == 1) return f(dp, integral_constant<int, 1>{});
+        if (DP > 128 || rt == 2) return f(dp, integral_constant<int, 2>{});
+        return f(dp, integral_constant<int, (DP > 128 ? 2 : 4)>{});
+    };
+    if (D <= 64) return rows(integral_constant<int, 64>{});
+    if (D <= 128) return rows(integral_constant<int, 128>{});
+    return rows(integral_constant<int, 256>{});
 }
 
 }  // namespace
@@ -486,18 +608,19 @@ bool attn_mma_supported(const AttnArgs& a) {
     };
     for (int i = 0; i < a.nseg; ++i)
         if (!ok(a.seg[i])) return false;
+    for (int i = 0; i < 2 && a.n_edge > 0; ++i)
+        if (i == 0 ? !ok(a.edge[0]) : (a.n_edge > a.edge0 && !ok(a.edge[1]))) return false;
     return true;
 }
 
-int attn_mma_row_tiles(int D, int rows) {
-    const int rt = rows <= 16 ? 1 : rows <= 32 || D > 128 ? 2 : 4;
-    return rt;
+int attn_mma_row_tiles(int D, int rows) { return rows <= 16 ? 1 : rows <= 32 || D > 128 ? 2 : 4; }
+
+int attn_mma_resident(int D, int rt) {
+    return dispatch(D, rt, [](auto dp, auto r) { return resident<decltype(dp)::value, decltype(r)::value>(); });
 }
 
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int rt, cudaStream_t s) {
-    if (a.D <= 64) return rt == 1 ? launch<64, 1>(a, grid, s) : rt == 2 ? launch<64, 2>(a, grid, s) : launch<64, 4>(a, grid, s);
-    if (a.D <= 128) return rt == 1 ? launch<128, 1>(a, grid, s) : rt == 2 ? launch<128, 2>(a, grid, s) : launch<128, 4>(a, grid, s);
-    return rt == 1 ? launch<256, 1>(a, grid, s) : launch<256, 2>(a, grid, s);
+    return dispatch(a.D, rt, [&](auto dp, auto r) { return launch<decltype(dp)::value, decltype(r)::value>(a, grid, s); });
 }
 
 }  // namespace muser
