@@ -49,6 +49,7 @@ struct AttnArgs {
     int32_t cluster;  // blocks of a cluster (attn_mma.cu); chunks behind nchunks are empty
     float* part_o;   // [parts][M*H][D]  unnormalised sums, one part per chunk or cluster
     float2* part_ml; // [parts][M*H]     maximum (base 2) and sum
+    unsigned* status;  // device status word (attn_tc.cu)
 };
 
 __device__ __forceinline__ const uint16_t* attn_row(const AttnArgs& a, int g, int r, bool value) {
@@ -78,5 +79,8 @@ bool attn_mma_supported(const AttnArgs& a);
 int attn_mma_row_tiles(int D, int rows);   // 16-row tiles of a block
 int attn_mma_resident(int D, int row_tiles);  // clusters of 8 blocks that run at once (0: unknown)
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int row_tiles, cudaStream_t s);
+// attn_tc.cu: planes that attn_mma_supported() takes, head_dim <= 128
+int attn_tc_resident(int D, int cluster);
+int launch_attn_tc(const AttnArgs& a, dim3 grid, cudaStream_t s);
 
 }  // namespace muser

@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "attn.cuh"
+#include "attn_parts.cuh"
 #include "kernels.cuh"
 
 namespace muser {
@@ -29,8 +30,6 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTileKeys = 64;
-constexpr float kOffset = 14.f;  // p <= 2^14
-constexpr float kNegInf = -INFINITY;
 
 template <int DP>
 constexpr int kStages = DP == 64 ? 4 : DP == 128 ? 3 : 2;
@@ -69,81 +68,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-// Copies 16 bytes, or zeroes them where `real` is false (src is then not read).
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-// The parts of two neighbouring elements: x = hi + lo to 22 bits.
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-    const __half2 h = __floats2half2_rn(x0, x1);
-    const float2 f = __half22float2(h);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = pack_h2(x0 - f.x, x1 - f.y);
-}
 // Byte offset of 16-byte piece c of row r in a tile of rows of DP halves.
 template <int DP>
 __device__ __forceinline__ uint32_t piece(int r, int c) {
     return static_cast<uint32_t>(r * DP * 2 + ((c ^ (r & 7)) << 4));
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
-}
-// 2^(m - M) of a partial result with maximum m, 0 where it has no rows.
-__device__ __forceinline__ float share(float m, float M) { return m == kNegInf ? 0.f : exp2f(m - M); }
-
-// Eight elements from d on of ragged row r, as binary16 (see attn_ragged).
-__device__ __forceinline__ uint4 attn_ragged8(const AttnArgs& a, int g, int r, int d, bool value) {
-    if (r < a.n_edge) {
-        const int e = r < a.edge0 ? 0 : 1;
-        const AttnSeg& S = a.edge[e];
-        return __ldcg(reinterpret_cast<const uint4*>((value ? S.v : S.k) + g * S.head_stride + (r - (e ? a.edge0 : 0)) * S.row_stride + d));
-    }
-    const float4* p = reinterpret_cast<const float4*>((value ? a.vt : a.kt) + (r - a.n_edge) * a.G * a.D + g * a.D + d);
-    const float4 x = __ldcg(p), y = __ldcg(p + 1);
-    return make_uint4(pack_h2(x.x, x.y), pack_h2(x.z, x.w), pack_h2(y.x, y.y), pack_h2(y.z, y.w));
-}
-// Whether one of eight binary16 values is infinite or NaN.
-__device__ __forceinline__ bool not_finite8(uint4 v) {
-    auto two = [](uint32_t w) { return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u; };
-    return two(v.x) || two(v.y) || two(v.z) || two(v.w);
-}
-
 // Stage `buf` <- common rows [r0, r0 + 64) of K/V head g; rows at or behind
 // `end`, and pieces behind the head's size, are zero.  `s`: the segment of
 // row r0, moved on from tile to tile.
@@ -471,71 +400,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
         }
     }
 
-    // the cluster's result, each block a share of the elements
-    const uint32_t cs_n = a.cluster, rank = cs_n > 1 ? cluster_rank() : 0;
-    if (cs_n > 1) cluster_sync();
-    else __syncthreads();
-    const int units = R * DP / 4, u0 = static_cast<int>(units * rank / cs_n), u1 = static_cast<int>(units * (rank + 1) / cs_n);
-    const int nclusters = gridDim.x / cs_n;
-    for (int x = u0 + tid; x < u1; x += kThreads) {
-        const int r = x / (DP / 4), d = x % (DP / 4) * 4;
-        if (r0 + r >= rows || d >= a.D) continue;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f, M = kNegInf;
-        const uint32_t mla = base + L::kMlOff + r * 8, oa = base + L::kOutOff + (r * L::kOutStride + d) * 4;
-        if (cs_n == 1) {
-            s = lds_float4(out + r * L::kOutStride + d);
-            M = ml[r].x;
-            l = ml[r].y;
-        } else {
-            for (uint32_t b = 0; b < cs_n; ++b) M = fmaxf(M, ld_cluster2(map_rank(mla, b)).x);
-#pragma unroll 4
-            for (uint32_t b = 0; b < cs_n; ++b) {
-                const float2 w = ld_cluster2(map_rank(mla, b));
-                const float4 v = ld_cluster4(map_rank(oa, b));
-                const float f = share(w.x, M);
-                l = fmaf(f, w.y, l);
-                s.x = fmaf(f, v.x, s.x);
-                s.y = fmaf(f, v.y, s.y);
-                s.z = fmaf(f, v.z, s.z);
-                s.w = fmaf(f, v.w, s.w);
-            }
-        }
-        const int64_t row = static_cast<int64_t>((r0 + r) / a.group) * a.H + g * a.group + (r0 + r) % a.group;
-        if (nclusters > 1) {
-            const int64_t slot = static_cast<int64_t>(c / static_cast<int>(cs_n)) * a.M * a.H + row;
-            *reinterpret_cast<float4*>(a.part_o + slot * a.D + d) = s;
-            if (d == 0) a.part_ml[slot] = make_float2(M, l);
-        } else {
-            const float inv = 1.f / l;
-            float4 y = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
-            if (a.gate) {
-                const float4 z = *reinterpret_cast<const float4*>(a.gate + row * a.D + d);
-                y.x /= 1.f + expf(-z.x);
-                y.y /= 1.f + expf(-z.y);
-                y.z /= 1.f + expf(-z.z);
-                y.w /= 1.f + expf(-z.w);
-            }
-            *reinterpret_cast<float4*>(a.out + row * a.D + d) = y;
-        }
-    }
-    if (cs_n > 1) cluster_sync();  // nobody leaves while its shared memory is read
-}
-
-template <int DP, int RT>
-cudaLaunchConfig_t config(const AttnArgs& a, dim3 grid, cudaStream_t s, cudaLaunchAttribute* attr) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Layout<DP, RT>::kBytes;
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(a.cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cfg;
+    join_cluster<DP, L::kOutStride, R, kThreads>(a, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff, true);
 }
 
 // The kernel's attributes, set once per device.
@@ -557,7 +422,7 @@ template <int DP, int RT>
 int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
     MUSER_TRY((prepare<DP, RT>()));
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = config<DP, RT>(a, grid, s, attr);
+    const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, kThreads, Layout<DP, RT>::kBytes, s, attr);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<DP, RT>, a);
     if (e != cudaSuccess) return cuda_fail(e, "attention: cudaLaunchKernelEx");
     return check_launch("attention");
@@ -571,10 +436,8 @@ int resident() {
     if (prepare<DP, RT>() != MUSER_OK || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
     int n = known[dev].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    AttnArgs a{};
-    a.cluster = 8;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = config<DP, RT>(a, dim3(8), nullptr, attr);
+    const cudaLaunchConfig_t cfg = cluster_config(8, dim3(8), kThreads, Layout<DP, RT>::kBytes, nullptr, attr);
     if (cudaOccupancyMaxActiveClusters(&n, attn_mma_kernel<DP, RT>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;

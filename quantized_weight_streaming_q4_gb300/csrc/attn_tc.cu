@@ -1,0 +1,465 @@
+// attn_tc.cu -- tree attention on the fifth-generation tensor cores, for head
+// sizes that are multiples of 8 up to 128 and 16-byte aligned planes.
+//
+// A block takes one K/V head, 128 of the group's M * group query vectors (one
+// per TMEM lane) and one chunk of the cached rows, in tiles of up to 128 keys:
+//   S = Q K^T  (tcgen05.mma, A = Q in TMEM, B = K in shared memory)
+//   p = 2^(S - m + 14), written over S in TMEM as the next product's A operand
+//   O = P V    (B = V as it lies in the cache: keys along K, N contiguous)
+// Even and odd tiles are two independent softmax streams, one warpgroup each:
+// a thread owns a query row, holds its maximum, sum and output (128 binary32
+// registers), and nothing passes between lanes.  While one stream's
+// exponentials run, the tensor core works for the other.  Every O tile is a
+// fresh accumulator that the thread adds to its registers: the tensor core's
+// additions truncate, and a long chain of them drifts (8.4e-6 of the result
+// after 3,456 keys on one accumulator; 8 steps do not show).
+//
+// Precision as in attn_mma.cu: q and p are each two binary16 parts, so both
+// products run twice, low parts first.
+//
+// Warps: 0 issues the matrix products, 1-3 copy K and V (16-byte asynchronous
+// copies into core matrices: 8 rows x 16 bytes; the same layout is K's
+// [keys][d] with d along K and V's with d along N), 4-7 and 8-11 are the two
+// streams.
+#include <algorithm>
+#include <atomic>
+
+#include "attn.cuh"
+#include "attn_parts.cuh"
+#include "kernels.cuh"
+
+namespace muser {
+namespace {
+
+constexpr int kThreads = 384, kProducers = 96;
+constexpr int kTile = 128;
+constexpr uint32_t kTmemCols = 512, kColO = 256, kColQ = 384;  // S0, S1 at 0 and 128
+
+template <int DP>
+struct Layout {
+    static constexpr uint32_t kItem = kTile * DP * 2;  // a K or a V tile
+    static constexpr uint32_t kOutStride = DP + 4;     // floats
+    static constexpr uint32_t kOutOff = 4 * kItem;     // items: K0, K1, V0, V1; then q, later the output
+    static constexpr uint32_t kMlOff = kOutOff + 128 * kOutStride * 4;
+    static constexpr uint32_t kMl2Off = kMlOff + 128 * 8;
+    static constexpr uint32_t kBarOff = kMl2Off + 128 * 8;
+    static constexpr uint32_t kBytes = kBarOff + 256;
+};
+enum Bar { kKFull = 0, kVFull = 2, kVEmpty = 4, kSFull = 6, kPFull = 8, kOFull = 10, kOFree = 12, kQReady = 13, kBars = 14 };
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 32 lanes x 32 columns of this warp's lane quadrant, one column a register.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+        "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+        "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+// Shared-memory matrix descriptor, no swizzle.  K along the rows' 16-byte
+// pieces (lbo: the next piece, sbo: the next 8 rows), or N along them (sbo:
+// the next piece, lbo: the next 8 rows).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+}
+// Instruction descriptor: D binary32, A and B binary16, M = 128; bit 16: B
+// has N along its contiguous direction.
+__device__ __forceinline__ uint32_t idesc(uint32_t n, bool b_n_major) {
+    return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accumulate ? 1 : 0)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Keys of tile t (a multiple of 16) and how many of them are real.
+struct Tiles {
+    int first, end, ragged, nragged, n;  // n: tiles, the ragged one first
+    __device__ __forceinline__ int start(int t) const { return first + (t - ragged) * kTile; }
+    __device__ __forceinline__ int real(int t) const { return t < ragged ? nragged : min(kTile, end - start(t)); }
+    __device__ __forceinline__ int keys(int t) const { return (real(t) + 15) & ~15; }
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a) {
+    using L = Layout<DP>;
+    constexpr uint32_t kPiece = 128, kRows8 = DP / 8 * 128;  // byte steps: the next 16-byte piece, the next 8 rows
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + kBars);
+    uint32_t* flags = tmem_slot + 1;
+    const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * 128;
+    const int rows = a.M * a.group;
+    Tiles T;
+    T.first = min(c * a.chunk, a.n_common);
+    T.end = min(T.first + a.chunk, a.n_common);
+    T.ragged = c == a.nchunks - 1 ? 1 : 0;
+    T.nragged = a.n_edge + a.M;
+    T.n = T.ragged + (T.end - T.first + kTile - 1) / kTile;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar[kKFull + i], kProducers);
+            mbar_init(&bar[kVFull + i], kProducers);
+            mbar_init(&bar[kVEmpty + i], 1);
+            mbar_init(&bar[kSFull + i], 1);
+            mbar_init(&bar[kPFull + i], 128);
+            mbar_init(&bar[kOFull + i], 1);  // one per stream: a stream may ask before the other's is done
+        }
+        mbar_init(&bar[kOFree], 128);
+        mbar_init(&bar[kQReady], 256);
+        *flags = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+    auto wait = [&](int b, int phase) {
+        if (ok) ok = mbar_wait_bounded(&bar[b], static_cast<uint32_t>(phase & 1), a.status, kDevStatusWaitTimeout);
+    };
+    float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
+    float2* ml2 = reinterpret_cast<float2*>(smem + L::kMl2Off);
+    float* out = reinterpret_cast<float*>(smem + L::kOutOff);
+
+    if (warp < 4) {
+        set_regs_down<40>();
+        if (warp == 0) {
+            // ------------------------------------------- matrix products
+            if (lane == 0 && T.n > 0) {
+                auto scores = [&](int t) {
+                    const int s = t & 1;
+                    wait(kKFull + s, t >> 1);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t id = idesc(static_cast<uint32_t>(T.keys(t)), false), kb = base + s * L::kItem;
+#pragma unroll
+                    for (int part = 1; part >= 0; --part)  // the low part of q first
+                        for (int ks = 0; ks < DP / 16; ++ks)
+                            mma(tmem + s * 128, tmem + kColQ + part * (DP / 2) + ks * 8,
+                                smem_desc(kb + ks * 2 * kPiece, kPiece, kRows8), id, part == 0 || ks > 0);
+                    mma_commit(&bar[kSFull + s]);
+                };
+                wait(kQReady, 0);
+                tc_fence_after();
+                for (int t = 0; t < 2 && t < T.n && ok; ++t) scores(t);
+                for (int t = 0; t < T.n && ok; ++t) {
+                    const int s = t & 1;
+                    wait(kPFull + s, t >> 1);
+                    wait(kVFull + s, t >> 1);
+                    if (t > 0) wait(kOFree, t - 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t id = idesc(DP, true), vb = base + (2 + s) * L::kItem;
+                    const int steps = T.keys(t) / 16;
+#pragma unroll
+                    for (int part = 1; part >= 0; --part)  // the low part of p first
+                        for (int ks = 0; ks < steps; ++ks)
+                            mma(tmem + kColO, tmem + s * 128 + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8,
+                                smem_desc(vb + ks * 2 * kRows8, kRows8, kPiece), id, part == 0 || ks > 0);
+                    mma_commit(&bar[kOFull + s]);
+                    mma_commit(&bar[kVEmpty + s]);
+                    if (t + 2 < T.n) scores(t + 2);
+                }
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------- K, V copies
+            const int pw = warp - 1, row8 = lane & 7, quarter = lane >> 3;  // a warp copies 8 rows x 4 pieces at once
+            int arrived = 0, seg = 0;  // items (K, V of tile 0, 1, ...) reported full
+            auto report = [&](int upto) {
+                fence_proxy_async_smem();
+                for (; arrived < upto; ++arrived)
+                    mbar_arrive(&bar[((arrived & 1) ? kVFull : kKFull) + ((arrived >> 1) & 1)]);
+            };
+            for (int item = 0; item < 2 * T.n && ok; ++item) {
+                const int t = item >> 1, s = t & 1, v = item & 1;
+                if (t >= 2) {
+                    uint64_t* b = &bar[v ? kVEmpty + s : kSFull + s];
+                    const uint32_t ph = static_cast<uint32_t>((t >> 1) - 1) & 1u;
+                    if (!mbar_try_wait(b, ph, 0)) {  // nothing to copy into: hand over what is under way
+                        cp_async_wait_all();
+                        report(item);
+                        if (!mbar_wait_bounded(b, ph, a.status, kDevStatusWaitTimeout)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                }
+                const uint32_t dst = base + (v * 2 + s) * L::kItem;
+                const int groups = T.keys(t) >> 3;  // 8 rows each
+                if (t < T.ragged) {
+                    // rows whose visibility differs: a value that is not finite becomes 0 and is noted
+                    for (int x = tid - 32; x < groups * 8 * (DP / 8); x += kProducers) {
+                        const int r = x / (DP / 8), p = x % (DP / 8);
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        if (r < T.nragged && p * 8 < a.D) w = attn_ragged8(a, g, r, p * 8, v != 0);
+                        if (not_finite8(w)) {
+                            atomicOr(flags, 1u << r);
+                            w = make_uint4(0, 0, 0, 0);
+                        }
+                        sts_uint4(smem + (v * 2 + s) * L::kItem + (r >> 3) * kRows8 + p * kPiece + (r & 7) * 16, w);
+                    }
+                } else {
+                    const int begin = T.start(t), real = T.real(t);
+                    while (begin >= a.seg_end[seg]) ++seg;
+                    int sg = seg;
+                    for (int x = pw; x < groups * (DP / 32); x += 3) {
+                        const int r = (x / (DP / 32)) * 8 + row8, p = (x % (DP / 32)) * 4 + quarter;
+                        const int row = min(begin + r, T.end - 1);
+                        while (row >= a.seg_end[sg]) ++sg;
+                        const AttnSeg& S = a.seg[sg];
+                        const bool in = p * 8 < a.D;
+                        const uint16_t* src = (v ? S.v : S.k) + g * S.head_stride +
+                                              (row - (sg == 0 ? 0 : a.seg_end[sg - 1])) * S.row_stride + (in ? p * 8 : 0);
+                        cp_async16_zfill(dst + (r >> 3) * kRows8 + p * kPiece + (r & 7) * 16, src, in && r < real);
+                    }
+                }
+                cp_async_commit();
+                if (item > 0) {
+                    cp_async_wait<1>();
+                    report(item);
+                }
+            }
+            cp_async_wait_all();
+            report(2 * T.n);  // every item has been filled unless ok is false: nobody waits for it then
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------- the streams
+        set_regs_up<232>();
+        const int w = (warp - 4) >> 2, row = tid & 127;  // stream, query row = TMEM lane
+        const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        // q: 16-byte copies into the output's place, then each thread its row
+        for (int x = tid - 128; x < 128 * (DP / 4); x += 256) {
+            const int r = x / (DP / 4), d = x % (DP / 4) * 4, qr = r0 + r;
+            const bool real = qr < rows && d < a.D;
+            const float* src = a.q + (real ? (static_cast<int64_t>(qr / a.group) * a.H + g * a.group + qr % a.group) * a.D + d : 0);
+            cp_async16_zfill(base + L::kOutOff + (r * L::kOutStride + d) * 4, src, real);
+        }
+        cp_async_wait_all();
+        named_barrier_sync(1, 256);
+        float mx = 0.f;
+#pragma unroll 8
+        for (int d = 0; d < DP; d += 4) {
+            const float4 x = lds_float4(out + row * L::kOutStride + d);
+            mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+        }
+        mx *= fabsf(a.scale_log2);
+        const int e = min(100, max(-100, ((__float_as_int(mx) >> 23) & 0xff) - 127)) - 7;
+        const float qscale = a.scale_log2, up = __int_as_float((127 - e) << 23), down = __int_as_float((127 + e) << 23);
+#pragma unroll
+        for (int h = 0; h < DP / 64; ++h) {
+            uint32_t q32[32];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float4 x = lds_float4(out + row * L::kOutStride + h * 64 + i * 4);
+                uint32_t hi0, lo0, hi1, lo1;
+                split2(x.x * qscale * up, x.y * qscale * up, hi0, lo0);
+                split2(x.z * qscale * up, x.w * qscale * up, hi1, lo1);
+                q32[2 * i] = w == 0 ? hi0 : lo0;
+                q32[2 * i + 1] = w == 0 ? hi1 : lo1;
+            }
+            tmem_st32(mine + kColQ + w * (DP / 2) + h * 32, q32);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar[kQReady]);
+
+        const uint32_t mask = r0 + row < rows ? a.mask[(r0 + row) / a.group] : 0u;
+        float m = kNegInf, l = 0.f;
+        float o[DP];
+#pragma unroll
+        for (int d = 0; d < DP; ++d) o[d] = 0.f;
+        for (int t = w; t < T.n && ok; t += 2) {
+            const uint32_t scol = mine + w * 128;
+            const int real = T.real(t), chunks = (real + 31) >> 5;
+            const bool ragged = t < T.ragged;
+            // bit j of seen(c): this row sees key 32 c + j
+            auto seen = [&](int ch) {
+                if (ragged) return mask;
+                const int left = real - ch * 32;
+                return left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+            };
+            wait(kSFull + w, t >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            float tm = kNegInf;
+            for (int ch = 0; ch < chunks; ++ch) {
+                float s[32];
+                tmem_ld32(scol + ch * 32, s);
+                const uint32_t see = seen(ch);
+                tc_wait_ld();
+                if (see == 0xffffffffu) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) tm = fmaxf(tm, s[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) tm = fmaxf(tm, (see >> j) & 1u ? s[j] : kNegInf);
+                }
+            }
+            const float mn = fmaxf(m, tm * down);
+            const float al = m == kNegInf ? 0.f : ex2(m - mn);
+            m = mn;
+            const float off = mn == kNegInf ? 0.f : kOffset - mn;
+            float l0 = 0.f, l1 = 0.f;
+            for (int ch = 0; ch < chunks; ++ch) {
+                float s[32];
+                tmem_ld32(scol + ch * 32, s);
+                const uint32_t see = seen(ch);
+                tc_wait_ld();
+                uint32_t p[32];
+                if (see != 0xffffffffu) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) s[j] = (see >> j) & 1u ? s[j] : kNegInf;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float p0 = ex2(fmaf(s[j], down, off)), p1 = ex2(fmaf(s[j + 1], down, off));
+                    l0 += p0;
+                    l1 += p1;
+                    split2(p0, p1, p[j / 2], p[16 + j / 2]);
+                }
+                tmem_st32(scol + ch * 32, p);
+            }
+            l = fmaf(l, al, l0 + l1);
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bar[kPFull + w]);
+            wait(kOFull + w, t >> 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ch = 0; ch < DP / 32; ++ch) {
+                float s[32];
+                tmem_ld32(mine + kColO + ch * 32, s);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[ch * 32 + j] = fmaf(o[ch * 32 + j], al, s[j]);
+            }
+            tc_fence_before();
+            mbar_arrive(&bar[kOFree]);
+        }
+        // the two streams' results joined in the output's place
+        named_barrier_sync(1, 256);  // q is no longer read
+        if (w == 1) {
+            ml2[row] = make_float2(m, l);
+#pragma unroll
+            for (int d = 0; d < DP; d += 4) sts_float4(out + row * L::kOutStride + d, make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]));
+        }
+        named_barrier_sync(1, 256);
+        if (w == 0) {
+            const float2 other = ml2[row];
+            const float M = fmaxf(m, other.x), f = share(m, M), f2 = share(other.x, M);
+            l = fmaf(l, f, other.y * f2);
+            if (mask & *flags) l = NAN;  // this row sees a ragged row that is not finite
+#pragma unroll
+            for (int d = 0; d < DP; d += 4) {
+                const float4 v = lds_float4(out + row * L::kOutStride + d);
+                sts_float4(out + row * L::kOutStride + d,
+                           make_float4(fmaf(o[d], f, v.x * f2), fmaf(o[d + 1], f, v.y * f2), fmaf(o[d + 2], f, v.z * f2),
+                                       fmaf(o[d + 3], f, v.w * f2)));
+            }
+            ml[row] = make_float2(M, l);
+        }
+    }
+    tc_fence_before();
+    ok = __syncthreads_and(ok);
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+    join_cluster<DP, L::kOutStride, 128, kThreads>(a, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff, ok);
+}
+
+template <int DP>
+int prepare() {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaGetDevice");
+    if (dev < 64 && ((done.load(std::memory_order_acquire) >> dev) & 1u)) return MUSER_OK;
+    e = cudaFuncSetAttribute(attn_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::kBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_tc_kernel<DP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
+    if (dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+    return MUSER_OK;
+}
+
+template <int DP>
+int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
+    MUSER_TRY(prepare<DP>());
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, kThreads, Layout<DP>::kBytes, s, attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP>, a);
+    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaLaunchKernelEx");
+    return check_launch("attention");
+}
+
+template <int DP>
+int resident(int cluster) {
+    static std::atomic<int> known[64][5];
+    int dev = 0, k = 0;
+    while ((1 << k) < cluster) ++k;
+    if (prepare<DP>() != MUSER_OK || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+    int n = known[dev][k].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = cluster_config(cluster, dim3(cluster), kThreads, Layout<DP>::kBytes, nullptr, attr);
+    if (cudaOccupancyMaxActiveClusters(&n, attn_tc_kernel<DP>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[dev][k].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+}  // namespace
+
+int attn_tc_resident(int D, int cluster) { return D <= 64 ? resident<64>(cluster) : resident<128>(cluster); }
+
+int launch_attn_tc(const AttnArgs& a, dim3 grid, cudaStream_t s) {
+    return a.D <= 64 ? launch<64>(a, grid, s) : launch<128>(a, grid, s);
+}
+
+}  // namespace muser
