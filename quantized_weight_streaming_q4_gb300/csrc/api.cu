@@ -1162,7 +1162,8 @@ static int plane_runs(const muser_kv_plane& P, int64_t head_dim, int64_t first, 
     while (first < last) {
         const int64_t slot = (P.origin_physical + (first - P.origin_logical)) % P.capacity;
         const int64_t count = std::min(last - first, P.capacity - slot);
-        seg[n] = AttnSeg{P.key + slot * row_stride, P.value + slot * row_stride, row_stride, head_stride};
+        seg[n] = AttnSeg{P.key + slot * row_stride, P.value + slot * row_stride, row_stride, head_stride,
+                         static_cast<int32_t>(count)};
         rows[n++] = count;
         first += count;
     }

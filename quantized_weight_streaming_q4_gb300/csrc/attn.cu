@@ -178,8 +178,6 @@ int launch_generic(AttnArgs a, void* scratch, cudaStream_t s) {
 
 // Tensor-core kernel: 128 query rows a block, tiles of 128 keys.
 int launch_tc(AttnArgs a, void* scratch, cudaStream_t s) {
-    a.status = device_status_word();
-    if (!a.status) return set_error(MUSER_ERR_CUDA, "attention: no device status word");
     const int rows = a.M * a.group, blocks = (rows + 127) / 128, heads = a.G * blocks;
     int chunks = std::min(16, std::max(1, (a.n_common + 127) / 128));
     a.cluster = 1;
@@ -202,6 +200,8 @@ int launch_tc(AttnArgs a, void* scratch, cudaStream_t s) {
 
 int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
     if (!attn_mma_supported(a)) return launch_generic(a, scratch, s);
+    a.status = device_status_word();
+    if (!a.status) return set_error(MUSER_ERR_CUDA, "attention: no device status word");
     if (a.D <= 128 && a.M * a.group > 32) return launch_tc(a, scratch, s);
     const int rows = a.M * a.group, rt = attn_mma_row_tiles(a.D, rows);
     const int blocks = (rows + 16 * rt - 1) / (16 * rt), heads = a.G * blocks;

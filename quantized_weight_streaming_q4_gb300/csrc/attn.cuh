@@ -3,6 +3,8 @@
 // visibility differs between query rows.
 #pragma once
 
+#include <cuda.h>  // CUtensorMap (types only)
+
 #include "common.cuh"
 
 namespace muser {
@@ -16,6 +18,7 @@ struct AttnSeg {
     const uint16_t* k;
     const uint16_t* v;
     int64_t row_stride, head_stride;
+    int32_t rows;
 };
 constexpr int kAttnMaxSeg = 6;   // sink plane, first rows, window: each may wrap once
 constexpr int kAttnMaxRagged = MUSER_MAX_M - 1 + MUSER_MAX_M;  // fits a 32-bit mask
@@ -49,7 +52,7 @@ struct AttnArgs {
     int32_t cluster;  // blocks of a cluster (attn_mma.cu); chunks behind nchunks are empty
     float* part_o;   // [parts][M*H][D]  unnormalised sums, one part per chunk or cluster
     float2* part_ml; // [parts][M*H]     maximum (base 2) and sum
-    unsigned* status;  // device status word (attn_tc.cu)
+    unsigned* status;  // device status word
 };
 
 __device__ __forceinline__ const uint16_t* attn_row(const AttnArgs& a, int g, int r, bool value) {
@@ -74,11 +77,46 @@ __device__ __forceinline__ float attn_ragged(const AttnArgs& a, int g, int r, in
     return __half2float(__float2half_rn(f));
 }
 
+// One tensor map per segment and of K and V each: (64 elements) x (tile rows)
+// x (1 head) boxes of a segment's rows, 128-byte swizzle.  Rows behind the
+// segment's end and elements behind the head's read as zero, so no row that
+// is not in the segment gets into shared memory.
+struct AttnMaps {
+    CUtensorMap k[kAttnMaxSeg], v[kAttnMaxSeg];
+};
+
+// The tiles of one chunk: its common rows in runs of up to `tile` rows that do
+// not cross a segment's end.
+struct AttnWalk {
+    int pos, end, seg;
+    __device__ __forceinline__ AttnWalk(const AttnArgs& a, int c)
+        : pos(min(c * a.chunk, a.n_common)), end(min(pos + a.chunk, a.n_common)), seg(0) {}
+    __device__ __forceinline__ int count(const AttnArgs& a, int tile) const {
+        int n = 0, at = pos;
+        for (int s = 0; at < end; ++s) {
+            const int stop = min(end, a.seg_end[s]);
+            if (stop > at) n += (stop - at + tile - 1) / tile, at = stop;
+        }
+        return n;
+    }
+    // The next tile's rows (it must exist), their segment and first row there.
+    __device__ __forceinline__ int next(const AttnArgs& a, int tile, int& s, int& row) {
+        while (pos >= a.seg_end[seg]) ++seg;
+        s = seg;
+        row = pos - (seg == 0 ? 0 : a.seg_end[seg - 1]);
+        const int n = min(tile, min(end, a.seg_end[seg]) - pos);
+        pos += n;
+        return n;
+    }
+};
+
 // attn_mma.cu
 bool attn_mma_supported(const AttnArgs& a);
 int attn_mma_row_tiles(int D, int rows);   // 16-row tiles of a block
 int attn_mma_resident(int D, int row_tiles);  // clusters of 8 blocks that run at once (0: unknown)
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int row_tiles, cudaStream_t s);
+// The segments' tensor maps, boxes of `tile` rows (attn_mma.cu).
+int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps);
 // attn_tc.cu: planes that attn_mma_supported() takes, head_dim <= 128
 int attn_tc_resident(int D, int cluster);
 int launch_attn_tc(const AttnArgs& a, dim3 grid, cudaStream_t s);

@@ -3,10 +3,10 @@
 //
 // A block takes one K/V head, 16 * RT of the group's M * group query vectors
 // and one chunk of the cached rows; its four warps are RT row tiles times
-// 4 / RT shares of every stage's keys.  K and V tiles come by 16-byte
-// asynchronous copies, kStages deep; a row's 16-byte pieces are stored
-// exclusive-or its low three bits, so the fragment loads of eight rows hit
-// eight different bank groups.
+// 4 / RT shares of every stage's keys.  K and V tiles come by TMA, kStages
+// deep, in its 128-byte swizzle, so the fragment loads of eight rows hit eight
+// different bank groups.  (16-byte asynchronous copies of the same tiles
+// stopped at about 13 bytes a clock and SM: 4,160 GB/s over 130,815 rows.)
 //
 // Precision: the planes are binary16, q is binary32 and so is the result.  A
 // query vector is scaled by a power of two and split into two binary16 parts
@@ -17,8 +17,11 @@
 // The blocks of a cluster hold neighbouring chunks of the same rows and join
 // their (maximum, sum, output) triples through distributed shared memory; with
 // one cluster per row block the result is final and there is no second kernel.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 #include <type_traits>
 
 #include "attn.cuh"
@@ -39,13 +42,13 @@ template <int DP, int RT>
 struct Layout {
     static constexpr int R = 16 * RT, KW = kWarps / RT;
     static constexpr int kOutStride = DP + 8;  // floats; rows 32 bytes apart in the banks
-    static constexpr int kStageOff = 0;
     static constexpr int kOutOff = kStages<DP> * 2 * kTileBytes<DP>;            // q parts, then the block's output
     static constexpr int kMlOff = kOutOff + R * kOutStride * 4;                 // float2[R]: the block's maximum and sum
     static constexpr int kMlwOff = kMlOff + R * 8;                              // float2[KW][R]
     static constexpr int kScaleOff = kMlwOff + KW * R * 8;                      // float[R]
     static constexpr int kFlagOff = kScaleOff + R * 4;                          // uint32: ragged rows that are not finite
-    static constexpr int kBytes = kFlagOff + 16;
+    static constexpr int kBarOff = kFlagOff + 16;                               // uint64[kStages]: a stage has landed
+    static constexpr int kBytes = kBarOff + 8 * kStages<DP>;
     static_assert(R * kOutStride * 4 >= 2 * R * DP * 2, "the q parts fit under the output");
     static_assert(KW == 1 || KW * R * kOutStride * 4 <= kOutOff, "the warps' outputs fit under the stages");
 };
@@ -68,55 +71,8 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-// Byte offset of 16-byte piece c of row r in a tile of rows of DP halves.
-template <int DP>
-__device__ __forceinline__ uint32_t piece(int r, int c) {
-    return static_cast<uint32_t>(r * DP * 2 + ((c ^ (r & 7)) << 4));
-}
-// Stage `buf` <- common rows [r0, r0 + 64) of K/V head g; rows at or behind
-// `end`, and pieces behind the head's size, are zero.  `s`: the segment of
-// row r0, moved on from tile to tile.
-template <int DP>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, int g, int r0, int end, uint32_t buf, int& s) {
-    constexpr int kPieces = DP / 8, kRowsAtOnce = kThreads / kPieces, kEach = kTileKeys / kRowsAtOnce;
-    const int c = threadIdx.x % kPieces, first = threadIdx.x / kPieces;
-    const bool in = c * 8 < a.D;
-    // a row's pieces keep their place modulo 8 rows: kRowsAtOnce is 4, 8 or 16
-    const uint32_t dst = buf + piece<DP>(first, c), dst4 = buf + piece<DP>(first + 4, c);
-    auto at = [&](int j) {
-        return kRowsAtOnce == 4 ? ((j & 1) ? dst4 : dst) + (j >> 1) * 8 * DP * 2 : dst + j * kRowsAtOnce * DP * 2;
-    };
-    while (r0 >= a.seg_end[s]) ++s;
-    if (r0 + kTileKeys <= min(a.seg_end[s], end)) {  // the whole tile in one run of slots
-        const AttnSeg& S = a.seg[s];
-        const int64_t off = g * S.head_stride + (r0 - (s == 0 ? 0 : a.seg_end[s - 1]) + first) * S.row_stride + (in ? c * 8 : 0);
-        const uint16_t* k = S.k + off;
-        const uint16_t* v = S.v + off;
-        const int64_t step = kRowsAtOnce * S.row_stride;
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            cp_async16_zfill(at(j), k, in);
-            cp_async16_zfill(at(j) + kTileBytes<DP>, v, in);
-            k += step;
-            v += step;
-        }
-        return;
-    }
-#pragma unroll 1
-    for (int j = 0; j < kEach; ++j) {
-        const int r = first + j * kRowsAtOnce, row = min(r0 + r, end - 1);
-        int t = s;
-        while (row >= a.seg_end[t]) ++t;
-        const AttnSeg& S = a.seg[t];
-        const int64_t off = g * S.head_stride + (row - (t == 0 ? 0 : a.seg_end[t - 1])) * S.row_stride + (in ? c * 8 : 0);
-        const bool real = in && r0 + r < end;
-        cp_async16_zfill(buf + piece<DP>(r, c), S.k + off, real);
-        cp_async16_zfill(buf + kTileBytes<DP> + piece<DP>(r, c), S.v + off, real);
-    }
-}
-
 template <int DP, int RT>
-__global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps) {
     using L = Layout<DP, RT>;
     constexpr int R = L::R, KW = L::KW, NS = kStages<DP>;
     constexpr bool kQReg = DP <= 128;  // the q parts stay in registers
@@ -126,19 +82,30 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
     const int rt = warp % RT, kw = warp / RT;
     const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * R;
     const int rows = a.M * a.group;
-    const int first = min(c * a.chunk, a.n_common), end = min(first + a.chunk, a.n_common);
-    const int ntiles = (end - first + kTileKeys - 1) / kTileKeys;
+    AttnWalk load(a, c), walk(a, c);
+    const int ntiles = walk.count(a, kTileKeys);
     const bool ragged = c == a.nchunks - 1;
     float* cs = reinterpret_cast<float*>(smem + L::kScaleOff);
     uint32_t* flags = reinterpret_cast<uint32_t*>(smem + L::kFlagOff);
-    if (tid == 0) *flags = 0;
-
-    int seg = 0;
-    // the first stages' copies go out; the last stage is left to the ragged rows
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+    // thread 0: the next tile's boxes into stage t % NS
+    auto load_tile = [&](int t) {
+        int s, row;
+        load.next(a, kTileKeys, s, row);
+        const uint32_t buf = base + (t % NS) * 2 * kTileBytes<DP>;
+        mbar_arrive_expect_tx(&bar[t % NS], 2 * kTileBytes<DP>);
 #pragma unroll
-    for (int t = 0; t < NS - 1; ++t) {
-        if (t < ntiles) load_tile<DP>(a, g, first + t * kTileKeys, end, base + t * 2 * kTileBytes<DP>, seg);
-        cp_async_commit();
+        for (int x = 0; x < DP / 64; ++x) {
+            tma_load_box(buf + x * kTileKeys * 128, &maps.k[s], x, row, g, &bar[t % NS]);
+            tma_load_box(buf + kTileBytes<DP> + x * kTileKeys * 128, &maps.v[s], x, row, g, &bar[t % NS]);
+        }
+    };
+    if (tid == 0) {
+        *flags = 0;
+        for (int i = 0; i < NS; ++i) mbar_init(&bar[i], 1);
+        fence_mbar_init();
+        // the last stage is left to the ragged rows
+        for (int t = 0; t < NS - 1 && t < ntiles; ++t) load_tile(t);
     }
 
     // the ragged rows' loads (below) go out before q's
@@ -197,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
                 split2(x[j][u].x * f, x[j][u].y * f, hi.x, lo.x);
                 split2(x[j][u].z * f, x[j][u].w * f, hi.y, lo.y);
                 if (d < DP) {
-                    const uint32_t at = piece<DP>(rr, d >> 3) + (d & 7) * 2;
+                    const uint32_t at = piece<R>(rr, d >> 3) + (d & 7) * 2;
                     *reinterpret_cast<uint2*>(smem + L::kOutOff + at) = hi;
                     *reinterpret_cast<uint2*>(smem + L::kOutOff + R * DP * 2 + at) = lo;
                 }
@@ -208,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
 
     const int gr = lane >> 2, qt = lane & 3;  // fragment row and column pair
     uint32_t qh[kQReg ? DP / 16 : 1][4], ql[kQReg ? DP / 16 : 1][4];
-    auto q_addr = [&](int ks) { return base + L::kOutOff + piece<DP>(rt * 16 + (lane & 15), ks * 2 + (lane >> 4)); };
+    auto q_addr = [&](int ks) { return base + L::kOutOff + piece<R>(rt * 16 + (lane & 15), ks * 2 + (lane >> 4)); };
     if constexpr (kQReg) {
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
@@ -235,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) {
             uint32_t kf[4];  // keys 0-7: d 0-7, 8-15; keys 8-15: the same
-            ldsm4(kf, kbuf + piece<DP>(k0 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)));
+            ldsm4(kf, kbuf + piece<kTileKeys>(k0 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)));
             if constexpr (kQReg) {
                 mma16816(sl[0], ql[ks], kf[0], kf[1]);
                 mma16816(sl[1], ql[ks], kf[2], kf[3]);
@@ -297,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
 #pragma unroll
         for (int n = 0; n < DP / 16; ++n) {
             uint32_t vf[4];  // d 0-7: keys 0-7, 8-15; d 8-15: the same
-            ldsm4t(vf, vbuf + piece<DP>(k0 + (lane & 15), n * 2 + (lane >> 4)));
+            ldsm4t(vf, vbuf + piece<kTileKeys>(k0 + (lane & 15), n * 2 + (lane >> 4)));
             mma16816(o[2 * n], pl, vf[0], vf[1]);
             mma16816(o[2 * n + 1], pl, vf[2], vf[3]);
             mma16816(o[2 * n], ph, vf[0], vf[1]);
@@ -319,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
                 bad |= 1u << r;
                 kp[j] = vp[j] = make_uint4(0, 0, 0, 0);
             }
-            const uint32_t at = buf + piece<DP>(r, x % kPieces);
+            const uint32_t at = buf + piece<kTileKeys>(r, x % kPieces);
             sts_uint4(smem + at, kp[j]);
             sts_uint4(smem + at + kTileBytes<DP>, vp[j]);
         }
@@ -333,16 +300,19 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
         __syncthreads();
     }
 
+    bool ok = true;
+    int landed = 0;
     for (int t = 0; t < ntiles; ++t) {
-        cp_async_wait<NS - 2>();
+        int sg, row;
+        const int n = walk.next(a, kTileKeys, sg, row);  // keys of this tile: at least 1
+        ok = ok && mbar_wait_bounded(&bar[t % NS], static_cast<uint32_t>(t / NS) & 1u, a.status, kDevStatusWaitTimeout);
+        landed += ok ? 1 : 0;
         __syncthreads();
-        {
-            const int nx = t + NS - 1;  // into the stage that every warp has left
-            if (nx < ntiles) load_tile<DP>(a, g, first + nx * kTileKeys, end, base + (nx % NS) * 2 * kTileBytes<DP>, seg);
-            cp_async_commit();
+        if (tid == 0 && ok && t + NS - 1 < ntiles) {  // into the stage that every warp has left
+            fence_proxy_async_smem();
+            load_tile(t + NS - 1);
         }
         const uint32_t kbuf = base + (t % NS) * 2 * kTileBytes<DP>;
-        const int n = end - first - t * kTileKeys;  // keys of this tile: at least 1
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
             const int k0 = (kw + j * KW) * 16;
@@ -350,7 +320,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
             if (n > k0) step(kbuf, k0, see, see, n - k0 >= 16);
         }
     }
-    cp_async_wait<0>();
+    if (tid == 0 && !ok)  // the copies under way still write into this block's memory
+        for (int t = landed; t < min(ntiles, landed + NS); ++t)
+            mbar_wait_bounded(&bar[t % NS], static_cast<uint32_t>(t / NS) & 1u, a.status, kDevStatusTxTimeout);
+    ok = __syncthreads_and(ok);
 
     // the block's result: rows' maxima and sums over the warps that share them
 #pragma unroll
@@ -400,7 +373,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
         }
     }
 
-    join_cluster<DP, L::kOutStride, R, kThreads>(a, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff, true);
+    join_cluster<DP, L::kOutStride, R, kThreads>(a, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff, ok);
 }
 
 // The kernel's attributes, set once per device.
@@ -423,7 +396,9 @@ int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
     MUSER_TRY((prepare<DP, RT>()));
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, kThreads, Layout<DP, RT>::kBytes, s, attr);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<DP, RT>, a);
+    AttnMaps maps;
+    MUSER_TRY(encode_attn_maps(a, kTileKeys, maps));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<DP, RT>, a, maps);
     if (e != cudaSuccess) return cuda_fail(e, "attention: cudaLaunchKernelEx");
     return check_launch("attention");
 }
@@ -480,6 +455,33 @@ int attn_mma_row_tiles(int D, int rows) { return rows <= 16 ? 1 : rows <= 32 || 
 
 int attn_mma_resident(int D, int rt) {
     return dispatch(D, rt, [](auto dp, auto r) { return resident<decltype(dp)::value, decltype(r)::value>(); });
+}
+
+int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps) {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    if (fn == nullptr) return set_error(MUSER_ERR_CUDA, "attention: cuTensorMapEncodeTiled is not available");
+    for (int i = 0; i < a.nseg; ++i)
+        for (int v = 0; v < 2; ++v) {
+            const AttnSeg& S = a.seg[i];
+            const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(S.rows), static_cast<cuuint64_t>(a.G)};
+            const cuuint64_t strides[2] = {static_cast<cuuint64_t>(S.row_stride) * 2, static_cast<cuuint64_t>(S.head_stride) * 2};
+            const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(tile), 1}, one[3] = {1, 1, 1};
+            const CUresult r = fn(v ? &maps.v[i] : &maps.k[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                                  const_cast<uint16_t*>(v ? S.v : S.k), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+            if (r != CUDA_SUCCESS)
+                return set_error(MUSER_ERR_CUDA, "attention: cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+        }
+    return MUSER_OK;
 }
 
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int rt, cudaStream_t s) {

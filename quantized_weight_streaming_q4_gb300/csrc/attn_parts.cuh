@@ -81,6 +81,23 @@ __device__ __forceinline__ bool not_finite8(uint4 v) {
     return two(v.x) || two(v.y) || two(v.z) || two(v.w);
 }
 
+// A box of a segment's rows into shared memory (see AttnMaps): elements
+// [64 x, 64 x + 64), rows from `row` on, of head g.
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, int x, int row, int g, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst),
+        "l"(map), "r"(x * 64), "r"(row), "r"(g), "r"(smem_u32(bar))
+        : "memory");
+}
+// Byte offset of 16-byte piece c of row r in a tile of ROWS rows: blocks of 64
+// elements, 128 bytes a row, the piece's low three bits exclusive-or the row's
+// (the tensor maps' 128-byte swizzle; eight rows' pieces hit eight bank groups).
+template <int ROWS>
+__device__ __forceinline__ uint32_t piece(int r, int c) {
+    return static_cast<uint32_t>((c >> 3) * ROWS * 128 + r * 128 + (((c ^ r) & 7) << 4));
+}
+
 // The cluster's result: the blocks hold the same R query rows' (maximum, sum)
 // pairs at shared address mla and outputs at oa (row stride STRIDE floats);
 // each joins a share of the elements and writes them out, final or as a part.

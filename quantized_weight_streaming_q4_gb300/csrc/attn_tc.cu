@@ -17,10 +17,11 @@
 // Precision as in attn_mma.cu: q and p are each two binary16 parts, so both
 // products run twice, low parts first.
 //
-// Warps: 0 issues the matrix products, 1-3 copy K and V (16-byte asynchronous
-// copies into core matrices: 8 rows x 16 bytes; the same layout is K's
-// [keys][d] with d along K and V's with d along N), 4-7 and 8-11 are the two
-// streams.
+// Warps: 0 issues the matrix products, 1 and 2 the TMA loads of K and of V
+// (128-byte swizzle: K with d contiguous along the product's K, V along its
+// N), 4-7 and 8-11 are the two streams; 1-3 also store the rows whose
+// visibility differs.  K and V wait for their buffers apart: one thread for
+// both held a free K buffer back behind V's.
 #include <algorithm>
 #include <atomic>
 
@@ -31,7 +32,7 @@
 namespace muser {
 namespace {
 
-constexpr int kThreads = 384, kProducers = 96;
+constexpr int kThreads = 384;
 constexpr int kTile = 128;
 constexpr uint32_t kTmemCols = 512, kColO = 256, kColQ = 384;  // S0, S1 at 0 and 128
 
@@ -39,7 +40,7 @@ template <int DP>
 struct Layout {
     static constexpr uint32_t kItem = kTile * DP * 2;  // a K or a V tile
     static constexpr uint32_t kOutStride = DP + 4;     // floats
-    static constexpr uint32_t kOutOff = 4 * kItem;     // items: K0, K1, V0, V1; then q, later the output
+    static constexpr uint32_t kOutOff = 4 * kItem;     // behind K0, K1, V0, V1: q, later the output
     static constexpr uint32_t kMlOff = kOutOff + 128 * kOutStride * 4;
     static constexpr uint32_t kMl2Off = kMlOff + 128 * 8;
     static constexpr uint32_t kBarOff = kMl2Off + 128 * 8;
@@ -73,23 +74,24 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
         : "r"(taddr)
         : "memory");
 }
-// Shared-memory matrix descriptor, no swizzle.  K along the rows' 16-byte
-// pieces (lbo: the next piece, sbo: the next 8 rows), or N along them (sbo:
-// the next piece, lbo: the next 8 rows).
+// Shared-memory matrix descriptor, 128-byte swizzle: sbo the next 8 rows; lbo,
+// where the rows' elements lie along N, the next 64 of them.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
     return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 // Instruction descriptor: D binary32, A and B binary16, M = 128; bit 16: B
 // has N along its contiguous direction.
 __device__ __forceinline__ uint32_t idesc(uint32_t n, bool b_n_major) {
     return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate) {
+// One product of 16 along K; ACC: add to D.
+template <bool ACC>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t id) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"(accumulate ? 1 : 0)
+        "r"(a), "l"(b), "r"(id), "n"(ACC ? 1 : 0)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -105,18 +107,10 @@ __device__ __forceinline__ void set_regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Keys of tile t (a multiple of 16) and how many of them are real.
-struct Tiles {
-    int first, end, ragged, nragged, n;  // n: tiles, the ragged one first
-    __device__ __forceinline__ int start(int t) const { return first + (t - ragged) * kTile; }
-    __device__ __forceinline__ int real(int t) const { return t < ragged ? nragged : min(kTile, end - start(t)); }
-    __device__ __forceinline__ int keys(int t) const { return (real(t) + 15) & ~15; }
-};
-
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps) {
     using L = Layout<DP>;
-    constexpr uint32_t kPiece = 128, kRows8 = DP / 8 * 128;  // byte steps: the next 16-byte piece, the next 8 rows
+    constexpr uint32_t kHalf = kTile * 128;  // bytes from 64 elements of a tile's rows to the next 64
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -125,17 +119,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     uint32_t* flags = tmem_slot + 1;
     const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * 128;
     const int rows = a.M * a.group;
-    Tiles T;
-    T.first = min(c * a.chunk, a.n_common);
-    T.end = min(T.first + a.chunk, a.n_common);
-    T.ragged = c == a.nchunks - 1 ? 1 : 0;
-    T.nragged = a.n_edge + a.M;
-    T.n = T.ragged + (T.end - T.first + kTile - 1) / kTile;
+    // tile 0 of the last chunk holds the ragged rows; the common ones follow
+    AttnWalk walk(a, c);
+    const int ragged = c == a.nchunks - 1 ? 1 : 0, nragged = a.n_edge + a.M;
+    const int ntiles = ragged + walk.count(a, kTile);
+    auto next_tile = [&](int t, int& s, int& row) { return t < ragged ? nragged : walk.next(a, kTile, s, row); };
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar[kKFull + i], kProducers);
-            mbar_init(&bar[kVFull + i], kProducers);
+            mbar_init(&bar[kKFull + i], 1);
+            mbar_init(&bar[kVFull + i], 1);
             mbar_init(&bar[kVEmpty + i], 1);
             mbar_init(&bar[kSFull + i], 1);
             mbar_init(&bar[kPFull + i], 128);
@@ -166,103 +159,90 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         set_regs_down<40>();
         if (warp == 0) {
             // ------------------------------------------- matrix products
-            if (lane == 0 && T.n > 0) {
+            if (lane == 0 && ntiles > 0) {
+                int keys[2];  // of the tiles in the two score buffers, a multiple of 16
                 auto scores = [&](int t) {
                     const int s = t & 1;
+                    int sg, row;
+                    keys[s] = (next_tile(t, sg, row) + 15) & ~15;
                     wait(kKFull + s, t >> 1);
                     if (!ok) return;
                     tc_fence_after();
-                    const uint32_t id = idesc(static_cast<uint32_t>(T.keys(t)), false), kb = base + s * L::kItem;
+                    const uint32_t id = idesc(static_cast<uint32_t>(keys[s]), false), d = tmem + s * 128, q = tmem + kColQ;
+                    const uint64_t kd = smem_desc(base + s * L::kItem, 16, 1024);
+                    auto at = [&](int ks) { return kd + ((ks >> 2) * kHalf + (ks & 3) * 32 >> 4); };
+                    mma<false>(d, q + DP / 2, kd, id);  // the low part of q first
 #pragma unroll
-                    for (int part = 1; part >= 0; --part)  // the low part of q first
-                        for (int ks = 0; ks < DP / 16; ++ks)
-                            mma(tmem + s * 128, tmem + kColQ + part * (DP / 2) + ks * 8,
-                                smem_desc(kb + ks * 2 * kPiece, kPiece, kRows8), id, part == 0 || ks > 0);
+                    for (int ks = 1; ks < DP / 16; ++ks) mma<true>(d, q + DP / 2 + ks * 8, at(ks), id);
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks) mma<true>(d, q + ks * 8, at(ks), id);
                     mma_commit(&bar[kSFull + s]);
                 };
                 wait(kQReady, 0);
                 tc_fence_after();
-                for (int t = 0; t < 2 && t < T.n && ok; ++t) scores(t);
-                for (int t = 0; t < T.n && ok; ++t) {
+                for (int t = 0; t < 2 && t < ntiles && ok; ++t) scores(t);
+                for (int t = 0; t < ntiles && ok; ++t) {
                     const int s = t & 1;
                     wait(kPFull + s, t >> 1);
                     wait(kVFull + s, t >> 1);
                     if (t > 0) wait(kOFree, t - 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t id = idesc(DP, true), vb = base + (2 + s) * L::kItem;
-                    const int steps = T.keys(t) / 16;
+                    const uint32_t id = idesc(DP, true), d = tmem + kColO, p = tmem + s * 128;
+                    const uint64_t vd = smem_desc(base + (2 + s) * L::kItem, kHalf, 1024);
+                    const int steps = keys[s] / 16;
+                    mma<false>(d, p + 16, vd, id);  // the low part of p first
 #pragma unroll
-                    for (int part = 1; part >= 0; --part)  // the low part of p first
-                        for (int ks = 0; ks < steps; ++ks)
-                            mma(tmem + kColO, tmem + s * 128 + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8,
-                                smem_desc(vb + ks * 2 * kRows8, kRows8, kPiece), id, part == 0 || ks > 0);
+                    for (int ks = 1; ks < kTile / 16; ++ks)
+                        if (ks < steps) mma<true>(d, p + (ks >> 1) * 32 + 16 + (ks & 1) * 8, vd + (ks * 2048 >> 4), id);
+#pragma unroll
+                    for (int ks = 0; ks < kTile / 16; ++ks)
+                        if (ks < steps) mma<true>(d, p + (ks >> 1) * 32 + (ks & 1) * 8, vd + (ks * 2048 >> 4), id);
                     mma_commit(&bar[kOFull + s]);
                     mma_commit(&bar[kVEmpty + s]);
-                    if (t + 2 < T.n) scores(t + 2);
+                    if (t + 2 < ntiles) scores(t + 2);
                 }
             }
-            __syncwarp();
         } else {
-            // ------------------------------------------------- K, V copies
-            const int pw = warp - 1, row8 = lane & 7, quarter = lane >> 3;  // a warp copies 8 rows x 4 pieces at once
-            int arrived = 0, seg = 0;  // items (K, V of tile 0, 1, ...) reported full
-            auto report = [&](int upto) {
+            // ------------------------------------------------- K, V loads
+            if (ragged) {
+                // a value that is not finite becomes 0 and is noted
+                const int n = (nragged + 15) & ~15;
+                for (int x = tid - 32; x < 2 * n * (DP / 8); x += 96) {
+                    const int v = x >= n * (DP / 8) ? 1 : 0, y = x - v * n * (DP / 8), r = y / (DP / 8), p = y % (DP / 8);
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (r < nragged && p * 8 < a.D) w = attn_ragged8(a, g, r, p * 8, v != 0);
+                    if (not_finite8(w)) {
+                        atomicOr(flags, 1u << r);
+                        w = make_uint4(0, 0, 0, 0);
+                    }
+                    sts_uint4(smem + v * 2 * L::kItem + piece<kTile>(r, p), w);
+                }
                 fence_proxy_async_smem();
-                for (; arrived < upto; ++arrived)
-                    mbar_arrive(&bar[((arrived & 1) ? kVFull : kKFull) + ((arrived >> 1) & 1)]);
-            };
-            for (int item = 0; item < 2 * T.n && ok; ++item) {
-                const int t = item >> 1, s = t & 1, v = item & 1;
-                if (t >= 2) {
-                    uint64_t* b = &bar[v ? kVEmpty + s : kSFull + s];
-                    const uint32_t ph = static_cast<uint32_t>((t >> 1) - 1) & 1u;
-                    if (!mbar_try_wait(b, ph, 0)) {  // nothing to copy into: hand over what is under way
-                        cp_async_wait_all();
-                        report(item);
-                        if (!mbar_wait_bounded(b, ph, a.status, kDevStatusWaitTimeout)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                }
-                const uint32_t dst = base + (v * 2 + s) * L::kItem;
-                const int groups = T.keys(t) >> 3;  // 8 rows each
-                if (t < T.ragged) {
-                    // rows whose visibility differs: a value that is not finite becomes 0 and is noted
-                    for (int x = tid - 32; x < groups * 8 * (DP / 8); x += kProducers) {
-                        const int r = x / (DP / 8), p = x % (DP / 8);
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (r < T.nragged && p * 8 < a.D) w = attn_ragged8(a, g, r, p * 8, v != 0);
-                        if (not_finite8(w)) {
-                            atomicOr(flags, 1u << r);
-                            w = make_uint4(0, 0, 0, 0);
-                        }
-                        sts_uint4(smem + (v * 2 + s) * L::kItem + (r >> 3) * kRows8 + p * kPiece + (r & 7) * 16, w);
-                    }
-                } else {
-                    const int begin = T.start(t), real = T.real(t);
-                    while (begin >= a.seg_end[seg]) ++seg;
-                    int sg = seg;
-                    for (int x = pw; x < groups * (DP / 32); x += 3) {
-                        const int r = (x / (DP / 32)) * 8 + row8, p = (x % (DP / 32)) * 4 + quarter;
-                        const int row = min(begin + r, T.end - 1);
-                        while (row >= a.seg_end[sg]) ++sg;
-                        const AttnSeg& S = a.seg[sg];
-                        const bool in = p * 8 < a.D;
-                        const uint16_t* src = (v ? S.v : S.k) + g * S.head_stride +
-                                              (row - (sg == 0 ? 0 : a.seg_end[sg - 1])) * S.row_stride + (in ? p * 8 : 0);
-                        cp_async16_zfill(dst + (r >> 3) * kRows8 + p * kPiece + (r & 7) * 16, src, in && r < real);
-                    }
-                }
-                cp_async_commit();
-                if (item > 0) {
-                    cp_async_wait<1>();
-                    report(item);
-                }
+                named_barrier_sync(2, 96);
             }
-            cp_async_wait_all();
-            report(2 * T.n);  // every item has been filled unless ok is false: nobody waits for it then
+            if (warp < 3 && lane == 0) {
+                const int v = warp - 1, full = v ? kVFull : kKFull, empty = v ? kVEmpty : kSFull;
+                int t = 0;
+                for (; t < ntiles; ++t) {
+                    const int s = t & 1;
+                    int sg, row;
+                    next_tile(t, sg, row);
+                    if (t < ragged) {
+                        mbar_arrive(&bar[full + s]);
+                        continue;
+                    }
+                    if (t >= 2) wait(empty + s, (t >> 1) - 1);
+                    if (!ok) break;
+                    const uint32_t dst = base + (v * 2 + s) * L::kItem;
+                    const CUtensorMap* map = v ? &maps.v[sg] : &maps.k[sg];
+                    mbar_arrive_expect_tx(&bar[full + s], L::kItem);
+#pragma unroll
+                    for (int x = 0; x < DP / 64; ++x) tma_load_box(dst + x * kHalf, map, x, row, g, &bar[full + s]);
+                }
+                for (int u = max(ragged, t - 2); u < t && !ok; ++u)  // copies under way still write into this block's memory
+                    mbar_wait_bounded(&bar[full + (u & 1)], static_cast<uint32_t>(u >> 1) & 1u, a.status, kDevStatusTxTimeout);
+            }
         }
         __syncwarp();
     } else {
@@ -311,13 +291,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         float o[DP];
 #pragma unroll
         for (int d = 0; d < DP; ++d) o[d] = 0.f;
-        for (int t = w; t < T.n && ok; t += 2) {
+        for (int t = 0; t < ntiles && ok; ++t) {
+            int sg, srow;
+            const int real = next_tile(t, sg, srow), chunks = (real + 31) >> 5;
+            if ((t & 1) != w) continue;
             const uint32_t scol = mine + w * 128;
-            const int real = T.real(t), chunks = (real + 31) >> 5;
-            const bool ragged = t < T.ragged;
             // bit j of seen(c): this row sees key 32 c + j
             auto seen = [&](int ch) {
-                if (ragged) return mask;
+                if (t < ragged) return mask;
                 const int left = real - ch * 32;
                 return left >= 32 ? 0xffffffffu : (1u << left) - 1u;
             };
@@ -431,7 +412,9 @@ int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
     MUSER_TRY(prepare<DP>());
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, kThreads, Layout<DP>::kBytes, s, attr);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP>, a);
+    AttnMaps maps;
+    MUSER_TRY(encode_attn_maps(a, kTile, maps));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DP>, a, maps);
     if (e != cudaSuccess) return cuda_fail(e, "attention: cudaLaunchKernelEx");
     return check_launch("attention");
 }
