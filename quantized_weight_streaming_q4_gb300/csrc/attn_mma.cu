@@ -373,7 +373,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
         }
     }
 
-    join_cluster<DP, L::kOutStride, R, kThreads>(a, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff, ok);
+    if (a.cluster > 1) cluster_sync();
+    else __syncthreads();
+    if (ok) join_cluster<DP, L::kOutStride, R, kThreads>(a, tid, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff);
+    if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
 }
 
 // The kernel's attributes, set once per device.

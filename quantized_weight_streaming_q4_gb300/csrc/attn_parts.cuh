@@ -62,7 +62,7 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
     return v;
 }
 // 2^(m - M) of a partial result with maximum m, 0 where it has no rows.
-__device__ __forceinline__ float share(float m, float M) { return m == kNegInf ? 0.f : exp2f(m - M); }
+__device__ __forceinline__ float share(float m, float M) { return m == kNegInf ? 0.f : ex2(m - M); }
 
 // Eight elements from d on of ragged row r, as binary16 (see attn_ragged).
 __device__ __forceinline__ uint4 attn_ragged8(const AttnArgs& a, int g, int r, int d, bool value) {
@@ -101,60 +101,75 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
 // The cluster's result: the blocks hold the same R query rows' (maximum, sum)
 // pairs at shared address mla and outputs at oa (row stride STRIDE floats);
 // each joins a share of the elements and writes them out, final or as a part.
-// Every thread of every block of the cluster calls it; with `ok` false the
-// block has nothing to give and writes nothing.
+// Called by THREADS threads (tid counts them) between two cluster barriers.
+// The remote loads of all blocks go out together: one after another they took
+// 16 round trips, about 5 us in a cluster of 16.
 template <int DP, int STRIDE, int R, int THREADS>
-__device__ __forceinline__ void join_cluster(const AttnArgs& a, int c, int g, int r0, int rows, uint32_t mla, uint32_t oa,
-                                             bool ok) {
-    const uint32_t n = a.cluster, rank = n > 1 ? cluster_rank() : 0;
-    if (n > 1) cluster_sync();
-    else __syncthreads();
-    const int units = R * DP / 4, u0 = static_cast<int>(units * rank / n), u1 = static_cast<int>(units * (rank + 1) / n);
+__device__ __forceinline__ void join_cluster(const AttnArgs& a, int tid, int c, int g, int r0, int rows, uint32_t mla,
+                                             uint32_t oa) {
+    const int n = a.cluster, rank = n > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int units = R * DP / 4, u0 = units * rank / n, u1 = units * (rank + 1) / n;
     const int nclusters = gridDim.x / n;
-    for (int x = u0 + static_cast<int>(threadIdx.x); x < u1 && ok; x += THREADS) {
+    for (int x = u0 + tid; x < u1; x += THREADS) {
         const int r = x / (DP / 4), d = x % (DP / 4) * 4;
         if (r0 + r >= rows || d >= a.D) continue;
+        const int i = (r0 + r) / a.group;
+        const int64_t row = static_cast<int64_t>(i) * a.H + g * a.group + (r0 + r) - i * a.group;
+        const uint32_t ma = mla + r * 8, va = oa + (r * STRIDE + d) * 4;
+        const bool final = nclusters == 1;
+        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (final && a.gate) z = __ldcg(reinterpret_cast<const float4*>(a.gate + row * a.D + d));
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         float l = 0.f, M = kNegInf;
-        const uint32_t ma = mla + r * 8, va = oa + (r * STRIDE + d) * 4;
-        if (n == 1) {
-            const float2 w = ld_cluster2(ma);
-            s = ld_cluster4(va);
-            M = w.x;
-            l = w.y;
-        } else {
-            for (uint32_t b = 0; b < n; ++b) M = fmaxf(M, ld_cluster2(map_rank(ma, b)).x);
-#pragma unroll 4
-            for (uint32_t b = 0; b < n; ++b) {
-                const float2 w = ld_cluster2(map_rank(ma, b));
-                const float4 v = ld_cluster4(map_rank(va, b));
-                const float f = share(w.x, M);
-                l = fmaf(f, w.y, l);
-                s.x = fmaf(f, v.x, s.x);
-                s.y = fmaf(f, v.y, s.y);
-                s.z = fmaf(f, v.z, s.z);
-                s.w = fmaf(f, v.w, s.w);
+        for (int b0 = 0; b0 < n; b0 += 8) {  // eight blocks' at a time, the running maximum carried
+            float2 w[8];
+            float4 v[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                w[b] = make_float2(kNegInf, 0.f);
+                if (b0 + b < n) {
+                    w[b] = ld_cluster2(map_rank(ma, b0 + b));
+                    v[b] = ld_cluster4(map_rank(va, b0 + b));
+                }
+            }
+            float mn = M;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) mn = fmaxf(mn, w[b].x);
+            const float f0 = share(M, mn);
+            M = mn;
+            l *= f0;
+            s.x *= f0;
+            s.y *= f0;
+            s.z *= f0;
+            s.w *= f0;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                if (b0 + b < n) {
+                    const float f = share(w[b].x, M);
+                    l = fmaf(f, w[b].y, l);
+                    s.x = fmaf(f, v[b].x, s.x);
+                    s.y = fmaf(f, v[b].y, s.y);
+                    s.z = fmaf(f, v[b].z, s.z);
+                    s.w = fmaf(f, v[b].w, s.w);
+                }
             }
         }
-        const int64_t row = static_cast<int64_t>((r0 + r) / a.group) * a.H + g * a.group + (r0 + r) % a.group;
-        if (nclusters > 1) {
-            const int64_t slot = static_cast<int64_t>(c / static_cast<int>(n)) * a.M * a.H + row;
-            *reinterpret_cast<float4*>(a.part_o + slot * a.D + d) = s;
-            if (d == 0) a.part_ml[slot] = make_float2(M, l);
-        } else {
+        if (final) {
             const float inv = 1.f / l;
             float4 y = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
             if (a.gate) {
-                const float4 z = *reinterpret_cast<const float4*>(a.gate + row * a.D + d);
                 y.x /= 1.f + expf(-z.x);
                 y.y /= 1.f + expf(-z.y);
                 y.z /= 1.f + expf(-z.z);
                 y.w /= 1.f + expf(-z.w);
             }
             *reinterpret_cast<float4*>(a.out + row * a.D + d) = y;
+        } else {
+            const int64_t slot = static_cast<int64_t>(c / n) * a.M * a.H + row;
+            *reinterpret_cast<float4*>(a.part_o + slot * a.D + d) = s;
+            if (d == 0) a.part_ml[slot] = make_float2(M, l);
         }
     }
-    if (n > 1) cluster_sync();  // nobody leaves while its shared memory is read
 }
 
 inline cudaLaunchConfig_t cluster_config(int cluster, dim3 grid, int threads, size_t smem, cudaStream_t s,

@@ -63,6 +63,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
@@ -97,6 +104,11 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 template <int N>
 __device__ __forceinline__ void set_regs_up() {
@@ -146,8 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    bool ok = true;
+    constexpr uint32_t tmem = 0;  // the address of an allocation of all columns
+    bool ok = *tmem_slot == tmem;
     auto wait = [&](int b, int phase) {
         if (ok) ok = mbar_wait_bounded(&bar[b], static_cast<uint32_t>(phase & 1), a.status, kDevStatusWaitTimeout);
     };
@@ -159,7 +171,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         set_regs_down<40>();
         if (warp == 0) {
             // ------------------------------------------- matrix products
-            if (lane == 0 && ntiles > 0) {
+            // The whole warp runs the loop and one thread issues: under `lane ==
+            // 0` alone every operand goes through a vector register, 130
+            // cycles a product where the tensor core takes 64.
+            const bool leader = elect_one();
+            if (ntiles > 0) {
                 int keys[2];  // of the tiles in the two score buffers, a multiple of 16
                 auto scores = [&](int t) {
                     const int s = t & 1;
@@ -171,12 +187,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     const uint32_t id = idesc(static_cast<uint32_t>(keys[s]), false), d = tmem + s * 128, q = tmem + kColQ;
                     const uint64_t kd = smem_desc(base + s * L::kItem, 16, 1024);
                     auto at = [&](int ks) { return kd + ((ks >> 2) * kHalf + (ks & 3) * 32 >> 4); };
-                    mma<false>(d, q + DP / 2, kd, id);  // the low part of q first
+                    if (leader) {
+                        mma<false>(d, q + DP / 2, kd, id);  // the low part of q first
 #pragma unroll
-                    for (int ks = 1; ks < DP / 16; ++ks) mma<true>(d, q + DP / 2 + ks * 8, at(ks), id);
+                        for (int ks = 1; ks < DP / 16; ++ks) mma<true>(d, q + DP / 2 + ks * 8, at(ks), id);
 #pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks) mma<true>(d, q + ks * 8, at(ks), id);
-                    mma_commit(&bar[kSFull + s]);
+                        for (int ks = 0; ks < DP / 16; ++ks) mma<true>(d, q + ks * 8, at(ks), id);
+                        mma_commit(&bar[kSFull + s]);
+                    }
+                    __syncwarp();
                 };
                 wait(kQReady, 0);
                 tc_fence_after();
@@ -191,15 +210,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     const uint32_t id = idesc(DP, true), d = tmem + kColO, p = tmem + s * 128;
                     const uint64_t vd = smem_desc(base + (2 + s) * L::kItem, kHalf, 1024);
                     const int steps = keys[s] / 16;
-                    mma<false>(d, p + 16, vd, id);  // the low part of p first
+                    if (leader) {
+                        mma<false>(d, p + 16, vd, id);  // the low part of p first
 #pragma unroll
-                    for (int ks = 1; ks < kTile / 16; ++ks)
-                        if (ks < steps) mma<true>(d, p + (ks >> 1) * 32 + 16 + (ks & 1) * 8, vd + (ks * 2048 >> 4), id);
+                        for (int ks = 1; ks < kTile / 16; ++ks)
+                            if (ks < steps) mma<true>(d, p + (ks >> 1) * 32 + 16 + (ks & 1) * 8, vd + (ks * 2048 >> 4), id);
 #pragma unroll
-                    for (int ks = 0; ks < kTile / 16; ++ks)
-                        if (ks < steps) mma<true>(d, p + (ks >> 1) * 32 + (ks & 1) * 8, vd + (ks * 2048 >> 4), id);
-                    mma_commit(&bar[kOFull + s]);
-                    mma_commit(&bar[kVEmpty + s]);
+                        for (int ks = 0; ks < kTile / 16; ++ks)
+                            if (ks < steps) mma<true>(d, p + (ks >> 1) * 32 + (ks & 1) * 8, vd + (ks * 2048 >> 4), id);
+                        mma_commit(&bar[kOFull + s]);
+                        mma_commit(&bar[kVEmpty + s]);
+                    }
+                    __syncwarp();
                     if (t + 2 < ntiles) scores(t + 2);
                 }
             }
@@ -245,42 +267,62 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
         }
         __syncwarp();
+        // This warpgroup has 40 registers a thread: it shares no code with the
+        // streams from here on, only the barriers.
+        tc_fence_before();
+        __syncthreads_and(ok);
+        if (warp == 0) {
+            tc_fence_after();
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        }
+        if (a.cluster > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
     } else {
         // ------------------------------------------------------- the streams
         set_regs_up<232>();
         const int w = (warp - 4) >> 2, row = tid & 127;  // stream, query row = TMEM lane
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        // q: 16-byte copies into the output's place, then each thread its row
-        for (int x = tid - 128; x < 128 * (DP / 4); x += 256) {
-            const int r = x / (DP / 4), d = x % (DP / 4) * 4, qr = r0 + r;
-            const bool real = qr < rows && d < a.D;
-            const float* src = a.q + (real ? (static_cast<int64_t>(qr / a.group) * a.H + g * a.group + qr % a.group) * a.D + d : 0);
-            cp_async16_zfill(base + L::kOutOff + (r * L::kOutStride + d) * 4, src, real);
+        // q: 16-byte copies into the output's place, 256 / (DP / 4) rows at a
+        // time (row r of the block: tree row i, head j of the group); then a
+        // thread splits half a row
+        {
+            constexpr int kStep = 256 / (DP / 4);
+            const int d = (tid - 128) % (DP / 4) * 4;
+            int r = (tid - 128) / (DP / 4), i = (r0 + r) / a.group, j = r0 + r - i * a.group;
+            const int skip = (a.H - a.group) * a.D;  // from one tree row's group to the next
+            const float* src = a.q + static_cast<int64_t>(g * a.group + r0 + r) * a.D + static_cast<int64_t>(i) * skip + d;
+            const uint32_t dst = base + L::kOutOff + d * 4;
+#pragma unroll 4
+            for (; r < 128; r += kStep) {
+                const bool real = r0 + r < rows && d < a.D;
+                cp_async16_zfill(dst + r * L::kOutStride * 4, real ? src : a.q, real);
+                src += kStep * a.D;
+                for (j += kStep; j >= a.group; j -= a.group) src += skip;
+            }
         }
         cp_async_wait_all();
         named_barrier_sync(1, 256);
         float mx = 0.f;
-#pragma unroll 8
+#pragma unroll
         for (int d = 0; d < DP; d += 4) {
             const float4 x = lds_float4(out + row * L::kOutStride + d);
             mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
         }
-        mx *= fabsf(a.scale_log2);
-        const int e = min(100, max(-100, ((__float_as_int(mx) >> 23) & 0xff) - 127)) - 7;
+        const int e = min(100, max(-100, ((__float_as_int(mx * fabsf(a.scale_log2)) >> 23) & 0xff) - 127)) - 7;
         const float qscale = a.scale_log2, up = __int_as_float((127 - e) << 23), down = __int_as_float((127 + e) << 23);
 #pragma unroll
-        for (int h = 0; h < DP / 64; ++h) {
-            uint32_t q32[32];
+        for (int h = 0; h < DP / 64; ++h) {  // 32 elements: 16 columns of the high parts and 16 of the low ones
+            uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float4 x = lds_float4(out + row * L::kOutStride + h * 64 + i * 4);
-                uint32_t hi0, lo0, hi1, lo1;
-                split2(x.x * qscale * up, x.y * qscale * up, hi0, lo0);
-                split2(x.z * qscale * up, x.w * qscale * up, hi1, lo1);
-                q32[2 * i] = w == 0 ? hi0 : lo0;
-                q32[2 * i + 1] = w == 0 ? hi1 : lo1;
+            for (int i = 0; i < 8; ++i) {
+                const float4 x = lds_float4(out + row * L::kOutStride + w * (DP / 2) + h * 32 + i * 4);
+                split2(x.x * qscale * up, x.y * qscale * up, hi[2 * i], lo[2 * i]);
+                split2(x.z * qscale * up, x.w * qscale * up, hi[2 * i + 1], lo[2 * i + 1]);
             }
-            tmem_st32(mine + kColQ + w * (DP / 2) + h * 32, q32);
+            tmem_st16(mine + kColQ + w * (DP / 4) + h * 16, hi);
+            tmem_st16(mine + kColQ + DP / 2 + w * (DP / 4) + h * 16, lo);
         }
         tc_wait_st();
         tc_fence_before();
@@ -383,14 +425,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
             ml[row] = make_float2(M, l);
         }
+        tc_fence_before();
+        ok = __syncthreads_and(ok);
+        if (a.cluster > 1) cluster_sync();
+        if (ok) join_cluster<DP, L::kOutStride, 128, 256>(a, tid - 128, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff);
+        if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
     }
-    tc_fence_before();
-    ok = __syncthreads_and(ok);
-    if (warp == 0) {
-        tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
-    }
-    join_cluster<DP, L::kOutStride, 128, kThreads>(a, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff, ok);
 }
 
 template <int DP>
