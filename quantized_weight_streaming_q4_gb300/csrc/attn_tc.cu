@@ -19,7 +19,7 @@
 //
 // Warps: 0 issues the matrix products, 1 and 2 the TMA loads of K and of V
 // (128-byte swizzle: K with d contiguous along the product's K, V along its
-// N), 4-7 and 8-11 are the two streams; 1-3 also store the rows whose
+// N); 4-7 and 8-11 are the two streams, which also store the rows whose
 // visibility differs.  K and V wait for their buffers apart: one thread for
 // both held a free K buffer back behind V's.
 #include <algorithm>
@@ -46,7 +46,7 @@ struct Layout {
     static constexpr uint32_t kBarOff = kMl2Off + 128 * 8;
     static constexpr uint32_t kBytes = kBarOff + 256;
 };
-enum Bar { kKFull = 0, kVFull = 2, kVEmpty = 4, kSFull = 6, kPFull = 8, kOFull = 10, kOFree = 12, kQReady = 13, kBars = 14 };
+enum Bar { kKFull = 0, kVFull = 2, kVEmpty = 4, kSFull = 6, kPFull = 8, kOFull = 10, kOFree = 12, kQReady = 13, kRagged = 14, kBars = 15 };
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         mbar_init(&bar[kOFree], 128);
         mbar_init(&bar[kQReady], 256);
+        mbar_init(&bar[kRagged], 256);
         *flags = 0;
         fence_mbar_init();
     }
@@ -227,22 +228,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
         } else {
             // ------------------------------------------------- K, V loads
-            if (ragged) {
-                // a value that is not finite becomes 0 and is noted
-                const int n = (nragged + 15) & ~15;
-                for (int x = tid - 32; x < 2 * n * (DP / 8); x += 96) {
-                    const int v = x >= n * (DP / 8) ? 1 : 0, y = x - v * n * (DP / 8), r = y / (DP / 8), p = y % (DP / 8);
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (r < nragged && p * 8 < a.D) w = attn_ragged8(a, g, r, p * 8, v != 0);
-                    if (not_finite8(w)) {
-                        atomicOr(flags, 1u << r);
-                        w = make_uint4(0, 0, 0, 0);
-                    }
-                    sts_uint4(smem + v * 2 * L::kItem + piece<kTile>(r, p), w);
-                }
-                fence_proxy_async_smem();
-                named_barrier_sync(2, 96);
-            }
             if (warp < 3 && lane == 0) {
                 const int v = warp - 1, full = v ? kVFull : kKFull, empty = v ? kVEmpty : kSFull;
                 int t = 0;
@@ -250,7 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     const int s = t & 1;
                     int sg, row;
                     next_tile(t, sg, row);
-                    if (t < ragged) {
+                    if (t < ragged) {  // the streams store this one
+                        wait(kRagged, 0);
+                        if (!ok) break;
                         mbar_arrive(&bar[full + s]);
                         continue;
                     }
@@ -284,32 +271,62 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         set_regs_up<232>();
         const int w = (warp - 4) >> 2, row = tid & 127;  // stream, query row = TMEM lane
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        // q: 16-byte copies into the output's place, 256 / (DP / 4) rows at a
-        // time (row r of the block: tree row i, head j of the group); then a
-        // thread splits half a row
+        // q and the ragged rows: coalesced loads, all in flight together, then
+        // through shared memory.  (Asynchronous 16-byte copies of q moved 12
+        // bytes a clock, 512-byte bulk copies 9.)
+        constexpr int kStep = 256 / (DP / 4), kQ = 128 / kStep;  // rows of one pass, passes
+        const int qd = (tid - 128) % (DP / 4) * 4, q0 = (tid - 128) / (DP / 4);
+        float4 q4[kQ];
         {
-            constexpr int kStep = 256 / (DP / 4);
-            const int d = (tid - 128) % (DP / 4) * 4;
-            int r = (tid - 128) / (DP / 4), i = (r0 + r) / a.group, j = r0 + r - i * a.group;
+            // row r0 + r of the block: tree row i, head j of the group
+            int i = (r0 + q0) / a.group, j = r0 + q0 - i * a.group;
             const int skip = (a.H - a.group) * a.D;  // from one tree row's group to the next
-            const float* src = a.q + static_cast<int64_t>(g * a.group + r0 + r) * a.D + static_cast<int64_t>(i) * skip + d;
-            const uint32_t dst = base + L::kOutOff + d * 4;
-#pragma unroll 4
-            for (; r < 128; r += kStep) {
-                const bool real = r0 + r < rows && d < a.D;
-                cp_async16_zfill(dst + r * L::kOutStride * 4, real ? src : a.q, real);
+            const float* src = a.q + static_cast<int64_t>(g * a.group + r0 + q0) * a.D + static_cast<int64_t>(i) * skip + qd;
+#pragma unroll
+            for (int u = 0; u < kQ; ++u) {
+                q4[u] = r0 + q0 + u * kStep < rows && qd < a.D ? __ldcg(reinterpret_cast<const float4*>(src))
+                                                               : make_float4(0.f, 0.f, 0.f, 0.f);
                 src += kStep * a.D;
                 for (j += kStep; j >= a.group; j -= a.group) src += skip;
             }
         }
-        cp_async_wait_all();
+        constexpr int kEach = 2 * 32 * (DP / 8) / 256;
+        uint4 x[kEach];
+        if (ragged) {
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int y = u * 256 + tid - 128, v = u >= kEach / 2 ? 1 : 0, r = y / (DP / 8) - v * 32, p = y % (DP / 8);
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (r < nragged && p * 8 < a.D) x[u] = attn_ragged8(a, g, r, p * 8, v != 0);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kQ; ++u) sts_float4(out + (q0 + u * kStep) * L::kOutStride + qd, q4[u]);
+        if (ragged) {  // stored as tile 0; a value that is not finite becomes 0 and is noted
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int y = u * 256 + tid - 128, v = u >= kEach / 2 ? 1 : 0, r = y / (DP / 8) - v * 32, p = y % (DP / 8);
+                if (not_finite8(x[u])) {
+                    atomicOr(flags, 1u << r);
+                    x[u] = make_uint4(0, 0, 0, 0);
+                }
+                sts_uint4(smem + v * 2 * L::kItem + piece<kTile>(r, p), x[u]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bar[kRagged]);
+        }
         named_barrier_sync(1, 256);
+        // a thread takes half a row, the row's largest element from both
         float mx = 0.f;
 #pragma unroll
-        for (int d = 0; d < DP; d += 4) {
-            const float4 x = lds_float4(out + row * L::kOutStride + d);
-            mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+        for (int i = 0; i < DP / 8; ++i) {
+            q4[i] = lds_float4(out + row * L::kOutStride + w * (DP / 2) + i * 4);
+            mx = fmaxf(fmaxf(mx, fmaxf(fabsf(q4[i].x), fabsf(q4[i].y))), fmaxf(fabsf(q4[i].z), fabsf(q4[i].w)));
         }
+        float* half = reinterpret_cast<float*>(ml);  // [2][128]
+        half[w * 128 + row] = mx;
+        named_barrier_sync(1, 256);
+        mx = fmaxf(mx, half[(w ^ 1) * 128 + row]);
         const int e = min(100, max(-100, ((__float_as_int(mx * fabsf(a.scale_log2)) >> 23) & 0xff) - 127)) - 7;
         const float qscale = a.scale_log2, up = __int_as_float((127 - e) << 23), down = __int_as_float((127 + e) << 23);
 #pragma unroll
@@ -317,9 +334,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             uint32_t hi[16], lo[16];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float4 x = lds_float4(out + row * L::kOutStride + w * (DP / 2) + h * 32 + i * 4);
-                split2(x.x * qscale * up, x.y * qscale * up, hi[2 * i], lo[2 * i]);
-                split2(x.z * qscale * up, x.w * qscale * up, hi[2 * i + 1], lo[2 * i + 1]);
+                const float4 f = q4[h * 8 + i];
+                split2(f.x * qscale * up, f.y * qscale * up, hi[2 * i], lo[2 * i]);
+                split2(f.z * qscale * up, f.w * qscale * up, hi[2 * i + 1], lo[2 * i + 1]);
             }
             tmem_st16(mine + kColQ + w * (DP / 4) + h * 16, hi);
             tmem_st16(mine + kColQ + DP / 2 + w * (DP / 4) + h * 16, lo);
