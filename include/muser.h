@@ -611,12 +611,13 @@ size_t muser_tree_verify_scratch_bytes(int64_t vocab, int M);
  *   kept rows ascending, then -1.  The token is -1 when the walk meets a row
  *   with a NaN, a +infinity, only -infinities, or a largest logit /
  *   temperature beyond about +-22,000.  vocab <= 2^20, temperature 0 or >= 0.001.
- *   Probabilities below 2^-42 of the row's largest may count as 0; decisions
- *   are otherwise those of exact arithmetic to about 2^-37 (2^-33 where logit /
- *   temperature is in the thousands), and a remainder of
- *   a smaller share than that may count as nothing left.
- *   One cooperative launch whose blocks wait for one another (bounded in
- *   time, muser_device_status() bit 1, result then unwritten).
+ *   Acceptance is decided to about 2^-19 of the compared probabilities (equal
+ *   rows accept every token).  The next token is that of exact arithmetic to
+ *   about 2^-37 of the cumulative sum (2^-33 where logit / temperature is in
+ *   the thousands); a probability below 2^-41 of the row's largest, or a
+ *   remainder that small, may count as nothing.
+ *   Sampling is one cooperative launch whose blocks wait for one another
+ *   (bounded in time, muser_device_status() bit 1, result then unwritten).
  *   scratch: device memory of muser_tree_verify_scratch_bytes(), 16-byte
  *   aligned, zero-filled before its first use; its first 256 bytes are left
  *   zero, the rest is not.  Calls that can run at the same time must not

@@ -1,23 +1,31 @@
 // verify.cu -- verification of drafted (tree) tokens against the target's
 // probabilities from given random numbers, and the token that follows.
 //
-// One cooperative launch.  All blocks first stream the logits once: per row
-// the sum of 2^(l * log2(e) / T) (or, at temperature 0, the first maximum).
-// After a grid barrier every block walks the tree by itself, from the same
-// numbers, so all take the same path; only where a child is rejected, or at
-// the end, do they pass over one pair of rows together, each over its own
-// slice of the vocabulary.
+// Sampling is one cooperative launch:
+//  1. Every row with children is streamed once, in slices that a warp each
+//     sums (2^(l log2(e) / T), binary32).  The acceptance tests need no more:
+//     an error of 1e-6 in p / q moves a decision with probability 1e-6.
+//  2. After a grid barrier every block walks the tree by itself from the same
+//     numbers, so all take the same path.
+//  3. What needs the whole vocabulary of one node (a rejected child's
+//     remainder, the next token) all blocks do together, each on its own slice
+//     of tokens, whose weights stay in shared memory, with one barrier each.
+// Temperature 0 is an ordinary launch; the last block to finish its maxima
+// walks.
 //
-// Weights are integers.  With R an integer >= the row's largest exponent, a
-// token's weight is round(2^(l log2(e) / T - R) * 2^42): sums of integers do
-// not depend on their order, so the sampled token is the same whatever the
-// grid, and a token is decided by comparing integers.  The exponential is
-// good to about 2^-38: a binary32 one (2^-23) would move some of the 2e5
-// borders of the cumulative sums by enough to pick a neighbour about once in a
-// thousand draws.  FP64 has no rate to speak of on GB300, so none of the
-// per-token work uses it; it is kept for a few scalars per row.
+// The next token comes from integer weights: with R an integer >= the largest
+// exponent, round(2^(l log2(e) / T - R) * 2^42), good to about 2^-38.  Sums of
+// integers do not depend on their order, so neither does the token; and a
+// binary32 exponential (2^-23) would move some of the 2e5 borders of the
+// cumulative sums far enough to pick a neighbour about once in a thousand
+// draws.  FP64 has no rate to speak of on GB300: it is kept for a few scalars.
+//
+// Bound: the rows' bytes (24 MB for 15 drafts over 202,048 tokens: 3.6 us),
+// then latency: a launch, two to four grid barriers of 1.5 us and the loads
+// behind them.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "kernels.cuh"
 
@@ -25,12 +33,13 @@ namespace muser {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kFrac = 42;             // fraction bits of a weight
-constexpr int kRows = 2 * MUSER_MAX_M;  // target rows, then draft rows
-constexpr int kTable = 128;
-constexpr int kMaxParts = 256;        // blocks that can share one row
+constexpr int kFrac = 42;  // fraction bits of a weight
+constexpr int kRows = 2 * MUSER_MAX_M;
+constexpr int kVerifyTable = 128;
+constexpr int kMaxSlices = 256;  // of a row
+constexpr int kMaxBlocks = 256;
 constexpr float kMaxExponent = 32768.f;
-constexpr int kBadRow = 1 << 24;      // exponent mark of a row that holds a NaN or an infinity
+constexpr int kBad = 1 << 24;  // exponent mark of a slice that holds a NaN or an infinity
 constexpr uint64_t kGridWaitNs = 2000000000ull;
 
 struct VerifyArgs {
@@ -41,30 +50,21 @@ struct VerifyArgs {
     int32_t* result;       // [M + 2]
     int M, V;
     float c_hi, c_lo;      // log2(e) / T
-    int greedy, vec;       // vec: rows are 16-byte aligned
+    int vec;               // rows are 16-byte aligned
     int parent[MUSER_MAX_M];
-    int nrows;             // rows that are read: target rows 0..M-1, then the draft rows listed
-    int draft_row[MUSER_MAX_M];  // node whose draft row is row M + i
-    int draft_at[MUSER_MAX_M];   // row index of node i's draft row, or -1
-    int64_t per_block;     // logits per block of the first pass, a multiple of 4
-    int slice;             // tokens per block of the walk's passes
+    int nrows;             // rows streamed first (greedy: all; else rows with children, targets then drafts)
+    int row_node[kRows];   // their nodes
+    int ntarget;           // how many of them are target rows
+    int target_at[MUSER_MAX_M], draft_at[MUSER_MAX_M];  // row index of a node's rows, or -1
+    int slices, slice_len; // of a row in the first pass
+    int span;              // tokens per block in the passes over one node
     unsigned* sync;        // arrivals, exits
-    uint64_t* part_sum;    // [kRows][kMaxParts]
-    int* part_exp;         // [kRows][kMaxParts]
-    uint64_t* pass_sum;    // [2][kMaxParts]: the walk's passes, two buffers in turn
+    float2* part;          // [kRows][kMaxSlices] (sum, exponent); greedy: uint64 keys
+    uint64_t* sums;        // [4][kMaxBlocks]: two passes' buffers in turn, two values each
+    int* exps;             // [kMaxBlocks]
     unsigned* status;
+    uint64_t table[kVerifyTable];  // 2^(j / 128) * 2^kFrac
 };
-
-__device__ __forceinline__ const float* row_ptr(const VerifyArgs& a, int row) {
-    return row < a.M ? a.target + static_cast<int64_t>(row) * a.V
-                     : a.draft + static_cast<int64_t>(a.draft_row[row - a.M]) * a.V;
-}
-
-// 2^(j / 128) * 2^kFrac, j = 0..127, filled once per block in binary64.
-__device__ void fill_table(uint64_t* table) {
-    for (int j = threadIdx.x; j < kTable; j += blockDim.x)
-        table[j] = static_cast<uint64_t>(exp2(static_cast<double>(j) / kTable) * static_cast<double>(1ull << kFrac) + 0.5);
-}
 
 // round(2^(l * c - R) * 2^kFrac) for an integer R >= l * c; 0 where that is
 // below 2^-20 of the last bit and for l = -inf.  l * c = n + j / 128 + r with
@@ -74,8 +74,8 @@ __device__ void fill_table(uint64_t* table) {
 __device__ __forceinline__ uint64_t weight(float l, float c_hi, float c_lo, int R, const uint64_t* table) {
     const float h = l * c_hi;
     const float e = fmaf(l, c_lo, fmaf(l, c_hi, -h));
-    const float nj = rintf(h * static_cast<float>(kTable));
-    const float r0 = fmaf(-1.f / kTable, nj, h);  // exact: h - nj / 128
+    const float nj = rintf(h * static_cast<float>(kVerifyTable));
+    const float r0 = fmaf(-1.f / kVerifyTable, nj, h);  // exact: h - nj / 128
     const float r = r0 + e, rl = e - (r - r0);
     constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654323148236e-09f;
     const float y = r * kLn2Hi;
@@ -89,7 +89,7 @@ __device__ __forceinline__ uint64_t weight(float l, float c_hi, float c_lo, int 
     const int g = ((__float_as_int(yb) - __float_as_int(kMagic1)) << 9) +
                   (__float_as_int(rest + kMagic2) - __float_as_int(kMagic2));
     const int i = static_cast<int>(nj);
-    const uint64_t t = table[i & (kTable - 1)];
+    const uint64_t t = table[i & (kVerifyTable - 1)];
     // t * (1 + g 2^-39): t >> 11 has 32 bits
     const int64_t prod = static_cast<int64_t>(static_cast<uint32_t>(t >> 11)) * static_cast<int64_t>(g);
     const uint64_t w = t + static_cast<uint64_t>(prod >> (39 - 11));
@@ -98,15 +98,22 @@ __device__ __forceinline__ uint64_t weight(float l, float c_hi, float c_lo, int 
     return down > 0 ? (w + (1ull << (down - 1))) >> down : w;
 }
 
-// Thread-level running sum of weights with its own reference exponent.
-struct Running {
-    uint64_t sum;
-    int R;
-};
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint64_t shifted(uint64_t s, int by) { return by < 64 ? s >> by : 0; }
-__device__ __forceinline__ Running join(Running a, Running b) {
-    const int R = max(a.R, b.R);
-    return {shifted(a.sum, R - a.R) + shifted(b.sum, R - b.R), R};
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ uint64_t ldcg64(const uint64_t* p) {
+    return __ldcg(reinterpret_cast<const unsigned long long*>(p));
+}
+__device__ __forceinline__ const float* row_ptr(const VerifyArgs& a, int row) {
+    return (row < a.ntarget ? a.target : a.draft) + static_cast<int64_t>(a.row_node[row]) * a.V;
 }
 
 // Every block has arrived `times` times.  False if it gave up waiting.
@@ -133,222 +140,174 @@ __device__ bool grid_barrier(const VerifyArgs& a, unsigned times, int* flag) {
     return *flag != 0;
 }
 
-struct Shared {
-    uint64_t table[kTable];
-    uint64_t warp_sum[kWarps];
-    int warp_exp[kWarps];
-    float warp_max[kWarps];
-    int warp_arg[kWarps];
-    uint64_t row_sum[kRows];  // weights' sum of a row, with its exponent
-    int row_exp[kRows];
-    double px[MUSER_MAX_M], qx[MUSER_MAX_M], u[MUSER_MAX_M];  // of node i: p(x_i), q(x_i) in its parent's rows
-    int token[MUSER_MAX_M], arg[MUSER_MAX_M];
-    uint64_t total;
-    uint64_t blocks[kMaxParts];
-    int flag;
-    int found;
-};
-
-__device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
+// Calls f(x, i) for this lane's logits x = p[i], lo <= i < hi, in batches whose
+// loads are in flight together (four at a time where `vec`, else one).
+template <typename F>
+__device__ __forceinline__ void for_slice(const float* p, int lo, int hi, bool vec, F&& f) {
+    const int lane = threadIdx.x & 31;
+    if (vec) {  // lo is a multiple of 4
+        constexpr int kBatch = 8;
+        const float4* p4 = reinterpret_cast<const float4*>(p + lo);
+        const int n4 = (hi - lo) >> 2;
+        int i = lane;
+        for (; i + (kBatch - 1) * 32 < n4; i += kBatch * 32) {
+            float4 v[kBatch];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+            for (int u = 0; u < kBatch; ++u) v[u] = __ldcg(p4 + i + u * 32);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) f(v[u], lo + 4 * (i + u * 32));
+        }
+        for (; i < n4; i += 32) f(__ldcg(p4 + i), lo + 4 * i);
+        return;
+    }
+    for (int i = lo + lane; i < hi; i += 128) {
+        float4 v;
+        v.x = __ldcg(p + i);
+        v.y = i + 32 < hi ? __ldcg(p + i + 32) : -INFINITY;
+        v.z = i + 64 < hi ? __ldcg(p + i + 64) : -INFINITY;
+        v.w = i + 96 < hi ? __ldcg(p + i + 96) : -INFINITY;
+        f(v, i);
+    }
 }
 
-// ------------------------------------------------- first pass over all rows
-// Block b streams logits [b * per_block, (b + 1) * per_block) of the rows laid
-// end to end and leaves one partial per row it touches.
-__device__ int first_block(const VerifyArgs& a, int row) {
-    return static_cast<int>(static_cast<int64_t>(row) * a.V / a.per_block);
-}
-__device__ int last_block(const VerifyArgs& a, int row) {
-    return static_cast<int>((static_cast<int64_t>(row + 1) * a.V - 1) / a.per_block);
+// The warp's unit of the first pass: slice u % slices of row u / slices.
+__device__ __forceinline__ bool my_unit(const VerifyArgs& a, int& row, int& lo, int& hi) {
+    const int u = static_cast<int>((threadIdx.x >> 5) * gridDim.x + blockIdx.x);  // spread over the blocks
+    row = u / a.slices;
+    lo = (u - row * a.slices) * a.slice_len;
+    hi = min(lo + a.slice_len, a.V);
+    return row < a.nrows;
 }
 
-template <bool GREEDY>
-__device__ void stream_rows(const VerifyArgs& a, Shared& S) {
-    const int64_t all = static_cast<int64_t>(a.nrows) * a.V;
-    const int64_t b0 = blockIdx.x * a.per_block, b1 = min(b0 + a.per_block, all);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int64_t at = b0; at < b1;) {
-        const int row = static_cast<int>(at / a.V);
-        const int64_t base = static_cast<int64_t>(row) * a.V;
-        const int lo = static_cast<int>(at - base), hi = static_cast<int>(min(b1 - base, static_cast<int64_t>(a.V)));
-        const float* p = row_ptr(a, row);
-        Running run{0, -(1 << 23)};
+// ----------------------------------------------------------- temperature 0
+// The first maximum of a row as one number: the value's bits in an order that
+// integers share, then the index counted down.  A NaN or +infinity is above
+// all.
+__device__ __forceinline__ uint64_t max_key(float x, int i) {
+    const uint32_t b = __float_as_uint(x == 0.f ? 0.f : x);
+    const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
+    return x < INFINITY ? (static_cast<uint64_t>(o) << 32) | (0xffffffffu - static_cast<uint32_t>(i)) : ~0ull;
+}
+
+__global__ void __launch_bounds__(kThreads) verify_greedy_kernel(const __grid_constant__ VerifyArgs a) {
+    __shared__ int s_last, s_arg[MUSER_MAX_M], s_token[MUSER_MAX_M];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint64_t* keys = reinterpret_cast<uint64_t*>(a.part);
+    int row, lo, hi;
+    if (my_unit(a, row, lo, hi)) {
         float best = -INFINITY;
-        int arg = 0x7fffffff, bad = 0;
-        auto take4 = [&](const float (&x)[4], int n, int i) {
-            if constexpr (GREEDY) {
+        int arg = 0x7fffffff;
+        bool bad = false;
+        const int step = a.vec ? 1 : 32;
+        for_slice(row_ptr(a, row), lo, hi, a.vec, [&](float4 v, int i) {
+            bad |= !(fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) < INFINITY) | (v.x != v.x) | (v.y != v.y) | (v.z != v.z) | (v.w != v.w);
+            if (v.x > best) best = v.x, arg = i;
+            if (v.y > best) best = v.y, arg = i + step;
+            if (v.z > best) best = v.z, arg = i + 2 * step;
+            if (v.w > best) best = v.w, arg = i + 3 * step;
+        });
+        uint64_t key = bad ? ~0ull : max_key(best, arg);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < n) {
-                        bad |= !(x[k] < INFINITY);
-                        if (x[k] > best) {
-                            best = x[k];
-                            arg = i + k;
-                        }
-                    }
-            } else {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < n) {
-                        bad |= !(x[k] < INFINITY);
-                        mx = fmaxf(mx, x[k]);
-                    }
-                const float t = ceilf(mx * a.c_hi + 0.01f);
-                bad |= t > kMaxExponent;
-                if (t >= -kMaxExponent && t <= kMaxExponent) {
-                    const int R = static_cast<int>(t);
-                    if (R > run.R) {
-                        run.sum = shifted(run.sum, R - run.R);
-                        run.R = R;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < n) run.sum += weight(x[k], a.c_hi, a.c_lo, run.R, S.table);
-                }
-            }
-        };
-        if (a.vec && (lo & 3) == 0) {
-            const int n4 = (hi - lo) >> 2;
-            const float4* p4 = reinterpret_cast<const float4*>(p + lo);
-#pragma unroll 4
-            for (int i = threadIdx.x; i < n4; i += kThreads) {
-                const float4 v = __ldcg(p4 + i);
-                const float x[4] = {v.x, v.y, v.z, v.w};
-                take4(x, 4, lo + 4 * i);
-            }
-            for (int i = lo + 4 * n4 + threadIdx.x; i < hi; i += kThreads) {
-                const float x[4] = {__ldcg(p + i), 0.f, 0.f, 0.f};
-                take4(x, 1, i);
-            }
-        } else {
-            for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
-                const float x[4] = {__ldcg(p + i), 0.f, 0.f, 0.f};
-                take4(x, 1, i);
-            }
+        for (int o = 16; o > 0; o >>= 1) {
+            const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+            key = key > other ? key : other;
         }
-        bad = __syncthreads_or(bad);
-        const int slot = row * kMaxParts + static_cast<int>(blockIdx.x) - first_block(a, row);
-        if constexpr (GREEDY) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float ob = __shfl_xor_sync(0xffffffffu, best, o);
-                const int oa = __shfl_xor_sync(0xffffffffu, arg, o);
-                if (ob > best || (ob == best && oa < arg)) {
-                    best = ob;
-                    arg = oa;
-                }
-            }
-            if (lane == 0) {
-                S.warp_max[warp] = best;
-                S.warp_arg[warp] = arg;
-            }
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                for (int w = 1; w < kWarps; ++w)
-                    if (S.warp_max[w] > best || (S.warp_max[w] == best && S.warp_arg[w] < arg)) {
-                        best = S.warp_max[w];
-                        arg = S.warp_arg[w];
-                    }
-                a.part_sum[slot] = (static_cast<uint64_t>(__float_as_uint(best)) << 32) | static_cast<uint32_t>(arg);
-                a.part_exp[slot] = bad ? kBadRow : 0;
-            }
-        } else {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const Running other{__shfl_xor_sync(0xffffffffu, run.sum, o), __shfl_xor_sync(0xffffffffu, run.R, o)};
-                run = join(run, other);
-            }
-            if (lane == 0) {
-                S.warp_sum[warp] = run.sum;
-                S.warp_exp[warp] = run.R;
-            }
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                for (int w = 1; w < kWarps; ++w) run = join(run, Running{S.warp_sum[w], S.warp_exp[w]});
-                a.part_sum[slot] = run.sum;
-                a.part_exp[slot] = bad ? kBadRow : run.R;
-            }
+        if (lane == 0) keys[row * kMaxSlices + lo / a.slice_len] = key;
+    }
+    __syncthreads();
+    if (tid == 0) s_last = atom_add_acq_rel_gpu(a.sync, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+    if (tid >= 1 && tid < a.M) s_token[tid] = __ldg(a.tokens + tid);
+    for (int r = warp; r < a.nrows; r += kWarps) {
+        uint64_t key = 0;
+        for (int i = lane; i < a.slices; i += 32) {
+            const uint64_t k = ldcg64(keys + r * kMaxSlices + i);
+            key = key > k ? key : k;
         }
-        __syncthreads();
-        at = base + hi;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+            key = key > other ? key : other;
+        }
+        const uint64_t none = 0x00800000ull << 32;  // keys of -infinity lie below
+        if (lane == 0) s_arg[r] = key == ~0ull || key < none ? -1 : static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int cur = 0, n = 1;
+        a.result[2] = 0;
+        for (int i = 1; i < a.M; ++i)
+            if (a.parent[i] == cur && s_arg[cur] >= 0 && s_token[i] == s_arg[cur]) a.result[2 + n++] = cur = i;
+        a.result[0] = n;
+        a.result[1] = s_arg[cur];
+        for (; n < a.M; ++n) a.result[2 + n] = -1;
+        a.sync[0] = 0;
     }
 }
 
-// ---------------------------------------------------- passes over one node
-// w(v) = max(P(v) - f Q(v), 0) with P, Q the weights of the node's target and
-// draft rows; without a draft row P(v), but 0 for the removed tokens.  f =
-// fm * 2^fe with fm in [2^63, 2^64), or no Q at all (fm = 0).
-struct Pass {
-    int row, draft;   // row indexes; draft < 0: none
-    uint64_t fm;
-    int fe;
-    uint32_t removed; // nodes whose tokens are removed (no draft row)
+// ---------------------------------------------------------------- sampling
+struct Shared {
+    uint64_t table[kVerifyTable];
+    uint64_t warp_a[kWarps], warp_b[kWarps];
+    float warp_max[kWarps];
+    float row_sum[kRows], row_exp[kRows];  // a row's sum (NaN: no distribution) and exponent
+    float px[MUSER_MAX_M], qx[MUSER_MAX_M], u[MUSER_MAX_M];  // of node i: p(x_i), q(x_i) in its parent's rows
+    int token[MUSER_MAX_M];
+    uint64_t total_a, total_b, before;
+    int owner, exp, flag, found;
 };
 
-__device__ __forceinline__ uint64_t pass_weight(const VerifyArgs& a, const Shared& S, const Pass& P, int v) {
-    uint64_t w = weight(__ldcg(row_ptr(a, P.row) + v), a.c_hi, a.c_lo, S.row_exp[P.row], S.table);
-    if (P.fm) {
-        // f Q = (Q 2^19) fm 2^-64 * 2^(fe + 45): Q 2^19 < 2^62
-        const uint64_t q = weight(__ldcg(row_ptr(a, P.draft) + v), a.c_hi, a.c_lo, S.row_exp[P.draft], S.table);
-        const uint64_t t = __umul64hi(q << 19, P.fm);
-        const int sh = P.fe + 64 - 19;
-        uint64_t fq;
-        if (sh <= 0) fq = shifted(t, -sh);
-        else fq = sh >= __clzll(static_cast<long long>(t)) ? ~0ull >> 1 : t << sh;
-        if (t == 0) fq = 0;
-        w = w > fq ? w - fq : 0;
+// Logits [v0, v1) of the vocabulary are this block's in a pass; a thread's are
+// `per` neighbouring ones.
+struct Span {
+    int v0, n, per, first, last;  // first..last: this thread's, relative to v0
+    __device__ __forceinline__ explicit Span(const VerifyArgs& a) {
+        v0 = min(static_cast<int>(blockIdx.x) * a.span, a.V);
+        n = min(a.span, a.V - v0);
+        per = (a.span + kThreads - 1) / kThreads;
+        first = min(static_cast<int>(threadIdx.x) * per, n);
+        last = min(first + per, n);
     }
-    for (uint32_t left = P.removed; left; left &= left - 1)
-        if (S.token[__ffs(left) - 1] == v) w = 0;
-    return w;
-}
+};
 
-// This thread's part of the block's slice: tokens [v0, v1), in order.
-__device__ __forceinline__ void my_tokens(const VerifyArgs& a, int& v0, int& v1) {
-    const int s0 = static_cast<int>(blockIdx.x) * a.slice, s1 = min(s0 + a.slice, a.V);
-    const int per = (a.slice + kThreads - 1) / kThreads;
-    v0 = min(s0 + static_cast<int>(threadIdx.x) * per, s1);
-    v1 = min(v0 + per, s1);
-}
-
-__device__ uint64_t thread_sum(const VerifyArgs& a, const Shared& S, const Pass& P) {
-    int v0, v1;
-    my_tokens(a, v0, v1);
-    uint64_t sum = 0;
-    for (int v = v0; v < v1; ++v) sum += pass_weight(a, S, P, v);
-    return sum;
-}
-
-// The pass of all blocks: leaves every block's sum in S.blocks and the total
-// in S.total; `mine` is this thread's sum.  False if a barrier gave up.
-__device__ bool pass(const VerifyArgs& a, Shared& S, const Pass& P, unsigned& barriers, uint64_t& mine) {
+// Block sums of two values, to thread 0 and from there to sums[][block].
+__device__ __forceinline__ void publish(const VerifyArgs& a, Shared& S, uint64_t x, uint64_t y, unsigned barriers) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t* sums = a.pass_sum + (barriers & 1) * kMaxParts;
-    mine = thread_sum(a, S, P);
-    const uint64_t w = warp_sum64(mine);
-    if (lane == 0) S.warp_sum[warp] = w;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        uint64_t t = 0;
-        for (int i = 0; i < kWarps; ++i) t += S.warp_sum[i];
-        __stcg(reinterpret_cast<unsigned long long*>(sums + blockIdx.x), static_cast<unsigned long long>(t));
+    x = warp_sum64(x);
+    y = warp_sum64(y);
+    if (lane == 0) {
+        S.warp_a[warp] = x;
+        S.warp_b[warp] = y;
     }
-    if (!grid_barrier(a, ++barriers, &S.flag)) return false;
-    for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += kThreads)
-        S.blocks[b] = __ldcg(reinterpret_cast<const unsigned long long*>(sums + b));
     __syncthreads();
     if (warp == 0) {
-        uint64_t t = 0;
-        for (int b = lane; b < static_cast<int>(gridDim.x); b += 32) t += S.blocks[b];
-        t = warp_sum64(t);
-        if (lane == 0) S.total = t;
+        x = warp_sum64(lane < kWarps ? S.warp_a[lane] : 0);
+        y = warp_sum64(lane < kWarps ? S.warp_b[lane] : 0);
+        if (lane == 0) {
+            uint64_t* to = a.sums + (barriers & 1) * 2 * kMaxBlocks + blockIdx.x;
+            __stcg(reinterpret_cast<unsigned long long*>(to), static_cast<unsigned long long>(x));
+            __stcg(reinterpret_cast<unsigned long long*>(to + kMaxBlocks), static_cast<unsigned long long>(y));
+        }
+    }
+}
+// The totals over all blocks of what was published before the last barrier.
+__device__ __forceinline__ void totals(const VerifyArgs& a, Shared& S, unsigned barriers) {
+    if (threadIdx.x < 32) {
+        const uint64_t* from = a.sums + (barriers & 1) * 2 * kMaxBlocks;
+        uint64_t x = 0, y = 0;
+        for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += 32) {
+            x += ldcg64(from + b);
+            y += ldcg64(from + kMaxBlocks + b);
+        }
+        x = warp_sum64(x);
+        y = warp_sum64(y);
+        if (threadIdx.x == 0) {
+            S.total_a = x;
+            S.total_b = y;
+        }
     }
     __syncthreads();
-    return true;
 }
 
 // floor(u * total) for a float u in [0, 1).
@@ -363,275 +322,402 @@ __device__ uint64_t fraction_of(float u, uint64_t total) {
     return down >= 64 ? hi >> (down - 64) : (lo >> down) | (hi << (64 - down));
 }
 
-template <bool GREEDY>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
-    __shared__ Shared S;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    fill_table(S.table);
-    __syncthreads();
-    stream_rows<GREEDY>(a, S);
-    unsigned barriers = 1;
-    bool ok = grid_barrier(a, barriers, &S.flag);
-    if (ok) {
-        // every block: the rows' sums (or maxima) and the drafted tokens' probabilities
-        for (int row = warp; row < a.nrows; row += kWarps) {
-            const int n = last_block(a, row) - first_block(a, row) + 1;
-            if constexpr (GREEDY) {
-                float best = -INFINITY;
-                int arg = 0x7fffffff, bad = 0;
-                for (int i = lane; i < n; i += 32) {
-                    const uint64_t v = __ldcg(reinterpret_cast<const unsigned long long*>(a.part_sum + row * kMaxParts + i));
-                    bad |= __ldcg(a.part_exp + row * kMaxParts + i);
-                    const float f = __uint_as_float(static_cast<uint32_t>(v >> 32));
-                    const int x = static_cast<int>(v & 0xffffffffu);
-                    if (f > best || (f == best && x < arg)) {
-                        best = f;
-                        arg = x;
-                    }
-                }
+// The block in whose share of the total the sampled point lies: warp 0 sums the
+// blocks' values (brought to the largest exponent) in order.  Leaves the total,
+// the owner, the sum before it and the exponent in S; owner -1: nothing to
+// sample, -2: no distribution.
+__device__ __forceinline__ void find_owner(const VerifyArgs& a, Shared& S, unsigned barriers, const int* exps) {
+    if (threadIdx.x < 32) {
+        constexpr int kEach = kMaxBlocks / 32;
+        const int lane = threadIdx.x, nb = gridDim.x, each = (nb + 31) / 32;
+        const uint64_t* from = a.sums + (barriers & 1) * 2 * kMaxBlocks;
+        uint64_t x[kEach];
+        int e[kEach], R = -(1 << 23);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const float ob = __shfl_xor_sync(0xffffffffu, best, o);
-                    const int oa = __shfl_xor_sync(0xffffffffu, arg, o);
-                    bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-                    if (ob > best || (ob == best && oa < arg)) {
-                        best = ob;
-                        arg = oa;
-                    }
-                }
-                if (lane == 0) S.arg[row] = bad || arg == 0x7fffffff ? -1 : arg;
-            } else {
-                Running run{0, -(1 << 23)};
-                int bad = 0;
-                for (int i = lane; i < n; i += 32) {
-                    const Running o{__ldcg(reinterpret_cast<const unsigned long long*>(a.part_sum + row * kMaxParts + i)),
-                                    __ldcg(a.part_exp + row * kMaxParts + i)};
-                    bad |= o.R == kBadRow;
-                    run = join(run, o);
-                }
+        for (int k = 0; k < kEach; ++k) {
+            const int b = lane * each + k;
+            const bool in = k < each && b < nb;
+            x[k] = in ? ldcg64(from + b) : 0;
+            e[k] = in && exps ? __ldcg(exps + b) : (exps ? -(1 << 23) : 0);
+            R = max(R, e[k]);
+        }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const Running other{__shfl_xor_sync(0xffffffffu, run.sum, o), __shfl_xor_sync(0xffffffffu, run.R, o)};
-                    bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-                    run = join(run, other);
-                }
-                if (lane == 0) {
-                    S.row_sum[row] = bad ? 0 : run.sum;
-                    S.row_exp[row] = run.R;
-                }
-            }
+        for (int o = 16; o > 0; o >>= 1) R = max(R, __shfl_xor_sync(0xffffffffu, R, o));
+        uint64_t mine = 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            x[k] = shifted(x[k], R - e[k]);
+            mine += x[k];
         }
-        if (tid >= 1 && tid < a.M) S.token[tid] = __ldg(a.tokens + tid);
-        __syncthreads();
-        if constexpr (!GREEDY) {
-            if (tid < a.M) {
-                S.u[tid] = static_cast<double>(__ldg(a.uniform + tid));
-                const int x = tid ? S.token[tid] : -1;
-                double p = 0.0, q = 0.0;
-                if (x >= 0 && x < a.V) {
-                    const int up = a.parent[tid], dr = a.draft ? a.draft_at[up] : -1;
-                    if (S.row_sum[up])
-                        p = static_cast<double>(weight(__ldcg(row_ptr(a, up) + x), a.c_hi, a.c_lo, S.row_exp[up], S.table)) /
-                            static_cast<double>(S.row_sum[up]);
-                    if (dr >= 0 && S.row_sum[dr])
-                        q = static_cast<double>(weight(__ldcg(row_ptr(a, dr) + x), a.c_hi, a.c_lo, S.row_exp[dr], S.table)) /
-                            static_cast<double>(S.row_sum[dr]);
-                }
-                S.px[tid] = p;
-                S.qx[tid] = q;
-            }
-            __syncthreads();
+        uint64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
         }
-
-        // the walk: the same in every thread of every block
-        int cur = 0, n = 1, next = -1;
-        uint32_t kept = 1u;
-        if constexpr (GREEDY) {
-            for (int i = 1; i < a.M; ++i)
-                if (a.parent[i] == cur && S.arg[cur] >= 0 && S.token[i] == S.arg[cur]) {
-                    cur = i;
-                    kept |= 1u << i;
-                    ++n;
-                }
-            next = S.arg[cur];
-        } else {
-            double c = 0.0, left = 1.0;
-            uint64_t mine = 0;
-            bool passed = false;  // S.blocks, S.total and mine are those of this node's present state
-            Pass P{0, -1, 0, 0, 0u};
-            auto at_node = [&](int i) {
-                cur = i;
-                c = 0.0;
-                left = 1.0;
-                passed = false;
-                P = Pass{i, a.draft ? a.draft_at[i] : -1, 0, 0, 0u};
-            };
-            at_node(0);
-            bool valid = S.row_sum[0] != 0;
-            for (int i = 1; i < a.M && valid && ok; ++i) {
-                if (a.parent[i] != cur) continue;
-                if (P.draft >= 0 && S.row_sum[P.draft] == 0) {
-                    valid = false;
+        const uint64_t total = __shfl_sync(0xffffffffu, incl, 31);
+        const uint64_t r = fraction_of(__ldg(a.uniform), total);
+        if (lane == 0) {
+            S.total_a = total;
+            S.exp = R;
+            S.owner = R >= kBad ? -2 : -1;
+        }
+        __syncwarp();
+        uint64_t before = incl - mine;
+        if (R < kBad && r >= before && r < incl) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                if (r >= before && r - before < x[k]) {
+                    S.owner = lane * each + k;
+                    S.before = r - before;  // the point within the block's share
                     break;
                 }
-                if (P.draft >= 0) {
-                    if (S.u[i] * left * S.qx[i] < S.px[i] - c * S.qx[i]) {
-                        at_node(i);
-                        kept |= 1u << i;
-                        ++n;
-                        valid = S.row_sum[i] != 0;
-                        continue;
-                    }
-                    c += left;
-                    const double f = c * (static_cast<double>(S.row_sum[P.row]) / static_cast<double>(S.row_sum[P.draft]));
-                    const long long bits = __double_as_longlong(f);
-                    P.fm = (static_cast<uint64_t>(bits & 0xfffffffffffffll) | 0x10000000000000ull) << 11;
-                    P.fe = static_cast<int>((bits >> 52) & 0x7ff) - 1023 - 63;
-                    ok = pass(a, S, P, barriers, mine);
-                    passed = true;
-                    left = static_cast<double>(S.total) / static_cast<double>(S.row_sum[P.row]);
-                } else {
-                    bool again = false;  // the token of a rejected sibling has nothing left
-                    for (uint32_t r = P.removed; r; r &= r - 1) again = again || S.token[__ffs(r) - 1] == S.token[i];
-                    if (!again && S.u[i] * left < S.px[i]) {
-                        at_node(i);
-                        kept |= 1u << i;
-                        ++n;
-                        valid = S.row_sum[i] != 0;
-                        continue;
-                    }
-                    if (!again) left -= S.px[i];
-                    P.removed |= 1u << i;
-                }
+                before += x[k];
             }
-            if (ok && valid && !passed) ok = pass(a, S, P, barriers, mine);
-            if (ok && valid && S.total == 0) {  // nothing is left of the target's row: the row itself
-                P.fm = 0;
-                P.removed = 0;
-                ok = pass(a, S, P, barriers, mine);
-            }
-            if (ok && valid) {
-                // the block that holds the token finds it; the others are done
-                const uint64_t r = fraction_of(__ldg(a.uniform), S.total);
-                uint64_t before = 0;
-                int owner = 0;
-                for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-                    if (before + S.blocks[b] > r) {
-                        owner = b;
-                        break;
-                    }
-                    before += S.blocks[b];
-                }
-                if (owner == static_cast<int>(blockIdx.x)) {
-                    uint64_t incl = mine;
+        }
+    }
+    __syncthreads();
+}
+
+// The token at point r of this block's weights w(k), k = 0..n-1; `mine` is the
+// sum of this thread's.
+template <typename W>
+__device__ __forceinline__ int find_token(Shared& S, const Span& P, uint64_t mine, uint64_t r, W&& w) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t incl = mine;
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                        if (lane >= o) incl += v;
-                    }
-                    if (lane == 31) S.warp_sum[warp] = incl;
-                    __syncthreads();
-                    uint64_t start = before + incl - mine;
-                    for (int w = 0; w < warp; ++w) start += S.warp_sum[w];
-                    if (r >= start && r < start + mine) {
-                        int v0, v1;
-                        my_tokens(a, v0, v1);
-                        uint64_t t = start;
-                        for (int v = v0; v < v1; ++v) {
-                            t += pass_weight(a, S, P, v);
-                            if (t > r) {
-                                S.found = v;
-                                break;
-                            }
-                        }
-                    }
-                    __syncthreads();
-                    next = S.found;
-                    if (tid == 0) a.result[1] = next;
-                }
-            } else if (ok && blockIdx.x == 0 && tid == 0) {
-                a.result[1] = -1;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) S.warp_a[warp] = incl;
+    __syncthreads();
+    uint64_t start = incl - mine;
+    for (int i = 0; i < warp; ++i) start += S.warp_a[i];
+    if (r >= start && r - start < mine) {
+        uint64_t t = start;
+        for (int k = P.first; k < P.last; ++k) {
+            t += w(k);
+            if (t > r) {
+                S.found = P.v0 + k;
+                break;
             }
         }
-        if (blockIdx.x == 0 && tid == 0 && ok) {
-            a.result[0] = n;
-            if constexpr (GREEDY) a.result[1] = next;
-            int at = 0;
-            for (int i = 0; i < a.M; ++i)
-                if ((kept >> i) & 1u) a.result[2 + at++] = i;
-            for (; at < a.M; ++at) a.result[2 + at] = -1;
+    }
+    __syncthreads();
+    return S.found;
+}
+
+__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
+    __shared__ Shared S;
+    extern __shared__ uint64_t held[];  // [span] target weights, [span] draft weights
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Span P(a);
+    uint64_t* wp = held;
+    uint64_t* wq = held + a.span;
+    for (int j = tid; j < kVerifyTable; j += kThreads) S.table[j] = a.table[j];
+    unsigned barriers = 0;
+    bool ok = true;
+    if (a.nrows > 0) {
+        int row, lo, hi;
+        if (my_unit(a, row, lo, hi)) {
+            float sum = 0.f, R = -kMaxExponent;
+            for_slice(row_ptr(a, row), lo, hi, a.vec, [&](float4 v, int) {
+                const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) * a.c_hi;
+                if (t > R) {
+                    const float Rn = ceilf(t);
+                    sum *= ex2(R - Rn);
+                    R = Rn;
+                }
+                sum += (ex2(fmaf(v.x, a.c_hi, -R)) + ex2(fmaf(v.y, a.c_hi, -R))) +
+                       (ex2(fmaf(v.z, a.c_hi, -R)) + ex2(fmaf(v.w, a.c_hi, -R)));
+            });
+            float Rm = R;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) Rm = fmaxf(Rm, __shfl_xor_sync(0xffffffffu, Rm, o));
+            sum = warp_sum(sum * ex2(R - Rm));  // a NaN or +infinity leaves a NaN here
+            if (lane == 0) __stcg(a.part + row * kMaxSlices + lo / a.slice_len, make_float2(sum, Rm));
         }
+        ok = grid_barrier(a, ++barriers, &S.flag);
+        // every block: the rows' sums and the drafted tokens' probabilities
+        if (tid >= 1 && tid < a.M) {
+            S.token[tid] = __ldg(a.tokens + tid);
+            S.u[tid] = __ldg(a.uniform + tid);
+        }
+        __syncthreads();
+        float lx = -INFINITY, ly = -INFINITY;
+        if (tid >= 1 && tid < a.M && S.token[tid] >= 0 && S.token[tid] < a.V) {
+            const int up = a.parent[tid];
+            lx = __ldcg(row_ptr(a, a.target_at[up]) + S.token[tid]);
+            if (a.draft) ly = __ldcg(row_ptr(a, a.draft_at[up]) + S.token[tid]);
+        }
+        for (int r = warp; r < a.nrows; r += kWarps) {
+            float2 x[kMaxSlices / 32];
+            float R = -kMaxExponent, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxSlices / 32; ++k) {
+                x[k] = lane + 32 * k < a.slices ? __ldcg(a.part + r * kMaxSlices + lane + 32 * k) : make_float2(0.f, -kMaxExponent);
+                R = fmaxf(R, x[k].y);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, o));
+#pragma unroll
+            for (int k = 0; k < kMaxSlices / 32; ++k) sum = fmaf(x[k].x, ex2(x[k].y - R), sum);
+            sum = warp_sum(sum);
+            if (lane == 0) {
+                S.row_sum[r] = sum > 0.f && R <= kMaxExponent ? sum : NAN;
+                S.row_exp[r] = R;
+            }
+        }
+        __syncthreads();
+        if (tid >= 1 && tid < a.M) {
+            const int up = a.parent[tid], tr = a.target_at[up], dr = a.draft_at[up];
+            S.px[tid] = ex2(fmaf(lx, a.c_hi, -S.row_exp[tr])) / S.row_sum[tr];
+            S.qx[tid] = a.draft ? ex2(fmaf(ly, a.c_hi, -S.row_exp[dr])) / S.row_sum[dr] : 0.f;
+        }
+        __syncthreads();
+    }
+
+    // This thread's weights of a row, in order: w(k, the logit), four loads at a time.
+    auto each_logit = [&](const float* row, auto&& w) {
+        for (int k = P.first; k < P.last; k += 4) {
+            float x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = k + u < P.last ? __ldcg(row + P.v0 + k + u) : 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (k + u < P.last) w(k + u, x[u]);
+        }
+    };
+
+    // The walk: the same in every thread of every block.
+    int cur = 0, n = 1;
+    uint32_t kept = 1u, removed = 0u;
+    bool valid = true, rejected = false;  // rejected: the node's weights are held, c, left, mine are of its remainder
+    double c = 0.0, left = 1.0;
+    uint64_t fm = 0, mine = 0, sum_p = 0, sum_q = 0;  // f = fm 2^fe
+    int fe = 0;
+    // w = max(P - f Q, 0): f Q = (Q 2^19) fm 2^-64 * 2^(fe + 45), Q 2^19 < 2^62
+    auto remainder = [&](int k) {
+        const uint64_t t = __umul64hi(wq[k] << 19, fm);
+        const int sh = fe + 64 - 19;
+        const uint64_t fq = t == 0 ? 0 : sh <= 0 ? shifted(t, -sh) : sh >= __clzll(static_cast<long long>(t)) ? ~0ull >> 1 : t << sh;
+        return wp[k] > fq ? wp[k] - fq : 0;
+    };
+    auto remainder_pass = [&]() {
+        mine = 0;
+        for (int k = P.first; k < P.last; ++k) mine += remainder(k);
+        publish(a, S, mine, 0, ++barriers);
+        ok = grid_barrier(a, barriers, &S.flag);
+    };
+    for (int i = 1; i < a.M && valid && ok; ++i) {
+        if (a.parent[i] != cur) continue;
+        const int tr = a.target_at[cur], dr = a.draft_at[cur];
+        valid = S.row_sum[tr] == S.row_sum[tr] && (!a.draft || S.row_sum[dr] == S.row_sum[dr]);
+        if (!valid) break;
+        bool again = false;  // a token that was certain, and rejected, has nothing left
+        for (uint32_t r = removed; r; r &= r - 1) again = again || S.token[__ffs(r) - 1] == S.token[i];
+        const float p = S.px[i], q = a.draft ? S.qx[i] : 1.f;
+        if (!again && S.u[i] * static_cast<float>(left) * q < p - (a.draft ? static_cast<float>(c) * q : 0.f)) {
+            cur = i;
+            kept |= 1u << i;
+            ++n;
+            removed = 0;
+            c = 0.0;
+            left = 1.0;
+            rejected = false;
+        } else if (!a.draft) {
+            if (!again) left -= static_cast<double>(p);
+            removed |= 1u << i;
+        } else {
+            if (!rejected) {  // the node's weights, to shared memory, and their sums
+                const int Rp = static_cast<int>(S.row_exp[tr]) + 1, Rq = static_cast<int>(S.row_exp[dr]) + 1;
+                uint64_t sp = 0, sq = 0;
+                each_logit(row_ptr(a, tr), [&](int k, float x) { sp += wp[k] = weight(x, a.c_hi, a.c_lo, Rp, S.table); });
+                each_logit(row_ptr(a, dr), [&](int k, float x) { sq += wq[k] = weight(x, a.c_hi, a.c_lo, Rq, S.table); });
+                publish(a, S, sp, sq, ++barriers);
+                ok = grid_barrier(a, barriers, &S.flag);
+                if (!ok) break;
+                totals(a, S, barriers);
+                sum_p = S.total_a;
+                sum_q = S.total_b;
+                rejected = true;
+            }
+            c += left;
+            const double f = c * (static_cast<double>(sum_p) / static_cast<double>(sum_q));
+            const long long bits = __double_as_longlong(f);
+            fm = (static_cast<uint64_t>(bits & 0xfffffffffffffll) | 0x10000000000000ull) << 11;
+            fe = static_cast<int>((bits >> 52) & 0x7ff) - 1023 - 63;
+            remainder_pass();
+            if (!ok) break;
+            totals(a, S, barriers);
+            left = static_cast<double>(S.total_a) / static_cast<double>(sum_p);
+        }
+    }
+
+    // The next token.
+    int token = -1;
+    bool owner = blockIdx.x == 0;  // who writes it
+    if (ok && valid) {
+        if (rejected && left == 0.0) {  // nothing is left of the target's row: the row itself
+            fm = 0;
+            remainder_pass();
+        }
+        // without rejections: weights relative to the block's own largest exponent
+        const float* row = a.target + static_cast<int64_t>(cur) * a.V;
+        for (int again = 0; !rejected && again < 2 && ok; ++again) {
+            float mx = -INFINITY;
+            bool bad = false;
+            each_logit(row, [&](int, float x) {
+                bad |= !(x < INFINITY);
+                mx = fmaxf(mx, x);
+            });
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (lane == 0) S.warp_max[warp] = mx;
+            bad = __syncthreads_or(bad);
+            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, S.warp_max[w]);
+            const float t = ceilf(mx * a.c_hi + 0.01f);
+            const bool some = t >= -kMaxExponent && t <= kMaxExponent;
+            const int R = some ? static_cast<int>(t) : -(1 << 23);
+            mine = 0;
+            each_logit(row, [&](int k, float x) {
+                uint64_t w = some ? weight(x, a.c_hi, a.c_lo, R, S.table) : 0;
+                for (uint32_t r = removed; r; r &= r - 1)
+                    if (S.token[__ffs(r) - 1] == P.v0 + k) w = 0;
+                mine += wp[k] = w;
+            });
+            if (tid == 0) __stcg(a.exps + blockIdx.x, bad || t > kMaxExponent ? kBad : R);
+            publish(a, S, mine, 0, ++barriers);
+            ok = grid_barrier(a, barriers, &S.flag);
+            if (!ok) break;
+            find_owner(a, S, barriers, a.exps);
+            if (S.owner != -1 || removed == 0) break;
+            removed = 0;  // nothing is left: the row itself
+            ok = grid_barrier(a, ++barriers, &S.flag);  // before exps are written again
+        }
+        if (rejected && ok) find_owner(a, S, barriers, nullptr);
+        if (ok && S.owner >= 0) {
+            owner = S.owner == static_cast<int>(blockIdx.x);
+            if (owner) {
+                uint64_t r = S.before;
+                if (!rejected) r <<= S.exp - __ldcg(a.exps + blockIdx.x);
+                token = rejected ? find_token(S, P, mine, r, remainder) : find_token(S, P, mine, r, [&](int k) { return wp[k]; });
+            }
+        }
+    }
+    if (ok && owner && tid == 0) a.result[1] = token;
+    if (ok && blockIdx.x == 0 && tid == 0) {
+        a.result[0] = n;
+        int at = 2;
+        for (int i = 0; i < a.M; ++i)
+            if ((kept >> i) & 1u) a.result[at++] = i;
+        for (; at < a.M + 2; ++at) a.result[at] = -1;
     }
     // the last block to leave zeroes the counters for the next call
     __syncthreads();
-    if (tid == 0) {
-        const unsigned left = atom_add_acq_rel_gpu(a.sync + 1, 1u);
-        if (left == gridDim.x - 1) {
-            a.sync[0] = 0;
-            a.sync[1] = 0;
-        }
+    if (tid == 0 && atom_add_acq_rel_gpu(a.sync + 1, 1u) == gridDim.x - 1) {
+        a.sync[0] = 0;
+        a.sync[1] = 0;
     }
+}
+
+struct Scratch {
+    size_t part, sums, exps, bytes;
+};
+constexpr Scratch layout() {
+    Scratch s{};
+    s.part = 256;
+    s.sums = s.part + kRows * kMaxSlices * 8;
+    s.exps = s.sums + 4 * kMaxBlocks * 8;
+    s.bytes = s.exps + kMaxBlocks * 4;
+    return s;
+}
+
+const uint64_t* weight_table() {
+    static uint64_t table[kVerifyTable];
+    static std::once_flag once;
+    std::call_once(once, [] {
+        for (int j = 0; j < kVerifyTable; ++j)
+            table[j] = static_cast<uint64_t>(std::exp2(static_cast<double>(j) / kVerifyTable) * static_cast<double>(1ull << kFrac) + 0.5);
+    });
+    return table;
 }
 
 }  // namespace
 
-size_t verify_scratch_bytes() {
-    return 256 + static_cast<size_t>(kRows) * kMaxParts * (sizeof(uint64_t) + sizeof(int)) + 2 * kMaxParts * sizeof(uint64_t);
-}
+size_t verify_scratch_bytes() { return layout().bytes; }
 
 int launch_verify(const float* target, const float* draft, const int32_t* tokens, const int32_t* parent, int M,
                   int64_t vocab, double temperature, const float* uniform, int32_t* result, void* scratch,
                   cudaStream_t s) {
     VerifyArgs a{};
-    a.greedy = temperature == 0.0;
+    const bool greedy = temperature == 0.0;
     a.target = target;
-    a.draft = a.greedy ? nullptr : draft;
+    a.draft = greedy ? nullptr : draft;
     a.tokens = tokens;
     a.uniform = uniform;
     a.result = result;
     a.M = M;
     a.V = static_cast<int>(vocab);
-    const double c = a.greedy ? 1.0 : 1.4426950408889634074 / temperature;
+    const double c = greedy ? 1.0 : 1.4426950408889634074 / temperature;
     a.c_hi = static_cast<float>(c);
     a.c_lo = static_cast<float>(c - static_cast<double>(a.c_hi));
-    a.vec = vocab % 4 == 0 && is_aligned(target, 16) && (!a.draft || is_aligned(draft, 16));
-    a.nrows = M;
+    a.vec = vocab % 4 == 0;  // the matrices are 16-byte aligned
+    bool inner[MUSER_MAX_M] = {};
     for (int i = 0; i < M; ++i) {
         a.parent[i] = i == 0 ? -1 : (parent ? parent[i] : i - 1);
-        a.draft_at[i] = -1;
+        if (i > 0) inner[a.parent[i]] = true;
+        a.target_at[i] = a.draft_at[i] = -1;
     }
-    for (int i = 0; i < M && a.draft; ++i) {
-        bool inner = false;
-        for (int j = 1; j < M; ++j) inner = inner || a.parent[j] == i;
-        if (!inner) continue;
-        a.draft_row[a.nrows - M] = i;
-        a.draft_at[i] = a.nrows++;
-    }
-    const int sms = sm_count();
+    for (int i = 0; i < M; ++i)
+        if (greedy || inner[i]) a.row_node[a.target_at[i] = a.nrows++] = i;
+    a.ntarget = a.nrows;
+    for (int i = 0; i < M && a.draft; ++i)
+        if (inner[i]) a.row_node[a.draft_at[i] = a.nrows++] = i;
+    const int sms = std::min(sm_count(), kMaxBlocks);
     if (sms < 1) return set_error(MUSER_ERR_CUDA, "tree_verify: cannot read the SM count");
-    const int64_t all = static_cast<int64_t>(a.nrows) * vocab;
-    // at least 2,048 logits per block, one block per SM at most
-    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxParts), all / 2048));
-    a.per_block = ((all + blocks - 1) / blocks + 3) / 4 * 4;
-    a.slice = static_cast<int>((vocab + blocks - 1) / blocks);
+    // The first pass gives every warp of the device one slice of a row, of 512
+    // logits at least; the passes over one node give a block 1,024 tokens at
+    // least (fewer blocks meet faster at a barrier).
+    int blocks = greedy ? 1 : static_cast<int>(std::min<int64_t>(sms, (vocab + 1023) / 1024));
+    if (a.nrows > 0) {
+        const int64_t most = std::max<int64_t>(1, std::min<int64_t>(sms * kWarps / a.nrows, (vocab + 511) / 512));
+        a.slices = static_cast<int>(std::min<int64_t>(most, kMaxSlices));
+        a.slice_len = static_cast<int>(((vocab + a.slices - 1) / a.slices + 3) / 4 * 4);
+        a.slices = static_cast<int>((vocab + a.slice_len - 1) / a.slice_len);
+        blocks = std::max(blocks, std::min(sms, a.nrows * a.slices));
+    }
+    a.span = static_cast<int>((vocab + blocks - 1) / blocks);
+    const Scratch L = layout();
     uint8_t* p = static_cast<uint8_t*>(scratch);
     a.sync = reinterpret_cast<unsigned*>(p);
-    a.part_sum = reinterpret_cast<uint64_t*>(p + 256);
-    a.pass_sum = a.part_sum + kRows * kMaxParts;
-    a.part_exp = reinterpret_cast<int*>(a.pass_sum + 2 * kMaxParts);
+    a.part = reinterpret_cast<float2*>(p + L.part);
+    a.sums = reinterpret_cast<uint64_t*>(p + L.sums);
+    a.exps = reinterpret_cast<int*>(p + L.exps);
     a.status = device_status_word();
     if (!a.status) return set_error(MUSER_ERR_CUDA, "tree_verify: no device status word");
+    std::copy(weight_table(), weight_table() + kVerifyTable, a.table);
+    if (greedy) {
+        verify_greedy_kernel<<<blocks, kThreads, 0, s>>>(a);
+        return check_launch("tree_verify");
+    }
+    const size_t smem = static_cast<size_t>(a.span) * 16u;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return cuda_fail(e, "tree_verify: cudaFuncSetAttribute");
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;  // every block resident at once (grid barriers)
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = a.greedy ? cudaLaunchKernelEx(&cfg, verify_kernel<true>, a)
-                                   : cudaLaunchKernelEx(&cfg, verify_kernel<false>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel, a);
     if (e != cudaSuccess) return cuda_fail(e, "tree_verify: cudaLaunchKernelEx");
     return check_launch("tree_verify");
 }
