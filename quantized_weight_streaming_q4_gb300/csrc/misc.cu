@@ -200,7 +200,16 @@ __global__ void kv_store_kernel(uint16_t* key, uint16_t* value, const float* k, 
 // The accepted rows of a drafted tree, binary32 to binary16, into the planes
 // of many layers: blockIdx.y is the plane, a thread takes 8 (vec) or 1
 // consecutive elements of one row of K and of V.
-__global__ void kv_commit_kernel(const __grid_constant__ CommitArgs a) {
+// The launch copies its parameters, 64 bytes a plane: N is the least of 4, 64
+// and 128 that takes them.
+template <int N>
+struct CommitParams {
+    int n;
+    int32_t path[MUSER_MAX_M];
+    CommitPlane plane[N];
+};
+template <int N>
+__global__ void kv_commit_kernel(const __grid_constant__ CommitParams<N> a) {
     const CommitPlane& P = a.plane[blockIdx.y];
     const int step = P.vec ? 8 : 1;
     const int per_row = P.kv_dim / step, total = (a.n - P.j0) * per_row;
@@ -450,8 +459,18 @@ int launch_kv_commit(const CommitArgs& a, cudaStream_t s) {
     }
     const int bs = 128;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((most + bs - 1) / bs, 1024)), static_cast<unsigned>(a.n_planes));
-    kv_commit_kernel<<<grid, bs, 0, s>>>(a);
-    return check_launch("kv_commit");
+    auto go = [&](auto size) {
+        constexpr int N = decltype(size)::value;
+        CommitParams<N> p;
+        p.n = a.n;
+        std::copy(a.path, a.path + a.n, p.path);
+        std::copy(a.plane, a.plane + a.n_planes, p.plane);
+        kv_commit_kernel<N><<<grid, bs, 0, s>>>(p);
+        return check_launch("kv_commit");
+    };
+    if (a.n_planes <= 4) return go(std::integral_constant<int, 4>{});
+    if (a.n_planes <= 64) return go(std::integral_constant<int, 64>{});
+    return go(std::integral_constant<int, kCommitMaxPlanes>{});
 }
 
 int launch_occupy(int ctas, int64_t microseconds, cudaStream_t s) {

@@ -60,7 +60,7 @@ struct VerifyArgs {
     int span;              // tokens per block in the passes over one node
     unsigned* sync;        // arrivals, exits
     float2* part;          // [kRows][kMaxSlices] (sum, exponent); greedy: uint64 keys
-    uint64_t* sums;        // [4][kMaxBlocks]: two passes' buffers in turn, two values each
+    uint64_t* sums;        // [2][4][kMaxBlocks]: two passes' buffers in turn, four values each
     int* exps;             // [kMaxBlocks]
     unsigned* status;
     uint64_t table[kVerifyTable];  // 2^(j / 128) * 2^kFrac
@@ -116,22 +116,27 @@ __device__ __forceinline__ const float* row_ptr(const VerifyArgs& a, int row) {
     return (row < a.ntarget ? a.target : a.draft) + static_cast<int64_t>(a.row_node[row]) * a.V;
 }
 
-// Every block has arrived `times` times.  False if it gave up waiting.
+// Every block has arrived `times` times.  False if it gave up waiting.  The
+// clock is read every 32nd poll: reading it each time doubled the wait.
 __device__ bool grid_barrier(const VerifyArgs& a, unsigned times, int* flag) {
     __syncthreads();
     if (threadIdx.x == 0) {
-        atom_add_acq_rel_gpu(a.sync, 1u);
+        asm volatile("fence.acq_rel.gpu;\n\tred.relaxed.gpu.global.add.u32 [%0], 1;" ::"l"(a.sync) : "memory");
         const unsigned want = gridDim.x * times;
-        const uint64_t t0 = global_ns();
+        uint64_t t0 = 0;
         int ok = 1;
-        for (;;) {
+        for (unsigned poll = 1;; ++poll) {
             unsigned v;
             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.sync) : "memory");
             if (v >= want) break;
-            if (global_ns() - t0 > kGridWaitNs) {
-                atomicOr(a.status, kDevStatusWaitTimeout);
-                ok = 0;
-                break;
+            if (poll % 32 == 0) {
+                const uint64_t t = global_ns();
+                if (t0 == 0) t0 = t;
+                if (t - t0 > kGridWaitNs) {
+                    atomicOr(a.status, kDevStatusWaitTimeout);
+                    ok = 0;
+                    break;
+                }
             }
         }
         *flag = ok;
@@ -249,14 +254,39 @@ __global__ void __launch_bounds__(kThreads) verify_greedy_kernel(const __grid_co
 // ---------------------------------------------------------------- sampling
 struct Shared {
     uint64_t table[kVerifyTable];
-    uint64_t warp_a[kWarps], warp_b[kWarps];
+    uint64_t warp[4][kWarps];
     float warp_max[kWarps];
     float row_sum[kRows], row_exp[kRows];  // a row's sum (NaN: no distribution) and exponent
     float px[MUSER_MAX_M], qx[MUSER_MAX_M], u[MUSER_MAX_M];  // of node i: p(x_i), q(x_i) in its parent's rows
     int token[MUSER_MAX_M];
-    uint64_t total_a, total_b, before;
-    int owner, exp, flag, found;
+    // the present node's remainder, thread 0's binary64 and what all read of it
+    double c, left, sum_p, sum_q;
+    float c_f, left_f;
+    uint64_t fm;  // f = c sum_p / sum_q = fm 2^fe, fm in [2^63, 2^64)
+    int fe;
+    // the sampled point: its block (-1: nothing to sample, -2: no distribution), the place in its share
+    int owner, exp;
+    uint64_t before;
+    int flag, found;
 };
+
+__device__ __forceinline__ void split_factor(double f, uint64_t& fm, int& fe) {
+    const long long bits = __double_as_longlong(f);
+    fm = (static_cast<uint64_t>(bits & 0xfffffffffffffll) | 0x10000000000000ull) << 11;
+    fe = static_cast<int>((bits >> 52) & 0x7ff) - 1023 - 63;
+}
+__device__ __forceinline__ void split_factor(float f, uint64_t& fm, int& fe) {
+    const int bits = __float_as_int(f);
+    fm = static_cast<uint64_t>((bits & 0x7fffff) | 0x800000) << 40;
+    fe = ((bits >> 23) & 0xff) - 127 - 63;
+}
+__device__ __forceinline__ uint64_t scaled(uint64_t t, int sh) {
+    return t == 0 ? 0 : sh <= 0 ? shifted(t, -sh) : sh >= __clzll(static_cast<long long>(t)) ? ~0ull >> 1 : t << sh;
+}
+// f q of a weight (at most 2^43: 19 bits are kept below the last one) and of a
+// block's sum of them.
+__device__ __forceinline__ uint64_t times_f(uint64_t q, uint64_t fm, int fe) { return scaled(__umul64hi(q << 19, fm), fe + 64 - 19); }
+__device__ __forceinline__ uint64_t sum_times_f(uint64_t q, uint64_t fm, int fe) { return scaled(__umul64hi(q, fm), fe + 64); }
 
 // Logits [v0, v1) of the vocabulary are this block's in a pass; a thread's are
 // `per` neighbouring ones.
@@ -271,43 +301,25 @@ struct Span {
     }
 };
 
-// Block sums of two values, to thread 0 and from there to sums[][block].
-__device__ __forceinline__ void publish(const VerifyArgs& a, Shared& S, uint64_t x, uint64_t y, unsigned barriers) {
+// The block's sums of N values, to the pass's buffer.
+template <int N>
+__device__ __forceinline__ void publish(const VerifyArgs& a, Shared& S, const uint64_t (&v)[N], unsigned barriers) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    x = warp_sum64(x);
-    y = warp_sum64(y);
-    if (lane == 0) {
-        S.warp_a[warp] = x;
-        S.warp_b[warp] = y;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const uint64_t x = warp_sum64(v[j]);
+        if (lane == 0) S.warp[j][warp] = x;
     }
     __syncthreads();
     if (warp == 0) {
-        x = warp_sum64(lane < kWarps ? S.warp_a[lane] : 0);
-        y = warp_sum64(lane < kWarps ? S.warp_b[lane] : 0);
-        if (lane == 0) {
-            uint64_t* to = a.sums + (barriers & 1) * 2 * kMaxBlocks + blockIdx.x;
-            __stcg(reinterpret_cast<unsigned long long*>(to), static_cast<unsigned long long>(x));
-            __stcg(reinterpret_cast<unsigned long long*>(to + kMaxBlocks), static_cast<unsigned long long>(y));
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint64_t x = warp_sum64(lane < kWarps ? S.warp[j][lane] : 0);
+            if (lane == 0)
+                __stcg(reinterpret_cast<unsigned long long*>(a.sums + ((barriers & 1) * 4 + j) * kMaxBlocks + blockIdx.x),
+                       static_cast<unsigned long long>(x));
         }
     }
-}
-// The totals over all blocks of what was published before the last barrier.
-__device__ __forceinline__ void totals(const VerifyArgs& a, Shared& S, unsigned barriers) {
-    if (threadIdx.x < 32) {
-        const uint64_t* from = a.sums + (barriers & 1) * 2 * kMaxBlocks;
-        uint64_t x = 0, y = 0;
-        for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += 32) {
-            x += ldcg64(from + b);
-            y += ldcg64(from + kMaxBlocks + b);
-        }
-        x = warp_sum64(x);
-        y = warp_sum64(y);
-        if (threadIdx.x == 0) {
-            S.total_a = x;
-            S.total_b = y;
-        }
-    }
-    __syncthreads();
 }
 
 // floor(u * total) for a float u in [0, 1).
@@ -322,31 +334,71 @@ __device__ uint64_t fraction_of(float u, uint64_t total) {
     return down >= 64 ? hi >> (down - 64) : (lo >> down) | (hi << (64 - down));
 }
 
-// The block in whose share of the total the sampled point lies: warp 0 sums the
-// blocks' values (brought to the largest exponent) in order.  Leaves the total,
-// the owner, the sum before it and the exponent in S; owner -1: nothing to
-// sample, -2: no distribution.
-__device__ __forceinline__ void find_owner(const VerifyArgs& a, Shared& S, unsigned barriers, const int* exps) {
+// What a pass over the present node left, put together by warp 0 of every
+// block from the blocks' published sums:
+//  kLeaf   weights relative to each block's own exponent;
+//  kFirst  the first rejected child: sums of P, of Q, and of both over the tokens
+//          with P > f0 Q, f0 being f from the first pass's binary32 sums.  With
+//          f = sum P / sum Q now exact, a block's share is sum P - f sum Q over
+//          those tokens; the few between f0 and f (1e-6 apart) are worth 1e-6
+//          of themselves.  This saves the barrier between f and the shares;
+//  kNext   a further rejected child, or the row itself: the shares.
+// Leaves the remainder's size, and the sampled point's block and place there.
+enum PassKind { kLeaf, kFirst, kNext };
+template <PassKind KIND>
+__device__ __forceinline__ void settle(const VerifyArgs& a, Shared& S, unsigned barriers) {
     if (threadIdx.x < 32) {
         constexpr int kEach = kMaxBlocks / 32;
         const int lane = threadIdx.x, nb = gridDim.x, each = (nb + 31) / 32;
-        const uint64_t* from = a.sums + (barriers & 1) * 2 * kMaxBlocks;
-        uint64_t x[kEach];
-        int e[kEach], R = -(1 << 23);
+        const uint64_t* from = a.sums + (barriers & 1) * 4 * kMaxBlocks;
+        const float u = __ldg(a.uniform);
+        uint64_t x[kEach], fm = 0;
+        int e[kEach], R = KIND == kLeaf ? -(1 << 23) : 0, fe = 0;
+        if constexpr (KIND == kFirst) {
+            uint64_t sp = 0, sq = 0;
+            for (int b = lane; b < nb; b += 32) {
+                sp += ldcg64(from + b);
+                sq += ldcg64(from + kMaxBlocks + b);
+            }
+            sp = warp_sum64(sp);
+            sq = warp_sum64(sq);
+            if (lane == 0) {
+                S.sum_p = static_cast<double>(sp);
+                S.sum_q = static_cast<double>(sq);
+                S.c = 1.0;
+                split_factor(S.sum_p / S.sum_q, fm, fe);
+                S.fm = fm;
+                S.fe = fe;
+            }
+            fm = __shfl_sync(0xffffffffu, fm, 0);
+            fe = __shfl_sync(0xffffffffu, fe, 0);
+        }
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int b = lane * each + k;
             const bool in = k < each && b < nb;
-            x[k] = in ? ldcg64(from + b) : 0;
-            e[k] = in && exps ? __ldcg(exps + b) : (exps ? -(1 << 23) : 0);
-            R = max(R, e[k]);
+            x[k] = 0;
+            e[k] = R;
+            if (in) {
+                if constexpr (KIND == kFirst) {
+                    const uint64_t p = ldcg64(from + 2 * kMaxBlocks + b), q = sum_times_f(ldcg64(from + 3 * kMaxBlocks + b), fm, fe);
+                    x[k] = p > q ? p - q : 0;
+                } else {
+                    x[k] = ldcg64(from + b);
+                    if constexpr (KIND == kLeaf) e[k] = __ldcg(a.exps + b);
+                }
+            }
         }
+        if constexpr (KIND == kLeaf) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) R = max(R, __shfl_xor_sync(0xffffffffu, R, o));
+            for (int k = 0; k < kEach; ++k) R = max(R, e[k]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) R = max(R, __shfl_xor_sync(0xffffffffu, R, o));
+        }
         uint64_t mine = 0;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            x[k] = shifted(x[k], R - e[k]);
+            if constexpr (KIND == kLeaf) x[k] = shifted(x[k], R - e[k]);
             mine += x[k];
         }
         uint64_t incl = mine;
@@ -356,11 +408,15 @@ __device__ __forceinline__ void find_owner(const VerifyArgs& a, Shared& S, unsig
             if (lane >= o) incl += v;
         }
         const uint64_t total = __shfl_sync(0xffffffffu, incl, 31);
-        const uint64_t r = fraction_of(__ldg(a.uniform), total);
+        const uint64_t r = fraction_of(u, total);
         if (lane == 0) {
-            S.total_a = total;
             S.exp = R;
             S.owner = R >= kBad ? -2 : -1;
+            if constexpr (KIND != kLeaf) {
+                S.left = static_cast<double>(total) / S.sum_p;
+                S.left_f = static_cast<float>(S.left);
+                S.c_f = static_cast<float>(S.c);
+            }
         }
         __syncwarp();
         uint64_t before = incl - mine;
@@ -379,21 +435,29 @@ __device__ __forceinline__ void find_owner(const VerifyArgs& a, Shared& S, unsig
     __syncthreads();
 }
 
-// The token at point r of this block's weights w(k), k = 0..n-1; `mine` is the
-// sum of this thread's.
+// The token at point r of this block's weights w(k), k = 0..n-1 (the last one
+// with a weight, should r lie behind them).
 template <typename W>
-__device__ __forceinline__ int find_token(Shared& S, const Span& P, uint64_t mine, uint64_t r, W&& w) {
+__device__ __forceinline__ int find_token(Shared& S, const Span& P, uint64_t r, W&& w) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t mine = 0;
+    for (int k = P.first; k < P.last; ++k) mine += w(k);
     uint64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
     }
-    if (lane == 31) S.warp_a[warp] = incl;
+    if (lane == 31) S.warp[0][warp] = incl;
+    if (threadIdx.x == 0) S.found = P.v0;
     __syncthreads();
-    uint64_t start = incl - mine;
-    for (int i = 0; i < warp; ++i) start += S.warp_a[i];
+    uint64_t start = incl - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i == warp) start += total;
+        total += S.warp[0][i];
+    }
+    if (r >= total) r = total ? total - 1 : 0;
     if (r >= start && r - start < mine) {
         uint64_t t = start;
         for (int k = P.first; k < P.last; ++k) {
@@ -438,19 +502,19 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             sum = warp_sum(sum * ex2(R - Rm));  // a NaN or +infinity leaves a NaN here
             if (lane == 0) __stcg(a.part + row * kMaxSlices + lo / a.slice_len, make_float2(sum, Rm));
         }
+        // the drafted tokens' logits, in flight during the barrier
+        float lx = -INFINITY, ly = -INFINITY;
+        if (tid >= 1 && tid < a.M) {
+            const int x = __ldg(a.tokens + tid), up = a.parent[tid];
+            S.token[tid] = x;
+            S.u[tid] = __ldg(a.uniform + tid);
+            if (x >= 0 && x < a.V) {
+                lx = __ldcg(row_ptr(a, a.target_at[up]) + x);
+                if (a.draft) ly = __ldcg(row_ptr(a, a.draft_at[up]) + x);
+            }
+        }
         ok = grid_barrier(a, ++barriers, &S.flag);
         // every block: the rows' sums and the drafted tokens' probabilities
-        if (tid >= 1 && tid < a.M) {
-            S.token[tid] = __ldg(a.tokens + tid);
-            S.u[tid] = __ldg(a.uniform + tid);
-        }
-        __syncthreads();
-        float lx = -INFINITY, ly = -INFINITY;
-        if (tid >= 1 && tid < a.M && S.token[tid] >= 0 && S.token[tid] < a.V) {
-            const int up = a.parent[tid];
-            lx = __ldcg(row_ptr(a, a.target_at[up]) + S.token[tid]);
-            if (a.draft) ly = __ldcg(row_ptr(a, a.draft_at[up]) + S.token[tid]);
-        }
         for (int r = warp; r < a.nrows; r += kWarps) {
             float2 x[kMaxSlices / 32];
             float R = -kMaxExponent, sum = 0.f;
@@ -490,25 +554,22 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         }
     };
 
-    // The walk: the same in every thread of every block.
+    // The walk: the same in every thread of every block.  Binary64 is thread
+    // 0's alone: one division by all 512 threads holds an SM for 3 us.
     int cur = 0, n = 1;
     uint32_t kept = 1u, removed = 0u;
-    bool valid = true, rejected = false;  // rejected: the node's weights are held, c, left, mine are of its remainder
-    double c = 0.0, left = 1.0;
-    uint64_t fm = 0, mine = 0, sum_p = 0, sum_q = 0;  // f = fm 2^fe
-    int fe = 0;
-    // w = max(P - f Q, 0): f Q = (Q 2^19) fm 2^-64 * 2^(fe + 45), Q 2^19 < 2^62
-    auto remainder = [&](int k) {
-        const uint64_t t = __umul64hi(wq[k] << 19, fm);
-        const int sh = fe + 64 - 19;
-        const uint64_t fq = t == 0 ? 0 : sh <= 0 ? shifted(t, -sh) : sh >= __clzll(static_cast<long long>(t)) ? ~0ull >> 1 : t << sh;
+    bool valid = true, rejected = false;  // rejected: the node's weights are held, S describes its remainder
+    float left = 1.f, c = 0.f;
+    auto remainder = [&](int k) {  // max(P - f Q, 0)
+        const uint64_t fq = S.fm ? times_f(wq[k], S.fm, S.fe) : 0;
         return wp[k] > fq ? wp[k] - fq : 0;
     };
     auto remainder_pass = [&]() {
-        mine = 0;
-        for (int k = P.first; k < P.last; ++k) mine += remainder(k);
-        publish(a, S, mine, 0, ++barriers);
+        uint64_t v[1] = {0};
+        for (int k = P.first; k < P.last; ++k) v[0] += remainder(k);
+        publish(a, S, v, ++barriers);
         ok = grid_barrier(a, barriers, &S.flag);
+        if (ok) settle<kNext>(a, S, barriers);
     };
     for (int i = 1; i < a.M && valid && ok; ++i) {
         if (a.parent[i] != cur) continue;
@@ -518,49 +579,61 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         bool again = false;  // a token that was certain, and rejected, has nothing left
         for (uint32_t r = removed; r; r &= r - 1) again = again || S.token[__ffs(r) - 1] == S.token[i];
         const float p = S.px[i], q = a.draft ? S.qx[i] : 1.f;
-        if (!again && S.u[i] * static_cast<float>(left) * q < p - (a.draft ? static_cast<float>(c) * q : 0.f)) {
+        if (!again && S.u[i] * left * q < p - (a.draft ? c * q : 0.f)) {
             cur = i;
             kept |= 1u << i;
             ++n;
             removed = 0;
-            c = 0.0;
-            left = 1.0;
+            c = 0.f;
+            left = 1.f;
             rejected = false;
-        } else if (!a.draft) {
-            if (!again) left -= static_cast<double>(p);
+            continue;
+        }
+        if (!a.draft) {
+            if (!again) left -= p;
             removed |= 1u << i;
+            continue;
+        }
+        if (!rejected) {  // the node's weights, to shared memory
+            const int Rp = static_cast<int>(S.row_exp[tr]) + 1, Rq = static_cast<int>(S.row_exp[dr]) + 1;
+            uint64_t fm, v[4] = {0, 0, 0, 0};
+            int fe;
+            split_factor(S.row_sum[tr] / S.row_sum[dr], fm, fe);
+            each_logit(row_ptr(a, tr), [&](int k, float x) { v[0] += wp[k] = weight(x, a.c_hi, a.c_lo, Rp, S.table); });
+            each_logit(row_ptr(a, dr), [&](int k, float x) {
+                const uint64_t y = weight(x, a.c_hi, a.c_lo, Rq, S.table);
+                v[1] += wq[k] = y;
+                if (wp[k] > times_f(y, fm, fe)) {
+                    v[2] += wp[k];
+                    v[3] += y;
+                }
+            });
+            publish(a, S, v, ++barriers);
+            ok = grid_barrier(a, barriers, &S.flag);
+            if (!ok) break;
+            settle<kFirst>(a, S, barriers);
+            rejected = true;
         } else {
-            if (!rejected) {  // the node's weights, to shared memory, and their sums
-                const int Rp = static_cast<int>(S.row_exp[tr]) + 1, Rq = static_cast<int>(S.row_exp[dr]) + 1;
-                uint64_t sp = 0, sq = 0;
-                each_logit(row_ptr(a, tr), [&](int k, float x) { sp += wp[k] = weight(x, a.c_hi, a.c_lo, Rp, S.table); });
-                each_logit(row_ptr(a, dr), [&](int k, float x) { sq += wq[k] = weight(x, a.c_hi, a.c_lo, Rq, S.table); });
-                publish(a, S, sp, sq, ++barriers);
-                ok = grid_barrier(a, barriers, &S.flag);
-                if (!ok) break;
-                totals(a, S, barriers);
-                sum_p = S.total_a;
-                sum_q = S.total_b;
-                rejected = true;
+            if (tid == 0) {
+                S.c += S.left;
+                split_factor(S.c * (S.sum_p / S.sum_q), S.fm, S.fe);
             }
-            c += left;
-            const double f = c * (static_cast<double>(sum_p) / static_cast<double>(sum_q));
-            const long long bits = __double_as_longlong(f);
-            fm = (static_cast<uint64_t>(bits & 0xfffffffffffffll) | 0x10000000000000ull) << 11;
-            fe = static_cast<int>((bits >> 52) & 0x7ff) - 1023 - 63;
+            __syncthreads();
             remainder_pass();
             if (!ok) break;
-            totals(a, S, barriers);
-            left = static_cast<double>(S.total_a) / static_cast<double>(sum_p);
         }
+        left = S.left_f;
+        c = S.c_f;
     }
 
     // The next token.
     int token = -1;
     bool owner = blockIdx.x == 0;  // who writes it
     if (ok && valid) {
-        if (rejected && left == 0.0) {  // nothing is left of the target's row: the row itself
-            fm = 0;
+        if (rejected && S.owner == -1) {  // nothing is left of the target's row: the row itself
+            __syncthreads();
+            if (tid == 0) S.fm = 0;
+            __syncthreads();
             remainder_pass();
         }
         // without rejections: weights relative to the block's own largest exponent
@@ -576,33 +649,32 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             if (lane == 0) S.warp_max[warp] = mx;
             bad = __syncthreads_or(bad);
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, S.warp_max[w]);
             const float t = ceilf(mx * a.c_hi + 0.01f);
             const bool some = t >= -kMaxExponent && t <= kMaxExponent;
             const int R = some ? static_cast<int>(t) : -(1 << 23);
-            mine = 0;
+            uint64_t v[1] = {0};
             each_logit(row, [&](int k, float x) {
                 uint64_t w = some ? weight(x, a.c_hi, a.c_lo, R, S.table) : 0;
                 for (uint32_t r = removed; r; r &= r - 1)
                     if (S.token[__ffs(r) - 1] == P.v0 + k) w = 0;
-                mine += wp[k] = w;
+                v[0] += wp[k] = w;
             });
             if (tid == 0) __stcg(a.exps + blockIdx.x, bad || t > kMaxExponent ? kBad : R);
-            publish(a, S, mine, 0, ++barriers);
+            publish(a, S, v, ++barriers);
             ok = grid_barrier(a, barriers, &S.flag);
             if (!ok) break;
-            find_owner(a, S, barriers, a.exps);
+            settle<kLeaf>(a, S, barriers);
             if (S.owner != -1 || removed == 0) break;
             removed = 0;  // nothing is left: the row itself
             ok = grid_barrier(a, ++barriers, &S.flag);  // before exps are written again
         }
-        if (rejected && ok) find_owner(a, S, barriers, nullptr);
         if (ok && S.owner >= 0) {
             owner = S.owner == static_cast<int>(blockIdx.x);
             if (owner) {
-                uint64_t r = S.before;
-                if (!rejected) r <<= S.exp - __ldcg(a.exps + blockIdx.x);
-                token = rejected ? find_token(S, P, mine, r, remainder) : find_token(S, P, mine, r, [&](int k) { return wp[k]; });
+                if (rejected) token = find_token(S, P, S.before, remainder);
+                else token = find_token(S, P, S.before << (S.exp - __ldcg(a.exps + blockIdx.x)), [&](int k) { return wp[k]; });
             }
         }
     }
@@ -629,7 +701,7 @@ constexpr Scratch layout() {
     Scratch s{};
     s.part = 256;
     s.sums = s.part + kRows * kMaxSlices * 8;
-    s.exps = s.sums + 4 * kMaxBlocks * 8;
+    s.exps = s.sums + 8 * kMaxBlocks * 8;
     s.bytes = s.exps + kMaxBlocks * 4;
     return s;
 }
