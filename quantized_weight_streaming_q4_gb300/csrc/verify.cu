@@ -37,7 +37,7 @@ constexpr int kFrac = 42;  // fraction bits of a weight
 constexpr int kRows = 2 * MUSER_MAX_M;
 constexpr int kVerifyTable = 128;
 constexpr int kMaxSlices = 256;  // of a row
-constexpr int kMaxBlocks = 256;
+constexpr int kMaxBlocks = 160;  // 152 SMs; a lane of the warp that joins the blocks' sums takes 5
 constexpr float kMaxExponent = 32768.f;
 constexpr int kBad = 1 << 24;  // exponent mark of a slice that holds a NaN or an infinity
 constexpr uint64_t kGridWaitNs = 2000000000ull;
@@ -52,6 +52,7 @@ struct VerifyArgs {
     float c_hi, c_lo;      // log2(e) / T
     int vec;               // rows are 16-byte aligned
     int parent[MUSER_MAX_M];
+    uint32_t children[MUSER_MAX_M];
     int nrows;             // rows streamed first (greedy: all; else rows with children, targets then drafts)
     int row_node[kRows];   // their nodes
     int ntarget;           // how many of them are target rows
@@ -60,7 +61,7 @@ struct VerifyArgs {
     int span;              // tokens per block in the passes over one node
     unsigned* sync;        // arrivals, exits
     float2* part;          // [kRows][kMaxSlices] (sum, exponent); greedy: uint64 keys
-    uint64_t* sums;        // [2][4][kMaxBlocks]: two passes' buffers in turn, four values each
+    uint64_t* sums;        // [2][kMaxBlocks][4]: two passes' buffers in turn, a record a block
     int* exps;             // [kMaxBlocks]
     unsigned* status;
     uint64_t table[kVerifyTable];  // 2^(j / 128) * 2^kFrac
@@ -118,7 +119,7 @@ __device__ __forceinline__ const float* row_ptr(const VerifyArgs& a, int row) {
 
 // Every block has arrived `times` times.  False if it gave up waiting.  The
 // clock is read every 32nd poll: reading it each time doubled the wait.
-__device__ bool grid_barrier(const VerifyArgs& a, unsigned times, int* flag) {
+__device__ __forceinline__ bool grid_barrier(const VerifyArgs& a, unsigned times, int* flag) {
     __syncthreads();
     if (threadIdx.x == 0) {
         asm volatile("fence.acq_rel.gpu;\n\tred.relaxed.gpu.global.add.u32 [%0], 1;" ::"l"(a.sync) : "memory");
@@ -259,8 +260,10 @@ struct Shared {
     float row_sum[kRows], row_exp[kRows];  // a row's sum (NaN: no distribution) and exponent
     float px[MUSER_MAX_M], qx[MUSER_MAX_M], u[MUSER_MAX_M];  // of node i: p(x_i), q(x_i) in its parent's rows
     int token[MUSER_MAX_M];
-    // the present node's remainder, thread 0's binary64 and what all read of it
-    double c, left, sum_p, sum_q;
+    uint32_t first, fine;  // bit i: node i passes the test of a first child; its parent's rows are distributions
+    // the present node's remainder: sums of P, Q and of what is left; c (thread 0's, in binary64)
+    uint64_t sum_p, sum_q, total;
+    double c;
     float c_f, left_f;
     uint64_t fm;  // f = c sum_p / sum_q = fm 2^fe, fm in [2^63, 2^64)
     int fe;
@@ -279,6 +282,23 @@ __device__ __forceinline__ void split_factor(float f, uint64_t& fm, int& fe) {
     const int bits = __float_as_int(f);
     fm = static_cast<uint64_t>((bits & 0x7fffff) | 0x800000) << 40;
     fe = ((bits >> 23) & 0xff) - 127 - 63;
+}
+// p / q for p, q > 0, to about 2^-60: with s = q 2^z in [1/2, 1), r = 1/s from
+// binary32 and two Newton steps r += r (1 - s r) in 64-bit fixed point.
+__device__ __forceinline__ void split_quotient(uint64_t p, uint64_t q, uint64_t& fm, int& fe) {
+    const int zp = __clzll(static_cast<long long>(p)), zq = __clzll(static_cast<long long>(q));
+    const uint64_t pn = p << zp, s = q << zq;
+    const float r0 = 1.f / (static_cast<float>(static_cast<uint32_t>(s >> 40)) * 0x1p-24f);
+    uint64_t r = static_cast<uint64_t>(static_cast<uint32_t>(r0 * 0x1p30f)) << 32;  // r 2^62
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const long long e = static_cast<long long>((1ull << 62) - __umul64hi(s, r));  // small, either sign
+        r += static_cast<uint64_t>(__mul64hi(static_cast<long long>(r >> 1), e << 3));
+    }
+    const uint64_t f = __umul64hi(pn, r);
+    const int z = __clzll(static_cast<long long>(f));
+    fm = f << z;
+    fe = zq - zp - 62 - z;
 }
 __device__ __forceinline__ uint64_t scaled(uint64_t t, int sh) {
     return t == 0 ? 0 : sh <= 0 ? shifted(t, -sh) : sh >= __clzll(static_cast<long long>(t)) ? ~0ull >> 1 : t << sh;
@@ -301,7 +321,7 @@ struct Span {
     }
 };
 
-// The block's sums of N values, to the pass's buffer.
+// The block's sums of N values, to its record of the pass's buffer.
 template <int N>
 __device__ __forceinline__ void publish(const VerifyArgs& a, Shared& S, const uint64_t (&v)[N], unsigned barriers) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -312,18 +332,19 @@ __device__ __forceinline__ void publish(const VerifyArgs& a, Shared& S, const ui
     }
     __syncthreads();
     if (warp == 0) {
+        uint64_t t[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const uint64_t x = warp_sum64(lane < kWarps ? S.warp[j][lane] : 0);
-            if (lane == 0)
-                __stcg(reinterpret_cast<unsigned long long*>(a.sums + ((barriers & 1) * 4 + j) * kMaxBlocks + blockIdx.x),
-                       static_cast<unsigned long long>(x));
+        for (int j = 0; j < N; ++j) t[j] = warp_sum64(lane < kWarps ? S.warp[j][lane] : 0);
+        if (lane == 0) {
+            ulonglong2* to = reinterpret_cast<ulonglong2*>(a.sums + ((barriers & 1) * kMaxBlocks + blockIdx.x) * 4);
+            __stcg(to, make_ulonglong2(t[0], N > 1 ? t[N > 1 ? 1 : 0] : 0));
+            if (N > 2) __stcg(to + 1, make_ulonglong2(t[N > 2 ? 2 : 0], t[N > 2 ? 3 : 0]));
         }
     }
 }
 
 // floor(u * total) for a float u in [0, 1).
-__device__ uint64_t fraction_of(float u, uint64_t total) {
+__device__ __forceinline__ uint64_t fraction_of(float u, uint64_t total) {
     if (!(u > 0.f)) return 0;
     u = fminf(u, 0x1.fffffep-1f);
     const int e = (__float_as_int(u) >> 23) & 0xff;  // u = mant * 2^(e - 150)
@@ -350,43 +371,50 @@ __device__ __forceinline__ void settle(const VerifyArgs& a, Shared& S, unsigned 
     if (threadIdx.x < 32) {
         constexpr int kEach = kMaxBlocks / 32;
         const int lane = threadIdx.x, nb = gridDim.x, each = (nb + 31) / 32;
-        const uint64_t* from = a.sums + (barriers & 1) * 4 * kMaxBlocks;
+        const ulonglong2* from = reinterpret_cast<const ulonglong2*>(a.sums + (barriers & 1) * 4 * kMaxBlocks);
         const float u = __ldg(a.uniform);
         uint64_t x[kEach], fm = 0;
         int e[kEach], R = KIND == kLeaf ? -(1 << 23) : 0, fe = 0;
+        ulonglong2 s0[kEach], s1[KIND == kFirst ? kEach : 1];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {  // every load of the lane's blocks in flight together
+            const int b = lane * each + k;
+            const bool in = k < each && b < nb;
+            s0[k] = make_ulonglong2(0, 0);
+            if (KIND == kFirst) s1[KIND == kFirst ? k : 0] = make_ulonglong2(0, 0);
+            e[k] = R;
+            if (in) {
+                s0[k] = __ldcg(from + 2 * b);
+                if (KIND == kFirst) s1[KIND == kFirst ? k : 0] = __ldcg(from + 2 * b + 1);
+                if (KIND == kLeaf) e[k] = __ldcg(a.exps + b);
+            }
+        }
         if constexpr (KIND == kFirst) {
             uint64_t sp = 0, sq = 0;
-            for (int b = lane; b < nb; b += 32) {
-                sp += ldcg64(from + b);
-                sq += ldcg64(from + kMaxBlocks + b);
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                sp += s0[k].x;
+                sq += s0[k].y;
             }
             sp = warp_sum64(sp);
             sq = warp_sum64(sq);
+            split_quotient(sp, sq, fm, fe);  // c = 1
             if (lane == 0) {
-                S.sum_p = static_cast<double>(sp);
-                S.sum_q = static_cast<double>(sq);
+                S.sum_p = sp;
+                S.sum_q = sq;
                 S.c = 1.0;
-                split_factor(S.sum_p / S.sum_q, fm, fe);
+                S.c_f = 1.f;
                 S.fm = fm;
                 S.fe = fe;
             }
-            fm = __shfl_sync(0xffffffffu, fm, 0);
-            fe = __shfl_sync(0xffffffffu, fe, 0);
         }
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int b = lane * each + k;
-            const bool in = k < each && b < nb;
-            x[k] = 0;
-            e[k] = R;
-            if (in) {
-                if constexpr (KIND == kFirst) {
-                    const uint64_t p = ldcg64(from + 2 * kMaxBlocks + b), q = sum_times_f(ldcg64(from + 3 * kMaxBlocks + b), fm, fe);
-                    x[k] = p > q ? p - q : 0;
-                } else {
-                    x[k] = ldcg64(from + b);
-                    if constexpr (KIND == kLeaf) e[k] = __ldcg(a.exps + b);
-                }
+            if constexpr (KIND == kFirst) {
+                const uint64_t q = sum_times_f(s1[k].y, fm, fe);
+                x[k] = s1[k].x > q ? s1[k].x - q : 0;
+            } else {
+                x[k] = s0[k].x;
             }
         }
         if constexpr (KIND == kLeaf) {
@@ -413,9 +441,8 @@ __device__ __forceinline__ void settle(const VerifyArgs& a, Shared& S, unsigned 
             S.exp = R;
             S.owner = R >= kBad ? -2 : -1;
             if constexpr (KIND != kLeaf) {
-                S.left = static_cast<double>(total) / S.sum_p;
-                S.left_f = static_cast<float>(S.left);
-                S.c_f = static_cast<float>(S.c);
+                S.total = total;
+                S.left_f = static_cast<float>(total) / static_cast<float>(S.sum_p);
             }
         }
         __syncwarp();
@@ -472,7 +499,7 @@ __device__ __forceinline__ int find_token(Shared& S, const Span& P, uint64_t r, 
     return S.found;
 }
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ Shared S;
     extern __shared__ uint64_t held[];  // [span] target weights, [span] draft weights
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -515,29 +542,47 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         }
         ok = grid_barrier(a, ++barriers, &S.flag);
         // every block: the rows' sums and the drafted tokens' probabilities
-        for (int r = warp; r < a.nrows; r += kWarps) {
-            float2 x[kMaxSlices / 32];
+        float2 x[2][kMaxSlices / 32];  // a warp has two rows at most: their loads go out together
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = warp + j * kWarps;
+#pragma unroll
+            for (int k = 0; k < kMaxSlices / 32; ++k)
+                x[j][k] = r < a.nrows && lane + 32 * k < a.slices ? __ldcg(a.part + r * kMaxSlices + lane + 32 * k)
+                                                                  : make_float2(0.f, -kMaxExponent);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
             float R = -kMaxExponent, sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < kMaxSlices / 32; ++k) {
-                x[k] = lane + 32 * k < a.slices ? __ldcg(a.part + r * kMaxSlices + lane + 32 * k) : make_float2(0.f, -kMaxExponent);
-                R = fmaxf(R, x[k].y);
-            }
+            for (int k = 0; k < kMaxSlices / 32; ++k) R = fmaxf(R, x[j][k].y);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, o));
 #pragma unroll
-            for (int k = 0; k < kMaxSlices / 32; ++k) sum = fmaf(x[k].x, ex2(x[k].y - R), sum);
+            for (int k = 0; k < kMaxSlices / 32; ++k) sum = fmaf(x[j][k].x, ex2(x[j][k].y - R), sum);
             sum = warp_sum(sum);
-            if (lane == 0) {
-                S.row_sum[r] = sum > 0.f && R <= kMaxExponent ? sum : NAN;
-                S.row_exp[r] = R;
+            if (lane == 0 && warp + j * kWarps < a.nrows) {
+                S.row_sum[warp + j * kWarps] = sum > 0.f && R <= kMaxExponent ? sum : NAN;
+                S.row_exp[warp + j * kWarps] = R;
             }
         }
         __syncthreads();
-        if (tid >= 1 && tid < a.M) {
-            const int up = a.parent[tid], tr = a.target_at[up], dr = a.draft_at[up];
-            S.px[tid] = ex2(fmaf(lx, a.c_hi, -S.row_exp[tr])) / S.row_sum[tr];
-            S.qx[tid] = a.draft ? ex2(fmaf(ly, a.c_hi, -S.row_exp[dr])) / S.row_sum[dr] : 0.f;
+        if (warp == 0) {  // lane i: node i's probabilities, and whether it is accepted if it is its parent's first child
+            bool first = false, fine = true;
+            if (lane >= 1 && lane < a.M) {
+                const int up = a.parent[lane], tr = a.target_at[up], dr = a.draft_at[up];
+                const float p = ex2(fmaf(lx, a.c_hi, -S.row_exp[tr])) / S.row_sum[tr];
+                const float q = a.draft ? ex2(fmaf(ly, a.c_hi, -S.row_exp[dr])) / S.row_sum[dr] : 1.f;
+                S.px[lane] = p;
+                S.qx[lane] = q;
+                first = S.u[lane] * q < p;
+                fine = S.row_sum[tr] == S.row_sum[tr] && (!a.draft || S.row_sum[dr] == S.row_sum[dr]);
+            }
+            const uint32_t f = __ballot_sync(0xffffffffu, first), g = __ballot_sync(0xffffffffu, fine);
+            if (lane == 0) {
+                S.first = f;
+                S.fine = g;
+            }
         }
         __syncthreads();
     }
@@ -558,6 +603,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     // 0's alone: one division by all 512 threads holds an SM for 3 us.
     int cur = 0, n = 1;
     uint32_t kept = 1u, removed = 0u;
+    const uint32_t first = a.nrows ? S.first : 0u, fine = a.nrows ? S.fine : 0u;
     bool valid = true, rejected = false;  // rejected: the node's weights are held, S describes its remainder
     float left = 1.f, c = 0.f;
     auto remainder = [&](int k) {  // max(P - f Q, 0)
@@ -571,16 +617,24 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         ok = grid_barrier(a, barriers, &S.flag);
         if (ok) settle<kNext>(a, S, barriers);
     };
-    for (int i = 1; i < a.M && valid && ok; ++i) {
-        if (a.parent[i] != cur) continue;
-        const int tr = a.target_at[cur], dr = a.draft_at[cur];
-        valid = S.row_sum[tr] == S.row_sum[tr] && (!a.draft || S.row_sum[dr] == S.row_sum[dr]);
+    uint32_t children = a.children[0];  // of the present node, not tried yet
+    while (children && ok) {
+        const int i = __ffs(children) - 1;
+        valid = (fine >> i) & 1u;
         if (!valid) break;
-        bool again = false;  // a token that was certain, and rejected, has nothing left
-        for (uint32_t r = removed; r; r &= r - 1) again = again || S.token[__ffs(r) - 1] == S.token[i];
-        const float p = S.px[i], q = a.draft ? S.qx[i] : 1.f;
-        if (!again && S.u[i] * left * q < p - (a.draft ? c * q : 0.f)) {
+        bool taken = (first >> i) & 1u;
+        if (rejected || removed) {  // not a first child
+            bool again = false;  // a token that was certain, and rejected, has nothing left
+            for (uint32_t r = removed; r; r &= r - 1) again = again || S.token[__ffs(r) - 1] == S.token[i];
+            const float p = S.px[i], q = S.qx[i];
+            taken = !again && S.u[i] * left * q < p - c * q;
+            if (!taken && !a.draft && !again) left -= p;
+        } else if (!taken && !a.draft) {
+            left = 1.f - S.px[i];
+        }
+        if (taken) {
             cur = i;
+            children = a.children[i];
             kept |= 1u << i;
             ++n;
             removed = 0;
@@ -589,25 +643,40 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             rejected = false;
             continue;
         }
+        children &= children - 1;
         if (!a.draft) {
-            if (!again) left -= p;
             removed |= 1u << i;
             continue;
         }
+        const int tr = a.target_at[cur], dr = a.draft_at[cur];
         if (!rejected) {  // the node's weights, to shared memory
             const int Rp = static_cast<int>(S.row_exp[tr]) + 1, Rq = static_cast<int>(S.row_exp[dr]) + 1;
             uint64_t fm, v[4] = {0, 0, 0, 0};
             int fe;
             split_factor(S.row_sum[tr] / S.row_sum[dr], fm, fe);
-            each_logit(row_ptr(a, tr), [&](int k, float x) { v[0] += wp[k] = weight(x, a.c_hi, a.c_lo, Rp, S.table); });
-            each_logit(row_ptr(a, dr), [&](int k, float x) {
-                const uint64_t y = weight(x, a.c_hi, a.c_lo, Rq, S.table);
-                v[1] += wq[k] = y;
-                if (wp[k] > times_f(y, fm, fe)) {
-                    v[2] += wp[k];
-                    v[3] += y;
+            const float* pr = row_ptr(a, tr) + P.v0;
+            const float* qr = row_ptr(a, dr) + P.v0;
+            for (int k = P.first; k < P.last; k += 4) {  // eight loads in flight together
+                float x[4], y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[j] = k + j < P.last ? __ldcg(pr + k + j) : -INFINITY;
+                    y[j] = k + j < P.last ? __ldcg(qr + k + j) : -INFINITY;
                 }
-            });
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (k + j >= P.last) break;
+                    const uint64_t w = weight(x[j], a.c_hi, a.c_lo, Rp, S.table), z = weight(y[j], a.c_hi, a.c_lo, Rq, S.table);
+                    wp[k + j] = w;
+                    wq[k + j] = z;
+                    v[0] += w;
+                    v[1] += z;
+                    if (w > times_f(z, fm, fe)) {
+                        v[2] += w;
+                        v[3] += z;
+                    }
+                }
+            }
             publish(a, S, v, ++barriers);
             ok = grid_barrier(a, barriers, &S.flag);
             if (!ok) break;
@@ -615,8 +684,9 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             rejected = true;
         } else {
             if (tid == 0) {
-                S.c += S.left;
-                split_factor(S.c * (S.sum_p / S.sum_q), S.fm, S.fe);
+                S.c += static_cast<double>(S.total) / static_cast<double>(S.sum_p);
+                S.c_f = static_cast<float>(S.c);
+                split_factor(S.c * (static_cast<double>(S.sum_p) / static_cast<double>(S.sum_q)), S.fm, S.fe);
             }
             __syncthreads();
             remainder_pass();
@@ -641,9 +711,11 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         for (int again = 0; !rejected && again < 2 && ok; ++again) {
             float mx = -INFINITY;
             bool bad = false;
-            each_logit(row, [&](int, float x) {
+            float* logit = reinterpret_cast<float*>(wq);  // this thread's own, until the weights are made
+            each_logit(row, [&](int k, float x) {
                 bad |= !(x < INFINITY);
                 mx = fmaxf(mx, x);
+                logit[k] = x;
             });
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -655,12 +727,12 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             const bool some = t >= -kMaxExponent && t <= kMaxExponent;
             const int R = some ? static_cast<int>(t) : -(1 << 23);
             uint64_t v[1] = {0};
-            each_logit(row, [&](int k, float x) {
-                uint64_t w = some ? weight(x, a.c_hi, a.c_lo, R, S.table) : 0;
+            for (int k = P.first; k < P.last; ++k) {
+                uint64_t w = some ? weight(logit[k], a.c_hi, a.c_lo, R, S.table) : 0;
                 for (uint32_t r = removed; r; r &= r - 1)
                     if (S.token[__ffs(r) - 1] == P.v0 + k) w = 0;
                 v[0] += wp[k] = w;
-            });
+            }
             if (tid == 0) __stcg(a.exps + blockIdx.x, bad || t > kMaxExponent ? kBad : R);
             publish(a, S, v, ++barriers);
             ok = grid_barrier(a, barriers, &S.flag);
@@ -739,7 +811,10 @@ int launch_verify(const float* target, const float* draft, const int32_t* tokens
     bool inner[MUSER_MAX_M] = {};
     for (int i = 0; i < M; ++i) {
         a.parent[i] = i == 0 ? -1 : (parent ? parent[i] : i - 1);
-        if (i > 0) inner[a.parent[i]] = true;
+        if (i > 0) {
+            inner[a.parent[i]] = true;
+            a.children[a.parent[i]] |= 1u << i;
+        }
         a.target_at[i] = a.draft_at[i] = -1;
     }
     for (int i = 0; i < M; ++i)
