@@ -176,23 +176,27 @@ int launch_generic(AttnArgs a, void* scratch, cudaStream_t s) {
     return launch_combine(a, a.nchunks, s);
 }
 
-// Tensor-core kernel: 128 query rows a block, tiles of 128 keys.
-int launch_tc(AttnArgs a, void* scratch, cudaStream_t s) {
-    const int rows = a.M * a.group, blocks = (rows + 127) / 128, heads = a.G * blocks;
+// The tensor-core kernels, one block per SM: tiles of 128 keys, blocks of R
+// query rows.
+template <typename Resident, typename Launch>
+int launch_tiles(AttnArgs a, int R, void* scratch, cudaStream_t s, Resident&& resident, Launch&& launch) {
+    const int rows = a.M * a.group, blocks = (rows + R - 1) / R, heads = a.G * blocks;
+    // up to 16 chunks of 128 keys: one cluster and no second kernel
     int chunks = std::min(16, std::max(1, (a.n_common + 127) / 128));
     a.cluster = 1;
     while (a.cluster < chunks) a.cluster *= 2;
     if (a.n_common > 16 * 256) {  // one block per SM, in small clusters
-        a.cluster = 4;
-        const int most = attn_tc_resident(a.D, 4) / heads;
-        if (most > 4) chunks = std::min(4 * most, static_cast<int>(4 * max_parts(a.G, rows)));
-        else a.cluster = 16;
+        const int most = resident(4) / heads;
+        if (most > 4) {
+            a.cluster = 4;
+            chunks = std::min(4 * most, static_cast<int>(4 * max_parts(a.G, rows)));
+        }
     }
     a.chunk = std::max(16, ((a.n_common + chunks - 1) / chunks + 15) / 16 * 16);
     a.nchunks = std::max(1, (a.n_common + a.chunk - 1) / a.chunk);
     const int clusters = (a.nchunks + a.cluster - 1) / a.cluster;
     place_parts(a, clusters, scratch);
-    MUSER_TRY(launch_attn_tc(a, dim3(static_cast<unsigned>(clusters * a.cluster), static_cast<unsigned>(a.G), static_cast<unsigned>(blocks)), s));
+    MUSER_TRY(launch(a, dim3(static_cast<unsigned>(clusters * a.cluster), static_cast<unsigned>(a.G), static_cast<unsigned>(blocks))));
     return clusters > 1 ? launch_combine(a, clusters, s) : MUSER_OK;
 }
 
@@ -202,7 +206,14 @@ int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
     if (!attn_mma_supported(a)) return launch_generic(a, scratch, s);
     a.status = device_status_word();
     if (!a.status) return set_error(MUSER_ERR_CUDA, "attention: no device status word");
-    if (a.D <= 128 && a.M * a.group > 32) return launch_tc(a, scratch, s);
+    if (a.D <= 128 && a.M * a.group <= 32) {
+        const int rows = a.M * a.group;
+        return launch_tiles(a, rows <= 16 ? 16 : 32, scratch, s, [&](int cluster) { return attn_few_resident(rows, cluster); },
+                            [&](const AttnArgs& b, dim3 grid) { return launch_attn_few(b, grid, s); });
+    }
+    if (a.D <= 128)
+        return launch_tiles(a, 128, scratch, s, [&](int cluster) { return attn_tc_resident(a.D, cluster); },
+                            [&](const AttnArgs& b, dim3 grid) { return launch_attn_tc(b, grid, s); });
     const int rows = a.M * a.group, rt = attn_mma_row_tiles(a.D, rows);
     const int blocks = (rows + 16 * rt - 1) / (16 * rt), heads = a.G * blocks;
     const int tiles = std::max(1, (a.n_common + 63) / 64);

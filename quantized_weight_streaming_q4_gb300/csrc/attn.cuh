@@ -117,6 +117,9 @@ int attn_mma_resident(int D, int row_tiles);  // clusters of 8 blocks that run a
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int row_tiles, cudaStream_t s);
 // The segments' tensor maps, boxes of `tile` rows (attn_mma.cu).
 int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps);
+// attn_few.cu: up to 32 query rows a K/V head, planes as for attn_tc.cu
+int attn_few_resident(int rows, int cluster);
+int launch_attn_few(const AttnArgs& a, dim3 grid, cudaStream_t s);
 // attn_tc.cu: planes that attn_mma_supported() takes, head_dim <= 128
 int attn_tc_resident(int D, int cluster);
 int launch_attn_tc(const AttnArgs& a, dim3 grid, cudaStream_t s);
