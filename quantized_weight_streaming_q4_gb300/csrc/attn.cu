@@ -107,25 +107,82 @@ __global__ void __launch_bounds__(kGenWarps * 32) attn_generic_kernel(const __gr
     }
 }
 
-// Joins the chunks: out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c, times
-// sigmoid(gate).  One block per query vector; the parts in a fixed order.
-__global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnArgs a, int parts) {
+// Joins the parts: out = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c, times
+// sigmoid(gate).  One block per query vector; its threads are groups of
+// ceil(D / 4) that take every kGroups-th part, eight loads in flight each, and
+// are added in a fixed order.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid_constant__ AttnArgs a, int parts) {
+    __shared__ float4 so[kJoinThreads];
+    __shared__ float2 sl[kJoinThreads];
+    pdl_launch_dependents();
+    pdl_wait();
     const int64_t row = blockIdx.x, rows = static_cast<int64_t>(a.M) * a.H;
-    float m = kNegInf;
-    for (int c = 0; c < parts; ++c) m = fmaxf(m, a.part_ml[c * rows + row].x);
-    for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
-        float l = 0.f, o = 0.f;
-        for (int c = 0; c < parts; ++c) {
-            const float2 ml = a.part_ml[c * rows + row];
-            if (ml.x == kNegInf && ml.y == 0.f) continue;  // a chunk without rows
-            const float w = exp2f(ml.x - m);
-            l = fmaf(w, ml.y, l);
-            o = fmaf(w, a.part_o[(c * rows + row) * a.D + d], o);
-        }
-        o /= l;
-        if (a.gate) o /= 1.f + expf(-a.gate[row * a.D + d]);
-        a.out[row * a.D + d] = o;
+    const bool vec = a.D % 4 == 0;
+    const int per = vec ? a.D / 4 : a.D, groups = max(1, kJoinThreads / per);
+    const int group = threadIdx.x / per, e = threadIdx.x % per;
+    float m = kNegInf, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f), z = o;
+    const bool in = group < groups;
+    if (in && group == 0 && a.gate) {
+        if (vec) z = __ldcg(reinterpret_cast<const float4*>(a.gate + row * a.D) + e);
+        else z.x = __ldcg(a.gate + row * a.D + e);
     }
+    for (int c0 = group; in && c0 < parts; c0 += 8 * groups) {
+        float2 w[8];
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int c = c0 + k * groups;
+            w[k] = make_float2(kNegInf, 0.f);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < parts) {
+                w[k] = __ldcg(a.part_ml + c * rows + row);
+                const float* p = a.part_o + (c * rows + row) * a.D;
+                if (vec) v[k] = __ldcg(reinterpret_cast<const float4*>(p) + e);
+                else v[k].x = __ldcg(p + e);
+            }
+        }
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mn = fmaxf(mn, w[k].x);
+        const float f0 = m == kNegInf ? 0.f : exp2f(m - mn);
+        m = mn;
+        l *= f0;
+        o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (w[k].x == kNegInf && w[k].y == 0.f) continue;  // a part without rows
+            const float f = exp2f(w[k].x - m);
+            l = fmaf(f, w[k].y, l);
+            o = make_float4(fmaf(f, v[k].x, o.x), fmaf(f, v[k].y, o.y), fmaf(f, v[k].z, o.z), fmaf(f, v[k].w, o.w));
+        }
+    }
+    so[threadIdx.x] = o;
+    sl[threadIdx.x] = make_float2(m, l);
+    __syncthreads();
+    if (!in || group != 0) return;
+    for (int k = 0; k < groups; ++k) m = fmaxf(m, sl[k * per + e].x);
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < groups; ++k) {
+        const float2 w = sl[k * per + e];
+        if (w.x == kNegInf && w.y == 0.f) continue;
+        const float4 v = so[k * per + e];
+        const float f = exp2f(w.x - m);
+        l = fmaf(f, w.y, l);
+        o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
+    }
+    const float inv = 1.f / l;
+    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (a.gate) {
+        o.x /= 1.f + expf(-z.x);
+        o.y /= 1.f + expf(-z.y);
+        o.z /= 1.f + expf(-z.z);
+        o.w /= 1.f + expf(-z.w);
+    }
+    if (vec) reinterpret_cast<float4*>(a.out + row * a.D)[e] = o;
+    else a.out[row * a.D + e] = o.x;
 }
 
 // Chunks of the common rows: about two blocks per SM, at least 64 rows each.
@@ -156,7 +213,17 @@ void place_parts(AttnArgs& a, int parts, void* scratch) {
 }
 
 int launch_combine(const AttnArgs& a, int parts, cudaStream_t s) {
-    attn_combine_kernel<<<a.M * a.H, 128, 0, s>>>(a, parts);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.M * a.H));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_combine_kernel, a, parts);
+    if (e != cudaSuccess) return cuda_fail(e, "attention combine: cudaLaunchKernelEx");
     return check_launch("attention combine");
 }
 
@@ -214,7 +281,7 @@ int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
     if (a.D <= 128)
         return launch_tiles(a, 128, scratch, s, [&](int cluster) { return attn_tc_resident(a.D, cluster); },
                             [&](const AttnArgs& b, dim3 grid) { return launch_attn_tc(b, grid, s); });
-    const int rows = a.M * a.group, rt = attn_mma_row_tiles(a.D, rows);
+    const int rows = a.M * a.group, rt = attn_mma_row_tiles(rows);
     const int blocks = (rows + 16 * rt - 1) / (16 * rt), heads = a.G * blocks;
     const int tiles = std::max(1, (a.n_common + 63) / 64);
     // up to 16 chunks of at least 128 keys: one cluster and no second kernel;
@@ -224,7 +291,7 @@ int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
     a.cluster = 1;
     while (a.cluster < one) a.cluster *= 2;
     if (tiles > 64) {
-        const int most = attn_mma_resident(a.D, rt) / heads;
+        const int most = attn_mma_resident(rt) / heads;
         if (most > 2) {
             a.cluster = 8;
             chunks = std::min({8 * most, tiles / 2, static_cast<int>(8 * max_parts(a.G, rows))});

@@ -112,8 +112,8 @@ struct AttnWalk {
 
 // attn_mma.cu
 bool attn_mma_supported(const AttnArgs& a);
-int attn_mma_row_tiles(int D, int rows);   // 16-row tiles of a block
-int attn_mma_resident(int D, int row_tiles);  // clusters of 8 blocks that run at once (0: unknown)
+int attn_mma_row_tiles(int rows);      // 16-row tiles of a block
+int attn_mma_resident(int row_tiles);  // clusters of 8 blocks that run at once (0: unknown)
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int row_tiles, cudaStream_t s);
 // The segments' tensor maps, boxes of `tile` rows (attn_mma.cu).
 int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps);

@@ -50,7 +50,8 @@ struct Layout {
     static constexpr uint32_t kQOff = kPOff + 2 * kPBytes;  // [d / 64][2 R][128 bytes]
     static constexpr uint32_t kScaleOff = kQOff + 2 * kN * 128;      // float[R]
     static constexpr uint32_t kRedOff = kScaleOff + R * 4;           // float[kGroups][4][16]
-    static constexpr uint32_t kMlOff = kRedOff + kGroups * 256;      // float2[R]
+    static constexpr uint32_t kMaxOff = kRedOff + kGroups * 256;     // float[R]: the rows' references
+    static constexpr uint32_t kMlOff = kMaxOff + R * 4;              // float2[R]
     static constexpr uint32_t kBarOff = kMlOff + R * 8;
     static constexpr uint32_t kBytes = kBarOff + 256;
     static constexpr uint32_t kOutStride = 132;             // floats; the output takes P's and q's place
@@ -103,12 +104,38 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
     float* cs = reinterpret_cast<float*>(smem + L::kScaleOff);
     const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * R;
     const int rows = a.M * a.group;
-    // tile 0 of the last chunk holds the ragged rows; the common ones follow
+    // One tile of the last chunk holds the ragged rows: the last one, where every
+    // tile has a stage of its own (a reference taken from the few ragged keys
+    // alone would soon have to move), else tile 0.
     AttnWalk walk(a, c);
-    const int ragged = c == a.nchunks - 1 ? 1 : 0, nragged = a.n_edge + a.M;
-    const int ntiles = ragged + walk.count(a, kTile);
-    auto next_tile = [&](int t, int& s, int& row) { return t < ragged ? nragged : walk.next(a, kTile, s, row); };
+    const bool ragged = c == a.nchunks - 1;
+    const int nragged = a.n_edge + a.M, ntiles = (ragged ? 1 : 0) + walk.count(a, kTile);
+    const int rt = !ragged ? -1 : ntiles <= kNS ? ntiles - 1 : 0;
+    auto next_tile = [&](int t, int& s, int& row) { return t == rt ? nragged : walk.next(a, kTile, s, row); };
 
+    // q and the ragged rows: the loads of the softmax warpgroups go out first.
+    // Thread (row, 16 elements); row r of the block: tree row i, head j of the group
+    pdl_launch_dependents();
+    const int w = (warp - 4) >> 2, th = tid & 127, id = 1 + w;  // 16 rows from 16 w on; key, later element
+    const int qr = th >> 3, d0 = (th & 7) * 16;
+    float4 x4[4];
+    uint4 y[8];
+    if (warp >= 4) {
+        pdl_wait();  // no global access before this
+        const int r = r0 + w * 16 + qr, i = r / a.group;
+        const float* src = a.q + (static_cast<int64_t>(i) * a.H + g * a.group + r - i * a.group) * a.D + d0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            x4[u] = r < rows && d0 + 4 * u < a.D ? __ldcg(reinterpret_cast<const float4*>(src) + u) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ragged && w == 0) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int rr = (u & 3) * 8 + (th >> 4), p = th & 15;
+                y[u] = make_uint4(0, 0, 0, 0);
+                if (rr < nragged && p * 8 < a.D) y[u] = attn_ragged8(a, g, rr, p * 8, u >= 4);
+            }
+        }
+    }
     if (tid == 0) {
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bar[kKFull + i], 1);
@@ -128,6 +155,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tmem_slot, L::kTmemCols);
+    if (warp < 4) pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -202,7 +230,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
                 const int st = t % kNS;
                 int sg, row;
                 next_tile(t, sg, row);
-                if (t < ragged) {  // a softmax warpgroup stores this one
+                if (t == rt) {  // a softmax warpgroup stores this one
                     wait(kRagged, 0);
                     if (!ok) break;
                     mbar_arrive(&bar[full + st]);
@@ -215,40 +243,24 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
                 mbar_arrive_expect_tx(&bar[full + st], boxes * kHalf);
                 for (uint32_t x = 0; x < boxes; ++x) tma_load_box(dst + x * kHalf, map, static_cast<int>(x), row, g, &bar[full + st]);
             }
-            for (int u = max(ragged, t - kNS); u < t && !ok; ++u)  // copies under way still write into this block's memory
-                mbar_wait_bounded(&bar[full + u % kNS], static_cast<uint32_t>(u / kNS) & 1u, a.status, kDevStatusTxTimeout);
+            for (int u = max(0, t - kNS); u < t && !ok; ++u)  // copies under way still write into this block's memory
+                if (u != rt) mbar_wait_bounded(&bar[full + u % kNS], static_cast<uint32_t>(u / kNS) & 1u, a.status, kDevStatusTxTimeout);
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+        prefetch_gate<R, 32>(a, lane, g, r0, rows);
+    } else {
         // --------------------------------------- softmax and accumulation
-        const int w = (warp - 4) >> 2, th = tid & 127, id = 1 + w;  // 16 rows from 16 w on; key, later element
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + w * 16;
-        // q: thread (row, 16 elements); rows of the block: tree row i, head j of the group
         {
-            const int qr = th >> 3, d0 = (th & 7) * 16, r = r0 + w * 16 + qr, i = r / a.group;
-            const float* src = a.q + (static_cast<int64_t>(i) * a.H + g * a.group + r - i * a.group) * a.D + d0;
-            float4 x[4];
             float mx = 0.f;
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                x[u] = r < rows && d0 + 4 * u < a.D ? __ldcg(reinterpret_cast<const float4*>(src) + u) : make_float4(0.f, 0.f, 0.f, 0.f);
-            // the ragged rows' loads follow q's
-            uint4 y[8];
-            if (ragged && w == 0) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int rr = (u & 3) * 8 + (th >> 4), p = th & 15;
-                    y[u] = make_uint4(0, 0, 0, 0);
-                    if (rr < nragged && p * 8 < a.D) y[u] = attn_ragged8(a, g, rr, p * 8, u >= 4);
-                }
-            }
-#pragma unroll
             for (int u = 0; u < 4; ++u) {
-                x[u].x *= a.scale_log2;
-                x[u].y *= a.scale_log2;
-                x[u].z *= a.scale_log2;
-                x[u].w *= a.scale_log2;
-                mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x[u].x), fabsf(x[u].y))), fmaxf(fabsf(x[u].z), fabsf(x[u].w)));
+                x4[u].x *= a.scale_log2;
+                x4[u].y *= a.scale_log2;
+                x4[u].z *= a.scale_log2;
+                x4[u].w *= a.scale_log2;
+                mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x4[u].x), fabsf(x4[u].y))), fmaxf(fabsf(x4[u].z), fabsf(x4[u].w)));
             }
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -258,10 +270,10 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 uint4 hi, lo;
-                split2(x[2 * u].x * up, x[2 * u].y * up, hi.x, lo.x);
-                split2(x[2 * u].z * up, x[2 * u].w * up, hi.y, lo.y);
-                split2(x[2 * u + 1].x * up, x[2 * u + 1].y * up, hi.z, lo.z);
-                split2(x[2 * u + 1].z * up, x[2 * u + 1].w * up, hi.w, lo.w);
+                split2(x4[2 * u].x * up, x4[2 * u].y * up, hi.x, lo.x);
+                split2(x4[2 * u].z * up, x4[2 * u].w * up, hi.y, lo.y);
+                split2(x4[2 * u + 1].x * up, x4[2 * u + 1].y * up, hi.z, lo.z);
+                split2(x4[2 * u + 1].z * up, x4[2 * u + 1].w * up, hi.w, lo.w);
                 const int p = (d0 >> 3) + u;
                 sts_uint4(smem + L::kQOff + piece<L::kN>(w * 16 + qr, p), hi);
                 sts_uint4(smem + L::kQOff + piece<L::kN>(R + w * 16 + qr, p), lo);
@@ -272,7 +284,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             }
             fence_proxy_async_smem();
             mbar_arrive(&bar[kQReady]);
-            if (ragged && w == 0) {  // stored as tile 0; a value that is not finite becomes 0 and is noted
+            if (ragged && w == 0) {  // stored as tile rt; a value that is not finite becomes 0 and is noted
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const int rr = (u & 3) * 8 + (th >> 4), p = th & 15;
@@ -280,7 +292,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
                         atomicOr(flags, 1u << rr);
                         y[u] = make_uint4(0, 0, 0, 0);
                     }
-                    if (p < 8 || a.D > 64) sts_uint4(smem + (u >= 4 ? L::kVOff : 0u) + piece<kTile>(rr, p), y[u]);
+                    if (p < 8 || a.D > 64) sts_uint4(smem + (u >= 4 ? L::kVOff : 0u) + rt % kNS * kItem + piece<kTile>(rr, p), y[u]);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bar[kRagged]);
@@ -312,7 +324,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             int sg, srow;
             const int real = next_tile(t, sg, srow);
             uint32_t see = th < real ? 0xffffu : 0u;  // bit j: row j sees this thread's key
-            if (t < ragged) {
+            if (t == rt) {
                 see = 0;
                 int i = (r0 + w * 16) / a.group, k = r0 + w * 16 - i * a.group;
 #pragma unroll
@@ -368,6 +380,10 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
                     o[j] *= f;
                     x[j] = s[j] == kNegInf ? kNegInf : s[j] + b[j];
                 }
+                if (th == 0) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + j] = m[j];
+                }
                 named_barrier_sync(id, 128);  // red is free again
             }
             // p, its parts to P [keys][2 R]
@@ -397,13 +413,11 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         if ((lane & 1) == 0) red[(warp & 3) * 16 + (lane >> 1)] = l[0];
         named_barrier_sync(1 + L::kGroups, 128 * L::kGroups);  // every group's last product is done: P and q are free
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            out[(w * 16 + j) * L::kOutStride + th] = o[j];
-            if (th == j) {
-                float sum = (red[j] + red[16 + j]) + (red[32 + j] + red[48 + j]);
-                if ((spoiled >> j) & 1u) sum = NAN;
-                ml[w * 16 + j] = make_float2(m[j], sum);
-            }
+        for (int j = 0; j < 16; ++j) out[(w * 16 + j) * L::kOutStride + th] = o[j];
+        if (th < 16) {
+            float sum = (red[th] + red[16 + th]) + (red[32 + th] + red[48 + th]);
+            if ((spoiled >> th) & 1u) sum = NAN;
+            ml[w * 16 + th] = make_float2(ntiles > 0 ? reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + th] : kNegInf, sum);
         }
     }
     tc_fence_before();
@@ -413,7 +427,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         tmem_free(tmem, L::kTmemCols);
     }
     if (a.cluster > 1) cluster_sync();
-    if (ok) join_cluster<128, L::kOutStride, R, L::kThreads>(a, tid, c, g, r0, rows, base + L::kMlOff, base + L::kPOff);
+    if (ok) join_cluster<128, L::kOutStride, R, L::kThreads, 8>(a, tid, c, g, r0, rows, base + L::kMlOff, base + L::kPOff);
     if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
 }
 
@@ -434,7 +448,7 @@ int prepare() {
 template <int R>
 int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
     MUSER_TRY(prepare<R>());
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, Layout<R>::kThreads, Layout<R>::kBytes, s, attr);
     AttnMaps maps;
     MUSER_TRY(encode_attn_maps(a, kTile, maps));
@@ -451,7 +465,7 @@ int resident(int cluster) {
     if (prepare<R>() != MUSER_OK || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
     int n = known[dev][k].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(cluster, dim3(cluster), Layout<R>::kThreads, Layout<R>::kBytes, nullptr, attr);
     if (cudaOccupancyMaxActiveClusters(&n, attn_few_kernel<R>, &cfg) != cudaSuccess) {
         cudaGetLastError();

@@ -1,12 +1,11 @@
 // attn_mma.cu -- tree attention on warp-level matrix products (mma.sync), for
-// head sizes that are multiples of 8 up to 256 and 16-byte aligned planes.
+// head sizes above 128 (multiples of 8, up to 256) and 16-byte aligned planes.
 //
 // A block takes one K/V head, 16 * RT of the group's M * group query vectors
 // and one chunk of the cached rows; its four warps are RT row tiles times
-// 4 / RT shares of every stage's keys.  K and V tiles come by TMA, kStages
+// 4 / RT shares of every stage's keys.  K and V tiles come by TMA, two stages
 // deep, in its 128-byte swizzle, so the fragment loads of eight rows hit eight
-// different bank groups.  (16-byte asynchronous copies of the same tiles
-// stopped at about 13 bytes a clock and SM: 4,160 GB/s over 130,815 rows.)
+// different bank groups.
 //
 // Precision: the planes are binary16, q is binary32 and so is the result.  A
 // query vector is scaled by a power of two and split into two binary16 parts
@@ -17,12 +16,16 @@
 // The blocks of a cluster hold neighbouring chunks of the same rows and join
 // their (maximum, sum, output) triples through distributed shared memory; with
 // one cluster per row block the result is final and there is no second kernel.
+//
+// Bound: mma.sync itself, about 16 cycles a 16 x 8 x 16 product and scheduler,
+// an eighth of tcgen05's rate: heads up to 128 take attn_few.cu or attn_tc.cu.
+// A head of 256 has 128 binary32 outputs a thread, which is why the q parts
+// are read from shared memory for every key tile.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
 #include <mutex>
-#include <type_traits>
 
 #include "attn.cuh"
 #include "attn_parts.cuh"
@@ -34,21 +37,19 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTileKeys = 64;
 
-template <int DP>
-constexpr int kStages = DP == 64 ? 4 : DP == 128 ? 3 : 2;
-template <int DP>
+constexpr int DP = 256, kStages = 2;
 constexpr int kTileBytes = kTileKeys * DP * 2;  // of K or of V
-template <int DP, int RT>
+template <int RT>
 struct Layout {
     static constexpr int R = 16 * RT, KW = kWarps / RT;
     static constexpr int kOutStride = DP + 8;  // floats; rows 32 bytes apart in the banks
-    static constexpr int kOutOff = kStages<DP> * 2 * kTileBytes<DP>;            // q parts, then the block's output
+    static constexpr int kOutOff = kStages * 2 * kTileBytes;            // q parts, then the block's output
     static constexpr int kMlOff = kOutOff + R * kOutStride * 4;                 // float2[R]: the block's maximum and sum
     static constexpr int kMlwOff = kMlOff + R * 8;                              // float2[KW][R]
     static constexpr int kScaleOff = kMlwOff + KW * R * 8;                      // float[R]
     static constexpr int kFlagOff = kScaleOff + R * 4;                          // uint32: ragged rows that are not finite
     static constexpr int kBarOff = kFlagOff + 16;                               // uint64[kStages]: a stage has landed
-    static constexpr int kBytes = kBarOff + 8 * kStages<DP>;
+    static constexpr int kBytes = kBarOff + 8 * kStages;
     static_assert(R * kOutStride * 4 >= 2 * R * DP * 2, "the q parts fit under the output");
     static_assert(KW == 1 || KW * R * kOutStride * 4 <= kOutOff, "the warps' outputs fit under the stages");
 };
@@ -71,11 +72,10 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-template <int DP, int RT>
+template <int RT>
 __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps) {
-    using L = Layout<DP, RT>;
-    constexpr int R = L::R, KW = L::KW, NS = kStages<DP>;
-    constexpr bool kQReg = DP <= 128;  // the q parts stay in registers
+    using L = Layout<RT>;
+    constexpr int R = L::R, KW = L::KW, NS = kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -92,18 +92,22 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
     auto load_tile = [&](int t) {
         int s, row;
         load.next(a, kTileKeys, s, row);
-        const uint32_t buf = base + (t % NS) * 2 * kTileBytes<DP>;
-        mbar_arrive_expect_tx(&bar[t % NS], 2 * kTileBytes<DP>);
+        const uint32_t buf = base + (t % NS) * 2 * kTileBytes;
+        mbar_arrive_expect_tx(&bar[t % NS], 2 * kTileBytes);
 #pragma unroll
         for (int x = 0; x < DP / 64; ++x) {
             tma_load_box(buf + x * kTileKeys * 128, &maps.k[s], x, row, g, &bar[t % NS]);
-            tma_load_box(buf + kTileBytes<DP> + x * kTileKeys * 128, &maps.v[s], x, row, g, &bar[t % NS]);
+            tma_load_box(buf + kTileBytes + x * kTileKeys * 128, &maps.v[s], x, row, g, &bar[t % NS]);
         }
     };
+    pdl_launch_dependents();
     if (tid == 0) {
         *flags = 0;
         for (int i = 0; i < NS; ++i) mbar_init(&bar[i], 1);
         fence_mbar_init();
+    }
+    pdl_wait();  // no global access before this
+    if (tid == 0) {
         // the last stage is left to the ragged rows
         for (int t = 0; t < NS - 1 && t < ntiles; ++t) load_tile(t);
     }
@@ -124,9 +128,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
         }
     }
 
+    prefetch_gate<R, kThreads>(a, tid, g, r0, rows);
     // q: scaled to base 2 and to [2^7, 2^8), split, into shared memory; a
     // warp's rows in batches whose loads are in flight together
-    constexpr int kQRows = R / kWarps, kQBatch = kQRows < 8 ? kQRows : (DP > 128 ? 4 : 8), kQV = (DP + 127) / 128;
+    constexpr int kQRows = R / kWarps, kQBatch = 4, kQV = DP / 128;
 #pragma unroll
     for (int b = 0; b < kQRows; b += kQBatch) {
         float4 x[kQBatch][kQV];
@@ -174,15 +179,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
     __syncthreads();
 
     const int gr = lane >> 2, qt = lane & 3;  // fragment row and column pair
-    uint32_t qh[kQReg ? DP / 16 : 1][4], ql[kQReg ? DP / 16 : 1][4];
     auto q_addr = [&](int ks) { return base + L::kOutOff + piece<R>(rt * 16 + (lane & 15), ks * 2 + (lane >> 4)); };
-    if constexpr (kQReg) {
-#pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks) {
-            ldsm4(qh[ks], q_addr(ks));
-            ldsm4(ql[ks], q_addr(ks) + R * DP * 2);
-        }
-    }
     const float c0 = cs[rt * 16 + gr], c1 = cs[rt * 16 + gr + 8];
     float m0 = kNegInf, m1 = kNegInf, l0 = 0.f, l1 = 0.f;
     float o[DP / 8][4];
@@ -203,20 +200,13 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
         for (int ks = 0; ks < DP / 16; ++ks) {
             uint32_t kf[4];  // keys 0-7: d 0-7, 8-15; keys 8-15: the same
             ldsm4(kf, kbuf + piece<kTileKeys>(k0 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)));
-            if constexpr (kQReg) {
-                mma16816(sl[0], ql[ks], kf[0], kf[1]);
-                mma16816(sl[1], ql[ks], kf[2], kf[3]);
-                mma16816(sh[0], qh[ks], kf[0], kf[1]);
-                mma16816(sh[1], qh[ks], kf[2], kf[3]);
-            } else {
-                uint32_t f[4];
-                ldsm4(f, q_addr(ks) + R * DP * 2);
-                mma16816(sl[0], f, kf[0], kf[1]);
-                mma16816(sl[1], f, kf[2], kf[3]);
-                ldsm4(f, q_addr(ks));
-                mma16816(sh[0], f, kf[0], kf[1]);
-                mma16816(sh[1], f, kf[2], kf[3]);
-            }
+            uint32_t f[4];
+            ldsm4(f, q_addr(ks) + R * DP * 2);
+            mma16816(sl[0], f, kf[0], kf[1]);
+            mma16816(sl[1], f, kf[2], kf[3]);
+            ldsm4(f, q_addr(ks));
+            mma16816(sh[0], f, kf[0], kf[1]);
+            mma16816(sh[1], f, kf[2], kf[3]);
         }
         float t0 = kNegInf, t1 = kNegInf;
 #pragma unroll
@@ -260,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
             split2(p0, p1, ph[2 * n], pl[2 * n]);
             split2(p2, p3, ph[2 * n + 1], pl[2 * n + 1]);
         }
-        const uint32_t vbuf = kbuf + kTileBytes<DP>;
+        const uint32_t vbuf = kbuf + kTileBytes;
 #pragma unroll
         for (int n = 0; n < DP / 16; ++n) {
             uint32_t vf[4];  // d 0-7: keys 0-7, 8-15; d 8-15: the same
@@ -277,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
     // that does not see it; those that do become NaN at the end.
     bool spoiled0 = false, spoiled1 = false;
     if (ragged) {
-        const uint32_t buf = (NS - 1) * 2 * kTileBytes<DP>;
+        const uint32_t buf = (NS - 1) * 2 * kTileBytes;
         uint32_t bad = 0;
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
@@ -288,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
             }
             const uint32_t at = buf + piece<kTileKeys>(r, x % kPieces);
             sts_uint4(smem + at, kp[j]);
-            sts_uint4(smem + at + kTileBytes<DP>, vp[j]);
+            sts_uint4(smem + at + kTileBytes, vp[j]);
         }
         if (bad) atomicOr(flags, bad);
         __syncthreads();
@@ -312,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
             fence_proxy_async_smem();
             load_tile(t + NS - 1);
         }
-        const uint32_t kbuf = base + (t % NS) * 2 * kTileBytes<DP>;
+        const uint32_t kbuf = base + (t % NS) * 2 * kTileBytes;
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
             const int k0 = (kw + j * KW) * 16;
@@ -375,68 +365,53 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
 
     if (a.cluster > 1) cluster_sync();
     else __syncthreads();
-    if (ok) join_cluster<DP, L::kOutStride, R, kThreads>(a, tid, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff);
+    if (ok) join_cluster<DP, L::kOutStride, R, kThreads, 1>(a, tid, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff);
     if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
 }
 
 // The kernel's attributes, set once per device.
-template <int DP, int RT>
+template <int RT>
 int prepare() {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "attention: cudaGetDevice");
     if (dev < 64 && ((done.load(std::memory_order_acquire) >> dev) & 1u)) return MUSER_OK;
-    e = cudaFuncSetAttribute(attn_mma_kernel<DP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP, RT>::kBytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_mma_kernel<DP, RT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(attn_mma_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<RT>::kBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_mma_kernel<RT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
     if (dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_release);
     return MUSER_OK;
 }
 
-template <int DP, int RT>
+template <int RT>
 int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
-    MUSER_TRY((prepare<DP, RT>()));
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, kThreads, Layout<DP, RT>::kBytes, s, attr);
+    MUSER_TRY((prepare<RT>()));
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, kThreads, Layout<RT>::kBytes, s, attr);
     AttnMaps maps;
     MUSER_TRY(encode_attn_maps(a, kTileKeys, maps));
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<DP, RT>, a, maps);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_mma_kernel<RT>, a, maps);
     if (e != cudaSuccess) return cuda_fail(e, "attention: cudaLaunchKernelEx");
     return check_launch("attention");
 }
 
 // Clusters of 8 blocks that the device holds at once.
-template <int DP, int RT>
+template <int RT>
 int resident() {
     static std::atomic<int> known[64];
     int dev = 0;
-    if (prepare<DP, RT>() != MUSER_OK || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+    if (prepare<RT>() != MUSER_OK || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
     int n = known[dev].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = cluster_config(8, dim3(8), kThreads, Layout<DP, RT>::kBytes, nullptr, attr);
-    if (cudaOccupancyMaxActiveClusters(&n, attn_mma_kernel<DP, RT>, &cfg) != cudaSuccess) {
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = cluster_config(8, dim3(8), kThreads, Layout<RT>::kBytes, nullptr, attr);
+    if (cudaOccupancyMaxActiveClusters(&n, attn_mma_kernel<RT>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
     known[dev].store(n, std::memory_order_relaxed);
     return n;
-}
-
-// The row tiles' and head sizes' instantiation.
-template <typename F>
-auto dispatch(int D, int rt, F&& f) {
-    using std::integral_constant;
-    auto rows = [&](auto dp) {
-        constexpr int DP = decltype(dp)::value;
-        if (rt == 1) return f(dp, integral_constant<int, 1>{});
-        if (DP > 128 || rt == 2) return f(dp, integral_constant<int, 2>{});
-        return f(dp, integral_constant<int, (DP > 128 ? 2 : 4)>{});
-    };
-    if (D <= 64) return rows(integral_constant<int, 64>{});
-    if (D <= 128) return rows(integral_constant<int, 128>{});
-    return rows(integral_constant<int, 256>{});
 }
 
 }  // namespace
@@ -454,11 +429,8 @@ bool attn_mma_supported(const AttnArgs& a) {
     return true;
 }
 
-int attn_mma_row_tiles(int D, int rows) { return rows <= 16 ? 1 : rows <= 32 || D > 128 ? 2 : 4; }
-
-int attn_mma_resident(int D, int rt) {
-    return dispatch(D, rt, [](auto dp, auto r) { return resident<decltype(dp)::value, decltype(r)::value>(); });
-}
+int attn_mma_row_tiles(int rows) { return rows <= 16 ? 1 : 2; }
+int attn_mma_resident(int rt) { return rt == 1 ? resident<1>() : resident<2>(); }
 
 int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps) {
     static std::once_flag once;
@@ -488,7 +460,7 @@ int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps) {
 }
 
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int rt, cudaStream_t s) {
-    return dispatch(a.D, rt, [&](auto dp, auto r) { return launch<decltype(dp)::value, decltype(r)::value>(a, grid, s); });
+    return rt == 1 ? launch<1>(a, grid, s) : launch<2>(a, grid, s);
 }
 
 }  // namespace muser

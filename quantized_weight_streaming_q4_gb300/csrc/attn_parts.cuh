@@ -98,43 +98,58 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
     return static_cast<uint32_t>((c >> 3) * ROWS * 128 + r * 128 + (((c ^ r) & 7) << 4));
 }
 
+// Brings the lines of the output gate that join_cluster will read into L2:
+// LANES threads, those of the block's R rows that fall to its rank.
+template <int R, int LANES>
+__device__ __forceinline__ void prefetch_gate(const AttnArgs& a, int lane, int g, int r0, int rows) {
+    if (a.gate == nullptr) return;
+    const int n = a.cluster, rank = n > 1 ? static_cast<int>(cluster_rank()) : 0, lines = (a.D * 4 + 127) / 128;
+    for (int x = lane + R * lines * rank / n; x < R * lines * (rank + 1) / n; x += LANES) {
+        const int r = r0 + x / lines, i = r / a.group;
+        if (r < rows) prefetch_l2(a.gate + (static_cast<int64_t>(i) * a.H + g * a.group + r - i * a.group) * a.D + x % lines * 32);
+    }
+}
+
 // The cluster's result: the blocks hold the same R query rows' (maximum, sum)
 // pairs at shared address mla and outputs at oa (row stride STRIDE floats);
 // each joins a share of the elements and writes them out, final or as a part.
-// Called by THREADS threads (tid counts them) between two cluster barriers.
-// The remote loads of all blocks go out together: one after another they took
-// 16 round trips, about 5 us in a cluster of 16.
-template <int DP, int STRIDE, int R, int THREADS>
+// Called by THREADS threads (tid counts them, whole warps) between two cluster
+// barriers.  An element's blocks are shared by SPLIT neighbouring lanes (or n,
+// if that is less), whose remote loads are all in flight together: one after
+// another they took 16 round trips, about 5 us in a cluster of 16.
+template <int DP, int STRIDE, int R, int THREADS, int SPLIT>
 __device__ __forceinline__ void join_cluster(const AttnArgs& a, int tid, int c, int g, int r0, int rows, uint32_t mla,
                                              uint32_t oa) {
-    const int n = a.cluster, rank = n > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int units = R * DP / 4, u0 = units * rank / n, u1 = units * (rank + 1) / n;
-    const int nclusters = gridDim.x / n;
-    for (int x = u0 + tid; x < u1; x += THREADS) {
-        const int r = x / (DP / 4), d = x % (DP / 4) * 4;
-        if (r0 + r >= rows || d >= a.D) continue;
+    constexpr int kEach = 16 / SPLIT < 8 ? 16 / SPLIT : 8;  // blocks of a lane loaded together
+    const int n = a.cluster, rank = n > 1 ? static_cast<int>(cluster_rank()) : 0, split = min(n, SPLIT);
+    const int units = R * DP / 4, u0 = units * rank / n, items = (units * (rank + 1) / n - u0) * split;
+    const bool final = gridDim.x == static_cast<unsigned>(n);
+    for (int item = tid; item < (items + 31) / 32 * 32; item += THREADS) {
+        const int x = u0 + item / split, sub = item % split, r = x / (DP / 4), d = x % (DP / 4) * 4;
+        const bool real = item < items && r0 + r < rows && d < a.D;
         const int i = (r0 + r) / a.group;
         const int64_t row = static_cast<int64_t>(i) * a.H + g * a.group + (r0 + r) - i * a.group;
         const uint32_t ma = mla + r * 8, va = oa + (r * STRIDE + d) * 4;
-        const bool final = nclusters == 1;
         float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (final && a.gate) z = __ldcg(reinterpret_cast<const float4*>(a.gate + row * a.D + d));
+        if (real && final && a.gate) z = __ldcg(reinterpret_cast<const float4*>(a.gate + row * a.D + d));
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         float l = 0.f, M = kNegInf;
-        for (int b0 = 0; b0 < n; b0 += 8) {  // eight blocks' at a time, the running maximum carried
-            float2 w[8];
-            float4 v[8];
+        for (int b0 = sub; b0 < n; b0 += kEach * split) {
+            float2 w[kEach];
+            float4 v[kEach];
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                w[b] = make_float2(kNegInf, 0.f);
-                if (b0 + b < n) {
-                    w[b] = ld_cluster2(map_rank(ma, b0 + b));
-                    v[b] = ld_cluster4(map_rank(va, b0 + b));
+            for (int k = 0; k < kEach; ++k) {
+                const int b = b0 + k * split;
+                w[k] = make_float2(kNegInf, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (real && b < n) {
+                    w[k] = ld_cluster2(n > 1 ? map_rank(ma, b) : ma);
+                    v[k] = ld_cluster4(n > 1 ? map_rank(va, b) : va);
                 }
             }
             float mn = M;
 #pragma unroll
-            for (int b = 0; b < 8; ++b) mn = fmaxf(mn, w[b].x);
+            for (int k = 0; k < kEach; ++k) mn = fmaxf(mn, w[k].x);
             const float f0 = share(M, mn);
             M = mn;
             l *= f0;
@@ -143,17 +158,27 @@ __device__ __forceinline__ void join_cluster(const AttnArgs& a, int tid, int c, 
             s.z *= f0;
             s.w *= f0;
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                if (b0 + b < n) {
-                    const float f = share(w[b].x, M);
-                    l = fmaf(f, w[b].y, l);
-                    s.x = fmaf(f, v[b].x, s.x);
-                    s.y = fmaf(f, v[b].y, s.y);
-                    s.z = fmaf(f, v[b].z, s.z);
-                    s.w = fmaf(f, v[b].w, s.w);
-                }
+            for (int k = 0; k < kEach; ++k) {
+                const float f = share(w[k].x, M);
+                if (w[k].x == kNegInf && w[k].y == 0.f) continue;  // no rows there
+                l = fmaf(f, w[k].y, l);
+                s.x = fmaf(f, v[k].x, s.x);
+                s.y = fmaf(f, v[k].y, s.y);
+                s.z = fmaf(f, v[k].z, s.z);
+                s.w = fmaf(f, v[k].w, s.w);
             }
         }
+        for (int o = 1; o < split; o <<= 1) {
+            const float mo = __shfl_xor_sync(0xffffffffu, M, o), mn = fmaxf(M, mo);
+            const float f = share(M, mn), fo = share(mo, mn);
+            M = mn;
+            l = fmaf(f, l, fo * __shfl_xor_sync(0xffffffffu, l, o));
+            s.x = fmaf(f, s.x, fo * __shfl_xor_sync(0xffffffffu, s.x, o));
+            s.y = fmaf(f, s.y, fo * __shfl_xor_sync(0xffffffffu, s.y, o));
+            s.z = fmaf(f, s.z, fo * __shfl_xor_sync(0xffffffffu, s.z, o));
+            s.w = fmaf(f, s.w, fo * __shfl_xor_sync(0xffffffffu, s.w, o));
+        }
+        if (!real || sub != 0) continue;
         if (final) {
             const float inv = 1.f / l;
             float4 y = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
@@ -172,6 +197,9 @@ __device__ __forceinline__ void join_cluster(const AttnArgs& a, int tid, int c, 
     }
 }
 
+// Launch attributes: the cluster, and programmatic stream serialization (the
+// blocks start while the kernel before them on the stream still runs and wait
+// for it before their first global access).
 inline cudaLaunchConfig_t cluster_config(int cluster, dim3 grid, int threads, size_t smem, cudaStream_t s,
                                          cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg{};
@@ -183,8 +211,10 @@ inline cudaLaunchConfig_t cluster_config(int cluster, dim3 grid, int threads, si
     attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cfg;
 }
 

@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const int ntiles = ragged + walk.count(a, kTile);
     auto next_tile = [&](int t, int& s, int& row) { return t < ragged ? nragged : walk.next(a, kTile, s, row); };
 
+    pdl_launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[kKFull + i], 1);
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (warp == 0) {
         tmem_alloc(tmem_slot, kTmemCols);
     }
+    pdl_wait();  // no global access before this
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -157,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
         } else {
             // ------------------------------------------------- K, V loads
+            if (warp == 3) prefetch_gate<128, 32>(a, lane, g, r0, rows);
             if (warp < 3 && lane == 0) {
                 const int v = warp - 1, full = v ? kVFull : kKFull, empty = v ? kVEmpty : kSFull;
                 int t = 0;
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         tc_fence_before();
         ok = __syncthreads_and(ok);
         if (a.cluster > 1) cluster_sync();
-        if (ok) join_cluster<DP, L::kOutStride, 128, 256>(a, tid - 128, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff);
+        if (ok) join_cluster<DP, L::kOutStride, 128, 256, 1>(a, tid - 128, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff);
         if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
     }
 }
@@ -396,7 +399,7 @@ int prepare() {
 template <int DP>
 int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
     MUSER_TRY(prepare<DP>());
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, kThreads, Layout<DP>::kBytes, s, attr);
     AttnMaps maps;
     MUSER_TRY(encode_attn_maps(a, kTile, maps));
@@ -413,7 +416,7 @@ int resident(int cluster) {
     if (prepare<DP>() != MUSER_OK || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
     int n = known[dev][k].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(cluster, dim3(cluster), kThreads, Layout<DP>::kBytes, nullptr, attr);
     if (cudaOccupancyMaxActiveClusters(&n, attn_tc_kernel<DP>, &cfg) != cudaSuccess) {
         cudaGetLastError();
