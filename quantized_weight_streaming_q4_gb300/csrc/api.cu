@@ -1225,6 +1225,13 @@ int muser_kv_tree_attention(const muser_kv_plane* plane, const muser_kv_plane* s
             return set_error(MUSER_ERR_INVALID_ARG, "%s: out and scratch must not overlap q, k, v or gate", fn);
     if (ranges_overlap(out, nq, scratch, scratch_bytes))
         return set_error(MUSER_ERR_INVALID_ARG, "%s: out and scratch must not overlap", fn);
+    for (const muser_kv_plane* p : {plane, sink}) {
+        if (!p) continue;
+        const size_t np = static_cast<size_t>(p->capacity) * static_cast<size_t>(p->kv_dim) * 2u;
+        for (const void* b : {static_cast<const void*>(p->key), static_cast<const void*>(p->value)})
+            if (ranges_overlap(out, nq, b, np) || ranges_overlap(scratch, scratch_bytes, b, np))
+                return set_error(MUSER_ERR_INVALID_ARG, "%s: out and scratch must not overlap the planes", fn);
+    }
 
     AttnArgs a{};
     a.q = q;

@@ -243,23 +243,49 @@ int launch_generic(AttnArgs a, void* scratch, cudaStream_t s) {
     return launch_combine(a, a.nchunks, s);
 }
 
-// The tensor-core kernels, one block per SM: tiles of 128 keys, blocks of R
-// query rows.
-template <typename Resident, typename Launch>
-int launch_tiles(AttnArgs a, int R, void* scratch, cudaStream_t s, Resident&& resident, Launch&& launch) {
-    const int rows = a.M * a.group, blocks = (rows + R - 1) / R, heads = a.G * blocks;
-    // up to 16 chunks of 128 keys: one cluster and no second kernel
-    int chunks = std::min(16, std::max(1, (a.n_common + 127) / 128));
-    a.cluster = 1;
-    while (a.cluster < chunks) a.cluster *= 2;
-    if (a.n_common > 16 * 256) {  // one block per SM, in small clusters
-        const int most = resident(4) / heads;
-        if (most > 4) {
-            a.cluster = 4;
-            chunks = std::min(4 * most, static_cast<int>(4 * max_parts(a.G, rows)));
+// The split of the common rows for the tensor-core kernels (tiles of 128 keys,
+// one block per SM, `heads` K/V heads times row blocks): clusters of c blocks,
+// k of them a head.  One cluster joins its blocks' results itself; more leave
+// parts for a second kernel (2.7 us).  A tile takes a block `tile_us`, or
+// `tile_full_us` where all SMs share the memory's rate, and 5 us beside its
+// tiles; clusters beyond those that run at once wait for a turn (of 16 blocks
+// 7 clusters are resident).  Measured, one token, 16 K/V heads of 64, 2,048
+// rows: clusters of 16 in three turns 23.9 us, of 4 at once 11.2 us; 2 heads of
+// 128: one cluster of 16 a head 8.4 us (11.0 with parts), and over 32,768 rows
+// 21.4 us (14.0 with parts).
+struct Split {
+    int cluster, chunks;
+};
+Split choose_split(int heads, int tiles, int parts, double tile_us, double tile_full_us, const AttnResident& resident) {
+    Split best{1, 1};
+    double least = 1e30;
+    for (int c = 16, e = 4; e >= 0; c /= 2, --e) {
+        const int most = resident.clusters[e];
+        if (most < 1 || (c > 1 && c / 2 >= tiles)) continue;
+        for (const int k : {1, std::min(parts, most / heads)}) {
+            if (k < 1) continue;
+            const int chunks = std::min(c * k, std::max(1, tiles)), clusters = (chunks + c - 1) / c;
+            const int waves = (heads * clusters + most - 1) / most, per = (std::max(1, tiles) + chunks - 1) / chunks;
+            const double busy = std::min(1.0, heads * chunks / 144.0);
+            const double us = waves * (5.0 + per * std::max(tile_us, tile_full_us * busy)) + (clusters > 1 ? 2.7 : 0.0);
+            if (us < least - 1e-9) {
+                least = us;
+                best = Split{c, chunks};
+            }
         }
     }
-    a.chunk = std::max(16, ((a.n_common + chunks - 1) / chunks + 15) / 16 * 16);
+    return best;
+}
+
+template <typename Launch>
+int launch_tiles(AttnArgs a, int R, double tile_us, double tile_full_us, void* scratch, cudaStream_t s,
+                 const AttnResident* resident, Launch&& launch) {
+    if (resident == nullptr) return MUSER_ERR_CUDA;  // the message is set
+    const int rows = a.M * a.group, blocks = (rows + R - 1) / R;
+    const Split split = choose_split(a.G * blocks, (a.n_common + 127) / 128, static_cast<int>(max_parts(a.G, rows)), tile_us,
+                                     tile_full_us, *resident);
+    a.cluster = split.cluster;
+    a.chunk = std::max(16, ((a.n_common + split.chunks - 1) / split.chunks + 15) / 16 * 16);
     a.nchunks = std::max(1, (a.n_common + a.chunk - 1) / a.chunk);
     const int clusters = (a.nchunks + a.cluster - 1) / a.cluster;
     place_parts(a, clusters, scratch);
@@ -275,12 +301,11 @@ int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
     if (!a.status) return set_error(MUSER_ERR_CUDA, "attention: no device status word");
     if (a.D <= 128 && a.M * a.group <= 32) {
         const int rows = a.M * a.group;
-        return launch_tiles(a, rows <= 16 ? 16 : 32, scratch, s, [&](int cluster) { return attn_few_resident(rows, cluster); },
-                            [&](const AttnArgs& b, dim3 grid) { return launch_attn_few(b, grid, s); });
+        return launch_tiles(a, rows <= 16 ? 16 : 32, 0.85, a.D <= 64 ? 0.85 : 1.4, scratch, s,
+                            attn_few_resident(rows), [&](const AttnArgs& b, dim3 grid) { return launch_attn_few(b, grid, s); });
     }
     if (a.D <= 128)
-        return launch_tiles(a, 128, scratch, s, [&](int cluster) { return attn_tc_resident(a.D, cluster); },
-                            [&](const AttnArgs& b, dim3 grid) { return launch_attn_tc(b, grid, s); });
+        return launch_tiles(a, 128, 1.6, 1.6, scratch, s, attn_tc_resident(a.D), [&](const AttnArgs& b, dim3 grid) { return launch_attn_tc(b, grid, s); });
     const int rows = a.M * a.group, rt = attn_mma_row_tiles(rows);
     const int blocks = (rows + 16 * rt - 1) / (16 * rt), heads = a.G * blocks;
     const int tiles = std::max(1, (a.n_common + 63) / 64);
@@ -290,8 +315,10 @@ int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
     int chunks = one;
     a.cluster = 1;
     while (a.cluster < one) a.cluster *= 2;
+    const int* resident = attn_mma_resident(rt);
+    if (resident == nullptr) return MUSER_ERR_CUDA;  // the message is set
     if (tiles > 64) {
-        const int most = attn_mma_resident(rt) / heads;
+        const int most = *resident / heads;
         if (most > 2) {
             a.cluster = 8;
             chunks = std::min({8 * most, tiles / 2, static_cast<int>(8 * max_parts(a.G, rows))});

@@ -110,18 +110,24 @@ struct AttnWalk {
     }
 };
 
+// Clusters of 2^e blocks of a kernel that the current device runs at once (0:
+// none), found once per device.
+struct AttnResident {
+    int clusters[5];
+};
+
 // attn_mma.cu
 bool attn_mma_supported(const AttnArgs& a);
-int attn_mma_row_tiles(int rows);      // 16-row tiles of a block
-int attn_mma_resident(int row_tiles);  // clusters of 8 blocks that run at once (0: unknown)
+int attn_mma_row_tiles(int rows);             // 16-row tiles of a block
+const int* attn_mma_resident(int row_tiles);  // clusters of 8 blocks that run at once
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int row_tiles, cudaStream_t s);
 // The segments' tensor maps, boxes of `tile` rows (attn_mma.cu).
 int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps);
 // attn_few.cu: up to 32 query rows a K/V head, planes as for attn_tc.cu
-int attn_few_resident(int rows, int cluster);
+const AttnResident* attn_few_resident(int rows);
 int launch_attn_few(const AttnArgs& a, dim3 grid, cudaStream_t s);
 // attn_tc.cu: planes that attn_mma_supported() takes, head_dim <= 128
-int attn_tc_resident(int D, int cluster);
+const AttnResident* attn_tc_resident(int D);
 int launch_attn_tc(const AttnArgs& a, dim3 grid, cudaStream_t s);
 
 }  // namespace muser

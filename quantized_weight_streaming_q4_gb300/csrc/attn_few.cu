@@ -15,16 +15,15 @@
 //
 // A thread of a softmax warpgroup holds one key's scores against 16 rows, and
 // later one output element of the same rows.  The maximum over keys would be a
-// reduction across lanes for every tile; instead p = 2^(s - m + 8) with a
+// reduction across lanes for every tile; instead p = 2^(s - m + 11) with a
 // reference m per row that is the first tile's maximum and moves only when
-// some s exceeds it by more than 7 (binary16 ends at 2^16), which all threads
+// some s exceeds it by more than 4 (binary16 ends at 2^16), which all threads
 // agree on with one barrier.  The result does not depend on m but for
 // rounding.  O tiles are fresh accumulators added in registers.
 //
 // Bound: the planes' bytes for long caches (TMA, three stages of 64 KB in
 // flight a block), latency for short ones.
 #include <algorithm>
-#include <atomic>
 
 #include "attn.cuh"
 #include "attn_parts.cuh"
@@ -37,7 +36,7 @@ namespace {
 constexpr int kTile = 128;              // keys of a tile
 constexpr uint32_t kItem = kTile * 256; // a K or a V tile: two blocks of 64 elements a row
 constexpr uint32_t kHalf = kTile * 128;
-constexpr float kOff = 8.f, kMost = 15.f;
+constexpr float kOff = 11.f, kMost = 15.f;
 
 template <int R>
 struct Layout {
@@ -133,6 +132,19 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
                 const int rr = (u & 3) * 8 + (th >> 4), p = th & 15;
                 y[u] = make_uint4(0, 0, 0, 0);
                 if (rr < nragged && p * 8 < a.D) y[u] = attn_ragged8(a, g, rr, p * 8, u >= 4);
+            }
+        }
+    }
+    uint32_t ragged_see = 0;  // bit j: row j sees ragged key th
+    if (warp >= 4 && ragged && th < 32) {
+        int i = (r0 + w * 16) / a.group, k = r0 + w * 16 - i * a.group;
+        uint32_t seen = i < a.M ? (a.mask[i] >> th) & 1u : 0u;
+        for (int j = 0; j < 16; ++j) {
+            ragged_see |= seen << j;
+            if (++k == a.group) {
+                k = 0;
+                ++i;
+                seen = i < a.M ? (a.mask[i] >> th) & 1u : 0u;
             }
         }
     }
@@ -307,7 +319,6 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             b[j] = 0.f;
             l[j] = o[j] = 0.f;
         }
-        uint32_t spoiled = 0;  // bit j: row j sees a ragged row that is not finite
         auto drain = [&](int t) {  // adds the output tile t
             wait(kOFull + (t & 1), t >> 1);
             if (!ok) return;
@@ -324,17 +335,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             int sg, srow;
             const int real = next_tile(t, sg, srow);
             uint32_t see = th < real ? 0xffffu : 0u;  // bit j: row j sees this thread's key
-            if (t == rt) {
-                see = 0;
-                int i = (r0 + w * 16) / a.group, k = r0 + w * 16 - i * a.group;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const uint32_t seen = i < a.M ? a.mask[i] : 0u;
-                    if (th < 32 && ((seen >> th) & 1u)) see |= 1u << j;
-                    if (seen & *flags) spoiled |= 1u << j;
-                    if (++k == a.group) k = 0, ++i;
-                }
-            }
+            if (t == rt) see = ragged_see;
             wait(kSFull + (t & 1), t >> 1);
             if (!ok) *gave_up = 1;
             tc_fence_after();
@@ -416,7 +417,8 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         for (int j = 0; j < 16; ++j) out[(w * 16 + j) * L::kOutStride + th] = o[j];
         if (th < 16) {
             float sum = (red[th] + red[16 + th]) + (red[32 + th] + red[48 + th]);
-            if ((spoiled >> th) & 1u) sum = NAN;
+            const int i = (r0 + w * 16 + th) / a.group;
+            if (ragged && i < a.M && (a.mask[i] & *flags)) sum = NAN;  // it sees a ragged row that is not finite
             ml[w * 16 + th] = make_float2(ntiles > 0 ? reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + th] : kNegInf, sum);
         }
     }
@@ -431,23 +433,28 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
     if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
 }
 
+// The kernel's attributes and resident clusters, once per device; null with
+// the error set where that fails.
 template <int R>
-int prepare() {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaGetDevice");
-    if (dev < 64 && ((done.load(std::memory_order_acquire) >> dev) & 1u)) return MUSER_OK;
-    e = cudaFuncSetAttribute(attn_few_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<R>::kBytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_few_kernel<R>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
-    if (dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_release);
-    return MUSER_OK;
+const AttnResident* resident() {
+    return device_once<R, AttnResident>([](AttnResident& r) {
+        cudaError_t e = cudaFuncSetAttribute(attn_few_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<R>::kBytes);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_few_kernel<R>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
+        for (int i = 0; i < 5; ++i) {
+            cudaLaunchAttribute attr[2];
+            const cudaLaunchConfig_t cfg = cluster_config(1 << i, dim3(1u << i), Layout<R>::kThreads, Layout<R>::kBytes, nullptr, attr);
+            if (cudaOccupancyMaxActiveClusters(&r.clusters[i], attn_few_kernel<R>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                r.clusters[i] = 0;
+            }
+        }
+        return static_cast<int>(MUSER_OK);
+    });
 }
 
 template <int R>
 int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
-    MUSER_TRY(prepare<R>());
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, Layout<R>::kThreads, Layout<R>::kBytes, s, attr);
     AttnMaps maps;
@@ -457,27 +464,9 @@ int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
     return check_launch("attention");
 }
 
-template <int R>
-int resident(int cluster) {
-    static std::atomic<int> known[64][5];
-    int dev = 0, k = 0;
-    while ((1 << k) < cluster) ++k;
-    if (prepare<R>() != MUSER_OK || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
-    int n = known[dev][k].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = cluster_config(cluster, dim3(cluster), Layout<R>::kThreads, Layout<R>::kBytes, nullptr, attr);
-    if (cudaOccupancyMaxActiveClusters(&n, attn_few_kernel<R>, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    known[dev][k].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 }  // namespace
 
-int attn_few_resident(int rows, int cluster) { return rows <= 16 ? resident<16>(cluster) : resident<32>(cluster); }
+const AttnResident* attn_few_resident(int rows) { return rows <= 16 ? resident<16>() : resident<32>(); }
 
 int launch_attn_few(const AttnArgs& a, dim3 grid, cudaStream_t s) {
     return a.M * a.group <= 16 ? launch<16>(a, grid, s) : launch<32>(a, grid, s);

@@ -24,7 +24,6 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <atomic>
 #include <mutex>
 
 #include "attn.cuh"
@@ -369,24 +368,26 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
     if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
 }
 
-// The kernel's attributes, set once per device.
+// The kernel's attributes and its resident clusters of 8, once per device;
+// null with the error set where that fails.
 template <int RT>
-int prepare() {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaGetDevice");
-    if (dev < 64 && ((done.load(std::memory_order_acquire) >> dev) & 1u)) return MUSER_OK;
-    e = cudaFuncSetAttribute(attn_mma_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<RT>::kBytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_mma_kernel<RT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
-    if (dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_release);
-    return MUSER_OK;
+const int* resident() {
+    return device_once<RT, int>([](int& clusters) {
+        cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<RT>::kBytes);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_mma_kernel<RT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = cluster_config(8, dim3(8), kThreads, Layout<RT>::kBytes, nullptr, attr);
+        if (cudaOccupancyMaxActiveClusters(&clusters, attn_mma_kernel<RT>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            clusters = 0;
+        }
+        return static_cast<int>(MUSER_OK);
+    });
 }
 
 template <int RT>
 int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
-    MUSER_TRY((prepare<RT>()));
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, kThreads, Layout<RT>::kBytes, s, attr);
     AttnMaps maps;
@@ -396,31 +397,15 @@ int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
     return check_launch("attention");
 }
 
-// Clusters of 8 blocks that the device holds at once.
-template <int RT>
-int resident() {
-    static std::atomic<int> known[64];
-    int dev = 0;
-    if (prepare<RT>() != MUSER_OK || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
-    int n = known[dev].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = cluster_config(8, dim3(8), kThreads, Layout<RT>::kBytes, nullptr, attr);
-    if (cudaOccupancyMaxActiveClusters(&n, attn_mma_kernel<RT>, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    known[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 }  // namespace
 
-// Whether the planes' rows can be copied 16 bytes at a time.
+// Whether TMA and 16-byte loads can read the planes' rows.
 bool attn_mma_supported(const AttnArgs& a) {
     if (a.D % 8 != 0) return false;
     auto ok = [](const AttnSeg& s) {
-        return is_aligned(s.k, 16) && is_aligned(s.v, 16) && s.row_stride % 8 == 0 && s.head_stride % 8 == 0;
+        constexpr int64_t kMost = int64_t{1} << 39;  // a tensor map's strides are below 2^40 bytes
+        return is_aligned(s.k, 16) && is_aligned(s.v, 16) && s.row_stride % 8 == 0 && s.head_stride % 8 == 0 &&
+               s.row_stride < kMost && s.head_stride < kMost;
     };
     for (int i = 0; i < a.nseg; ++i)
         if (!ok(a.seg[i])) return false;
@@ -430,7 +415,7 @@ bool attn_mma_supported(const AttnArgs& a) {
 }
 
 int attn_mma_row_tiles(int rows) { return rows <= 16 ? 1 : 2; }
-int attn_mma_resident(int rt) { return rt == 1 ? resident<1>() : resident<2>(); }
+const int* attn_mma_resident(int rt) { return rt == 1 ? resident<1>() : resident<2>(); }
 
 int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps) {
     static std::once_flag once;

@@ -3,6 +3,9 @@
 // visibility differs, and the joining of a cluster's partial results.
 #pragma once
 
+#include <atomic>
+#include <mutex>
+
 #include "attn.cuh"
 
 namespace muser {
@@ -180,13 +183,13 @@ __device__ __forceinline__ void join_cluster(const AttnArgs& a, int tid, int c, 
         }
         if (!real || sub != 0) continue;
         if (final) {
-            const float inv = 1.f / l;
+            const float inv = __fdividef(1.f, l);  // l is between 2^-10 and 2^46: a step or two off
             float4 y = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
             if (a.gate) {
-                y.x /= 1.f + expf(-z.x);
-                y.y /= 1.f + expf(-z.y);
-                y.z /= 1.f + expf(-z.z);
-                y.w /= 1.f + expf(-z.w);
+                y.x = __fdividef(y.x, 1.f + expf(-z.x));
+                y.y = __fdividef(y.y, 1.f + expf(-z.y));
+                y.z = __fdividef(y.z, 1.f + expf(-z.z));
+                y.w = __fdividef(y.w, 1.f + expf(-z.w));
             }
             *reinterpret_cast<float4*>(a.out + row * a.D + d) = y;
         } else {
@@ -195,6 +198,30 @@ __device__ __forceinline__ void join_cluster(const AttnArgs& a, int tid, int c, 
             if (d == 0) a.part_ml[slot] = make_float2(M, l);
         }
     }
+}
+
+// What `make` fills in, once per device and kernel (TAG tells a file's kernels
+// apart); null where it failed.
+template <int TAG, typename T, typename F>
+const T* device_once(F&& make) {
+    constexpr int kDevices = 64;
+    static T value[kDevices];
+    static std::atomic<bool> done[kDevices];
+    static std::mutex mu;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= kDevices) {
+        cuda_fail(e != cudaSuccess ? e : cudaErrorInvalidDevice, "attention: cudaGetDevice");
+        return nullptr;
+    }
+    if (!done[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!done[dev].load(std::memory_order_relaxed)) {
+            if (make(value[dev]) != MUSER_OK) return nullptr;
+            done[dev].store(true, std::memory_order_release);
+        }
+    }
+    return &value[dev];
 }
 
 // Launch attributes: the cluster, and programmatic stream serialization (the

@@ -23,7 +23,6 @@
 // visibility differs.  K and V wait for their buffers apart: one thread for
 // both held a free K buffer back behind V's.
 #include <algorithm>
-#include <atomic>
 
 #include "attn.cuh"
 #include "attn_parts.cuh"
@@ -68,6 +67,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     auto next_tile = [&](int t, int& s, int& row) { return t < ragged ? nragged : walk.next(a, kTile, s, row); };
 
     pdl_launch_dependents();
+    // q and the ragged rows: coalesced loads of the streams, all in flight
+    // together and before the block's set-up, then through shared memory.
+    // (Asynchronous 16-byte copies of q moved 12 bytes a clock, 512-byte bulk
+    // copies 9.)
+    constexpr int kStep = 256 / (DP / 4), kQ = 128 / kStep;  // rows of one pass, passes
+    const int qd = tid % (DP / 4) * 4, q0 = (tid - 128) / (DP / 4);
+    float4 q4[kQ];
+    constexpr int kEach = 2 * 32 * (DP / 8) / 256;
+    uint4 x[kEach];
+    if (warp >= 4) {
+        pdl_wait();  // no global access before this
+        // row r0 + r of the block: tree row i, head j of the group
+        int i = (r0 + q0) / a.group, j = r0 + q0 - i * a.group;
+        const int skip = (a.H - a.group) * a.D;  // from one tree row's group to the next
+        const float* src = a.q + static_cast<int64_t>(g * a.group + r0 + q0) * a.D + static_cast<int64_t>(i) * skip + qd;
+#pragma unroll
+        for (int u = 0; u < kQ; ++u) {
+            q4[u] = r0 + q0 + u * kStep < rows && qd < a.D ? __ldcg(reinterpret_cast<const float4*>(src))
+                                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+            src += kStep * a.D;
+            for (j += kStep; j >= a.group; j -= a.group) src += skip;
+        }
+        if (ragged) {
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                const int y = u * 256 + tid - 128, v = u >= kEach / 2 ? 1 : 0, r = y / (DP / 8) - v * 32, p = y % (DP / 8);
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (r < nragged && p * 8 < a.D) x[u] = attn_ragged8(a, g, r, p * 8, v != 0);
+            }
+        }
+    }
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[kKFull + i], 1);
@@ -86,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (warp == 0) {
         tmem_alloc(tmem_slot, kTmemCols);
     }
-    pdl_wait();  // no global access before this
+    if (warp < 4) pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -203,35 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         set_regs_up<232>();
         const int w = (warp - 4) >> 2, row = tid & 127;  // stream, query row = TMEM lane
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        // q and the ragged rows: coalesced loads, all in flight together, then
-        // through shared memory.  (Asynchronous 16-byte copies of q moved 12
-        // bytes a clock, 512-byte bulk copies 9.)
-        constexpr int kStep = 256 / (DP / 4), kQ = 128 / kStep;  // rows of one pass, passes
-        const int qd = (tid - 128) % (DP / 4) * 4, q0 = (tid - 128) / (DP / 4);
-        float4 q4[kQ];
-        {
-            // row r0 + r of the block: tree row i, head j of the group
-            int i = (r0 + q0) / a.group, j = r0 + q0 - i * a.group;
-            const int skip = (a.H - a.group) * a.D;  // from one tree row's group to the next
-            const float* src = a.q + static_cast<int64_t>(g * a.group + r0 + q0) * a.D + static_cast<int64_t>(i) * skip + qd;
-#pragma unroll
-            for (int u = 0; u < kQ; ++u) {
-                q4[u] = r0 + q0 + u * kStep < rows && qd < a.D ? __ldcg(reinterpret_cast<const float4*>(src))
-                                                               : make_float4(0.f, 0.f, 0.f, 0.f);
-                src += kStep * a.D;
-                for (j += kStep; j >= a.group; j -= a.group) src += skip;
-            }
-        }
-        constexpr int kEach = 2 * 32 * (DP / 8) / 256;
-        uint4 x[kEach];
-        if (ragged) {
-#pragma unroll
-            for (int u = 0; u < kEach; ++u) {
-                const int y = u * 256 + tid - 128, v = u >= kEach / 2 ? 1 : 0, r = y / (DP / 8) - v * 32, p = y % (DP / 8);
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (r < nragged && p * 8 < a.D) x[u] = attn_ragged8(a, g, r, p * 8, v != 0);
-            }
-        }
 #pragma unroll
         for (int u = 0; u < kQ; ++u) sts_float4(out + (q0 + u * kStep) * L::kOutStride + qd, q4[u]);
         if (ragged) {  // stored as tile 0; a value that is not finite becomes 0 and is noted
@@ -382,23 +383,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
 }
 
+// The kernel's attributes and resident clusters, once per device; null with
+// the error set where that fails.
 template <int DP>
-int prepare() {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaGetDevice");
-    if (dev < 64 && ((done.load(std::memory_order_acquire) >> dev) & 1u)) return MUSER_OK;
-    e = cudaFuncSetAttribute(attn_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::kBytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_tc_kernel<DP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
-    if (dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_release);
-    return MUSER_OK;
+const AttnResident* resident() {
+    return device_once<DP, AttnResident>([](AttnResident& r) {
+        cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::kBytes);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_tc_kernel<DP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
+        for (int i = 0; i < 5; ++i) {
+            cudaLaunchAttribute attr[2];
+            const cudaLaunchConfig_t cfg = cluster_config(1 << i, dim3(1u << i), kThreads, Layout<DP>::kBytes, nullptr, attr);
+            if (cudaOccupancyMaxActiveClusters(&r.clusters[i], attn_tc_kernel<DP>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                r.clusters[i] = 0;
+            }
+        }
+        return static_cast<int>(MUSER_OK);
+    });
 }
 
 template <int DP>
 int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
-    MUSER_TRY(prepare<DP>());
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = cluster_config(a.cluster, grid, kThreads, Layout<DP>::kBytes, s, attr);
     AttnMaps maps;
@@ -408,27 +414,9 @@ int launch(const AttnArgs& a, dim3 grid, cudaStream_t s) {
     return check_launch("attention");
 }
 
-template <int DP>
-int resident(int cluster) {
-    static std::atomic<int> known[64][5];
-    int dev = 0, k = 0;
-    while ((1 << k) < cluster) ++k;
-    if (prepare<DP>() != MUSER_OK || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
-    int n = known[dev][k].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = cluster_config(cluster, dim3(cluster), kThreads, Layout<DP>::kBytes, nullptr, attr);
-    if (cudaOccupancyMaxActiveClusters(&n, attn_tc_kernel<DP>, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    known[dev][k].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 }  // namespace
 
-int attn_tc_resident(int D, int cluster) { return D <= 64 ? resident<64>(cluster) : resident<128>(cluster); }
+const AttnResident* attn_tc_resident(int D) { return D <= 64 ? resident<64>() : resident<128>(); }
 
 int launch_attn_tc(const AttnArgs& a, dim3 grid, cudaStream_t s) {
     return a.D <= 64 ? launch<64>(a, grid, s) : launch<128>(a, grid, s);

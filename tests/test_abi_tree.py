@@ -40,6 +40,8 @@ def attend(L, plane=None, sink=None, q=Q, k=K, v=V, gate=None, M=2, H=32, parent
     (dict(scratch=SCR + 8), -3), (dict(nbytes=1024), -1),
     (dict(out=Q), -1), (dict(out=K + 16), -1), (dict(out=V), -1), (dict(gate=OUT), -1),   # overlaps
     (dict(scratch=Q - 1024), -1), (dict(out=SCR + 4096), -1),
+    (dict(out=FAKE + 4096), -1), (dict(scratch=FAKE * 3 - 64), -1),                       # the planes
+    (dict(sink=mu.KvPlane(OUT + 16, FAKE * 2, 4, 4, 0, 0, 256, 128, 0, 0)), -1),
     (dict(plane=mu.KvPlane(FAKE, FAKE * 2, 2048, 2049, 0, 0, 256, 128, 0, 0)), -1),
     (dict(plane=mu.KvPlane(FAKE, None, 2048, 0, 0, 0, 256, 128, 0, 0)), -1),
     (dict(plane=mu.KvPlane(FAKE, FAKE * 2, 2048, 0, 0, 0, 256, 0, 0, 0)), -1),      # head_dim is needed in both layouts

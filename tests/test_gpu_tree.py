@@ -160,6 +160,29 @@ def test_attention_large_queries_and_sharp_softmax(H, kvh, D):
     c.to_device().call().check()
 
 
+@pytest.mark.parametrize("H,kvh,D", [(32, 2, 128), (16, 2, 128), (5, 1, 64), (4, 2, 24), (4, 1, 256), (4, 1, 7)])
+@pytest.mark.parametrize("M", [1, 2, 9])
+@pytest.mark.parametrize("falling", [False, True])
+def test_attention_scores_that_grow_along_the_cache(H, kvh, D, M, falling):
+    """The running maximum moves in every tile (or is the first key's): scores run from 0 to 4 scale D, up to 45."""
+    n = 3001
+    c = Case(M, H, kvh, D, n, n, 0, False, seed=12)
+    rng = np.random.default_rng(M)
+    sign = rng.choice([-1.0, 1.0], (kvh, D))
+    ramp = np.linspace(0, 4, n)[::-1 if falling else 1]
+    k = (ramp[:, None, None] * sign + 0.1 * rng.standard_normal((n, kvh, D))).astype(np.float16)
+    c.key[:] = np.ascontiguousarray(k.reshape(-1)).view(np.uint16)
+    c.q = np.broadcast_to(sign[np.arange(H) // (H // kvh)].reshape(1, H * D), (M, H * D)).astype(np.float32) * \
+        (0.5 + rng.random((M, H * D), np.float32))
+    c.to_device().call().check()
+
+
+@pytest.mark.parametrize("M,H,kvh,D,n", [(1, 64, 64, 64, 2100), (3, 40, 20, 128, 700), (16, 64, 8, 128, 2048), (2, 8, 2, 256, 9000),
+                                         (13, 30, 2, 120, 5000), (1, 9, 9, 8, 300), (16, 512, 1, 64, 200)])
+def test_attention_many_heads_and_odd_splits(M, H, kvh, D, n):
+    Case(M, H, kvh, D, n, n + 1, 0, True, kind=BINARY, gate=True, seed=13).to_device().call().check()
+
+
 @pytest.mark.parametrize("H,kvh,D", [(32, 2, 128), (6, 2, 80), (4, 2, 5)])
 @pytest.mark.parametrize("bad", [np.nan, np.inf])
 def test_attention_what_is_not_seen_has_no_influence(H, kvh, D, bad):
