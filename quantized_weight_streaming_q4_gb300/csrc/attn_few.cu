@@ -103,11 +103,12 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
     float* cs = reinterpret_cast<float*>(smem + L::kScaleOff);
     const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * R;
     const int rows = a.M * a.group;
-    // One tile of the last chunk holds the ragged rows: the last one, where every
-    // tile has a stage of its own (a reference taken from the few ragged keys
-    // alone would soon have to move), else tile 0.
+    // A single token's own row starts the last chunk's sums (`self`).  A tree's
+    // rows, and those at the windows' lower edge, are a tile of that chunk: the
+    // last one, where every tile has a stage of its own (a reference taken from
+    // the few ragged keys alone would soon have to move), else tile 0.
     AttnWalk walk(a, c);
-    const bool ragged = c == a.nchunks - 1;
+    const bool self = c == a.nchunks - 1 && a.M == 1, ragged = c == a.nchunks - 1 && a.M > 1;
     const int nragged = a.n_edge + a.M, ntiles = (ragged ? 1 : 0) + walk.count(a, kTile);
     const int rt = !ragged ? -1 : ntiles <= kNS ? ntiles - 1 : 0;
     auto next_tile = [&](int t, int& s, int& row) { return t == rt ? nragged : walk.next(a, kTile, s, row); };
@@ -119,6 +120,8 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
     const int qr = th >> 3, d0 = (th & 7) * 16;
     float4 x4[4];
     uint4 y[8];
+    float4 ks[4];
+    float vs = 0.f;
     if (warp >= 4) {
         pdl_wait();  // no global access before this
         const int r = r0 + w * 16 + qr, i = r / a.group;
@@ -126,6 +129,12 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             x4[u] = r < rows && d0 + 4 * u < a.D ? __ldcg(reinterpret_cast<const float4*>(src) + u) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (self) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                ks[u] = d0 + 4 * u < a.D ? __ldcg(reinterpret_cast<const float4*>(a.kt + g * a.D + d0) + u) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (th < a.D) vs = __ldcg(a.vt + g * a.D + th);
+        }
         if (ragged && w == 0) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -260,7 +269,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 3) {
-        prefetch_gate<R, 32>(a, lane, g, r0, rows);
+        if (gridDim.x > 1) prefetch_gate<R, 32>(a, lane, g, r0, rows);
     } else {
         // --------------------------------------- softmax and accumulation
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + w * 16;
@@ -276,6 +285,28 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             }
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (self) {  // the row's score against itself, K rounded as the cache will hold it
+                float dot = 0.f;
+                bool fine = true;
+                auto add = [&](float q, float k) {
+                    const float k16 = __half2float(__float2half_rn(k));
+                    fine = fine && fabsf(k16) < INFINITY;
+                    dot = fmaf(q, k16, dot);
+                };
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    add(x4[u].x, ks[u].x);
+                    add(x4[u].y, ks[u].y);
+                    add(x4[u].z, ks[u].z);
+                    add(x4[u].w, ks[u].w);
+                }
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                vs = __half2float(__float2half_rn(vs));
+                fine = fine && fabsf(vs) < INFINITY;
+                if (!fine) atomicOr(flags, 1u);
+                if ((th & 7) == 0) reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + qr] = dot;
+            }
             const int e = min(100, max(-100, ((__float_as_int(mx) >> 23) & 0xff) - 127)) - 7;
             const float up = __int_as_float((127 - e) << 23);
             if ((th & 7) == 0) cs[w * 16 + qr] = __int_as_float((127 + e) << 23);
@@ -315,10 +346,12 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             sc[j] = cs[w * 16 + j];
-            m[j] = kNegInf;
-            b[j] = 0.f;
-            l[j] = o[j] = 0.f;
+            m[j] = self ? reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + j] : kNegInf;
+            b[j] = self ? kOff - m[j] : 0.f;
+            l[j] = self && th == 0 ? 0x1p11f : 0.f;  // 2^kOff
+            o[j] = self ? 0x1p11f * vs : 0.f;
         }
+        if (self) named_barrier_sync(id, 128);  // before the references are written again
         auto drain = [&](int t) {  // adds the output tile t
             wait(kOFull + (t & 1), t >> 1);
             if (!ok) return;
@@ -351,7 +384,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
                 top = fmaxf(top, x[j]);
             }
             bool drained = t == 0;
-            const bool anew = group_any(id, t == 0 || top > kMost);
+            const bool anew = group_any(id, (t == 0 && !self) || top > kMost);
             if (*gave_up) {
                 ok = false;
                 break;
@@ -412,14 +445,40 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         float* red = reinterpret_cast<float*>(smem + L::kRedOff) + w * 64;
         fold16(l, [](float p, float q) { return p + q; });
         if ((lane & 1) == 0) red[(warp & 3) * 16 + (lane >> 1)] = l[0];
+        if (gridDim.x == 1) {  // nothing to join: straight to memory, a row at a time
+            float z[16];
+            const int64_t at = static_cast<int64_t>(g) * a.group * a.D + th;
+            // row r of the block: tree row i, head k of the group
+            int i = (r0 + w * 16) / a.group, k = r0 + w * 16 - i * a.group;
+            auto row_at = [&](int ti, int tk) { return at + (static_cast<int64_t>(ti) * a.H + tk) * a.D; };
+            int zi = i, zk = k;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                z[j] = 0.f;
+                if (a.gate && zi < a.M && th < a.D) z[j] = __ldcg(a.gate + row_at(zi, zk));
+                if (++zk == a.group) zk = 0, ++zi;
+            }
+            named_barrier_sync(id, 128);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float sum = (red[j] + red[16 + j]) + (red[32 + j] + red[48 + j]);
+                if (i < a.M && th < a.D && ok) {
+                    if (a.mask[i] & *flags) sum = NAN;  // it sees a ragged row that is not finite
+                    float v = o[j] * __fdividef(1.f, sum);
+                    if (a.gate) v = __fdividef(v, 1.f + expf(-z[j]));
+                    a.out[row_at(i, k)] = v;
+                }
+                if (++k == a.group) k = 0, ++i;
+            }
+        }
         named_barrier_sync(1 + L::kGroups, 128 * L::kGroups);  // every group's last product is done: P and q are free
 #pragma unroll
         for (int j = 0; j < 16; ++j) out[(w * 16 + j) * L::kOutStride + th] = o[j];
         if (th < 16) {
             float sum = (red[th] + red[16 + th]) + (red[32 + th] + red[48 + th]);
             const int i = (r0 + w * 16 + th) / a.group;
-            if (ragged && i < a.M && (a.mask[i] & *flags)) sum = NAN;  // it sees a ragged row that is not finite
-            ml[w * 16 + th] = make_float2(ntiles > 0 ? reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + th] : kNegInf, sum);
+            if ((ragged || self) && i < a.M && (a.mask[i] & *flags)) sum = NAN;  // it sees a ragged row that is not finite
+            ml[w * 16 + th] = make_float2(ntiles > 0 || self ? reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + th] : kNegInf, sum);
         }
     }
     tc_fence_before();
@@ -428,6 +487,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         tc_fence_after();
         tmem_free(tmem, L::kTmemCols);
     }
+    if (gridDim.x == 1) return;
     if (a.cluster > 1) cluster_sync();
     if (ok) join_cluster<128, L::kOutStride, R, L::kThreads, 8>(a, tid, c, g, r0, rows, base + L::kMlOff, base + L::kPOff);
     if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
