@@ -173,13 +173,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const __grid
         l = fmaf(f, w.y, l);
         o = make_float4(fmaf(f, v.x, o.x), fmaf(f, v.y, o.y), fmaf(f, v.z, o.z), fmaf(f, v.w, o.w));
     }
-    const float inv = 1.f / l;
+    const float inv = __fdividef(1.f, l);
     o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     if (a.gate) {
-        o.x /= 1.f + expf(-z.x);
-        o.y /= 1.f + expf(-z.y);
-        o.z /= 1.f + expf(-z.z);
-        o.w /= 1.f + expf(-z.w);
+        o.x = __fdividef(o.x, 1.f + __expf(-z.x));
+        o.y = __fdividef(o.y, 1.f + __expf(-z.y));
+        o.z = __fdividef(o.z, 1.f + __expf(-z.z));
+        o.w = __fdividef(o.w, 1.f + __expf(-z.w));
     }
     if (vec) reinterpret_cast<float4*>(a.out + row * a.D)[e] = o;
     else a.out[row * a.D + e] = o.x;

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             }
         }
     }
+    if (warp == 3) touch_args(a, lane);
     if (tid == 0) {
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bar[kKFull + i], 1);
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 3) {
-        if (gridDim.x > 1) prefetch_gate<R, 32>(a, lane, g, r0, rows);
+        prefetch_gate<R, 32>(a, lane, g, r0, rows);
     } else {
         // --------------------------------------- softmax and accumulation
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + w * 16;
@@ -342,6 +343,21 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             }
         }
         named_barrier_sync(id, 128);  // the rows' scales
+        const bool alone = gridDim.x == 1;  // nothing to join: straight to memory, a row at a time
+        const int ti0 = (r0 + w * 16) / a.group, tk0 = r0 + w * 16 - ti0 * a.group;  // row r: tree row, head of the group
+        const int live = th < a.D ? min(16, rows - r0 - w * 16) : 0;  // of this thread's rows
+        const int64_t at0 = (static_cast<int64_t>(ti0) * a.H + g * a.group + tk0) * a.D + th;
+        const int skip = (a.H - a.group) * a.D;  // from one tree row's group to the next
+        float z[16];
+        if (alone && a.gate) {
+            const float* p = a.gate + at0;
+#pragma unroll
+            for (int j = 0, k = tk0; j < 16; ++j) {
+                z[j] = j < live ? __ldcg(p) : 0.f;
+                p += a.D;
+                if (++k == a.group) k = 0, p += skip;
+            }
+        }
         float sc[16], b[16], m[16], l[16], o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -445,40 +461,30 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         float* red = reinterpret_cast<float*>(smem + L::kRedOff) + w * 64;
         fold16(l, [](float p, float q) { return p + q; });
         if ((lane & 1) == 0) red[(warp & 3) * 16 + (lane >> 1)] = l[0];
-        if (gridDim.x == 1) {  // nothing to join: straight to memory, a row at a time
-            float z[16];
-            const int64_t at = static_cast<int64_t>(g) * a.group * a.D + th;
-            // row r of the block: tree row i, head k of the group
-            int i = (r0 + w * 16) / a.group, k = r0 + w * 16 - i * a.group;
-            auto row_at = [&](int ti, int tk) { return at + (static_cast<int64_t>(ti) * a.H + tk) * a.D; };
-            int zi = i, zk = k;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                z[j] = 0.f;
-                if (a.gate && zi < a.M && th < a.D) z[j] = __ldcg(a.gate + row_at(zi, zk));
-                if (++zk == a.group) zk = 0, ++zi;
-            }
-            named_barrier_sync(id, 128);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float sum = (red[j] + red[16 + j]) + (red[32 + j] + red[48 + j]);
-                if (i < a.M && th < a.D && ok) {
-                    if (a.mask[i] & *flags) sum = NAN;  // it sees a ragged row that is not finite
-                    float v = o[j] * __fdividef(1.f, sum);
-                    if (a.gate) v = __fdividef(v, 1.f + expf(-z[j]));
-                    a.out[row_at(i, k)] = v;
-                }
-                if (++k == a.group) k = 0, ++i;
-            }
-        }
-        named_barrier_sync(1 + L::kGroups, 128 * L::kGroups);  // every group's last product is done: P and q are free
-#pragma unroll
-        for (int j = 0; j < 16; ++j) out[(w * 16 + j) * L::kOutStride + th] = o[j];
+        named_barrier_sync(id, 128);
         if (th < 16) {
             float sum = (red[th] + red[16 + th]) + (red[32 + th] + red[48 + th]);
             const int i = (r0 + w * 16 + th) / a.group;
             if ((ragged || self) && i < a.M && (a.mask[i] & *flags)) sum = NAN;  // it sees a ragged row that is not finite
-            ml[w * 16 + th] = make_float2(ntiles > 0 || self ? reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + th] : kNegInf, sum);
+            if (alone) cs[w * 16 + th] = __fdividef(1.f, sum);
+            else ml[w * 16 + th] = make_float2(ntiles > 0 || self ? reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + th] : kNegInf, sum);
+        }
+        if (alone) {
+            named_barrier_sync(id, 128);
+            float* p = a.out + at0;
+#pragma unroll
+            for (int j = 0, k = tk0; j < 16; ++j) {
+                float v = o[j] * cs[w * 16 + j];
+                if (a.gate) v = __fdividef(v, 1.f + __expf(-z[j]));
+                if (j < live && ok) *p = v;
+                p += a.D;
+                if (++k == a.group) k = 0, p += skip;
+            }
+        }
+        named_barrier_sync(1 + L::kGroups, 128 * L::kGroups);  // every group's last product is done: P and q are free
+        if (!alone) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) out[(w * 16 + j) * L::kOutStride + th] = o[j];
         }
     }
     tc_fence_before();
