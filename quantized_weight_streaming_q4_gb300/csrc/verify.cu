@@ -199,6 +199,8 @@ __global__ void __launch_bounds__(kThreads) verify_greedy_kernel(const __grid_co
     __shared__ int s_last, s_arg[MUSER_MAX_M], s_token[MUSER_MAX_M];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t* keys = reinterpret_cast<uint64_t*>(a.part);
+    pdl_launch_dependents();
+    pdl_wait();  // no global access before this
     int row, lo, hi;
     if (my_unit(a, row, lo, hi)) {
         float best = -INFINITY;
@@ -507,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
     uint64_t* wp = held;
     uint64_t* wq = held + a.span;
     for (int j = tid; j < kVerifyTable; j += kThreads) S.table[j] = a.table[j];
+    pdl_wait();  // no global access before this
     unsigned barriers = 0;
     bool ok = true;
     if (a.nrows > 0) {
@@ -845,26 +848,24 @@ int launch_verify(const float* target, const float* draft, const int32_t* tokens
     a.status = device_status_word();
     if (!a.status) return set_error(MUSER_ERR_CUDA, "tree_verify: no device status word");
     std::copy(weight_table(), weight_table() + kVerifyTable, a.table);
-    if (greedy) {
-        verify_greedy_kernel<<<blocks, kThreads, 0, s>>>(a);
-        return check_launch("tree_verify");
-    }
     const size_t smem = static_cast<size_t>(a.span) * 16u;
-    if (smem > 40 * 1024) {
+    if (!greedy && smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return cuda_fail(e, "tree_verify: cudaFuncSetAttribute");
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = greedy ? 0 : smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;  // every block resident at once (grid barriers)
-    attr[0].val.cooperative = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeCooperative;  // every block resident at once (grid barriers)
+    attr[1].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel, a);
+    cfg.numAttrs = greedy ? 1 : 2;
+    const cudaError_t e = greedy ? cudaLaunchKernelEx(&cfg, verify_greedy_kernel, a) : cudaLaunchKernelEx(&cfg, verify_kernel, a);
     if (e != cudaSuccess) return cuda_fail(e, "tree_verify: cudaLaunchKernelEx");
     return check_launch("tree_verify");
 }
