@@ -297,20 +297,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             wait(kSFull + w, t >> 1);
             if (!ok) break;
             tc_fence_after();
-            float tm = kNegInf;
+            float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};  // four chains of maxima
             for (int ch = 0; ch < chunks; ++ch) {
                 float s[32];
                 tmem_ld32(scol + ch * 32, s);
                 const uint32_t see = seen(ch);
                 tc_wait_ld();
-                if (see == 0xffffffffu) {
+                if (see != 0xffffffffu) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) tm = fmaxf(tm, s[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) tm = fmaxf(tm, (see >> j) & 1u ? s[j] : kNegInf);
+                    for (int j = 0; j < 32; ++j) s[j] = (see >> j) & 1u ? s[j] : kNegInf;
                 }
+#pragma unroll
+                for (int j = 0; j < 32; j += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], fmaxf(s[j + k], s[j + k + 4]));
             }
+            const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             const float mn = fmaxf(m, tm * down);
             const float al = m == kNegInf ? 0.f : ex2(m - mn);
             m = mn;
