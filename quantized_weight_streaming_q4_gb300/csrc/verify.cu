@@ -10,8 +10,8 @@
 //  3. What needs the whole vocabulary of one node (a rejected child's
 //     remainder, the next token) all blocks do together, each on its own slice
 //     of tokens, whose weights stay in shared memory, with one barrier each.
-// Temperature 0 is an ordinary launch; the last block to finish its maxima
-// walks.
+// Temperature 0, and a single row, are ordinary launches: the last block to
+// finish its maxima (its slice's sum) walks (finds the token).
 //
 // The next token comes from integer weights: with R an integer >= the largest
 // exponent, round(2^(l log2(e) / T - R) * 2^42), good to about 2^-38.  Sums of
@@ -310,12 +310,12 @@ __device__ __forceinline__ uint64_t scaled(uint64_t t, int sh) {
 __device__ __forceinline__ uint64_t times_f(uint64_t q, uint64_t fm, int fe) { return scaled(__umul64hi(q << 19, fm), fe + 64 - 19); }
 __device__ __forceinline__ uint64_t sum_times_f(uint64_t q, uint64_t fm, int fe) { return scaled(__umul64hi(q, fm), fe + 64); }
 
-// Logits [v0, v1) of the vocabulary are this block's in a pass; a thread's are
-// `per` neighbouring ones.
+// The tokens v0..v0+n-1 are a block's in a pass; a thread's are `per`
+// neighbouring ones.
 struct Span {
     int v0, n, per, first, last;  // first..last: this thread's, relative to v0
-    __device__ __forceinline__ explicit Span(const VerifyArgs& a) {
-        v0 = min(static_cast<int>(blockIdx.x) * a.span, a.V);
+    __device__ __forceinline__ Span(const VerifyArgs& a, int block) {
+        v0 = min(block * a.span, a.V);
         n = min(a.span, a.V - v0);
         per = (a.span + kThreads - 1) / kThreads;
         first = min(static_cast<int>(threadIdx.x) * per, n);
@@ -501,112 +501,174 @@ __device__ __forceinline__ int find_token(Shared& S, const Span& P, uint64_t r, 
     return S.found;
 }
 
+// f(k, the logit) for this thread's tokens, in order, four loads at a time.
+template <typename F>
+__device__ __forceinline__ void each_logit(const Span& P, const float* row, F&& f) {
+    for (int k = P.first; k < P.last; k += 4) {
+        float x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = k + u < P.last ? __ldcg(row + P.v0 + k + u) : 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (k + u < P.last) f(k + u, x[u]);
+    }
+}
+
+// A row's weights relative to the block's own largest exponent, 0 for the
+// tokens of the nodes in `removed`: to w, their sum and the exponent published.
+__device__ __forceinline__ void leaf_pass(const VerifyArgs& a, Shared& S, const Span& P, const float* row, uint32_t removed,
+                                          uint64_t* w, float* logit, unsigned barriers) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float mx = -INFINITY;
+    bool bad = false;
+    each_logit(P, row, [&](int k, float x) {
+        bad |= !(x < INFINITY);
+        mx = fmaxf(mx, x);
+        logit[k] = x;
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) S.warp_max[warp] = mx;
+    bad = __syncthreads_or(bad);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, S.warp_max[i]);
+    const float t = ceilf(mx * a.c_hi + 0.01f);
+    const bool some = t >= -kMaxExponent && t <= kMaxExponent;
+    const int R = some ? static_cast<int>(t) : -(1 << 23);
+    uint64_t v[1] = {0};
+    for (int k = P.first; k < P.last; ++k) {
+        uint64_t x = some ? weight(logit[k], a.c_hi, a.c_lo, R, S.table) : 0;
+        for (uint32_t r = removed; r; r &= r - 1)
+            if (S.token[__ffs(r) - 1] == P.v0 + k) x = 0;
+        v[0] += w[k] = x;
+    }
+    if (tid == 0) __stcg(a.exps + blockIdx.x, bad || t > kMaxExponent ? kBad : R);
+    publish(a, S, v, barriers);
+}
+
+// One row and nothing drafted: the last block to finish its slice finds the
+// token, on the owner's slice anew.
+__global__ void __launch_bounds__(kThreads, 1) verify_sample_kernel(const __grid_constant__ VerifyArgs a) {
+    __shared__ Shared S;
+    extern __shared__ uint64_t held[];  // [span] weights, [span] logits
+    const int tid = threadIdx.x;
+    for (int j = tid; j < kVerifyTable; j += kThreads) S.table[j] = a.table[j];
+    pdl_launch_dependents();
+    pdl_wait();  // no global access before this
+    __syncthreads();
+    leaf_pass(a, S, Span(a, blockIdx.x), a.target, 0u, held, reinterpret_cast<float*>(held + a.span), 0);
+    __syncthreads();
+    if (tid == 0) S.flag = atom_add_acq_rel_gpu(a.sync, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!S.flag) return;
+    settle<kLeaf>(a, S, 0);
+    int token = -1;
+    if (S.owner >= 0) {
+        const Span P(a, S.owner);
+        const int R = __ldcg(a.exps + S.owner);
+        each_logit(P, a.target, [&](int k, float x) { held[k] = weight(x, a.c_hi, a.c_lo, R, S.table); });
+        token = find_token(S, P, S.before << (S.exp - R), [&](int k) { return held[k]; });
+    }
+    if (tid == 0) {
+        a.result[0] = 1;
+        a.result[1] = token;
+        a.result[2] = 0;
+        a.sync[0] = 0;
+    }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ Shared S;
     extern __shared__ uint64_t held[];  // [span] target weights, [span] draft weights
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Span P(a);
+    const Span P(a, blockIdx.x);
     uint64_t* wp = held;
     uint64_t* wq = held + a.span;
     for (int j = tid; j < kVerifyTable; j += kThreads) S.table[j] = a.table[j];
     pdl_wait();  // no global access before this
     unsigned barriers = 0;
     bool ok = true;
-    if (a.nrows > 0) {
-        int row, lo, hi;
-        if (my_unit(a, row, lo, hi)) {
-            float sum = 0.f, R = -kMaxExponent;
-            for_slice(row_ptr(a, row), lo, hi, a.vec, [&](float4 v, int) {
-                const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) * a.c_hi;
-                if (t > R) {
-                    const float Rn = ceilf(t);
-                    sum *= ex2(R - Rn);
-                    R = Rn;
-                }
-                sum += (ex2(fmaf(v.x, a.c_hi, -R)) + ex2(fmaf(v.y, a.c_hi, -R))) +
-                       (ex2(fmaf(v.z, a.c_hi, -R)) + ex2(fmaf(v.w, a.c_hi, -R)));
-            });
-            float Rm = R;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) Rm = fmaxf(Rm, __shfl_xor_sync(0xffffffffu, Rm, o));
-            sum = warp_sum(sum * ex2(R - Rm));  // a NaN or +infinity leaves a NaN here
-            if (lane == 0) __stcg(a.part + row * kMaxSlices + lo / a.slice_len, make_float2(sum, Rm));
-        }
-        // the drafted tokens' logits, in flight during the barrier
-        float lx = -INFINITY, ly = -INFINITY;
-        if (tid >= 1 && tid < a.M) {
-            const int x = __ldg(a.tokens + tid), up = a.parent[tid];
-            S.token[tid] = x;
-            S.u[tid] = __ldg(a.uniform + tid);
-            if (x >= 0 && x < a.V) {
-                lx = __ldcg(row_ptr(a, a.target_at[up]) + x);
-                if (a.draft) ly = __ldcg(row_ptr(a, a.draft_at[up]) + x);
+    int row, lo, hi;
+    if (my_unit(a, row, lo, hi)) {
+        float sum = 0.f, R = -kMaxExponent;
+        for_slice(row_ptr(a, row), lo, hi, a.vec, [&](float4 v, int) {
+            const float t = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) * a.c_hi;
+            if (t > R) {
+                const float Rn = ceilf(t);
+                sum *= ex2(R - Rn);
+                R = Rn;
             }
-        }
-        ok = grid_barrier(a, ++barriers, &S.flag);
-        // every block: the rows' sums and the drafted tokens' probabilities
-        float2 x[2][kMaxSlices / 32];  // a warp has two rows at most: their loads go out together
+            sum += (ex2(fmaf(v.x, a.c_hi, -R)) + ex2(fmaf(v.y, a.c_hi, -R))) +
+                   (ex2(fmaf(v.z, a.c_hi, -R)) + ex2(fmaf(v.w, a.c_hi, -R)));
+        });
+        float Rm = R;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = warp + j * kWarps;
-#pragma unroll
-            for (int k = 0; k < kMaxSlices / 32; ++k)
-                x[j][k] = r < a.nrows && lane + 32 * k < a.slices ? __ldcg(a.part + r * kMaxSlices + lane + 32 * k)
-                                                                  : make_float2(0.f, -kMaxExponent);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float R = -kMaxExponent, sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < kMaxSlices / 32; ++k) R = fmaxf(R, x[j][k].y);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, o));
-#pragma unroll
-            for (int k = 0; k < kMaxSlices / 32; ++k) sum = fmaf(x[j][k].x, ex2(x[j][k].y - R), sum);
-            sum = warp_sum(sum);
-            if (lane == 0 && warp + j * kWarps < a.nrows) {
-                S.row_sum[warp + j * kWarps] = sum > 0.f && R <= kMaxExponent ? sum : NAN;
-                S.row_exp[warp + j * kWarps] = R;
-            }
-        }
-        __syncthreads();
-        if (warp == 0) {  // lane i: node i's probabilities, and whether it is accepted if it is its parent's first child
-            bool first = false, fine = true;
-            if (lane >= 1 && lane < a.M) {
-                const int up = a.parent[lane], tr = a.target_at[up], dr = a.draft_at[up];
-                const float p = ex2(fmaf(lx, a.c_hi, -S.row_exp[tr])) / S.row_sum[tr];
-                const float q = a.draft ? ex2(fmaf(ly, a.c_hi, -S.row_exp[dr])) / S.row_sum[dr] : 1.f;
-                S.px[lane] = p;
-                S.qx[lane] = q;
-                first = S.u[lane] * q < p;
-                fine = S.row_sum[tr] == S.row_sum[tr] && (!a.draft || S.row_sum[dr] == S.row_sum[dr]);
-            }
-            const uint32_t f = __ballot_sync(0xffffffffu, first), g = __ballot_sync(0xffffffffu, fine);
-            if (lane == 0) {
-                S.first = f;
-                S.fine = g;
-            }
-        }
-        __syncthreads();
+        for (int o = 16; o > 0; o >>= 1) Rm = fmaxf(Rm, __shfl_xor_sync(0xffffffffu, Rm, o));
+        sum = warp_sum(sum * ex2(R - Rm));  // a NaN or +infinity leaves a NaN here
+        if (lane == 0) __stcg(a.part + row * kMaxSlices + lo / a.slice_len, make_float2(sum, Rm));
     }
-
-    // This thread's weights of a row, in order: w(k, the logit), four loads at a time.
-    auto each_logit = [&](const float* row, auto&& w) {
-        for (int k = P.first; k < P.last; k += 4) {
-            float x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] = k + u < P.last ? __ldcg(row + P.v0 + k + u) : 0.f;
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (k + u < P.last) w(k + u, x[u]);
+    // the drafted tokens' logits, in flight during the barrier
+    float lx = -INFINITY, ly = -INFINITY;
+    if (tid >= 1 && tid < a.M) {
+        const int x = __ldg(a.tokens + tid), up = a.parent[tid];
+        S.token[tid] = x;
+        S.u[tid] = __ldg(a.uniform + tid);
+        if (x >= 0 && x < a.V) {
+            lx = __ldcg(row_ptr(a, a.target_at[up]) + x);
+            if (a.draft) ly = __ldcg(row_ptr(a, a.draft_at[up]) + x);
         }
-    };
+    }
+    ok = grid_barrier(a, ++barriers, &S.flag);
+    // every block: the rows' sums and the drafted tokens' probabilities
+    float2 x[2][kMaxSlices / 32];  // a warp has two rows at most: their loads go out together
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int r = warp + j * kWarps;
+#pragma unroll
+        for (int k = 0; k < kMaxSlices / 32; ++k)
+            x[j][k] = r < a.nrows && lane + 32 * k < a.slices ? __ldcg(a.part + r * kMaxSlices + lane + 32 * k)
+                                                              : make_float2(0.f, -kMaxExponent);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        float R = -kMaxExponent, sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxSlices / 32; ++k) R = fmaxf(R, x[j][k].y);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, o));
+#pragma unroll
+        for (int k = 0; k < kMaxSlices / 32; ++k) sum = fmaf(x[j][k].x, ex2(x[j][k].y - R), sum);
+        sum = warp_sum(sum);
+        if (lane == 0 && warp + j * kWarps < a.nrows) {
+            S.row_sum[warp + j * kWarps] = sum > 0.f && R <= kMaxExponent ? sum : NAN;
+            S.row_exp[warp + j * kWarps] = R;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {  // lane i: node i's probabilities, and whether it is accepted if it is its parent's first child
+        bool first = false, fine = true;
+        if (lane >= 1 && lane < a.M) {
+            const int up = a.parent[lane], tr = a.target_at[up], dr = a.draft_at[up];
+            const float p = ex2(fmaf(lx, a.c_hi, -S.row_exp[tr])) / S.row_sum[tr];
+            const float q = a.draft ? ex2(fmaf(ly, a.c_hi, -S.row_exp[dr])) / S.row_sum[dr] : 1.f;
+            S.px[lane] = p;
+            S.qx[lane] = q;
+            first = S.u[lane] * q < p;
+            fine = S.row_sum[tr] == S.row_sum[tr] && (!a.draft || S.row_sum[dr] == S.row_sum[dr]);
+        }
+        const uint32_t f = __ballot_sync(0xffffffffu, first), g = __ballot_sync(0xffffffffu, fine);
+        if (lane == 0) {
+            S.first = f;
+            S.fine = g;
+        }
+    }
+    __syncthreads();
 
     // The walk: the same in every thread of every block.  Binary64 is thread
     // 0's alone: one division by all 512 threads holds an SM for 3 us.
     int cur = 0, n = 1;
     uint32_t kept = 1u, removed = 0u;
-    const uint32_t first = a.nrows ? S.first : 0u, fine = a.nrows ? S.fine : 0u;
+    const uint32_t first = S.first, fine = S.fine;
     bool valid = true, rejected = false;  // rejected: the node's weights are held, S describes its remainder
     float left = 1.f, c = 0.f;
     auto remainder = [&](int k) {  // max(P - f Q, 0)
@@ -712,32 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
         // without rejections: weights relative to the block's own largest exponent
         const float* row = a.target + static_cast<int64_t>(cur) * a.V;
         for (int again = 0; !rejected && again < 2 && ok; ++again) {
-            float mx = -INFINITY;
-            bool bad = false;
-            float* logit = reinterpret_cast<float*>(wq);  // this thread's own, until the weights are made
-            each_logit(row, [&](int k, float x) {
-                bad |= !(x < INFINITY);
-                mx = fmaxf(mx, x);
-                logit[k] = x;
-            });
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (lane == 0) S.warp_max[warp] = mx;
-            bad = __syncthreads_or(bad);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, S.warp_max[w]);
-            const float t = ceilf(mx * a.c_hi + 0.01f);
-            const bool some = t >= -kMaxExponent && t <= kMaxExponent;
-            const int R = some ? static_cast<int>(t) : -(1 << 23);
-            uint64_t v[1] = {0};
-            for (int k = P.first; k < P.last; ++k) {
-                uint64_t w = some ? weight(logit[k], a.c_hi, a.c_lo, R, S.table) : 0;
-                for (uint32_t r = removed; r; r &= r - 1)
-                    if (S.token[__ffs(r) - 1] == P.v0 + k) w = 0;
-                v[0] += wp[k] = w;
-            }
-            if (tid == 0) __stcg(a.exps + blockIdx.x, bad || t > kMaxExponent ? kBad : R);
-            publish(a, S, v, ++barriers);
+            leaf_pass(a, S, P, row, removed, wp, reinterpret_cast<float*>(wq), ++barriers);
             ok = grid_barrier(a, barriers, &S.flag);
             if (!ok) break;
             settle<kLeaf>(a, S, barriers);
@@ -849,10 +886,6 @@ int launch_verify(const float* target, const float* draft, const int32_t* tokens
     if (!a.status) return set_error(MUSER_ERR_CUDA, "tree_verify: no device status word");
     std::copy(weight_table(), weight_table() + kVerifyTable, a.table);
     const size_t smem = static_cast<size_t>(a.span) * 16u;
-    if (!greedy && smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return cuda_fail(e, "tree_verify: cudaFuncSetAttribute");
-    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(kThreads);
@@ -864,8 +897,13 @@ int launch_verify(const float* target, const float* draft, const int32_t* tokens
     attr[1].id = cudaLaunchAttributeCooperative;  // every block resident at once (grid barriers)
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = greedy ? 1 : 2;
-    const cudaError_t e = greedy ? cudaLaunchKernelEx(&cfg, verify_greedy_kernel, a) : cudaLaunchKernelEx(&cfg, verify_kernel, a);
+    cfg.numAttrs = greedy || M == 1 ? 1 : 2;
+    auto kern = greedy ? verify_greedy_kernel : M == 1 ? verify_sample_kernel : verify_kernel;
+    if (!greedy && smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return cuda_fail(e, "tree_verify: cudaFuncSetAttribute");
+    }
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess) return cuda_fail(e, "tree_verify: cudaLaunchKernelEx");
     return check_launch("tree_verify");
 }
