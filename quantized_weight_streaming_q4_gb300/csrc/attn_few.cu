@@ -375,7 +375,8 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             float hi[16], lo[16];
             tmem_ld16(mine + 2 * L::kN + (t & 1) * L::kN, hi);
             tmem_ld16(mine + 2 * L::kN + (t & 1) * L::kN + R, lo);
-            tc_wait_ld();
+            tc_wait_ld(hi);
+            tc_wait_ld(lo);
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] += hi[j] + lo[j];
             tc_fence_before();
@@ -391,7 +392,8 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             float s[16], x[16];
             tmem_ld16(mine + (t & 1) * L::kN, s);
             tmem_ld16(mine + (t & 1) * L::kN + R, x);
-            tc_wait_ld();
+            tc_wait_ld(s);
+            tc_wait_ld(x);
             float top = kNegInf;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {

@@ -173,13 +173,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     const uint64_t vd = desc_swizzle128(base + (2 + s) * L::kItem, kHalf, 1024);
                     const int steps = keys[s] / 16;
                     if (leader) {
-                        mma<false>(d, p + 16, vd, id);  // the low part of p first
+                        mma<false>(d, p + 8, vd, id);  // the low part of p first
 #pragma unroll
                         for (int ks = 1; ks < kTile / 16; ++ks)
-                            if (ks < steps) mma<true>(d, p + (ks >> 1) * 32 + 16 + (ks & 1) * 8, vd + (ks * 2048 >> 4), id);
+                            if (ks < steps) mma<true>(d, p + ks * 16 + 8, vd + (ks * 2048 >> 4), id);
 #pragma unroll
                         for (int ks = 0; ks < kTile / 16; ++ks)
-                            if (ks < steps) mma<true>(d, p + (ks >> 1) * 32 + (ks & 1) * 8, vd + (ks * 2048 >> 4), id);
+                            if (ks < steps) mma<true>(d, p + ks * 16, vd + (ks * 2048 >> 4), id);
                         mma_commit(&bar[kOFull + s]);
                         mma_commit(&bar[kVEmpty + s]);
                     }
@@ -297,12 +297,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             wait(kSFull + w, t >> 1);
             if (!ok) break;
             tc_fence_after();
-            float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};  // four chains of maxima
+            // the row's maximum: four chains, the next 32 columns under way
+            float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
             for (int ch = 0; ch < chunks; ++ch) {
                 float s[32];
                 tmem_ld32(scol + ch * 32, s);
                 const uint32_t see = seen(ch);
-                tc_wait_ld();
+                tc_wait_ld(s);
                 if (see != 0xffffffffu) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) s[j] = (see >> j) & 1u ? s[j] : kNegInf;
@@ -317,12 +318,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const float al = m == kNegInf ? 0.f : ex2(m - mn);
             m = mn;
             const float off = mn == kNegInf ? 0.f : kOffset - mn;
+            // p: over the 32 columns read go, for each 16 keys, 8 columns of high
+            // parts and 8 of low ones, the operand of one product
             float l0 = 0.f, l1 = 0.f;
             for (int ch = 0; ch < chunks; ++ch) {
                 float s[32];
                 tmem_ld32(scol + ch * 32, s);
                 const uint32_t see = seen(ch);
-                tc_wait_ld();
+                tc_wait_ld(s);
                 uint32_t p[32];
                 if (see != 0xffffffffu) {
 #pragma unroll
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     const float p0 = ex2(fmaf(s[j], down, off)), p1 = ex2(fmaf(s[j + 1], down, off));
                     l0 += p0;
                     l1 += p1;
-                    split2(p0, p1, p[j / 2], p[16 + j / 2]);
+                    split2(p0, p1, p[(j & 16) + (j & 15) / 2], p[(j & 16) + 8 + (j & 15) / 2]);
                 }
                 tmem_st32(scol + ch * 32, p);
             }
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             for (int ch = 0; ch < DP / 32; ++ch) {
                 float s[32];
                 tmem_ld32(mine + kColO + ch * 32, s);
-                tc_wait_ld();
+                tc_wait_ld(s);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[ch * 32 + j] = fmaf(o[ch * 32 + j], al, s[j]);
             }
