@@ -616,8 +616,9 @@ size_t muser_tree_verify_scratch_bytes(int64_t vocab, int M);
  *   about 2^-37 of the cumulative sum (2^-33 where logit / temperature is in
  *   the thousands); a probability below 2^-41 of the row's largest, or a
  *   remainder that small, may count as nothing.
- *   Sampling is one cooperative launch whose blocks wait for one another
- *   (bounded in time, muser_device_status() bit 1, result then unwritten).
+ *   Sampling with M > 1 is one launch whose blocks wait for one another: a
+ *   cooperative one (bounded in time, muser_device_status() bit 1, result
+ *   then unwritten), or over few logits one thread-block cluster.
  *   scratch: device memory of muser_tree_verify_scratch_bytes(), 16-byte
  *   aligned, zero-filled before its first use; its first 256 bytes are left
  *   zero, the rest is not.  Calls that can run at the same time must not
