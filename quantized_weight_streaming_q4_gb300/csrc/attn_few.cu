@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + kBars);
     uint32_t* flags = tmem_slot + 1;
-    volatile uint32_t* gave_up = tmem_slot + 2;  // a softmax thread's wait ran out: all leave at their next barrier
+    // a softmax thread's wait ran out: its warpgroup leaves at its next barrier
+    volatile uint32_t* gave_up = tmem_slot + 2 + (warp >= 8 ? 1 : 0);
     float* cs = reinterpret_cast<float*>(smem + L::kScaleOff);
     const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * R;
     const int rows = a.M * a.group;
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         mbar_init(&bar[kQReady], 128 * L::kGroups);
         mbar_init(&bar[kRagged], 128);
         *flags = 0;
-        *gave_up = 0;
+        tmem_slot[2] = tmem_slot[3] = 0;
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tmem_slot, L::kTmemCols);
