@@ -541,7 +541,10 @@ int muser_kv_restore(muser_kv_plane* plane, const uint16_t* k_rows, const uint16
  * row that other drafted rows still see.  One decode step is then, per layer,
  * muser_qmatvec_group and muser_kv_tree_attention; muser_lm_head;
  * muser_tree_verify; and muser_kv_tree_commit over all layers.  M = 1 is plain
- * decoding.  The attention call is the attention of Ch 10 Figure 10.1 with
+ * decoding.  What these calls read from host memory (the planes' metadata,
+ * parent, path, position) is fixed when a call is captured into a graph.
+ * Positions end at 2^62.
+ * The attention call is the attention of Ch 10 Figure 10.1 with
  * the window of Ch 15 §15.2 and the output's sigmoid gate (Ch 2 §2.7).
  */
 
@@ -610,7 +613,8 @@ size_t muser_tree_verify_scratch_bytes(int64_t vocab, int M);
  *   [M + 2]: the number n of kept rows (row 0 included), the next token, the
  *   kept rows ascending, then -1.  The token is -1 when the walk meets a row
  *   with a NaN, a +infinity, only -infinities, or a largest logit /
- *   temperature beyond about +-22,000.  vocab <= 2^20, temperature 0 or >= 0.001.
+ *   temperature beyond about +-22,000.  vocab <= 2^20, temperature 0 or
+ *   0.001..1e30.
  *   Acceptance is decided to about 2^-19 of the compared probabilities (equal
  *   rows accept every token).  The next token is that of exact arithmetic to
  *   about 2^-37 of the cumulative sum (2^-33 where logit / temperature is in
@@ -634,11 +638,11 @@ int muser_tree_verify(const float* target, const float* draft, const int32_t* to
  *   and v[i], exactly as n muser_kv_ring_write calls of one row from
  *   `position` on.  Every plane must end at `position` (else
  *   MUSER_ERR_CACHE_DISCONTINUITY); planes may differ in layout, capacity and
- *   length, and must not share memory.
+ *   length, and must not share memory.  kv_dim <= 2^26.
  *   planes: host array, updated on success; k, v: host arrays of device f32
  *   [M * kv_dim] pointers, 4-byte aligned (16-byte aligned ones with kv_dim,
  *   and head_dim for head-major planes, multiples of 8 take 16-byte
- *   accesses); path: host array of n rows, ascending, in 0..M-1.  n == 0
+ *   accesses), outside the planes; path: host array of n rows, ascending, in 0..M-1.  n == 0
  *   launches nothing.  Any error changes no plane.
  */
 int muser_kv_tree_commit(muser_kv_plane* planes, int n_planes, const float* const* k, const float* const* v, int M,

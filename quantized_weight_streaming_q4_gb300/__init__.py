@@ -388,15 +388,15 @@ def muser_kv_restore(plane: KvPlane, k_rows, v_rows, origin_logical: int, length
 
 
 def _ints(values):
-    """A host int32 array from a sequence; None and ctypes arrays pass through."""
-    if values is None or isinstance(values, ctypes.Array):
+    """A host int32 array from a sequence; None and c_int32 arrays pass through."""
+    if values is None or (isinstance(values, ctypes.Array) and values._type_ is ctypes.c_int32):
         return values
     return (ctypes.c_int32 * len(values))(*values)
 
 
 def _ptrs(values):
-    """A host array of device pointers from a sequence; ctypes arrays pass through."""
-    if isinstance(values, ctypes.Array):
+    """A host array of device pointers from a sequence; c_void_p arrays pass through."""
+    if isinstance(values, ctypes.Array) and values._type_ is ctypes.c_void_p:
         return values
     return (ctypes.c_void_p * len(values))(*[_ptr(t) for t in values])
 

@@ -1170,6 +1170,14 @@ static int plane_runs(const muser_kv_plane& P, int64_t head_dim, int64_t first, 
     return n;
 }
 
+// Positions of a tree's rows are sums of the plane's.
+static int check_positions(const char* fn, const muser_kv_plane& P) {
+    constexpr int64_t kMost = int64_t{1} << 62;
+    if (P.origin_logical > kMost || P.len > kMost)
+        return set_error(MUSER_ERR_UNSUPPORTED, "%s: positions beyond 2^62", fn);
+    return MUSER_OK;
+}
+
 // The checks of an attention call's head layout.
 static int check_heads(const char* fn, int64_t kv_dim, int64_t head_dim, int M, int n_heads) {
     MUSER_TRY(check_M(fn, M));
@@ -1197,11 +1205,13 @@ int muser_kv_tree_attention(const muser_kv_plane* plane, const muser_kv_plane* s
     const char* fn = "muser_kv_tree_attention";
     MUSER_TRY(check_plane(plane, fn));
     const muser_kv_plane& P = *plane;
+    MUSER_TRY(check_positions(fn, P));
     MUSER_TRY(check_heads(fn, P.kv_dim, P.head_dim, M, n_heads));
     int depth[MUSER_MAX_M];
     MUSER_TRY(check_tree(fn, parent, M, depth));
     if (sink) {
         MUSER_TRY(check_plane(sink, fn));
+        MUSER_TRY(check_positions(fn, *sink));
         if (sink->kv_dim != P.kv_dim || (sink->head_major && sink->head_dim != P.head_dim))
             return set_error(MUSER_ERR_INVALID_ARG, "%s: the sink plane's kv_dim/head_dim differ from the plane's", fn);
     }
@@ -1302,8 +1312,8 @@ int muser_tree_verify(const float* target, const float* draft, const int32_t* to
     if (vocab > kVerifyMaxVocab)
         return set_error(MUSER_ERR_UNSUPPORTED, "%s: vocab = %lld above %lld", fn, (long long)vocab,
                          (long long)kVerifyMaxVocab);
-    if (!(temperature >= 0.0) || !std::isfinite(temperature) || (temperature > 0.0 && temperature < 1e-3))
-        return set_error(MUSER_ERR_INVALID_ARG, "%s: temperature must be 0 (greedy) or at least 0.001", fn);
+    if (!(temperature == 0.0 || (temperature >= 1e-3 && temperature <= 1e30)))
+        return set_error(MUSER_ERR_INVALID_ARG, "%s: temperature must be 0 (greedy) or 0.001..1e30", fn);
     MUSER_TRY(check_f32(fn, "target", target));
     if (temperature > 0.0) {
         if (draft) MUSER_TRY(check_f32(fn, "draft", draft));
@@ -1351,6 +1361,9 @@ int muser_kv_tree_commit(muser_kv_plane* planes, int n_planes, const float* cons
     for (int i = 0; i < n_planes; ++i) {
         MUSER_TRY(check_plane(planes + i, fn));
         const muser_kv_plane& P = planes[i];
+        MUSER_TRY(check_positions(fn, P));
+        if (P.kv_dim > kCommitMaxKvDim)
+            return set_error(MUSER_ERR_UNSUPPORTED, "%s: plane %d: kv_dim = %d above %d", fn, i, P.kv_dim, kCommitMaxKvDim);
         if (P.origin_logical + P.len != position)
             return set_error(MUSER_ERR_CACHE_DISCONTINUITY, "%s: plane %d: cache discontinuity: expected position %lld, got %lld",
                              fn, i, (long long)(P.origin_logical + P.len), (long long)position);

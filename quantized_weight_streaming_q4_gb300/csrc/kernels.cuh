@@ -200,6 +200,7 @@ int launch_kv_window(uint16_t* key, uint16_t* value, uint16_t* k_rows, uint16_t*
 // rows path[j0..n) of k[p] and v[p] go to slots (slot + j) % capacity.  Rows
 // before j0 do not survive the append (a plane of fewer than n slots).
 constexpr int kCommitMaxPlanes = 128;
+constexpr int kCommitMaxKvDim = 1 << 26;  // an element of the rows has a 32-bit index
 struct CommitPlane {
     uint16_t* key;
     uint16_t* value;

@@ -133,3 +133,24 @@ def test_binding_checks_lengths(L):
     with pytest.raises(mu.MuserError, match="discontinuity"):
         mu.muser_kv_tree_commit([plane], [K], [V], 2, [0], 101, stream=0)
     assert (plane.len, plane.origin_logical) == (100, 0)
+
+
+def test_sizes_beyond_the_kernels_indexes_are_refused(L):
+    far = mu.KvPlane(FAKE, FAKE * 2, 2048, 100, (1 << 62) + 1, 0, 256, 128, 0, 0)
+    ring = mu.KvPlane(FAKE, FAKE * 2, 2048, 100, 0, 0, 256, 128, 0, 0)
+    assert attend(L, plane=far) == -2 and attend(L, plane=ring, sink=far) == -2
+    assert commit(L, [far], position=(1 << 62) + 101)[0] == -2
+    wide = mu.KvPlane(FAKE * 16, FAKE * 4096, 2, 1, 0, 0, (1 << 26) + 1, 1, 0, 0)
+    assert commit(L, [wide], position=1)[0] == -2 and "kv_dim" in mu.muser_last_error()
+    assert verify(L, T=1e31) == -1 and verify(L, T=5e-324) == -1
+
+
+def test_binding_converts_arrays_of_other_types(L):
+    """A c_int64 or numpy array is converted, not read as if it held 32-bit integers."""
+    import numpy as np
+    plane = mu.KvPlane(FAKE, FAKE * 2, 2048, 100, 0, 0, 256, 128, 0, 0)
+    for path in ((ctypes.c_int64 * 2)(1, 1), np.array([1, 1]), np.array([1, 1], dtype=np.int8)):
+        with pytest.raises(mu.MuserError, match=r"path\[1\] = 1"):
+            mu.muser_kv_tree_commit([plane], [K], [V], 4, path, 100, stream=0)
+    with pytest.raises(mu.MuserError, match=r"path\[1\] = 1"):
+        mu.muser_kv_tree_commit([plane], (ctypes.c_int64 * 1)(K), [V], 4, [1, 1], 100, stream=0)
