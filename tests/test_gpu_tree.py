@@ -406,6 +406,40 @@ def test_verify_rows_that_are_no_distribution(bad):
     assert c.run()[1] == -1
 
 
+@pytest.mark.parametrize("V", [511, 513, 39999, 40000, 40001, 65536])
+@pytest.mark.parametrize("kind,draft", [(CHAIN, True), (BINARY, True), (STAR, False)])
+def test_verify_where_the_launch_changes(V, kind, draft):
+    """Both sides of the sizes at which one cluster gives way to the whole grid, many siblings rejected."""
+    for M in (2, 16):
+        c = Verify(M, V, kind, 1.0, draft, 40 + M, close=1.5)
+        c.check()
+        c.u[1:] = np.maximum(c.u[1:], 0.95)
+        c.check()
+
+
+def test_verify_calls_of_all_kinds_share_scratch_in_a_stream():
+    cases = [Verify(16, 202048, BINARY, 0.7, True, 6), Verify(5, 9999, STAR, 1.0, False, 7), Verify(1, 32768, CHAIN, 1.0, False, 8),
+             Verify(9, 50257, CHAIN, 0.0, False, 9), Verify(16, 3000, STAR, 1.0, True, 10)]
+    cases[0].check()
+    for c in cases[1:]:
+        c.scratch = cases[0].scratch
+    wants = [c.want() for c in cases]
+    for i in (0, 1, 2, 3, 4, 4, 0, 3, 1, 0, 2, 4, 2, 1, 3):
+        assert np.array_equal(cases[i].run(), wants[i]), i
+
+
+@pytest.mark.parametrize("T,M,draft", [(1e-3, 1, False), (1e6, 1, False), (1e6, 8, True), (1e30, 1, False), (1e30, 8, True),
+                                       (1e30, 8, False)])
+def test_verify_extreme_temperatures(T, M, draft):
+    c = Verify(M, 5000, BINARY, T, draft, 30 + M)
+    c.target *= 0.5                     # at T = 0.001 within the range of exponents
+    c.target[:, 1::2] = -np.inf
+    if draft:
+        c.draft[:, 1::2] = -np.inf
+    c.tokens = drafted(np.random.default_rng(M), c.draft if draft else c.target, c.parent, T)
+    c.check()
+
+
 def test_verify_greedy_ties_take_the_lowest_index():
     c = Verify(3, 202048, CHAIN, 0.0, False, 1)
     c.target[:, [5, 77, 150000, 202047]] = 50.0
