@@ -193,15 +193,17 @@ int generic_chunks(int G, int blocks_per_head, int n_common) {
 
 }  // namespace
 
-// The most parts a call leaves for the second kernel.
-static int64_t max_parts(int64_t G, int64_t rows) {
+// The most parts a call leaves for the second kernel: of attn_tc.cu's, one for
+// each pair of SMs.
+static int64_t max_parts(int64_t G, int64_t rows, int64_t D) {
     const int64_t blocks = (rows + kGenWarps * kGenQ - 1) / (kGenWarps * kGenQ);
-    return std::max<int64_t>(1, kAttnBlocks / std::max<int64_t>(1, G * blocks));
+    const int64_t pairs = rows > 32 && D <= 128 ? 76 / (G * ((rows + 127) / 128)) : 0;
+    return std::max<int64_t>({1, kAttnBlocks / std::max<int64_t>(1, G * blocks), pairs});
 }
 
 size_t attn_scratch_bytes(int64_t kv_dim, int64_t head_dim, int M, int n_heads) {
     const int64_t G = kv_dim / head_dim;
-    const int64_t parts = max_parts(G, static_cast<int64_t>(M) * (n_heads / G));
+    const int64_t parts = max_parts(G, static_cast<int64_t>(M) * (n_heads / G), head_dim);
     return (static_cast<size_t>(parts * M * n_heads * (head_dim + 2)) * 4u + 15u) / 16u * 16u;
 }
 
@@ -282,10 +284,14 @@ int launch_tiles(AttnArgs a, int R, double tile_us, double tile_full_us, void* s
                  const AttnResident* resident, Launch&& launch) {
     if (resident == nullptr) return MUSER_ERR_CUDA;  // the message is set
     const int rows = a.M * a.group, blocks = (rows + R - 1) / R;
-    const Split split = choose_split(a.G * blocks, (a.n_common + 127) / 128, static_cast<int>(max_parts(a.G, rows)), tile_us,
+    // A tree's own rows are one more tile, of the last chunk, which therefore
+    // takes 128 common rows less (16 rows, 2,037 common rows, 16 chunks: three
+    // tiles in the last one 14.2 us, two in each 12.0).
+    const int n = a.n_common + (R == 128 || a.M > 1 ? 128 : 0);
+    const Split split = choose_split(a.G * blocks, (n + 127) / 128, static_cast<int>(max_parts(a.G, rows, a.D)), tile_us,
                                      tile_full_us, *resident);
     a.cluster = split.cluster;
-    a.chunk = std::max(16, ((a.n_common + split.chunks - 1) / split.chunks + 15) / 16 * 16);
+    a.chunk = std::max(16, ((n + split.chunks - 1) / split.chunks + 15) / 16 * 16);
     a.nchunks = std::max(1, (a.n_common + a.chunk - 1) / a.chunk);
     const int clusters = (a.nchunks + a.cluster - 1) / a.cluster;
     place_parts(a, clusters, scratch);
@@ -305,7 +311,7 @@ int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
                             attn_few_resident(rows), [&](const AttnArgs& b, dim3 grid) { return launch_attn_few(b, grid, s); });
     }
     if (a.D <= 128)
-        return launch_tiles(a, 128, 1.6, 1.6, scratch, s, attn_tc_resident(a.D), [&](const AttnArgs& b, dim3 grid) { return launch_attn_tc(b, grid, s); });
+        return launch_tiles(a, 128, 1.35, 1.35, scratch, s, attn_tc_resident(a.D), [&](const AttnArgs& b, dim3 grid) { return launch_attn_tc(b, grid, s); });
     const int rows = a.M * a.group, rt = attn_mma_row_tiles(rows);
     const int blocks = (rows + 16 * rt - 1) / (16 * rt), heads = a.G * blocks;
     const int tiles = std::max(1, (a.n_common + 63) / 64);
@@ -321,7 +327,7 @@ int launch_attention(AttnArgs a, void* scratch, cudaStream_t s) {
         const int most = *resident / heads;
         if (most > 2) {
             a.cluster = 8;
-            chunks = std::min({8 * most, tiles / 2, static_cast<int>(8 * max_parts(a.G, rows))});
+            chunks = std::min({8 * most, tiles / 2, static_cast<int>(8 * max_parts(a.G, rows, a.D))});
         }
     }
     a.chunk = std::max(64, ((a.n_common + chunks - 1) / chunks + 15) / 16 * 16);

@@ -88,23 +88,27 @@ struct AttnMaps {
 // The tiles of one chunk: its common rows in runs of up to `tile` rows that do
 // not cross a segment's end.
 struct AttnWalk {
-    int pos, end, seg;
+    int pos, end, seg, first, stop;  // first, stop: the segment's run, read when pos gets there
     __device__ __forceinline__ AttnWalk(const AttnArgs& a, int c)
-        : pos(min(c * a.chunk, a.n_common)), end(min(pos + a.chunk, a.n_common)), seg(0) {}
+        : pos(min(c * a.chunk, a.n_common)), end(min(pos + a.chunk, a.n_common)), seg(0), first(0), stop(0) {}
     __device__ __forceinline__ int count(const AttnArgs& a, int tile) const {
         int n = 0, at = pos;
         for (int s = 0; at < end; ++s) {
-            const int stop = min(end, a.seg_end[s]);
-            if (stop > at) n += (stop - at + tile - 1) / tile, at = stop;
+            const int upto = min(end, a.seg_end[s]);
+            if (upto > at) n += (upto - at + tile - 1) / tile, at = upto;
         }
         return n;
     }
     // The next tile's rows (it must exist), their segment and first row there.
     __device__ __forceinline__ int next(const AttnArgs& a, int tile, int& s, int& row) {
-        while (pos >= a.seg_end[seg]) ++seg;
+        if (pos >= stop) {
+            while (pos >= a.seg_end[seg]) ++seg;
+            first = seg == 0 ? 0 : a.seg_end[seg - 1];
+            stop = min(end, a.seg_end[seg]);
+        }
         s = seg;
-        row = pos - (seg == 0 ? 0 : a.seg_end[seg - 1]);
-        const int n = min(tile, min(end, a.seg_end[seg]) - pos);
+        row = pos - first;
+        const int n = min(tile, stop - pos);
         pos += n;
         return n;
     }

@@ -43,8 +43,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -63,6 +66,15 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
     float2 v;
     asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
     return v;
+}
+// `bytes` of this block's shared memory to another's, whose barrier counts them.
+__device__ __forceinline__ void copy_to_block(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 // 2^(m - M) of a partial result with maximum m, 0 where it has no rows.
 __device__ __forceinline__ float share(float m, float M) { return m == kNegInf ? 0.f : ex2(m - M); }
@@ -192,6 +204,50 @@ __device__ __forceinline__ void join_cluster(const AttnArgs& a, int tid, int c, 
             s.w = fmaf(f, s.w, fo * __shfl_xor_sync(0xffffffffu, s.w, o));
         }
         if (!real || sub != 0) continue;
+        if (final) {
+            const float inv = __fdividef(1.f, l);  // l is between 2^-10 and 2^46: a step or two off
+            float4 y = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+            if (a.gate) {
+                y.x = __fdividef(y.x, 1.f + __expf(-z.x));
+                y.y = __fdividef(y.y, 1.f + __expf(-z.y));
+                y.z = __fdividef(y.z, 1.f + __expf(-z.z));
+                y.w = __fdividef(y.w, 1.f + __expf(-z.w));
+            }
+            *reinterpret_cast<float4*>(a.out + row * a.D + d) = y;
+        } else {
+            const int64_t slot = static_cast<int64_t>(c / n) * a.M * a.H + row;
+            *reinterpret_cast<float4*>(a.part_o + slot * a.D + d) = s;
+            if (d == 0) a.part_ml[slot] = make_float2(M, l);
+        }
+    }
+}
+
+// The cluster's result from what its blocks have copied into this one's `out`:
+// of n blocks, rank b's rows [rank R / n, (rank + 1) R / n) at row b R / n, each
+// DP outputs, the maximum and the sum.  Every element is joined and written
+// out, final or as a part.
+template <int DP, int STRIDE, int R, int THREADS>
+__device__ __forceinline__ void merge_cluster(const AttnArgs& a, int tid, int c, int g, int r0, int rows, const float* out) {
+    const int n = a.cluster, rank = n > 1 ? static_cast<int>(cluster_rank()) : 0, per = R / n;
+    const bool final = gridDim.x == static_cast<unsigned>(n);
+    for (int x = tid; x < per * (DP / 4); x += THREADS) {
+        const int own = x / (DP / 4), d = x % (DP / 4) * 4, r = r0 + rank * per + own, i = r / a.group;
+        if (r >= rows || d >= a.D) continue;
+        const int64_t row = static_cast<int64_t>(i) * a.H + g * a.group + r - i * a.group;
+        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (final && a.gate) z = __ldcg(reinterpret_cast<const float4*>(a.gate + row * a.D + d));
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f, M = kNegInf;
+        const float* p = out + own * STRIDE;
+#pragma unroll 2
+        for (int b = 0; b < n; ++b, p += per * STRIDE) {
+            const float2 w = *reinterpret_cast<const float2*>(p + DP);
+            const float4 v = lds_float4(p + d);
+            const float mn = fmaxf(M, w.x), f = share(M, mn), fb = share(w.x, mn);
+            M = mn;
+            l = fmaf(fb, w.y, l * f);
+            s = make_float4(fmaf(fb, v.x, s.x * f), fmaf(fb, v.y, s.y * f), fmaf(fb, v.z, s.z * f), fmaf(fb, v.w, s.w * f));
+        }
         if (final) {
             const float inv = __fdividef(1.f, l);  // l is between 2^-10 and 2^46: a step or two off
             float4 y = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);

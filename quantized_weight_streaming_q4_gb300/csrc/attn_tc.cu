@@ -6,13 +6,15 @@
 //   S = Q K^T  (tcgen05.mma, A = Q in TMEM, B = K in shared memory)
 //   p = 2^(S - m + 14), written over S in TMEM as the next product's A operand
 //   O = P V    (B = V as it lies in the cache: keys along K, N contiguous)
-// Even and odd tiles are two independent softmax streams, one warpgroup each:
-// a thread owns a query row, holds its maximum, sum and output (128 binary32
-// registers), and nothing passes between lanes.  While one stream's
+// Even and odd tiles are two independent softmax streams, one warpgroup each: a
+// thread owns a query row of its tiles, whose p are relative to the tile's own
+// maximum, so a stream depends on nothing but its scores, and nothing passes
+// between lanes.  A third warpgroup holds the rows' outputs (128 binary32
+// registers a thread) and adds each tile's with its share.  While one stream's
 // exponentials run, the tensor core works for the other.  Every O tile is a
-// fresh accumulator that the thread adds to its registers: the tensor core's
-// additions truncate, and a long chain of them drifts (8.4e-6 of the result
-// after 3,456 keys on one accumulator; 8 steps do not show).
+// fresh accumulator added in registers: the tensor core's additions truncate,
+// and a long chain of them drifts (8.4e-6 of the result after 3,456 keys on one
+// accumulator; 8 steps do not show).
 //
 // Precision as in attn_mma.cu: q and p are each two binary16 parts, so both
 // products run twice, low parts first.
@@ -20,8 +22,14 @@
 // Warps: 0 issues the matrix products, 1 and 2 the TMA loads of K and of V
 // (128-byte swizzle: K with d contiguous along the product's K, V along its
 // N); 4-7 and 8-11 are the two streams, which also store the rows whose
-// visibility differs.  K and V wait for their buffers apart: one thread for
-// both held a free K buffer back behind V's.
+// visibility differs; 12-15 the outputs.  K and V wait for their buffers apart:
+// one thread for both held a free K buffer back behind V's.  The registers are
+// split 40 : 144 : 144 : 184 a thread; a stream that held all 128 scores of its
+// row spilled (83 us below).
+//
+// Bound: the tensor pipe, 32 products of 64 cycles a tile, 2,050 of about 2,500
+// cycles (16 rows, 130,815 rows: 56 us); for short caches what comes before the
+// first product and behind the last (16 rows, 2,048 rows: 12 us).
 #include <algorithm>
 
 #include "attn.cuh"
@@ -32,21 +40,21 @@
 namespace muser {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kTile = 128;
 constexpr uint32_t kTmemCols = 512, kColO = 256, kColQ = 384;  // S0, S1 at 0 and 128
 
 template <int DP>
 struct Layout {
     static constexpr uint32_t kItem = kTile * DP * 2;  // a K or a V tile
-    static constexpr uint32_t kOutStride = DP + 4;     // floats
-    static constexpr uint32_t kOutOff = 4 * kItem;     // behind K0, K1, V0, V1: q, later the output
-    static constexpr uint32_t kMlOff = kOutOff + 128 * kOutStride * 4;
-    static constexpr uint32_t kMl2Off = kMlOff + 128 * 8;
-    static constexpr uint32_t kBarOff = kMl2Off + 128 * 8;
+    static constexpr uint32_t kOutStride = DP + 4;     // floats: q, or outputs with their row's maximum and sum
+    static constexpr uint32_t kOutOff = 4 * kItem;     // behind K0, K1, V0, V1: q, later the cluster's outputs
+    static constexpr uint32_t kHalfOff = kOutOff + 128 * kOutStride * 4;  // float[2][128]
+    static constexpr uint32_t kStatOff = kHalfOff + 128 * 8;  // float2[4][128]: four tiles' maxima and sums
+    static constexpr uint32_t kBarOff = kStatOff + 4 * 128 * 8;
     static constexpr uint32_t kBytes = kBarOff + 256;
 };
-enum Bar { kKFull = 0, kVFull = 2, kVEmpty = 4, kSFull = 6, kPFull = 8, kOFull = 10, kOFree = 12, kQReady = 13, kRagged = 14, kBars = 15 };
+enum Bar { kKFull = 0, kVFull = 2, kVEmpty = 4, kSFull = 6, kPFull = 8, kOFull = 10, kQReady = 12, kRagged = 13, kJoin = 14, kBars = 15 };
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps) {
@@ -61,12 +69,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * 128;
     const int rows = a.M * a.group;
     // tile 0 of the last chunk holds the ragged rows; the common ones follow
-    AttnWalk walk(a, c);
     const int ragged = c == a.nchunks - 1 ? 1 : 0, nragged = a.n_edge + a.M;
-    const int ntiles = ragged + walk.count(a, kTile);
-    auto next_tile = [&](int t, int& s, int& row) { return t < ragged ? nragged : walk.next(a, kTile, s, row); };
 
     pdl_launch_dependents();
+    if (warp == 3) touch_args(a, lane);
+    if (warp < 3 && lane == 0 && a.nseg > 0) prefetch_map(warp == 1 ? &maps.k[0] : &maps.v[0]);
     // q and the ragged rows: coalesced loads of the streams, all in flight
     // together and before the block's set-up, then through shared memory.
     // (Asynchronous 16-byte copies of q moved 12 bytes a clock, 512-byte bulk
@@ -76,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     float4 q4[kQ];
     constexpr int kEach = 2 * 32 * (DP / 8) / 256;
     uint4 x[kEach];
-    if (warp >= 4) {
+    if (warp >= 4 && warp < 12) {
         pdl_wait();  // no global access before this
         // row r0 + r of the block: tree row i, head j of the group
         int i = (r0 + q0) / a.group, j = r0 + q0 - i * a.group;
@@ -104,33 +111,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             mbar_init(&bar[kVFull + i], 1);
             mbar_init(&bar[kVEmpty + i], 1);
             mbar_init(&bar[kSFull + i], 1);
-            mbar_init(&bar[kPFull + i], 128);
-            mbar_init(&bar[kOFull + i], 1);  // one per stream: a stream may ask before the other's is done
+            mbar_init(&bar[kPFull + i], 256);  // the stream's p, and the output tile before is read
+            mbar_init(&bar[kOFull + i], 1);
         }
-        mbar_init(&bar[kOFree], 128);
         mbar_init(&bar[kQReady], 256);
         mbar_init(&bar[kRagged], 256);
+        mbar_init(&bar[kJoin], 1);
         *flags = 0;
         fence_mbar_init();
+        if (a.cluster > 1) mbar_arrive_expect_tx(&bar[kJoin], 128 * L::kOutStride * 4);
     }
     if (warp == 0) {
         tmem_alloc(tmem_slot, kTmemCols);
     }
-    if (warp < 4) pdl_wait();
+    if (warp < 4 || warp >= 12) pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (warp >= 12) mbar_arrive(&bar[kPFull]);  // no output tile before the first
+    AttnWalk walk(a, c);
+    const int ntiles = ragged + walk.count(a, kTile);
+    auto next_tile = [&](int t, int& s, int& row) { return t < ragged ? nragged : walk.next(a, kTile, s, row); };
     constexpr uint32_t tmem = 0;  // the address of an allocation of all columns
     bool ok = *tmem_slot == tmem;
     auto wait = [&](int b, int phase) {
         if (ok) ok = mbar_wait_bounded(&bar[b], static_cast<uint32_t>(phase & 1), a.status, kDevStatusWaitTimeout);
     };
-    float2* ml = reinterpret_cast<float2*>(smem + L::kMlOff);
-    float2* ml2 = reinterpret_cast<float2*>(smem + L::kMl2Off);
+    float2* stat = reinterpret_cast<float2*>(smem + L::kStatOff);
     float* out = reinterpret_cast<float*>(smem + L::kOutOff);
 
     if (warp < 4) {
         set_regs_down<40>();
+        if (a.cluster > 1) cluster_arrive();
         if (warp == 0) {
             // ------------------------------------------- matrix products
             // The whole warp runs the loop and one thread issues: under `lane ==
@@ -143,8 +155,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     const int s = t & 1;
                     int sg, row;
                     keys[s] = (next_tile(t, sg, row) + 15) & ~15;
-                    wait(kKFull + s, t >> 1);
-                    if (!ok) return;
                     tc_fence_after();
                     const uint32_t id = idesc(static_cast<uint32_t>(keys[s]), false, false), d = tmem + s * 128, q = tmem + kColQ;
                     const uint64_t kd = desc_swizzle128(base + s * L::kItem, 16, 1024);
@@ -159,14 +169,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     }
                     __syncwarp();
                 };
-                wait(kQReady, 0);
-                tc_fence_after();
-                for (int t = 0; t < 2 && t < ntiles && ok; ++t) scores(t);
-                for (int t = 0; t < ntiles && ok; ++t) {
+                // Two waits at once, half of the lanes each.
+                auto wait_both = [&](int b0, int phase0, int b1, int phase1) {
+                    wait(lane & 1 ? b1 : b0, lane & 1 ? phase1 : phase0);
+                    ok = __all_sync(0xffffffffu, ok);
+                };
+                wait_both(kQReady, 0, kKFull, 0);
+                if (ok) scores(0);
+                wait_both(kVFull, 0, ntiles > 1 ? kKFull + 1 : kVFull, 0);
+                if (ok && ntiles > 1) scores(1);
+    #pragma unroll 1
+            for (int t = 0; t < ntiles && ok; ++t) {
                     const int s = t & 1;
-                    wait(kPFull + s, t >> 1);
-                    wait(kVFull + s, t >> 1);
-                    if (t > 0) wait(kOFree, t - 1);
+                    wait(kPFull + s, t >> 1);  // and the output tile before is read
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t id = idesc(DP, false, true), d = tmem + kColO, p = tmem + s * 128;
@@ -184,7 +199,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         mma_commit(&bar[kVEmpty + s]);
                     }
                     __syncwarp();
-                    if (t + 2 < ntiles) scores(t + 2);
+                    // The queue holds about 330 cycles of products: what the warp
+                    // does between them has to take less (a wait that is over takes
+                    // 180).
+                    if (t + 2 < ntiles) {
+                        wait_both(kKFull + s, (t + 2) >> 1, kVFull + (s ^ 1), (t + 1) >> 1);
+                        if (ok) scores(t + 2);
+                    } else if (t + 1 < ntiles) {
+                        wait(kVFull + (s ^ 1), (t + 1) >> 1);
+                    }
                 }
             }
         } else {
@@ -216,175 +239,211 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
         }
         __syncwarp();
-        // This warpgroup has 40 registers a thread: it shares no code with the
-        // streams from here on, only the barriers.
+        // This warpgroup has 56 registers a thread: it shares no code with the
+        // others from here on, only the barriers.
         tc_fence_before();
-        __syncthreads_and(ok);
+        if (a.cluster > 1) {
+            cluster_wait();
+            cluster_sync();
+        } else {
+            __syncthreads();
+        }
         if (warp == 0) {
             tc_fence_after();
             tmem_free(tmem, kTmemCols);
         }
-        if (a.cluster > 1) {
-            cluster_sync();
-            cluster_sync();
-        }
     } else {
-        // ------------------------------------------------------- the streams
-        set_regs_up<232>();
-        const int w = (warp - 4) >> 2, row = tid & 127;  // stream, query row = TMEM lane
+        const int row = tid & 127;  // query row = TMEM lane
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-#pragma unroll
-        for (int u = 0; u < kQ; ++u) sts_float4(out + (q0 + u * kStep) * L::kOutStride + qd, q4[u]);
-        if (ragged) {  // stored as tile 0; a value that is not finite becomes 0 and is noted
-#pragma unroll
-            for (int u = 0; u < kEach; ++u) {
-                const int y = u * 256 + tid - 128, v = u >= kEach / 2 ? 1 : 0, r = y / (DP / 8) - v * 32, p = y % (DP / 8);
-                if (not_finite8(x[u])) {
-                    atomicOr(flags, 1u << r);
-                    x[u] = make_uint4(0, 0, 0, 0);
-                }
-                sts_uint4(smem + v * 2 * L::kItem + piece<kTile>(r, p), x[u]);
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&bar[kRagged]);
-        }
-        named_barrier_sync(1, 256);
-        // a thread takes half a row, the row's largest element from both
-        float mx = 0.f;
-#pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-            q4[i] = lds_float4(out + row * L::kOutStride + w * (DP / 2) + i * 4);
-            mx = fmaxf(fmaxf(mx, fmaxf(fabsf(q4[i].x), fabsf(q4[i].y))), fmaxf(fabsf(q4[i].z), fabsf(q4[i].w)));
-        }
-        float* half = reinterpret_cast<float*>(ml);  // [2][128]
-        half[w * 128 + row] = mx;
-        named_barrier_sync(1, 256);
-        mx = fmaxf(mx, half[(w ^ 1) * 128 + row]);
-        const int e = min(100, max(-100, ((__float_as_int(mx * fabsf(a.scale_log2)) >> 23) & 0xff) - 127)) - 7;
-        const float qscale = a.scale_log2, up = __int_as_float((127 - e) << 23), down = __int_as_float((127 + e) << 23);
-#pragma unroll
-        for (int h = 0; h < DP / 64; ++h) {  // 32 elements: 16 columns of the high parts and 16 of the low ones
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 f = q4[h * 8 + i];
-                split2(f.x * qscale * up, f.y * qscale * up, hi[2 * i], lo[2 * i]);
-                split2(f.z * qscale * up, f.w * qscale * up, hi[2 * i + 1], lo[2 * i + 1]);
-            }
-            tmem_st16(mine + kColQ + w * (DP / 4) + h * 16, hi);
-            tmem_st16(mine + kColQ + DP / 2 + w * (DP / 4) + h * 16, lo);
-        }
-        tc_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bar[kQReady]);
-
         const uint32_t mask = r0 + row < rows ? a.mask[(r0 + row) / a.group] : 0u;
-        float m = kNegInf, l = 0.f;
-        float o[DP];
+        if (warp < 12) {
+            set_regs_up<144>();
+            // --------------------------------------------------- the streams
+            const int w = (warp - 4) >> 2;
 #pragma unroll
-        for (int d = 0; d < DP; ++d) o[d] = 0.f;
-        for (int t = 0; t < ntiles && ok; ++t) {
-            int sg, srow;
-            const int real = next_tile(t, sg, srow), chunks = (real + 31) >> 5;
-            if ((t & 1) != w) continue;
-            const uint32_t scol = mine + w * 128;
-            // bit j of seen(c): this row sees key 32 c + j
-            auto seen = [&](int ch) {
-                if (t < ragged) return mask;
-                const int left = real - ch * 32;
-                return left >= 32 ? 0xffffffffu : (1u << left) - 1u;
-            };
-            wait(kSFull + w, t >> 1);
-            if (!ok) break;
-            tc_fence_after();
-            // the row's maximum: four chains, the next 32 columns under way
-            float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-            for (int ch = 0; ch < chunks; ++ch) {
-                float s[32];
-                tmem_ld32(scol + ch * 32, s);
-                const uint32_t see = seen(ch);
-                tc_wait_ld(s);
-                if (see != 0xffffffffu) {
+            for (int u = 0; u < kQ; ++u) sts_float4(out + (q0 + u * kStep) * L::kOutStride + qd, q4[u]);
+            if (ragged) {  // stored as tile 0; a value that is not finite becomes 0 and is noted
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) s[j] = (see >> j) & 1u ? s[j] : kNegInf;
+                for (int u = 0; u < kEach; ++u) {
+                    const int y = u * 256 + tid - 128, v = u >= kEach / 2 ? 1 : 0, r = y / (DP / 8) - v * 32, p = y % (DP / 8);
+                    if (not_finite8(x[u])) {
+                        atomicOr(flags, 1u << r);
+                        x[u] = make_uint4(0, 0, 0, 0);
+                    }
+                    sts_uint4(smem + v * 2 * L::kItem + piece<kTile>(r, p), x[u]);
                 }
-#pragma unroll
-                for (int j = 0; j < 32; j += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], fmaxf(s[j + k], s[j + k + 4]));
+                fence_proxy_async_smem();
+                mbar_arrive(&bar[kRagged]);
             }
-            const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            const float mn = fmaxf(m, tm * down);
-            const float al = m == kNegInf ? 0.f : ex2(m - mn);
-            m = mn;
-            const float off = mn == kNegInf ? 0.f : kOffset - mn;
-            // p: over the 32 columns read go, for each 16 keys, 8 columns of high
-            // parts and 8 of low ones, the operand of one product
-            float l0 = 0.f, l1 = 0.f;
-            for (int ch = 0; ch < chunks; ++ch) {
-                float s[32];
-                tmem_ld32(scol + ch * 32, s);
-                const uint32_t see = seen(ch);
-                tc_wait_ld(s);
-                uint32_t p[32];
-                if (see != 0xffffffffu) {
+            named_barrier_sync(1, 256);
+            // a thread takes half a row, the row's largest element from both
+            float mx = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) s[j] = (see >> j) & 1u ? s[j] : kNegInf;
-                }
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const float p0 = ex2(fmaf(s[j], down, off)), p1 = ex2(fmaf(s[j + 1], down, off));
-                    l0 += p0;
-                    l1 += p1;
-                    split2(p0, p1, p[(j & 16) + (j & 15) / 2], p[(j & 16) + 8 + (j & 15) / 2]);
-                }
-                tmem_st32(scol + ch * 32, p);
+            for (int i = 0; i < DP / 8; ++i) {
+                q4[i] = lds_float4(out + row * L::kOutStride + w * (DP / 2) + i * 4);
+                mx = fmaxf(fmaxf(mx, fmaxf(fabsf(q4[i].x), fabsf(q4[i].y))), fmaxf(fabsf(q4[i].z), fabsf(q4[i].w)));
             }
-            l = fmaf(l, al, l0 + l1);
+            float* half = reinterpret_cast<float*>(smem + L::kHalfOff);
+            half[w * 128 + row] = mx;
+            named_barrier_sync(1, 256);
+            mx = fmaxf(mx, half[(w ^ 1) * 128 + row]);
+            const int e = min(100, max(-100, ((__float_as_int(mx * fabsf(a.scale_log2)) >> 23) & 0xff) - 127)) - 7;
+            const float qscale = a.scale_log2, up = __int_as_float((127 - e) << 23), down = __int_as_float((127 + e) << 23);
+#pragma unroll
+            for (int h = 0; h < DP / 64; ++h) {  // 32 elements: 16 columns of the high parts and 16 of the low ones
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 f = q4[h * 8 + i];
+                    split2(f.x * qscale * up, f.y * qscale * up, hi[2 * i], lo[2 * i]);
+                    split2(f.z * qscale * up, f.w * qscale * up, hi[2 * i + 1], lo[2 * i + 1]);
+                }
+                tmem_st16(mine + kColQ + w * (DP / 4) + h * 16, hi);
+                tmem_st16(mine + kColQ + DP / 2 + w * (DP / 4) + h * 16, lo);
+            }
             tc_wait_st();
             tc_fence_before();
-            mbar_arrive(&bar[kPFull + w]);
-            wait(kOFull + w, t >> 1);
-            if (!ok) break;
-            tc_fence_after();
+            mbar_arrive(&bar[kQReady]);
+            if (a.cluster > 1) cluster_arrive();  // q's place is free for the others' results
+
+            const uint32_t scol = mine + w * 128;
+#pragma unroll 1
+            for (int t = 0; t < ntiles && ok; ++t) {
+                int sg, srow;
+                const int real = next_tile(t, sg, srow), chunks = (real + 31) >> 5;
+                if ((t & 1) != w) continue;
+                wait(kSFull + w, t >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                // Columns [64 h, 64 h + 64) of the scores, -infinity where this
+                // row does not see the key.  More at once did not fit the registers.
+                float s[2][32];
+                auto load = [&](int h) {
+                    if (real == kTile && t >= ragged) {
+                        tmem_ld32(scol + h * 64, s[0]);
+                        tmem_ld32(scol + h * 64 + 32, s[1]);
+                        tc_wait_ld(s[0]);
+                        tc_wait_ld(s[1]);
+                        return;
+                    }
 #pragma unroll
-            for (int ch = 0; ch < DP / 32; ++ch) {
-                float s[32];
-                tmem_ld32(mine + kColO + ch * 32, s);
-                tc_wait_ld(s);
+                    for (int k = 0; k < 2; ++k) {
+                        const int ch = 2 * h + k, left = min(32, max(0, real - ch * 32));
+                        const uint32_t see = t < ragged ? (ch == 0 ? mask : 0u) : left == 32 ? 0xffffffffu : (1u << left) - 1u;
+                        if (ch < chunks) tmem_ld32(scol + ch * 32, s[k]);
+                        tc_wait_ld(s[k]);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[ch * 32 + j] = fmaf(o[ch * 32 + j], al, s[j]);
+                        for (int j = 0; j < 32; ++j) s[k][j] = (see >> j) & 1u ? s[k][j] : kNegInf;
+                    }
+                };
+                float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll 1
+                for (int h = 1; h >= 0; --h) {
+                    load(h);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) top[q] = fmaxf(top[q], fmaxf(s[k][j + q], s[k][j + q + 4]));
+                }
+                const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * down;
+                const float off = m == kNegInf ? 0.f : kOffset - m;
+                // p: over the 32 columns read go, for each 16 keys, 8 columns of high
+                // parts and 8 of low ones, the operand of one product
+                float l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if (2 * h >= chunks) break;
+                    if (h == 1) load(1);  // the first half is still here
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (2 * h + k >= chunks) break;
+                        uint32_t p[32];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float p0 = ex2(fmaf(s[k][j], down, off)), p1 = ex2(fmaf(s[k][j + 1], down, off));
+                            l0 += p0;
+                            l1 += p1;
+                            split2(p0, p1, p[(j & 16) + (j & 15) / 2], p[(j & 16) + 8 + (j & 15) / 2]);
+                        }
+                        tmem_st32(scol + h * 64 + k * 32, p);
+                    }
+                }
+                // Read before tile t is: S(t) came after P V of t - 2, that after the
+                // output of t - 3, hence after the use of t - 4's.
+                stat[(t & 3) * 128 + row] = make_float2(m, l0 + l1);
+                tc_wait_st();
+                tc_fence_before();
+                mbar_arrive(&bar[kPFull + w]);
             }
-            tc_fence_before();
-            mbar_arrive(&bar[kOFree]);
-        }
-        // the two streams' results joined in the output's place
-        named_barrier_sync(1, 256);  // q is no longer read
-        if (w == 1) {
-            ml2[row] = make_float2(m, l);
+            if (a.cluster > 1) cluster_wait();
+            else named_barrier_sync(2, 384);
+        } else {
+            // ---------------------------------------------------- the output
+            set_regs_up<184>();
+            if (a.cluster > 1) cluster_arrive();
+            float m = kNegInf, l = 0.f;
+            float o[DP];
 #pragma unroll
-            for (int d = 0; d < DP; d += 4) sts_float4(out + row * L::kOutStride + d, make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]));
-        }
-        named_barrier_sync(1, 256);
-        if (w == 0) {
-            const float2 other = ml2[row];
-            const float M = fmaxf(m, other.x), f = share(m, M), f2 = share(other.x, M);
-            l = fmaf(l, f, other.y * f2);
-            if (mask & *flags) l = NAN;  // this row sees a ragged row that is not finite
+            for (int d = 0; d < DP; ++d) o[d] = 0.f;
+#pragma unroll 1
+            for (int t = 0; t < ntiles && ok; ++t) {
+                const int s = t & 1;
+                wait(kPFull + s, t >> 1);
+                if (!ok) break;
+                const float2 tile = stat[(t & 3) * 128 + row];
+                const float mn = fmaxf(m, tile.x), f = share(m, mn), ft = share(tile.x, mn);
+                m = mn;
+                l = fmaf(l, f, tile.y * ft);
+                wait(kOFull + s, t >> 1);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-            for (int d = 0; d < DP; d += 4) {
-                const float4 v = lds_float4(out + row * L::kOutStride + d);
-                sts_float4(out + row * L::kOutStride + d,
-                           make_float4(fmaf(o[d], f, v.x * f2), fmaf(o[d + 1], f, v.y * f2), fmaf(o[d + 2], f, v.z * f2),
-                                       fmaf(o[d + 3], f, v.w * f2)));
+                for (int ch = 0; ch < DP / 32; ++ch) {
+                    float x[32];
+                    tmem_ld32(mine + kColO + ch * 32, x);
+                    tc_wait_ld(x);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[ch * 32 + j] = fmaf(o[ch * 32 + j], f, x[j] * ft);
+                }
+                tc_fence_before();
+                if (t + 1 < ntiles) mbar_arrive(&bar[kPFull + (s ^ 1)]);
             }
-            ml[row] = make_float2(M, l);
+            // no wait ran out, and no ragged row that this row sees is not finite
+            if (!ok || (mask & *flags)) l = NAN;
+            // To the K and V tiles' place, and from there to the blocks that join
+            // the rows.  (Reading the others' shared memory took 6,000 cycles in
+            // a cluster of 4, storing there as long.)
+            float* to = a.cluster > 1 ? reinterpret_cast<float*>(smem) : out;
+            if (a.cluster > 1) cluster_wait();  // the others' q has been read
+            else named_barrier_sync(2, 384);
+            *reinterpret_cast<float2*>(to + row * L::kOutStride + DP) = make_float2(m, l);
+#pragma unroll
+            for (int d = 0; d < DP; d += 4) sts_float4(to + row * L::kOutStride + d, make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]));
+            if (a.cluster > 1) {
+                fence_proxy_async_smem();
+                named_barrier_sync(3, 128);
+                if (row < a.cluster) {
+                    const uint32_t bytes = 128 / a.cluster * L::kOutStride * 4;
+                    copy_to_block(map_rank(base + L::kOutOff + cluster_rank() * bytes, row), base + row * bytes, bytes,
+                                  map_rank(base + L::kBarOff + kJoin * 8, row));
+                }
+            }
         }
         tc_fence_before();
-        ok = __syncthreads_and(ok);
-        if (a.cluster > 1) cluster_sync();
-        if (ok) join_cluster<DP, L::kOutStride, 128, 256, 1>(a, tid - 128, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff);
-        if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
+        if (a.cluster > 1) {
+            wait(kJoin, 0);
+            __syncwarp();
+            cluster_arrive();
+        } else {
+            __syncthreads();
+        }
+        merge_cluster<DP, L::kOutStride, 128, 384>(a, tid - 128, c, g, r0, rows, out);
+        if (a.cluster > 1) {
+            __syncwarp();
+            cluster_wait();  // nobody leaves while copies read its shared memory
+        }
     }
 }
 
