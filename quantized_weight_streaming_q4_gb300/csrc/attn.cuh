@@ -46,9 +46,9 @@ struct AttnArgs {
     int32_t edge0;    // rows of edge[0]
     int32_t n_edge;
     uint32_t mask[MUSER_MAX_M];
-    // split: chunk c of the common rows is [c * chunk, min((c + 1) * chunk,
-    // n_common)); the ragged rows belong to the last chunk
-    int32_t chunk, nchunks;
+    // split: chunk c of the common rows is [c * chunk - shift, (c + 1) * chunk -
+    // shift) within 0..n_common; the ragged rows belong to the last chunk
+    int32_t chunk, nchunks, shift;
     int32_t cluster;  // blocks of a cluster (attn_mma.cu); chunks behind nchunks are empty
     float* part_o;   // [parts][M*H][D]  unnormalised sums, one part per chunk or cluster
     float2* part_ml; // [parts][M*H]     maximum (base 2) and sum
@@ -90,7 +90,8 @@ struct AttnMaps {
 struct AttnWalk {
     int pos, end, seg, first, stop;  // first, stop: the segment's run, read when pos gets there
     __device__ __forceinline__ AttnWalk(const AttnArgs& a, int c)
-        : pos(min(c * a.chunk, a.n_common)), end(min(pos + a.chunk, a.n_common)), seg(0), first(0), stop(0) {}
+        : pos(min(max(0, c * a.chunk - a.shift), a.n_common)), end(min((c + 1) * a.chunk - a.shift, a.n_common)), seg(0),
+          first(0), stop(0) {}
     __device__ __forceinline__ int count(const AttnArgs& a, int tile) const {
         int n = 0, at = pos;
         for (int s = 0; at < end; ++s) {

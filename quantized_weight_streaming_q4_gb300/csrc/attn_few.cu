@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
     if (gridDim.x == 1) return;
     if (a.cluster > 1) cluster_sync();
     if (ok) join_cluster<128, L::kOutStride, R, L::kThreads, 8>(a, tid, c, g, r0, rows, base + L::kMlOff, base + L::kPOff);
-    if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
+    if (a.cluster > 1) cluster_leave();
 }
 
 // The kernel's attributes and resident clusters, once per device; null with

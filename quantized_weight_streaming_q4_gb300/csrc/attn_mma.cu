@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
     if (a.cluster > 1) cluster_sync();
     else __syncthreads();
     if (ok) join_cluster<DP, L::kOutStride, R, kThreads, 1>(a, tid, c, g, r0, rows, base + L::kMlOff, base + L::kOutOff);
-    if (a.cluster > 1) cluster_sync();  // nobody leaves while its shared memory is read
+    if (a.cluster > 1) cluster_leave();
 }
 
 // The kernel's attributes and its resident clusters of 8, once per device;

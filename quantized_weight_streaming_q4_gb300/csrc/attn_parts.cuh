@@ -76,6 +76,13 @@ __device__ __forceinline__ void copy_to_block(uint32_t dst, uint32_t src, uint32
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
+// The last barrier: nobody leaves while its shared memory is read.  What was
+// read has arrived (it was used), and nothing needs the release, which would
+// wait for the output's stores.
+__device__ __forceinline__ void cluster_leave() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    cluster_wait();
+}
 // 2^(m - M) of a partial result with maximum m, 0 where it has no rows.
 __device__ __forceinline__ float share(float m, float M) { return m == kNegInf ? 0.f : ex2(m - M); }
 
