@@ -81,6 +81,8 @@ class KvPlane(ctypes.Structure):
 def lib():
     """The loaded libmuser (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -150,25 +152,26 @@ def _qt(qtype) -> int:
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    try:
+        return t.data_ptr()
+    except AttributeError:  # an address or None (a call passes up to nine tensors)
+        if t is None or isinstance(t, int):
+            return t
+        raise
 
 
-_raw_stream = None
+_raw_stream = _device = None
 
 
 def _stream(stream) -> int | None:
-    global _raw_stream
+    global _raw_stream, _device
     if stream is None:
         if _raw_stream is None:
             import torch
             torch.cuda.init()
             # the current stream's handle without building a Stream object (3 us of a call)
-            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
-        return _raw_stream[0](_raw_stream[1]())
+            _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -389,14 +392,14 @@ def muser_kv_restore(plane: KvPlane, k_rows, v_rows, origin_logical: int, length
 
 def _ints(values):
     """A host int32 array from a sequence; None and c_int32 arrays pass through."""
-    if values is None or (isinstance(values, ctypes.Array) and values._type_ is ctypes.c_int32):
+    if values is None or getattr(values, "_type_", None) is ctypes.c_int32:
         return values
     return (ctypes.c_int32 * len(values))(*values)
 
 
 def _ptrs(values):
     """A host array of device pointers from a sequence; c_void_p arrays pass through."""
-    if isinstance(values, ctypes.Array) and values._type_ is ctypes.c_void_p:
+    if getattr(values, "_type_", None) is ctypes.c_void_p:
         return values
     return (ctypes.c_void_p * len(values))(*[_ptr(t) for t in values])
 
@@ -415,9 +418,9 @@ def muser_kv_tree_attention(plane: KvPlane, q, k, v, M: int, n_heads: int, out, 
     if parent is not None and len(parent) != M:
         raise ValueError("parent: one entry per row")
     _check("muser_kv_tree_attention",
-           lib().muser_kv_tree_attention(ctypes.byref(plane), None if sink is None else ctypes.byref(sink), _ptr(q),
-                                         _ptr(k), _ptr(v), _ptr(gate), M, n_heads, parent, window, n_sink, scale,
-                                         _ptr(out), _ptr(scratch), scratch_bytes, _stream(stream)))
+           lib().muser_kv_tree_attention(plane, sink, _ptr(q), _ptr(k), _ptr(v), None if gate is None else _ptr(gate), M,
+                                         n_heads, parent, window, n_sink, scale, _ptr(out), _ptr(scratch), scratch_bytes,
+                                         _stream(stream)))
 
 
 def muser_tree_verify_scratch_bytes(vocab: int, M: int) -> int:
@@ -432,7 +435,7 @@ def muser_tree_verify(target, draft, tokens, parent, M: int, vocab: int, tempera
     if parent is not None and len(parent) != M:
         raise ValueError("parent: one entry per row")
     _check("muser_tree_verify",
-           lib().muser_tree_verify(_ptr(target), _ptr(draft), _ptr(tokens), parent, M, vocab, temperature,
+           lib().muser_tree_verify(_ptr(target), None if draft is None else _ptr(draft), _ptr(tokens), parent, M, vocab, temperature,
                                    _ptr(uniform), _ptr(result), _ptr(scratch), scratch_bytes, _stream(stream)))
 
 
