@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
     const int w = (warp - 4) >> 2, th = tid & 127, id = 1 + w;  // 16 rows from 16 w on; key, later element
     const int qr = th >> 3, d0 = (th & 7) * 16;
     float4 x4[4];
-    uint4 y[8];
+    RaggedRaw raw[8];
     float4 ks[4];
     float vs = 0.f;
     if (warp >= 4) {
@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 const int rr = (u & 3) * 8 + (th >> 4), p = th & 15;
-                y[u] = make_uint4(0, 0, 0, 0);
-                if (rr < nragged && p * 8 < a.D) y[u] = attn_ragged8(a, g, rr, p * 8, u >= 4);
+                raw[u] = RaggedRaw{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (rr < nragged && p * 8 < a.D) raw[u] = attn_ragged_load(a, g, rr, p * 8, u >= 4);
             }
         }
     }
@@ -333,11 +333,12 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const int rr = (u & 3) * 8 + (th >> 4), p = th & 15;
-                    if (not_finite8(y[u])) {
+                    uint4 y = attn_ragged_pack(a, rr, raw[u]);
+                    if (not_finite8(y)) {
                         atomicOr(flags, 1u << rr);
-                        y[u] = make_uint4(0, 0, 0, 0);
+                        y = make_uint4(0, 0, 0, 0);
                     }
-                    if (p < 8 || a.D > 64) sts_uint4(smem + (u >= 4 ? L::kVOff : 0u) + rt % kNS * kItem + piece<kTile>(rr, p), y[u]);
+                    if (p < 8 || a.D > 64) sts_uint4(smem + (u >= 4 ? L::kVOff : 0u) + rt % kNS * kItem + piece<kTile>(rr, p), y);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bar[kRagged]);

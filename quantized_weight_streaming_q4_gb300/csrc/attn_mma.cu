@@ -116,13 +116,22 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
     const int nragged = a.n_edge + a.M;
     uint4 kp[kEach], vp[kEach];
     if (ragged) {
+        RaggedRaw kr[kEach], vr[kEach];
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int x = tid + j * kThreads, r = x / kPieces, d = x % kPieces * 8;
+            if (r < nragged && d < a.D) {
+                kr[j] = attn_ragged_load(a, g, r, d, false);
+                vr[j] = attn_ragged_load(a, g, r, d, true);
+            }
+        }
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
             const int x = tid + j * kThreads, r = x / kPieces, d = x % kPieces * 8;
             kp[j] = vp[j] = make_uint4(0, 0, 0, 0);
             if (r < nragged && d < a.D) {
-                kp[j] = attn_ragged8(a, g, r, d, false);
-                vp[j] = attn_ragged8(a, g, r, d, true);
+                kp[j] = attn_ragged_pack(a, r, kr[j]);
+                vp[j] = attn_ragged_pack(a, r, vr[j]);
             }
         }
     }

@@ -86,16 +86,30 @@ __device__ __forceinline__ void cluster_leave() {
 // 2^(m - M) of a partial result with maximum m, 0 where it has no rows.
 __device__ __forceinline__ float share(float m, float M) { return m == kNegInf ? 0.f : ex2(m - M); }
 
-// Eight elements from d on of ragged row r, as binary16 (see attn_ragged).
-__device__ __forceinline__ uint4 attn_ragged8(const AttnArgs& a, int g, int r, int d, bool value) {
+// Eight elements from d on of ragged row r (see attn_ragged), as they lie in
+// memory: the loads of several go out before the first is packed, which waits
+// for it.
+struct RaggedRaw {
+    uint4 a, b;
+};
+__device__ __forceinline__ RaggedRaw attn_ragged_load(const AttnArgs& a, int g, int r, int d, bool value) {
+    RaggedRaw raw{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     if (r < a.n_edge) {
         const int e = r < a.edge0 ? 0 : 1;
         const AttnSeg& S = a.edge[e];
-        return __ldcg(reinterpret_cast<const uint4*>((value ? S.v : S.k) + g * S.head_stride + (r - (e ? a.edge0 : 0)) * S.row_stride + d));
+        raw.a = __ldcg(reinterpret_cast<const uint4*>((value ? S.v : S.k) + g * S.head_stride + (r - (e ? a.edge0 : 0)) * S.row_stride + d));
+    } else {
+        const uint4* p = reinterpret_cast<const uint4*>((value ? a.vt : a.kt) + (r - a.n_edge) * a.G * a.D + g * a.D + d);
+        raw.a = __ldcg(p);
+        raw.b = __ldcg(p + 1);
     }
-    const float4* p = reinterpret_cast<const float4*>((value ? a.vt : a.kt) + (r - a.n_edge) * a.G * a.D + g * a.D + d);
-    const float4 x = __ldcg(p), y = __ldcg(p + 1);
-    return make_uint4(pack_h2(x.x, x.y), pack_h2(x.z, x.w), pack_h2(y.x, y.y), pack_h2(y.z, y.w));
+    return raw;
+}
+// The same as binary16.
+__device__ __forceinline__ uint4 attn_ragged_pack(const AttnArgs& a, int r, const RaggedRaw& raw) {
+    if (r < a.n_edge) return raw.a;
+    auto two = [](uint32_t x, uint32_t y) { return pack_h2(__uint_as_float(x), __uint_as_float(y)); };
+    return make_uint4(two(raw.a.x, raw.a.y), two(raw.a.z, raw.a.w), two(raw.b.x, raw.b.y), two(raw.b.z, raw.b.w));
 }
 // Whether one of eight binary16 values is infinite or NaN.
 __device__ __forceinline__ bool not_finite8(uint4 v) {

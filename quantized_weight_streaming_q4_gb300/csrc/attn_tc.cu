@@ -85,6 +85,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     uint4 x[kEach];
     if (warp >= 4 && warp < 12) {
         pdl_wait();  // no global access before this
+        RaggedRaw raw[kEach];
+        auto ragged_at = [&](int u, int& r, int& p) {  // row and piece; of V where it returns true
+            const int y = u * 256 + tid - 128, v = u >= kEach / 2 ? 1 : 0;
+            r = y / (DP / 8) - v * 32;
+            p = y % (DP / 8);
+            return v != 0;
+        };
+        if (ragged) {
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                int r, p;
+                const bool v = ragged_at(u, r, p);
+                raw[u] = RaggedRaw{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (r < nragged && p * 8 < a.D) raw[u] = attn_ragged_load(a, g, r, p * 8, v);
+            }
+        }
         // row r0 + r of the block: tree row i, head j of the group
         int i = (r0 + q0) / a.group, j = r0 + q0 - i * a.group;
         const int skip = (a.H - a.group) * a.D;  // from one tree row's group to the next
@@ -99,9 +115,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (ragged) {
 #pragma unroll
             for (int u = 0; u < kEach; ++u) {
-                const int y = u * 256 + tid - 128, v = u >= kEach / 2 ? 1 : 0, r = y / (DP / 8) - v * 32, p = y % (DP / 8);
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (r < nragged && p * 8 < a.D) x[u] = attn_ragged8(a, g, r, p * 8, v != 0);
+                int r, p;
+                ragged_at(u, r, p);
+                x[u] = attn_ragged_pack(a, r, raw[u]);
             }
         }
     }
