@@ -249,8 +249,8 @@ int launch_generic(AttnArgs a, void* scratch, cudaStream_t s) {
 // one block per SM, `heads` K/V heads times row blocks): clusters of c blocks,
 // k of them a head.  One cluster joins its blocks' results itself; more leave
 // parts for a second kernel (2.7 us).  A tile takes a block `tile_us`, or
-// `tile_full_us` where all SMs share the memory's rate, and 5 us beside its
-// tiles; clusters beyond those that run at once wait for a turn (of 16 blocks
+// `tile_full_us` where all SMs share the memory's rate, and beside its tiles 5
+// us, or 3.5 where it joins no other; clusters beyond those that run at once wait for a turn (of 16 blocks
 // 7 clusters are resident).  Measured, one token, 16 K/V heads of 64, 2,048
 // rows: clusters of 16 in three turns 23.9 us, of 4 at once 11.2 us; 2 heads of
 // 128: one cluster of 16 a head 8.4 us (11.0 with parts), and over 32,768 rows
@@ -269,7 +269,7 @@ Split choose_split(int heads, int tiles, int parts, double tile_us, double tile_
             const int chunks = std::min(c * k, std::max(1, tiles)), clusters = (chunks + c - 1) / c;
             const int waves = (heads * clusters + most - 1) / most, per = (std::max(1, tiles) + chunks - 1) / chunks;
             const double busy = std::min(1.0, heads * chunks / 144.0);
-            const double us = waves * (5.0 + per * std::max(tile_us, tile_full_us * busy)) + (clusters > 1 ? 2.7 : 0.0);
+            const double us = waves * ((chunks > 1 ? 5.0 : 3.5) + per * std::max(tile_us, tile_full_us * busy)) + (clusters > 1 ? 2.7 : 0.0);
             if (us < least - 1e-9) {
                 least = us;
                 best = Split{c, chunks};
@@ -301,6 +301,7 @@ int launch_tiles(AttnArgs a, int R, double tile_us, double tile_full_us, void* s
     const int tiles = (a.chunk + 127) / 128, rows0 = lead_rows + std::max(0, tiles - lead) * 128;
     a.shift = lead == 0 ? 0 : std::min(std::max(0, a.chunk - rows0), lead * 128 - lead_rows);
     a.nchunks = std::max(1, (a.n_common + a.shift + a.chunk - 1) / a.chunk);
+    if (a.nchunks == 1) a.cluster = 1;  // nothing to join; else blocks without rows share in the join
     const int clusters = (a.nchunks + a.cluster - 1) / a.cluster;
     place_parts(a, clusters, scratch);
     MUSER_TRY(launch(a, dim3(static_cast<unsigned>(clusters * a.cluster), static_cast<unsigned>(a.G), static_cast<unsigned>(blocks))));
