@@ -49,7 +49,7 @@ struct AttnArgs {
     // split: chunk c of the common rows is [c * chunk - shift, (c + 1) * chunk -
     // shift) within 0..n_common; the ragged rows belong to the last chunk
     int32_t chunk, nchunks, shift;
-    int32_t cluster;  // blocks of a cluster (attn_mma.cu); chunks behind nchunks are empty
+    int32_t cluster;  // blocks of a cluster; chunks behind nchunks are empty
     float* part_o;   // [parts][M*H][D]  unnormalised sums, one part per chunk or cluster
     float2* part_ml; // [parts][M*H]     maximum (base 2) and sum
     unsigned* status;  // device status word

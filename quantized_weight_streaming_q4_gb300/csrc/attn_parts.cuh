@@ -1,4 +1,4 @@
-// attn_parts.cuh -- device code that the two matrix-product attention kernels
+// attn_parts.cuh -- device code that the matrix-product attention kernels
 // share: splitting binary32 values into two binary16 parts, the rows whose
 // visibility differs, and the joining of a cluster's partial results.
 #pragma once

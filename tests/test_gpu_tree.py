@@ -139,6 +139,18 @@ def test_attention_windows_and_sinks(H, kvh, D, M, n, cap, origin, window, n_sin
         Case(M, H, kvh, D, n, cap, origin, hm, window, n_sink, kind, sink_rows, gate=True, seed=2).to_device().call().check()
 
 
+@pytest.mark.parametrize("sink_rows", [1, 4, 60, 127, 128, 131])
+@pytest.mark.parametrize("M,n,H,kvh,D", [(1, 2048, 32, 2, 128), (5, 2048, 20, 5, 64), (16, 2048, 32, 2, 128), (16, 600, 32, 2, 128),
+                                         (1, 130, 32, 2, 128), (3, 260, 6, 2, 80), (1, 20000, 32, 2, 128), (16, 20000, 32, 2, 128)])
+def test_attention_short_runs_before_the_ring(sink_rows, M, n, H, kvh, D):
+    """First rows kept in a plane that wraps (two short runs), then a full ring that wraps."""
+    c = Case(M, H, kvh, D, n, n, 10 * n + 77, False, n, sink_rows, TWO, sink_rows, gate=True, seed=sink_rows)
+    rng = np.random.default_rng(sink_rows)
+    r, sk, sv = plane(rng, sink_rows + 3, kvh, D, sink_rows, 0, True, physical=sink_rows + 2)
+    c.sink = (r, sk, sv, True)
+    c.to_device().call().check()
+
+
 @pytest.mark.parametrize("n", [1024, 4097, 33000])
 @pytest.mark.parametrize("M,H,kvh,D", [(1, 32, 2, 128), (4, 32, 2, 128), (16, 32, 2, 128), (16, 16, 16, 64)])
 def test_attention_long(n, M, H, kvh, D):
