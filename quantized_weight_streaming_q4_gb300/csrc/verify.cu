@@ -22,7 +22,10 @@
 //
 // Bound: the rows' bytes (24 MB for 15 drafts over 202,048 tokens: 3.6 us),
 // then latency: a launch, two to four grid barriers of 1.5 us (0.2 us in a
-// cluster) and the loads behind them.
+// cluster) and the loads behind them.  Outside a graph a cooperative launch
+// takes 2.6 us more than another one (15 drafts, 202,048 tokens: 18.4 us, 15.8
+// as an ordinary launch), but only it makes the waiting safe beside other
+// kernels.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -38,7 +41,7 @@ constexpr int kRows = 2 * MUSER_MAX_M;
 constexpr int kVerifyTable = 128;
 constexpr int kMaxSlices = 256;  // of a row
 constexpr int kClusterBlocks = 16;
-constexpr int64_t kClusterVocab = 40000, kClusterLogits = 800000;
+constexpr int64_t kClusterVocab = 40000, kClusterLogits = 1000000;
 constexpr int kMaxBlocks = 160;  // 152 SMs; a lane of the warp that joins the blocks' sums takes 5
 constexpr float kMaxExponent = 32768.f;
 constexpr int kBad = 1 << 24;  // exponent mark of a slice that holds a NaN or an infinity
@@ -886,11 +889,12 @@ int launch_verify(const float* target, const float* draft, const int32_t* tokens
     a.ntarget = a.nrows;
     for (int i = 0; i < M && a.draft; ++i)
         if (inner[i]) a.row_node[a.draft_at[i] = a.nrows++] = i;
-    // Few logits: one cluster, whose barriers outweigh the other SMs.  Measured,
-    // 15 drafts in a binary tree: 10,000 tokens 10.9 us in a cluster, 14.0 on the
-    // grid; 32,768 14.4 and 15.1; 65,536 18.2 and 13.7.  A chain of 15, whose
-    // first pass reads twice the rows: 20,000 tokens 12.7 and 13.1, 32,768 13.7
-    // and 12.6.
+    // Few tokens: one cluster, whose barriers outweigh the other SMs.  Measured
+    // in a graph, 15 drafts in a binary tree: 10,000 tokens 10.9 us in a cluster,
+    // 14.0 on the grid; 32,768 14.4 and 15.1; 65,536 18.2 and 13.7.  A chain of
+    // 15, whose first pass reads twice the rows: 20,000 tokens 12.7 and 13.1,
+    // 32,768 13.7 and 12.6.  Outside a graph the cooperative launch adds to the
+    // grid's: the chain of 15, 32,768 tokens 13.5 and 14.6, 39,999 17.3 and 15.2.
     const bool cluster = !greedy && M > 1 && vocab <= kClusterVocab && a.nrows * vocab <= kClusterLogits;
     const int sms = cluster ? kClusterBlocks : std::min(sm_count(), kMaxBlocks);
     if (sms < 1) return set_error(MUSER_ERR_CUDA, "tree_verify: cannot read the SM count");
