@@ -1357,7 +1357,7 @@ int muser_kv_tree_commit(muser_kv_plane* planes, int n_planes, const float* cons
             return set_error(MUSER_ERR_INVALID_ARG, "%s: path[%d] = %d (rows 0..M-1, ascending)", fn, j, path[j]);
         a.path[j] = path[j];
     }
-    std::pair<uintptr_t, uintptr_t> span[2 * kCommitMaxPlanes];
+    std::pair<uintptr_t, uintptr_t> span[2 * kCommitMaxPlanes], ordered[2 * kCommitMaxPlanes];  // keys', then values'
     for (int i = 0; i < n_planes; ++i) {
         MUSER_TRY(check_plane(planes + i, fn));
         const muser_kv_plane& P = planes[i];
@@ -1378,13 +1378,15 @@ int muser_kv_tree_commit(muser_kv_plane* planes, int n_planes, const float* cons
         C.vec = C.head_dim % 8 == 0 && is_aligned(P.key, 16) && is_aligned(P.value, 16) && is_aligned(k[i], 16) &&
                 is_aligned(v[i], 16);
         const uintptr_t bytes = static_cast<uintptr_t>(P.capacity) * static_cast<uintptr_t>(P.kv_dim) * 2u;
-        span[2 * i] = {reinterpret_cast<uintptr_t>(P.key), reinterpret_cast<uintptr_t>(P.key) + bytes};
-        span[2 * i + 1] = {reinterpret_cast<uintptr_t>(P.value), reinterpret_cast<uintptr_t>(P.value) + bytes};
+        span[i] = {reinterpret_cast<uintptr_t>(P.key), reinterpret_cast<uintptr_t>(P.key) + bytes};
+        span[n_planes + i] = {reinterpret_cast<uintptr_t>(P.value), reinterpret_cast<uintptr_t>(P.value) + bytes};
     }
     if (n == 0) return MUSER_OK;
-    std::sort(span, span + 2 * n_planes);
+    for (auto* s : {span, span + n_planes})  // planes of one allocation come in order
+        if (!std::is_sorted(s, s + n_planes)) std::sort(s, s + n_planes);
+    std::merge(span, span + n_planes, span + n_planes, span + 2 * n_planes, ordered);
     for (int i = 1; i < 2 * n_planes; ++i)
-        if (span[i].first < span[i - 1].second)
+        if (ordered[i].first < ordered[i - 1].second)
             return set_error(MUSER_ERR_INVALID_ARG, "%s: two planes share memory", fn);
     MUSER_TRY(launch_kv_commit(a, as_stream(stream)));
     for (int i = 0; i < n_planes; ++i) {

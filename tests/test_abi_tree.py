@@ -135,6 +135,19 @@ def test_binding_checks_lengths(L):
     assert (plane.len, plane.origin_logical) == (100, 0)
 
 
+def test_commit_finds_planes_that_share_memory_in_any_order(L):
+    def plane(key, value):
+        return mu.KvPlane(key, value, 128, 100, 0, 0, 256, 128, 0, 0)   # 65,536 bytes each
+
+    S, B = 65536, FAKE * 16
+    for order in ([0, 1, 2], [2, 0, 1], [1, 2, 0]):
+        apart = [plane(B + 2 * S * i, B + 2 * S * i + S) for i in range(3)]
+        for bad in (plane(B + S * 2 + 16, B + S * 9), plane(B + S * 9, B + S * 3 - 16), plane(B + S * 9, B + S * 10 - 16)):
+            planes = [apart[i] for i in order] + [bad]
+            assert commit(L, planes)[0] == -1 and "share memory" in mu.muser_last_error(), (order, bad.key - B, bad.value - B)
+            assert commit(L, planes[::-1])[0] == -1
+
+
 def test_sizes_beyond_the_kernels_indexes_are_refused(L):
     far = mu.KvPlane(FAKE, FAKE * 2, 2048, 100, (1 << 62) + 1, 0, 256, 128, 0, 0)
     ring = mu.KvPlane(FAKE, FAKE * 2, 2048, 100, 0, 0, 256, 128, 0, 0)
