@@ -204,14 +204,15 @@ static int64_t max_parts(int64_t G, int64_t rows, int64_t D) {
 size_t attn_scratch_bytes(int64_t kv_dim, int64_t head_dim, int M, int n_heads) {
     const int64_t G = kv_dim / head_dim;
     const int64_t parts = max_parts(G, static_cast<int64_t>(M) * (n_heads / G), head_dim);
-    return (static_cast<size_t>(parts * M * n_heads * (head_dim + 2)) * 4u + 15u) / 16u * 16u;
+    return attn_part_layout(parts, static_cast<int64_t>(M) * n_heads, head_dim).bytes;
 }
 
 namespace {
 
 void place_parts(AttnArgs& a, int parts, void* scratch) {
-    a.part_o = static_cast<float*>(scratch);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(parts) * a.M * a.H * a.D);
+    a.part_ml = static_cast<float2*>(scratch);
+    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
+                                        attn_part_layout(parts, static_cast<int64_t>(a.M) * a.H, a.D).o);
 }
 
 int launch_combine(const AttnArgs& a, int parts, cudaStream_t s) {

@@ -55,6 +55,17 @@ struct AttnArgs {
     unsigned* status;  // device status word
 };
 
+// Where the parts lie in the scratch memory (bytes; it is 16-byte aligned): the
+// (maximum, sum) pairs first, then the sums from the next 16-byte boundary on.
+// Behind the sums, whose number may be odd, the pairs would miss their own 8.
+struct AttnPartLayout {
+    size_t o, bytes;
+};
+constexpr AttnPartLayout attn_part_layout(int64_t parts, int64_t rows, int64_t D) {
+    const size_t o = (static_cast<size_t>(parts * rows) * 8u + 15u) / 16u * 16u;
+    return AttnPartLayout{o, o + (static_cast<size_t>(parts * rows * D) * 4u + 15u) / 16u * 16u};
+}
+
 __device__ __forceinline__ const uint16_t* attn_row(const AttnArgs& a, int g, int r, bool value) {
     int s = 0;
 #pragma unroll

@@ -167,3 +167,38 @@ def test_binding_converts_arrays_of_other_types(L):
             mu.muser_kv_tree_commit([plane], [K], [V], 4, path, 100, stream=0)
     with pytest.raises(mu.MuserError, match=r"path\[1\] = 1"):
         mu.muser_kv_tree_commit([plane], (ctypes.c_int64 * 1)(K), [V], 4, [1, 1], 100, stream=0)
+
+
+def host_program(tmp_path, source):
+    """Runs a C++ program (no GPU) against the library's headers; returns what it prints."""
+    import subprocess
+    from quantized_weight_streaming_q4_gb300 import buildlib
+    (tmp_path / "p.cu").write_text(source)
+    subprocess.run([buildlib._nvcc(), *buildlib.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-I", buildlib.INCLUDE, "-I",
+                    buildlib.CSRC, str(tmp_path / "p.cu"), "-o", str(tmp_path / "p")], check=True, capture_output=True)
+    return subprocess.run([str(tmp_path / "p")], check=True, capture_output=True, text=True).stdout.split()
+
+
+def test_attention_parts_are_aligned_in_the_scratch(L, tmp_path):
+    """The (maximum, sum) pairs are read and written 8 bytes at a time, the sums 16 (head sizes that are multiples of 4),
+    whatever the parity of parts, rows and head size; neither reaches into the other nor past the scratch bytes."""
+    out = host_program(tmp_path, r"""
+#include <cstdio>
+#include "attn.cuh"
+int main() {
+    int bad = 0, n = 0;
+    for (long long parts : {1, 2, 3, 11, 101, 304})
+        for (long long rows : {1, 3, 9, 27, 32, 48, 16384})
+            for (long long D : {1, 3, 5, 7, 33, 65, 128, 136, 255, 256}) {
+                const muser::AttnPartLayout l = muser::attn_part_layout(parts, rows, D);
+                const size_t pairs = parts * rows * 8, sums = parts * rows * D * 4;
+                bad += l.o % 16 != 0 || l.o < pairs || l.bytes < l.o + sums || l.bytes % 16 != 0;
+                ++n;
+            }
+    std::printf("%d %d\n", bad, n);
+}
+""")
+    assert out == ["0", "420"]
+    for M, H, kvh, D in ((1, 3, 3, 5), (1, 1, 1, 7), (3, 9, 9, 33), (5, 3, 1, 65), (16, 32, 2, 128)):
+        n = mu.muser_kv_tree_attention_scratch_bytes(kvh * D, D, M, H)
+        assert n % 16 == 0 and n >= M * H * (8 + 4 * D)

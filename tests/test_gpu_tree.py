@@ -158,6 +158,14 @@ def test_attention_long(n, M, H, kvh, D):
     c.to_device().call().check()
 
 
+@pytest.mark.parametrize("M,H,kvh,D,n", [(1, 3, 3, 5, 10), (1, 1, 1, 7, 0), (3, 9, 9, 33, 20), (5, 3, 1, 65, 700), (1, 1, 1, 1, 3),
+                                         (7, 5, 5, 129, 333), (15, 21, 7, 255, 100)])
+@pytest.mark.parametrize("gate", [False, True])
+def test_attention_odd_rows_heads_and_head_sizes(M, H, kvh, D, n, gate):
+    """An odd number of sums in the scratch: the maxima beside them are 8 bytes each."""
+    Case(M, H, kvh, D, n, n + 1, 0, False, gate=gate, seed=21).to_device().call().check()
+
+
 @pytest.mark.parametrize("offset", [1, 4])
 def test_attention_planes_off_the_16_byte_grid(offset):
     Case(3, 4, 2, 64, 77, 80, 0, False, offset=offset).to_device().call().check()
