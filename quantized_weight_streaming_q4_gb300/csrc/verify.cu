@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) verify_greedy_kernel(const __grid_co
 struct Shared {
     uint64_t table[kVerifyTable];
     uint64_t warp[4][kWarps];
-    float warp_max[kWarps];
+    float warp_max[kWarps], warp_left[kWarps];
     float row_sum[kRows], row_exp[kRows];  // a row's sum (NaN: no distribution) and exponent
     float px[MUSER_MAX_M], qx[MUSER_MAX_M], u[MUSER_MAX_M];  // of node i: p(x_i), q(x_i) in its parent's rows
     int token[MUSER_MAX_M];
@@ -707,20 +707,56 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
         ok = grid_barrier<CLUSTER>(a, barriers, &S.flag);
         if (ok) settle<kNext>(a, S, barriers);
     };
+    // Drafts that are certain: what is left of the node's row without the tokens
+    // of `gone`, as a sum of the others, every block the same one.  As 1 - p it
+    // would be a rounding error where p is nearly 1.  The slices without such a
+    // token are summed already; the others are read anew.
+    auto left_without = [&](int row, uint32_t gone) {
+        const float R = S.row_exp[row];
+        const float* p = row_ptr(a, row);
+        auto hits = [&](int x, int lo, int hi) { return x >= lo && x < min(hi, a.V); };
+        float sum = 0.f;
+        if (tid < a.slices) {
+            bool whole = true;
+            for (uint32_t r = gone; r; r &= r - 1) whole = whole && !hits(S.token[__ffs(r) - 1], tid * a.slice_len, (tid + 1) * a.slice_len);
+            if (whole) {
+                const float2 w = __ldcg(a.part + row * kMaxSlices + tid);
+                sum = w.x * ex2(w.y - R);
+            }
+        }
+        for (uint32_t r = gone; r; r &= r - 1) {
+            const int x = S.token[__ffs(r) - 1];
+            if (!hits(x, 0, a.V)) continue;
+            const int lo = x / a.slice_len * a.slice_len, hi = min(lo + a.slice_len, a.V);
+            bool done = false;  // by an earlier token of the same slice
+            for (uint32_t e = gone & ((r & -r) - 1); e; e &= e - 1) done = done || hits(S.token[__ffs(e) - 1], lo, hi);
+            if (done) continue;
+            for (int k = lo + tid; k < hi; k += kThreads) {
+                bool out = false;
+                for (uint32_t e = gone; e; e &= e - 1) out = out || S.token[__ffs(e) - 1] == k;
+                const float w = ex2(fmaf(__ldcg(p + k), a.c_hi, -R));
+                if (!out) sum += w;
+            }
+        }
+        sum = warp_sum(sum);
+        __syncthreads();  // the last call's sums have been read
+        if (lane == 0) S.warp_left[warp] = sum;
+        __syncthreads();
+        sum = 0.f;
+        for (int w = 0; w < kWarps; ++w) sum += S.warp_left[w];
+        return sum / S.row_sum[row];
+    };
     uint32_t children = a.children[cur];  // of the present node, not tried yet
     while (children && ok) {
         const int i = __ffs(children) - 1;
         valid = (fine >> i) & 1u;
         if (!valid) break;
-        bool taken = (first >> i) & 1u;
+        bool taken = (first >> i) & 1u, again = false;
         if (rejected || removed) {  // not a first child
-            bool again = false;  // a token that was certain, and rejected, has nothing left
+            // a token that was certain, and rejected, has nothing left
             for (uint32_t r = removed; r; r &= r - 1) again = again || S.token[__ffs(r) - 1] == S.token[i];
             const float p = S.px[i], q = S.qx[i];
             taken = !again && S.u[i] * left * q < p - c * q;
-            if (!taken && !a.draft && !again) left -= p;
-        } else if (!taken && !a.draft) {
-            left = 1.f - S.px[i];
         }
         if (taken) {
             cur = i;
@@ -736,6 +772,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
         children &= children - 1;
         if (!a.draft) {
             removed |= 1u << i;
+            if (children && !again) {  // a difference is as good as a sum while more than half of the row is left
+                left -= S.px[i];
+                if (left < 0.5f) left = left_without(a.target_at[cur], removed);
+            }
             continue;
         }
         const int tr = a.target_at[cur], dr = a.draft_at[cur];

@@ -385,6 +385,41 @@ def test_verify_duplicate_and_foreign_tokens():
             c.check()
 
 
+@pytest.mark.parametrize("V", [200, 5001, 39999, 50257, 202048])
+@pytest.mark.parametrize("rest", [0.6, 0.3, 1e-2, 1e-5, 3e-7])
+@pytest.mark.parametrize("T", [1.0, 0.1])
+def test_verify_siblings_after_a_nearly_certain_one(V, rest, T):
+    """Drafts taken as certain: the first child has all but `rest` of the row and is rejected; its siblings are decided
+    against what is left.  Their uniforms lie 2^-14 of the threshold p / left above it, then (one of them) below it; both
+    are decided to about 2^-19."""
+    M = 7
+    rng = np.random.default_rng(V)
+    for taken in (2, 3, 6):
+        c = Verify(M, V, STAR, T, False, taken)
+        c.tokens[1:] = rng.choice(V, M - 1, replace=False)
+        if taken == 6:
+            c.tokens[2] = min(c.tokens[1] ^ 1, V - 1)    # a neighbour: in the same share of the row
+            c.tokens[4] = c.tokens[1]                    # the same again: nothing is left of it
+            c.tokens[3] = (c.tokens[2] + V // 2) % V
+            c.tokens[5], c.tokens[6] = (c.tokens[1] + V // 3) % V, (c.tokens[1] + V // 5) % V
+        z = T * rng.standard_normal(V)
+        z[c.tokens[2:]] = T * (4 + rng.random(M - 2))
+        z[c.tokens[1]] = -np.inf
+        z[c.tokens[1]] = T * (np.log(np.exp(z / T).sum()) + np.log((1 - rest) / rest))
+        c.target[0] = z
+        p = np.exp((c.target[0].astype(np.float64) - float(c.target[0].max())) / T)
+        p /= p.sum()
+        left = p.copy()
+        c.u[1] = 1 - 2.0 ** -24
+        for i in range(1, M):
+            x = int(c.tokens[i])
+            if i > 1 and left[x] > 0:
+                c.u[i] = min(left[x] / left.sum() * (1 + (2.0 ** -14 if i < taken else -2.0 ** -14)), 1 - 2.0 ** -24)
+            left[x] = 0.0
+        want = c.check()
+        assert want[:2].tolist()[0] == 2 and want[3] == taken, want
+
+
 def test_verify_masked_logits_and_sharp_rows():
     for T in (1.0, 0.05):
         for seed in range(4):
