@@ -529,6 +529,8 @@ __device__ __forceinline__ void each_logit(const Span& P, const float* row, F&& 
 
 // A row's weights relative to the block's own largest exponent, 0 for the
 // tokens of the nodes in `removed`: to w, their sum and the exponent published.
+// The removed tokens have no part in that exponent: the others' weights would
+// lose as many bits as such a token is more likely than they are.
 __device__ __forceinline__ void leaf_pass(const VerifyArgs& a, Shared& S, const Span& P, const float* row, uint32_t removed,
                                           uint64_t* w, float* logit, unsigned barriers) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -536,6 +538,8 @@ __device__ __forceinline__ void leaf_pass(const VerifyArgs& a, Shared& S, const 
     bool bad = false;
     each_logit(P, row, [&](int k, float x) {
         bad |= !(x < INFINITY);
+        for (uint32_t r = removed; r; r &= r - 1)
+            if (S.token[__ffs(r) - 1] == P.v0 + k) x = -INFINITY;
         mx = fmaxf(mx, x);
         logit[k] = x;
     });
@@ -550,10 +554,7 @@ __device__ __forceinline__ void leaf_pass(const VerifyArgs& a, Shared& S, const 
     const int R = some ? static_cast<int>(t) : -(1 << 23);
     uint64_t v[1] = {0};
     for (int k = P.first; k < P.last; ++k) {
-        uint64_t x = some ? weight(logit[k], a.c_hi, a.c_lo, R, S.table) : 0;
-        for (uint32_t r = removed; r; r &= r - 1)
-            if (S.token[__ffs(r) - 1] == P.v0 + k) x = 0;
-        v[0] += w[k] = x;
+        v[0] += w[k] = some ? weight(logit[k], a.c_hi, a.c_lo, R, S.table) : 0;
     }
     if (tid == 0) __stcg(a.exps + blockIdx.x, bad || t > kMaxExponent ? kBad : R);
     publish(a, S, v, barriers);

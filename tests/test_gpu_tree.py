@@ -420,6 +420,32 @@ def test_verify_siblings_after_a_nearly_certain_one(V, rest, T):
         assert want[:2].tolist()[0] == 2 and want[3] == taken, want
 
 
+@pytest.mark.parametrize("V,blocks", [(39999, 16), (50257, 50), (3000, 16), (1000003, 152)])
+@pytest.mark.parametrize("rest", [0.3, 1e-3, 2.4e-6, 7e-8])
+def test_verify_next_token_after_a_nearly_certain_one(V, blocks, rest):
+    """The next token of a row whose nearly certain token was drafted, taken as certain and rejected: the shares of the
+    others are as fine as if that token had never been there.  uniform[0] points at the middle of a token's share, for
+    tokens behind the rejected one in its block's share of the vocabulary and elsewhere.  (uniform[1] = 1 - 2^-24
+    rejects p = 1 - rest; with 7e-8 left they are 1e-8 apart, acceptance is decided to 2^-19 = 1.9e-6: either is right.)"""
+    rng = np.random.default_rng(V)
+    c = Verify(2, V, CHAIN, 1.0, False, 1)
+    z = 0.3 * rng.standard_normal(V)
+    span = (V + blocks - 1) // blocks
+    x = c.tokens[1] = span * 3 + 5
+    z[x] = -np.inf
+    z[x] = np.log(np.exp(z).sum()) + np.log((1 - rest) / rest)
+    c.target[0] = z
+    p = np.exp(c.target[0].astype(np.float64) - float(c.target[0].max()))
+    p[x] = 0.0
+    total, c.u[1] = np.cumsum(p), 1 - 2.0 ** -24
+    for v in [0, V - 1, *rng.integers(x + 1, span * 4, 40).tolist(), *rng.integers(0, V, 10).tolist()]:
+        if v != x:
+            c.u[0] = (total[v] - p[v] / 2) / total[-1]
+            if rest < 2.0 ** -19 and c.run()[0] == 2:
+                continue
+            assert c.check().tolist() == [1, v, 0, -1]
+
+
 def test_verify_masked_logits_and_sharp_rows():
     for T in (1.0, 0.05):
         for seed in range(4):
