@@ -230,18 +230,27 @@ int launch_combine(const AttnArgs& a, int parts, cudaStream_t s) {
     return check_launch("attention combine");
 }
 
+constexpr size_t generic_smem(int D) { return (2 * kGenTile * (D + 1) + kGenWarps * kGenQ * D) * sizeof(float); }
+static_assert(generic_smem(128) <= 48 * 1024, "heads up to 128 need no attribute");
+
+const int* generic_ready() {
+    return device_once<0, int>([](int& most) {
+        most = static_cast<int>(generic_smem(kGenMaxD));
+        const cudaError_t e = cudaFuncSetAttribute(attn_generic_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        return e == cudaSuccess ? static_cast<int>(MUSER_OK) : cuda_fail(e, "attention: cudaFuncSetAttribute");
+    });
+}
+
 int launch_generic(AttnArgs a, void* scratch, cudaStream_t s) {
     const int rows = a.M * a.group, blocks = (rows + kGenWarps * kGenQ - 1) / (kGenWarps * kGenQ);
     a.nchunks = generic_chunks(a.G, blocks, a.n_common);
     a.chunk = std::max(32, ((a.n_common + a.nchunks - 1) / a.nchunks + 31) / 32 * 32);
     a.nchunks = std::max(1, (a.n_common + a.chunk - 1) / a.chunk);
     place_parts(a, a.nchunks, scratch);
-    const size_t smem = (2 * kGenTile * (a.D + 1) + kGenWarps * kGenQ * a.D) * sizeof(float);
     const dim3 grid(static_cast<unsigned>(a.nchunks), static_cast<unsigned>(a.G), static_cast<unsigned>(blocks));
     auto kern = a.D <= 64 ? attn_generic_kernel<2> : a.D <= 128 ? attn_generic_kernel<4> : attn_generic_kernel<8>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return cuda_fail(e, "attention: cudaFuncSetAttribute");
-    kern<<<grid, kGenWarps * 32, smem, s>>>(a);
+    if (a.D > 128 && generic_ready() == nullptr) return MUSER_ERR_CUDA;  // the message is set
+    kern<<<grid, kGenWarps * 32, generic_smem(a.D), s>>>(a);
     MUSER_TRY(check_launch("attention"));
     return launch_combine(a, a.nchunks, s);
 }

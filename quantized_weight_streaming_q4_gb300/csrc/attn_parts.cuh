@@ -3,10 +3,8 @@
 // visibility differs, and the joining of a cluster's partial results.
 #pragma once
 
-#include <atomic>
-#include <mutex>
-
 #include "attn.cuh"
+#include "kernels.cuh"
 
 namespace muser {
 namespace {
@@ -285,30 +283,6 @@ __device__ __forceinline__ void merge_cluster(const AttnArgs& a, int tid, int c,
             if (d == 0) a.part_ml[slot] = make_float2(M, l);
         }
     }
-}
-
-// What `make` fills in, once per device and kernel (TAG tells a file's kernels
-// apart); null where it failed.
-template <int TAG, typename T, typename F>
-const T* device_once(F&& make) {
-    constexpr int kDevices = 64;
-    static T value[kDevices];
-    static std::atomic<bool> done[kDevices];
-    static std::mutex mu;
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || dev >= kDevices) {
-        cuda_fail(e != cudaSuccess ? e : cudaErrorInvalidDevice, "attention: cudaGetDevice");
-        return nullptr;
-    }
-    if (!done[dev].load(std::memory_order_acquire)) {
-        std::lock_guard<std::mutex> lk(mu);
-        if (!done[dev].load(std::memory_order_relaxed)) {
-            if (make(value[dev]) != MUSER_OK) return nullptr;
-            done[dev].store(true, std::memory_order_release);
-        }
-    }
-    return &value[dev];
 }
 
 // Launch attributes: the cluster, and programmatic stream serialization (the

@@ -1,9 +1,38 @@
 // kernels.cuh -- launch interfaces between libmuser's translation units.
 #pragma once
 
+#include <atomic>
+#include <mutex>
+
 #include "common.cuh"
 
 namespace muser {
+
+// What `make` fills in, once per device and kernel (TAG tells a file's kernels
+// apart); null where it failed.  A kernel's attributes are set here, to what its
+// largest call needs: set for each call, two host threads' calls of different
+// sizes would undo each other's.
+template <int TAG, typename T, typename F>
+const T* device_once(F&& make) {
+    constexpr int kDevices = 64;
+    static T value[kDevices];
+    static std::atomic<bool> done[kDevices];
+    static std::mutex mu;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= kDevices) {
+        cuda_fail(e != cudaSuccess ? e : cudaErrorInvalidDevice, "cudaGetDevice");
+        return nullptr;
+    }
+    if (!done[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!done[dev].load(std::memory_order_relaxed)) {
+            if (make(value[dev]) != MUSER_OK) return nullptr;
+            done[dev].store(true, std::memory_order_release);
+        }
+    }
+    return &value[dev];
+}
 
 enum EpiKind { kEpiStore = 0, kEpiSiluMul = 1, kEpiTail = 2, kEpiSoftcap = 3 };
 // Where the one-token kernel's x comes from: memory, or the previous layer's

@@ -896,6 +896,23 @@ const uint64_t* weight_table() {
     return table;
 }
 
+// The sampling kernels' attributes.  A block holds 16 bytes a token of its
+// span, which is 1,024 tokens (a cluster's: 2,500) or a share of the vocabulary
+// among all blocks.
+const int* verify_ready() {
+    return device_once<0, int>([](int& most) {
+        const int blocks = std::min(sm_count(), kMaxBlocks);
+        if (blocks < 1) return set_error(MUSER_ERR_CUDA, "tree_verify: cannot read the SM count");
+        most = static_cast<int>(std::max<int64_t>((kVerifyMaxVocab + blocks - 1) / blocks, 1024) * 16);
+        cudaError_t e = cudaFuncSetAttribute(verify_sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(verify_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(verify_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return e == cudaSuccess ? static_cast<int>(MUSER_OK) : cuda_fail(e, "tree_verify: cudaFuncSetAttribute");
+    });
+}
+static_assert((kClusterVocab + kClusterBlocks - 1) / kClusterBlocks * 16 + sizeof(Shared) <= 48 * 1024,
+              "a cluster's blocks need no attribute for their shared memory");
+
 }  // namespace
 
 size_t verify_scratch_bytes() { return layout().bytes; }
@@ -982,14 +999,7 @@ int launch_verify(const float* target, const float* draft, const int32_t* tokens
     cfg.attrs = attr;
     cfg.numAttrs = greedy || M == 1 ? 1 : 2;
     auto kern = greedy ? verify_greedy_kernel : M == 1 ? verify_sample_kernel : cluster ? verify_kernel<true> : verify_kernel<false>;
-    if (cluster) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return cuda_fail(e, "tree_verify: cudaFuncSetAttribute");
-    }
-    if (!greedy && smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return cuda_fail(e, "tree_verify: cudaFuncSetAttribute");
-    }
+    if (!greedy && verify_ready() == nullptr) return MUSER_ERR_CUDA;  // the message is set
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess) return cuda_fail(e, "tree_verify: cudaLaunchKernelEx");
     return check_launch("tree_verify");

@@ -273,6 +273,41 @@ def test_attention_repeats_bit_for_bit_on_streams_and_in_graphs():
     assert np.array_equal(host(c.out), want[0]) and np.array_equal(host(d.out), want[1])
 
 
+def from_two_threads(*calls, times=3000):
+    """Runs the calls at the same time, each again and again in a thread of its own; raises what one of them raised."""
+    import threading
+    errors, start = [], threading.Barrier(len(calls))
+
+    def loop(call):
+        try:
+            start.wait()
+            for _ in range(times):
+                call()
+                if errors:
+                    break
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=loop, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    if errors:
+        raise errors[0]
+
+
+def test_attention_of_two_head_sizes_from_two_threads():
+    """Head sizes 256 and 136 off the 16-byte grid: one kernel, two amounts of shared memory."""
+    cases = [Case(1, 2, 1, D, 5, 8, 0, False, offset=1, seed=22).to_device() for D in (256, 136)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    from_two_threads(*[lambda c=c, s=s: c.call(s) for c, s in zip(cases, streams)])
+    for c in cases:
+        c.check()
+
+
 # --------------------------------------------------------------- verification
 class Verify:
     def __init__(self, M, V, kind=CHAIN, T=1.0, draft=True, seed=0, close=0.6):
@@ -519,6 +554,21 @@ def test_verify_extreme_temperatures(T, M, draft):
         c.draft[:, 1::2] = -np.inf
     c.tokens = drafted(np.random.default_rng(M), c.draft if draft else c.target, c.parent, T)
     c.check()
+
+
+def test_verify_of_two_vocabularies_from_two_threads():
+    """2^20 and 500,000 tokens: one kernel, two amounts of shared memory."""
+    cases, calls = [Verify(1, V, CHAIN, 1.0, False, 8) for V in (1 << 20, 500000)], []
+    for c in cases:
+        c.args = dev(c.target), dev(c.tokens), dev(c.u), torch.full((3,), -77, dtype=torch.int32, device="cuda")
+        c.n = mu.muser_tree_verify_scratch_bytes(c.V, 1)
+        c.scratch, s = torch.zeros(c.n // 4, device="cuda"), torch.cuda.Stream()
+        calls.append(lambda c=c, s=s: mu.muser_tree_verify(c.args[0], None, c.args[1], None, 1, c.V, c.T, c.args[2],
+                                                           c.args[3], c.scratch, c.n, s))
+    torch.cuda.synchronize()
+    from_two_threads(*calls)
+    for c in cases:
+        assert np.array_equal(host(c.args[3]), c.want())
 
 
 def test_verify_greedy_ties_take_the_lowest_index():
