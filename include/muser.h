@@ -566,8 +566,11 @@ size_t muser_kv_tree_attention_scratch_bytes(int64_t kv_dim, int64_t head_dim, i
  *    - itself, and an ancestor j if depth_i - depth_j < window or j's
  *      position is below n_sink.
  *   No other row has any influence, whatever its slot holds (infinities and
- *   NaN included).  A score or a value that is not finite in a row that is
- *   seen makes the outputs that read it not finite.
+ *   NaN included).  In a row that is seen, a value that is not finite and a
+ *   score that is NaN or +infinity make the outputs that read them not finite.
+ *   A score of -infinity (of a key beyond binary16) counts as weight 0, or
+ *   makes the output NaN: which of the two depends on the kernel and on the
+ *   query's low bits, since an infinity times a part of it that is 0 is NaN.
  *   plane: host struct, read only, head_dim set in both layouts; sink: the
  *   same kv_dim and head_dim, either layout, or NULL.  q, out, gate: device
  *   f32 [M * n_heads*head_dim]; k, v: device f32 [M * kv_dim], used as

@@ -232,6 +232,41 @@ def test_attention_what_is_not_seen_has_no_influence(H, kvh, D, bad):
     assert np.abs(got[1:] - want[1:]).max() <= attention_bound(c2.q, c2.scale, 5.0, D, 5.0)
 
 
+@pytest.mark.parametrize("M,H,kvh,D", [(1, 32, 2, 128), (2, 32, 2, 128), (9, 20, 5, 64), (16, 32, 2, 128), (16, 32, 1, 64), (1, 4, 1, 256),
+                                       (9, 8, 2, 136), (1, 4, 2, 5), (9, 6, 2, 7)])
+@pytest.mark.parametrize("where", ["cached", "first", "edge", "tree"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_attention_one_infinite_key_element(M, H, kvh, D, where, sign):
+    """A key with one infinite element.  Queries of that sign there: a score of +infinity, nothing finite.  Queries of
+    the other sign: -infinity, which counts as weight 0 or makes the output NaN.  Rows that do not see it: no influence."""
+    n, window = 700, 300
+    if where == "edge" and M == 1:
+        pytest.skip("one row has one window")
+    c = Case(M, H, kvh, D, n, n, 0, False, window=window, kind=CHAIN, seed=23)
+    element = D // 2
+    c.q.reshape(M, H, D)[:, :, element] = 0.25 + np.abs(c.q.reshape(M, H, D)[:, :, element])
+    seeing = np.ones(M, bool)
+    if where == "tree":
+        c.k.reshape(M, kvh, D)[M - 1, :, element] = sign * np.inf
+        seeing[:M - 1] = False                  # the last row of a chain
+    else:
+        at = {"cached": n - 100, "first": n - window + M, "edge": n - window + 1}[where]
+        c.key.reshape(n, kvh, D).view(np.float16)[at, :, element] = sign * np.inf
+        if where == "edge":
+            seeing[1:] = False                  # position 401: the root's alone
+    want = c.want()                             # exp(-infinity) = 0 there
+    got = host(c.to_device().call().out)[:M * H * D].reshape(M, -1)
+    assert np.isfinite(want[~seeing]).all() and np.isfinite(got[~seeing]).all()
+    bound = attention_bound(c.q, c.scale, 5.0, D, 5.0)
+    if (~seeing).any():
+        assert np.abs(got[~seeing] - want[~seeing]).max() <= bound
+    if sign > 0:
+        assert not np.isfinite(got[seeing]).any()
+    else:
+        ok = np.isnan(got[seeing]) | (np.abs(got[seeing] - want[seeing]) <= bound)
+        assert np.isfinite(want[seeing]).all() and ok.all()
+
+
 def test_attention_offsets_past_32_bits():
     """A head-major plane of 2^24 slots (2^32 elements a buffer): the second head's rows lie past 2^31 elements."""
     cap, kvh, D, n = 1 << 24, 2, 128, 300
