@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) verify_greedy_kernel(const __grid_co
     if (tid == 0) s_last = atom_add_acq_rel_gpu(a.sync, 1u) == gridDim.x - 1;
     __syncthreads();
     if (!s_last) return;
-    if (tid >= 1 && tid < a.M) s_token[tid] = __ldg(a.tokens + tid);
+    if (tid >= 1 && tid < a.M) s_token[tid] = __ldcg(a.tokens + tid);
     for (int r = warp; r < a.nrows; r += kWarps) {
         uint64_t key = 0;
         for (int i = lane; i < a.slices; i += 32) {
@@ -387,7 +387,7 @@ __device__ __forceinline__ void settle(const VerifyArgs& a, Shared& S, unsigned 
         constexpr int kEach = kMaxBlocks / 32;
         const int lane = threadIdx.x, nb = gridDim.x, each = (nb + 31) / 32;
         const ulonglong2* from = reinterpret_cast<const ulonglong2*>(a.sums + (barriers & 1) * 4 * kMaxBlocks);
-        const float u = __ldg(a.uniform);
+        const float u = __ldcg(a.uniform);
         uint64_t x[kEach], fm = 0;
         int e[kEach], R = KIND == kLeaf ? -(1 << 23) : 0, fe = 0;
         ulonglong2 s0[kEach], s1[KIND == kFirst ? kEach : 1];
@@ -626,9 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
     // the drafted tokens' logits, in flight during the barrier
     float lx = -INFINITY, ly = -INFINITY;
     if (tid >= 1 && tid < a.M) {
-        const int x = __ldg(a.tokens + tid), up = a.parent[tid];
+        const int x = __ldcg(a.tokens + tid), up = a.parent[tid];
         S.token[tid] = x;
-        S.u[tid] = __ldg(a.uniform + tid);
+        S.u[tid] = __ldcg(a.uniform + tid);
         if (x >= 0 && x < a.V) {
             lx = __ldcg(row_ptr(a, a.target_at[up]) + x);
             if (a.draft) ly = __ldcg(row_ptr(a, a.draft_at[up]) + x);

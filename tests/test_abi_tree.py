@@ -202,3 +202,14 @@ int main() {
     for M, H, kvh, D in ((1, 3, 3, 5), (1, 1, 1, 7), (3, 9, 9, 33), (5, 3, 1, 65), (16, 32, 2, 128)):
         n = mu.muser_kv_tree_attention_scratch_bytes(kvh * D, D, M, H)
         assert n % 16 == 0 and n >= M * H * (8 + 4 * D)
+
+
+def test_programmatically_launched_kernels_load_nothing_on_the_read_only_path():
+    """A non-coherent load may move above the wait for the kernel before, whose output it then misses.  attn.cu's
+    CUDA-core kernel has no such wait (an ordinary launch)."""
+    from quantized_weight_streaming_q4_gb300 import buildlib
+    for name in ("verify.cu", "attn_few.cu", "attn_tc.cu", "attn_mma.cu", "attn_parts.cuh", "tc.cuh"):
+        with open(os.path.join(buildlib.CSRC, name)) as f:
+            text = f.read()
+        for load in ("ldg(", "ldg_", "global.nc", "attn_ragged("):
+            assert load not in text, (name, load)
