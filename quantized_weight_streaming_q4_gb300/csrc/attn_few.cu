@@ -99,8 +99,12 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + kBars);
     uint32_t* flags = tmem_slot + 1;
-    // a softmax thread's wait ran out: its warpgroup leaves at its next barrier
-    volatile uint32_t* gave_up = tmem_slot + 2 + (warp >= 8 ? 1 : 0);
+    // A softmax thread's wait ran out: its warpgroup leaves at its next barrier,
+    // all of it at the same one.  What is noted behind a tile's first barrier
+    // goes to a word that is read behind the next tile's (one for even tiles, one
+    // for odd ones) or behind the reference's barrier (the third): no thread is
+    // so far ahead that it writes the word which another still has to read.
+    volatile uint32_t* gave_up = tmem_slot + 2 + (warp >= 8 ? 3 : 0);
     float* cs = reinterpret_cast<float*>(smem + L::kScaleOff);
     const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * R;
     const int rows = a.M * a.group;
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         mbar_init(&bar[kQReady], 128 * L::kGroups);
         mbar_init(&bar[kRagged], 128);
         *flags = 0;
-        tmem_slot[2] = tmem_slot[3] = 0;
+        for (int i = 2; i < 8; ++i) tmem_slot[i] = 0;
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tmem_slot, L::kTmemCols);
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             uint32_t see = th < real ? 0xffffu : 0u;  // bit j: row j sees this thread's key
             if (t == rt) see = ragged_see;
             wait(kSFull + (t & 1), t >> 1);
-            if (!ok) *gave_up = 1;
+            if (!ok) gave_up[t & 1] = 1;
             tc_fence_after();
             float s[16], x[16];
             tmem_ld16(mine + (t & 1) * L::kN, s);
@@ -405,13 +409,13 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             }
             bool drained = t == 0;
             const bool anew = group_any(id, (t == 0 && !self) || top > kMost);
-            if (*gave_up) {
+            if (gave_up[t & 1]) {
                 ok = false;
                 break;
             }
             if (anew) {  // a new reference: the largest score so far
                 if (!drained) drain(t - 1);
-                if (!ok) *gave_up = 1;
+                if (!ok) gave_up[2] = 1;
                 drained = true;
                 float* red = reinterpret_cast<float*>(smem + L::kRedOff) + w * 64;
                 float v[16];
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
                 fold16(v, [](float p, float q) { return fmaxf(p, q); });
                 if ((lane & 1) == 0) red[(warp & 3) * 16 + (lane >> 1)] = v[0];
                 named_barrier_sync(id, 128);
-                if (*gave_up) {
+                if (gave_up[2]) {
                     ok = false;
                     break;
                 }
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             tc_fence_before();
             mbar_arrive(&bar[kPFull + (t & 1)]);
             if (!drained) drain(t - 1);
-            if (!ok) *gave_up = 1;
+            if (!ok) gave_up[(t + 1) & 1] = 1;
         }
         if (ntiles > 0 && ok) drain(ntiles - 1);
         // the rows' sums over the keys' threads, then this chunk's result
