@@ -99,12 +99,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + kBars);
     uint32_t* flags = tmem_slot + 1;
-    // A softmax thread's wait ran out: its warpgroup leaves at its next barrier,
-    // all of it at the same one.  What is noted behind a tile's first barrier
-    // goes to a word that is read behind the next tile's (one for even tiles, one
-    // for odd ones) or behind the reference's barrier (the third): no thread is
-    // so far ahead that it writes the word which another still has to read.
-    volatile uint32_t* gave_up = tmem_slot + 2 + (warp >= 8 ? 3 : 0);
+    volatile uint32_t* lost = tmem_slot + 2;  // a wait of a softmax thread ran out
     float* cs = reinterpret_cast<float*>(smem + L::kScaleOff);
     const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * R;
     const int rows = a.M * a.group;
@@ -178,7 +173,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         mbar_init(&bar[kQReady], 128 * L::kGroups);
         mbar_init(&bar[kRagged], 128);
         *flags = 0;
-        for (int i = 2; i < 8; ++i) tmem_slot[i] = 0;
+        *lost = 0;
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(tmem_slot, L::kTmemCols);
@@ -187,6 +182,10 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // A thread whose wait has run out waits no more and goes on with what is
+    // there: warps and warpgroups stay together at the instructions and barriers
+    // that take all of them.  The block's rows become NaN; what it would have
+    // joined is not written.
     bool ok = true;
     auto wait = [&](int b, int phase) {
         if (ok) ok = mbar_wait_bounded(&bar[b], static_cast<uint32_t>(phase & 1), a.status, kDevStatusWaitTimeout);
@@ -207,11 +206,10 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             int sg, row;
             keys[s] = next_tile(t, sg, row);
             wait(kKFull + st, t / kNS);
-            if (!ok) return;
             tc_fence_after();
             const uint64_t kd = desc_swizzle128(base + st * kItem, 16, 1024);
             const uint32_t d = tm + s * L::kN;
-            if (leader) {
+            if (leader && ok) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
                     if (ks < ksteps) {
@@ -226,18 +224,17 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         };
         wait(kQReady, 0);
         tc_fence_after();
-        if (ntiles > 0 && ok) scores(0);
-        for (int t = 0; t < ntiles && ok; ++t) {
+        if (ntiles > 0) scores(0);
+        for (int t = 0; t < ntiles; ++t) {
             const int s = t & 1, st = t % kNS, steps = (keys[s] + 15) / 16;
             if (t + 1 < ntiles) scores(t + 1);
             wait(kPFull + s, t >> 1);
             wait(kVFull + st, t / kNS);
-            if (!ok) break;
             tc_fence_after();
             const uint64_t vd = desc_swizzle128(base + L::kVOff + st * kItem, kHalf, 1024);
             const uint64_t pd = desc_bits(base + L::kPOff + s * L::kPBytes, L::kKeyRow, 128);
             const uint32_t d = tm + 2 * L::kN + s * L::kN;
-            if (leader) {
+            if (leader && ok) {
                 mma_ss<false>(d, vd, pd, ido);
 #pragma unroll
                 for (int ks = 1; ks < kTile / 16; ++ks)
@@ -376,7 +373,6 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
         if (self) named_barrier_sync(id, 128);  // before the references are written again
         auto drain = [&](int t) {  // adds the output tile t
             wait(kOFull + (t & 1), t >> 1);
-            if (!ok) return;
             tc_fence_after();
             float hi[16], lo[16];
             tmem_ld16(mine + 2 * L::kN + (t & 1) * L::kN, hi);
@@ -393,7 +389,6 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             uint32_t see = th < real ? 0xffffu : 0u;  // bit j: row j sees this thread's key
             if (t == rt) see = ragged_see;
             wait(kSFull + (t & 1), t >> 1);
-            if (!ok) gave_up[t & 1] = 1;
             tc_fence_after();
             float s[16], x[16];
             tmem_ld16(mine + (t & 1) * L::kN, s);
@@ -409,13 +404,8 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             }
             bool drained = t == 0;
             const bool anew = group_any(id, (t == 0 && !self) || top > kMost);
-            if (gave_up[t & 1]) {
-                ok = false;
-                break;
-            }
             if (anew) {  // a new reference: the largest score so far
                 if (!drained) drain(t - 1);
-                if (!ok) gave_up[2] = 1;
                 drained = true;
                 float* red = reinterpret_cast<float*>(smem + L::kRedOff) + w * 64;
                 float v[16];
@@ -424,10 +414,6 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
                 fold16(v, [](float p, float q) { return fmaxf(p, q); });
                 if ((lane & 1) == 0) red[(warp & 3) * 16 + (lane >> 1)] = v[0];
                 named_barrier_sync(id, 128);
-                if (gave_up[2]) {
-                    ok = false;
-                    break;
-                }
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float mn = fmaxf(fmaxf(fmaxf(m[j], red[j]), fmaxf(red[16 + j], red[32 + j])), red[48 + j]);
@@ -462,29 +448,31 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
             tc_fence_before();
             mbar_arrive(&bar[kPFull + (t & 1)]);
             if (!drained) drain(t - 1);
-            if (!ok) gave_up[(t + 1) & 1] = 1;
         }
-        if (ntiles > 0 && ok) drain(ntiles - 1);
+        if (ntiles > 0) drain(ntiles - 1);
         // the rows' sums over the keys' threads, then this chunk's result
         float* red = reinterpret_cast<float*>(smem + L::kRedOff) + w * 64;
         fold16(l, [](float p, float q) { return p + q; });
         if ((lane & 1) == 0) red[(warp & 3) * 16 + (lane >> 1)] = l[0];
+        if (!ok) *lost = 1;
         named_barrier_sync(id, 128);
         if (th < 16) {
             float sum = (red[th] + red[16 + th]) + (red[32 + th] + red[48 + th]);
             const int i = (r0 + w * 16 + th) / a.group;
             if ((ragged || self) && i < a.M && (a.mask[i] & *flags)) sum = NAN;  // it sees a ragged row that is not finite
+            if (*lost) sum = NAN;
             if (alone) cs[w * 16 + th] = __fdividef(1.f, sum);
             else ml[w * 16 + th] = make_float2(ntiles > 0 || self ? reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + th] : kNegInf, sum);
         }
         if (alone) {
-            named_barrier_sync(id, 128);
+            named_barrier_sync(1 + L::kGroups, 128 * L::kGroups);
+            const bool any_lost = *lost != 0;  // the other warpgroup's too
             float* p = a.out + at0;
 #pragma unroll
             for (int j = 0, k = tk0; j < 16; ++j) {
                 float v = o[j] * cs[w * 16 + j];
                 if (a.gate) v = __fdividef(v, 1.f + __expf(-z[j]));
-                if (j < live && ok) *p = v;
+                if (j < live) *p = any_lost ? NAN : v;
                 p += a.D;
                 if (++k == a.group) k = 0, p += skip;
             }

@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + kBars);
     uint32_t* flags = tmem_slot + 1;
+    volatile uint32_t* lost = tmem_slot + 2;  // a wait of the block ran out
     const int c = blockIdx.x, g = blockIdx.y, r0 = blockIdx.z * 128;
     const int rows = a.M * a.group;
     // tile 0 of the last chunk holds the ragged rows; the common ones follow
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         mbar_init(&bar[kRagged], 256);
         mbar_init(&bar[kJoin], 1);
         *flags = 0;
+        *lost = 0;
         fence_mbar_init();
         if (a.cluster > 1) mbar_arrive_expect_tx(&bar[kJoin], 128 * L::kOutStride * 4);
     }
@@ -149,9 +151,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const int ntiles = ragged + walk.count(a, kTile);
     auto next_tile = [&](int t, int& s, int& row) { return t < ragged ? nragged : walk.next(a, kTile, s, row); };
     constexpr uint32_t tmem = 0;  // the address of an allocation of all columns
+    // A thread whose wait has run out waits no more and goes on with what is
+    // there, so that its warp stays together at the instructions that take all
+    // of it.  The block's rows become NaN.
     bool ok = *tmem_slot == tmem;
+    if (!ok) *lost = 1;
     auto wait = [&](int b, int phase) {
-        if (ok) ok = mbar_wait_bounded(&bar[b], static_cast<uint32_t>(phase & 1), a.status, kDevStatusWaitTimeout);
+        if (!ok) return;
+        ok = mbar_wait_bounded(&bar[b], static_cast<uint32_t>(phase & 1), a.status, kDevStatusWaitTimeout);
+        if (!ok) *lost = 1;
     };
     float2* stat = reinterpret_cast<float2*>(smem + L::kStatOff);
     float* out = reinterpret_cast<float*>(smem + L::kOutOff);
@@ -194,16 +202,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 if (ok) scores(0);
                 wait_both(kVFull, 0, ntiles > 1 ? kKFull + 1 : kVFull, 0);
                 if (ok && ntiles > 1) scores(1);
-    #pragma unroll 1
-            for (int t = 0; t < ntiles && ok; ++t) {
+#pragma unroll 1
+                for (int t = 0; t < ntiles; ++t) {
                     const int s = t & 1;
                     wait(kPFull + s, t >> 1);  // and the output tile before is read
-                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t id = idesc(DP, false, true), d = tmem + kColO, p = tmem + s * 128;
                     const uint64_t vd = desc_swizzle128(base + (2 + s) * L::kItem, kHalf, 1024);
                     const int steps = keys[s] / 16;
-                    if (leader) {
+                    if (leader && ok) {
                         mma<false>(d, p + 8, vd, id);  // the low part of p first
 #pragma unroll
                         for (int ks = 1; ks < kTile / 16; ++ks)
@@ -324,12 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 
             const uint32_t scol = mine + w * 128;
 #pragma unroll 1
-            for (int t = 0; t < ntiles && ok; ++t) {
+            for (int t = 0; t < ntiles; ++t) {
                 int sg, srow;
                 const int real = next_tile(t, sg, srow), chunks = (real + 31) >> 5;
                 if ((t & 1) != w) continue;
                 wait(kSFull + w, t >> 1);
-                if (!ok) break;
                 tc_fence_after();
                 // Columns [64 h, 64 h + 64) of the scores, -infinity where this
                 // row does not see the key.  More at once did not fit the registers.
@@ -404,16 +410,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
             for (int d = 0; d < DP; ++d) o[d] = 0.f;
 #pragma unroll 1
-            for (int t = 0; t < ntiles && ok; ++t) {
+            for (int t = 0; t < ntiles; ++t) {
                 const int s = t & 1;
                 wait(kPFull + s, t >> 1);
-                if (!ok) break;
                 const float2 tile = stat[(t & 3) * 128 + row];
                 const float mn = fmaxf(m, tile.x), f = share(m, mn), ft = share(tile.x, mn);
                 m = mn;
                 l = fmaf(l, f, tile.y * ft);
                 wait(kOFull + s, t >> 1);
-                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int ch = 0; ch < DP / 32; ++ch) {
@@ -426,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 tc_fence_before();
                 if (t + 1 < ntiles) mbar_arrive(&bar[kPFull + (s ^ 1)]);
             }
-            // no wait ran out, and no ragged row that this row sees is not finite
-            if (!ok || (mask & *flags)) l = NAN;
+            // a wait ran out, or a ragged row that this row sees is not finite
+            if (*lost || (mask & *flags)) l = NAN;
             // To the K and V tiles' place, and from there to the blocks that join
             // the rows.  (Reading the others' shared memory took 6,000 cycles in
             // a cluster of 4, storing there as long.)
