@@ -459,10 +459,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         } else {
             __syncthreads();
         }
-        merge_cluster<DP, L::kOutStride, 128, 384>(a, tid - 128, c, g, r0, rows, out);
+        if (ok) merge_cluster<DP, L::kOutStride, 128, 384>(a, tid - 128, c, g, r0, rows, out);
         if (a.cluster > 1) {
             __syncwarp();
             cluster_wait();  // nobody leaves while copies read its shared memory
+            // Every block has issued its copies by now: after a wait that ran out
+            // they may still be on their way here.
+            if (!ok) mbar_wait_bounded(&bar[kJoin], 0u, a.status, kDevStatusTxTimeout);
         }
     }
 }
