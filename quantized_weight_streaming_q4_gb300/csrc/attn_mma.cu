@@ -11,7 +11,11 @@
 // query vector is scaled by a power of two and split into two binary16 parts
 // (22 bits); p = 2^(s - m + 14) is split likewise (the offset keeps the low
 // part of all but vanishing weights out of the subnormals), so both products
-// run twice, and sums are binary32.  One part alone would be off by 2^-12.
+// run twice, and sums are binary32.  One part alone would be off by 2^-12.  The
+// products' additions truncate: the outputs of every 16 keys are a fresh
+// accumulator, added in registers.  Values of one sign over 8,125 keys a block
+// were 2.9e-5 too small on one accumulator, 1.2e-7 off so, at 4 to 7 % of the
+// time (16 rows, 16 heads of 256 on one, 130,000 rows: 541 -> 563 us).
 //
 // The blocks of a cluster hold neighbouring chunks of the same rows and join
 // their (maximum, sum, output) triples through distributed shared memory; with
@@ -263,10 +267,16 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
         for (int n = 0; n < DP / 16; ++n) {
             uint32_t vf[4];  // d 0-7: keys 0-7, 8-15; d 8-15: the same
             ldsm4t(vf, vbuf + piece<kTileKeys>(k0 + (lane & 15), n * 2 + (lane >> 4)));
-            mma16816(o[2 * n], pl, vf[0], vf[1]);
-            mma16816(o[2 * n + 1], pl, vf[2], vf[3]);
-            mma16816(o[2 * n], ph, vf[0], vf[1]);
-            mma16816(o[2 * n + 1], ph, vf[2], vf[3]);
+            float y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            mma16816(y[0], pl, vf[0], vf[1]);
+            mma16816(y[1], pl, vf[2], vf[3]);
+            mma16816(y[0], ph, vf[0], vf[1]);
+            mma16816(y[1], ph, vf[2], vf[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[2 * n][e] += y[0][e];
+                o[2 * n + 1][e] += y[1][e];
+            }
         }
     };
 

@@ -166,6 +166,35 @@ def test_attention_odd_rows_heads_and_head_sizes(M, H, kvh, D, n, gate):
     Case(M, H, kvh, D, n, n + 1, 0, False, gate=gate, seed=21).to_device().call().check()
 
 
+@pytest.mark.parametrize("M,H,kvh,D,n", [(16, 16, 1, 256, 130000), (16, 8, 2, 200, 40000), (16, 32, 2, 128, 130000), (1, 32, 2, 128, 130000),
+                                         (16, 32, 4, 64, 60000), (2, 2, 1, 7, 130000)])
+def test_attention_long_sums_do_not_drift(M, H, kvh, D, n):
+    """Values of one sign, so that sums which lose their last bits downwards lose them together.  Against binary64, of the
+    result's norm: sums of n / 16 terms to nearest lose 2^-25 of themselves at random each, sqrt(8192) 2^-25 = 2.7e-6 for
+    the longest if no block shared it (a sixteenth of the rows or less a block: 7e-7); the products of 16 keys or of a
+    tile lose 8 steps of 2^-24 at most (4.8e-7); queries and weights are held to 2^-22 and exponentials to 2^-22, at random
+    (2.4e-7 each); the division 2^-23: 1.8e-6 in all.  4e-6 is twice that; one accumulator that truncates over 8,000 keys
+    would lose 2e-5."""
+    c = Case(M, H, kvh, D, 8, n, 0, True, seed=24)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    key = torch.randn(kvh, n, D, generator=g, device="cuda").half()
+    value = (1 + 0.25 * torch.rand(kvh, n, D, generator=g, device="cuda")).half()
+    c.q *= 0.5
+    c.v = 1 + np.abs(c.v) / 4
+    c.to_device()
+    c.plane = mu.KvPlane(key.data_ptr(), value.data_ptr(), n, n, 0, 0, kvh * D, D, 1, 0)
+    got = host(c.call().out)[:M * H * D].reshape(M, H, D)
+    group, want = H // kvh, np.empty((M, H, D))
+    tk, tv = (t.half().double().view(M, kvh, D) for t in (c.dk, c.dv))
+    for i in range(M):                       # a chain: row i sees the plane and rows 0..i
+        for h in range(kvh):
+            k, v = (torch.cat([a[h].double(), b[:i + 1, h]]) for a, b in ((key, tk), (value, tv)))
+            q = c.dq.double().view(M, kvh, group, D)[i, h]
+            want[i, h * group:(h + 1) * group] = (torch.softmax(c.scale * (q @ k.T), 1) @ v).cpu().numpy()
+    rel = np.linalg.norm(got - want) / np.linalg.norm(want)
+    assert rel <= 4e-6, rel
+
+
 @pytest.mark.parametrize("offset", [1, 4])
 def test_attention_planes_off_the_16_byte_grid(offset):
     Case(3, 4, 2, 64, 77, 80, 0, False, offset=offset).to_device().call().check()
