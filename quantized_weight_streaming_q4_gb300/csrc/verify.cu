@@ -65,6 +65,7 @@ struct VerifyArgs {
     int slices, slice_len; // of a row in the first pass
     int span;              // tokens per block in the passes over one node
     unsigned* sync;        // arrivals, exits
+    uint64_t* near;        // [MUSER_MAX_M] by node, see kFirst
     float2* part;          // [kRows][kMaxSlices] (sum, exponent); greedy: uint64 keys
     uint64_t* sums;        // [2][kMaxBlocks][4]: two passes' buffers in turn, a record a block
     int* exps;             // [kMaxBlocks]
@@ -283,6 +284,7 @@ struct Shared {
     // the sampled point: its block (-1: nothing to sample, -2: no distribution), the place in its share
     int owner, exp;
     uint64_t before;
+    uint64_t near[MUSER_MAX_M], near_all;  // kFirst: draft weights near f0, the block's by node, all blocks'
     int flag, found;
     int cur, n;  // the walk along accepted first children
     uint32_t kept;
@@ -376,8 +378,14 @@ __device__ __forceinline__ uint64_t fraction_of(float u, uint64_t total) {
 //  kFirst  the first rejected child: sums of P, of Q, and of both over the tokens
 //          with P > f0 Q, f0 being f from the first pass's binary32 sums.  With
 //          f = sum P / sum Q now exact, a block's share is sum P - f sum Q over
-//          those tokens; the few between f0 and f (1e-6 apart) are worth 1e-6
-//          of themselves.  This saves the barrier between f and the shares;
+//          those tokens.  This saves the barrier between f and the shares, but
+//          the tokens between f0 and f are on the wrong side, each off by at
+//          most |f - f0| Q.  They are among those with |P - f0 Q| <= 2^-20 f0 Q,
+//          whose Q the blocks that have any add up (expected is one of 202,048
+//          tokens): where that could come to 2^-38 of the row or 2^-20 of what
+//          is left, or f0 is further off (logits in the thousands), a pass with
+//          f follows (rows that are nearly equal: 202,048 logits 1e-5 apart put
+//          the next token off by five);
 //  kNext   a further rejected child, or the row itself: the shares.
 // Leaves the remainder's size, and the sampled point's block and place there.
 enum PassKind { kLeaf, kFirst, kNext };
@@ -601,9 +609,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
     uint64_t* wp = held;
     uint64_t* wq = held + a.span;
     for (int j = tid; j < kVerifyTable; j += kThreads) S.table[j] = a.table[j];
+    if (tid < MUSER_MAX_M) S.near[tid] = 0;
     pdl_wait();  // no global access before this
     unsigned barriers = 0;
-    bool ok = true;
+    bool ok = true, any_near = false;
     int row, lo, hi;
     if (my_unit(a, row, lo, hi)) {
         float sum = 0.f, R = -kMaxExponent;
@@ -780,9 +789,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
             continue;
         }
         const int tr = a.target_at[cur], dr = a.draft_at[cur];
+        bool pass = rejected;
         if (!rejected) {  // the node's weights, to shared memory
             const int Rp = static_cast<int>(S.row_exp[tr]) + 1, Rq = static_cast<int>(S.row_exp[dr]) + 1;
-            uint64_t fm, v[4] = {0, 0, 0, 0};
+            uint64_t fm, near = 0, v[4] = {0, 0, 0, 0};
             int fe;
             split_factor(S.row_sum[tr] / S.row_sum[dr], fm, fe);
             const float* pr = row_ptr(a, tr) + P.v0;
@@ -802,17 +812,36 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
                     wq[k + j] = z;
                     v[0] += w;
                     v[1] += z;
-                    if (w > times_f(z, fm, fe)) {
+                    const uint64_t fz = times_f(z, fm, fe);
+                    if (w > fz) {
                         v[2] += w;
                         v[3] += z;
                     }
+                    // (below 2^20 units what such a token is off by is less than one)
+                    if ((w > fz ? w - fz : fz - w) <= (fz >> 20)) near += z;
                 }
             }
+            if (__any_sync(0xffffffffu, near != 0)) {
+                near = warp_sum64(near);
+                if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&S.near[cur]), static_cast<unsigned long long>(near));
+            }
             publish(a, S, v, ++barriers);
+            if (tid == 0 && S.near[cur] != 0)
+                atomicAdd(reinterpret_cast<unsigned long long*>(a.near + cur), static_cast<unsigned long long>(S.near[cur]));
             ok = grid_barrier<CLUSTER>(a, barriers, &S.flag);
             if (!ok) break;
+            if (tid == 32) S.near_all = ldcg64(a.near + cur);  // beside warp 0
             settle<kFirst>(a, S, barriers);
             rejected = true;
+            const uint64_t apart = S.fe == fe ? (S.fm > fm ? S.fm - fm : fm - S.fm)
+                                 : fe == S.fe + 1 ? fm - (S.fm >> 1) : S.fe == fe + 1 ? S.fm - (fm >> 1) : ~0ull;
+            const int one = S.fe == fe ? 63 : 62;  // |f - f0| / f = apart / 2^one at most
+            pass = apart >> (one - 20) != 0;
+            if (S.near_all != 0) {
+                any_near = true;
+                const float off = static_cast<float>(apart) * __int_as_float((127 - one) << 23);
+                pass = pass || off * (static_cast<float>(S.near_all) / static_cast<float>(S.sum_q)) > fminf(0x1p-38f, 0x1p-20f * S.left_f);
+            }
         } else {
             __syncthreads();  // every thread has read the last remainder's c
             if (tid == 0) {
@@ -821,6 +850,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
                 split_factor(S.c * (static_cast<double>(S.sum_p) / static_cast<double>(S.sum_q)), S.fm, S.fe);
             }
             __syncthreads();
+        }
+        if (pass) {
             remainder_pass();
             if (!ok) break;
         }
@@ -865,12 +896,19 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
             if ((kept >> i) & 1u) a.result[at++] = i;
         for (; at < a.M + 2; ++at) a.result[at] = -1;
     }
-    if constexpr (CLUSTER) return;
+    if constexpr (CLUSTER) {
+        if (any_near) {  // in every block or in none
+            ok = grid_barrier<CLUSTER>(a, ++barriers, &S.flag);  // all have read
+            if (blockIdx.x == 0 && tid < MUSER_MAX_M) a.near[tid] = 0;
+        }
+        return;
+    }
     // the last block to leave zeroes the counters for the next call
     __syncthreads();
     if (tid == 0 && atom_add_acq_rel_gpu(a.sync + 1, 1u) == gridDim.x - 1) {
         a.sync[0] = 0;
         a.sync[1] = 0;
+        for (int i = 0; i < MUSER_MAX_M; ++i) a.near[i] = 0;
     }
 }
 
@@ -972,6 +1010,7 @@ int launch_verify(const float* target, const float* draft, const int32_t* tokens
     const Scratch L = layout();
     uint8_t* p = static_cast<uint8_t*>(scratch);
     a.sync = reinterpret_cast<unsigned*>(p);
+    a.near = reinterpret_cast<uint64_t*>(p + 128);  // of the 256 bytes that are left zero
     a.part = reinterpret_cast<float2*>(p + L.part);
     a.sums = reinterpret_cast<uint64_t*>(p + L.sums);
     a.exps = reinterpret_cast<int*>(p + L.exps);

@@ -545,6 +545,57 @@ def test_verify_next_token_after_a_nearly_certain_one(V, blocks, rest):
             assert c.check().tolist() == [1, v, 0, -1]
 
 
+@pytest.mark.parametrize("V", [3000, 50257, 202048])
+@pytest.mark.parametrize("noise", [1e-5, 1e-4, 1e-2])
+def test_verify_next_token_where_the_rows_are_nearly_equal(V, noise):
+    """A drafter whose logits differ by `noise` (the same model in other numerics): what a rejection leaves is that small,
+    and uniform[0] points at the middle of a token's share of it.  A token's weight is off by 2^-37 of itself and 2^-43 of
+    the row's largest (at most e^10 of it): 2^-37 / noise + 2^-28.5 / noise of its share, 3e-4 at most, and at random along
+    the cumulative sum (450 steps at most for 202,048 tokens: 0.13 of a share)."""
+    rng = np.random.default_rng(V)
+    c = Verify(2, V, CHAIN, 1.0, True, 2)
+    c.target[0] = np.clip(rng.standard_normal(V), -4, 4)
+    c.draft[0] = c.target[0] + np.float32(noise) * rng.standard_normal(V).astype(np.float32)
+    p, q = (np.exp(t[0].astype(np.float64)) for t in (c.target, c.draft))
+    p, q = p / p.sum(), q / q.sum()
+    c.tokens[1] = np.argmin(p / q)               # rejected: p / q is 1 - 3 noise, against u = 1 - 2^-24
+    c.u[1] = 1 - 2.0 ** -24
+    left = np.maximum(p - q, 0)
+    total = np.cumsum(left)
+    wrong = []
+    for v in rng.choice(np.flatnonzero(left > 0.1 * noise / V), 40):
+        c.u[0] = (total[v] - left[v] / 2) / total[-1]
+        want, got = c.want(), c.run()
+        assert want.tolist() == [1, v, 0, -1]
+        wrong += [] if np.array_equal(got, want) else [(int(got[1]), int(v))]
+    assert not wrong, wrong
+
+
+@pytest.mark.parametrize("V", [3000, 50257])
+@pytest.mark.parametrize("offset", [0.0, 100.0, 900.0])
+def test_verify_next_token_where_the_rows_lie_apart(V, offset):
+    """The draft's logits lie `offset` lower (the same distribution): at temperature 0.1 the binary32 sums of the rows then
+    differ by up to 9,000 log2(e) 2^-25 = 4e-4 of themselves.  The rows differ by 0.02 in logit / temperature; weights are
+    good to 2^-33 there, 2^-33 / 0.02 = 6e-9 of a token's share, and a share is at least 1e-6 of the sum."""
+    rng = np.random.default_rng(V + 1)
+    c = Verify(2, V, CHAIN, 0.1, True, 2)
+    c.target[0] = 1000 + 0.1 * np.clip(rng.standard_normal(V), -4, 4)
+    c.draft[0] = c.target[0] - offset + 0.002 * rng.standard_normal(V)
+    p, q = (np.exp((t[0].astype(np.float64) - float(t[0].max())) / c.T) for t in (c.target, c.draft))
+    p, q = p / p.sum(), q / q.sum()
+    c.tokens[1] = np.argmin(p / q)
+    c.u[1] = 1 - 2.0 ** -24
+    left = np.maximum(p - q, 0)
+    total = np.cumsum(left)
+    wrong = []
+    for v in rng.choice(np.flatnonzero(left > 0.1 * left.sum() / V), 40):
+        c.u[0] = (total[v] - left[v] / 2) / total[-1]
+        want, got = c.want(), c.run()
+        assert want.tolist() == [1, v, 0, -1]
+        wrong += [] if np.array_equal(got, want) else [(got.tolist(), int(v))]
+    assert not wrong, wrong
+
+
 def test_verify_masked_logits_and_sharp_rows():
     for T in (1.0, 0.05):
         for seed in range(4):
