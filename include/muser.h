@@ -576,7 +576,8 @@ size_t muser_kv_tree_attention_scratch_bytes(int64_t kv_dim, int64_t head_dim, i
  *   f32 [M * n_heads*head_dim]; k, v: device f32 [M * kv_dim], used as
  *   muser_kv_ring_write would store them (rounded to binary16).  Scores, the
  *   softmax and the sums are binary32.  n_heads is a multiple of kv_heads;
- *   head_dim <= 256, n_heads <= 1024 (MUSER_ERR_UNSUPPORTED).
+ *   head_dim <= 256, n_heads <= 1024 (MUSER_ERR_UNSUPPORTED); |scale| up to
+ *   2.35e38 (its product with log2(e) is binary32).
  *   scratch: device memory of muser_kv_tree_attention_scratch_bytes(),
  *   16-byte aligned, zero-filled before its first use.  It holds partial
  *   results and is not left zero-filled: lend it to no call that wants that.

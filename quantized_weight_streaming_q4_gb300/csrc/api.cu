@@ -1216,7 +1216,8 @@ int muser_kv_tree_attention(const muser_kv_plane* plane, const muser_kv_plane* s
             return set_error(MUSER_ERR_INVALID_ARG, "%s: the sink plane's kv_dim/head_dim differ from the plane's", fn);
     }
     if (window < 0 || n_sink < 0) return set_error(MUSER_ERR_INVALID_ARG, "%s: window and n_sink must be >= 0", fn);
-    if (!std::isfinite(scale)) return set_error(MUSER_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    if (!std::isfinite(scale_log2)) return set_error(MUSER_ERR_INVALID_ARG, "%s: scale * log2(e) must be finite", fn);
     if (P.len > (int64_t{1} << 29) || (sink && sink->len > (int64_t{1} << 29)))
         return set_error(MUSER_ERR_UNSUPPORTED, "%s: more than 2^29 cached rows", fn);
     MUSER_TRY(check_f32(fn, "q", q));
@@ -1254,7 +1255,7 @@ int muser_kv_tree_attention(const muser_kv_plane* plane, const muser_kv_plane* s
     a.D = P.head_dim;
     a.G = P.kv_dim / P.head_dim;
     a.group = n_heads / a.G;
-    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    a.scale_log2 = scale_log2;
     const int64_t first = P.origin_logical, end = first + P.len;  // end: the root's position
     int deepest = 0;
     for (int i = 0; i < M; ++i) deepest = std::max(deepest, depth[i]);

@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(Layout<R>::kThreads, 1)
                 if (!fine) atomicOr(flags, 1u);
                 if ((th & 7) == 0) reinterpret_cast<float*>(smem + L::kMaxOff)[w * 16 + qr] = dot;
             }
-            const int e = min(100, max(-100, ((__float_as_int(mx) >> 23) & 0xff) - 127)) - 7;
+            const int e = min(127, max(-119, ((__float_as_int(mx) >> 23) & 0xff) - 127)) - 7;
             const float up = __int_as_float((127 - e) << 23);
             if ((th & 7) == 0) cs[w * 16 + qr] = __int_as_float((127 + e) << 23);
 #pragma unroll

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const __grid_constan
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int e = min(100, max(-100, ((__float_as_int(mx) >> 23) & 0xff) - 127)) - 7;
+            const int e = min(127, max(-119, ((__float_as_int(mx) >> 23) & 0xff) - 127)) - 7;
             const float f = __int_as_float((127 - e) << 23);
             if (lane == 0) cs[rr] = __int_as_float((127 + e) << 23);
 #pragma unroll

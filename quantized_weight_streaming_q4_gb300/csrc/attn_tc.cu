@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             half[w * 128 + row] = mx;
             named_barrier_sync(1, 256);
             mx = fmaxf(mx, half[(w ^ 1) * 128 + row]);
-            const int e = min(100, max(-100, ((__float_as_int(mx * fabsf(a.scale_log2)) >> 23) & 0xff) - 127)) - 7;
+            const int e = min(127, max(-119, ((__float_as_int(mx * fabsf(a.scale_log2)) >> 23) & 0xff) - 127)) - 7;
             const float qscale = a.scale_log2, up = __int_as_float((127 - e) << 23), down = __int_as_float((127 + e) << 23);
 #pragma unroll
             for (int h = 0; h < DP / 64; ++h) {  // 32 elements: 16 columns of the high parts and 16 of the low ones

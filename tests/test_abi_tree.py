@@ -158,6 +158,13 @@ def test_sizes_beyond_the_kernels_indexes_are_refused(L):
     assert verify(L, T=1e31) == -1 and verify(L, T=5e-324) == -1
 
 
+def test_a_scale_that_overflows_in_base_2_is_refused(L):
+    """The kernels' exponentials are of base 2: the scale times log2(e) is held in binary32 as well."""
+    assert attend(L, scale=2.4e38) == -1 and "scale" in mu.muser_last_error()
+    assert attend(L, scale=-2.4e38) == -1
+    assert attend(L, scale=2.3e38, nbytes=1024) == -1 and "scratch_bytes" in mu.muser_last_error()
+
+
 def test_binding_converts_arrays_of_other_types(L):
     """A c_int64 or numpy array is converted, not read as if it held 32-bit integers."""
     import numpy as np

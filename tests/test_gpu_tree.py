@@ -209,6 +209,30 @@ def test_attention_large_queries_and_sharp_softmax(H, kvh, D):
     c.to_device().call().check()
 
 
+@pytest.mark.parametrize("H,kvh,D", [(32, 2, 128), (5, 1, 64), (4, 2, 24), (4, 1, 256), (4, 1, 7)])
+@pytest.mark.parametrize("M", [1, 2, 9])
+@pytest.mark.parametrize("power", [-140, -110, 100, 117])
+def test_attention_scores_at_the_ends_of_binary32(H, kvh, D, M, power):
+    """scale = 2^power: finite scores of up to 2^117 (a sum of D products below 2^7 times log2(e): 2^126), whose largest
+    takes all the weight, and vanishing ones, whose weights are alike."""
+    c = Case(M, H, kvh, D, 300, 300, 0, False, seed=25)
+    c.q = np.clip(c.q, -3, 3) / np.float32(D / 4)
+    c.scale = 2.0 ** power
+    c.to_device().call()
+    n = M * H * D
+    got, want = host(c.out)[:n].reshape(M, -1), c.want()
+    assert np.isfinite(got).all()
+    if power < 0:
+        assert np.abs(got - want).max() <= 2.0 ** -18      # a mean of 300 values up to 5: 5 (300 / 32 + 8) 2^-24
+    else:   # one row's value, unless two scores are within the binary32 sums' error, 2^-17 of themselves
+        k = np.concatenate([c.key.view(np.float16).reshape(300, kvh, D), c.k.astype(np.float16).reshape(M, kvh, D)]).astype(np.float64)
+        for i in range(M):
+            for h in range(H):
+                sc = np.sort(k[:301 + i, h // (H // kvh)] @ c.q.reshape(M, H, D)[i, h].astype(np.float64))
+                if sc[-1] - sc[-2] > 2.0 ** -15 * np.abs(sc).max():
+                    assert np.abs(got - want).reshape(M, H, D)[i, h].max() <= 2.0 ** -18, (i, h)
+
+
 @pytest.mark.parametrize("H,kvh,D", [(32, 2, 128), (16, 2, 128), (5, 1, 64), (4, 2, 24), (4, 1, 256), (4, 1, 7)])
 @pytest.mark.parametrize("M", [1, 2, 9])
 @pytest.mark.parametrize("falling", [False, True])
