@@ -574,8 +574,11 @@ size_t muser_kv_tree_attention_scratch_bytes(int64_t kv_dim, int64_t head_dim, i
  *   plane: host struct, read only, head_dim set in both layouts; sink: the
  *   same kv_dim and head_dim, either layout, or NULL.  q, out, gate: device
  *   f32 [M * n_heads*head_dim]; k, v: device f32 [M * kv_dim], used as
- *   muser_kv_ring_write would store them (rounded to binary16).  Scores, the
- *   softmax and the sums are binary32.  n_heads is a multiple of kv_heads;
+ *   muser_kv_ring_write would store them (rounded to binary16).  Scores,
+ *   maxima and sums are binary32; for the tensor cores a query vector and the
+ *   weights are each the sum of two binary16 numbers (22 bits, a query
+ *   element's relative to its vector's largest), and exponentials and the last
+ *   division are good to about 2^-22.  n_heads is a multiple of kv_heads;
  *   head_dim <= 256, n_heads <= 1024 (MUSER_ERR_UNSUPPORTED); |scale| up to
  *   2.35e38 (its product with log2(e) is binary32).
  *   scratch: device memory of muser_kv_tree_attention_scratch_bytes(),
@@ -619,11 +622,13 @@ size_t muser_tree_verify_scratch_bytes(int64_t vocab, int M);
  *   with a NaN, a +infinity, only -infinities, or a largest logit /
  *   temperature beyond about +-22,000.  vocab <= 2^20, temperature 0 or
  *   0.001..1e30.
- *   Acceptance is decided to about 2^-19 of the compared probabilities (equal
- *   rows accept every token).  The next token is that of exact arithmetic to
- *   about 2^-37 of the cumulative sum (2^-33 where logit / temperature is in
- *   the thousands); a probability below 2^-41 of the row's largest, or a
- *   remainder that small, may count as nothing.
+ *   Acceptance is decided to about 2^-19 of the compared probabilities (p_r and
+ *   c * q_r; equal rows accept every token).  The next token is that of exact
+ *   arithmetic to about 2^-37 of the row's cumulative sum (2^-33 where logit /
+ *   temperature is in the thousands), also where draft rows leave little of it;
+ *   without draft rows, of the cumulative sum of the tokens that are left.  A
+ *   probability below 2^-41 of the largest of these tokens, or a remainder that
+ *   small, may count as nothing.
  *   Sampling with M > 1 is one launch whose blocks wait for one another: a
  *   cooperative one (bounded in time, muser_device_status() bit 1, result
  *   then unwritten), or over few logits one thread-block cluster.

@@ -258,7 +258,7 @@ int launch_generic(AttnArgs a, void* scratch, cudaStream_t s) {
 // The split of the common rows for the tensor-core kernels (tiles of 128 keys,
 // one block per SM, `heads` K/V heads times row blocks): clusters of c blocks,
 // k of them a head.  One cluster joins its blocks' results itself; more leave
-// parts for a second kernel (2.7 us).  A tile takes a block `tile_us`, or
+// parts for a second kernel (2.7 us; 5.9 for 512 rows of 19 parts).  A tile takes a block `tile_us`, or
 // `tile_full_us` where all SMs share the memory's rate, and beside its tiles 5
 // us, or 3.5 where it joins no other; clusters beyond those that run at once wait for a turn (of 16 blocks
 // 7 clusters are resident).  Measured, one token, 16 K/V heads of 64, 2,048

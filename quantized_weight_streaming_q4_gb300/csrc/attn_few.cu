@@ -22,7 +22,7 @@
 // rounding.  O tiles are fresh accumulators added in registers.
 //
 // Bound: the planes' bytes for long caches (TMA, three stages of 64 KB in
-// flight a block), latency for short ones.
+// flight a block, two for 32 rows), latency for short ones.
 #include <algorithm>
 
 #include "attn.cuh"

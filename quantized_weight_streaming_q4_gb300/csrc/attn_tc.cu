@@ -27,9 +27,11 @@
 // split 40 : 144 : 144 : 184 a thread; a stream that held all 128 scores of its
 // row spilled (83 us below).
 //
-// Bound: the tensor pipe, 32 products of 64 cycles a tile, 2,050 of about 2,500
-// cycles (16 rows, 130,815 rows: 56 us); for short caches what comes before the
-// first product and behind the last (16 rows, 2,048 rows: 12 us).
+// Bound: the tensor pipe, 32 products of 64 cycles a tile, 2,050 of about 2,700
+// cycles; of the 57 to 60 us of 16 rows over 130,815 rows that is 38, beside 7.5
+// from the launch to the first scores, 6.2 for the join and 5.9 for the second
+// kernel.  For short caches what comes before the first product and behind the
+// last (16 rows, 2,048 rows: 12 us).
 #include <algorithm>
 
 #include "attn.cuh"
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
         }
         __syncwarp();
-        // This warpgroup has 56 registers a thread: it shares no code with the
+        // This warpgroup has 40 registers a thread: it shares no code with the
         // others from here on, only the barriers.
         tc_fence_before();
         if (a.cluster > 1) {

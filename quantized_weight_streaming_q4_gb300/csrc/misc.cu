@@ -200,7 +200,7 @@ __global__ void kv_store_kernel(uint16_t* key, uint16_t* value, const float* k, 
 // The accepted rows of a drafted tree, binary32 to binary16, into the planes
 // of many layers: blockIdx.y is the plane, a thread takes 8 (vec) or 1
 // consecutive elements of one row of K and of V.
-// The launch copies its parameters, 64 bytes a plane: N is the least of 4, 64
+// The launch copies its parameters, 72 bytes a plane: N is the least of 4, 64
 // and 128 that takes them.
 template <int N>
 struct CommitParams {

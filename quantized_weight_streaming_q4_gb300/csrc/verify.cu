@@ -65,7 +65,7 @@ struct VerifyArgs {
     int slices, slice_len; // of a row in the first pass
     int span;              // tokens per block in the passes over one node
     unsigned* sync;        // arrivals, exits
-    uint64_t* near;        // [MUSER_MAX_M] by node, see kFirst
+    unsigned* near;        // [MUSER_MAX_M] by node, see kFirst
     float2* part;          // [kRows][kMaxSlices] (sum, exponent); greedy: uint64 keys
     uint64_t* sums;        // [2][kMaxBlocks][4]: two passes' buffers in turn, a record a block
     int* exps;             // [kMaxBlocks]
@@ -284,7 +284,7 @@ struct Shared {
     // the sampled point: its block (-1: nothing to sample, -2: no distribution), the place in its share
     int owner, exp;
     uint64_t before;
-    uint64_t near[MUSER_MAX_M], near_all;  // kFirst: draft weights near f0, the block's by node, all blocks'
+    unsigned near[MUSER_MAX_M], near_all;  // kFirst: draft weights near f0, the block's by node, all blocks'
     int flag, found;
     int cur, n;  // the walk along accepted first children
     uint32_t kept;
@@ -389,6 +389,8 @@ __device__ __forceinline__ uint64_t fraction_of(float u, uint64_t total) {
 //  kNext   a further rejected child, or the row itself: the shares.
 // Leaves the remainder's size, and the sampled point's block and place there.
 enum PassKind { kLeaf, kFirst, kNext };
+constexpr int kNearUnit = 16;             // bits of a unit in which Q near f0 is added up
+constexpr unsigned kNearMost = 1u << 18;  // units of a token or a block: more counts as all of Q
 template <PassKind KIND>
 __device__ __forceinline__ void settle(const VerifyArgs& a, Shared& S, unsigned barriers) {
     if (threadIdx.x < 32) {
@@ -792,7 +794,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
         bool pass = rejected;
         if (!rejected) {  // the node's weights, to shared memory
             const int Rp = static_cast<int>(S.row_exp[tr]) + 1, Rq = static_cast<int>(S.row_exp[dr]) + 1;
-            uint64_t fm, near = 0, v[4] = {0, 0, 0, 0};
+            uint64_t fm, v[4] = {0, 0, 0, 0};
+            unsigned near = 0;  // in units of 2^kNearUnit, upwards
             int fe;
             split_factor(S.row_sum[tr] / S.row_sum[dr], fm, fe);
             const float* pr = row_ptr(a, tr) + P.v0;
@@ -818,19 +821,18 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
                         v[3] += z;
                     }
                     // (below 2^20 units what such a token is off by is less than one)
-                    if ((w > fz ? w - fz : fz - w) <= (fz >> 20)) near += z;
+                    if ((w > fz ? w - fz : fz - w) <= (fz >> 20) && z != 0) near += min(static_cast<unsigned>(z >> kNearUnit) + 1, kNearMost);
                 }
             }
             if (__any_sync(0xffffffffu, near != 0)) {
-                near = warp_sum64(near);
-                if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&S.near[cur]), static_cast<unsigned long long>(near));
+                near = __reduce_add_sync(0xffffffffu, near);
+                if (lane == 0) atomicAdd(&S.near[cur], near);
             }
             publish(a, S, v, ++barriers);
-            if (tid == 0 && S.near[cur] != 0)
-                atomicAdd(reinterpret_cast<unsigned long long*>(a.near + cur), static_cast<unsigned long long>(S.near[cur]));
+            if (tid == 0 && S.near[cur] != 0) atomicAdd(a.near + cur, min(S.near[cur], kNearMost));
             ok = grid_barrier<CLUSTER>(a, barriers, &S.flag);
             if (!ok) break;
-            if (tid == 32) S.near_all = ldcg64(a.near + cur);  // beside warp 0
+            if (tid == 32) S.near_all = __ldcg(a.near + cur);  // beside warp 0
             settle<kFirst>(a, S, barriers);
             rejected = true;
             const uint64_t apart = S.fe == fe ? (S.fm > fm ? S.fm - fm : fm - S.fm)
@@ -839,8 +841,16 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
             pass = apart >> (one - 20) != 0;
             if (S.near_all != 0) {
                 any_near = true;
-                const float off = static_cast<float>(apart) * __int_as_float((127 - one) << 23);
-                pass = pass || off * (static_cast<float>(S.near_all) / static_cast<float>(S.sum_q)) > fminf(0x1p-38f, 0x1p-20f * S.left_f);
+                // the same times near / sum Q, each as a power of 2 not below it, then as it is
+                const bool all = S.near_all >= kNearMost;
+                const int bound = 64 - __clzll(static_cast<long long>(apart)) - one +
+                                  (all ? 0 : 32 - __clz(static_cast<int>(S.near_all)) + kNearUnit - 63 + __clzll(static_cast<long long>(S.sum_q)));
+                const int most = min(-38, -20 + (__float_as_int(S.left_f) >> 23) - 127);
+                if (bound > most) {
+                    const float off = static_cast<float>(apart) * __int_as_float((127 - one) << 23);
+                    const float share = all ? 1.f : static_cast<float>(S.near_all) * (1 << kNearUnit) / static_cast<float>(S.sum_q);
+                    pass = pass || off * share > fminf(0x1p-38f, 0x1p-20f * S.left_f);
+                }
             }
         } else {
             __syncthreads();  // every thread has read the last remainder's c
@@ -908,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
     if (tid == 0 && atom_add_acq_rel_gpu(a.sync + 1, 1u) == gridDim.x - 1) {
         a.sync[0] = 0;
         a.sync[1] = 0;
-        for (int i = 0; i < MUSER_MAX_M; ++i) a.near[i] = 0;
+        for (int i = 0; i < MUSER_MAX_M / 4; ++i) reinterpret_cast<uint4*>(a.near)[i] = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -1010,7 +1020,7 @@ int launch_verify(const float* target, const float* draft, const int32_t* tokens
     const Scratch L = layout();
     uint8_t* p = static_cast<uint8_t*>(scratch);
     a.sync = reinterpret_cast<unsigned*>(p);
-    a.near = reinterpret_cast<uint64_t*>(p + 128);  // of the 256 bytes that are left zero
+    a.near = reinterpret_cast<unsigned*>(p + 128);  // of the 256 bytes that are left zero
     a.part = reinterpret_cast<float2*>(p + L.part);
     a.sums = reinterpret_cast<uint64_t*>(p + L.sums);
     a.exps = reinterpret_cast<int*>(p + L.exps);
