@@ -271,6 +271,8 @@ struct Shared {
     uint64_t table[kVerifyTable];
     uint64_t warp[4][kWarps];
     float warp_max[kWarps], warp_left[kWarps];
+    int slice[MUSER_MAX_M], slices;  // those with a child's token
+    uint32_t slice_kids[MUSER_MAX_M];
     float row_sum[kRows], row_exp[kRows];  // a row's sum (NaN: no distribution) and exponent
     float px[MUSER_MAX_M], qx[MUSER_MAX_M], u[MUSER_MAX_M];  // of node i: p(x_i), q(x_i) in its parent's rows
     int token[MUSER_MAX_M];
@@ -707,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
     uint32_t kept = S.kept, removed = 0u;
     const uint32_t first = S.first, fine = S.fine;
     bool valid = true, rejected = false;  // rejected: the node's weights are held, S describes its remainder
-    float left = 1.f, c = 0.f;
+    float left = 1.f, c = 0.f, rest = -1.f;
     auto remainder = [&](int k) {  // max(P - f Q, 0)
         const uint64_t fq = S.fm ? times_f(wq[k], S.fm, S.fe) : 0;
         return wp[k] > fq ? wp[k] - fq : 0;
@@ -719,45 +721,63 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
         ok = grid_barrier<CLUSTER>(a, barriers, &S.flag);
         if (ok) settle<kNext>(a, S, barriers);
     };
-    // Drafts that are certain: what is left of the node's row without the tokens
-    // of `gone`, as a sum of the others, every block the same one.  As 1 - p it
-    // would be a rounding error where p is nearly 1.  The slices without such a
-    // token are summed already; the others are read anew.
-    auto left_without = [&](int row, uint32_t gone) {
+    // Drafts that are certain: what is left of a row without the rejected tokens,
+    // as a sum of the others, every block the same one.  As 1 - p it would be a
+    // rounding error where p is nearly 1.  A node's sum over the tokens that are
+    // no child's is made once: the slices without such a token are summed
+    // already, the others are read anew.
+    auto rest_of = [&](int row, uint32_t kids) {
         const float R = S.row_exp[row];
         const float* p = row_ptr(a, row);
-        auto hits = [&](int x, int lo, int hi) { return x >= lo && x < min(hi, a.V); };
+        __syncthreads();  // the last call's sums have been read
+        if (warp == 0) {
+            const bool mine = lane < a.M && ((kids >> lane) & 1u) && S.token[lane] >= 0 && S.token[lane] < a.V;
+            const int slice = mine ? S.token[lane] / a.slice_len : -1 - lane;
+            const uint32_t same = __match_any_sync(0xffffffffu, slice);  // of every lane
+            const bool lead = mine && (same & ((1u << lane) - 1u)) == 0;
+            const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+            if (lead) {
+                S.slice[__popc(leads & ((1u << lane) - 1u))] = slice;
+                S.slice_kids[__popc(leads & ((1u << lane) - 1u))] = same;
+            }
+            if (lane == 0) S.slices = __popc(leads);
+        }
+        __syncthreads();
         float sum = 0.f;
         if (tid < a.slices) {
             bool whole = true;
-            for (uint32_t r = gone; r; r &= r - 1) whole = whole && !hits(S.token[__ffs(r) - 1], tid * a.slice_len, (tid + 1) * a.slice_len);
+            for (int i = 0; i < S.slices; ++i) whole = whole && S.slice[i] != tid;
             if (whole) {
                 const float2 w = __ldcg(a.part + row * kMaxSlices + tid);
                 sum = w.x * ex2(w.y - R);
             }
         }
-        for (uint32_t r = gone; r; r &= r - 1) {
-            const int x = S.token[__ffs(r) - 1];
-            if (!hits(x, 0, a.V)) continue;
-            const int lo = x / a.slice_len * a.slice_len, hi = min(lo + a.slice_len, a.V);
-            bool done = false;  // by an earlier token of the same slice
-            for (uint32_t e = gone & ((r & -r) - 1); e; e &= e - 1) done = done || hits(S.token[__ffs(e) - 1], lo, hi);
-            if (done) continue;
-            for (int k = lo + tid; k < hi; k += kThreads) {
-                bool out = false;
-                for (uint32_t e = gone; e; e &= e - 1) out = out || S.token[__ffs(e) - 1] == k;
-                const float w = ex2(fmaf(__ldcg(p + k), a.c_hi, -R));
-                if (!out) sum += w;
+        const int slices = S.slices, len = a.slice_len;
+        constexpr int kBatch = 8;  // loads in flight together
+        for (int k0 = tid; k0 < slices * len; k0 += kBatch * kThreads) {
+            float x[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int k = k0 + u * kThreads, i = k / len;
+                const int v = i < slices ? (S.slice[i] - i) * len + k : a.V;
+                x[u] = v < a.V ? __ldcg(p + v) : -INFINITY;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int k = k0 + u * kThreads, i = k / len;
+                for (uint32_t e = i < slices ? S.slice_kids[i] : 0u; e; e &= e - 1)
+                    if (S.token[__ffs(e) - 1] == (S.slice[i] - i) * len + k) x[u] = -INFINITY;
+                sum += ex2(fmaf(x[u], a.c_hi, -R));
             }
         }
         sum = warp_sum(sum);
-        __syncthreads();  // the last call's sums have been read
         if (lane == 0) S.warp_left[warp] = sum;
         __syncthreads();
         sum = 0.f;
         for (int w = 0; w < kWarps; ++w) sum += S.warp_left[w];
         return sum / S.row_sum[row];
     };
+    uint32_t alike = 0;  // the node's children with this lane's child's token
     uint32_t children = a.children[cur];  // of the present node, not tried yet
     while (children && ok) {
         const int i = __ffs(children) - 1;
@@ -778,6 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
             removed = 0;
             c = 0.f;
             left = 1.f;
+            rest = -1.f;
             rejected = false;
             continue;
         }
@@ -786,7 +807,16 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(const __grid_consta
             removed |= 1u << i;
             if (children && !again) {  // a difference is as good as a sum while more than half of the row is left
                 left -= S.px[i];
-                if (left < 0.5f) left = left_without(a.target_at[cur], removed);
+                if (left < 0.5f) {
+                    const uint32_t kids = a.children[cur];
+                    const bool child = lane < a.M && ((kids >> lane) & 1u);
+                    if (rest < 0.f) {
+                        rest = rest_of(a.target_at[cur], kids);
+                        alike = __match_any_sync(0xffffffffu, child ? S.token[lane] : static_cast<int>(0x80000000u) + lane) & kids;
+                    }
+                    // and the probabilities of the other children's tokens, each once
+                    left = rest + warp_sum(child && !(alike & removed) && !(alike & ((1u << lane) - 1u)) ? S.px[lane] : 0.f);
+                }
             }
             continue;
         }
