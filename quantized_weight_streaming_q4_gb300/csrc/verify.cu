@@ -548,9 +548,14 @@ __device__ __forceinline__ void leaf_pass(const VerifyArgs& a, Shared& S, const 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float mx = -INFINITY;
     bool bad = false;
+    uint32_t mine = 0;  // of `removed`, those whose token is this thread's
+    for (uint32_t r = removed; r; r &= r - 1) {
+        const int k = S.token[__ffs(r) - 1] - P.v0;
+        if (k >= P.first && k < P.last) mine |= r & -r;
+    }
     each_logit(P, row, [&](int k, float x) {
         bad |= !(x < INFINITY);
-        for (uint32_t r = removed; r; r &= r - 1)
+        for (uint32_t r = mine; r; r &= r - 1)
             if (S.token[__ffs(r) - 1] == P.v0 + k) x = -INFINITY;
         mx = fmaxf(mx, x);
         logit[k] = x;
