@@ -658,6 +658,184 @@ int muser_kv_tree_commit(muser_kv_plane* planes, int n_planes, const float* cons
                          const int32_t* path, int n, int64_t position, void* stream);
 
 /*
+ * Several sequences, or beams, at once.  The rows of a pass then belong to
+ * different sequences, whose cached K/V rows lie in pages: a layer's cache is
+ * `pages` pages of page_rows token rows, and a table (device memory) says of
+ * each sequence which page holds its rows k*page_rows .. (k+1)*page_rows-1.
+ * The tables are one for all layers that keep the same rows.  Everything that
+ * changes from step to step (tables, lengths, positions, slots) is device
+ * memory, so a step can be captured into a graph and replayed.  One step is
+ * muser_kv_page_tables; in each layer muser_qmatvec_group and
+ * muser_kv_paged_attention, which also stores the new rows; muser_lm_head; and
+ * the choice of the tokens, of beams with muser_beam_select, whose `parent`
+ * and `add` are the next step's muser_kv_page_tables arguments, with
+ * muser_kv_page_copy behind it.  A prompt's rows are stored with
+ * muser_kv_page_write and then attended to with k = v = NULL.
+ */
+#define MUSER_MAX_SEQUENCES 256
+
+/*
+ * A layer's paged K/V cache.  key/value are device binary16 buffers of
+ * pages*page_rows*kv_dim halves.  Token-major index of element e of row r of
+ * page p: (p*page_rows + r)*kv_dim + e; head-major: ((p*kv_heads +
+ * e/head_dim)*page_rows + r)*head_dim + e%head_dim.  The struct is host memory
+ * and never written.
+ */
+typedef struct {
+    uint16_t* key;
+    uint16_t* value;
+    int64_t pages;
+    int32_t page_rows;
+    int32_t kv_dim;
+    int32_t head_dim;
+    int32_t head_major;
+    int32_t reserved;
+} muser_kv_pages;
+
+/*
+ * muser_kv_page_tables -- the page tables of the next step from the present
+ *   ones and the rows that each sequence gains or loses.  Row i of the new
+ *   tables goes on from sequence p = parent[i] (NULL: i; -1: an empty one), of
+ *   L = length[p] rows, and has max(0, L + add[i]) rows (add NULL: 1 each).  Of
+ *   its rows the first keep = min(L, L + add[i]) are p's: they lie in the same
+ *   pages.  The page that row `keep` would go into, where it is partly filled
+ *   and the sequence grows, is its own: if another new sequence holds that page
+ *   too, all but one of them (the lowest i, where all of them grow in it; none,
+ *   where one holds it without growing in it) get another page, and the triple
+ *   (old page, new page, rows to copy) goes into `copies`.  Further pages are
+ *   those that no new table holds, the lowest first, given to the rows in
+ *   order, a copied page before new ones.  Pages that no table holds any more
+ *   are thereby free.  With a window, a page whose rows lie before it (below
+ *   keep - window + 1) and are not among the first n_sink is given up: its
+ *   entry becomes -1.  Entries outside 0..pages-1 stay as they are and hold
+ *   nothing.
+ *   table: device int32 [n_old][stride], length: [n_old]; parent, add: [n] or
+ *   NULL; a parent outside -1..n_old-1 counts as -1.  table_out: [n][stride];
+ *   entries from ceil(rows/page_rows) on are left as they were.  length_out,
+ *   last: [n]; last[i] is the position of row i's newest row if the sequence
+ *   grew, else -1: the `position` of a pass with one new row each.  first:
+ *   [n+1], the number of new rows of the sequences before i.  slots, position,
+ *   sequence: [max_new]; new row first[i] + j of sequence i is at position
+ *   keep + j, in slot page*page_rows + position%page_rows of the cache; entries
+ *   behind the last new row become -1.  copies: [3n], only the triples are
+ *   written.  result: [8]: status, new rows, copies, pages taken, pages free
+ *   afterwards, 0, 0, 0.  last, first, slots, position, sequence may be NULL;
+ *   copies only where parent is NULL too and no two sequences share a partly
+ *   filled page (else result reports status 4).  Outputs overlap nothing,
+ *   except that with parent NULL table_out may be table and length_out length.
+ *   status 0: done.  1: too few free pages; 2: a sequence beyond
+ *   stride*page_rows rows; 3: more than max_new new rows (slots, position or
+ *   sequence given); 4: see copies.  Then no sequence grows (add counts as
+ *   min(add, 0)), there are no new rows and no copies.
+ *   n, n_old <= MUSER_MAX_SEQUENCES; pages <= 2^20; pages*page_rows < 2^31;
+ *   stride*page_rows <= 2^27.
+ */
+int muser_kv_page_tables(const int32_t* table, const int32_t* length, int n_old, const int32_t* parent,
+                         const int32_t* add, int n, int64_t stride, int64_t pages, int page_rows, int64_t window,
+                         int64_t n_sink, int32_t* table_out, int32_t* length_out, int32_t* last, int32_t* first,
+                         int32_t* slots, int32_t* position, int32_t* sequence, int64_t max_new, int32_t* copies,
+                         int32_t* result, void* stream);
+
+/*
+ * muser_kv_page_copy -- copies[j] = (source page, destination page, rows), j <
+ *   *count: the first `rows` rows of the page, K and V, in the caches of up to
+ *   128 layers, in one launch.
+ *   layers: host array, equal but for key and value; copies: device int32
+ *   [3*max_copies]; count: device int32, read as at most max_copies (result + 2
+ *   of muser_kv_page_tables).  Triples with a page outside the cache are
+ *   skipped, rows count as at most page_rows.  No destination is a source or
+ *   another destination.
+ */
+int muser_kv_page_copy(const muser_kv_pages* layers, int n_layers, const int32_t* copies, const int32_t* count,
+                       int max_copies, void* stream);
+
+/*
+ * muser_kv_page_write -- store rows of K and V in a layer's cache, rounded to
+ *   binary16 (to nearest even): row j of k and v in slot slots[j], the slots of
+ *   muser_kv_page_tables.  A slot outside the cache (-1) is skipped.
+ *   k, v: device f32 [rows*kv_dim], 4-byte aligned (16-byte alignment, with
+ *   kv_dim and, head-major, head_dim multiples of 8, takes 16-byte accesses);
+ *   slots: device int32 [rows], no two alike.  rows <= 2^31-1.
+ */
+int muser_kv_page_write(const muser_kv_pages* cache, const float* k, const float* v, const int32_t* slots,
+                        int64_t rows, void* stream);
+
+/* Scratch bytes muser_kv_paged_attention needs; it does not depend on the
+ * sequences' lengths.  0 for a shape the call does not take. */
+size_t muser_kv_paged_attention_scratch_bytes(int64_t kv_dim, int64_t head_dim, int n, int n_heads);
+
+/*
+ * muser_kv_paged_attention -- attention of n token rows, each over the cached
+ *   rows of its own sequence: out[i, h] = sum_j a_j v_j, a = softmax(scale *
+ *   q[i, h] . k_j); with `gate`, times 1/(1+exp(-gate[i, h])) elementwise.
+ *   Query head h reads K/V head h / (n_heads / kv_heads).
+ *   Row i is the token at position t = position[i] of sequence sequence[i]
+ *   (NULL: i), whose pages are row sequence[i] of `table`.  It sees the row at
+ *   position p <= t if t - p < window (window 0: always) or p < n_sink; p = t,
+ *   itself, is k[i], v[i] rounded to binary16, and is stored in its place in
+ *   the cache (unless its table entry is outside 0..pages-1).  With k = v =
+ *   NULL its own row is read from the cache too: several rows of one sequence
+ *   then go in one call, once muser_kv_page_write has stored them.  With k and
+ *   v no two rows are of one sequence, and no row's page is another's that is
+ *   written to.
+ *   A row with position[i] < 0 or a sequence outside 0..n_tables-1 is left as
+ *   it was.  Rows in a page whose entry is outside 0..pages-1, or beyond the
+ *   table's stride, are not seen; a token that sees nothing gives zeros.  No
+ *   row that is not seen has any influence, whatever its slot holds.
+ *   Infinities and NaN in rows that are seen, types, precision and limits are
+ *   as for muser_kv_tree_attention (the outputs that read them are not finite,
+ *   a score of -infinity counts as weight 0 or makes the output NaN).
+ *   table: device int32 [n_tables][stride]; position, sequence: device int32
+ *   [n]; q, out, gate: device f32 [n * n_heads*head_dim]; k, v: device f32
+ *   [n * kv_dim].  n <= MUSER_MAX_SEQUENCES, head_dim <= 256, n_heads <= 1024,
+ *   stride*page_rows <= 2^27.  Page sizes that are powers of two from 8 on,
+ *   with head_dim a multiple of 8 and 16-byte aligned buffers, run on the
+ *   tensor cores.
+ *   The work is split over the device by the rows that are seen; the same
+ *   positions give the same split and bit for bit the same results.
+ *   scratch: device memory of muser_kv_paged_attention_scratch_bytes(), 16-byte
+ *   aligned, zero-filled before its first use; its first 1,024 bytes are left
+ *   zero, the rest is not.  Calls that can run at the same time must not share
+ *   it.  out and scratch overlap nothing else.
+ */
+int muser_kv_paged_attention(const muser_kv_pages* cache, const int32_t* table, int64_t stride, int n_tables,
+                             const int32_t* position, const int32_t* sequence, const float* q, const float* k,
+                             const float* v, const float* gate, int n, int n_heads, int64_t window, int64_t n_sink,
+                             float scale, float* out, void* scratch, size_t scratch_bytes, void* stream);
+
+/* Scratch bytes muser_beam_select needs (0 for sizes it does not take). */
+size_t muser_beam_select_scratch_bytes(int groups, int beams, int64_t vocab, int n);
+
+/*
+ * muser_beam_select -- one step of beam search for `groups` requests of `beams`
+ *   beams: of a request's beams r and tokens v the n with the largest
+ *   score[r] + logits[r, v] - log(sum_w exp(logits[r, w])), the largest first,
+ *   equal ones by the lower (r, v).  A beam with ended[r] != 0 goes on in one
+ *   way only, with end_token and its score unchanged.
+ *   logits: device f32 [groups*beams*vocab]; score: f32 and ended (or NULL):
+ *   int32 [groups*beams].  For each request n entries: parent: the row r;
+ *   token; score_out: the sum, rounded once; ended_out (or NULL): 1 if ended[r]
+ *   or the token is end_token, else 0; add (or NULL): 1 - ended_out.
+ *   end_token -1: none, then ended is NULL.
+ *   A candidate whose sum is -infinity or NaN (a row with a NaN or +infinity, a
+ *   score of -infinity) is none.  Where a request has fewer than n, the rest
+ *   are parent -1, token -1, score -infinity, ended 1, add 0.
+ *   Log-probabilities are those of 64 bits to about 2^-24 (the sums over the
+ *   vocabulary are of binary32 exponentials); the tokens of one beam are
+ *   compared exactly.
+ *   groups*beams <= MUSER_MAX_SEQUENCES, beams <= 32, n <= 64 and <=
+ *   beams*vocab, vocab <= 2^20.  With n == beams, score_out may be score and
+ *   ended_out ended; else outputs and scratch overlap nothing.
+ *   scratch: device memory of muser_beam_select_scratch_bytes(), 16-byte
+ *   aligned, zero-filled before its first use; its first 1,024 bytes are left
+ *   zero, the rest is not.  Calls that can run at the same time must not share
+ *   it.
+ */
+int muser_beam_select(const float* logits, const float* score, const int32_t* ended, int groups, int beams,
+                      int64_t vocab, int n, int32_t end_token, int32_t* parent, int32_t* token, float* score_out,
+                      int32_t* ended_out, int32_t* add, void* scratch, size_t scratch_bytes, void* stream);
+
+/*
  * muser_sync -- wait until all work enqueued on `stream` has finished, for at
  *   most timeout_ms milliseconds (the book's bounded wait_for_completion,
  *   Ch 2 §2.10).  Returns MUSER_OK, MUSER_ERR_TIMEOUT (the work keeps

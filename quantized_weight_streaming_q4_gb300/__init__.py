@@ -28,7 +28,9 @@ __all__ = [
     "MUSER_STATIC_SCRATCH_BYTES", "MUSER_BOUNDARY_SCRATCH_BYTES", "FfnLayer", "muser_ffn_workspace_bytes", "muser_ffn_stack_launches",
     "muser_ffn_stack", "KvPlane", "muser_kv_ring_write", "muser_kv_snapshot", "muser_kv_restore",
     "muser_kv_tree_attention_scratch_bytes", "muser_kv_tree_attention", "muser_tree_verify_scratch_bytes",
-    "muser_tree_verify", "muser_kv_tree_commit", "muser_sync", "muser_debug_spin", "muser_debug_occupy",
+    "muser_tree_verify", "muser_kv_tree_commit", "KvPages", "muser_kv_page_tables", "muser_kv_page_copy",
+    "muser_kv_page_write", "muser_kv_paged_attention_scratch_bytes", "muser_kv_paged_attention",
+    "muser_beam_select_scratch_bytes", "muser_beam_select", "muser_sync", "muser_debug_spin", "muser_debug_occupy",
     "muser_device_sm_count", "muser_device_status",
 ]
 
@@ -76,6 +78,12 @@ class KvPlane(ctypes.Structure):
                 ("origin_physical", ctypes.c_int64), ("kv_dim", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("head_major", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class KvPages(ctypes.Structure):
+    _fields_ = [("key", ctypes.c_void_p), ("value", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_rows", ctypes.c_int32), ("kv_dim", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("head_major", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def lib():
@@ -132,6 +140,14 @@ def lib():
             "muser_tree_verify_scratch_bytes": (SZ, [I64, I]),
             "muser_tree_verify": (I, [P, P, P, P, I, I64, ctypes.c_double, P, P, P, SZ, P]),
             "muser_kv_tree_commit": (I, [ctypes.POINTER(KvPlane), I, P, P, I, P, I, I64, P]),
+            "muser_kv_page_tables": (I, [P, P, I, P, P, I, I64, I64, I, I64, I64, P, P, P, P, P, P, P, I64, P, P, P]),
+            "muser_kv_page_copy": (I, [ctypes.POINTER(KvPages), I, P, P, I, P]),
+            "muser_kv_page_write": (I, [ctypes.POINTER(KvPages), P, P, P, I64, P]),
+            "muser_kv_paged_attention_scratch_bytes": (SZ, [I64, I64, I, I]),
+            "muser_kv_paged_attention": (I, [ctypes.POINTER(KvPages), P, I64, I, P, P, P, P, P, P, I, I, I64, I64, F, P, P,
+                                             SZ, P]),
+            "muser_beam_select_scratch_bytes": (SZ, [I, I, I64, I]),
+            "muser_beam_select": (I, [P, P, P, I, I, I64, I, ctypes.c_int32, P, P, P, P, P, P, SZ, P]),
             "muser_sync": (I, [P, I]),
             "muser_debug_spin": (I, [I64, P]),
             "muser_debug_occupy": (I, [I, I64, P]),
@@ -452,6 +468,71 @@ def muser_kv_tree_commit(planes, ks, vs, M: int, path, position: int, stream=Non
     if arr is not planes:
         for mine, new in zip(planes, arr):
             mine.len, mine.origin_logical, mine.origin_physical = new.len, new.origin_logical, new.origin_physical
+
+
+def _table_shape(table, rows, width):
+    """The page tables' rows and entries a row: the tensor's, where they are not given."""
+    if rows is None or width is None:
+        shape = table.shape
+        rows = shape[0] if rows is None else rows
+        width = shape[1] if width is None else width
+    return rows, width
+
+
+def muser_kv_page_tables(table, length, n: int, pages: int, page_rows: int, table_out, length_out, result, parent=None,
+                         add=None, window: int = 0, n_sink: int = 0, last=None, first=None, slots=None, position=None,
+                         sequence=None, max_new: int = 0, copies=None, n_old=None, width=None, stream=None) -> None:
+    """The next step's page tables, in device memory throughout.  table: int32
+    [n_old, width] (the sizes are taken from the tensor where they are None)."""
+    n_old, width = _table_shape(table, n_old, width)
+    _check("muser_kv_page_tables",
+           lib().muser_kv_page_tables(_ptr(table), _ptr(length), n_old, _ptr(parent), _ptr(add), n, width, pages, page_rows,
+                                      window, n_sink, _ptr(table_out), _ptr(length_out), _ptr(last), _ptr(first),
+                                      _ptr(slots), _ptr(position), _ptr(sequence), max_new, _ptr(copies), _ptr(result),
+                                      _stream(stream)))
+
+
+def muser_kv_page_copy(layers, copies, count, max_copies: int, stream=None) -> None:
+    """layers: a ctypes array of KvPages, or a list of KvPages; copies, count: device int32."""
+    if not isinstance(layers, ctypes.Array):
+        layers = (KvPages * len(layers))(*layers)
+    _check("muser_kv_page_copy",
+           lib().muser_kv_page_copy(layers, len(layers), _ptr(copies), _ptr(count), max_copies, _stream(stream)))
+
+
+def muser_kv_page_write(cache: KvPages, k, v, slots, rows: int, stream=None) -> None:
+    """Stores rows of K and V in the slots that muser_kv_page_tables gave them."""
+    _check("muser_kv_page_write", lib().muser_kv_page_write(cache, _ptr(k), _ptr(v), _ptr(slots), rows, _stream(stream)))
+
+
+def muser_kv_paged_attention_scratch_bytes(kv_dim: int, head_dim: int, n: int, n_heads: int) -> int:
+    return lib().muser_kv_paged_attention_scratch_bytes(kv_dim, head_dim, n, n_heads)
+
+
+def muser_kv_paged_attention(cache: KvPages, table, position, q, n: int, n_heads: int, out, scale: float, scratch,
+                             scratch_bytes: int, k=None, v=None, gate=None, sequence=None, window: int = 0,
+                             n_sink: int = 0, n_tables=None, width=None, stream=None) -> None:
+    """Attention of n token rows, each over its own sequence's pages; k, v: the
+    rows' own K and V, which are stored too (None: they lie in the cache).
+    table: int32 [n_tables, width] (from the tensor where they are None)."""
+    n_tables, width = _table_shape(table, n_tables, width)
+    _check("muser_kv_paged_attention",
+           lib().muser_kv_paged_attention(cache, _ptr(table), width, n_tables, _ptr(position), _ptr(sequence), _ptr(q),
+                                          _ptr(k), _ptr(v), _ptr(gate), n, n_heads, window, n_sink, scale, _ptr(out),
+                                          _ptr(scratch), scratch_bytes, _stream(stream)))
+
+
+def muser_beam_select_scratch_bytes(groups: int, beams: int, vocab: int, n: int) -> int:
+    return lib().muser_beam_select_scratch_bytes(groups, beams, vocab, n)
+
+
+def muser_beam_select(logits, score, groups: int, beams: int, vocab: int, n: int, parent, token, score_out, scratch,
+                      scratch_bytes: int, ended=None, end_token: int = -1, ended_out=None, add=None, stream=None) -> None:
+    """The n best ways on of each request's beams: rows, tokens and scores."""
+    _check("muser_beam_select",
+           lib().muser_beam_select(_ptr(logits), _ptr(score), _ptr(ended), groups, beams, vocab, n, end_token, _ptr(parent),
+                                   _ptr(token), _ptr(score_out), _ptr(ended_out), _ptr(add), _ptr(scratch), scratch_bytes,
+                                   _stream(stream)))
 
 
 def muser_sync(stream=None, timeout_ms: int = -1) -> int:

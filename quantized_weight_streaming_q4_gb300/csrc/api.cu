@@ -11,6 +11,7 @@
 #include <utility>
 
 #include "attn.cuh"
+#include "checks.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -32,6 +33,12 @@ int cuda_fail(cudaError_t e, const char* what) {
 int check_launch(const char* what) {
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? MUSER_OK : cuda_fail(e, what);
+}
+
+int check_f32(const char* fn, const char* name, const void* p) {
+    if (p == nullptr) return set_error(MUSER_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+    if (!is_aligned(p, 16)) return set_error(MUSER_ERR_MISALIGNED, "%s: %s not 16-byte aligned", fn, name);
+    return MUSER_OK;
 }
 
 namespace {
@@ -75,12 +82,6 @@ int check_matrix(const char* fn, int qtype, const void* W, int64_t rows, int64_t
         return set_error(MUSER_ERR_INVALID_ARG, "%s: cols = %lld must be a positive multiple of 256", fn, (long long)cols);
     if (!is_aligned(W, 16))
         return set_error(MUSER_ERR_MISALIGNED, "%s: weight pointer not 16-byte aligned", fn);
-    return MUSER_OK;
-}
-
-int check_f32(const char* fn, const char* name, const void* p) {
-    if (p == nullptr) return set_error(MUSER_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
-    if (!is_aligned(p, 16)) return set_error(MUSER_ERR_MISALIGNED, "%s: %s not 16-byte aligned", fn, name);
     return MUSER_OK;
 }
 
@@ -1017,12 +1018,6 @@ int muser_ffn_stack(const muser_ffn_layer* layers, int n_layers, const float* en
         std::swap(x, xnext);
     }
     return MUSER_OK;
-}
-
-// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
-static bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
 // Detached rows (count rows of kv_dim halves each) must not overlap the planes.

@@ -139,6 +139,10 @@ const int* attn_mma_resident(int row_tiles);  // clusters of 8 blocks that run a
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int row_tiles, cudaStream_t s);
 // The segments' tensor maps, boxes of `tile` rows (attn_mma.cu).
 int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps);
+// The maps of a paged cache's keys and values: (64 elements) x (box rows) x (1
+// head) x (1 page) boxes, 128-byte swizzle; what is not in the cache reads as zero.
+int encode_page_maps(uint16_t* key, uint16_t* value, const uint64_t (&dims)[4], const uint64_t (&strides)[3], int box_rows,
+                     CUtensorMap (&maps)[2]);
 // attn_few.cu: up to 32 query rows a K/V head, planes as for attn_tc.cu
 const AttnResident* attn_few_resident(int rows);
 int launch_attn_few(const AttnArgs& a, dim3 grid, cudaStream_t s);

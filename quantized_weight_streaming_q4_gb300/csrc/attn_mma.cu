@@ -438,10 +438,13 @@ const int* attn_mma_resident(int rt) { return rt == 1 ? resident<1>() : resident
 
 // The driver's encoder, and its call that gives a map another address: V's map
 // is K's but for that, and an encoding is 0.4 us of a call's host time.
-int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps) {
+struct MapEncoder {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    PFN_cuTensorMapReplaceAddress_v12000 readdress = nullptr;
+};
+static const MapEncoder& map_encoder() {
     static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-    static PFN_cuTensorMapReplaceAddress_v12000 readdress = nullptr;
+    static MapEncoder m;
     std::call_once(once, [] {
         void *f = nullptr, *r = nullptr;
         cudaDriverEntryPointQueryResult q{};
@@ -449,26 +452,48 @@ int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps) {
             q == cudaDriverEntryPointSuccess &&
             cudaGetDriverEntryPointByVersion("cuTensorMapReplaceAddress", &r, 12000, cudaEnableDefault, &q) == cudaSuccess &&
             q == cudaDriverEntryPointSuccess) {
-            readdress = reinterpret_cast<PFN_cuTensorMapReplaceAddress_v12000>(r);
-            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+            m.readdress = reinterpret_cast<PFN_cuTensorMapReplaceAddress_v12000>(r);
+            m.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
         }
     });
-    if (encode == nullptr) return set_error(MUSER_ERR_CUDA, "attention: cuTensorMapEncodeTiled is not available");
+    return m;
+}
+
+// K's map of binary16 boxes in the 128-byte swizzle, and V's.
+static int encode_pair(CUtensorMap& k, CUtensorMap& v, const uint16_t* key, const uint16_t* value, int rank,
+                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+    const MapEncoder& m = map_encoder();
+    if (m.encode == nullptr) return set_error(MUSER_ERR_CUDA, "attention: cuTensorMapEncodeTiled is not available");
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    CUresult r = m.encode(&k, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(rank), const_cast<uint16_t*>(key), dims,
+                          strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) {
+        v = k;
+        r = m.readdress(&v, const_cast<uint16_t*>(value));
+    }
+    if (r != CUDA_SUCCESS) return set_error(MUSER_ERR_CUDA, "attention: a tensor map could not be made (%d)", static_cast<int>(r));
+    return MUSER_OK;
+}
+
+int encode_attn_maps(const AttnArgs& a, int tile, AttnMaps& maps) {
     for (int i = 0; i < a.nseg; ++i) {
         const AttnSeg& S = a.seg[i];
         const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(S.rows), static_cast<cuuint64_t>(a.G)};
         const cuuint64_t strides[2] = {static_cast<cuuint64_t>(S.row_stride) * 2, static_cast<cuuint64_t>(S.head_stride) * 2};
-        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(tile), 1}, one[3] = {1, 1, 1};
-        CUresult r = encode(&maps.k[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(S.k), dims, strides, box, one,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        if (r == CUDA_SUCCESS) {
-            maps.v[i] = maps.k[i];
-            r = readdress(&maps.v[i], const_cast<uint16_t*>(S.v));
-        }
-        if (r != CUDA_SUCCESS) return set_error(MUSER_ERR_CUDA, "attention: a tensor map could not be made (%d)", static_cast<int>(r));
+        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(tile), 1};
+        MUSER_TRY(encode_pair(maps.k[i], maps.v[i], S.k, S.v, 3, dims, strides, box));
     }
     return MUSER_OK;
+}
+
+int encode_page_maps(uint16_t* key, uint16_t* value, const uint64_t (&dims)[4], const uint64_t (&strides)[3], int box_rows,
+                     CUtensorMap (&maps)[2]) {
+    cuuint64_t d[4], st[3];
+    for (int i = 0; i < 4; ++i) d[i] = dims[i];
+    for (int i = 0; i < 3; ++i) st[i] = strides[i];
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    return encode_pair(maps[0], maps[1], key, value, 4, d, st, box);
 }
 
 int launch_attn_mma(const AttnArgs& a, dim3 grid, int rt, cudaStream_t s) {

@@ -1,0 +1,305 @@
+// beam.cu -- one step of beam search: log-probabilities, their sum with the
+// beams' scores, and the largest n of a request's beams and tokens.
+//
+// One launch and one pass over the logits.  A row is cut into parts, one a
+// block, which stay in registers: their maximum m, sum of exp(x - m), and the
+// part's n largest logits, in order (within a row the sum orders as the logit).
+// The last block of a request to finish joins them: the rows' log-sums, the
+// sums in 64 bits, and the n largest of beams * parts * n.
+//
+// The n largest of many values: the values are dealt to 64 groups; the n-th
+// largest of the groups' maxima is at most the n-th largest value, and few
+// values are above it (of 10,000 random ones about 20 for n = 16).  These go to
+// a list, where each counts how many come before it.  Where the list would not
+// take them (thousands of equal logits), the values are taken one by one.
+#include <algorithm>
+
+#include "kernels.cuh"
+#include "pages.cuh"
+
+namespace muser {
+namespace {
+
+constexpr int kThreads = 512, kVec = 8, kPerThread = 4 * kVec;
+constexpr int kMost = kThreads * kPerThread - 4;  // logits of a part; up to 3 elements before it share its first 16 bytes
+constexpr int kGroups = 64, kGroupLanes = kThreads / kGroups, kList = 1024;
+constexpr float kNegInf = -INFINITY;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct Stat {
+    float max;
+    float pad;
+    double sum;
+};
+struct Cand {
+    float x;
+    int32_t index;  // the token
+};
+
+// Ordered as the numbers: a larger value has a larger key, and no key is 0
+// but that of NaN, which counts as none.
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);  // -0 as 0
+    return x != x ? 0u : (b & 0x80000000u ? ~b : b | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t key_of(double x) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
+    return x != x ? 0ull : (b >> 63 ? ~b : b | 0x8000000000000000ull);
+}
+
+template <typename K>
+struct Pick {
+    K group[kGroups];      // the groups' maxima
+    K list_key[kList];
+    int32_t list_at[kList];
+    K red_key[kThreads / 32];
+    int32_t red_at[kThreads / 32];
+    K floor;
+    int32_t count;
+};
+
+// The n largest keys (ties: the lower `at`) among what all threads hold: each
+// calls each(f), which calls f(key, at) for its values, key 0 for none.
+// put(rank, key, at) is called for rank 0..found-1, in some order; returns found.
+template <typename K, typename Each, typename Put>
+__device__ __forceinline__ int largest(Pick<K>& S, int n, Each&& each, Put&& put) {
+    const int tid = threadIdx.x;
+    K top = 0;
+    each([&](K k, int) { top = k > top ? k : top; });
+#pragma unroll
+    for (int o = 1; o < kGroupLanes; o <<= 1) {
+        const K x = __shfl_xor_sync(0xffffffffu, top, o);
+        top = x > top ? x : top;
+    }
+    if (tid % kGroupLanes == 0) S.group[tid / kGroupLanes] = top;
+    if (tid == 0) S.count = 0;
+    __syncthreads();
+    if (tid < kGroups) {  // the n-th largest of the maxima (n <= kGroups)
+        const K mine = S.group[tid];
+        int before = 0;
+#pragma unroll 16
+        for (int j = 0; j < kGroups; ++j) before += (S.group[j] > mine || (S.group[j] == mine && j < tid)) ? 1 : 0;
+        if (before == n - 1) S.floor = mine;
+    }
+    __syncthreads();
+    const K least = S.floor;
+    each([&](K k, int at) {
+        if (k != 0 && k >= least) {
+            const int i = atomicAdd(&S.count, 1);
+            if (i < kList) {
+                S.list_key[i] = k;
+                S.list_at[i] = at;
+            }
+        }
+    });
+    __syncthreads();
+    const int count = S.count;
+    if (count <= kList) {
+        for (int i = tid; i < count; i += kThreads) {
+            const K k = S.list_key[i];
+            const int at = S.list_at[i];
+            int rank = 0;
+            for (int j = 0; j < count; ++j) rank += (S.list_key[j] > k || (S.list_key[j] == k && S.list_at[j] < at)) ? 1 : 0;
+            if (rank < n) put(rank, k, at);
+        }
+        return min(count, n);
+    }
+    // one after another: the first behind the last one taken
+    K last = ~K{0};
+    int last_at = -1;
+    for (int rank = 0; rank < n; ++rank) {
+        K best = 0;
+        int best_at = 0x7fffffff;
+        each([&](K k, int at) {
+            if (k != 0 && (k < last || (k == last && at > last_at)) && (k > best || (k == best && at < best_at))) best = k, best_at = at;
+        });
+        auto join = [&](K k, int at) {
+            if (k > best || (k == best && at < best_at)) best = k, best_at = at;
+        };
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) join(__shfl_xor_sync(0xffffffffu, best, o), __shfl_xor_sync(0xffffffffu, best_at, o));
+        if ((tid & 31) == 0) {
+            S.red_key[tid >> 5] = best;
+            S.red_at[tid >> 5] = best_at;
+        }
+        __syncthreads();
+        for (int w = 0; w < kThreads / 32; ++w) join(S.red_key[w], S.red_at[w]);
+        __syncthreads();
+        if (best == 0) return rank;
+        if (tid == 0) put(rank, best, best_at);
+        last = best;
+        last_at = best_at;
+    }
+    return n;
+}
+
+struct BeamShared {
+    union {
+        Pick<uint32_t> part;
+        Pick<uint64_t> all;
+    };
+    double base[kBeamMaxBeams];  // score - log-sum
+    int32_t ended[kBeamMaxBeams];
+    float red_max[kThreads / 32];
+    double red_sum[kThreads / 32];
+    int32_t last;
+};
+
+__global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_constant__ BeamArgs a) {
+    __shared__ BeamShared S;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int part = blockIdx.x, row = blockIdx.y, g = row / a.beams;
+    Stat* const stat = static_cast<Stat*>(a.stat);
+    Cand* const cand = static_cast<Cand*>(a.cand);
+    pdl_launch_dependents();
+    pdl_wait();
+    const bool ended = a.ended && __ldg(a.ended + row) != 0;
+    Cand* const mine = cand + (static_cast<int64_t>(row) * a.parts + part) * a.n;
+    if (ended) {  // one way on, with probability 1
+        if (tid < a.n) mine[tid] = Cand{part == 0 && tid == 0 ? 0.f : kNegInf, a.end_token};
+        if (tid == 0) stat[row * a.parts + part] = Stat{0.f, 0.f, 1.0};
+    } else {
+        const int v0 = static_cast<int>(static_cast<int64_t>(a.vocab) * part / a.parts);
+        const int len = static_cast<int>(static_cast<int64_t>(a.vocab) * (part + 1) / a.parts) - v0;
+        const float* p = a.logits + static_cast<int64_t>(row) * a.vocab + v0;
+        const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / 4u);
+        p -= off;  // 16-byte aligned; element i of the part is p[off + i]
+        float x[kPerThread];
+#pragma unroll
+        for (int u = 0; u < kVec; ++u) {
+            const int i = 4 * (tid + u * kThreads) - off;
+            if (i >= 0 && i + 4 <= len) {
+                const float4 v = __ldcs(reinterpret_cast<const float4*>(p + off + i));
+                x[4 * u] = v.x, x[4 * u + 1] = v.y, x[4 * u + 2] = v.z, x[4 * u + 3] = v.w;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[4 * u + c] = i + c >= 0 && i + c < len ? __ldcs(p + off + i + c) : kNegInf;
+            }
+        }
+        float m = kNegInf;
+#pragma unroll
+        for (int u = 0; u < kPerThread; ++u) m = fmaxf(m, x[u]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) S.red_max[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, S.red_max[w]);
+        // only -infinities (or NaN): exp(x - m) would be NaN where a sum of 0 is meant
+        const float ref = m == kNegInf ? 0.f : m;
+        float s = 0.f;
+#pragma unroll
+        for (int u = 0; u < kPerThread; ++u) s += exp2f((x[u] - ref) * kLog2e);
+        double sum = s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) S.red_sum[warp] = sum;
+        const int found = largest(
+            S.part, a.n,
+            [&](auto&& f) {
+#pragma unroll
+                for (int u = 0; u < kPerThread; ++u)
+                    f(x[u] == kNegInf ? 0u : key_of(x[u]), 4 * (tid + u / 4 * kThreads) - off + u % 4);
+            },
+            [&](int rank, uint32_t k, int at) {
+                mine[rank] = Cand{__uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k), v0 + at};
+            });
+        if (tid >= found && tid < a.n) mine[tid] = Cand{kNegInf, 0};
+        __syncthreads();
+        if (tid == 0) {
+            double total = 0.0;
+            for (int w = 0; w < kThreads / 32; ++w) total += S.red_sum[w];
+            stat[row * a.parts + part] = Stat{m, 0.f, total};
+        }
+    }
+    // the request's last block goes on
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();
+        const unsigned blocks = static_cast<unsigned>(a.beams * a.parts);
+        S.last = atom_add_acq_rel_gpu(a.ticket + g, 1u) == blocks - 1u;
+        if (S.last) a.ticket[g] = 0;
+    }
+    __syncthreads();
+    if (!S.last) return;
+    for (int b = warp; b < a.beams; b += kThreads / 32) {
+        const int r = g * a.beams + b;
+        const Stat* st = stat + r * a.parts;
+        float m = kNegInf;
+        for (int i = lane; i < a.parts; i += 32) m = fmaxf(m, __ldcg(&st[i].max));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        double s = 0.0;
+        for (int i = lane; i < a.parts; i += 32) {
+            const float pm = __ldcg(&st[i].max);
+            const double ps = __ldcg(&st[i].sum);
+            s += pm == kNegInf ? ps : ps * exp(static_cast<double>(pm) - static_cast<double>(m));  // ps: 0, or NaN
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) {
+            const bool end = a.ended && __ldg(a.ended + r) != 0;
+            S.base[b] = static_cast<double>(__ldcg(a.score + r)) - (end ? 0.0 : static_cast<double>(m) + log(s));
+            S.ended[b] = end;
+        }
+    }
+    __syncthreads();
+    const int per_row = a.parts * a.n, total = a.beams * per_row;
+    const Cand* all = cand + static_cast<int64_t>(g) * total;
+    const int out = g * a.n;
+    constexpr uint64_t kNone = 0x000fffffffffffffull;  // the key of -infinity
+    const int found = largest(
+        S.all, a.n,
+        [&](auto&& f) {
+            for (int e = tid; e < total; e += kThreads) {
+                const float2 c = __ldcg(reinterpret_cast<const float2*>(all + e));
+                const int b = e / per_row;
+                const uint64_t k = key_of(S.base[b] + static_cast<double>(c.x));
+                f(c.x == kNegInf || k <= kNone ? 0ull : k, b * a.vocab + __float_as_int(c.y));
+            }
+        },
+        [&](int rank, uint64_t k, int at) {
+            const int b = at / a.vocab, v = at - b * a.vocab;
+            const bool end = S.ended[b] || v == a.end_token;
+            a.parent[out + rank] = g * a.beams + b;
+            a.token[out + rank] = v;
+            a.score_out[out + rank] = static_cast<float>(__longlong_as_double(static_cast<long long>(k >> 63 ? k & 0x7fffffffffffffffull : ~k)));
+            if (a.ended_out) a.ended_out[out + rank] = end;
+            if (a.add) a.add[out + rank] = !end;
+        });
+    for (int i = found + tid; i < a.n; i += kThreads) {
+        a.parent[out + i] = -1;
+        a.token[out + i] = -1;
+        a.score_out[out + i] = kNegInf;
+        if (a.ended_out) a.ended_out[out + i] = 1;
+        if (a.add) a.add[out + i] = 0;
+    }
+}
+
+// Parts of a row: two blocks an SM, at least 2,048 logits each.
+int parts_of(int rows, int64_t vocab) {
+    const int64_t least = (vocab + kMost - 1) / kMost, most = (vocab + 2047) / 2048;
+    return static_cast<int>(std::max(least, std::min<int64_t>(most, std::max(1, 304 / rows))));
+}
+constexpr size_t kTicketBytes = 1024;
+static_assert(kTicketBytes >= kMaxSequences * sizeof(unsigned), "a ticket a request");
+
+}  // namespace
+
+size_t beam_scratch_bytes(int groups, int beams, int64_t vocab, int n) {
+    const size_t parts = static_cast<size_t>(groups) * beams * parts_of(groups * beams, vocab);
+    return kTicketBytes + parts * sizeof(Stat) + (parts * n * sizeof(Cand) + 15u) / 16u * 16u;
+}
+
+int launch_beam_select(BeamArgs a, void* scratch, cudaStream_t s) {
+    const int rows = a.groups * a.beams;
+    a.parts = parts_of(rows, a.vocab);
+    uint8_t* p = static_cast<uint8_t*>(scratch);
+    a.ticket = reinterpret_cast<unsigned*>(p);
+    a.stat = p + kTicketBytes;
+    a.cand = p + kTicketBytes + static_cast<size_t>(rows) * a.parts * sizeof(Stat);
+    return launch_after("beam selection", beam_select_kernel, dim3(static_cast<unsigned>(a.parts), static_cast<unsigned>(rows)),
+                        kThreads, 0, 1, s, a);
+}
+
+}  // namespace muser
