@@ -794,7 +794,7 @@ size_t muser_kv_paged_attention_scratch_bytes(int64_t kv_dim, int64_t head_dim, 
  *   The work is split over the device by the rows that are seen; the same
  *   positions give the same split and bit for bit the same results.
  *   scratch: device memory of muser_kv_paged_attention_scratch_bytes(), 16-byte
- *   aligned, zero-filled before its first use; its first 1,024 bytes are left
+ *   aligned, zero-filled before its first use; its first 2,048 bytes are left
  *   zero, the rest is not.  Calls that can run at the same time must not share
  *   it.  out and scratch overlap nothing else.
  */
@@ -817,12 +817,12 @@ size_t muser_beam_select_scratch_bytes(int groups, int beams, int64_t vocab, int
  *   token; score_out: the sum, rounded once; ended_out (or NULL): 1 if ended[r]
  *   or the token is end_token, else 0; add (or NULL): 1 - ended_out.
  *   end_token -1: none, then ended is NULL.
- *   A candidate whose sum is -infinity or NaN (a row with a NaN or +infinity, a
- *   score of -infinity) is none.  Where a request has fewer than n, the rest
- *   are parent -1, token -1, score -infinity, ended 1, add 0.
- *   Log-probabilities are those of 64 bits to about 2^-24 (the sums over the
- *   vocabulary are of binary32 exponentials); the tokens of one beam are
- *   compared exactly.
+ *   A candidate whose sum is -infinity or NaN is none: of a row with a NaN, or
+ *   whose largest logit is beyond +-2^20, and of a score of -infinity.  Where a
+ *   request has fewer than n, the rest are parent -1, token -1, score
+ *   -infinity, ended 1, add 0.
+ *   The sums are compared to 48 bits; a row's log-sum is good to about 2^-22
+ *   (binary32 exponentials, added up in fixed point), the same for equal rows.
  *   groups*beams <= MUSER_MAX_SEQUENCES, beams <= 32, n <= 64 and <=
  *   beams*vocab, vocab <= 2^20.  With n == beams, score_out may be score and
  *   ended_out ended; else outputs and scratch overlap nothing.

@@ -2,10 +2,16 @@
 // beams' scores, and the largest n of a request's beams and tokens.
 //
 // One launch and one pass over the logits.  A row is cut into parts, one a
-// block, which stay in registers: their maximum m, sum of exp(x - m), and the
-// part's n largest logits, in order (within a row the sum orders as the logit).
-// The last block of a request to finish joins them: the rows' log-sums, the
-// sums in 64 bits, and the n largest of beams * parts * n.
+// block, which stay in registers: the sum of 2^(x log2(e) - E) with an integer
+// E, in fixed point, and the part's n largest logits, in order (within a row
+// the sum orders as the logit).  The last block of a request to finish joins
+// them: the rows' log-sums (the parts' sums are shifted, exactly), and the n
+// largest of beams * parts * n sums, of which only the parts whose largest is
+// among the requests' largest are looked at further.
+//
+// Binary64 is a thirty-second of binary32's rate here and is left to one
+// logarithm a row: the sums score + x - log-sum are pairs of binary32 numbers
+// (48 bits), compared as 64-bit keys.
 //
 // The n largest of many values: the values are dealt to 64 groups; the n-th
 // largest of the groups' maxima is at most the n-th largest value, and few
@@ -24,12 +30,15 @@ constexpr int kThreads = 512, kVec = 8, kPerThread = 4 * kVec;
 constexpr int kMost = kThreads * kPerThread - 4;  // logits of a part; up to 3 elements before it share its first 16 bytes
 constexpr int kGroups = 64, kGroupLanes = kThreads / kGroups, kList = 1024;
 constexpr float kNegInf = -INFINITY;
-constexpr float kLog2e = 1.44269504088896340736f;
+// log2(e) to 48 bits
+constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746887e-8f;
+constexpr float kFixed = 0x1p40f;     // a sum of 2^20 terms below 2 is below 2^61
+constexpr float kMostLogit = 0x1p20f;  // beyond it binary32 leaves too little of a logit's fraction
 
 struct Stat {
-    float max;
+    float e;       // E, or NaN: no sum
     float pad;
-    double sum;
+    uint64_t sum;  // times 2^40
 };
 struct Cand {
     float x;
@@ -42,9 +51,15 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t b = __float_as_uint(x + 0.f);  // -0 as 0
     return x != x ? 0u : (b & 0x80000000u ? ~b : b | 0x80000000u);
 }
-__device__ __forceinline__ uint64_t key_of(double x) {
-    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
-    return x != x ? 0ull : (b >> 63 ? ~b : b | 0x8000000000000000ull);
+__device__ __forceinline__ float from_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+
+// The key of a pair plus x, to 48 bits; 0 for -infinity and NaN.
+__device__ __forceinline__ uint64_t sum_key(float2 base, float x) {
+    const float s = base.x + x, t = s - base.x;
+    const float err = (base.x - (s - t)) + (x - t) + base.y;  // what the first sum lost
+    const float hi = s + err;
+    if (!(hi > kNegInf)) return s > kNegInf ? static_cast<uint64_t>(key_of(s)) << 32 : 0;  // s may be +infinity: no low part
+    return static_cast<uint64_t>(key_of(hi)) << 32 | key_of(err - (hi - s));
 }
 
 template <typename K>
@@ -58,14 +73,10 @@ struct Pick {
     int32_t count;
 };
 
-// The n largest keys (ties: the lower `at`) among what all threads hold: each
-// calls each(f), which calls f(key, at) for its values, key 0 for none.
-// put(rank, key, at) is called for rank 0..found-1, in some order; returns found.
-template <typename K, typename Each, typename Put>
-__device__ __forceinline__ int largest(Pick<K>& S, int n, Each&& each, Put&& put) {
+// The n-th largest of the 64 groups' maxima (n <= 64); `top` is the thread's.
+template <typename K>
+__device__ __forceinline__ K floor_of(Pick<K>& S, int n, K top) {
     const int tid = threadIdx.x;
-    K top = 0;
-    each([&](K k, int) { top = k > top ? k : top; });
 #pragma unroll
     for (int o = 1; o < kGroupLanes; o <<= 1) {
         const K x = __shfl_xor_sync(0xffffffffu, top, o);
@@ -74,7 +85,7 @@ __device__ __forceinline__ int largest(Pick<K>& S, int n, Each&& each, Put&& put
     if (tid % kGroupLanes == 0) S.group[tid / kGroupLanes] = top;
     if (tid == 0) S.count = 0;
     __syncthreads();
-    if (tid < kGroups) {  // the n-th largest of the maxima (n <= kGroups)
+    if (tid < kGroups) {
         const K mine = S.group[tid];
         int before = 0;
 #pragma unroll 16
@@ -82,7 +93,16 @@ __device__ __forceinline__ int largest(Pick<K>& S, int n, Each&& each, Put&& put
         if (before == n - 1) S.floor = mine;
     }
     __syncthreads();
-    const K least = S.floor;
+    return S.floor;
+}
+
+// The n largest keys (ties: the lower `at`), none of which is below `least`,
+// among what all threads hold: each calls each(f), which calls f(key, at) for
+// its values, key 0 for none.  put(rank, key, at) is called for rank
+// 0..found-1, in some order; returns found.
+template <typename K, typename Each, typename Put>
+__device__ __forceinline__ int largest(Pick<K>& S, int n, K least, Each&& each, Put&& put) {
+    const int tid = threadIdx.x;
     each([&](K k, int at) {
         if (k != 0 && k >= least) {
             const int i = atomicAdd(&S.count, 1);
@@ -99,6 +119,7 @@ __device__ __forceinline__ int largest(Pick<K>& S, int n, Each&& each, Put&& put
             const K k = S.list_key[i];
             const int at = S.list_at[i];
             int rank = 0;
+#pragma unroll 4
             for (int j = 0; j < count; ++j) rank += (S.list_key[j] > k || (S.list_key[j] == k && S.list_at[j] < at)) ? 1 : 0;
             if (rank < n) put(rank, k, at);
         }
@@ -110,12 +131,12 @@ __device__ __forceinline__ int largest(Pick<K>& S, int n, Each&& each, Put&& put
     for (int rank = 0; rank < n; ++rank) {
         K best = 0;
         int best_at = 0x7fffffff;
-        each([&](K k, int at) {
-            if (k != 0 && (k < last || (k == last && at > last_at)) && (k > best || (k == best && at < best_at))) best = k, best_at = at;
-        });
         auto join = [&](K k, int at) {
             if (k > best || (k == best && at < best_at)) best = k, best_at = at;
         };
+        each([&](K k, int at) {
+            if (k != 0 && (k < last || (k == last && at > last_at))) join(k, at);
+        });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) join(__shfl_xor_sync(0xffffffffu, best, o), __shfl_xor_sync(0xffffffffu, best_at, o));
         if ((tid & 31) == 0) {
@@ -133,15 +154,23 @@ __device__ __forceinline__ int largest(Pick<K>& S, int n, Each&& each, Put&& put
     return n;
 }
 
+// Parts of a request: a beam's are at most 65 (2^20 tokens) or a share of 304.
+constexpr int kHeads = 5, kMostLists = kHeads * kThreads;
+static_assert(kBeamMaxBeams * ((kBeamMaxVocab + kMost - 1) / kMost) <= kMostLists && 304 <= kMostLists, "a request's parts");
+
 struct BeamShared {
     union {
         Pick<uint32_t> part;
         Pick<uint64_t> all;
     };
-    double base[kBeamMaxBeams];  // score - log-sum
+    float2 base[kBeamMaxBeams];  // score - log-sum, as a pair
+    float e[kBeamMaxBeams];      // the rows' largest E, and their sums
+    uint64_t total[kBeamMaxBeams];
     int32_t ended[kBeamMaxBeams];
+    uint16_t open[kMostLists];   // parts that may hold one of the n largest
+    int32_t opened;
     float red_max[kThreads / 32];
-    double red_sum[kThreads / 32];
+    uint64_t red_sum[kThreads / 32];
     int32_t last;
 };
 
@@ -157,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     Cand* const mine = cand + (static_cast<int64_t>(row) * a.parts + part) * a.n;
     if (ended) {  // one way on, with probability 1
         if (tid < a.n) mine[tid] = Cand{part == 0 && tid == 0 ? 0.f : kNegInf, a.end_token};
-        if (tid == 0) stat[row * a.parts + part] = Stat{0.f, 0.f, 1.0};
+        if (tid == 0) stat[row * a.parts + part] = Stat{0.f, 0.f, 1};
     } else {
         const int v0 = static_cast<int>(static_cast<int64_t>(a.vocab) * part / a.parts);
         const int len = static_cast<int>(static_cast<int64_t>(a.vocab) * (part + 1) / a.parts) - v0;
@@ -185,32 +214,38 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, S.red_max[w]);
-        // only -infinities (or NaN): exp(x - m) would be NaN where a sum of 0 is meant
-        const float ref = m == kNegInf ? 0.f : m;
+        // a part that is all below -2^20 (masked) adds nothing to a row that is not
+        const bool some = m >= -kMostLogit;
+        const float e = some && m <= kMostLogit ? floorf(m * kLog2e) : 0.f;
         float s = 0.f;
 #pragma unroll
-        for (int u = 0; u < kPerThread; ++u) s += exp2f((x[u] - ref) * kLog2e);
-        double sum = s;
+        for (int u = 0; u < kPerThread; ++u) s += exp2f(fmaf(x[u], kLog2eLow, fmaf(x[u], kLog2e, -e)));
+        // NaN, or infinite: the row has no sum
+        const bool bad = __syncthreads_or(!(s < INFINITY) || m > kMostLogit);
+        if (!some) s = 0.f;
+        uint64_t sum = bad ? 0 : __float2ull_rn(s * kFixed);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) S.red_sum[warp] = sum;
+        float top = kNegInf;
+#pragma unroll
+        for (int u = 0; u < kPerThread; ++u) top = fmaxf(top, x[u]);
+        const uint32_t least = floor_of(S.part, a.n, top == kNegInf ? 0u : key_of(top));
+        if (tid < 32) {  // the warps' sums
+            uint64_t total = lane < kThreads / 32 ? S.red_sum[lane] : 0;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            if (lane == 0) stat[row * a.parts + part] = Stat{bad ? NAN : e, 0.f, total};
+        }
         const int found = largest(
-            S.part, a.n,
+            S.part, a.n, least,
             [&](auto&& f) {
 #pragma unroll
                 for (int u = 0; u < kPerThread; ++u)
                     f(x[u] == kNegInf ? 0u : key_of(x[u]), 4 * (tid + u / 4 * kThreads) - off + u % 4);
             },
-            [&](int rank, uint32_t k, int at) {
-                mine[rank] = Cand{__uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k), v0 + at};
-            });
+            [&](int rank, uint32_t k, int at) { mine[rank] = Cand{from_key(k), v0 + at}; });
         if (tid >= found && tid < a.n) mine[tid] = Cand{kNegInf, 0};
-        __syncthreads();
-        if (tid == 0) {
-            double total = 0.0;
-            for (int w = 0; w < kThreads / 32; ++w) total += S.red_sum[w];
-            stat[row * a.parts + part] = Stat{m, 0.f, total};
-        }
     }
     // the request's last block goes on
     __syncthreads();
@@ -222,40 +257,72 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     }
     __syncthreads();
     if (!S.last) return;
-    for (int b = warp; b < a.beams; b += kThreads / 32) {
-        const int r = g * a.beams + b;
-        const Stat* st = stat + r * a.parts;
-        float m = kNegInf;
-        for (int i = lane; i < a.parts; i += 32) m = fmaxf(m, __ldcg(&st[i].max));
+    // the parts' largest, on the way while the rows' sums are made
+    const int lists = a.beams * a.parts;
+    const Cand* all = cand + static_cast<int64_t>(g) * lists * a.n;
+    float head[kHeads];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        double s = 0.0;
+    for (int i = 0; i < kHeads; ++i) {
+        const int l = tid + i * kThreads;
+        head[i] = l < lists ? __ldcg(&all[l * a.n].x) : kNegInf;
+    }
+    if (tid == 0) S.opened = 0;
+    for (int b = warp; b < a.beams; b += kThreads / 32) {
+        const Stat* st = stat + (g * a.beams + b) * a.parts;
+        float e = kNegInf;
+        bool bad = false;
         for (int i = lane; i < a.parts; i += 32) {
-            const float pm = __ldcg(&st[i].max);
-            const double ps = __ldcg(&st[i].sum);
-            s += pm == kNegInf ? ps : ps * exp(static_cast<double>(pm) - static_cast<double>(m));  // ps: 0, or NaN
+            const float pe = __ldcg(&st[i].e);
+            bad = bad || pe != pe;
+            if (__ldcg(&st[i].sum) != 0) e = fmaxf(e, pe);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
+        uint64_t s = 0;
+        for (int i = lane; i < a.parts; i += 32) {
+            const float behind = e - __ldcg(&st[i].e);
+            if (behind < 64.f) s += __ldcg(&st[i].sum) >> static_cast<int>(fmaxf(behind, 0.f));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        bad = __any_sync(0xffffffffu, bad);
         if (lane == 0) {
-            const bool end = a.ended && __ldg(a.ended + r) != 0;
-            S.base[b] = static_cast<double>(__ldcg(a.score + r)) - (end ? 0.0 : static_cast<double>(m) + log(s));
-            S.ended[b] = end;
+            S.e[b] = bad ? NAN : e;
+            S.total[b] = s;
         }
     }
     __syncthreads();
-    const int per_row = a.parts * a.n, total = a.beams * per_row;
-    const Cand* all = cand + static_cast<int64_t>(g) * total;
-    const int out = g * a.n;
-    constexpr uint64_t kNone = 0x000fffffffffffffull;  // the key of -infinity
+    if (tid < a.beams) {
+        const int r = g * a.beams + tid;
+        const bool end = a.ended && __ldg(a.ended + r) != 0;
+        const double score = __ldcg(a.score + r);
+        // ln(total 2^(e - 40))
+        double sum = score - (end ? 0.0 : (static_cast<double>(S.e[tid]) - 40.0 + log2(static_cast<double>(S.total[tid]))) * 0.693147180559945309417);
+        if (!end && S.total[tid] == 0) sum = NAN;
+        const float hi = static_cast<float>(sum);
+        S.base[tid] = make_float2(hi, fabsf(hi) < INFINITY ? static_cast<float>(sum - hi) : 0.f);
+        S.ended[tid] = end;
+    }
+    __syncthreads();
+    uint64_t key[kHeads], top = 0;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        key[i] = head[i] == kNegInf ? 0 : sum_key(S.base[(tid + i * kThreads) / a.parts], head[i]);
+        top = key[i] > top ? key[i] : top;
+    }
+    const uint64_t least = floor_of(S.all, a.n, top);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+        if (key[i] != 0 && key[i] >= least) S.open[atomicAdd(&S.opened, 1)] = static_cast<uint16_t>(tid + i * kThreads);
+    __syncthreads();
+    const int total = S.opened * a.n, out = g * a.n;
     const int found = largest(
-        S.all, a.n,
+        S.all, a.n, least,
         [&](auto&& f) {
             for (int e = tid; e < total; e += kThreads) {
-                const float2 c = __ldcg(reinterpret_cast<const float2*>(all + e));
-                const int b = e / per_row;
-                const uint64_t k = key_of(S.base[b] + static_cast<double>(c.x));
-                f(c.x == kNegInf || k <= kNone ? 0ull : k, b * a.vocab + __float_as_int(c.y));
+                const int i = e / a.n, l = S.open[i], b = l / a.parts;
+                const float2 c = __ldcg(reinterpret_cast<const float2*>(all + l * a.n + e - i * a.n));
+                f(c.x == kNegInf ? 0 : sum_key(S.base[b], c.x), b * a.vocab + __float_as_int(c.y));
             }
         },
         [&](int rank, uint64_t k, int at) {
@@ -263,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
             const bool end = S.ended[b] || v == a.end_token;
             a.parent[out + rank] = g * a.beams + b;
             a.token[out + rank] = v;
-            a.score_out[out + rank] = static_cast<float>(__longlong_as_double(static_cast<long long>(k >> 63 ? k & 0x7fffffffffffffffull : ~k)));
+            a.score_out[out + rank] = from_key(static_cast<uint32_t>(k >> 32));
             if (a.ended_out) a.ended_out[out + rank] = end;
             if (a.add) a.add[out + rank] = !end;
         });

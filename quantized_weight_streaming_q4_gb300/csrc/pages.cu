@@ -28,8 +28,9 @@ struct TabShared {
     int64_t new_end[kRows];    // new rows up to this one's
     int32_t task_end[kRows];   // runs of entries of the rows up to this one
     int32_t copy_at[kRows];
-    int64_t warp64[kTabWarps];
-    int32_t warp_a[kTabWarps], warp_b[kTabWarps];
+    int32_t free_end[kTabThreads];  // free pages in the words of the threads up to this one
+    int64_t warp64[kTabWarps][1];
+    int32_t warp1[kTabWarps][1], warp3[kTabWarps][3];
     int64_t total_new;
     int32_t status, total_need, total_copy, free;
 };
@@ -49,30 +50,31 @@ __device__ __forceinline__ int find_row(const T* end, int n, T x) {
     return lo;
 }
 
-// Inclusive prefix sum over the block's threads; `warp` has kTabWarps entries.
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T* warp) {
+// Inclusive prefix sums of N values over the block's threads; `warp` has N
+// entries a warp.
+template <typename T, int N>
+__device__ __forceinline__ void block_scan(T (&v)[N], T (*warp)[N]) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const T x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-    }
-    if (lane == 31) warp[w] = v;
-    __syncthreads();
-    if (w == 0) {
-        T x = lane < kTabWarps ? warp[lane] : 0;
+    for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const T y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+        for (int i = 0; i < N; ++i) {
+            const T x = __shfl_up_sync(0xffffffffu, v[i], o);
+            if (lane >= o) v[i] += x;
         }
-        if (lane < kTabWarps) warp[lane] = x;
+    if (lane == 31)
+#pragma unroll
+        for (int i = 0; i < N; ++i) warp[w][i] = v[i];
+    __syncthreads();
+    T before[N] = {}, mine[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        mine[i] = lane < w ? warp[lane][i] : T{0};
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mine[i] += __shfl_xor_sync(0xffffffffu, mine[i], o);
+        before[i] = mine[i];
+        v[i] += before[i];
     }
-    __syncthreads();
-    if (w > 0) v += warp[w - 1];
-    __syncthreads();
-    return v;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -129,8 +131,9 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
         if (now > keep && keep % R != 0 && (S.own[tid] < 0 || S.own[tid] >= a.pages)) S.own[tid] = -2;  // there is none: a new page, nothing to copy
         tasks = ceil_div(ceil_div(keep, R), 32 * kEach);
     }
-    const int task_end = block_scan(tasks, S.warp_a);
-    if (tid < a.n) S.task_end[tid] = task_end;
+    int task_end[1] = {tasks};
+    block_scan(task_end, S.warp1);
+    if (tid < a.n) S.task_end[tid] = task_end[0];
     if (ranks > 1) cluster_sync();  // the first block's bits are clear
     else __syncthreads();
     // mark, and copy the entries that stay
@@ -177,53 +180,62 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
         int need = 0;
         int64_t fresh = 0;
         if (tid < a.n) {
-            need = copy + ceil_div(S.rows[tid], R) - ceil_div(S.keep[tid], R);
+            need = min(copy + ceil_div(S.rows[tid], R) - ceil_div(S.keep[tid], R), a.pages + 1);  // more than there are is too many
             fresh = S.rows[tid] - S.keep[tid];
             S.copy[tid] = copy;
         }
         const bool listed = copy && own >= 0;
-        const int need_end = block_scan(need, S.warp_a);
-        const int64_t new_end = block_scan(fresh, S.warp64);
-        const int copy_end = block_scan(listed ? 1 : 0, S.warp_b);
-        if (tid < a.n) {
-            S.need_end[tid] = need_end;
-            S.new_end[tid] = new_end;
-            S.copy_at[tid] = copy_end - (listed ? 1 : 0);
-        }
+        __syncthreads();
         // sweep: a thread counts the free pages of a run of words
         const int per = ceil_div(words, kTabThreads), w0 = min(words, tid * per), w1 = min(words, w0 + per);
         int free = 0;
         for (int w = w0; w < w1; ++w) free += __popc(~bits[w]);
-        const int free_end = block_scan(free, S.warp_a);
-        if (tid == kTabThreads - 1) S.free = free_end;
-        if (tid == a.n - 1) {
-            S.total_need = need_end;
-            S.total_new = new_end;
-            S.total_copy = copy_end;
+        int sums[3] = {need, listed ? 1 : 0, free};
+        int64_t new_sum[1] = {fresh};
+        block_scan(sums, S.warp3);
+        block_scan(new_sum, S.warp64);
+        const int64_t new_end = new_sum[0];
+        if (tid < a.n) {
+            S.need_end[tid] = sums[0];
+            S.new_end[tid] = new_end;
+            S.copy_at[tid] = sums[1] - (listed ? 1 : 0);
         }
-        __syncthreads();
-        if (tid == 0 && S.status == 0) {
-            if (S.total_copy > 0 && a.copies == nullptr) S.status = 4;
-            else if (S.total_new > a.max_new && (a.slots || a.position || a.sequence)) S.status = 3;
-            else if (S.total_need > S.free) S.status = 1;
+        S.free_end[tid] = sums[2];
+        if (tid == kTabThreads - 1) {
+            S.free = sums[2];
+            S.total_need = sums[0];
+            S.total_new = new_end;
+            S.total_copy = sums[1];
+            if (S.status == 0) {
+                if (sums[1] > 0 && a.copies == nullptr) S.status = 4;
+                else if (new_end > a.max_new && (a.slots || a.position || a.sequence)) S.status = 3;
+                else if (sums[0] > sums[2]) S.status = 1;
+            }
         }
         __syncthreads();
         const bool done = S.status == 0;
         const int give = done ? S.total_need : 0;
-        int at = free_end - free;
-        for (int w = w0; w < w1 && at < give; ++w)
-            for (uint32_t left = ~bits[w]; left && at < give; left &= left - 1, ++at) {
-                const int page = 32 * w + __ffs(left) - 1;
-                const int i = find_row(S.need_end, a.n, at);
-                const int j = at - (i == 0 ? 0 : S.need_end[i - 1]), held = ceil_div(S.keep[i], R);
-                a.table_out[i * a.stride + held + j - S.copy[i]] = page;
-                if (j == 0 && S.copy[i] && S.own[i] >= 0) {
-                    int32_t* c = a.copies + 3 * S.copy_at[i];
-                    c[0] = S.own[i];
-                    c[1] = page;
-                    c[2] = S.keep[i] % R;
-                }
+        for (int at = tid; at < give; at += kTabThreads) {
+            // the free page of rank `at`: its thread's words, the word, the bit
+            const int owner = find_row(S.free_end, kTabThreads, at);
+            int left = at - (owner == 0 ? 0 : S.free_end[owner - 1]), w = owner * per;
+            uint32_t open = ~bits[w];
+            for (int c = __popc(open); left >= c; c = __popc(open)) {
+                left -= c;
+                open = ~bits[++w];
             }
+            for (; left > 0; --left) open &= open - 1;
+            const int page = 32 * w + __ffs(open) - 1;
+            const int i = find_row(S.need_end, a.n, at);
+            const int j = at - (i == 0 ? 0 : S.need_end[i - 1]), held = ceil_div(S.keep[i], R);
+            a.table_out[i * a.stride + held + j - S.copy[i]] = page;
+            if (j == 0 && S.copy[i] && S.own[i] >= 0) {
+                int32_t* c = a.copies + 3 * S.copy_at[i];
+                c[0] = S.own[i];
+                c[1] = page;
+                c[2] = S.keep[i] % R;
+            }
+        }
         if (tid < a.n) {
             const int keep = S.keep[tid], rows = done ? S.rows[tid] : keep;
             a.length_out[tid] = rows;
@@ -264,16 +276,28 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
     if (ranks > 1) cluster_sync();  // the first block leaves when its memory has been read
     else __syncthreads();
     const int64_t total = S.total_new;
-    for (int64_t j = static_cast<int64_t>(rank) * kTabThreads + tid; j < a.max_new; j += static_cast<int64_t>(ranks) * kTabThreads) {
-        int slot = -1, pos = -1, seq = -1;
-        if (j < total) {
-            seq = find_row(S.new_end, a.n, j);
-            pos = S.keep[seq] + static_cast<int>(j - (seq == 0 ? 0 : S.new_end[seq - 1]));
-            slot = __ldcg(a.table_out + seq * a.stride + pos / R) * R + pos % R;
+    constexpr int kSlots = 4;  // of a thread's turn, their table entries on the way together
+    const int64_t turn = static_cast<int64_t>(ranks) * kTabThreads;
+    for (int64_t j0 = static_cast<int64_t>(rank) * kTabThreads + tid; j0 < a.max_new; j0 += kSlots * turn) {
+        int slot[kSlots], pos[kSlots], seq[kSlots];
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u) {
+            const int64_t j = j0 + u * turn;
+            slot[u] = pos[u] = seq[u] = -1;
+            if (j < total) {
+                seq[u] = find_row(S.new_end, a.n, j);
+                pos[u] = S.keep[seq[u]] + static_cast<int>(j - (seq[u] == 0 ? 0 : S.new_end[seq[u] - 1]));
+                slot[u] = __ldcg(a.table_out + seq[u] * a.stride + pos[u] / R);
+            }
         }
-        if (a.slots) a.slots[j] = slot;
-        if (a.position) a.position[j] = pos;
-        if (a.sequence) a.sequence[j] = seq;
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u) {
+            const int64_t j = j0 + u * turn;
+            if (j >= a.max_new) break;
+            if (a.slots) a.slots[j] = seq[u] < 0 ? -1 : slot[u] * R + pos[u] % R;
+            if (a.position) a.position[j] = pos[u];
+            if (a.sequence) a.sequence[j] = seq[u];
+        }
     }
 }
 

@@ -238,7 +238,7 @@ class Case:
         got = host(self.out)[:size].reshape(self.n, -1)
         check_canary(self.out, size)
         check_canary(self.scratch, self.nbytes // 4)
-        assert not host(self.scratch)[:256].any(), "the tickets are left zero"
+        assert not host(self.scratch)[:512].any(), "the tickets are left zero"
         want, stored = self.want()
         vmax = np.abs(self.v).max() if self.own else 0
         f = self.cache.value.astype(np.float32)
@@ -486,6 +486,30 @@ def test_select_rows_that_are_not_finite():
     run_select(x, score, 2, 4, 6)
     x[3, :] = -np.inf
     run_select(x[:4], score[:4], 1, 4, 4)  # no way on at all
+
+
+@pytest.mark.parametrize("mask", [-1e9, float(np.finfo(np.float32).min), -np.inf])
+def test_select_masked_tokens(mask):
+    """Tokens masked by large negative numbers: whole parts of a row, all but one token, and rows that are all masked."""
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((6, 30000)).astype(np.float32)
+    x[0, 100:] = mask
+    x[1, :29990] = mask
+    x[2, 1:] = mask
+    x[3, ::2] = mask
+    run_select(x, np.arange(6, dtype=np.float32), 1, 6, 16)
+    run_select(x, np.arange(6, dtype=np.float32), 6, 1, 2)
+    x[5, :] = mask
+    nothing = x[4:].copy()
+    nothing[1] = -np.inf  # no way on from a row whose largest logit is beyond -2^20
+    got = []
+    for y in (x[4:], nothing):
+        o = [torch.zeros(8, dtype=torch.int32, device="cuda") for _ in range(2)]
+        so, nb = torch.zeros(8, device="cuda"), mu.muser_beam_select_scratch_bytes(1, 2, 30000, 8)
+        mu.muser_beam_select(dev(y), dev(np.array([-9.0, 0.0], np.float32)), 1, 2, 30000, 8, o[0], o[1], so,
+                             torch.zeros(nb // 4, device="cuda"), nb)
+        got.append([host(t).copy() for t in (*o, so)])
+    assert all(np.array_equal(a, b) for a, b in zip(*got)) and set(got[0][0]) == {0}
 
 
 def test_select_first_step():
