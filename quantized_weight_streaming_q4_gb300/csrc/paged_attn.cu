@@ -14,7 +14,10 @@ namespace {
 // lane, lane + 32, ...; one pass with the running maximum and sum.
 constexpr int kTile = 32, kThreads = 256, kWarps = kThreads / 32, kQ = kPagedRows / kWarps;
 constexpr int kMaxD = 256;
-constexpr size_t smem_bytes(int D) { return (2 * kTile * (D + 1) + kPagedRows * D) * sizeof(float); }
+constexpr size_t smem_bytes(int D) {
+    const size_t n = (2 * kTile * (D + 1) + kPagedRows * D) * sizeof(float);
+    return n < kJoinBytes ? kJoinBytes : n;
+}
 static_assert(smem_bytes(128) <= 46 * 1024, "heads up to 128 need no attribute");
 
 template <int ND>  // output elements per lane: D <= 32 * ND
@@ -22,7 +25,7 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
     extern __shared__ float sm[];
     __shared__ PagedPlan plan;
     __shared__ int32_t slot[kTile];  // a row's page * page_rows + row, or -1
-    __shared__ int32_t join;
+    __shared__ uint32_t flag;
     const int D = a.D, DP = D + 1;
     float* ks = sm;
     float* vs = ks + kTile * DP;
@@ -30,8 +33,8 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     pdl_wait();
-    make_plan<kTile>(a, plan);
-    PagedWalk walk(a, plan);
+    const uint32_t chunk = make_plan<kTile>(a, plan, reinterpret_cast<uint32_t*>(sm));
+    PagedWalk<kTile> walk(a, plan, chunk);
     PagedRun run;
     while (walk.next(a, plan, run)) {
         const Sight<kTile> sight(a, plan.t[run.row]);
@@ -142,9 +145,8 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
         }
         __syncthreads();
         if (run.whole()) continue;
-        if (tid == 0) join = last_part(a, run);
+        finish_item<kThreads>(a, run, tid, sm, flag);
         __syncthreads();
-        if (join) join_parts<kThreads>(a, run, tid);
     }
 }
 

@@ -67,6 +67,7 @@ struct Layout {
     static constexpr int kFull = 0, kEmpty = kNS, kSFull = 2 * kNS, kPFull = kSFull + 2, kOFull = kPFull + 2,
                          kQFull = kOFull + 2, kQFree = kQFull + 2, kBars = kQFree + 2;
     static_assert(kBars * 8 + 16 <= 384, "the barriers fit");
+    static_assert(kJoinBytes <= 2 * kPBytes, "the parts' shares fit where P was");
 };
 
 // Whether `mine` holds for any of the 128 threads that share barrier `id`.
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 64) prefetch_map(&vmap);
     pdl_wait();  // no global access before this
     tc_fence_before();
-    make_plan<kTile>(a, plan);
+    const uint32_t chunk = make_plan<kTile>(a, plan, reinterpret_cast<uint32_t*>(smem + L::kPOff));
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     // A thread whose wait has run out waits no more and goes on with what is
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](int b, int phase) {
         if (ok) ok = mbar_wait_bounded(&bar[b], static_cast<uint32_t>(phase & 1), a.status, kDevStatusWaitTimeout);
     };
-    PagedWalk walk(a, plan);
+    PagedWalk<kTile> walk(a, plan, chunk);
     PagedRun run;
     const int D = a.D;
 
@@ -417,6 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < NH; ++h) o[h][j] = counts ? 0x1p11f * vs[h] : 0.f;
             }
+            float z[NH][R];  // the output's gate, where this block writes the output
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    z[h][j] = a.gate && run.whole() && j < live && th + 128 * h < D ? __ldcg(a.gate + (row0 + j) * D + th + 128 * h) : 0.f;
             bool fresh = !self;  // no reference yet
             auto drain = [&](int i) {  // adds the output tile i
                 wait(L::kOFull + (i & 1), i >> 1);
@@ -524,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (d >= D) continue;
                     if (whole) {
                         const float y = o[h][j] * inv;
-                        a.out[(row0 + j) * D + d] = a.gate ? gated(y, __ldcg(a.gate + (row0 + j) * D + d)) : y;
+                        a.out[(row0 + j) * D + d] = a.gate ? gated(y, z[h][j]) : y;
                     } else {
                         a.part_o[(part + j) * D + d] = o[h][j];
                     }
@@ -532,10 +539,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             named_barrier_sync(1, 128);  // red is free again; the part is written
             if (whole) continue;
-            if (th == 0) joining = last_part(a, run);
+            // P's place is free: the run's last product has been read
+            finish_item<128>(a, run, th, reinterpret_cast<float*>(smem + L::kPOff), joining);
             named_barrier_sync(1, 128);
-            if (joining) join_parts<128>(a, run, th);
-            named_barrier_sync(1, 128);  // `joining` has been read
         }
     }
     tc_fence_before();
