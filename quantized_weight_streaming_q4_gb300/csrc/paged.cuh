@@ -81,15 +81,41 @@ struct Sight {
 struct PagedPlan {
     int32_t t[kMaxSequences];
     uint32_t before[kMaxSequences + 1];
+    uint32_t chunk, first_row;  // first_row: that the block's first unit is of
 };
 constexpr int kMostChunk = 8, kWholeTiles = 4;
 
 __device__ __forceinline__ uint32_t ceil_div(uint32_t x, uint32_t y) { return (x + y - 1) / y; }
 
-// Fills the plan; all of the block's threads (256) call it.  Returns the chunk.
-// `warp_sums`: 80 words of shared memory.
+// x / y; most calls' numbers fit 32 bits, whose division is a third of the work.
+__device__ __forceinline__ uint64_t divide(uint64_t x, uint64_t y) {
+    if ((x | y) >> 32) return x / y;
+    return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+}
+
+// A block's share [at, end) of `total` units; blocks behind the units' number
+// have none.
+struct PagedShare {
+    uint64_t total, at, end;
+    uint32_t blocks;
+    __device__ __forceinline__ PagedShare(const PagedArgs& a, uint32_t units) : at(0), end(0) {
+        total = static_cast<uint64_t>(units) * static_cast<uint32_t>(a.G * a.blocks_per_head);
+        blocks = total < gridDim.x ? static_cast<uint32_t>(total) : gridDim.x;
+        if (blockIdx.x >= blocks) return;
+        if (total == blocks) {
+            at = blockIdx.x;
+            end = at + 1;
+        } else {
+            at = divide(total * blockIdx.x, blocks);
+            end = divide(total * (blockIdx.x + 1), blocks);
+        }
+    }
+};
+
+// Fills the plan; all of the block's threads (256) call it.  `warp_sums`: 80
+// words of shared memory.
 template <int TILE>
-__device__ __forceinline__ uint32_t make_plan(const PagedArgs& a, PagedPlan& plan, uint32_t* warp_sums) {
+__device__ __forceinline__ void make_plan(const PagedArgs& a, PagedPlan& plan, uint32_t* warp_sums) {
     static_assert(kMaxSequences == 256, "a thread a token row");
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int warps = (a.n + 31) / 32;  // that have rows
@@ -97,8 +123,12 @@ __device__ __forceinline__ uint32_t make_plan(const PagedArgs& a, PagedPlan& pla
     int t = -1;
     if (tid < a.n) {
         t = __ldcg(a.position + tid);
-        const int s = a.sequence ? __ldcg(a.sequence + tid) : tid;
-        if (s < 0 || s >= a.n_tables) t = -1;
+        if (a.sequence) {
+            const int s = __ldcg(a.sequence + tid);
+            if (s < 0 || s >= a.n_tables) t = -1;
+        } else if (tid >= a.n_tables) {
+            t = -1;
+        }
         t = min(t, 0x3fffffff);
     }
     plan.t[tid] = t;
@@ -106,29 +136,25 @@ __device__ __forceinline__ uint32_t make_plan(const PagedArgs& a, PagedPlan& pla
     // sums over the rows: tiles, the longest, and pieces for each chunk
     if (w < warps) {
         const uint32_t most = __reduce_max_sync(0xffffffffu, mine);
-        uint32_t sums[kMostChunk];
+        if (lane == 0) warp_sums[w * 10] = most;
 #pragma unroll
-        for (uint32_t c = 1; c <= kMostChunk; ++c) sums[c - 1] = __reduce_add_sync(0xffffffffu, ceil_div(mine, c));
-        if (lane == 0) {
-            warp_sums[w * 10] = most;
-#pragma unroll
-            for (int c = 0; c < kMostChunk; ++c) warp_sums[w * 10 + 1 + c] = sums[c];
+        for (uint32_t c = 1; c <= kMostChunk; ++c) {
+            const uint32_t sum = __reduce_add_sync(0xffffffffu, ceil_div(mine, c));
+            if (lane == 0) warp_sums[w * 10 + c] = sum;
         }
     }
     __syncthreads();
-    uint32_t most = 0, sums[kMostChunk] = {};
-    for (int j = 0; j < warps; ++j) {
-        most = max(most, warp_sums[j * 10]);
-#pragma unroll
-        for (int c = 0; c < kMostChunk; ++c) sums[c] += warp_sums[j * 10 + 1 + c];
-    }
-    const uint64_t per = static_cast<uint64_t>(a.G) * a.blocks_per_head;
-    uint32_t chunk = 0;
-#pragma unroll
-    for (int c = kMostChunk; c >= 1; --c)
-        if (sums[c - 1] * per <= gridDim.x) chunk = c;
-    if (chunk > 0 && most <= kWholeTiles) chunk = kWholeTiles;
-    uint32_t units = chunk == 0 ? mine : ceil_div(mine, chunk), v = units;
+    // lane c of every warp: the pieces of chunk c; lane 0: the longest
+    uint32_t sum = 0;
+    if (lane <= kMostChunk)
+        for (int j = 0; j < warps; ++j) sum = lane == 0 ? max(sum, warp_sums[j * 10]) : sum + warp_sums[j * 10 + lane];
+    const bool fits = lane > 0 && lane <= kMostChunk && static_cast<uint64_t>(sum) * static_cast<uint32_t>(a.G * a.blocks_per_head) <= gridDim.x;
+    const uint32_t fit = __ballot_sync(0xffffffffu, fits);
+    uint32_t chunk = fit == 0 ? 0 : __ffs(fit) - 1;
+    if (chunk > 0 && __shfl_sync(0xffffffffu, sum, 0) <= kWholeTiles) chunk = kWholeTiles;
+    const uint32_t all = __shfl_sync(0xffffffffu, sum, chunk == 0 ? 1 : chunk);
+    const uint32_t units = chunk <= 1 ? mine : divide(mine + chunk - 1, chunk);
+    uint32_t v = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
@@ -139,92 +165,79 @@ __device__ __forceinline__ uint32_t make_plan(const PagedArgs& a, PagedPlan& pla
         if (lane == 31) warp_sums[w] = v;
         __syncthreads();
         for (int j = 0; j < w; ++j) v += warp_sums[j];
-    } else if (w > 0) {
-        v = chunk == 0 ? sums[0] : 0;
-        if (chunk != 0) {
-#pragma unroll
-            for (int c = 1; c <= kMostChunk; ++c) v = static_cast<uint32_t>(c) == chunk ? sums[c - 1] : v;
-        }
-        units = 0;
     }
+    if (w >= warps) v = all;  // rows behind the last one
     plan.before[tid] = v - units;
-    if (tid == kMaxSequences - 1) plan.before[kMaxSequences] = v;
+    if (tid == 0) plan.before[kMaxSequences] = all;
+    const PagedShare share(a, all);
+    const uint64_t per = static_cast<uint32_t>(a.G * a.blocks_per_head);
+    if ((v - units) * per <= share.at && share.at < v * per) {
+        plan.first_row = tid;
+        plan.chunk = chunk;
+    }
     __syncthreads();
-    return chunk;
 }
 
 // A run of one item's tiles.
 struct PagedRun {
-    int row, head, r0;      // token row, K/V head, first of its query heads
-    int a, b, tiles;        // tiles [a, b) of `tiles`
-    int first, last;        // blocks that share the item
+    int row, head, r0;    // token row, K/V head, first of its query heads
+    int a, b, tiles;      // tiles [a, b) of `tiles`
+    uint64_t u0;          // the item's first unit, and their number
+    uint32_t units;
     __device__ __forceinline__ bool whole() const { return a == 0 && b == tiles; }
 };
-
-// x * y / z, in 32 bits where that is enough.
-__device__ __forceinline__ uint64_t mul_div(uint64_t x, uint32_t y, uint64_t z) {
-    if (((x * y) | z) >> 32) return x * y / z;
-    return static_cast<uint32_t>(x * y) / static_cast<uint32_t>(z);
-}
 
 // The block's runs, one after another.
 template <int TILE>
 struct PagedWalk {
-    uint64_t at, end, total;
-    uint32_t per;     // items of a token row
-    uint32_t blocks;  // that have work: each has a unit at least
+    PagedShare share;
     uint32_t chunk;
     int m;
-    __device__ __forceinline__ PagedWalk(const PagedArgs& a, const PagedPlan& plan, uint32_t chunk) : chunk(chunk) {
-        per = static_cast<uint32_t>(a.G * a.blocks_per_head);
-        total = static_cast<uint64_t>(plan.before[kMaxSequences]) * per;
-        blocks = static_cast<uint32_t>(min(total, static_cast<uint64_t>(gridDim.x)));
-        at = end = 0;
-        m = 0;
-        if (blockIdx.x >= blocks) return;
-        if (total == blocks) {
-            at = blockIdx.x;
-            end = at + 1;
-        } else {
-            at = mul_div(total, blockIdx.x, blocks);
-            end = mul_div(total, blockIdx.x + 1, blocks);
-        }
-        int lo = 0, hi = a.n - 1;
-        while (lo < hi) {  // the row that holds unit `at`
-            const int mid = (lo + hi) >> 1;
-            if (static_cast<uint64_t>(plan.before[mid + 1]) * per > at) hi = mid;
-            else lo = mid + 1;
-        }
-        m = lo;
-    }
-    __device__ __forceinline__ int owner(uint64_t unit) const { return static_cast<int>(((unit + 1) * blocks - 1) / total); }
+    __device__ __forceinline__ PagedWalk(const PagedArgs& a, const PagedPlan& plan)
+        : share(a, plan.before[kMaxSequences]), chunk(plan.chunk), m(static_cast<int>(plan.first_row)) {}
     __device__ __forceinline__ bool next(const PagedArgs& a, const PagedPlan& plan, PagedRun& run) {
-        if (at >= end) return false;
-        while (static_cast<uint64_t>(plan.before[m + 1]) * per <= at) ++m;
-        const uint64_t base = static_cast<uint64_t>(plan.before[m]) * per;
+        if (share.at >= share.end) return false;
+        const uint64_t per = static_cast<uint32_t>(a.G * a.blocks_per_head);
+        while (plan.before[m + 1] * per <= share.at) ++m;
+        const uint64_t base = plan.before[m] * per;
         const uint32_t units = plan.before[m + 1] - plan.before[m];  // of an item
-        const uint64_t off = at - base;
-        const uint32_t sub = static_cast<uint32_t>(mul_div(off, 1, units)), x = static_cast<uint32_t>(off - static_cast<uint64_t>(sub) * units);
+        const uint64_t off = share.at - base;
+        uint32_t sub = static_cast<uint32_t>(off), x = 0;
+        if (units > 1) {
+            sub = static_cast<uint32_t>(divide(off, units));
+            x = static_cast<uint32_t>(off - static_cast<uint64_t>(sub) * units);
+        }
         run.row = m;
-        run.head = static_cast<int>(sub) / a.blocks_per_head;
-        run.r0 = (static_cast<int>(sub) - run.head * a.blocks_per_head) * kPagedRows;
-        if (chunk != 0) {
-            run.tiles = Sight<TILE>(a, plan.t[m]).tiles;
-            run.a = run.tiles * x / units;
-            run.b = run.tiles * (x + 1) / units;
-            run.first = static_cast<int>(blockIdx.x - x);
-            run.last = run.first + static_cast<int>(units) - 1;
-            ++at;
+        run.units = units;
+        run.u0 = share.at - x;
+        run.head = static_cast<int>(sub);
+        run.r0 = 0;
+        if (a.blocks_per_head > 1) {
+            run.head = static_cast<int>(sub) / a.blocks_per_head;
+            run.r0 = (static_cast<int>(sub) - run.head * a.blocks_per_head) * kPagedRows;
+        }
+        if (chunk == 0) {
+            run.tiles = static_cast<int>(units);
+            run.a = static_cast<int>(x);
+            run.b = static_cast<int>(min(static_cast<uint64_t>(units), x + (share.end - share.at)));
+            share.at += run.b - run.a;
             return true;
         }
-        run.tiles = static_cast<int>(units);
-        run.a = static_cast<int>(x);
-        run.b = static_cast<int>(min(static_cast<uint64_t>(units), x + (end - at)));
-        const uint64_t u0 = base + static_cast<uint64_t>(sub) * units;
-        run.first = run.a == 0 ? static_cast<int>(blockIdx.x) : owner(u0);
-        run.last = run.b == run.tiles ? static_cast<int>(blockIdx.x) : owner(u0 + units - 1);
-        at += run.b - run.a;
+        run.tiles = Sight<TILE>(a, plan.t[m]).tiles;
+        run.a = 0;
+        run.b = run.tiles;
+        if (units > 1) {  // pieces of equal size, the first ones of a tile more
+            const int each = run.tiles / static_cast<int>(units), rest = run.tiles - each * static_cast<int>(units), i = static_cast<int>(x);
+            run.a = i * each + min(i, rest);
+            run.b = run.a + each + (i < rest ? 1 : 0);
+        }
+        ++share.at;
         return true;
+    }
+    // the first and the last block that share the run's item
+    __device__ __forceinline__ int owner(uint64_t unit) const {
+        if (share.total == share.blocks) return static_cast<int>(unit);
+        return static_cast<int>(divide((unit + 1) * share.blocks - 1, share.total));
     }
 };
 
@@ -234,113 +247,83 @@ __device__ __forceinline__ int part_of(int b, int first) { return 2 * b + (b == 
 
 __device__ __forceinline__ float gated(float y, float z) { return __fdividef(y, 1.f + __expf(-z)); }
 
-// Parts of the blocks from..from + (count - 1) * step are joined, into the
-// item's result or (!FINAL) into the first one's part: THREADS threads that
-// share barrier 1; `sm` has room for 18 * count floats.  The parts' shares are
-// found while their first sums are on the way.
-constexpr int kJoinMost = 24, kJoinBytes = 18 * kJoinMost * 4;
-template <int THREADS, bool FINAL>
-__device__ __forceinline__ void join_parts(const PagedArgs& a, const PagedRun& run, int from, int step, int count, int tid, float* sm) {
-    constexpr int U = 4, B = 8;  // pieces of a thread, parts in flight
-    const int live = min(kPagedRows, a.group - run.r0);
+// What the kernels do once a run, or once an item, is written as short loops:
+// instructions that an SM does not have at hand cost more than what they do
+// (unrolled for sixteen rows, the end of a run took 2.8 us, a join 15).
+
+// A row's float4s, a lane one or (D > 128) two.
+template <typename F>
+__device__ __forceinline__ void each_piece(int D, int lane, F&& f) {
+    for (int d = 4 * lane; d < D; d += 128) f(d);
+}
+__device__ __forceinline__ float4 load4(const float* p, bool vec, int left) {
+    if (vec) return __ldcg(reinterpret_cast<const float4*>(p));
+    return make_float4(__ldcg(p), left > 1 ? __ldcg(p + 1) : 0.f, left > 2 ? __ldcg(p + 2) : 0.f, left > 3 ? __ldcg(p + 3) : 0.f);
+}
+__device__ __forceinline__ void store4(float* p, float4 v, bool vec, int left) {
+    if (vec) {
+        *reinterpret_cast<float4*>(p) = v;
+        return;
+    }
+    p[0] = v.x;
+    if (left > 1) p[1] = v.y;
+    if (left > 2) p[2] = v.z;
+    if (left > 3) p[3] = v.w;
+}
+__device__ __forceinline__ float4 scaled(float4 v, float f) { return make_float4(v.x * f, v.y * f, v.z * f, v.w * f); }
+__device__ __forceinline__ float4 gated4(float4 v, float4 z) { return make_float4(gated(v.x, z.x), gated(v.y, z.y), gated(v.z, z.z), gated(v.w, z.w)); }
+
+// `count` parts, the first that of block `from` and each of a block `step`
+// further, are joined, into the item's result or (!final) into the first part.
+// A warp (w of W) takes every W-th row: its lanes hold the parts' shares.
+constexpr int kJoinMost = 16;
+__device__ __noinline__ void join_parts(const PagedArgs& a, const PagedRun& run, int first, int from, int step, int count, int w,
+                                        int W, bool final) {
+    constexpr int B = 8;  // loads in flight
+    const int lane = threadIdx.x & 31, live = min(kPagedRows, a.group - run.r0);
     const bool vec = a.D % 4 == 0;
-    const int per = vec ? a.D / 4 : a.D, units = live * per;
     const int64_t row0 = static_cast<int64_t>(run.row) * a.H + run.head * a.group + run.r0;
-    float* const inv = sm + 16 * count;
-    float* const most = inv + 16;
-    bool shares = false;
-    for (int x0 = tid; x0 - tid < units; x0 += U * THREADS) {
-        float4 o[U], z[U], v[U][B];
-        int r[U], d[U];
+    for (int j = w; j < live; j += W) {
+        float2 ml = make_float2(kNegInf, 0.f);
+        const int64_t mine = (static_cast<int64_t>(part_of(from + lane * step, first)) * kPagedRows) + j;  // of lane i: part i
+        if (lane < count) ml = __ldcg(a.part_ml + mine);
+        for (int d = 4 * lane; d - 4 * lane < a.D; d += 128) {
+            const bool real = d < a.D;
+            const float* p = a.part_o + (static_cast<int64_t>(part_of(from, first)) * kPagedRows + j) * a.D + d;
+            float4 z = make_float4(0.f, 0.f, 0.f, 0.f), o = z;
+            if (final && a.gate && real) z = load4(a.gate + (row0 + j) * a.D + d, vec, a.D - d);
+            float m = 0.f, l = 0.f, f = 0.f;
+            for (int i0 = 0; i0 < count; i0 += B) {
+                float4 v[B];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int x = x0 + u * THREADS;
-            r[u] = x < units ? x / per : -1;
-            d[u] = (x - r[u] * per) * (vec ? 4 : 1);
-            o[u] = z[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (FINAL && a.gate && r[u] >= 0) {
-                const float* p = a.gate + (row0 + r[u]) * a.D + d[u];
-                if (vec) z[u] = __ldcg(reinterpret_cast<const float4*>(p));
-                else z[u].x = __ldcg(p);
+                for (int i = 0; i < B; ++i) {
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (real && i0 + i < count)
+                        v[i] = load4(a.part_o + (static_cast<int64_t>(part_of(from + (i0 + i) * step, first)) * kPagedRows + j) * a.D + d, vec, a.D - d);
+                }
+                if (i0 == 0) {  // the shares, while the sums are on the way
+                    m = ml.x;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const bool empty = ml.x == kNegInf && ml.y == 0.f;  // no rows there: its sums are not looked at
+                    f = empty ? kNegInf : share(ml.x, m);
+                    l = warp_sum(empty ? 0.f : f * ml.y);
+                }
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    const float fi = __shfl_sync(0xffffffffu, f, min(i0 + i, 31));
+                    if (i0 + i < count && fi != kNegInf)
+                        o = make_float4(fmaf(fi, v[i].x, o.x), fmaf(fi, v[i].y, o.y), fmaf(fi, v[i].z, o.z), fmaf(fi, v[i].w, o.w));
+                }
             }
-        }
-        for (int i0 = 0; i0 < count; i0 += B) {
-#pragma unroll
-            for (int i = 0; i < B; ++i)
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    v[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (i0 + i < count && r[u] >= 0) {
-                        const float* p = a.part_o + (static_cast<int64_t>(part_of(from + (i0 + i) * step, run.first)) * kPagedRows + r[u]) * a.D + d[u];
-                        if (vec) v[u][i] = __ldcg(reinterpret_cast<const float4*>(p));
-                        else v[u][i].x = __ldcg(p);
-                    }
-                }
-            if (!shares) {
-                shares = true;
-                // sixteen rows' maxima and sums of a part, by sixteen threads; then a row a thread
-                float2 w[(kJoinMost * 16 + THREADS - 1) / THREADS];
-#pragma unroll
-                for (int k = 0; k < (kJoinMost * 16 + THREADS - 1) / THREADS; ++k) {
-                    const int y = tid + k * THREADS, row = y & 15;
-                    w[k] = make_float2(kNegInf, 0.f);
-                    if (y < 16 * count && row < live)
-                        w[k] = __ldcg(a.part_ml + static_cast<int64_t>(part_of(from + (y >> 4) * step, run.first)) * kPagedRows + row);
-                    if (y < 16 * count) sm[y] = w[k].x;
-                }
-                named_barrier_sync(1, THREADS);
-                if (tid < 16) {
-                    float m = kNegInf;
-                    for (int i = 0; i < count; ++i) m = fmaxf(m, sm[16 * i + tid]);
-                    most[tid] = m;
-                }
-                named_barrier_sync(1, THREADS);
-#pragma unroll
-                for (int k = 0; k < (kJoinMost * 16 + THREADS - 1) / THREADS; ++k) {
-                    const int y = tid + k * THREADS;
-                    const bool empty = w[k].x == kNegInf && w[k].y == 0.f;  // no rows there
-                    const float f = empty ? 0.f : share(w[k].x, most[y & 15]);
-                    if (y < 16 * count) sm[y] = empty ? kNegInf : f;  // -infinity: its sums are not looked at
-                    w[k].y = empty ? 0.f : f * w[k].y;
-                }
-                // the rows' sums: each thread's over its parts, then over a row's threads
-                float l = 0.f;
-#pragma unroll
-                for (int k = 0; k < (kJoinMost * 16 + THREADS - 1) / THREADS; ++k) l += w[k].y;
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                if (tid < 16) inv[tid] = 0.f;
-                named_barrier_sync(1, THREADS);
-                for (int q = 0; q < THREADS / 32; ++q) {  // one warp after another: always the same order
-                    if (tid >> 5 == q && (tid & 31) < 16) inv[tid & 15] += l;
-                    named_barrier_sync(1, THREADS);
-                }
-                if (!FINAL && tid < live)
-                    a.part_ml[static_cast<int64_t>(part_of(from, run.first)) * kPagedRows + tid] = make_float2(most[tid], inv[tid]);
-            }
-#pragma unroll
-            for (int i = 0; i < B; ++i)
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (i0 + i < count && r[u] >= 0) {
-                        const float f = sm[16 * (i0 + i) + r[u]];
-                        if (f == kNegInf) continue;
-                        o[u] = make_float4(fmaf(f, v[u][i].x, o[u].x), fmaf(f, v[u][i].y, o[u].y), fmaf(f, v[u][i].z, o[u].z), fmaf(f, v[u][i].w, o[u].w));
-                    }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (r[u] < 0) continue;
-            float* p;
-            if (FINAL) {
-                const float l = inv[r[u]], y = l == 0.f ? 0.f : __fdividef(1.f, l);
-                o[u] = make_float4(o[u].x * y, o[u].y * y, o[u].z * y, o[u].w * y);
-                if (a.gate) o[u] = make_float4(gated(o[u].x, z[u].x), gated(o[u].y, z[u].y), gated(o[u].z, z[u].z), gated(o[u].w, z[u].w));
-                p = a.out + (row0 + r[u]) * a.D + d[u];
+            if (!real) continue;
+            if (final) {
+                o = scaled(o, l == 0.f ? 0.f : __fdividef(1.f, l));
+                store4(a.out + (row0 + j) * a.D + d, a.gate ? gated4(o, z) : o, vec, a.D - d);
             } else {
-                p = a.part_o + (static_cast<int64_t>(part_of(from, run.first)) * kPagedRows + r[u]) * a.D + d[u];
+                store4(const_cast<float*>(p), o, vec, a.D - d);
+                if (d == 0) a.part_ml[mine] = make_float2(m, l);
             }
-            if (vec) *reinterpret_cast<float4*>(p) = o[u];
-            else *p = o[u].x;
         }
     }
 }
@@ -354,27 +337,28 @@ __device__ __forceinline__ bool last_of(unsigned* ticket, int count) {
     return last;
 }
 
-// After the block's part of an item is written: what is left to join, if this
-// is the last block to get there.  `flag` is in shared memory.
-template <int THREADS>
-__device__ __forceinline__ void finish_item(const PagedArgs& a, const PagedRun& run, int tid, float* sm, volatile uint32_t& flag) {
-    const int count = run.last - run.first + 1;
-    constexpr int kGroup = 8, kOnce = 16;
-    static_assert(kOnce <= kJoinMost && (kPagedMaxBlocks + kGroup - 1) / kGroup <= kJoinMost, "the shares fit");
+// After the block's part of an item is written, by `threads` threads (whole
+// warps) that share barrier 1 and have passed it since: what is left to join,
+// if this is the last block to get there.  `flag` is in shared memory.
+template <int TILE>
+__device__ __forceinline__ void finish_item(const PagedArgs& a, const PagedWalk<TILE>& walk, const PagedRun& run, int first, int tid,
+                                            int threads, volatile uint32_t& flag) {
+    const int last = walk.owner(run.u0 + run.units - 1), count = last - first + 1, w = tid >> 5, W = threads >> 5;
+    static_assert(kPagedMaxBlocks <= kJoinMost * kJoinMost, "two levels");
     int step = 1, parts = count;
-    if (count > kOnce) {
-        const int i = (static_cast<int>(blockIdx.x) - run.first) / kGroup, from = run.first + i * kGroup, size = min(kGroup, run.last - from + 1);
-        if (tid == 0) flag = last_of(a.ticket + part_of(from, run.first), size);
-        named_barrier_sync(1, THREADS);
+    if (count > kJoinMost) {
+        while (step * step < count) ++step;  // as many groups as parts in each
+        const int from = first + (static_cast<int>(blockIdx.x) - first) / step * step, size = min(step, last - from + 1);
+        if (tid == 0) flag = last_of(a.ticket + part_of(from, first), size);
+        named_barrier_sync(1, threads);
         if (!flag) return;
-        join_parts<THREADS, false>(a, run, from, 1, size, tid, sm);
-        step = kGroup;
-        parts = (count + kGroup - 1) / kGroup;
-        named_barrier_sync(1, THREADS);
+        join_parts(a, run, first, from, 1, size, w, W, false);
+        parts = (count + step - 1) / step;
+        named_barrier_sync(1, threads);
     }
-    if (tid == 0) flag = last_of(a.ticket + 2 * kPagedMaxBlocks + run.first, parts);
-    named_barrier_sync(1, THREADS);
-    if (flag) join_parts<THREADS, true>(a, run, run.first, step, parts, tid, sm);
+    if (tid == 0) flag = last_of(a.ticket + 2 * kPagedMaxBlocks + first, parts);
+    named_barrier_sync(1, threads);
+    if (flag) join_parts(a, run, first, first, step, parts, w, W, true);
 }
 
 }  // namespace

@@ -16,7 +16,7 @@ constexpr int kTile = 32, kThreads = 256, kWarps = kThreads / 32, kQ = kPagedRow
 constexpr int kMaxD = 256;
 constexpr size_t smem_bytes(int D) {
     const size_t n = (2 * kTile * (D + 1) + kPagedRows * D) * sizeof(float);
-    return n < kJoinBytes ? kJoinBytes : n;
+    return n < 512 ? 512 : n;  // the plan's sums
 }
 static_assert(smem_bytes(128) <= 46 * 1024, "heads up to 128 need no attribute");
 
@@ -33,8 +33,8 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     pdl_wait();
-    const uint32_t chunk = make_plan<kTile>(a, plan, reinterpret_cast<uint32_t*>(sm));
-    PagedWalk<kTile> walk(a, plan, chunk);
+    make_plan<kTile>(a, plan, reinterpret_cast<uint32_t*>(sm));
+    PagedWalk<kTile> walk(a, plan);
     PagedRun run;
     while (walk.next(a, plan, run)) {
         const Sight<kTile> sight(a, plan.t[run.row]);
@@ -128,11 +128,12 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
                 }
             }
         }
+        const int first = run.whole() ? 0 : walk.owner(run.u0);
 #pragma unroll
         for (int u = 0; u < kQ; ++u) {
             const int r = warp * kQ + u;
             if (r >= live) break;
-            const int64_t part = static_cast<int64_t>(part_of(blockIdx.x, run.first)) * kPagedRows + r;
+            const int64_t part = static_cast<int64_t>(part_of(blockIdx.x, first)) * kPagedRows + r;
             const float inv = l[u] == 0.f ? 0.f : __fdividef(1.f, l[u]);
             if (!run.whole() && lane == 0) a.part_ml[part] = make_float2(m[u], l[u]);
 #pragma unroll
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
         }
         __syncthreads();
         if (run.whole()) continue;
-        finish_item<kThreads>(a, run, tid, sm, flag);
+        finish_item(a, walk, run, first, tid, kThreads, flag);
         __syncthreads();
     }
 }

@@ -44,6 +44,9 @@ template <int R, int DB>  // query rows; blocks of 64 elements: D <= 64 * DB
 struct Layout {
     static constexpr uint32_t kItem = DB * kHalf;
     static constexpr int kNS = 196608 / static_cast<int>(kItem);  // stages of the ring: 12, 6 or 3
+    // the barriers: the stages' full and empty ones first
+    static constexpr int kFull = 0, kEmpty = kNS, kSFull = 2 * kNS, kPFull = kSFull + 2, kOFull = kPFull + 2,
+                         kQFull = kOFull + 2, kQFree = kQFull + 2, kBars = kQFree + 2;
     static constexpr uint32_t kN = 2 * R;                         // columns
     static constexpr uint32_t kKeyRow = kN / 8 * 128;             // P: bytes from 8 keys to the next 8
     static constexpr uint32_t kPBytes = kTile / 8 * kKeyRow;
@@ -53,8 +56,9 @@ struct Layout {
     static constexpr uint32_t kScaleOff = kPOff + 2 * kPBytes;    // float[2][16]: the rows' scales
     static constexpr uint32_t kSelfOff = kScaleOff + 2 * 64;      // float[2][16]: scores against themselves
     static constexpr uint32_t kRedOff = kSelfOff + 2 * 64;        // float[4][16]
-    static constexpr uint32_t kBarOff = kRedOff + 256;
-    static constexpr uint32_t kPlanOff = kBarOff + 384;
+    static constexpr uint32_t kSumsOff = kRedOff + 256;           // float[2][16]: the rows' sums and references
+    static constexpr uint32_t kBarOff = kSumsOff + 128;
+    static constexpr uint32_t kPlanOff = kBarOff + (kBars * 8 + 15) / 16 * 16;
     static constexpr uint32_t kUsed = kPlanOff + sizeof(PagedPlan) + 16;
     // with 64 elements a row the product's upper 64 lanes read the next stage, which is nobody's output
     static constexpr uint32_t kBytes = DB == 1 && kUsed < (kNS + 1) * kItem ? (kNS + 1) * kItem : kUsed;
@@ -63,11 +67,7 @@ struct Layout {
     static constexpr uint32_t kCols = 2 * kN + 2 * kOCols;
     static constexpr uint32_t kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
     static_assert(kBytes <= 227 * 1024, "a block's shared memory");
-    // the barriers: the stages' full and empty ones first
-    static constexpr int kFull = 0, kEmpty = kNS, kSFull = 2 * kNS, kPFull = kSFull + 2, kOFull = kPFull + 2,
-                         kQFull = kOFull + 2, kQFree = kQFull + 2, kBars = kQFree + 2;
-    static_assert(kBars * 8 + 16 <= 384, "the barriers fit");
-    static_assert(kJoinBytes <= 2 * kPBytes, "the parts' shares fit where P was");
+    static_assert(R * 128 * kHalves * 4 <= 2 * kPBytes, "a run's output fits where P was");
 };
 
 // Whether `mine` holds for any of the 128 threads that share barrier `id`.
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 64) prefetch_map(&vmap);
     pdl_wait();  // no global access before this
     tc_fence_before();
-    const uint32_t chunk = make_plan<kTile>(a, plan, reinterpret_cast<uint32_t*>(smem + L::kPOff));
+    make_plan<kTile>(a, plan, reinterpret_cast<uint32_t*>(smem + L::kPOff));
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     // A thread whose wait has run out waits no more and goes on with what is
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](int b, int phase) {
         if (ok) ok = mbar_wait_bounded(&bar[b], static_cast<uint32_t>(phase & 1), a.status, kDevStatusWaitTimeout);
     };
-    PagedWalk<kTile> walk(a, plan, chunk);
+    PagedWalk<kTile> walk(a, plan);
     PagedRun run;
     const int D = a.D;
 
@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int th = tid - 128;  // a key, later an output element
         const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         float* red = reinterpret_cast<float*>(smem + L::kRedOff);
+        float* sums = reinterpret_cast<float*>(smem + L::kSumsOff);
         int runs = 0, tile = 0;  // counted over all runs
         while (walk.next(a, plan, run)) {
             const int buf = runs % L::kQBufs;
@@ -418,12 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < NH; ++h) o[h][j] = counts ? 0x1p11f * vs[h] : 0.f;
             }
-            float z[NH][R];  // the output's gate, where this block writes the output
-#pragma unroll
-            for (int h = 0; h < NH; ++h)
-#pragma unroll
-                for (int j = 0; j < R; ++j)
-                    z[h][j] = a.gate && run.whole() && j < live && th + 128 * h < D ? __ldcg(a.gate + (row0 + j) * D + th + 128 * h) : 0.f;
             bool fresh = !self;  // no reference yet
             auto drain = [&](int i) {  // adds the output tile i
                 wait(L::kOFull + (i & 1), i >> 1);
@@ -476,9 +471,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fold<R>(v, [](float p, float q) { return fmaxf(p, q); });
                     if ((lane & (32 / R - 1)) == 0) red[(warp & 3) * 16 + lane / (32 / R)] = v[0];
                     named_barrier_sync(1, 128);
+                    if (th < R) red[th] = fmaxf(fmaxf(red[th], red[16 + th]), fmaxf(red[32 + th], red[48 + th]));
+                    named_barrier_sync(1, 128);
 #pragma unroll
                     for (int j = 0; j < R; ++j) {
-                        const float mn = fmaxf(fmaxf(fmaxf(m[j], red[j]), fmaxf(red[16 + j], red[32 + j])), red[48 + j]);
+                        const float mn = fmaxf(m[j], red[j]);
                         const float f = m[j] == kNegInf ? 0.f : ex2(m[j] - mn);
                         m[j] = mn;
                         b[j] = mn == kNegInf ? INFINITY : kOff - mn;  // no score yet: the next one asks again
@@ -516,31 +513,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((lane & (32 / R - 1)) == 0) red[(warp & 3) * 16 + lane / (32 / R)] = l[0];
             if (!ok) lost = 1;
             named_barrier_sync(1, 128);
-            const bool whole = run.whole(), bad = lost != 0;
-            const int64_t part = static_cast<int64_t>(part_of(blockIdx.x, run.first)) * kPagedRows;
+            // outputs by rows: an output element a thread, then a row a warp
+            float* stage = reinterpret_cast<float*>(smem + L::kPOff);  // P's place is free: its last product is done
+            constexpr int kStage = 128 * NH;
 #pragma unroll
-            for (int j = 0; j < R; ++j) {
-                if (j >= live) continue;
-                float sum = (red[j] + red[16 + j]) + (red[32 + j] + red[48 + j]);
-                if (bad) sum = NAN;
-                const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
-                if (!whole && th == j) a.part_ml[part + j] = make_float2(m[j], sum);
+            for (int h = 0; h < NH; ++h)
 #pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    const int d = th + 128 * h;
-                    if (d >= D) continue;
-                    if (whole) {
-                        const float y = o[h][j] * inv;
-                        a.out[(row0 + j) * D + d] = a.gate ? gated(y, z[h][j]) : y;
-                    } else {
-                        a.part_o[(part + j) * D + d] = o[h][j];
-                    }
-                }
+                for (int j = 0; j < R; ++j) stage[j * kStage + 128 * h + th] = o[h][j];
+            if (th < R) {
+                float sum = (red[th] + red[16 + th]) + (red[32 + th] + red[48 + th]);
+                if (lost != 0) sum = NAN;
+                sums[th] = sum;
+                float mine = m[0];
+#pragma unroll
+                for (int j = 1; j < R; ++j) mine = th == j ? m[j] : mine;
+                sums[16 + th] = mine;
             }
-            named_barrier_sync(1, 128);  // red is free again; the part is written
+            named_barrier_sync(1, 128);
+            const bool whole = run.whole();
+            const int first = whole ? 0 : walk.owner(run.u0);
+            const int64_t part = static_cast<int64_t>(part_of(blockIdx.x, first)) * kPagedRows;
+            for (int j = warp & 3; j < live; j += 4) {
+                const float sum = sums[j];
+                if (!whole && lane == 0) a.part_ml[part + j] = make_float2(sums[16 + j], sum);
+                const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+                each_piece(D, lane, [&](int d) {
+                    float4 y = lds_float4(stage + j * kStage + d);
+                    if (whole) {
+                        y = scaled(y, inv);
+                        if (a.gate) y = gated4(y, __ldcg(reinterpret_cast<const float4*>(a.gate + (row0 + j) * D + d)));
+                    }
+                    *reinterpret_cast<float4*>((whole ? a.out + (row0 + j) * D : a.part_o + (part + j) * D) + d) = y;
+                });
+            }
+            named_barrier_sync(1, 128);  // what was staged has been read; the part is written
             if (whole) continue;
-            // P's place is free: the run's last product has been read
-            finish_item<128>(a, run, th, reinterpret_cast<float*>(smem + L::kPOff), joining);
+            finish_item(a, walk, run, first, th, 128, joining);
             named_barrier_sync(1, 128);
         }
     }
