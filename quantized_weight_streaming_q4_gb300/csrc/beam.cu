@@ -250,7 +250,6 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     // the request's last block goes on
     __syncthreads();
     if (tid == 0) {
-        __threadfence();
         const unsigned blocks = static_cast<unsigned>(a.beams * a.parts);
         S.last = atom_add_acq_rel_gpu(a.ticket + g, 1u) == blocks - 1u;
         if (S.last) a.ticket[g] = 0;

@@ -10,7 +10,8 @@
 //    four tiles, so items of up to four are left whole; longer ones are cut as
 //    far as there are blocks.
 //  - else all items' tiles in a row are cut into as many equal runs as there are
-//    blocks, so that a run may end inside an item.
+//    blocks, so that a run may end inside an item.  An item counts as kOver tiles
+//    more than it has: that is what a block spends on its start and its end.
 // The blocks of an item leave partial results, and the last of them to finish
 // joins these in the items' order (of more than 16, eight at a time first).  No
 // block waits for another.
@@ -72,18 +73,21 @@ struct Sight {
         const int last = p0 + TILE <= low ? sink : end;
         return min(TILE, max(0, last - p0));
     }
-    // whether every row of the tile's first `n` is seen
-    __device__ __forceinline__ bool whole(int p0, int n) const { return n == TILE && (p0 >= low || p0 + TILE <= sink); }
 };
 
-// The split, in shared memory: positions (-1: no work) and the units before
-// each token row, tiles (chunk 0) or pieces of up to `chunk` tiles.
+// The split: positions (-1: no work) and the units before each token row,
+// tiles (chunk 0) or pieces of up to `chunk` tiles, in shared memory; the rest
+// in every warp's registers.
 struct PagedPlan {
     int32_t t[kMaxSequences];
     uint32_t before[kMaxSequences + 1];
-    uint32_t chunk, first_row;  // first_row: that the block's first unit is of
+};
+struct PagedSplit {
+    uint32_t units, chunk;
+    int first_row;  // that the block's first unit is of
 };
 constexpr int kMostChunk = 8, kWholeTiles = 4;
+constexpr uint32_t kOver = 2;
 
 __device__ __forceinline__ uint32_t ceil_div(uint32_t x, uint32_t y) { return (x + y - 1) / y; }
 
@@ -112,70 +116,86 @@ struct PagedShare {
     }
 };
 
-// Fills the plan; all of the block's threads (256) call it.  `warp_sums`: 80
-// words of shared memory.
-template <int TILE>
-__device__ __forceinline__ void make_plan(const PagedArgs& a, PagedPlan& plan, uint32_t* warp_sums) {
-    static_assert(kMaxSequences == 256, "a thread a token row");
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int warps = (a.n + 31) / 32;  // that have rows
-    uint32_t mine = 0;
-    int t = -1;
-    if (tid < a.n) {
-        t = __ldcg(a.position + tid);
-        if (a.sequence) {
-            const int s = __ldcg(a.sequence + tid);
-            if (s < 0 || s >= a.n_tables) t = -1;
-        } else if (tid >= a.n_tables) {
-            t = -1;
-        }
-        t = min(t, 0x3fffffff);
-    }
-    plan.t[tid] = t;
-    if (t >= 0) mine = static_cast<uint32_t>(Sight<TILE>(a, t).tiles);
-    // sums over the rows: tiles, the longest, and pieces for each chunk
-    if (w < warps) {
-        const uint32_t most = __reduce_max_sync(0xffffffffu, mine);
-        if (lane == 0) warp_sums[w * 10] = most;
-#pragma unroll
-        for (uint32_t c = 1; c <= kMostChunk; ++c) {
-            const uint32_t sum = __reduce_add_sync(0xffffffffu, ceil_div(mine, c));
-            if (lane == 0) warp_sums[w * 10 + c] = sum;
-        }
-    }
-    __syncthreads();
-    // lane c of every warp: the pieces of chunk c; lane 0: the longest
-    uint32_t sum = 0;
-    if (lane <= kMostChunk)
-        for (int j = 0; j < warps; ++j) sum = lane == 0 ? max(sum, warp_sums[j * 10]) : sum + warp_sums[j * 10 + lane];
+// The position of token row i, -1 where it has no work.
+__device__ __forceinline__ int position_of(const PagedArgs& a, int i) {
+    if (i >= a.n) return -1;
+    int t = __ldcg(a.position + i);
+    const int s = a.sequence ? __ldcg(a.sequence + i) : i;
+    if (s < 0 || s >= a.n_tables) t = -1;
+    return min(t, 0x3fffffff);
+}
+
+// The chunk for sums of pieces, lane c's those of chunk c (lane 0: the longest
+// row's tiles, lane 9: rows with work); `all` becomes the number of units.
+__device__ __forceinline__ uint32_t choose_chunk(const PagedArgs& a, uint32_t sum, uint32_t& all) {
+    const int lane = threadIdx.x & 31;
     const bool fits = lane > 0 && lane <= kMostChunk && static_cast<uint64_t>(sum) * static_cast<uint32_t>(a.G * a.blocks_per_head) <= gridDim.x;
     const uint32_t fit = __ballot_sync(0xffffffffu, fits);
     uint32_t chunk = fit == 0 ? 0 : __ffs(fit) - 1;
     if (chunk > 0 && __shfl_sync(0xffffffffu, sum, 0) <= kWholeTiles) chunk = kWholeTiles;
-    const uint32_t all = __shfl_sync(0xffffffffu, sum, chunk == 0 ? 1 : chunk);
-    const uint32_t units = chunk <= 1 ? mine : divide(mine + chunk - 1, chunk);
+    all = __shfl_sync(0xffffffffu, sum, chunk == 0 ? 1 : chunk);
+    const uint32_t rows = __shfl_sync(0xffffffffu, sum, kMostChunk + 1);
+    if (chunk == 0) all += kOver * rows;
+    return chunk;
+}
+
+// Fills the plan; all of the block's threads (256) call it.  Up to 32 token
+// rows every warp does it for itself, without a barrier; `warp_sums`: 80 words
+// of shared memory for more.
+template <int TILE>
+__device__ __forceinline__ PagedSplit make_plan(const PagedArgs& a, PagedPlan& plan, uint32_t* warp_sums) {
+    static_assert(kMaxSequences == 256, "a thread a token row");
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const bool one = a.n <= 32;
+    const int i = one ? lane : tid;
+    const int t = position_of(a, i);
+    const uint32_t mine = t >= 0 ? static_cast<uint32_t>(Sight<TILE>(a, t).tiles) : 0;
+    uint32_t sum = __reduce_max_sync(0xffffffffu, mine);  // lane 0; lane c: pieces of chunk c
+#pragma unroll
+    for (uint32_t c = 1; c <= kMostChunk; ++c) {
+        const uint32_t x = __reduce_add_sync(0xffffffffu, ceil_div(mine, c));
+        if (lane == static_cast<int>(c)) sum = x;
+    }
+    const uint32_t working = __popc(__ballot_sync(0xffffffffu, mine > 0));
+    if (lane == kMostChunk + 1) sum = working;
+    if (!one) {
+        if (lane <= kMostChunk + 1) warp_sums[w * 10 + lane] = sum;
+        __syncthreads();
+        sum = 0;
+        if (lane <= kMostChunk + 1)
+            for (int j = 0; j < 8; ++j) sum = lane == 0 ? max(sum, warp_sums[j * 10]) : sum + warp_sums[j * 10 + lane];
+        __syncthreads();
+    }
+    PagedSplit split;
+    split.chunk = choose_chunk(a, sum, split.units);
+    const uint32_t units = split.chunk == 0 ? (mine > 0 ? mine + kOver : 0) : ceil_div(mine, split.chunk);
     uint32_t v = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += x;
     }
-    if (warps > 1) {
-        __syncthreads();
+    if (!one) {
         if (lane == 31) warp_sums[w] = v;
         __syncthreads();
         for (int j = 0; j < w; ++j) v += warp_sums[j];
     }
-    if (w >= warps) v = all;  // rows behind the last one
-    plan.before[tid] = v - units;
-    if (tid == 0) plan.before[kMaxSequences] = all;
-    const PagedShare share(a, all);
+    // every warp writes the same where `one`
+    plan.t[i] = t;
+    plan.before[i] = v - units;
+    if (one ? lane == 31 : tid == 255) plan.before[i + 1] = v;
+    const PagedShare share(a, split.units);
     const uint64_t per = static_cast<uint32_t>(a.G * a.blocks_per_head);
-    if ((v - units) * per <= share.at && share.at < v * per) {
-        plan.first_row = tid;
-        plan.chunk = chunk;
+    const bool here = (v - units) * per <= share.at && share.at < v * per;
+    if (one) {
+        split.first_row = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        __syncwarp();
+    } else {
+        if (here) warp_sums[16] = i;
+        __syncthreads();
+        split.first_row = static_cast<int>(warp_sums[16]);
     }
-    __syncthreads();
+    return split;
 }
 
 // A run of one item's tiles.
@@ -193,10 +213,13 @@ struct PagedWalk {
     PagedShare share;
     uint32_t chunk;
     int m;
-    __device__ __forceinline__ PagedWalk(const PagedArgs& a, const PagedPlan& plan)
-        : share(a, plan.before[kMaxSequences]), chunk(plan.chunk), m(static_cast<int>(plan.first_row)) {}
+    __device__ __forceinline__ PagedWalk(const PagedArgs& a, const PagedSplit& split)
+        : share(a, split.units), chunk(split.chunk), m(split.first_row) {}
+    // no further run: what is left of the share ends before the next item's first tile
+    // (a share is more than kOver units, so there is a first run)
+    __device__ __forceinline__ bool last() const { return share.at + (chunk == 0 ? kOver : 0) >= share.end; }
     __device__ __forceinline__ bool next(const PagedArgs& a, const PagedPlan& plan, PagedRun& run) {
-        if (share.at >= share.end) return false;
+        if (last()) return false;
         const uint64_t per = static_cast<uint32_t>(a.G * a.blocks_per_head);
         while (plan.before[m + 1] * per <= share.at) ++m;
         const uint64_t base = plan.before[m] * per;
@@ -217,10 +240,11 @@ struct PagedWalk {
             run.r0 = (static_cast<int>(sub) - run.head * a.blocks_per_head) * kPagedRows;
         }
         if (chunk == 0) {
-            run.tiles = static_cast<int>(units);
-            run.a = static_cast<int>(x);
-            run.b = static_cast<int>(min(static_cast<uint64_t>(units), x + (share.end - share.at)));
-            share.at += run.b - run.a;
+            const uint32_t x1 = static_cast<uint32_t>(min(static_cast<uint64_t>(units), x + (share.end - share.at)));
+            run.tiles = static_cast<int>(units - kOver);
+            run.a = static_cast<int>(max(x, kOver) - kOver);
+            run.b = static_cast<int>(max(x1, kOver) - kOver);
+            share.at += x1 - x;
             return true;
         }
         run.tiles = Sight<TILE>(a, plan.t[m]).tiles;
@@ -234,11 +258,13 @@ struct PagedWalk {
         ++share.at;
         return true;
     }
-    // the first and the last block that share the run's item
+    // the first and the last block that have tiles of the run's item
     __device__ __forceinline__ int owner(uint64_t unit) const {
         if (share.total == share.blocks) return static_cast<int>(unit);
         return static_cast<int>(divide((unit + 1) * share.blocks - 1, share.total));
     }
+    __device__ __forceinline__ int first_block(const PagedRun& run) const { return owner(run.u0 + (chunk == 0 ? kOver : 0)); }
+    __device__ __forceinline__ int last_block(const PagedRun& run) const { return owner(run.u0 + run.units - 1); }
 };
 
 // The partial result of block `b` of an item's blocks first..last: the block
@@ -256,12 +282,14 @@ template <typename F>
 __device__ __forceinline__ void each_piece(int D, int lane, F&& f) {
     for (int d = 4 * lane; d < D; d += 128) f(d);
 }
-__device__ __forceinline__ float4 load4(const float* p, bool vec, int left) {
-    if (vec) return __ldcg(reinterpret_cast<const float4*>(p));
+template <bool VEC>
+__device__ __forceinline__ float4 load4(const float* p, int left) {
+    if (VEC) return __ldcg(reinterpret_cast<const float4*>(p));
     return make_float4(__ldcg(p), left > 1 ? __ldcg(p + 1) : 0.f, left > 2 ? __ldcg(p + 2) : 0.f, left > 3 ? __ldcg(p + 3) : 0.f);
 }
-__device__ __forceinline__ void store4(float* p, float4 v, bool vec, int left) {
-    if (vec) {
+template <bool VEC>
+__device__ __forceinline__ void store4(float* p, float4 v, int left) {
+    if (VEC) {
         *reinterpret_cast<float4*>(p) = v;
         return;
     }
@@ -275,90 +303,122 @@ __device__ __forceinline__ float4 gated4(float4 v, float4 z) { return make_float
 
 // `count` parts, the first that of block `from` and each of a block `step`
 // further, are joined, into the item's result or (!final) into the first part.
-// A warp (w of W) takes every W-th row: its lanes hold the parts' shares.
-constexpr int kJoinMost = 16;
-__device__ __noinline__ void join_parts(const PagedArgs& a, const PagedRun& run, int first, int from, int step, int count, int w,
-                                        int W, bool final) {
-    constexpr int B = 8;  // loads in flight
-    const int lane = threadIdx.x & 31, live = min(kPagedRows, a.group - run.r0);
-    const bool vec = a.D % 4 == 0;
-    const int64_t row0 = static_cast<int64_t>(run.row) * a.H + run.head * a.group + run.r0;
-    for (int j = w; j < live; j += W) {
-        float2 ml = make_float2(kNegInf, 0.f);
-        const int64_t mine = (static_cast<int64_t>(part_of(from + lane * step, first)) * kPagedRows) + j;  // of lane i: part i
-        if (lane < count) ml = __ldcg(a.part_ml + mine);
+// A warp (w of W) takes every W-th row, two at a time; its lanes hold the
+// parts' shares.
+constexpr int kJoinMost = 13;
+static_assert(kPagedMaxBlocks <= kJoinMost * kJoinMost, "two levels");
+// What a join needs, by value: through a reference to the kernel's parameters
+// every access went to memory, and a join took 15 us.
+struct JoinWork {
+    float2* part_ml;
+    float* part_o;
+    const float* gate;  // of the item's first row, or null
+    float* out;
+    unsigned* ticket;
+    int D, live, first, last;  // first, last: the item's blocks
+};
+template <bool VEC>
+__device__ __noinline__ void join_parts(const JoinWork a, int from, int step, int count, int w, int W, bool final) {
+    constexpr int B = 10, U = 2;  // loads in flight of a row, rows
+    const int lane = threadIdx.x & 31, live = a.live;
+    // part i's row j
+    auto place = [&](int i, int j) { return static_cast<int64_t>(part_of(from + i * step, a.first)) * kPagedRows + j; };
+    for (int j0 = w; j0 < live; j0 += U * W) {
+        float2 ml[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            ml[u] = lane < count && j0 + u * W < live ? __ldcg(a.part_ml + place(lane, j0 + u * W)) : make_float2(kNegInf, 0.f);
         for (int d = 4 * lane; d - 4 * lane < a.D; d += 128) {
-            const bool real = d < a.D;
-            const float* p = a.part_o + (static_cast<int64_t>(part_of(from, first)) * kPagedRows + j) * a.D + d;
-            float4 z = make_float4(0.f, 0.f, 0.f, 0.f), o = z;
-            if (final && a.gate && real) z = load4(a.gate + (row0 + j) * a.D + d, vec, a.D - d);
-            float m = 0.f, l = 0.f, f = 0.f;
-            for (int i0 = 0; i0 < count; i0 += B) {
-                float4 v[B];
+            float4 z[U], o[U];
+            float m[U], l[U], f[U];
 #pragma unroll
-                for (int i = 0; i < B; ++i) {
-                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (real && i0 + i < count)
-                        v[i] = load4(a.part_o + (static_cast<int64_t>(part_of(from + (i0 + i) * step, first)) * kPagedRows + j) * a.D + d, vec, a.D - d);
-                }
-                if (i0 == 0) {  // the shares, while the sums are on the way
-                    m = ml.x;
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    const bool empty = ml.x == kNegInf && ml.y == 0.f;  // no rows there: its sums are not looked at
-                    f = empty ? kNegInf : share(ml.x, m);
-                    l = warp_sum(empty ? 0.f : f * ml.y);
-                }
-#pragma unroll
-                for (int i = 0; i < B; ++i) {
-                    const float fi = __shfl_sync(0xffffffffu, f, min(i0 + i, 31));
-                    if (i0 + i < count && fi != kNegInf)
-                        o = make_float4(fmaf(fi, v[i].x, o.x), fmaf(fi, v[i].y, o.y), fmaf(fi, v[i].z, o.z), fmaf(fi, v[i].w, o.w));
-                }
+            for (int u = 0; u < U; ++u) {
+                o[u] = z[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (final && a.gate && d < a.D && j0 + u * W < live) z[u] = load4<VEC>(a.gate + static_cast<int64_t>(j0 + u * W) * a.D + d, a.D - d);
             }
-            if (!real) continue;
-            if (final) {
-                o = scaled(o, l == 0.f ? 0.f : __fdividef(1.f, l));
-                store4(a.out + (row0 + j) * a.D + d, a.gate ? gated4(o, z) : o, vec, a.D - d);
-            } else {
-                store4(const_cast<float*>(p), o, vec, a.D - d);
-                if (d == 0) a.part_ml[mine] = make_float2(m, l);
+            for (int i0 = 0; i0 < count; i0 += B) {
+                float4 v[U][B];
+#pragma unroll
+                for (int i = 0; i < B; ++i)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        v[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (i0 + i < count && d < a.D && j0 + u * W < live)
+                            v[u][i] = load4<VEC>(a.part_o + place(i0 + i, j0 + u * W) * a.D + d, a.D - d);
+                    }
+                if (i0 == 0) {  // the shares, while the sums are on the way
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        m[u] = ml[u].x;
+#pragma unroll
+                        for (int x = 16; x > 0; x >>= 1) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], x));
+                        const bool empty = ml[u].x == kNegInf && ml[u].y == 0.f;  // no rows there: its sums are not looked at
+                        f[u] = empty ? kNegInf : share(ml[u].x, m[u]);
+                        l[u] = warp_sum(empty ? 0.f : f[u] * ml[u].y);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < B; ++i)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const float fi = __shfl_sync(0xffffffffu, f[u], i0 + i);
+                        if (i0 + i < count && fi != kNegInf)
+                            o[u] = make_float4(fmaf(fi, v[u][i].x, o[u].x), fmaf(fi, v[u][i].y, o[u].y), fmaf(fi, v[u][i].z, o[u].z), fmaf(fi, v[u][i].w, o[u].w));
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = j0 + u * W;
+                if (d >= a.D || j >= live) continue;
+                if (final) {
+                    const float4 y = scaled(o[u], l[u] == 0.f ? 0.f : __fdividef(1.f, l[u]));
+                    store4<VEC>(a.out + static_cast<int64_t>(j) * a.D + d, a.gate ? gated4(y, z[u]) : y, a.D - d);
+                } else {
+                    store4<VEC>(a.part_o + place(0, j) * a.D + d, o[u], a.D - d);
+                    if (d == 0) a.part_ml[place(0, j)] = make_float2(m[u], l[u]);
+                }
             }
         }
     }
 }
 
 // Whether this was the last of `count` arrivals at a ticket; called by one
-// thread, when all threads that wrote what it announces have passed a barrier.
+// thread, when all threads that wrote what it announces have passed a barrier
+// with it (the atomic releases what is ordered before it).
 __device__ __forceinline__ bool last_of(unsigned* ticket, int count) {
-    __threadfence();
     const bool last = atom_add_acq_rel_gpu(ticket, 1u) == static_cast<unsigned>(count - 1);
     if (last) *ticket = 0;
     return last;
 }
 
-// After the block's part of an item is written, by `threads` threads (whole
-// warps) that share barrier 1 and have passed it since: what is left to join,
-// if this is the last block to get there.  `flag` is in shared memory.
-template <int TILE>
-__device__ __forceinline__ void finish_item(const PagedArgs& a, const PagedWalk<TILE>& walk, const PagedRun& run, int first, int tid,
-                                            int threads, volatile uint32_t& flag) {
-    const int last = walk.owner(run.u0 + run.units - 1), count = last - first + 1, w = tid >> 5, W = threads >> 5;
-    static_assert(kPagedMaxBlocks <= kJoinMost * kJoinMost, "two levels");
+// After the block's part of an item is written: what is left to join, if this
+// is the last block to get there.  Called by `threads` threads (whole warps; tid
+// counts them) that share barrier `id` and have passed a barrier with those that
+// wrote the part; `flag` is in shared memory.  `go`: thread 0 knows that it is
+// written (else the item stays open, and its tickets taken).
+template <bool VEC>
+__device__ __noinline__ void finish_item(const JoinWork a, int tid, int threads, int id, volatile uint32_t* flag, bool go) {
+    const int count = a.last - a.first + 1, w = tid >> 5, W = threads >> 5;
     int step = 1, parts = count;
     if (count > kJoinMost) {
         while (step * step < count) ++step;  // as many groups as parts in each
-        const int from = first + (static_cast<int>(blockIdx.x) - first) / step * step, size = min(step, last - from + 1);
-        if (tid == 0) flag = last_of(a.ticket + part_of(from, first), size);
-        named_barrier_sync(1, threads);
-        if (!flag) return;
-        join_parts(a, run, first, from, 1, size, w, W, false);
+        const int from = a.first + (static_cast<int>(blockIdx.x) - a.first) / step * step, size = min(step, a.last - from + 1);
+        if (tid == 0) *flag = go && last_of(a.ticket + part_of(from, a.first), size);
+        named_barrier_sync(id, threads);
+        if (!*flag) return;
+        join_parts<VEC>(a, from, 1, size, w, W, false);
         parts = (count + step - 1) / step;
-        named_barrier_sync(1, threads);
+        named_barrier_sync(id, threads);
     }
-    if (tid == 0) flag = last_of(a.ticket + 2 * kPagedMaxBlocks + first, parts);
-    named_barrier_sync(1, threads);
-    if (flag) join_parts(a, run, first, first, step, parts, w, W, true);
+    if (tid == 0) *flag = go && last_of(a.ticket + 2 * kPagedMaxBlocks + a.first, parts);
+    named_barrier_sync(id, threads);
+    if (*flag) join_parts<VEC>(a, a.first, step, parts, w, W, true);
+}
+template <int TILE>
+__device__ __forceinline__ JoinWork join_work(const PagedArgs& a, const PagedWalk<TILE>& walk, const PagedRun& run) {
+    const int64_t at = (static_cast<int64_t>(run.row) * a.H + run.head * a.group + run.r0) * a.D;
+    return JoinWork{a.part_ml, a.part_o, a.gate ? a.gate + at : nullptr, a.out + at, a.ticket, a.D, min(kPagedRows, a.group - run.r0),
+                    walk.first_block(run), walk.last_block(run)};
 }
 
 }  // namespace

@@ -33,10 +33,10 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     pdl_wait();
-    make_plan<kTile>(a, plan, reinterpret_cast<uint32_t*>(sm));
-    PagedWalk<kTile> walk(a, plan);
+    PagedWalk<kTile> walk(a, make_plan<kTile>(a, plan, reinterpret_cast<uint32_t*>(sm)));
     PagedRun run;
     while (walk.next(a, plan, run)) {
+        __syncthreads();  // the plan's sums, and the run before, are done with what `sm` held
         const Sight<kTile> sight(a, plan.t[run.row]);
         const int live = min(kPagedRows, a.group - run.r0);
         const int seq = a.sequence ? __ldcg(a.sequence + run.row) : run.row;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
                 }
             }
         }
-        const int first = run.whole() ? 0 : walk.owner(run.u0);
+        const int first = run.whole() ? 0 : walk.first_block(run);
 #pragma unroll
         for (int u = 0; u < kQ; ++u) {
             const int r = warp * kQ + u;
@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
         }
         __syncthreads();
         if (run.whole()) continue;
-        finish_item(a, walk, run, first, tid, kThreads, flag);
+        if (D % 4 == 0) finish_item<true>(join_work(a, walk, run), tid, kThreads, 1, &flag, true);
+        else finish_item<false>(join_work(a, walk, run), tid, kThreads, 1, &flag, true);
         __syncthreads();
     }
 }

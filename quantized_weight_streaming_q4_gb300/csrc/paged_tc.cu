@@ -46,7 +46,7 @@ struct Layout {
     static constexpr int kNS = 196608 / static_cast<int>(kItem);  // stages of the ring: 12, 6 or 3
     // the barriers: the stages' full and empty ones first
     static constexpr int kFull = 0, kEmpty = kNS, kSFull = 2 * kNS, kPFull = kSFull + 2, kOFull = kPFull + 2,
-                         kQFull = kOFull + 2, kQFree = kQFull + 2, kBars = kQFree + 2;
+                         kQFull = kOFull + 2, kQFree = kQFull + 2, kJoin = kQFree + 2, kBars = kJoin + 1;
     static constexpr uint32_t kN = 2 * R;                         // columns
     static constexpr uint32_t kKeyRow = kN / 8 * 128;             // P: bytes from 8 keys to the next 8
     static constexpr uint32_t kPBytes = kTile / 8 * kKeyRow;
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     PagedPlan& plan = *reinterpret_cast<PagedPlan*>(smem + L::kPlanOff);
     uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(smem + L::kPlanOff + sizeof(PagedPlan));
     volatile uint32_t& lost = (&tmem_slot)[1];  // a wait ran out
-    volatile uint32_t& joining = (&tmem_slot)[2];
+    volatile uint32_t* joining = &tmem_slot + 2;  // whether this block joins the parts of its first and of its last item
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
     pdl_launch_dependents();
@@ -151,16 +151,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar[L::kQFull + i], kQThreads);
             mbar_init(&bar[L::kQFree + i], 128);
         }
+        mbar_init(&bar[L::kJoin], 1);
         lost = 0;
         fence_mbar_init();
     }
     if (warp == 0) tmem_alloc(&tmem_slot, L::kTmemCols);
     if (tid == 32) prefetch_map(&kmap);
     if (tid == 64) prefetch_map(&vmap);
-    pdl_wait();  // no global access before this
     tc_fence_before();
-    make_plan<kTile>(a, plan, reinterpret_cast<uint32_t*>(smem + L::kPOff));
+    __syncthreads();  // the barriers and tensor memory
     tc_fence_after();
+    pdl_wait();  // no global access before this
+    const PagedSplit split = make_plan<kTile>(a, plan, reinterpret_cast<uint32_t*>(smem + L::kPOff));
     const uint32_t tmem = tmem_slot;
     // A thread whose wait has run out waits no more and goes on with what is
     // there, so that warps and warpgroups stay together; what it would write
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](int b, int phase) {
         if (ok) ok = mbar_wait_bounded(&bar[b], static_cast<uint32_t>(phase & 1), a.status, kDevStatusWaitTimeout);
     };
-    PagedWalk<kTile> walk(a, plan);
+    PagedWalk<kTile> walk(a, split);
     PagedRun run;
     const int D = a.D;
 
@@ -254,17 +256,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Sight<kTile> sight(a, plan.t[run.row]);
             const int seq = a.sequence ? __ldcg(a.sequence + run.row) : run.row;
             const int32_t* table = a.table + seq * a.stride;
-            // the page of this lane's box of tile t, -1 where no row of it is seen
+            // the page of this lane's box of tile t, -1 where no row of it is seen;
+            // looked at a tile later, so that nothing waits for the load
             auto entry = [&](int t) {
                 if (t >= run.b || lane >= boxes) return -1;
                 const int p0 = sight.first(t) * kTile, p = p0 + lane * box;
                 if (lane * box >= sight.real(p0) || (p + box <= sight.low && p >= sight.sink)) return -1;
-                const int page = __ldcg(table + (p >> a.page_shift));
-                return page >= 0 && page < a.pages ? page : -1;
+                return __ldcg(table + (p >> a.page_shift));
             };
-            int page = entry(run.a);
+            int next_page = entry(run.a);
             for (int t = run.a; t < run.b && ok; ++t) {
-                const int after = entry(t + 1);
+                const int page = static_cast<uint32_t>(next_page) < static_cast<uint32_t>(a.pages) ? next_page : -1;
+                next_page = entry(t + 1);
                 const int p = sight.first(t) * kTile + lane * box, row = p & (a.page_rows - 1);
                 const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
 #pragma unroll
@@ -284,7 +287,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int x = 0; x < blocks; ++x) load_box(dst + x * kHalf, v ? &vmap : &kmap, x, row, run.head, page, full);
                     }
                 }
-                page = after;
             }
         }
         if (!ok) {  // copies under way still write into this block's memory
@@ -384,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* red = reinterpret_cast<float*>(smem + L::kRedOff);
         float* sums = reinterpret_cast<float*>(smem + L::kSumsOff);
         int runs = 0, tile = 0;  // counted over all runs
+        JoinWork early{}, late{};  // items that the block shares: its first run's, its last run's
         while (walk.next(a, plan, run)) {
             const int buf = runs % L::kQBufs;
             const Sight<kTile> sight(a, plan.t[run.row]);
@@ -392,19 +395,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t row0 = static_cast<int64_t>(run.row) * a.H + run.head * a.group + run.r0;
             const int seq = a.sequence ? __ldcg(a.sequence + run.row) : run.row;
             const int32_t* table = a.table + seq * a.stride;
-            auto entry = [&](int t) {  // whether this thread's key of tile t is seen
-                if (t >= run.b) return false;
+            auto entry = [&](int t) {  // the page of this thread's key of tile t, -1 where it is not seen
                 const int p = sight.first(t) * kTile + th;
-                if (!sight.sees(p)) return false;
-                return static_cast<uint32_t>(__ldcg(table + (p >> a.page_shift))) < static_cast<uint32_t>(a.pages);
+                return t < run.b && sight.sees(p) ? __ldcg(table + (p >> a.page_shift)) : -1;
             };
-            bool see = entry(run.a);
+            int next_page = entry(run.a);
             float vs[NH];
 #pragma unroll
             for (int h = 0; h < NH; ++h)
                 vs[h] = self && th + 128 * h < D
                             ? __half2float(__float2half_rn(__ldcg(a.v + (static_cast<int64_t>(run.row) * a.G + run.head) * D + th + 128 * h)))
                             : 0.f;
+            // the gate of this warp's rows, where the block writes them out
+            float4 z[NH == 1 ? R / 4 : 1];
+            if (NH == 1) {
+#pragma unroll
+                for (int i = 0; i < R / 4; ++i) {
+                    const int j = (warp & 3) + 4 * i;
+                    z[i] = a.gate && run.whole() && j < live && 4 * lane < D ? __ldcg(reinterpret_cast<const float4*>(a.gate + (row0 + j) * D) + lane)
+                                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
             wait(L::kQFull + buf, runs / L::kQBufs);
             float sc[R], b[R], m[R], l[R], o[NH][R];
 #pragma unroll
@@ -437,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int t = run.a; t < run.b; ++t, ++tile) {
                 const int p0 = sight.first(t) * kTile, real = sight.real(p0);
-                const bool seen = see;
-                see = entry(t + 1);
+                const bool seen = static_cast<uint32_t>(next_page) < static_cast<uint32_t>(a.pages);
+                next_page = entry(t + 1);
                 if (!seen && th < (max(real, 1) + 15) / 16 * 16) {  // the product must not meet what this V row holds
                     const int vi = 2 * tile + 1, st = vi % kNS;
                     wait(L::kFull + st, vi / kNS);
@@ -531,25 +542,152 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             named_barrier_sync(1, 128);
             const bool whole = run.whole();
-            const int first = whole ? 0 : walk.owner(run.u0);
-            const int64_t part = static_cast<int64_t>(part_of(blockIdx.x, first)) * kPagedRows;
-            for (int j = warp & 3; j < live; j += 4) {
+            const JoinWork work = join_work(a, walk, run);
+            const int64_t part = static_cast<int64_t>(part_of(blockIdx.x, work.first)) * kPagedRows;
+            auto write_row = [&](int j, int d, float4 gate) {
+                float4 y = lds_float4(stage + j * kStage + d);
                 const float sum = sums[j];
-                if (!whole && lane == 0) a.part_ml[part + j] = make_float2(sums[16 + j], sum);
-                const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
-                each_piece(D, lane, [&](int d) {
-                    float4 y = lds_float4(stage + j * kStage + d);
-                    if (whole) {
-                        y = scaled(y, inv);
-                        if (a.gate) y = gated4(y, __ldcg(reinterpret_cast<const float4*>(a.gate + (row0 + j) * D + d)));
-                    }
-                    *reinterpret_cast<float4*>((whole ? a.out + (row0 + j) * D : a.part_o + (part + j) * D) + d) = y;
-                });
+                if (whole) {
+                    y = scaled(y, sum == 0.f ? 0.f : __fdividef(1.f, sum));
+                    if (a.gate) y = gated4(y, gate);
+                } else if (d == 0) {
+                    a.part_ml[part + j] = make_float2(sums[16 + j], sum);
+                }
+                *reinterpret_cast<float4*>((whole ? work.out + j * D : a.part_o + (part + j) * D) + d) = y;
+            };
+            if (NH == 1) {
+#pragma unroll
+                for (int i = 0; i < R / 4; ++i) {
+                    const int j = (warp & 3) + 4 * i;
+                    if (j < live && 4 * lane < D) write_row(j, 4 * lane, z[i]);
+                }
+            } else {
+                for (int j = warp & 3; j < live; j += 4)
+                    each_piece(D, lane, [&](int d) {
+                        write_row(j, d, whole && a.gate ? __ldcg(reinterpret_cast<const float4*>(work.gate + j * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f));
+                    });
+            }
+            if (!whole) {
+                fence_proxy_async();  // the block that joins copies the part
+                if (runs == 1) early = work;
+                else late = work;
             }
             named_barrier_sync(1, 128);  // what was staged has been read; the part is written
-            if (whole) continue;
-            finish_item(a, walk, run, first, th, 128, joining);
-            named_barrier_sync(1, 128);
+        }
+        // Joins: a shared item is its block's first or last one.  The parts come
+        // as bulk copies into the stages, which are free now.
+        constexpr uint32_t kRing = kNS * L::kItem, kSharesOff = kRing - 4096;
+        float* const buffer = reinterpret_cast<float*>(smem);
+        float2* const mls = reinterpret_cast<float2*>(smem + kSharesOff);                    // [parts][16]
+        float* const shares = reinterpret_cast<float*>(smem + kSharesOff + 2048);            // [parts][16]
+        float* const total = shares + 16 * kJoinMost;                                        // [16]
+        static_assert(kJoinMost * 128 <= 2048 && 2048 + (kJoinMost + 1) * 64 <= 4096, "the shares fit");
+        int copies = 0;  // waits on the copies' barrier
+        auto join = [&](const JoinWork& w, int from, int step, int count, bool final) {
+            const bool gate = final && w.gate;
+            // rows whose parts fit the ring
+            const int most = min(w.live, static_cast<int>(kSharesOff / (static_cast<uint32_t>(count + gate) * D * 4u)));
+            auto place = [&](int i) { return static_cast<int64_t>(part_of(from + i * step, w.first)) * kPagedRows; };
+            for (int r0 = 0; r0 < w.live; r0 += most) {
+                const int rows = min(most, w.live - r0);
+                const uint32_t bytes = static_cast<uint32_t>(rows) * D * 4u;
+                named_barrier_sync(1, 128);  // what the ring held has been read
+                if (th < 32) {
+                    fence_proxy_async();
+                    if (th == 0) mbar_arrive_expect_tx(&bar[L::kJoin], (count + gate) * bytes + (r0 == 0 ? count * 128u : 0u));
+                    __syncwarp();
+                    if (th < count) {
+                        tma_load_1d(buffer + th * rows * D, w.part_o + (place(th) + r0) * D, bytes, &bar[L::kJoin]);
+                        if (r0 == 0) tma_load_1d(mls + th * 16, w.part_ml + place(th), 128, &bar[L::kJoin]);
+                    } else if (gate && th == count) {
+                        tma_load_1d(buffer + th * rows * D, w.gate + r0 * D, bytes, &bar[L::kJoin]);
+                    }
+                }
+                wait(L::kJoin, copies++);
+                if (!ok && th == 0)  // the copies still write into this block's memory
+                    mbar_wait_bounded(&bar[L::kJoin], static_cast<uint32_t>(copies - 1) & 1u, a.status, kDevStatusTxTimeout);
+                if (r0 == 0) {  // eight threads a row, up to two parts each
+                    const int j = th >> 3, i = th & 7;
+                    const float2 e0 = i < count ? mls[i * 16 + j] : make_float2(kNegInf, 0.f);
+                    const float2 e1 = i + 8 < count ? mls[(i + 8) * 16 + j] : make_float2(kNegInf, 0.f);
+                    float m = fmaxf(e0.x, e1.x);
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    // -infinity: a part without rows, whose sums are not looked at
+                    const float f0 = e0.x == kNegInf && e0.y == 0.f ? kNegInf : share(e0.x, m);
+                    const float f1 = e1.x == kNegInf && e1.y == 0.f ? kNegInf : share(e1.x, m);
+                    float l = (f0 == kNegInf ? 0.f : f0 * e0.y) + (f1 == kNegInf ? 0.f : f1 * e1.y);
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                    if (i < count) shares[i * 16 + j] = f0;
+                    if (i + 8 < count) shares[(i + 8) * 16 + j] = f1;
+                    if (i == 0) {
+                        total[j] = l;
+                        if (!final && j < w.live) w.part_ml[place(0) + j] = make_float2(m, l);
+                    }
+                    named_barrier_sync(1, 128);
+                }
+                for (int j = warp & 3; j < rows; j += 4)
+                    each_piece(D, lane, [&](int d) {
+                        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                        for (int i = 0; i < count; ++i) {
+                            const float f = shares[i * 16 + r0 + j];
+                            const float4 v = lds_float4(buffer + (i * rows + j) * D + d);
+                            if (f != kNegInf) y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+                        }
+                        if (final) {
+                            const float l = total[r0 + j];
+                            y = scaled(y, l == 0.f ? 0.f : __fdividef(1.f, l));
+                            if (gate) y = gated4(y, lds_float4(buffer + (count * rows + j) * D + d));
+                        }
+                        float* to = final ? w.out + (r0 + j) * D : w.part_o + (place(0) + r0 + j) * D;
+                        if (ok) *reinterpret_cast<float4*>(to + d) = y;
+                    });
+            }
+        };
+        // An item of more than kJoinMost parts is joined by groups of `step` first.
+        auto step_of = [](const JoinWork& w) {
+            const int count = w.last - w.first + 1;
+            int step = 1;
+            if (count > kJoinMost)
+                while (step * step < count) ++step;
+            return step;
+        };
+        if ((th & 31) == 0 && th < 64) {  // both tickets at once
+            const JoinWork& w = th == 0 ? early : late;
+            uint32_t mine = 0;
+            if (w.live > 0) {
+                const int step = step_of(w), count = w.last - w.first + 1;
+                const int from = w.first + (static_cast<int>(blockIdx.x) - w.first) / step * step;
+                mine = step > 1 ? last_of(w.ticket + part_of(from, w.first), min(step, w.last - from + 1))
+                                : last_of(w.ticket + 2 * kPagedMaxBlocks + w.first, count);
+            }
+            joining[th >> 5] = mine;
+        }
+        named_barrier_sync(1, 128);
+#pragma unroll 1
+        for (int it = 0; it < 2; ++it) {
+            if (joining[it] == 0) continue;
+            const JoinWork w = it == 0 ? early : late;
+            const int count = w.last - w.first + 1, step = step_of(w), groups = (count + step - 1) / step;
+            bool final = step == 1;
+            int from = final ? w.first : w.first + (static_cast<int>(blockIdx.x) - w.first) / step * step;
+            int stride = 1, parts = final ? count : min(step, w.last - from + 1);
+#pragma unroll 1
+            for (;;) {
+                join(w, from, stride, parts, final);
+                if (final) break;
+                fence_proxy_async();
+                named_barrier_sync(1, 128);
+                if (th == 0) joining[it] = last_of(w.ticket + 2 * kPagedMaxBlocks + w.first, groups);
+                named_barrier_sync(1, 128);
+                if (joining[it] == 0) break;
+                from = w.first;
+                stride = step;
+                parts = groups;
+                final = true;
+            }
         }
     }
     tc_fence_before();
