@@ -9,8 +9,7 @@
 // largest of beams * parts * n sums, of which only the parts whose largest is
 // among the requests' largest are looked at further.
 //
-// Binary64 is a thirty-second of binary32's rate here and is left to one
-// logarithm a row: the sums score + x - log-sum are pairs of binary32 numbers
+// Binary64 is slow here and is left to a few operations a row: the sums score + x - log-sum are pairs of binary32 numbers
 // (48 bits), compared as 64-bit keys.
 //
 // The n largest of many values: the values are dealt to 64 groups; the n-th
@@ -74,24 +73,28 @@ struct Pick {
 };
 
 // The n-th largest of the 64 groups' maxima (n <= 64); `top` is the thread's.
+// A group's eight lanes compare its maximum with eight others each.
 template <typename K>
 __device__ __forceinline__ K floor_of(Pick<K>& S, int n, K top) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, g = tid / kGroupLanes;
+    static_assert(kGroupLanes == 8 && kGroups == 64, "eight by eight");
 #pragma unroll
     for (int o = 1; o < kGroupLanes; o <<= 1) {
         const K x = __shfl_xor_sync(0xffffffffu, top, o);
         top = x > top ? x : top;
     }
-    if (tid % kGroupLanes == 0) S.group[tid / kGroupLanes] = top;
+    if (tid % kGroupLanes == 0) S.group[g] = top;
     if (tid == 0) S.count = 0;
     __syncthreads();
-    if (tid < kGroups) {
-        const K mine = S.group[tid];
-        int before = 0;
-#pragma unroll 16
-        for (int j = 0; j < kGroups; ++j) before += (S.group[j] > mine || (S.group[j] == mine && j < tid)) ? 1 : 0;
-        if (before == n - 1) S.floor = mine;
+    int before = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const int j = tid % kGroupLanes + 8 * u;
+        before += (S.group[j] > top || (S.group[j] == top && j < g)) ? 1 : 0;
     }
+#pragma unroll
+    for (int o = 1; o < kGroupLanes; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    if (before == n - 1) S.floor = top;
     __syncthreads();
     return S.floor;
 }
@@ -115,13 +118,14 @@ __device__ __forceinline__ int largest(Pick<K>& S, int n, K least, Each&& each, 
     __syncthreads();
     const int count = S.count;
     if (count <= kList) {
-        for (int i = tid; i < count; i += kThreads) {
-            const K k = S.list_key[i];
-            const int at = S.list_at[i];
+        for (int i = tid / 8; i < (count + 3) / 4 * 4; i += kThreads / 8) {  // eight lanes a value; whole warps
+            const K k = i < count ? S.list_key[i] : 0;
+            const int at = i < count ? S.list_at[i] : 0;
             int rank = 0;
-#pragma unroll 4
-            for (int j = 0; j < count; ++j) rank += (S.list_key[j] > k || (S.list_key[j] == k && S.list_at[j] < at)) ? 1 : 0;
-            if (rank < n) put(rank, k, at);
+            for (int j = tid % 8; j < count; j += 8) rank += (S.list_key[j] > k || (S.list_key[j] == k && S.list_at[j] < at)) ? 1 : 0;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+            if (i < count && rank < n && tid % 8 == 0) put(rank, k, at);
         }
         return min(count, n);
     }
@@ -184,27 +188,27 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     pdl_wait();
     const bool ended = a.ended && __ldg(a.ended + row) != 0;
     Cand* const mine = cand + (static_cast<int64_t>(row) * a.parts + part) * a.n;
+    const int v0 = static_cast<int>(static_cast<int64_t>(a.vocab) * part / a.parts);
+    const int len = static_cast<int>(static_cast<int64_t>(a.vocab) * (part + 1) / a.parts) - v0;
+    const float* p = a.logits + static_cast<int64_t>(row) * a.vocab + v0;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / 4u);
+    p -= off;  // 16-byte aligned; element i of the part is p[off + i]
+    float x[kPerThread];
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+        const int i = 4 * (tid + u * kThreads) - off;
+        if (i >= 0 && i + 4 <= len) {
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(p + off + i));
+            x[4 * u] = v.x, x[4 * u + 1] = v.y, x[4 * u + 2] = v.z, x[4 * u + 3] = v.w;
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[4 * u + c] = i + c >= 0 && i + c < len ? __ldcs(p + off + i + c) : kNegInf;
+        }
+    }
     if (ended) {  // one way on, with probability 1
         if (tid < a.n) mine[tid] = Cand{part == 0 && tid == 0 ? 0.f : kNegInf, a.end_token};
         if (tid == 0) stat[row * a.parts + part] = Stat{0.f, 0.f, 1};
     } else {
-        const int v0 = static_cast<int>(static_cast<int64_t>(a.vocab) * part / a.parts);
-        const int len = static_cast<int>(static_cast<int64_t>(a.vocab) * (part + 1) / a.parts) - v0;
-        const float* p = a.logits + static_cast<int64_t>(row) * a.vocab + v0;
-        const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / 4u);
-        p -= off;  // 16-byte aligned; element i of the part is p[off + i]
-        float x[kPerThread];
-#pragma unroll
-        for (int u = 0; u < kVec; ++u) {
-            const int i = 4 * (tid + u * kThreads) - off;
-            if (i >= 0 && i + 4 <= len) {
-                const float4 v = __ldcs(reinterpret_cast<const float4*>(p + off + i));
-                x[4 * u] = v.x, x[4 * u + 1] = v.y, x[4 * u + 2] = v.z, x[4 * u + 3] = v.w;
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) x[4 * u + c] = i + c >= 0 && i + c < len ? __ldcs(p + off + i + c) : kNegInf;
-            }
-        }
         float m = kNegInf;
 #pragma unroll
         for (int u = 0; u < kPerThread; ++u) m = fmaxf(m, x[u]);
@@ -240,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
         const int found = largest(
             S.part, a.n, least,
             [&](auto&& f) {
+                if (key_of(top) < least) return;  // most threads have none
 #pragma unroll
                 for (int u = 0; u < kPerThread; ++u)
                     f(x[u] == kNegInf ? 0u : key_of(x[u]), 4 * (tid + u / 4 * kThreads) - off + u % 4);
@@ -268,19 +273,26 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     if (tid == 0) S.opened = 0;
     for (int b = warp; b < a.beams; b += kThreads / 32) {
         const Stat* st = stat + (g * a.beams + b) * a.parts;
-        float e = kNegInf;
-        bool bad = false;
-        for (int i = lane; i < a.parts; i += 32) {
-            const float pe = __ldcg(&st[i].e);
-            bad = bad || pe != pe;
-            if (__ldcg(&st[i].sum) != 0) e = fmaxf(e, pe);
+        // the lane's first part stays in registers; beyond 32 the others are read twice
+        auto read = [&](int i) {
+            const uint4 w = __ldcg(reinterpret_cast<const uint4*>(st + i));
+            return Stat{__uint_as_float(w.x), 0.f, static_cast<uint64_t>(w.w) << 32 | w.z};
+        };
+        const Stat mine = lane < a.parts ? read(lane) : Stat{0.f, 0.f, 0};
+        float e = mine.sum != 0 ? mine.e : kNegInf;
+        bool bad = mine.e != mine.e;
+        for (int i = lane + 32; i < a.parts; i += 32) {
+            const Stat p = read(i);
+            bad = bad || p.e != p.e;
+            if (p.sum != 0) e = fmaxf(e, p.e);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
         uint64_t s = 0;
         for (int i = lane; i < a.parts; i += 32) {
-            const float behind = e - __ldcg(&st[i].e);
-            if (behind < 64.f) s += __ldcg(&st[i].sum) >> static_cast<int>(fmaxf(behind, 0.f));
+            const Stat p = i == lane ? mine : read(i);
+            const float behind = e - p.e;
+            if (behind < 64.f) s += p.sum >> static_cast<int>(fmaxf(behind, 0.f));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -294,10 +306,13 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     if (tid < a.beams) {
         const int r = g * a.beams + tid;
         const bool end = a.ended && __ldg(a.ended + r) != 0;
-        const double score = __ldcg(a.score + r);
-        // ln(total 2^(e - 40))
-        double sum = score - (end ? 0.0 : (static_cast<double>(S.e[tid]) - 40.0 + log2(static_cast<double>(S.total[tid]))) * 0.693147180559945309417);
-        if (!end && S.total[tid] == 0) sum = NAN;
+        // ln(total 2^(e - 40)): the leading bit's place, and the logarithm of what follows it
+        const uint64_t t = S.total[tid];
+        const int place = 63 - __clzll(static_cast<long long>(t | 1));
+        const float fraction = log2f(static_cast<float>(t << (63 - place)) * 0x1p-63f);
+        double sum = __ldcg(a.score + r);
+        if (!end) sum -= (static_cast<double>(S.e[tid] + static_cast<float>(place - 40)) + fraction) * 0.693147180559945309417;
+        if (!end && t == 0) sum = NAN;
         const float hi = static_cast<float>(sum);
         S.base[tid] = make_float2(hi, fabsf(hi) < INFINITY ? static_cast<float>(sum - hi) : 0.f);
         S.ended[tid] = end;

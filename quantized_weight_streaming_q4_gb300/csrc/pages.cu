@@ -25,13 +25,15 @@ struct TabShared {
     int32_t parent[kRows], keep[kRows], rows[kRows], own[kRows];  // own: the page a row goes on in, or -1
     int32_t need_end[kRows];   // pages given to the rows up to this one
     int32_t copy[kRows];
-    int64_t new_end[kRows];    // new rows up to this one's
+    int32_t held[kRows];       // pages of the rows that stay
+    int32_t new_end[kRows];    // new rows up to this one's; beyond 2^31 - 1 they are too many anyhow
     int32_t task_end[kRows];   // runs of entries of the rows up to this one
     int32_t copy_at[kRows];
     int32_t free_end[kTabThreads];  // free pages in the words of the threads up to this one
     int64_t warp64[kTabWarps][1];
     int32_t warp1[kTabWarps][1], warp3[kTabWarps][3];
     int64_t total_new;
+    int32_t listed;            // new rows that get slots
     int32_t status, total_need, total_copy, free;
 };
 constexpr int kEach = 8;  // entries of a lane's turn
@@ -183,6 +185,7 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
             need = min(copy + ceil_div(S.rows[tid], R) - ceil_div(S.keep[tid], R), a.pages + 1);  // more than there are is too many
             fresh = S.rows[tid] - S.keep[tid];
             S.copy[tid] = copy;
+            S.held[tid] = ceil_div(S.keep[tid], R);
         }
         const bool listed = copy && own >= 0;
         __syncthreads();
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
         const int64_t new_end = new_sum[0];
         if (tid < a.n) {
             S.need_end[tid] = sums[0];
-            S.new_end[tid] = new_end;
+            S.new_end[tid] = static_cast<int32_t>(min(new_end, int64_t{0x7fffffff}));
             S.copy_at[tid] = sums[1] - (listed ? 1 : 0);
         }
         S.free_end[tid] = sums[2];
@@ -215,25 +218,25 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
         __syncthreads();
         const bool done = S.status == 0;
         const int give = done ? S.total_need : 0;
-        for (int at = tid; at < give; at += kTabThreads) {
-            // the free page of rank `at`: its thread's words, the word, the bit
-            const int owner = find_row(S.free_end, kTabThreads, at);
-            int left = at - (owner == 0 ? 0 : S.free_end[owner - 1]), w = owner * per;
-            uint32_t open = ~bits[w];
-            for (int c = __popc(open); left >= c; c = __popc(open)) {
-                left -= c;
-                open = ~bits[++w];
-            }
-            for (; left > 0; --left) open &= open - 1;
-            const int page = 32 * w + __ffs(open) - 1;
-            const int i = find_row(S.need_end, a.n, at);
-            const int j = at - (i == 0 ? 0 : S.need_end[i - 1]), held = ceil_div(S.keep[i], R);
-            a.table_out[i * a.stride + held + j - S.copy[i]] = page;
-            if (j == 0 && S.copy[i] && S.own[i] >= 0) {
-                int32_t* c = a.copies + 3 * S.copy_at[i];
-                c[0] = S.own[i];
-                c[1] = page;
-                c[2] = S.keep[i] % R;
+        // a warp takes a thread's words, a lane a page of each: its rank among the free ones
+        for (int owner = tid >> 5; owner < kTabThreads; owner += kTabWarps) {
+            int base = owner == 0 ? 0 : S.free_end[owner - 1];
+            if (base >= give) break;
+            const int end = min(words, (owner + 1) * per);
+            for (int w = owner * per; w < end; ++w) {
+                const uint32_t open = ~bits[w];
+                const int at = base + __popc(open & ((1u << lane) - 1u));
+                base += __popc(open);
+                if (!((open >> lane) & 1u) || at >= give) continue;
+                const int page = 32 * w + lane, i = find_row(S.need_end, a.n, at);
+                const int j = at - (i == 0 ? 0 : S.need_end[i - 1]);
+                a.table_out[i * a.stride + S.held[i] + j - S.copy[i]] = page;
+                if (j == 0 && S.copy[i] && S.own[i] >= 0) {
+                    int32_t* c = a.copies + 3 * S.copy_at[i];
+                    c[0] = S.own[i];
+                    c[1] = page;
+                    c[2] = S.keep[i] % R;
+                }
             }
         }
         if (tid < a.n) {
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
             for (int u = 0; u < 8; ++u) mine = tid == u ? v[u] : mine;
             a.result[tid] = mine;
         }
-        if (tid == 0 && !done) S.total_new = 0;
+        if (tid == 0) S.listed = done ? static_cast<int32_t>(min(S.total_new, int64_t{0x7fffffff})) : 0;
         __threadfence();  // the tables, for the other blocks
     }
     if (!(a.slots || a.position || a.sequence)) {
@@ -262,39 +265,40 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
     if (ranks > 1) cluster_sync();
     else __syncthreads();
     if (rank != 0) {  // the rows' ends from the first block
-        if (tid < a.n) {
-            int64_t v;
-            asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(map_first(smem_u32(&S.new_end[tid]))) : "memory");
-            S.new_end[tid] = v;
-        }
-        if (tid == 0) {
-            int64_t v;
-            asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v) : "r"(map_first(smem_u32(&S.total_new))) : "memory");
-            S.total_new = v;
-        }
+        auto fetch = [](const int32_t* p) {
+            int32_t v;
+            asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(map_first(smem_u32(p))) : "memory");
+            return v;
+        };
+        if (tid < a.n) S.new_end[tid] = fetch(&S.new_end[tid]);
+        if (tid == 0) S.listed = fetch(&S.listed);
     }
     if (ranks > 1) cluster_sync();  // the first block leaves when its memory has been read
     else __syncthreads();
-    const int64_t total = S.total_new;
-    constexpr int kSlots = 4;  // of a thread's turn, their table entries on the way together
-    const int64_t turn = static_cast<int64_t>(ranks) * kTabThreads;
-    for (int64_t j0 = static_cast<int64_t>(rank) * kTabThreads + tid; j0 < a.max_new; j0 += kSlots * turn) {
-        int slot[kSlots], pos[kSlots], seq[kSlots];
+    // A warp takes 32 * kSlots new rows in a row: their sequence is searched for
+    // once and followed from there, their table entries are on the way together.
+    const int total = S.listed;
+    constexpr int kSlots = 4;
+    const int shift = (R & (R - 1)) == 0 ? __ffs(R) - 1 : -1;
+    for (int64_t j0 = (static_cast<int64_t>(rank) * kTabWarps + (tid >> 5)) * 32 * kSlots; j0 < a.max_new;
+         j0 += static_cast<int64_t>(ranks) * kTabThreads * kSlots) {
+        int slot[kSlots], pos[kSlots], seq[kSlots], at = j0 < total ? find_row(S.new_end, a.n, static_cast<int>(j0)) : 0;
 #pragma unroll
         for (int u = 0; u < kSlots; ++u) {
-            const int64_t j = j0 + u * turn;
+            const int64_t j = j0 + 32 * u + lane;
             slot[u] = pos[u] = seq[u] = -1;
             if (j < total) {
-                seq[u] = find_row(S.new_end, a.n, j);
-                pos[u] = S.keep[seq[u]] + static_cast<int>(j - (seq[u] == 0 ? 0 : S.new_end[seq[u] - 1]));
-                slot[u] = __ldcg(a.table_out + seq[u] * a.stride + pos[u] / R);
+                while (S.new_end[at] <= j) ++at;
+                seq[u] = at;
+                pos[u] = S.keep[at] + static_cast<int>(j - (at == 0 ? 0 : S.new_end[at - 1]));
+                slot[u] = __ldcg(a.table_out + at * a.stride + (shift >= 0 ? pos[u] >> shift : pos[u] / R));
             }
         }
 #pragma unroll
         for (int u = 0; u < kSlots; ++u) {
-            const int64_t j = j0 + u * turn;
+            const int64_t j = j0 + 32 * u + lane;
             if (j >= a.max_new) break;
-            if (a.slots) a.slots[j] = seq[u] < 0 ? -1 : slot[u] * R + pos[u] % R;
+            if (a.slots) a.slots[j] = seq[u] < 0 ? -1 : slot[u] * R + (shift >= 0 ? pos[u] & (R - 1) : pos[u] % R);
             if (a.position) a.position[j] = pos[u];
             if (a.sequence) a.sequence[j] = seq[u];
         }
