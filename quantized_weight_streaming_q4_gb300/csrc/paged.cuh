@@ -10,8 +10,11 @@
 //    four tiles, so items of up to four are left whole; longer ones are cut as
 //    far as there are blocks.
 //  - else all items' tiles in a row are cut into as many equal runs as there are
-//    blocks, so that a run may end inside an item.  An item counts as kOver tiles
-//    more than it has: that is what a block spends on its start and its end.
+//    blocks, so that a run may end inside an item.  An item counts as some tiles
+//    more than it has, for what a block spends on its start and its end: two
+//    up to 8 query rows, four for 16 (16 sequences of 500 to 40,000 rows, 16
+//    query rows: 43.5 us with two, 39.8 with four; 48 sequences of 30 to 1,500
+//    rows, four query rows: 25.7 and 26.7).
 // The blocks of an item leave partial results, and the last of them to finish
 // joins these in the items' order (of more than 16, eight at a time first).  No
 // block waits for another.
@@ -82,18 +85,15 @@ struct PagedPlan {
     int32_t t[kMaxSequences];
     uint32_t before[kMaxSequences + 1];
 };
-struct PagedSplit {
-    uint32_t units, chunk;
-    int first_row;  // that the block's first unit is of
-};
 constexpr int kMostChunk = 8, kWholeTiles = 4;
-constexpr uint32_t kOver = 2;
+__device__ __forceinline__ uint32_t over(const PagedArgs& a) { return a.group > 8 ? 4u : 2u; }
 
 __device__ __forceinline__ uint32_t ceil_div(uint32_t x, uint32_t y) { return (x + y - 1) / y; }
 
 // x / y; most calls' numbers fit 32 bits, whose division is a third of the work.
+__device__ __noinline__ uint64_t divide64(uint64_t x, uint64_t y) { return x / y; }
 __device__ __forceinline__ uint64_t divide(uint64_t x, uint64_t y) {
-    if ((x | y) >> 32) return x / y;
+    if ((x | y) >> 32) return divide64(x, y);
     return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
 }
 
@@ -102,6 +102,7 @@ __device__ __forceinline__ uint64_t divide(uint64_t x, uint64_t y) {
 struct PagedShare {
     uint64_t total, at, end;
     uint32_t blocks;
+    PagedShare() = default;
     __device__ __forceinline__ PagedShare(const PagedArgs& a, uint32_t units) : at(0), end(0) {
         total = static_cast<uint64_t>(units) * static_cast<uint32_t>(a.G * a.blocks_per_head);
         blocks = total < gridDim.x ? static_cast<uint32_t>(total) : gridDim.x;
@@ -114,6 +115,12 @@ struct PagedShare {
             end = divide(total * (blockIdx.x + 1), blocks);
         }
     }
+};
+
+struct PagedSplit {
+    PagedShare share;
+    uint32_t chunk;
+    int first_row;  // that the block's first unit is of
 };
 
 // The position of token row i, -1 where it has no work.
@@ -135,7 +142,7 @@ __device__ __forceinline__ uint32_t choose_chunk(const PagedArgs& a, uint32_t su
     if (chunk > 0 && __shfl_sync(0xffffffffu, sum, 0) <= kWholeTiles) chunk = kWholeTiles;
     all = __shfl_sync(0xffffffffu, sum, chunk == 0 ? 1 : chunk);
     const uint32_t rows = __shfl_sync(0xffffffffu, sum, kMostChunk + 1);
-    if (chunk == 0) all += kOver * rows;
+    if (chunk == 0) all += over(a) * rows;
     return chunk;
 }
 
@@ -167,8 +174,9 @@ __device__ __forceinline__ PagedSplit make_plan(const PagedArgs& a, PagedPlan& p
         __syncthreads();
     }
     PagedSplit split;
-    split.chunk = choose_chunk(a, sum, split.units);
-    const uint32_t units = split.chunk == 0 ? (mine > 0 ? mine + kOver : 0) : ceil_div(mine, split.chunk);
+    uint32_t all;
+    split.chunk = choose_chunk(a, sum, all);
+    const uint32_t units = split.chunk == 0 ? (mine > 0 ? mine + over(a) : 0) : ceil_div(mine, split.chunk);
     uint32_t v = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -184,7 +192,7 @@ __device__ __forceinline__ PagedSplit make_plan(const PagedArgs& a, PagedPlan& p
     plan.t[i] = t;
     plan.before[i] = v - units;
     if (one ? lane == 31 : tid == 255) plan.before[i + 1] = v;
-    const PagedShare share(a, split.units);
+    const PagedShare share = split.share = PagedShare(a, all);
     const uint64_t per = static_cast<uint32_t>(a.G * a.blocks_per_head);
     const bool here = (v - units) * per <= share.at && share.at < v * per;
     if (one) {
@@ -211,13 +219,14 @@ struct PagedRun {
 template <int TILE>
 struct PagedWalk {
     PagedShare share;
-    uint32_t chunk;
+    uint32_t chunk, extra;  // extra: units of an item before its first tile
     int m;
     __device__ __forceinline__ PagedWalk(const PagedArgs& a, const PagedSplit& split)
-        : share(a, split.units), chunk(split.chunk), m(split.first_row) {}
+        : share(split.share), chunk(split.chunk), extra(chunk == 0 ? over(a) : 0), m(split.first_row) {}
     // no further run: what is left of the share ends before the next item's first tile
-    // (a share is more than kOver units, so there is a first run)
-    __device__ __forceinline__ bool last() const { return share.at + (chunk == 0 ? kOver : 0) >= share.end; }
+    // (a share is more units than that: more pieces of 8 tiles than blocks make as
+    // many units as pieces times one more, at least)
+    __device__ __forceinline__ bool last() const { return share.at + extra >= share.end; }
     __device__ __forceinline__ bool next(const PagedArgs& a, const PagedPlan& plan, PagedRun& run) {
         if (last()) return false;
         const uint64_t per = static_cast<uint32_t>(a.G * a.blocks_per_head);
@@ -241,9 +250,9 @@ struct PagedWalk {
         }
         if (chunk == 0) {
             const uint32_t x1 = static_cast<uint32_t>(min(static_cast<uint64_t>(units), x + (share.end - share.at)));
-            run.tiles = static_cast<int>(units - kOver);
-            run.a = static_cast<int>(max(x, kOver) - kOver);
-            run.b = static_cast<int>(max(x1, kOver) - kOver);
+            run.tiles = static_cast<int>(units - extra);
+            run.a = static_cast<int>(max(x, extra) - extra);
+            run.b = static_cast<int>(max(x1, extra) - extra);
             share.at += x1 - x;
             return true;
         }
@@ -263,7 +272,7 @@ struct PagedWalk {
         if (share.total == share.blocks) return static_cast<int>(unit);
         return static_cast<int>(divide((unit + 1) * share.blocks - 1, share.total));
     }
-    __device__ __forceinline__ int first_block(const PagedRun& run) const { return owner(run.u0 + (chunk == 0 ? kOver : 0)); }
+    __device__ __forceinline__ int first_block(const PagedRun& run) const { return owner(run.u0 + extra); }
     __device__ __forceinline__ int last_block(const PagedRun& run) const { return owner(run.u0 + run.units - 1); }
 };
 

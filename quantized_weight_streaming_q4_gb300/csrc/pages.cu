@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
 // page of a layer's keys or values, all its loads in flight before the first
 // store; blocks go round, since how many copies there are is known on the
 // device only.
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 128;
 
 template <int N>
 struct PageCopyParams {
