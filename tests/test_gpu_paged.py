@@ -388,6 +388,38 @@ def test_attention_other_streams_and_unaligned_caches():
     Case([300, 2, 90], 32, 2, 128, 64, True, offset=4).to_device().call().check()
 
 
+@pytest.mark.parametrize("hm", [False, True])
+@pytest.mark.parametrize("D", [128, 20])
+def test_offsets_beyond_32_bits(hm, D):
+    """A cache of 2^32 bytes and more: the last pages are written, copied and read."""
+    G, H, R = 2, 8, 64
+    pages = (1 << 32) // (R * G * D * 2) + 9
+    rng = np.random.default_rng(7)
+    n = 150
+    key, value = (torch.empty(pages * R * G * D, dtype=torch.int16, device="cuda") for _ in range(2))
+    handle = mu.KvPages(key.data_ptr(), value.data_ptr(), pages, R, G * D, D, int(hm), 0)
+    table = np.array([[pages - 1, pages - 4, pages - 6]], np.int32)
+    slots = ints([table[0, p // R] * R + p % R for p in range(n)])
+    k, v = (rng.standard_normal((n, G * D)).astype(np.float32) for _ in range(2))
+    mu.muser_kv_page_write(handle, dev(k), dev(v), slots, n)
+    mu.muser_kv_page_copy([handle], ints([[pages - 6, pages - 2, n - 2 * R]]), ints([1]), 1)
+    table[0, 2] = pages - 2
+    q = rng.standard_normal((1, H * D)).astype(np.float32)
+    nk, nv = (rng.standard_normal((1, G * D)).astype(np.float32) for _ in range(2))
+    nb = mu.muser_kv_paged_attention_scratch_bytes(G * D, D, 1, H)
+    out = torch.empty(H * D, device="cuda")
+    mu.muser_kv_paged_attention(handle, ints(table), ints([n]), dev(q), 1, H, out, 0.3, torch.zeros(nb // 4, device="cuda"), nb,
+                                k=dev(nk), v=dev(nv))
+    small = np.zeros((3, R, G, D), np.float16), np.zeros((3, R, G, D), np.float16)
+    for dst, src in zip(small, (k, v)):
+        dst.reshape(-1, G * D)[:n] = src.astype(np.float16)
+    want, _ = paged.paged_attention(small[0], small[1], 3, R, G, D, False, [[0, 1, 2]], [n], q, H, 0.3, nk, nv)
+    assert np.linalg.norm(host(out) - want[0]) <= 1e-5 * np.linalg.norm(want[0])
+    page = value.view(pages, -1)[pages - 2].clone().view(torch.float16).cpu().numpy()
+    row = page.reshape(G, R, D)[:, n % R] if hm else page.reshape(R, G, D)[n % R]
+    assert np.array_equal(row.reshape(-1), nv[0].astype(np.float16))
+
+
 def test_attention_agrees_with_the_ring():
     """One token over one sequence: the tree attention over a plane gives the same to rounding."""
     c = Case([1000], 32, 2, 128, 64, False).to_device()
