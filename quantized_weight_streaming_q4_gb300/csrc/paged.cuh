@@ -90,37 +90,35 @@ __device__ __forceinline__ uint32_t over(const PagedArgs& a) { return a.group > 
 
 __device__ __forceinline__ uint32_t ceil_div(uint32_t x, uint32_t y) { return (x + y - 1) / y; }
 
-// x / y; most calls' numbers fit 32 bits, whose division is a third of the work.
-__device__ __noinline__ uint64_t divide64(uint64_t x, uint64_t y) { return x / y; }
-__device__ __forceinline__ uint64_t divide(uint64_t x, uint64_t y) {
-    if ((x | y) >> 32) return divide64(x, y);
-    return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+// x / y for x < 2^24 and a quotient below 2^20, by way of binary32.
+__device__ __forceinline__ uint32_t quotient(uint32_t x, uint32_t y) {
+    uint32_t q = __float2uint_rz(__fdividef(static_cast<float>(x), static_cast<float>(y)));
+    const int r = static_cast<int>(x - q * y);  // the quotient is one off at most
+    return r < 0 ? q - 1 : r >= static_cast<int>(y) ? q + 1 : q;
 }
 
-// A block's share [at, end) of `total` units; blocks behind the units' number
-// have none.
+// A block's share [at, end) of `total` < 2^24 units; blocks behind the units'
+// number have none.
 struct PagedShare {
-    uint64_t total, at, end;
-    uint32_t blocks;
+    uint32_t total, blocks, at, end;
     PagedShare() = default;
-    __device__ __forceinline__ PagedShare(const PagedArgs& a, uint32_t units) : at(0), end(0) {
-        total = static_cast<uint64_t>(units) * static_cast<uint32_t>(a.G * a.blocks_per_head);
-        blocks = total < gridDim.x ? static_cast<uint32_t>(total) : gridDim.x;
+    __device__ __forceinline__ explicit PagedShare(uint32_t units) : total(units), at(0), end(0) {
+        blocks = min(total, gridDim.x);
         if (blockIdx.x >= blocks) return;
         if (total == blocks) {
             at = blockIdx.x;
             end = at + 1;
         } else {
-            at = divide(total * blockIdx.x, blocks);
-            end = divide(total * (blockIdx.x + 1), blocks);
+            at = total * blockIdx.x / blocks;
+            end = total * (blockIdx.x + 1) / blocks;
         }
     }
 };
 
 struct PagedSplit {
     PagedShare share;
-    uint32_t chunk;
-    int first_row;  // that the block's first unit is of
+    uint32_t chunk, shift;  // shift: a unit is 2^shift tiles (0 unless a call has more than 2^23)
+    int first_row;          // that the block's first unit is of
 };
 
 // The position of token row i, -1 where it has no work.
@@ -133,17 +131,15 @@ __device__ __forceinline__ int position_of(const PagedArgs& a, int i) {
 }
 
 // The chunk for sums of pieces, lane c's those of chunk c (lane 0: the longest
-// row's tiles, lane 9: rows with work); `all` becomes the number of units.
-__device__ __forceinline__ uint32_t choose_chunk(const PagedArgs& a, uint32_t sum, uint32_t& all) {
+// row's tiles), or 0, and what makes 2^23 units at most.
+__device__ __forceinline__ void choose_units(const PagedArgs& a, uint32_t sum, PagedSplit& split) {
     const int lane = threadIdx.x & 31;
-    const bool fits = lane > 0 && lane <= kMostChunk && static_cast<uint64_t>(sum) * static_cast<uint32_t>(a.G * a.blocks_per_head) <= gridDim.x;
-    const uint32_t fit = __ballot_sync(0xffffffffu, fits);
-    uint32_t chunk = fit == 0 ? 0 : __ffs(fit) - 1;
-    if (chunk > 0 && __shfl_sync(0xffffffffu, sum, 0) <= kWholeTiles) chunk = kWholeTiles;
-    all = __shfl_sync(0xffffffffu, sum, chunk == 0 ? 1 : chunk);
-    const uint32_t rows = __shfl_sync(0xffffffffu, sum, kMostChunk + 1);
-    if (chunk == 0) all += over(a) * rows;
-    return chunk;
+    const uint64_t all = static_cast<uint64_t>(sum) * static_cast<uint32_t>(a.G * a.blocks_per_head);
+    const uint32_t fit = __ballot_sync(0xffffffffu, lane > 0 && lane <= kMostChunk && all <= gridDim.x);
+    split.chunk = fit == 0 ? 0 : __ffs(fit) - 1;
+    if (split.chunk > 0 && __shfl_sync(0xffffffffu, sum, 0) <= kWholeTiles) split.chunk = kWholeTiles;
+    const uint32_t high = __shfl_sync(0xffffffffu, static_cast<uint32_t>(all >> 23), 1);
+    split.shift = high == 0 ? 0 : 32 - __clz(high);
 }
 
 // Fills the plan; all of the block's threads (256) call it.  Up to 32 token
@@ -163,38 +159,42 @@ __device__ __forceinline__ PagedSplit make_plan(const PagedArgs& a, PagedPlan& p
         const uint32_t x = __reduce_add_sync(0xffffffffu, ceil_div(mine, c));
         if (lane == static_cast<int>(c)) sum = x;
     }
-    const uint32_t working = __popc(__ballot_sync(0xffffffffu, mine > 0));
-    if (lane == kMostChunk + 1) sum = working;
     if (!one) {
-        if (lane <= kMostChunk + 1) warp_sums[w * 10 + lane] = sum;
+        if (lane <= kMostChunk) warp_sums[w * 10 + lane] = sum;
         __syncthreads();
         sum = 0;
-        if (lane <= kMostChunk + 1)
+        if (lane <= kMostChunk)
             for (int j = 0; j < 8; ++j) sum = lane == 0 ? max(sum, warp_sums[j * 10]) : sum + warp_sums[j * 10 + lane];
         __syncthreads();
     }
     PagedSplit split;
-    uint32_t all;
-    split.chunk = choose_chunk(a, sum, all);
-    const uint32_t units = split.chunk == 0 ? (mine > 0 ? mine + over(a) : 0) : ceil_div(mine, split.chunk);
+    choose_units(a, sum, split);
+    const uint32_t units = mine == 0          ? 0
+                           : split.chunk == 0 ? ((mine + (1u << split.shift) - 1) >> split.shift) + over(a)
+                                              : quotient(mine + split.chunk - 1, split.chunk);
     uint32_t v = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += x;
     }
+    uint32_t all = __shfl_sync(0xffffffffu, v, 31);
     if (!one) {
         if (lane == 31) warp_sums[w] = v;
         __syncthreads();
-        for (int j = 0; j < w; ++j) v += warp_sums[j];
+        all = 0;
+        for (int j = 0; j < 8; ++j) {
+            if (j == w) v += all;
+            all += warp_sums[j];
+        }
     }
     // every warp writes the same where `one`
     plan.t[i] = t;
     plan.before[i] = v - units;
     if (one ? lane == 31 : tid == 255) plan.before[i + 1] = v;
-    const PagedShare share = split.share = PagedShare(a, all);
-    const uint64_t per = static_cast<uint32_t>(a.G * a.blocks_per_head);
-    const bool here = (v - units) * per <= share.at && share.at < v * per;
+    const uint32_t per = static_cast<uint32_t>(a.G * a.blocks_per_head);
+    split.share = PagedShare(all * per);
+    const bool here = (v - units) * per <= split.share.at && split.share.at < v * per;
     if (one) {
         split.first_row = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
         __syncwarp();
@@ -210,8 +210,7 @@ __device__ __forceinline__ PagedSplit make_plan(const PagedArgs& a, PagedPlan& p
 struct PagedRun {
     int row, head, r0;    // token row, K/V head, first of its query heads
     int a, b, tiles;      // tiles [a, b) of `tiles`
-    uint64_t u0;          // the item's first unit, and their number
-    uint32_t units;
+    uint32_t u0, units;   // the item's first unit, and their number
     __device__ __forceinline__ bool whole() const { return a == 0 && b == tiles; }
 };
 
@@ -219,25 +218,28 @@ struct PagedRun {
 template <int TILE>
 struct PagedWalk {
     PagedShare share;
-    uint32_t chunk, extra;  // extra: units of an item before its first tile
+    uint32_t per, chunk, shift, extra;  // per: items of a token row; extra: units of an item before its first tile
     int m;
     __device__ __forceinline__ PagedWalk(const PagedArgs& a, const PagedSplit& split)
-        : share(split.share), chunk(split.chunk), extra(chunk == 0 ? over(a) : 0), m(split.first_row) {}
+        : share(split.share),
+          per(static_cast<uint32_t>(a.G * a.blocks_per_head)),
+          chunk(split.chunk),
+          shift(split.shift),
+          extra(split.chunk == 0 ? over(a) : 0),
+          m(split.first_row) {}
     // no further run: what is left of the share ends before the next item's first tile
     // (a share is more units than that: more pieces of 8 tiles than blocks make as
     // many units as pieces times one more, at least)
     __device__ __forceinline__ bool last() const { return share.at + extra >= share.end; }
     __device__ __forceinline__ bool next(const PagedArgs& a, const PagedPlan& plan, PagedRun& run) {
         if (last()) return false;
-        const uint64_t per = static_cast<uint32_t>(a.G * a.blocks_per_head);
         while (plan.before[m + 1] * per <= share.at) ++m;
-        const uint64_t base = plan.before[m] * per;
         const uint32_t units = plan.before[m + 1] - plan.before[m];  // of an item
-        const uint64_t off = share.at - base;
-        uint32_t sub = static_cast<uint32_t>(off), x = 0;
+        uint32_t sub = share.at - plan.before[m] * per, x = 0;
         if (units > 1) {
-            sub = static_cast<uint32_t>(divide(off, units));
-            x = static_cast<uint32_t>(off - static_cast<uint64_t>(sub) * units);
+            const uint32_t off = sub;
+            sub = quotient(off, units);
+            x = off - sub * units;
         }
         run.row = m;
         run.units = units;
@@ -248,19 +250,18 @@ struct PagedWalk {
             run.head = static_cast<int>(sub) / a.blocks_per_head;
             run.r0 = (static_cast<int>(sub) - run.head * a.blocks_per_head) * kPagedRows;
         }
+        run.tiles = Sight<TILE>(a, plan.t[m]).tiles;
         if (chunk == 0) {
-            const uint32_t x1 = static_cast<uint32_t>(min(static_cast<uint64_t>(units), x + (share.end - share.at)));
-            run.tiles = static_cast<int>(units - extra);
-            run.a = static_cast<int>(max(x, extra) - extra);
-            run.b = static_cast<int>(max(x1, extra) - extra);
+            const uint32_t x1 = min(units, x + (share.end - share.at));
+            run.a = static_cast<int>((max(x, extra) - extra) << shift);
+            run.b = min(run.tiles, static_cast<int>((max(x1, extra) - extra) << shift));
             share.at += x1 - x;
             return true;
         }
-        run.tiles = Sight<TILE>(a, plan.t[m]).tiles;
         run.a = 0;
         run.b = run.tiles;
         if (units > 1) {  // pieces of equal size, the first ones of a tile more
-            const int each = run.tiles / static_cast<int>(units), rest = run.tiles - each * static_cast<int>(units), i = static_cast<int>(x);
+            const int each = static_cast<int>(quotient(run.tiles, units)), rest = run.tiles - each * static_cast<int>(units), i = static_cast<int>(x);
             run.a = i * each + min(i, rest);
             run.b = run.a + each + (i < rest ? 1 : 0);
         }
@@ -268,9 +269,9 @@ struct PagedWalk {
         return true;
     }
     // the first and the last block that have tiles of the run's item
-    __device__ __forceinline__ int owner(uint64_t unit) const {
+    __device__ __forceinline__ int owner(uint32_t unit) const {
         if (share.total == share.blocks) return static_cast<int>(unit);
-        return static_cast<int>(divide((unit + 1) * share.blocks - 1, share.total));
+        return static_cast<int>(((unit + 1) * share.blocks - 1) / share.total);
     }
     __device__ __forceinline__ int first_block(const PagedRun& run) const { return owner(run.u0 + extra); }
     __device__ __forceinline__ int last_block(const PagedRun& run) const { return owner(run.u0 + run.units - 1); }

@@ -420,6 +420,28 @@ def test_offsets_beyond_32_bits(hm, D):
     assert np.array_equal(row.reshape(-1), nv[0].astype(np.float16))
 
 
+def test_attention_of_more_tiles_than_units():
+    """2^24 tiles: the split counts in fours.  All of a sequence's 65,536 table entries name one page, so each of its 64
+    rows is seen 65,536 times and the result is the softmax over 64 rows.  A thread adds up to 32,768 tiles, each
+    addition off by half a step of 2^-24 of the sum at most: 2^-10 of the sums, once for the outputs and once for the
+    weights' total."""
+    rng = np.random.default_rng(11)
+    n, H, G, D, R, entries = 256, 2, 2, 8, 64, 65536
+    key, value = (rng.standard_normal((1, R, G, D)).astype(np.float16) for _ in range(2))
+    dk, dv = dev(key), dev(value)
+    q = rng.standard_normal((n, H * D)).astype(np.float32)
+    out = nan_like((n, H * D), 16)
+    nb = mu.muser_kv_paged_attention_scratch_bytes(G * D, D, n, H)
+    mu.muser_kv_paged_attention(mu.KvPages(dk.data_ptr(), dv.data_ptr(), 1, R, G * D, D, 0, 0), ints(np.zeros((1, entries))),
+                                ints([entries * R - 1] * n), dev(q), n, H, out, 0.3, torch.zeros(nb // 4, device="cuda"), nb,
+                                sequence=ints([0] * n))
+    got = host(out)[:n * H * D].reshape(n, -1)
+    check_canary(out, n * H * D)
+    want, _ = paged.paged_attention(key, value, 1, R, G, D, False, [[0]], [R - 1] * n, q, H, 0.3, sequence=[0] * n)
+    assert np.abs(got - np.stack(want)).max() <= 2 * 2.0 ** -10 * np.abs(value.astype(np.float32)).max()
+    assert mu.muser_device_status() == 0
+
+
 def test_attention_agrees_with_the_ring():
     """One token over one sequence: the tree attention over a plane gives the same to rounding."""
     c = Case([1000], 32, 2, 128, 64, False).to_device()
