@@ -9,6 +9,9 @@
 // largest of beams * parts * n sums, of which only the parts whose largest is
 // among the requests' largest are looked at further.
 //
+// Bound: latency, the logits being 1.9 us (16 beams of 202,048 tokens: 12.5 us:
+// 2.3 until they are there, 1.1 for the sum, 3 for the part's largest, 0.7 for
+// the ticket, 4 for the last block's work; 37 with binary64 sums).
 // Binary64 is slow here and is left to a few operations a row: the sums score + x - log-sum are pairs of binary32 numbers
 // (48 bits), compared as 64-bit keys.
 //

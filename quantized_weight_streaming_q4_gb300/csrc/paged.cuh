@@ -16,7 +16,7 @@
 //    query rows: 43.5 us with two, 39.8 with four; 48 sequences of 30 to 1,500
 //    rows, four query rows: 25.7 and 26.7).
 // The blocks of an item leave partial results, and the last of them to finish
-// joins these in the items' order (of more than 16, eight at a time first).  No
+// joins these in the items' order (of more than 16, in groups first).  No
 // block waits for another.
 #pragma once
 
@@ -292,30 +292,11 @@ template <typename F>
 __device__ __forceinline__ void each_piece(int D, int lane, F&& f) {
     for (int d = 4 * lane; d < D; d += 128) f(d);
 }
-template <bool VEC>
-__device__ __forceinline__ float4 load4(const float* p, int left) {
-    if (VEC) return __ldcg(reinterpret_cast<const float4*>(p));
-    return make_float4(__ldcg(p), left > 1 ? __ldcg(p + 1) : 0.f, left > 2 ? __ldcg(p + 2) : 0.f, left > 3 ? __ldcg(p + 3) : 0.f);
-}
-template <bool VEC>
-__device__ __forceinline__ void store4(float* p, float4 v, int left) {
-    if (VEC) {
-        *reinterpret_cast<float4*>(p) = v;
-        return;
-    }
-    p[0] = v.x;
-    if (left > 1) p[1] = v.y;
-    if (left > 2) p[2] = v.z;
-    if (left > 3) p[3] = v.w;
-}
 __device__ __forceinline__ float4 scaled(float4 v, float f) { return make_float4(v.x * f, v.y * f, v.z * f, v.w * f); }
 __device__ __forceinline__ float4 gated4(float4 v, float4 z) { return make_float4(gated(v.x, z.x), gated(v.y, z.y), gated(v.z, z.z), gated(v.w, z.w)); }
 
-// `count` parts, the first that of block `from` and each of a block `step`
-// further, are joined, into the item's result or (!final) into the first part.
-// A warp (w of W) takes every W-th row, two at a time; its lanes hold the
-// parts' shares.
-constexpr int kJoinMost = 13;
+// Parts that are joined at once; more of them in groups first.
+constexpr int kJoinMost = 16;
 static_assert(kPagedMaxBlocks <= kJoinMost * kJoinMost, "two levels");
 // What a join needs, by value: through a reference to the kernel's parameters
 // every access went to memory, and a join took 15 us.
@@ -327,71 +308,6 @@ struct JoinWork {
     unsigned* ticket;
     int D, live, first, last;  // first, last: the item's blocks
 };
-template <bool VEC>
-__device__ __noinline__ void join_parts(const JoinWork a, int from, int step, int count, int w, int W, bool final) {
-    constexpr int B = 10, U = 2;  // loads in flight of a row, rows
-    const int lane = threadIdx.x & 31, live = a.live;
-    // part i's row j
-    auto place = [&](int i, int j) { return static_cast<int64_t>(part_of(from + i * step, a.first)) * kPagedRows + j; };
-    for (int j0 = w; j0 < live; j0 += U * W) {
-        float2 ml[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            ml[u] = lane < count && j0 + u * W < live ? __ldcg(a.part_ml + place(lane, j0 + u * W)) : make_float2(kNegInf, 0.f);
-        for (int d = 4 * lane; d - 4 * lane < a.D; d += 128) {
-            float4 z[U], o[U];
-            float m[U], l[U], f[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                o[u] = z[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (final && a.gate && d < a.D && j0 + u * W < live) z[u] = load4<VEC>(a.gate + static_cast<int64_t>(j0 + u * W) * a.D + d, a.D - d);
-            }
-            for (int i0 = 0; i0 < count; i0 += B) {
-                float4 v[U][B];
-#pragma unroll
-                for (int i = 0; i < B; ++i)
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        v[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (i0 + i < count && d < a.D && j0 + u * W < live)
-                            v[u][i] = load4<VEC>(a.part_o + place(i0 + i, j0 + u * W) * a.D + d, a.D - d);
-                    }
-                if (i0 == 0) {  // the shares, while the sums are on the way
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        m[u] = ml[u].x;
-#pragma unroll
-                        for (int x = 16; x > 0; x >>= 1) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], x));
-                        const bool empty = ml[u].x == kNegInf && ml[u].y == 0.f;  // no rows there: its sums are not looked at
-                        f[u] = empty ? kNegInf : share(ml[u].x, m[u]);
-                        l[u] = warp_sum(empty ? 0.f : f[u] * ml[u].y);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < B; ++i)
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const float fi = __shfl_sync(0xffffffffu, f[u], i0 + i);
-                        if (i0 + i < count && fi != kNegInf)
-                            o[u] = make_float4(fmaf(fi, v[u][i].x, o[u].x), fmaf(fi, v[u][i].y, o[u].y), fmaf(fi, v[u][i].z, o[u].z), fmaf(fi, v[u][i].w, o[u].w));
-                    }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int j = j0 + u * W;
-                if (d >= a.D || j >= live) continue;
-                if (final) {
-                    const float4 y = scaled(o[u], l[u] == 0.f ? 0.f : __fdividef(1.f, l[u]));
-                    store4<VEC>(a.out + static_cast<int64_t>(j) * a.D + d, a.gate ? gated4(y, z[u]) : y, a.D - d);
-                } else {
-                    store4<VEC>(a.part_o + place(0, j) * a.D + d, o[u], a.D - d);
-                    if (d == 0) a.part_ml[place(0, j)] = make_float2(m[u], l[u]);
-                }
-            }
-        }
-    }
-}
-
 // Whether this was the last of `count` arrivals at a ticket; called by one
 // thread, when all threads that wrote what it announces have passed a barrier
 // with it (the atomic releases what is ordered before it).
@@ -401,29 +317,6 @@ __device__ __forceinline__ bool last_of(unsigned* ticket, int count) {
     return last;
 }
 
-// After the block's part of an item is written: what is left to join, if this
-// is the last block to get there.  Called by `threads` threads (whole warps; tid
-// counts them) that share barrier `id` and have passed a barrier with those that
-// wrote the part; `flag` is in shared memory.  `go`: thread 0 knows that it is
-// written (else the item stays open, and its tickets taken).
-template <bool VEC>
-__device__ __noinline__ void finish_item(const JoinWork a, int tid, int threads, int id, volatile uint32_t* flag, bool go) {
-    const int count = a.last - a.first + 1, w = tid >> 5, W = threads >> 5;
-    int step = 1, parts = count;
-    if (count > kJoinMost) {
-        while (step * step < count) ++step;  // as many groups as parts in each
-        const int from = a.first + (static_cast<int>(blockIdx.x) - a.first) / step * step, size = min(step, a.last - from + 1);
-        if (tid == 0) *flag = go && last_of(a.ticket + part_of(from, a.first), size);
-        named_barrier_sync(id, threads);
-        if (!*flag) return;
-        join_parts<VEC>(a, from, 1, size, w, W, false);
-        parts = (count + step - 1) / step;
-        named_barrier_sync(id, threads);
-    }
-    if (tid == 0) *flag = go && last_of(a.ticket + 2 * kPagedMaxBlocks + a.first, parts);
-    named_barrier_sync(id, threads);
-    if (*flag) join_parts<VEC>(a, a.first, step, parts, w, W, true);
-}
 template <int TILE>
 __device__ __forceinline__ JoinWork join_work(const PagedArgs& a, const PagedWalk<TILE>& walk, const PagedRun& run) {
     const int64_t at = (static_cast<int64_t>(run.row) * a.H + run.head * a.group + run.r0) * a.D;

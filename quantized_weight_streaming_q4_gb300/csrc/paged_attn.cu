@@ -8,6 +8,113 @@
 namespace muser {
 namespace {
 
+// ------------------------------------------------------- joining the parts
+template <bool VEC>
+__device__ __forceinline__ float4 load4(const float* p, int left) {
+    if (VEC) return __ldcg(reinterpret_cast<const float4*>(p));
+    return make_float4(__ldcg(p), left > 1 ? __ldcg(p + 1) : 0.f, left > 2 ? __ldcg(p + 2) : 0.f, left > 3 ? __ldcg(p + 3) : 0.f);
+}
+template <bool VEC>
+__device__ __forceinline__ void store4(float* p, float4 v, int left) {
+    if (VEC) {
+        *reinterpret_cast<float4*>(p) = v;
+        return;
+    }
+    p[0] = v.x;
+    if (left > 1) p[1] = v.y;
+    if (left > 2) p[2] = v.z;
+    if (left > 3) p[3] = v.w;
+}
+// `count` parts, the first that of block `from` and each of a block `step`
+// further, are joined, into the item's result or (!final) into the first part.
+// A warp (w of W) takes every W-th row, two at a time; its lanes hold the
+// parts' shares.
+template <bool VEC>
+__device__ __noinline__ void join_parts(const JoinWork a, int from, int step, int count, int w, int W, bool final) {
+    constexpr int B = 10, U = 2;  // loads in flight of a row, rows
+    const int lane = threadIdx.x & 31, live = a.live;
+    // part i's row j
+    auto place = [&](int i, int j) { return static_cast<int64_t>(part_of(from + i * step, a.first)) * kPagedRows + j; };
+    for (int j0 = w; j0 < live; j0 += U * W) {
+        float2 ml[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            ml[u] = lane < count && j0 + u * W < live ? __ldcg(a.part_ml + place(lane, j0 + u * W)) : make_float2(kNegInf, 0.f);
+        for (int d = 4 * lane; d - 4 * lane < a.D; d += 128) {
+            float4 z[U], o[U];
+            float m[U], l[U], f[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                o[u] = z[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (final && a.gate && d < a.D && j0 + u * W < live) z[u] = load4<VEC>(a.gate + static_cast<int64_t>(j0 + u * W) * a.D + d, a.D - d);
+            }
+            for (int i0 = 0; i0 < count; i0 += B) {
+                float4 v[U][B];
+#pragma unroll
+                for (int i = 0; i < B; ++i)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        v[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (i0 + i < count && d < a.D && j0 + u * W < live)
+                            v[u][i] = load4<VEC>(a.part_o + place(i0 + i, j0 + u * W) * a.D + d, a.D - d);
+                    }
+                if (i0 == 0) {  // the shares, while the sums are on the way
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        m[u] = ml[u].x;
+#pragma unroll
+                        for (int x = 16; x > 0; x >>= 1) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], x));
+                        const bool empty = ml[u].x == kNegInf && ml[u].y == 0.f;  // no rows there: its sums are not looked at
+                        f[u] = empty ? kNegInf : share(ml[u].x, m[u]);
+                        l[u] = warp_sum(empty ? 0.f : f[u] * ml[u].y);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < B; ++i)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const float fi = __shfl_sync(0xffffffffu, f[u], i0 + i);
+                        if (i0 + i < count && fi != kNegInf)
+                            o[u] = make_float4(fmaf(fi, v[u][i].x, o[u].x), fmaf(fi, v[u][i].y, o[u].y), fmaf(fi, v[u][i].z, o[u].z), fmaf(fi, v[u][i].w, o[u].w));
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = j0 + u * W;
+                if (d >= a.D || j >= live) continue;
+                if (final) {
+                    const float4 y = scaled(o[u], l[u] == 0.f ? 0.f : __fdividef(1.f, l[u]));
+                    store4<VEC>(a.out + static_cast<int64_t>(j) * a.D + d, a.gate ? gated4(y, z[u]) : y, a.D - d);
+                } else {
+                    store4<VEC>(a.part_o + place(0, j) * a.D + d, o[u], a.D - d);
+                    if (d == 0) a.part_ml[place(0, j)] = make_float2(m[u], l[u]);
+                }
+            }
+        }
+    }
+}
+
+// After the block's part of an item is written and a barrier passed: what is
+// left to join, if this is the last block to get there.  All of the block's
+// `threads` threads call it; `flag` is in shared memory.
+template <bool VEC>
+__device__ __noinline__ void finish_item(const JoinWork a, int tid, int threads, volatile uint32_t* flag) {
+    const int count = a.last - a.first + 1, w = tid >> 5, W = threads >> 5;
+    int step = 1, parts = count;
+    if (count > kJoinMost) {
+        while (step * step < count) ++step;  // as many groups as parts in each
+        const int from = a.first + (static_cast<int>(blockIdx.x) - a.first) / step * step, size = min(step, a.last - from + 1);
+        if (tid == 0) *flag = last_of(a.ticket + part_of(from, a.first), size);
+        __syncthreads();
+        if (!*flag) return;
+        join_parts<VEC>(a, from, 1, size, w, W, false);
+        parts = (count + step - 1) / step;
+        __syncthreads();
+    }
+    if (tid == 0) *flag = last_of(a.ticket + 2 * kPagedMaxBlocks + a.first, parts);
+    __syncthreads();
+    if (*flag) join_parts<VEC>(a, a.first, step, parts, w, W, true);
+}
 // --------------------------------------------------- any size, CUDA cores
 // As the tree attention's kernel for any head size: 32 rows at a time in shared
 // memory as binary32, a lane scores one row, then owns the output elements d =
@@ -146,8 +253,8 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
         }
         __syncthreads();
         if (run.whole()) continue;
-        if (D % 4 == 0) finish_item<true>(join_work(a, walk, run), tid, kThreads, 1, &flag, true);
-        else finish_item<false>(join_work(a, walk, run), tid, kThreads, 1, &flag, true);
+        if (D % 4 == 0) finish_item<true>(join_work(a, walk, run), tid, kThreads, &flag);
+        else finish_item<false>(join_work(a, walk, run), tid, kThreads, &flag);
         __syncthreads();
     }
 }

@@ -18,7 +18,10 @@ namespace {
 //
 // One cluster: its first block keeps the bits in shared memory, all blocks set
 // them there (reductions over distributed shared memory), and the first one
-// counts and gives pages out; then all blocks write the slots.
+// counts and gives pages out; then all blocks write the slots.  A cluster of
+// one block up to 16,384 entries and 8,192 slots, else of eight.
+// Bound: latency, a dozen dependent steps of about 0.7 us (16 beams of 500 to
+// 8,000 rows, one block: 7.8 us; 48 prompts, 48,000 new rows, eight: 15.5 us).
 constexpr int kTabThreads = 1024, kTabWarps = kTabThreads / 32, kRows = kMaxSequences;
 
 struct TabShared {
@@ -306,7 +309,8 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
 }
 
 // ------------------------------------------------------------------- copy
-// Bound: the rows' bytes, read and written once.  A block takes a part of a
+// Bound: the rows' bytes, read and written once (15 pages of 52 layers, 52 MB:
+// 12.9 us, of which 4 are the launch and the two reads before the data).  A block takes a part of a
 // page of a layer's keys or values, all its loads in flight before the first
 // store; blocks go round, since how many copies there are is known on the
 // device only.
@@ -364,7 +368,8 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ write
-// Bound: 4 bytes read and 2 written an element.  A thread takes 8 elements of a
+// Bound: 4 bytes read and 2 written an element (40,007 rows of 256, 123 MB:
+// 20.3 us, 6.06 TB/s).  A thread takes 8 elements of a
 // row of K and of V (or one, where rows are not 16-byte aligned).
 constexpr int kWriteThreads = 256;
 

@@ -367,6 +367,11 @@ def test_attention_large_and_growing_scores(H, G, D, R):
     c.to_device().call().check(kmax=16.0)
 
 
+@pytest.mark.parametrize("D", [128, 12])
+def test_attention_without_any_work(D):
+    Case([-1, -1, -5], 4, 2, D, 16, False).to_device().call().check()
+
+
 def test_attention_same_positions_same_bits():
     c = Case([5000, 77, 1300, 9000], 32, 2, 128, 64, False).to_device().call()
     first = host(c.out).copy()
