@@ -10,7 +10,7 @@
 namespace muser {
 namespace {
 
-constexpr int64_t kMostRows = int64_t{1} << 30;  // windows and kept first rows beyond it are all rows
+constexpr int64_t kMostRows = int64_t{1} << 30;  // of a table; windows over its rows, and kept first rows, beyond it are all of them
 
 // The checks of a paged cache that every call makes.
 int check_cache(const char* fn, const muser_kv_pages* cache) {
@@ -320,7 +320,7 @@ int muser_kv_paged_attention(const muser_kv_pages* cache, const int32_t* table, 
     a.D = C.head_dim;
     a.G = C.kv_dim / C.head_dim;
     a.group = n_heads / a.G;
-    a.window = clipped(window);
+    a.window = window > 0x7fffffff ? 0 : static_cast<int32_t>(window);  // no position is that far from another
     a.n_sink = clipped(n_sink);
     a.scale_log2 = scale_log2;
     return launch_paged_attention(a, scratch, as_stream(stream));

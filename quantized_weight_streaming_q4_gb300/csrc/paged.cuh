@@ -41,7 +41,7 @@ struct PagedArgs {
     const float *q, *k, *v, *gate;
     float* out;
     int n, H, G, D, group, blocks_per_head;
-    int32_t window, n_sink;
+    int32_t window, n_sink;  // window 0: all rows
     float scale_log2;
     unsigned* ticket;  // [2 * blocks] of eight parts, at the first one's place; [blocks] of an item, at its first block's
     float2* part_ml;   // [2 * blocks][16]: maximum (base 2) and sum
@@ -62,7 +62,7 @@ template <int TILE>
 struct Sight {
     int t, end, low, sink, lead, tail0, tiles;
     __device__ __forceinline__ Sight(const PagedArgs& a, int pos) : t(pos) {
-        end = min(a.k ? pos : pos + 1, a.rows_end);
+        end = a.k ? min(pos, a.rows_end) : min(pos, a.rows_end - 1) + 1;  // pos may be the largest int32
         low = a.window > 0 ? min(max(0, pos - a.window + 1), end) : 0;
         sink = min(a.n_sink, low);
         lead = (sink + TILE - 1) / TILE;
@@ -124,10 +124,8 @@ struct PagedSplit {
 // The position of token row i, -1 where it has no work.
 __device__ __forceinline__ int position_of(const PagedArgs& a, int i) {
     if (i >= a.n) return -1;
-    int t = __ldcg(a.position + i);
-    const int s = a.sequence ? __ldcg(a.sequence + i) : i;
-    if (s < 0 || s >= a.n_tables) t = -1;
-    return min(t, 0x3fffffff);
+    const int t = __ldcg(a.position + i), s = a.sequence ? __ldcg(a.sequence + i) : i;
+    return s >= 0 && s < a.n_tables ? t : -1;
 }
 
 // The chunk for sums of pieces, lane c's those of chunk c (lane 0: the longest

@@ -336,6 +336,18 @@ def test_attention_pages_that_are_not_there(D):
     c.to_device().call().check()
 
 
+@pytest.mark.parametrize("window", [(1 << 30) - 30, 1 << 30, (1 << 30) + 7, (1 << 31) - 40, (1 << 31) - 1, 1 << 31, 1 << 40, 0])
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("D", [128, 12])
+def test_attention_positions_far_behind_the_table(D, own, window):
+    """Up to the largest int32: which of the table's rows the window reaches goes by the position itself."""
+    far = [64, (1 << 30) - 31, (1 << 30) - 2, (1 << 30) - 1, 1 << 30, (1 << 30) + 20, (1 << 31) - 41, (1 << 31) - 2, (1 << 31) - 1]
+    c = Case([64] * len(far), 4, 2, D, 16, False, window, 5 if window else 0, own=own)
+    c.table = np.ascontiguousarray(c.table[:, :4])  # 64 rows
+    c.position = np.array(far, np.int32)
+    c.to_device().call().check()
+
+
 @pytest.mark.parametrize("D", [128, 12])
 @pytest.mark.parametrize("what", [0x7C00, 0xFC00, 0x7E00])
 def test_attention_rows_that_are_seen_and_not_finite(D, what):
