@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     Cand* const cand = static_cast<Cand*>(a.cand);
     pdl_launch_dependents();
     pdl_wait();
-    const bool ended = a.ended && __ldg(a.ended + row) != 0;
+    const bool ended = a.ended && __ldcg(a.ended + row) != 0;
     Cand* const mine = cand + (static_cast<int64_t>(row) * a.parts + part) * a.n;
     const int v0 = static_cast<int>(static_cast<int64_t>(a.vocab) * part / a.parts);
     const int len = static_cast<int>(static_cast<int64_t>(a.vocab) * (part + 1) / a.parts) - v0;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     __syncthreads();
     if (tid < a.beams) {
         const int r = g * a.beams + tid;
-        const bool end = a.ended && __ldg(a.ended + r) != 0;
+        const bool end = a.ended && __ldcg(a.ended + r) != 0;
         // ln(total 2^(e - 40)): the leading bit's place, and the logarithm of what follows it
         const uint64_t t = S.total[tid];
         const int place = 63 - __clzll(static_cast<long long>(t | 1));

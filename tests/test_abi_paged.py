@@ -141,3 +141,14 @@ def test_select_scratch(L):
     assert mu.muser_beam_select_scratch_bytes(1, 16, 202048, 16) > 1024
     for bad in ((0, 1, 10, 1), (1, 33, 10, 1), (1, 1, 10, 11), (1, 1, 1 << 21, 1), (300, 1, 10, 1), (1, 2, 100, 65)):
         assert mu.muser_beam_select_scratch_bytes(*bad) == 0
+
+
+@pytest.mark.parametrize("name", ["beam.cu", "paged_tc.cu", "paged.cuh", "pages.cuh"])
+def test_programmatically_launched_kernels_load_nothing_on_the_read_only_path(name):
+    """What the kernel before wrote, or what this one writes in place, is loaded past the read-only path: such a load may
+    move above the wait for the kernel before, or meet an old line of an SM's cache."""
+    from quantized_weight_streaming_q4_gb300 import buildlib
+    with open(os.path.join(buildlib.CSRC, name)) as f:
+        text = f.read()
+    for load in ("ldg(", "ldg_", "global.nc"):
+        assert load not in text, (name, load)

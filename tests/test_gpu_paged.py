@@ -591,6 +591,40 @@ def test_select_first_step():
     run_select(x, np.zeros(6, np.float32), 1, 6, 12)  # equal rows: every token six times, by beam
 
 
+@pytest.mark.parametrize("groups,beams,V", [(1, 16, 202048), (4, 4, 3000), (16, 1, 500)])
+def test_select_steps_in_place(groups, beams, V):
+    """Steps one behind the other on one stream: scores and flags in place, so that each reads what the one before wrote;
+    no other kernel between them.  Scores of untied logits differ by more than the steps' errors together."""
+    steps, n, end = 6, groups * beams, 5
+    rng = np.random.default_rng(V)
+    x = (2.0 * rng.standard_normal((steps, n, V))).astype(np.float32)
+    for s in range(steps):  # beams end in the first steps, one after another
+        x[s, rng.choice(n, max(1, n // 5), replace=False), end] = 30.0
+    dx = [dev(y) for y in x]
+    nb = mu.muser_beam_select_scratch_bytes(groups, beams, V, beams)
+    scratch = torch.zeros(nb // 4, device="cuda")
+    first = (-3.0 * rng.random(n)).astype(np.float32)
+    want, score, ended = [], first.astype(np.float64), np.zeros(n, np.int32)
+    for s in range(steps):
+        p, t, score, e = paged.beam_select(x[s], score, groups, beams, beams, ended, end)
+        ended = e.astype(np.int32)
+        want.append((p, t, score, ended))
+    assert 0 < want[0][3].sum() < want[-1][3].sum()
+    for _ in range(20):
+        dscore, dended = dev(first), ints([0] * n)
+        o = [[torch.full((n,), -7, dtype=torch.int32, device="cuda") for _ in range(3)] for _ in range(steps)]
+        torch.cuda.synchronize()
+        for s in range(steps):
+            mu.muser_beam_select(dx[s], dscore, groups, beams, V, beams, o[s][0], o[s][1], dscore, scratch, nb, ended=dended,
+                                 end_token=end, ended_out=dended, add=o[s][2])
+        for s in range(steps):
+            assert list(host(o[s][0])) == list(want[s][0]) and list(host(o[s][1])) == list(want[s][1]), s
+            assert list(host(o[s][2])) == [1 - y for y in want[s][3]], s
+        assert list(host(dended)) == list(want[-1][3])
+        # a step adds a rounding of the score and the log-sum's error
+        assert (np.abs(host(dscore) - want[-1][2]) <= steps * (2.0 ** -24 * np.abs(want[-1][2]) + 2.0 ** -22)).all()
+
+
 # ------------------------------------------------------------------ together
 class Search:
     """A beam search over a made-up one-layer model: q, k, v of a token and its position from tables, logits from the
