@@ -123,11 +123,11 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
     // the rows, in every block for itself
     int tasks = 0;
     if (tid < a.n) {
-        int p = a.parent ? __ldg(a.parent + tid) : tid;
+        int p = a.parent ? __ldcg(a.parent + tid) : tid;
         if (p < 0 || p >= a.n_old) p = -1;
         const int64_t most = a.stride * R;
         const int old = p < 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(max(0, __ldcg(a.length + p))), most));
-        const int64_t now = max(int64_t{0}, static_cast<int64_t>(old) + (a.add ? __ldg(a.add + tid) : 1));
+        const int64_t now = max(int64_t{0}, static_cast<int64_t>(old) + (a.add ? __ldcg(a.add + tid) : 1));
         const int keep = static_cast<int>(min(static_cast<int64_t>(old), now));
         if (now > most) S.status = 2;
         S.parent[tid] = p;
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kWriteThreads) page_write_kernel(const __grid_
          i += static_cast<int64_t>(gridDim.x) * kWriteThreads) {
         const int64_t j = i / per, src = i * kStep;
         const int e = static_cast<int>(i - j * per) * kStep;
-        const int64_t slot = __ldg(a.slots + j);
+        const int64_t slot = __ldcg(a.slots + j);
         if (slot < 0 || slot >= a.slot_end) continue;
         int64_t dst = slot * a.kv_dim + e;
         if (a.head_major) {
@@ -394,8 +394,8 @@ __global__ void __launch_bounds__(kWriteThreads) page_write_kernel(const __grid_
             dst = ((page * heads + head) * a.page_rows + (slot - page * a.page_rows)) * a.head_dim + (e - head * a.head_dim);
         }
         if (VEC) {
-            const float4 k0 = __ldg(reinterpret_cast<const float4*>(a.k + src)), k1 = __ldg(reinterpret_cast<const float4*>(a.k + src + 4));
-            const float4 v0 = __ldg(reinterpret_cast<const float4*>(a.v + src)), v1 = __ldg(reinterpret_cast<const float4*>(a.v + src + 4));
+            const float4 k0 = __ldcg(reinterpret_cast<const float4*>(a.k + src)), k1 = __ldcg(reinterpret_cast<const float4*>(a.k + src + 4));
+            const float4 v0 = __ldcg(reinterpret_cast<const float4*>(a.v + src)), v1 = __ldcg(reinterpret_cast<const float4*>(a.v + src + 4));
             const auto pack = [](float lo, float hi) {
                 const __half2 h = __floats2half2_rn(lo, hi);
                 return *reinterpret_cast<const uint32_t*>(&h);
@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(kWriteThreads) page_write_kernel(const __grid_
             *reinterpret_cast<uint4*>(a.key + dst) = make_uint4(pack(k0.x, k0.y), pack(k0.z, k0.w), pack(k1.x, k1.y), pack(k1.z, k1.w));
             *reinterpret_cast<uint4*>(a.value + dst) = make_uint4(pack(v0.x, v0.y), pack(v0.z, v0.w), pack(v1.x, v1.y), pack(v1.z, v1.w));
         } else {
-            a.key[dst] = __half_as_ushort(__float2half_rn(__ldg(a.k + src)));
-            a.value[dst] = __half_as_ushort(__float2half_rn(__ldg(a.v + src)));
+            a.key[dst] = __half_as_ushort(__float2half_rn(__ldcg(a.k + src)));
+            a.value[dst] = __half_as_ushort(__float2half_rn(__ldcg(a.v + src)));
         }
     }
 }
