@@ -152,14 +152,14 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
         const float* kt = a.k + static_cast<int64_t>(run.row) * a.G * D + run.head * D;
         const float* vt = a.v + static_cast<int64_t>(run.row) * a.G * D + run.head * D;
         const bool self = a.k && run.b == run.tiles;
-        for (int x = tid; x < kPagedRows * D; x += kThreads) qs[x] = x / D < live ? __ldg(a.q + row0 * D + x) : 0.f;
+        for (int x = tid; x < kPagedRows * D; x += kThreads) qs[x] = x / D < live ? __ldcg(a.q + row0 * D + x) : 0.f;
         if (self && run.r0 == 0 && sight.t < a.rows_end) {  // the new row, where the cache keeps it
             const int page = __ldcg(table + sight.t / a.page_rows), r = sight.t % a.page_rows;
             if (page >= 0 && page < a.pages) {
                 const int64_t at = page * a.page_stride + run.head * a.head_stride + r * a.row_stride;
                 for (int d = tid; d < D; d += kThreads) {
-                    a.key[at + d] = __half_as_ushort(__float2half_rn(__ldg(kt + d)));
-                    a.value[at + d] = __half_as_ushort(__float2half_rn(__ldg(vt + d)));
+                    a.key[at + d] = __half_as_ushort(__float2half_rn(__ldcg(kt + d)));
+                    a.value[at + d] = __half_as_ushort(__float2half_rn(__ldcg(vt + d)));
                 }
             }
         }
@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
                 const int r = x / D, d = x - r * D;
                 float k = 0.f, v = 0.f;
                 if (own) {
-                    k = __half2float(__float2half_rn(__ldg(kt + d)));
-                    v = __half2float(__float2half_rn(__ldg(vt + d)));
+                    k = __half2float(__float2half_rn(__ldcg(kt + d)));
+                    v = __half2float(__float2half_rn(__ldcg(vt + d)));
                 } else if (slot[r] >= 0) {
                     const int64_t at = (slot[r] / a.page_rows) * a.page_stride + run.head * a.head_stride +
                                        (slot[r] % a.page_rows) * a.row_stride + d;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(const __grid_co
                 const int d = lane + 32 * e;
                 if (d >= D) break;
                 if (!run.whole()) a.part_o[part * D + d] = o[u][e];
-                else a.out[(row0 + r) * D + d] = a.gate ? gated(o[u][e] * inv, __ldg(a.gate + (row0 + r) * D + d)) : o[u][e] * inv;
+                else a.out[(row0 + r) * D + d] = a.gate ? gated(o[u][e] * inv, __ldcg(a.gate + (row0 + r) * D + d)) : o[u][e] * inv;
             }
         }
         __syncthreads();

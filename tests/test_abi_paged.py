@@ -143,7 +143,7 @@ def test_select_scratch(L):
         assert mu.muser_beam_select_scratch_bytes(*bad) == 0
 
 
-@pytest.mark.parametrize("name", ["beam.cu", "paged_tc.cu", "paged.cuh", "pages.cuh", "pages.cu"])
+@pytest.mark.parametrize("name", ["beam.cu", "paged_attn.cu", "paged_tc.cu", "paged.cuh", "pages.cu", "pages.cuh"])
 def test_programmatically_launched_kernels_load_nothing_on_the_read_only_path(name):
     """What the kernel before wrote, or what this one writes in place, is loaded past the read-only path: such a load may
     move above the wait for the kernel before, or meet an old line of an SM's cache."""
