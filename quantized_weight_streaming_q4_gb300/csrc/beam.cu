@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     }
     __syncthreads();
     if (!S.last) return;
-    // the parts' largest, on the way while the rows' sums are made
+    // the parts' largest, flags and scores, on the way while the rows' sums are made
     const int lists = a.beams * a.parts;
     const Cand* all = cand + static_cast<int64_t>(g) * lists * a.n;
     float head[kHeads];
@@ -273,6 +273,9 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
         const int l = tid + i * kThreads;
         head[i] = l < lists ? __ldcg(&all[l * a.n].x) : kNegInf;
     }
+    const int r = g * a.beams + tid;  // a beam a thread
+    const bool end = tid < a.beams && a.ended && __ldcg(a.ended + r) != 0;
+    const float score = tid < a.beams ? __ldcg(a.score + r) : 0.f;
     if (tid == 0) S.opened = 0;
     for (int b = warp; b < a.beams; b += kThreads / 32) {
         const Stat* st = stat + (g * a.beams + b) * a.parts;
@@ -307,13 +310,11 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     }
     __syncthreads();
     if (tid < a.beams) {
-        const int r = g * a.beams + tid;
-        const bool end = a.ended && __ldcg(a.ended + r) != 0;
         // ln(total 2^(e - 40)): the leading bit's place, and the logarithm of what follows it
         const uint64_t t = S.total[tid];
         const int place = 63 - __clzll(static_cast<long long>(t | 1));
         const float fraction = log2f(static_cast<float>(t << (63 - place)) * 0x1p-63f);
-        double sum = __ldcg(a.score + r);
+        double sum = score;
         if (!end) sum -= (static_cast<double>(S.e[tid] + static_cast<float>(place - 40)) + fraction) * 0.693147180559945309417;
         if (!end && t == 0) sum = NAN;
         const float hi = static_cast<float>(sum);
