@@ -9,7 +9,7 @@
 // largest of beams * parts * n sums, of which only the parts whose largest is
 // among the requests' largest are looked at further.
 //
-// Bound: latency, the logits being 1.9 us (16 beams of 202,048 tokens: 12.5 us:
+// Bound: latency, the logits being 1.9 us (16 beams of 202,048 tokens: 12.3 us:
 // 2.3 until they are there, 1.1 for the sum, 3 for the part's largest, 0.7 for
 // the ticket, 4 for the last block's work; 37 with binary64 sums).
 // Binary64 is slow here and is left to a few operations a row: the sums score + x - log-sum are pairs of binary32 numbers
@@ -18,8 +18,13 @@
 // The n largest of many values: the values are dealt to 64 groups; the n-th
 // largest of the groups' maxima is at most the n-th largest value, and few
 // values are above it (of 10,000 random ones about 20 for n = 16).  These go to
-// a list, where each counts how many come before it.  Where the list would not
-// take them (thousands of equal logits), the values are taken one by one.
+// a list, where each counts how many come before it.  The last block's groups
+// are of the parts' largest alone, dealt so that every group has some of them.
+// Where these are fewer than n, the beams' scores far apart, or some groups
+// empty (less than 2,048 logits), many values are above: what the list took of
+// them is dealt to the groups again, for a closer bound.  Where the list would not
+// take them even so (thousands of equal logits), the values are taken one by
+// one, n times over (16 beams of 202,048 equal logits: 203 us; untied ones 12.3).
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -30,7 +35,10 @@ namespace {
 
 constexpr int kThreads = 512, kVec = 8, kPerThread = 4 * kVec;
 constexpr int kMost = kThreads * kPerThread - 4;  // logits of a part; up to 3 elements before it share its first 16 bytes
-constexpr int kGroups = 64, kGroupLanes = kThreads / kGroups, kList = 1024;
+constexpr int kGroups = 64, kGroupLanes = kThreads / kGroups, kList = 2048;
+// Entries that are ranked as they are; n = 64 leaves about 270 of random values.
+// The ranking is quadratic: a call of 1,500 logits, n = 64, is 24 us narrowed, 262 with all of them ranked.
+constexpr int kShort = 512;
 constexpr float kNegInf = -INFINITY;
 // log2(e) to 48 bits
 constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746887e-8f;
@@ -102,24 +110,59 @@ __device__ __forceinline__ K floor_of(Pick<K>& S, int n, K top) {
     return S.floor;
 }
 
-// The n largest keys (ties: the lower `at`), none of which is below `least`,
-// among what all threads hold: each calls each(f), which calls f(key, at) for
-// its values, key 0 for none.  put(rank, key, at) is called for rank
-// 0..found-1, in some order; returns found.
-template <typename K, typename Each, typename Put>
-__device__ __forceinline__ int largest(Pick<K>& S, int n, K least, Each&& each, Put&& put) {
-    const int tid = threadIdx.x;
+template <typename K>
+__device__ __forceinline__ void append(Pick<K>& S, K k, int at) {
+    const int i = atomicAdd(&S.count, 1);
+    if (i < kList) {
+        S.list_key[i] = k;
+        S.list_at[i] = at;
+    }
+}
+
+// Puts the keys that are not below `least` on the list, as far as it takes
+// them, and returns their number: each thread calls each(f), which calls
+// f(key, at) for its values, key 0 for none.
+template <typename K, typename Each>
+__device__ __forceinline__ int collect(Pick<K>& S, K least, Each&& each) {
     each([&](K k, int at) {
-        if (k != 0 && k >= least) {
-            const int i = atomicAdd(&S.count, 1);
-            if (i < kList) {
-                S.list_key[i] = k;
-                S.list_at[i] = at;
-            }
-        }
+        if (k != 0 && k >= least) append(S, k, at);
     });
     __syncthreads();
-    const int count = S.count;
+    return S.count;
+}
+
+// A list of more than kShort entries is cut down to those that are not below
+// the bound that its own entries give; of a list that did not take all `count`
+// of them this is only the bound, and the list is empty.
+template <typename K>
+__device__ __noinline__ int narrow(Pick<K>& S, int n, int count, K& least) {
+    constexpr int kEach = kList / kThreads;
+    const int tid = threadIdx.x;
+    K k[kEach], top = 0;
+    int at[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int i = tid + u * kThreads;
+        k[u] = i < count ? S.list_key[i] : 0;
+        at[u] = i < count ? S.list_at[i] : 0;
+        top = k[u] > top ? k[u] : top;
+    }
+    __syncthreads();  // the count and the list have been read
+    least = floor_of(S, n, top);
+    if (count > kList) return count;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u)
+        if (k[u] != 0 && k[u] >= least) append(S, k[u], at[u]);
+    __syncthreads();
+    return S.count;
+}
+
+// The n largest keys (ties: the lower `at`) among what all threads hold, of
+// which collect() found `count`.  put(rank, key, at) is called for rank
+// 0..found-1, in some order; returns found.
+template <typename K, typename Each, typename Put>
+__device__ __forceinline__ int largest(Pick<K>& S, int n, int count, Each&& each, Put&& put) {
+    const int tid = threadIdx.x;
     if (count <= kList) {
         for (int i = tid / 8; i < (count + 3) / 4 * 4; i += kThreads / 8) {  // eight lanes a value; whole warps
             const K k = i < count ? S.list_key[i] : 0;
@@ -244,15 +287,19 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
             for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
             if (lane == 0) stat[row * a.parts + part] = Stat{bad ? NAN : e, 0.f, total};
         }
-        const int found = largest(
-            S.part, a.n, least,
-            [&](auto&& f) {
-                if (key_of(top) < least) return;  // most threads have none
+        const auto each = [&](auto&& f) {
+            if (key_of(top) < least) return;  // most threads have none
 #pragma unroll
-                for (int u = 0; u < kPerThread; ++u)
-                    f(x[u] == kNegInf ? 0u : key_of(x[u]), 4 * (tid + u / 4 * kThreads) - off + u % 4);
-            },
-            [&](int rank, uint32_t k, int at) { mine[rank] = Cand{from_key(k), v0 + at}; });
+            for (int u = 0; u < kPerThread; ++u)
+                f(x[u] == kNegInf ? 0u : key_of(x[u]), 4 * (tid + u / 4 * kThreads) - off + u % 4);
+        };
+        int count = collect(S.part, least, each);
+        if (count > kShort && count <= kList) {
+            uint32_t closer;
+            count = narrow(S.part, a.n, count, closer);
+        }
+        const int found = largest(S.part, a.n, count, each,
+                                  [&](int rank, uint32_t k, int at) { mine[rank] = Cand{from_key(k), v0 + at}; });
         if (tid >= found && tid < a.n) mine[tid] = Cand{kNegInf, 0};
     }
     // the request's last block goes on
@@ -268,9 +315,10 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     const int lists = a.beams * a.parts;
     const Cand* all = cand + static_cast<int64_t>(g) * lists * a.n;
     float head[kHeads];
+    const int l0 = (threadIdx.x * kGroups | threadIdx.x / kGroupLanes) % kThreads;  // neighbours go to different groups
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-        const int l = tid + i * kThreads;
+        const int l = l0 + i * kThreads;
         head[i] = l < lists ? __ldcg(&all[l * a.n].x) : kNegInf;
     }
     const int r = g * a.beams + tid;  // a beam a thread
@@ -325,24 +373,36 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const __grid_c
     uint64_t key[kHeads], top = 0;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-        key[i] = head[i] == kNegInf ? 0 : sum_key(S.base[(tid + i * kThreads) / a.parts], head[i]);
+        key[i] = head[i] == kNegInf ? 0 : sum_key(S.base[(l0 + i * kThreads) / a.parts], head[i]);
         top = key[i] > top ? key[i] : top;
     }
     const uint64_t least = floor_of(S.all, a.n, top);
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
-        if (key[i] != 0 && key[i] >= least) S.open[atomicAdd(&S.opened, 1)] = static_cast<uint16_t>(tid + i * kThreads);
+        if (key[i] != 0 && key[i] >= least) S.open[atomicAdd(&S.opened, 1)] = static_cast<uint16_t>(l0 + i * kThreads);
     __syncthreads();
-    const int total = S.opened * a.n, out = g * a.n;
+    const int out = g * a.n;
+    const unsigned opened = S.opened, total = opened * a.n;
+    // part by part, or, of many, the parts' largest first, then their second largest, ...
+    const bool many = total > kShort;
+    const unsigned inner = many ? opened : a.n;
+    const auto each = [&](auto&& f) {
+        for (unsigned e = tid; e < total; e += kThreads) {
+            const unsigned y = e / inner, z = e - y * inner;
+            const int l = S.open[many ? z : y], b = l / a.parts;
+            const float2 c = __ldcg(reinterpret_cast<const float2*>(all + l * a.n + (many ? y : z)));
+            f(c.x == kNegInf ? 0 : sum_key(S.base[b], c.x), b * a.vocab + __float_as_int(c.y));
+        }
+    };
+    int count = collect(S.all, least, each);
+    for (int round = 0; count > kShort && round < 2; ++round) {
+        uint64_t closer;
+        const int all_of_them = count;
+        count = narrow(S.all, a.n, count, closer);
+        if (all_of_them > kList) count = collect(S.all, closer, each);
+    }
     const int found = largest(
-        S.all, a.n, least,
-        [&](auto&& f) {
-            for (int e = tid; e < total; e += kThreads) {
-                const int i = e / a.n, l = S.open[i], b = l / a.parts;
-                const float2 c = __ldcg(reinterpret_cast<const float2*>(all + l * a.n + e - i * a.n));
-                f(c.x == kNegInf ? 0 : sum_key(S.base[b], c.x), b * a.vocab + __float_as_int(c.y));
-            }
-        },
+        S.all, a.n, count, each,
         [&](int rank, uint64_t k, int at) {
             const int b = at / a.vocab, v = at - b * a.vocab;
             const bool end = S.ended[b] || v == a.end_token;

@@ -541,6 +541,42 @@ def test_select_equal_logits(V, n):
     run_select(x, np.array([-3.0, -3.0], np.float32), 1, 2, min(n, V))
 
 
+@pytest.mark.parametrize("groups,beams,n,V", [(1, 1, 16, 202048), (1, 16, 32, 20000), (1, 32, 64, 50000), (1, 32, 64, 2000),
+                                              (1, 1, 64, 1500), (1, 3, 64, 1100), (2, 16, 16, 16000), (2, 1, 64, 2047)])
+@pytest.mark.parametrize("spread", [0.0, 2.0, 50.0])
+def test_select_few_parts_and_far_scores(groups, beams, n, V, spread):
+    """Fewer parts than what bounds the n largest has groups, parts with empty groups, and beams of which some have no
+    part in the result."""
+    rng = np.random.default_rng(V + n)
+    x = (2.0 * rng.standard_normal((groups * beams, V))).astype(np.float32)
+    run_select(x, (-20.0 - spread * rng.random(groups * beams)).astype(np.float32), groups, beams, n)
+
+
+@pytest.mark.parametrize("beams,n,V", [(16, 32, 20000), (32, 64, 50000), (32, 64, 2000), (1, 64, 1500)])
+def test_select_of_untied_logits_takes_no_turns(beams, n, V):
+    """The n largest of untied logits are not taken one by one, which costs 15 to 90 times what the largest one does (the
+    list: 1.3 to 7 times)."""
+    rng = np.random.default_rng(V)
+    x, score = dev((2.0 * rng.standard_normal((beams, V))).astype(np.float32)), dev(-20.0 - rng.random(beams).astype(np.float32))
+    time = {}
+    for m in (1, n):
+        nb = mu.muser_beam_select_scratch_bytes(1, beams, V, m)
+        scratch, so = torch.zeros(nb // 4, device="cuda"), torch.zeros(m, device="cuda")
+        o = [torch.zeros(m, dtype=torch.int32, device="cuda") for _ in range(2)]
+        times = []
+        for _ in range(10):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            torch.cuda.synchronize()
+            e[0].record()
+            for _ in range(20):
+                mu.muser_beam_select(x, score, 1, beams, V, m, *o, so, scratch, nb)
+            e[1].record()
+            torch.cuda.synchronize()
+            times.append(e[0].elapsed_time(e[1]))
+        time[m] = min(times)
+    assert time[n] < 10 * time[1]
+
+
 def test_select_rows_that_are_not_finite():
     rng = np.random.default_rng(0)
     x = rng.standard_normal((8, 3000)).astype(np.float32)
