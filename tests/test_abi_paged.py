@@ -152,3 +152,45 @@ def test_programmatically_launched_kernels_load_nothing_on_the_read_only_path(na
         text = f.read()
     for load in ("ldg(", "ldg_", "global.nc"):
         assert load not in text, (name, load)
+
+
+def _tables_call(table, out, **kw):
+    z = 1 << 30  # never read: pages is 0, which the library refuses
+    mu.muser_kv_page_tables(table, z, 4, 0, 16, out, z + 4096, z + 8192, stream=0, **kw)
+
+
+def _attend_call(table, **kw):
+    z = 1 << 30
+    mu.muser_kv_paged_attention(cache(pages=0), table, z, z, 4, 32, z, 0.1, z, 0, stream=0, **kw)
+
+
+def test_binding_refuses_tables_that_are_not_rows_of_int32(L):
+    """A table's sizes come from its tensor, whose rows the library takes to lie one behind the other: a part of a wider
+    tensor, a tensor of another type or of other dimensions would be read as something else, an expanded one beyond its
+    end."""
+    torch = pytest.importorskip("torch")
+    good = torch.zeros(4, 8, dtype=torch.int32)
+    wide = torch.zeros(4, 10, dtype=torch.int32)
+    bad = [wide[:, :8], wide.t(), torch.zeros(1, 8, dtype=torch.int32).expand(4, 8), torch.zeros(4, 8, dtype=torch.int64),
+           torch.zeros(4, 8, dtype=torch.int16), torch.zeros(4, 8), torch.zeros(32, dtype=torch.int32),
+           torch.zeros(1, 4, 8, dtype=torch.int32)]
+    for t in bad:
+        for kw in ({}, dict(n_old=4), dict(width=8)):
+            with pytest.raises(ValueError, match="table"):
+                _tables_call(t, good, **kw)
+        for kw in ({}, dict(n_tables=4), dict(width=8)):
+            with pytest.raises(ValueError, match="table"):
+                _attend_call(t, **kw)
+    # the new tables have as many entries a row
+    for t in (wide[:, :8], torch.zeros(4, 7, dtype=torch.int32), torch.zeros(3, 8, dtype=torch.int32),
+              torch.zeros(4, 8, dtype=torch.int64), torch.zeros(4, 8)):
+        with pytest.raises(ValueError, match="table_out"):
+            _tables_call(good, t)
+    # what goes through to the library: tables as they should be, buffers of any form whose sizes are given, addresses
+    for call in (lambda: _tables_call(good, torch.zeros_like(good)), lambda: _tables_call(good, torch.zeros(9, 8, dtype=torch.int32)),
+                 lambda: _tables_call(good, torch.zeros(32, dtype=torch.int32)), lambda: _tables_call(good, 1 << 29),
+                 lambda: _tables_call(good.view(-1), torch.zeros_like(good), n_old=4, width=8),
+                 lambda: _tables_call(1 << 29, 1 << 28, n_old=4, width=8),
+                 lambda: _attend_call(good), lambda: _attend_call(wide[:, :8], n_tables=4, width=10), lambda: _attend_call(1 << 29, n_tables=4, width=8)):
+        with pytest.raises(mu.MuserError, match="pages and page_rows must be positive"):
+            call()
