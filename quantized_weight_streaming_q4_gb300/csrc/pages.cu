@@ -19,7 +19,8 @@ namespace {
 // One cluster: its first block keeps the bits in shared memory, all blocks set
 // them there (reductions over distributed shared memory), and the first one
 // counts and gives pages out; then all blocks write the slots.  A cluster of
-// one block up to 16,384 entries and 8,192 slots, else of sixteen.
+// one block up to 16,384 entries and 8,192 slots, else of sixteen (or what the
+// device can place).
 // Bound: latency, a dozen dependent steps of about 0.7 us (16 beams of 500 to
 // 8,000 rows, one block: 7.6 us; 48 prompts, 48,000 new rows: 13.9 us with
 // sixteen, 15.5 with eight).
@@ -410,20 +411,40 @@ __global__ void __launch_bounds__(kWriteThreads) page_write_kernel(const __grid_
 }
 
 struct Ready {
-    int smem;
+    int cluster;  // the most blocks that the device can place together
 };
 
 }  // namespace
 
 int launch_page_tables(const PageTableArgs& a, cudaStream_t s) {
     const Ready* r = device_once<0, Ready>([](Ready& x) {
-        x.smem = static_cast<int>(kMaxPages / 8);
-        cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, x.smem);
+        constexpr int kSmem = static_cast<int>(kMaxPages / 8);
+        cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        return e == cudaSuccess ? static_cast<int>(MUSER_OK) : cuda_fail(e, "page tables: cudaFuncSetAttribute");
+        if (e != cudaSuccess) return cuda_fail(e, "page tables: cudaFuncSetAttribute");
+        x.cluster = largest_cluster([](int size) {
+            cudaLaunchConfig_t cfg{};
+            cudaLaunchAttribute attr[1];
+            cfg.gridDim = dim3(static_cast<unsigned>(size));
+            cfg.blockDim = dim3(kTabThreads);
+            cfg.dynamicSmemBytes = kSmem;
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int clusters = 0;
+            if (cudaOccupancyMaxActiveClusters(&clusters, page_tables_kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                return false;
+            }
+            return clusters > 0;
+        });
+        return static_cast<int>(MUSER_OK);
     });
     if (r == nullptr) return MUSER_ERR_CUDA;  // the message is set
-    const int cluster = a.n * a.stride > 16384 || a.max_new > 8192 ? 16 : 1;
+    const int cluster = a.n * a.stride > 16384 || a.max_new > 8192 ? r->cluster : 1;
     return launch_after("page tables", page_tables_kernel, dim3(static_cast<unsigned>(cluster)), kTabThreads,
                         static_cast<size_t>((a.pages + 31) / 32) * 4u, cluster, s, a);
 }

@@ -35,6 +35,14 @@ int launch_after(const char* what, void (*kern)(Params...), dim3 grid, int threa
     return check_launch(what);
 }
 
+// The largest cluster, of up to sixteen blocks, that fits(size) says can be placed.
+template <typename F>
+int largest_cluster(F&& fits) {
+    for (int size : {16, 8, 4, 2})
+        if (fits(size)) return size;
+    return 1;
+}
+
 // pages.cu
 struct PageTableArgs {
     const int32_t *table, *length, *parent, *add;

@@ -6,6 +6,7 @@ import shutil
 import pytest
 
 import quantized_weight_streaming_q4_gb300 as mu
+from tests.test_abi_tree import host_program
 
 pytestmark = pytest.mark.skipif(shutil.which("nvcc") is None and not os.path.exists("/usr/local/cuda/bin/nvcc"),
                                 reason="nvcc not available")
@@ -194,3 +195,19 @@ def test_binding_refuses_tables_that_are_not_rows_of_int32(L):
                  lambda: _attend_call(good), lambda: _attend_call(wide[:, :8], n_tables=4, width=10), lambda: _attend_call(1 << 29, n_tables=4, width=8)):
         with pytest.raises(mu.MuserError, match="pages and page_rows must be positive"):
             call()
+
+
+def test_tables_take_the_clusters_that_the_device_can_place(L, tmp_path):
+    """Sixteen blocks are more than a device has to offer: fewer free SMs in its clusters' groups, and smaller clusters,
+    down to one block, do the same work."""
+    out = host_program(tmp_path, r"""
+#include <cstdio>
+#include "pages.cuh"
+int main() {
+    for (int most : {16, 15, 8, 7, 2, 1, 0}) {
+        const int c = muser::largest_cluster([&](int size) { return size <= most; });
+        std::printf("%d ", c);
+    }
+}
+""")
+    assert out == ["16", "8", "8", "4", "2", "1", "1"]
