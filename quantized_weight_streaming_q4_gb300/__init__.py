@@ -470,18 +470,26 @@ def muser_kv_tree_commit(planes, ks, vs, M: int, path, position: int, stream=Non
             mine.len, mine.origin_logical, mine.origin_physical = new.len, new.origin_logical, new.origin_physical
 
 
-def _int_rows(name: str, t) -> None:
-    if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+_int32 = None
+
+
+def _int_rows(name: str, t):
+    """The shape of a contiguous int32 tensor."""
+    global _int32
+    if _int32 is None:
+        import torch
+        _int32 = torch.int32
+    if t.dtype is not _int32 or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous int32")
+    return t.shape
 
 
 def _table_shape(table, rows, width):
     """The page tables' rows and entries a row: the tensor's, where they are not given."""
     if rows is None or width is None:
-        _int_rows("table", table)
-        if table.dim() != 2:
+        shape = _int_rows("table", table)
+        if len(shape) != 2:
             raise ValueError("table: one row per sequence")
-        shape = table.shape
         rows = shape[0] if rows is None else rows
         width = shape[1] if width is None else width
     return rows, width
@@ -495,9 +503,9 @@ def muser_kv_page_tables(table, length, n: int, pages: int, page_rows: int, tabl
     and table_out has to be int32 [n, width] then)."""
     sized = n_old is None or width is None
     n_old, width = _table_shape(table, n_old, width)
-    if sized and hasattr(table_out, "numel"):
-        _int_rows("table_out", table_out)
-        if table_out.numel() < n * width or (table_out.dim() == 2 and table_out.shape[1] != width):
+    if sized and not isinstance(table_out, int):
+        shape = _int_rows("table_out", table_out)
+        if shape != (n, width) and (table_out.numel() < n * width or (len(shape) == 2 and shape[1] != width)):
             raise ValueError("table_out: n rows as long as the table's")
     _check("muser_kv_page_tables",
            lib().muser_kv_page_tables(_ptr(table), _ptr(length), n_old, _ptr(parent), _ptr(add), n, width, pages, page_rows,
