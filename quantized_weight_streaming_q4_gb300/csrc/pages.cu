@@ -18,12 +18,21 @@ namespace {
 //
 // One cluster: its first block keeps the bits in shared memory, all blocks set
 // them there (reductions over distributed shared memory), and the first one
-// counts and gives pages out; then all blocks write the slots.  A cluster of
-// one block up to 16,384 entries and 8,192 slots, else of sixteen (or what the
-// device can place).
+// counts and gives pages out; then all blocks write the slots.
 // Bound: latency, a dozen dependent steps of about 0.7 us (16 beams of 500 to
-// 8,000 rows, one block: 7.6 us; 48 prompts, 48,000 new rows: 13.9 us with
+// 8,000 rows, one block: 7.8 us; 48 prompts, 48,000 new rows: 13.9 us with
 // sixteen, 15.5 with eight).
+//
+// Sixteen blocks (or what the device can place) where the slots are many, since
+// all of them write these; their marks cross to the first block's memory and are
+// slower than its own, the slower the more entries live.  us, one block and
+// sixteen: 48 sequences of 30 to 5,000 rows, pages of 16, 4,000 slots 11.0 and
+// 12.2, 8,200 13.5 and 12.2, 48,000 31.9 and 13.9; without slots 16 of 500 to
+// 8,000 in tables of 2,048 entries 7.6 and 9.4, of 30,000 to 120,000 (16,406
+// live entries) 12.4 and 18.1, 128 of these 54 and 102.  Rows of more than 128
+// sequences are marked in many turns: 256 of 250 to 1,000 rows 25.8 and 20.8,
+// tables of 128 entries with 4,033 live ones 26.2 and 22.4, with 17,447 28.5 and
+// 30.8; longer tables, when full, 41 and 63.
 constexpr int kTabThreads = 1024, kTabWarps = kTabThreads / 32, kRows = kMaxSequences;
 
 struct TabShared {
@@ -444,7 +453,8 @@ int launch_page_tables(const PageTableArgs& a, cudaStream_t s) {
         return static_cast<int>(MUSER_OK);
     });
     if (r == nullptr) return MUSER_ERR_CUDA;  // the message is set
-    const int cluster = a.n * a.stride > 16384 || a.max_new > 8192 ? r->cluster : 1;
+    const bool many = a.max_new > 8192 || (a.n > 128 && a.n * a.stride <= 32768);
+    const int cluster = many ? r->cluster : 1;
     return launch_after("page tables", page_tables_kernel, dim3(static_cast<unsigned>(cluster)), kTabThreads,
                         static_cast<size_t>((a.pages + 31) / 32) * 4u, cluster, s, a);
 }
