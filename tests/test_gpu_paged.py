@@ -459,6 +459,71 @@ def test_attention_of_more_tiles_than_units():
     assert mu.muser_device_status() == 0
 
 
+@pytest.mark.parametrize("G", [2, 3])
+def test_attention_units_of_several_tiles(G):
+    """More than 2^23 tiles (units of two tiles for G = 2, of four for G = 3), each of which is seen in the result.  A
+    sequence's 60,000 to 65,536 table entries name 31 pages at random; a few more pages, each named once, have a key that
+    weighs about as much as a tenth of all other rows: at the first tile, the last one, two drawn ones and those on both
+    sides of each place where a block's share ends.  The expected result is the softmax weighted by the pages' counts.
+    A thread adds up to 32,768 tiles, each addition off by half a step of 2^-24 of a sum that only grows: 2^-9 of the
+    sums, once for the outputs and once for the weights' total; leaving out or doubling one of the few pages must show
+    at four times that."""
+    n, R, D, entries, ordinary, special, H = 256, 64, 8, 65536, 31, 12, G
+    rng = np.random.default_rng(100 + G)
+    pages = ordinary + special
+    key = rng.standard_normal((pages, R, G, D)).astype(np.float16)
+    value = np.clip(rng.standard_normal((pages, R, G, D)), -4, 4).astype(np.float16)
+    key[..., 0] = 0
+    key[ordinary:, 0] = 0
+    key[ordinary:, 0, :, 0] = 45.0  # 0.3 * 45 above what the other rows' scores lie around
+    value[ordinary:, 0] = rng.choice([-4.0, 4.0], (special, G, D))
+    q = rng.standard_normal((n, H, D)).astype(np.float32)
+    q[..., 0] = 1.0
+    t = np.sort(rng.integers(60000 * R, entries * R, n)).astype(np.int64)
+    table = rng.integers(0, ordinary, (n, entries)).astype(np.int32)
+    tiles = t // 128 + 1
+    assert (tiles % 4 != 0).any() and tiles.sum() * G > 1 << 23
+    # the split: an item's units are its tiles in twos or fours and two more, the blocks' shares of all units are equal
+    shift = int(tiles.sum() * G >> 23).bit_length()
+    units = -(-tiles // (1 << shift)) + 2
+    before = np.concatenate([[0], np.cumsum(units)]) * G
+    blocks = min(160, torch.cuda.get_device_properties(0).multi_processor_count)
+    places = [[0, int(x) - 1, *rng.integers(1, x - 1, 2)] for x in tiles]
+    for b in range(1, blocks):
+        at = int(before[-1]) * b // blocks
+        i = int(np.searchsorted(before, at, side="right")) - 1
+        first = max((at - int(before[i])) % int(units[i]) - 2, 0) << shift
+        places[i] += [x for x in (first - 1, first) if 0 <= x < tiles[i]]
+    for i in range(n):
+        places[i] = sorted(set(int(x) for x in places[i]))
+        assert len(places[i]) <= special
+        for j, x in enumerate(places[i]):
+            table[i, min(2 * x + int(rng.integers(0, 2)), t[i] // R)] = ordinary + j
+    dk, dv = dev(key), dev(value)
+    out = nan_like((n, H * D), 16)
+    nb = mu.muser_kv_paged_attention_scratch_bytes(G * D, D, n, H)
+    mu.muser_kv_paged_attention(mu.KvPages(dk.data_ptr(), dv.data_ptr(), pages, R, G * D, D, 0, 0), ints(table), ints(t), dev(q), n,
+                                H, out, 0.3, torch.zeros(nb // 4, device="cuda"), nb)
+    got = host(out)[:n * H * D].reshape(n, H, D)
+    check_canary(out, n * H * D)
+    assert mu.muser_device_status() == 0
+    bound = 2 * 2.0 ** -9 * 4.0
+    for i in range(n):
+        full, rest = divmod(int(t[i]) + 1, R)
+        count = np.repeat(np.bincount(table[i, :full], minlength=pages)[:, None], R, 1)
+        if rest:
+            count[table[i, full], :rest] += 1
+        w = np.exp(0.3 * np.einsum("prhd,hd->hpr", key.astype(np.float64), q[i].astype(np.float64))) * count
+        o = np.einsum("hpr,prhd->hpd", w, value.astype(np.float64))
+        w = w.sum(2)
+        want = o.sum(1) / w.sum(1)[:, None]
+        assert np.abs(got[i] - want).max() <= bound, i
+        for j in range(ordinary, ordinary + len(places[i])):
+            for c in (-1, 1):
+                other = (o.sum(1) + c * o[:, j]) / (w.sum(1) + c * w[:, j])[:, None]
+                assert (np.abs(other - want).max(1) > 4 * bound).all(), "the page would not be missed"
+
+
 def test_attention_agrees_with_the_ring():
     """One token over one sequence: the tree attention over a plane gives the same to rounding."""
     c = Case([1000], 32, 2, 128, 64, False).to_device()
