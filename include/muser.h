@@ -708,7 +708,8 @@ typedef struct {
  *   are thereby free.  With a window, a page whose rows lie before it (below
  *   keep - window + 1) and are not among the first n_sink is given up: its
  *   entry becomes -1.  Entries outside 0..pages-1 stay as they are and hold
- *   nothing.
+ *   nothing.  A page that was given up does not come back: a sequence that later
+ *   loses rows (add < 0) no longer has the rows before its window.
  *   table: device int32 [n_old][stride], length: [n_old]; parent, add: [n] or
  *   NULL; a parent outside -1..n_old-1 counts as -1.  table_out: [n][stride];
  *   entries from ceil(rows/page_rows) on are left as they were.  length_out,
@@ -775,7 +776,8 @@ size_t muser_kv_paged_attention_scratch_bytes(int64_t kv_dim, int64_t head_dim, 
  *   itself, is k[i], v[i] rounded to binary16, and is stored in its place in
  *   the cache (unless its table entry is outside 0..pages-1).  With k = v =
  *   NULL its own row is read from the cache too: several rows of one sequence
- *   then go in one call, once muser_kv_page_write has stored them.  With k and
+ *   then go in one call, once muser_kv_page_write has stored them; each of them
+ *   reads what it sees for itself, as a row of another sequence does.  With k and
  *   v no two rows are of one sequence, and no row's page is another's that is
  *   written to.
  *   A row with position[i] < 0 or a sequence outside 0..n_tables-1 is left as

@@ -7,8 +7,8 @@
 // split for itself, in one of two ways:
 //  - few tiles a block: each item is cut into pieces of up to `chunk` tiles, one
 //    a block.  Joining the results of an item's blocks costs about as much as
-//    four tiles, so items of up to four are left whole; longer ones are cut as
-//    far as there are blocks.
+//    four tiles, so where no item has more than four, all are left whole; else
+//    all are cut, with the smallest chunk for which there are blocks.
 //  - else all items' tiles in a row are cut into as many equal runs as there are
 //    blocks, so that a run may end inside an item.  An item counts as some tiles
 //    more than it has, for what a block spends on its start and its end: two

@@ -321,10 +321,10 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
 
 // ------------------------------------------------------------------- copy
 // Bound: the rows' bytes, read and written once (15 pages of 52 layers, 52 MB:
-// 12.9 us, of which 4 are the launch and the two reads before the data).  A block takes a part of a
-// page of a layer's keys or values, all its loads in flight before the first
-// store; blocks go round, since how many copies there are is known on the
-// device only.
+// 11.3 to 13.6 us, of which 4 are the launch and, one behind the other, the
+// reads of the count and of a triple).  A block takes a part of a page of a
+// layer's keys or values, all its loads in flight before the first store; blocks
+// go round, since how many copies there are is known on the device only.
 constexpr int kCopyThreads = 128;
 
 template <int N>
@@ -380,8 +380,8 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
 
 // ------------------------------------------------------------------ write
 // Bound: 4 bytes read and 2 written an element (40,007 rows of 256, 123 MB:
-// 20.3 us, 6.06 TB/s).  A thread takes 8 elements of a
-// row of K and of V (or one, where rows are not 16-byte aligned).
+// 20.4 us, 6.03 TB/s).  A thread takes 8 elements of a row of K and of V (or
+// one, where rows are not 16-byte aligned).
 constexpr int kWriteThreads = 256;
 
 template <bool VEC>
