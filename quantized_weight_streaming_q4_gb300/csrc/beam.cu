@@ -40,9 +40,11 @@ namespace {
 constexpr int kThreads = 512, kVec = 8, kPerThread = 4 * kVec;
 constexpr int kMost = kThreads * kPerThread - 4;  // logits of a part; up to 3 elements before it share its first 16 bytes
 constexpr int kGroups = 64, kGroupLanes = kThreads / kGroups, kList = 2048;
-// Entries that are ranked as they are; n = 64 leaves about 270 of random values.
-// The ranking is quadratic: a call of 1,500 logits, n = 64, is 24 us narrowed, 262 with all of them ranked.
-constexpr int kShort = 512;
+// Entries that are ranked as they are (n = 64 leaves about 270 of random values),
+// and those that are ranked where a closer bound leaves more.  The ranking is
+// quadratic: a call of 1,500 logits, n = 64, is 24 us narrowed, 262 with all of
+// them ranked; of 1,500 equal ones, n = 4, 221 us ranked and 18 one by one.
+constexpr int kShort = 512, kRanked = 1024;
 constexpr float kNegInf = -INFINITY;
 // log2(e) to 48 bits
 constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746887e-8f;
@@ -167,7 +169,7 @@ __device__ __noinline__ int narrow(Pick<K>& S, int n, int count, K& least) {
 template <typename K, typename Each, typename Put>
 __device__ __forceinline__ int largest(Pick<K>& S, int n, int count, Each&& each, Put&& put) {
     const int tid = threadIdx.x;
-    if (count <= kList) {
+    if (count <= kRanked) {
         for (int i = tid / 8; i < (count + 3) / 4 * 4; i += kThreads / 8) {  // eight lanes a value; whole warps
             const K k = i < count ? S.list_key[i] : 0;
             const int at = i < count ? S.list_at[i] : 0;

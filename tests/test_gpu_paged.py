@@ -617,29 +617,40 @@ def test_select_few_parts_and_far_scores(groups, beams, n, V, spread):
     run_select(x, (-20.0 - spread * rng.random(groups * beams)).astype(np.float32), groups, beams, n)
 
 
+def select_time(x, score, n):
+    """The least of ten measurements of twenty selections."""
+    beams, V = x.shape
+    nb = mu.muser_beam_select_scratch_bytes(1, beams, V, n)
+    x, score, scratch, so = dev(x), dev(score), torch.zeros(nb // 4, device="cuda"), torch.zeros(n, device="cuda")
+    o = [torch.zeros(n, dtype=torch.int32, device="cuda") for _ in range(2)]
+    times = []
+    for _ in range(10):
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        torch.cuda.synchronize()
+        e[0].record()
+        for _ in range(20):
+            mu.muser_beam_select(x, score, 1, beams, V, n, *o, so, scratch, nb)
+        e[1].record()
+        torch.cuda.synchronize()
+        times.append(e[0].elapsed_time(e[1]))
+    return min(times)
+
+
 @pytest.mark.parametrize("beams,n,V", [(16, 32, 20000), (32, 64, 50000), (32, 64, 2000), (1, 64, 1500)])
 def test_select_of_untied_logits_takes_no_turns(beams, n, V):
     """The n largest of untied logits are not taken one by one, which costs 15 to 90 times what the largest one does (the
     list: 1.3 to 7 times)."""
     rng = np.random.default_rng(V)
-    x, score = dev((2.0 * rng.standard_normal((beams, V))).astype(np.float32)), dev(-20.0 - rng.random(beams).astype(np.float32))
-    time = {}
-    for m in (1, n):
-        nb = mu.muser_beam_select_scratch_bytes(1, beams, V, m)
-        scratch, so = torch.zeros(nb // 4, device="cuda"), torch.zeros(m, device="cuda")
-        o = [torch.zeros(m, dtype=torch.int32, device="cuda") for _ in range(2)]
-        times = []
-        for _ in range(10):
-            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
-            torch.cuda.synchronize()
-            e[0].record()
-            for _ in range(20):
-                mu.muser_beam_select(x, score, 1, beams, V, m, *o, so, scratch, nb)
-            e[1].record()
-            torch.cuda.synchronize()
-            times.append(e[0].elapsed_time(e[1]))
-        time[m] = min(times)
-    assert time[n] < 10 * time[1]
+    x, score = (2.0 * rng.standard_normal((beams, V))).astype(np.float32), (-20.0 - rng.random(beams)).astype(np.float32)
+    assert select_time(x, score, n) < 10 * select_time(x, score, 1)
+
+
+@pytest.mark.parametrize("V", [1100, 1500, 2000])
+def test_select_of_tied_logits_is_not_ranked(V):
+    """More equal logits than are worth a ranking (quadratic: 25 times the time of untied ones) are taken one by one
+    (twice)."""
+    x = np.random.default_rng(V).standard_normal((1, V)).astype(np.float32)
+    assert select_time(np.zeros_like(x), np.zeros(1, np.float32), 4) < 10 * select_time(x, np.zeros(1, np.float32), 4)
 
 
 def test_select_rows_that_are_not_finite():
