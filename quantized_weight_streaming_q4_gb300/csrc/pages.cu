@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kTabThreads, 1) page_tables_kernel(const __gri
 
 // ------------------------------------------------------------------- copy
 // Bound: the rows' bytes, read and written once (15 pages of 52 layers, 52 MB:
-// 11.3 to 13.6 us, of which 4 are the launch and, one behind the other, the
+// 11.3 to 13.8 us, of which 4 are the launch and, one behind the other, the
 // reads of the count and of a triple).  A block takes a part of a page of a
 // layer's keys or values, all its loads in flight before the first store; blocks
 // go round, since how many copies there are is known on the device only.
